@@ -11,8 +11,9 @@ w_i = exp((l_i - m) / T); top-k keeps the first k of the order (logit descending
 top-p keeps, of those, the tokens whose preceding mass is below p times their whole mass (always
 the first); min-p keeps the tokens with w_i >= min_p; the token is the lowest index at which the
 kept mass, summed in index order, exceeds u times the kept mass. T < 1e-5 takes the first token of
-the order. A row without a distribution (a NaN, or nothing above -inf) gives token -1 and
-log-probability -inf; +inf logits share the whole mass equally.
+the order. Beside the token
+comes the probability it had: its weight over the kept mass. A row without a distribution (a NaN,
+or nothing above -inf) gives token -1 and probability 0; +inf logits share the whole mass equally.
 """
 import math
 
