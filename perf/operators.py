@@ -11,9 +11,9 @@ w_i = exp((l_i - m) / T); top-k keeps the first k of the order (logit descending
 top-p keeps, of those, the tokens whose preceding mass is below p times their whole mass (always
 the first); min-p keeps the tokens with w_i >= min_p; the token is the lowest index at which the
 kept mass, summed in index order, exceeds u times the kept mass. T < 1e-5 takes the first token of
-the order. Beside the token
-comes the probability it had: its weight over the kept mass. A row without a distribution (a NaN,
-or nothing above -inf) gives token -1 and probability 0; +inf logits share the whole mass equally.
+the order. Beside the token comes the probability it had: its weight over the kept mass. A row
+without a distribution (a NaN, or nothing above -inf) gives token -1 and probability 0; +inf logits
+share the whole mass equally.
 """
 import math
 
@@ -77,8 +77,9 @@ def draw(rng):
         dtype = rng.choice(["bf16", "bf16", "q4_0", "f32"])
         rows = rng.randint(1, 6)
         K = _log(rng, 8, 256) * 32
-        N = min(_log(rng, 64, 65536), 200_000_000 // K)
-        M = rng.randint(1, 64)
+        # (32-bit weights are for small models: a few rows of a small matrix)
+        N = min(_log(rng, 64, 65536), (20_000_000 if dtype == "f32" else 200_000_000) // K)
+        M = rng.randint(1, 8 if dtype == "f32" else 64)
         return dict(op="lora", N=N, K=K, M=M, dtype=dtype, rank=8 * rng.randint(1, 12), adapters=_log(rng, 1, 24),
                     rows=rows, none=rng.random() < 0.4, gain=rng.random() < 0.5)
     V = _log(rng, 500, 262144)
