@@ -163,6 +163,33 @@ typedef struct {
     double tokens_per_pass; /* emitted / passes = 1 + accepted / passes */
 } spec_stats_t;
 
+/* Sampling settings of M rows, each "device" [M]; NULL leaves the setting out
+ * for every row. Per row, on logits l with maximum m and weights
+ * w_i = exp((l_i - m) / temperature):
+ *  temperature  below 1e-5: the most likely token (lowest index on ties);
+ *               negative, NaN or infinite: the row has no distribution;
+ *  top_k        > 0: the first top_k tokens of the order (logit descending,
+ *               index ascending);
+ *  top_p        < 1: of those, the tokens whose preceding mass is below top_p
+ *               times their whole mass, and always the first;
+ *  min_p        > 0: of those, the tokens with w_i >= min_p (at most 1);
+ *  uniform      u in [0, 1), required: the token is the lowest index at which
+ *               the kept mass, summed in index order, exceeds u times the kept
+ *               mass (u below 0 or NaN counts as 0, u >= 1 takes the last kept
+ *               token).
+ * Values outside these ranges (NaN included) leave top_k, top_p and min_p off.
+ * Weights are held in 40 fraction bits of the largest (smaller ones count as
+ * zero) and their sums are exact, so a row's token depends on nothing but the
+ * row. -inf logits are never chosen; +inf logits share the whole mass equally;
+ * a row with a NaN, or with nothing above -inf, has no distribution. */
+typedef struct {
+    const float *temperature;
+    const int32_t *top_k;
+    const float *top_p;
+    const float *min_p;
+    const float *uniform;
+} spec_sampling;
+
 typedef struct spec_ctx spec_ctx;
 
 /* Bytes of workspace needed for batches of up to B_max sequences, prompts of
@@ -246,6 +273,20 @@ spec_status spec_verify_topm(spec_ctx *ctx, int32_t B, const int32_t *seq_ids, i
 spec_status spec_verify_tree(spec_ctx *ctx, int32_t B, const int32_t *seq_ids, int32_t n,
                              const int32_t *tokens, const int32_t *parents, int32_t *out_tokens,
                              int32_t *n_emitted, float *logits_dbg, void *stream);
+
+/* Sampled verify: the rows of spec_verify, each sampled with its own settings
+ * (s: B*(k+1) rows, sequence b's row j at b*(k+1) + j), drafts kept while they
+ * equal the samples, then the target's own sample is emitted (see
+ * spec_accept_sampled); commits and rolls back as spec_verify does. The emitted
+ * tokens are those that sampling one token a pass (k = 0) with the same numbers
+ * would emit, where the pass's logits are the same. probs ("device" float
+ * [B][k+1], may be NULL) gets each emitted token's probability, 0 behind them.
+ * If a row that decides has no distribution, nothing of the pass is committed
+ * and spec_sync reports SPEC_EINVAL. k in [0, P-1] (P as for spec_verify). The
+ * rows' logits go to logits_dbg when given, else to the workspace. */
+spec_status spec_verify_sampled(spec_ctx *ctx, int32_t B, const int32_t *seq_ids, int32_t k,
+                                const int32_t *drafts, const spec_sampling *s, int32_t *out_tokens,
+                                int32_t *n_emitted, float *probs, float *logits_dbg, void *stream);
 
 /* spec_draft followed by spec_verify on the context's own draft buffer. */
 spec_status spec_step(spec_ctx *ctx, int32_t B, const int32_t *seq_ids, int32_t k,
@@ -333,6 +374,34 @@ spec_status spec_attention(const spec_model_desc *m, const spec_kv_desc *kv, int
                            const int32_t *seq_ids, const int32_t *seq_len, int32_t R, int32_t n_q_heads,
                            int32_t key_extra, const float *q, float *out, void *workspace, size_t ws_bytes,
                            void *stream);
+
+/* One token per row of logits ("device", dtype SPEC_F32 or SPEC_BF16, M rows of
+ * V at a stride of ld >= V elements; rows may start at any element), each row
+ * with its own settings. tokens ("device" int32 [M]) gets the token, -1 for a
+ * row without a distribution; probs ("device" float [M], may be NULL) the
+ * probability it had (its weight over the kept mass), 0 for such a row.
+ * Needs no workspace. V <= 2^21, M <= 2^20. */
+spec_status spec_sample(int32_t dtype, const void *logits, int64_t ld, int32_t M, int32_t V,
+                        const spec_sampling *s, int32_t *tokens, float *probs, void *stream);
+
+/* Sampled accept of drafts from the logits of a verify pass ("device", B*(k+1)
+ * rows: row j of sequence b, at b*(k+1) + j, scores the token after j drafts).
+ * Every row is sampled as by spec_sample; draft d_j is kept while every earlier
+ * one was and it equals the sample of row j-1; the step emits the kept drafts
+ * and the sample of the next row. With drafts that are single proposals this is
+ * rejection sampling: a draft is kept with its probability p(d), and a rejected
+ * position emits a token distributed as p without d, so the output is
+ * distributed as plain sampling ("Gemma 4's MTP drafter explained"
+ * (molayo1419.me), section "How does speculative decoding work?", states the
+ * greedy case). drafts ("device" int32 [B][k], unused for k = 0); out_tokens
+ * ("device" int32 [B][k+1]) gets the emitted tokens, then -1; n_emitted
+ * ("device" int32 [B]) their number, at least 1 unless the first row has no
+ * distribution (such a row ends the emission before it); probs ("device" float
+ * [B][k+1], may be NULL) their probabilities, 0 behind them.
+ * k in [0, 1023], B * (k+1) <= 2^20. */
+spec_status spec_accept_sampled(int32_t dtype, const void *logits, int64_t ld, int32_t B, int32_t k,
+                                int32_t V, const int32_t *drafts, const spec_sampling *s,
+                                int32_t *out_tokens, int32_t *n_emitted, float *probs, void *stream);
 
 /* Copy one slot's counters to the host (synchronises `stream`). */
 spec_status spec_stats(spec_ctx *ctx, int32_t slot, spec_stats_t *out, void *stream);

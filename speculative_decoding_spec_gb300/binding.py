@@ -23,7 +23,8 @@ EXPORTS = ["spec_workspace_bytes", "spec_init", "spec_prefill", "spec_draft", "s
            "spec_decode", "spec_inject_drafts", "spec_stats", "spec_sync", "spec_set_graphs",
            "spec_kernel_launches", "spec_status_str", "spec_destroy", "spec_linear",
            "spec_linear_workspace_bytes", "spec_linear_noalloc", "spec_set_option",
-           "spec_attention_workspace_bytes", "spec_attention", "spec_verify_topm", "spec_verify_tree"]
+           "spec_attention_workspace_bytes", "spec_attention", "spec_verify_topm", "spec_verify_tree",
+           "spec_verify_sampled", "spec_sample", "spec_accept_sampled"]
 SPEC_OPT_GRAPHS, SPEC_OPT_PREFETCH, SPEC_OPT_TEST_ATTN_WAIT = 1, 4, 8
 SPEC_OPT_WIDE_TRACE = 7
 SPEC_LINEAR_NOALLOC_MAX_ROWS = 523776
@@ -73,6 +74,10 @@ class spec_state(C.Structure):
 class spec_stats_t(C.Structure):
     _fields_ = [("passes", C.c_int64), ("drafted", C.c_int64), ("accepted", C.c_int64),
                 ("emitted", C.c_int64), ("tokens_per_pass", C.c_double)]
+
+
+class spec_sampling(C.Structure):
+    _fields_ = [(n, C.c_void_p) for n in ("temperature", "top_k", "top_p", "min_p", "uniform")]
 
 
 _lib = None
@@ -130,6 +135,12 @@ def lib():
     L.spec_verify_topm.argtypes = [p, i32, p, i32, p, i32, p, p, p, p]
     L.spec_verify_tree.restype = st
     L.spec_verify_tree.argtypes = [p, i32, p, i32, p, p, p, p, p, p]
+    L.spec_verify_sampled.restype = st
+    L.spec_verify_sampled.argtypes = [p, i32, p, i32, p, C.POINTER(spec_sampling), p, p, p, p, p]
+    L.spec_sample.restype = st
+    L.spec_sample.argtypes = [i32, p, C.c_int64, i32, i32, C.POINTER(spec_sampling), p, p, p]
+    L.spec_accept_sampled.restype = st
+    L.spec_accept_sampled.argtypes = [i32, p, C.c_int64, i32, i32, i32, p, C.POINTER(spec_sampling), p, p, p, p]
     L.spec_destroy.restype = None
     L.spec_destroy.argtypes = [p]
     _lib = L
@@ -137,8 +148,9 @@ def lib():
 
 
 class SpecError(RuntimeError):
-    def __init__(self, fn, code):
-        super().__init__("%s failed: %s (%d)" % (fn, lib().spec_status_str(code).decode(), code))
+    def __init__(self, fn, code, why=""):
+        super().__init__("%s failed: %s (%d)%s" % (fn, lib().spec_status_str(code).decode(), code,
+                                                   ": " + why if why else ""))
         self.code = code
 
 
@@ -222,6 +234,104 @@ def spec_attention(t, pool: torch.Tensor, block_table: torch.Tensor, layer: int,
                                              s.cuda_stream))
     out.workspace = ws      # error word in its first int
     return out
+
+
+def _need(fn, ok, why):
+    if not ok:
+        raise SpecError(fn, SPEC_EINVAL, why)
+
+
+_SETTINGS = (("temperature", torch.float32), ("top_k", torch.int32), ("top_p", torch.float32),
+             ("min_p", torch.float32), ("uniform", torch.float32))
+
+
+def _sampling(fn, device, M, *settings) -> spec_sampling:
+    """Settings of M rows (temperature, top_k, top_p, min_p, uniform; None: left out)."""
+    s = spec_sampling()
+    for (name, dtype), t in zip(_SETTINGS, settings):
+        if t is None:
+            _need(fn, name != "uniform", "uniform numbers are required")
+            continue
+        _need(fn, t.dtype == dtype and t.dim() == 1 and t.shape[0] == M and t.is_contiguous() and t.device == device,
+              "%s must be a contiguous %s tensor of %d rows on %s" % (name, dtype, M, device))
+        setattr(s, name, t.data_ptr())
+    return s
+
+
+_LOGIT_DTYPES = {torch.float32: 0, torch.bfloat16: 1}
+
+
+def _logits(fn, logits, rows=None):
+    """(dtype code, row stride) of a [M][V] logits tensor whose rows may be strided."""
+    _need(fn, logits.is_cuda and logits.dim() == 2 and logits.dtype in _LOGIT_DTYPES,
+          "logits must be a float32 or bfloat16 CUDA tensor [rows][V]")
+    M, V = logits.shape
+    _need(fn, M > 0 and V > 0 and (rows is None or M == rows), "logits must have %s rows" % (rows or "some"))
+    ld = logits.stride(0) if M > 1 else V
+    _need(fn, (V == 1 or logits.stride(1) == 1) and ld >= V, "the logits of a row must be contiguous")
+    return _LOGIT_DTYPES[logits.dtype], ld
+
+
+class _on:
+    """The tensor's device made current for a call, and the stream it goes to:
+    the given one, or the device's current one. What the call allocates belongs
+    to that stream."""
+
+    def __init__(self, t, stream):
+        self.ctx = None
+        if stream is not None:
+            self.ctx = torch.cuda.stream(stream)
+        elif t.device.index != torch.cuda.current_device():
+            self.ctx = torch.cuda.device(t.device)
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        return torch.cuda.current_stream().cuda_stream
+
+    def __exit__(self, *e):
+        if self.ctx is not None:
+            self.ctx.__exit__(*e)
+
+
+def spec_sample(logits: torch.Tensor, uniform: torch.Tensor, temperature: Optional[torch.Tensor] = None,
+                top_k: Optional[torch.Tensor] = None, top_p: Optional[torch.Tensor] = None,
+                min_p: Optional[torch.Tensor] = None, stream=None):
+    """One token per row of logits [M][V] (float32 or bfloat16, rows may be
+    strided), each row with its own settings ([M] tensors, None leaves one out;
+    include/spec.h spec_sampling). Returns (tokens int32 [M], probs float32 [M]);
+    a row without a distribution gives token -1 and probability 0."""
+    fn = "spec_sample"
+    dt, ld = _logits(fn, logits)
+    M, V = logits.shape
+    s = _sampling(fn, logits.device, M, temperature, top_k, top_p, min_p, uniform)
+    with _on(logits, stream) as st:
+        tokens = torch.empty(M, dtype=torch.int32, device=logits.device)
+        probs = torch.empty(M, dtype=torch.float32, device=logits.device)
+        check(fn, lib().spec_sample(dt, _ptr(logits), ld, M, V, C.byref(s), _ptr(tokens), _ptr(probs), st))
+    return tokens, probs
+
+
+def spec_accept_sampled(logits: torch.Tensor, drafts: torch.Tensor, uniform: torch.Tensor,
+                        temperature: Optional[torch.Tensor] = None, top_k: Optional[torch.Tensor] = None,
+                        top_p: Optional[torch.Tensor] = None, min_p: Optional[torch.Tensor] = None, stream=None):
+    """Sampled accept of drafts int32 [B][k] from the logits [B*(k+1)][V] of a
+    verify pass; the settings have a row for each row of logits. Returns
+    (out_tokens int32 [B][k+1], n_emitted int32 [B], probs float32 [B][k+1])."""
+    fn = "spec_accept_sampled"
+    _need(fn, drafts.dim() == 2 and drafts.dtype == torch.int32 and drafts.is_contiguous() and
+          drafts.device == logits.device, "drafts must be a contiguous int32 tensor [B][k] beside the logits")
+    B, k = drafts.shape
+    dt, ld = _logits(fn, logits, B * (k + 1))
+    M, V = logits.shape
+    s = _sampling(fn, logits.device, M, temperature, top_k, top_p, min_p, uniform)
+    with _on(logits, stream) as st:
+        out = torch.empty((B, k + 1), dtype=torch.int32, device=logits.device)
+        ne = torch.empty(B, dtype=torch.int32, device=logits.device)
+        probs = torch.empty((B, k + 1), dtype=torch.float32, device=logits.device)
+        check(fn, lib().spec_accept_sampled(dt, _ptr(logits), ld, B, k, V, _ptr(drafts) if k else None, C.byref(s),
+                                            _ptr(out), _ptr(ne), _ptr(probs), st))
+    return out, ne, probs
 
 
 _LINEAR_WS = {}
@@ -362,6 +472,27 @@ class Engine:
                                                          _ptr(out), _ptr(ne), _ptr(logits), self.stream.cuda_stream))
         self.leave()
         return out, ne
+
+    def spec_verify_sampled(self, seq_ids, drafts: torch.Tensor, uniform: torch.Tensor, temperature=None, top_k=None,
+                            top_p=None, min_p=None, logits: Optional[torch.Tensor] = None):
+        """Sampled verify: settings [B][k+1] (or flat), None leaves one out.
+        Returns (out_tokens, n_emitted, probs)."""
+        B, k = drafts.shape
+        M = B * (k + 1)
+        # (the converted tensors live until leave() orders their reuse after the copies)
+        given = [None if t is None else torch.as_tensor(t).reshape(-1).to(self.device, dtype)
+                 for (_, dtype), t in zip(_SETTINGS, (temperature, top_k, top_p, min_p, uniform))]
+        s = _sampling("spec_verify_sampled", self.pool.device, M,
+                      *(None if t is None else self._in(name, t) for (name, _), t in zip(_SETTINGS, given)))
+        self.enter()
+        out = self._buf("out_tokens", (B, k + 1))
+        ne = self._buf("n_emitted", (B,))
+        probs = self._buf("probs", (B, k + 1), torch.float32)
+        check("spec_verify_sampled", lib().spec_verify_sampled(
+            self.ctx, B, _ptr(seq_ids), k, _ptr(drafts) if k else None, C.byref(s), _ptr(out), _ptr(ne), _ptr(probs),
+            _ptr(logits), self.stream.cuda_stream))
+        self.leave()
+        return out, ne, probs
 
     def spec_draft(self, seq_ids, B: int, k: int):
         self.enter()

@@ -214,6 +214,38 @@ struct TopmArgs {
 };
 int topm_accept(const TopmArgs& a, cudaStream_t st);
 
+// One token per row of logits with the row's own sampling settings (sample.cu).
+struct SampleArgs {
+  int dtype;                   // DT_F32 or DT_BF16
+  const void* logits;          // [M] rows at stride ld
+  long long ld;
+  int M, V;
+  const float* temperature;    // [M] or null (1)
+  const int32_t* top_k;        // [M] or null (off)
+  const float *top_p, *min_p;  // [M] or null (off)
+  const float* uniform;        // [M]
+  int32_t* tokens;             // [M]
+  float* probs;                // [M] or null
+};
+int sample_rows(const SampleArgs& a, int pdl, cudaStream_t st);
+
+// Sampled accept: out_tokens holds every row's sample on entry, the emitted
+// tokens and -1 behind them on return. A pass gives its state (seq_len not
+// null) and its packed row maxima, consumed and zeroed here.
+struct AcceptSampledArgs {
+  int B, k;
+  const int32_t* drafts;       // [B][k]
+  int32_t* out_tokens;         // [B][k+1] in/out
+  float* probs;                // [B][k+1] in/out, or null
+  int32_t* n_emitted;          // [B]
+  const int32_t* seq_ids;
+  int32_t *seq_len, *pending, *sel_row;
+  int64_t* stats;
+  unsigned long long* best;
+  int* err;
+};
+int accept_sampled(const AcceptSampledArgs& a, cudaStream_t st);
+
 // Tree verify: the accepted path's K/V rows (all layers) moved from their
 // pass slots (seq_len_old + row) to consecutive positions (seq_len_old + j).
 // Skipped when the device error word is set (nothing was committed).

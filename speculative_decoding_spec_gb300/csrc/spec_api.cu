@@ -254,6 +254,19 @@ int launch_attention(int kv_dtype, AttnArgs at, unsigned int* counters, int wait
   return attention(at, st);
 }
 
+constexpr int SAMPLE_V_MAX = 1 << 21;      // weights of 40 bits sum to less than 2^61
+constexpr int SAMPLE_ROWS_MAX = 1 << 20;
+
+SampleArgs sample_args(int dtype, const void* logits, long long ld, int M, int V, const spec_sampling& s,
+                       int32_t* tokens, float* probs) {
+  SampleArgs a = {};
+  a.dtype = dtype == SPEC_F32 ? DT_F32 : DT_BF16;
+  a.logits = logits; a.ld = ld; a.M = M; a.V = V;
+  a.temperature = s.temperature; a.top_k = s.top_k; a.top_p = s.top_p; a.min_p = s.min_p;
+  a.uniform = s.uniform; a.tokens = tokens; a.probs = probs;
+  return a;
+}
+
 int run_attention(spec_ctx* c, AttnArgs at, cudaStream_t st, bool* flash = nullptr) {
   return launch_attention(c->m.kv_dtype, at, c->wk.attn_count, c->test_attn_wait, st, flash);
 }
@@ -300,7 +313,8 @@ AttnWork carve_attention(char* base, int B, int R, int nq, int nkv, int hd, int 
 // ---- the target pass: rows -> layers -> LM head + argmax + accept -----------
 int enqueue_pass(spec_ctx* c, int B, const int32_t* seq_ids, int R, int mode, const int32_t* tokens,
                  int32_t* out_tokens, int32_t* n_emitted, float* logits, cudaStream_t st, int top_m = 0,
-                 int tok_ld = 0, const int32_t* parents = nullptr) {
+                 int tok_ld = 0, const int32_t* parents = nullptr, const spec_sampling* sampling = nullptr,
+                 float* probs = nullptr) {
   const spec_model_desc& m = c->m;
   const Work& w = c->wk;
   const int M = B * R, d = m.d_model, hd = m.head_dim, nq = m.n_q_heads, nkv = m.n_kv_heads;
@@ -513,8 +527,8 @@ int enqueue_pass(spec_ctx* c, int B, const int32_t* seq_ids, int R, int mode, co
     t.path = w.path;
     t.path_ld = KMAX + 1;
   }
-  if (top_m > 0) {
-    // lenient accept: every row's logits kept, the accept runs in its own kernel
+  if (top_m > 0 || sampling) {
+    // lenient or sampled accept: every row's logits kept, the accept runs in its own kernel
     if (!g.Y) g.Y = w.lg;
     t.mode = TAIL_NONE;
   }
@@ -526,6 +540,14 @@ int enqueue_pass(spec_ctx* c, int B, const int32_t* seq_ids, int R, int mode, co
     ta.n_emitted = n_emitted; ta.seq_len = c->state.seq_len; ta.pending = c->state.pending; ta.sel_row = w.sel_row;
     ta.stats = c->state.stats; ta.err = w.err;
     LAUNCH(topm_accept(ta, st));
+  }
+  if (sampling) {
+    LAUNCH(sample_rows(sample_args(SPEC_F32, g.Y, m.vocab, M, m.vocab, *sampling, out_tokens, probs), 1, st));
+    AcceptSampledArgs aa = {};
+    aa.B = B; aa.k = R - 1; aa.drafts = tokens; aa.out_tokens = out_tokens; aa.probs = probs;
+    aa.n_emitted = n_emitted; aa.seq_ids = seq_ids; aa.seq_len = c->state.seq_len; aa.pending = c->state.pending;
+    aa.sel_row = w.sel_row; aa.stats = c->state.stats; aa.best = w.best; aa.err = w.err;
+    LAUNCH(accept_sampled(aa, st));
   }
   LAUNCH(commit_hidden(B, seq_ids, w.sel_row, w.x, d, c->w.g_final, m.rms_eps, c->state.hid, w.err, st));
   if (parents) {
@@ -853,6 +875,26 @@ spec_status spec_verify_tree(spec_ctx* c, int32_t B, const int32_t* seq_ids, int
                    });
 }
 
+spec_status spec_verify_sampled(spec_ctx* c, int32_t B, const int32_t* seq_ids, int32_t k, const int32_t* drafts,
+                                const spec_sampling* sp, int32_t* out_tokens, int32_t* n_emitted, float* probs,
+                                float* logits_dbg, void* stream) {
+  if (!batch_ok(c, B, seq_ids) || k < 0 || k > KMAX || k + 1 > c->pass_rows || !out_tokens || !n_emitted ||
+      (k > 0 && !drafts) || !sp || !sp->uniform)
+    return SPEC_EINVAL;
+  if (c->m.vocab > SAMPLE_V_MAX) return SPEC_EUNSUPPORTED;
+  const spec_sampling s = *sp;
+  cudaStream_t st = (cudaStream_t)stream;
+  return run_graph(c,
+                   key_of("verify_sampled",
+                          {B, k, (long long)seq_ids, (long long)drafts, (long long)s.temperature, (long long)s.top_k,
+                           (long long)s.top_p, (long long)s.min_p, (long long)s.uniform, (long long)out_tokens,
+                           (long long)n_emitted, (long long)probs, (long long)logits_dbg, (long long)st}),
+                   st, [&](cudaStream_t q) {
+                     return enqueue_pass(c, B, seq_ids, k + 1, TAIL_VERIFY, drafts, out_tokens, n_emitted,
+                                         logits_dbg, q, 0, 0, nullptr, &s, probs);
+                   });
+}
+
 spec_status spec_draft(spec_ctx* c, int32_t B, const int32_t* seq_ids, int32_t k, int32_t* drafts, void* stream) {
   if (!batch_ok(c, B, seq_ids) || k <= 0 || k > KMAX || !drafts) return SPEC_EINVAL;
   if (!c->has_drafter) return SPEC_ESTATE;
@@ -951,6 +993,30 @@ spec_status spec_attention(const spec_model_desc* m, const spec_kv_desc* kv, int
   at.out = out; at.err = w.err; at.standalone = 1;
   setup_device_attributes();
   if (launch_attention(m->kv_dtype, at, w.counters, 0, (cudaStream_t)stream) < 0) return SPEC_ECUDA;
+  return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ECUDA;
+}
+
+spec_status spec_sample(int32_t dtype, const void* logits, int64_t ld, int32_t M, int32_t V, const spec_sampling* s,
+                        int32_t* tokens, float* probs, void* stream) {
+  if ((dtype != SPEC_F32 && dtype != SPEC_BF16) || !logits || M <= 0 || V <= 0 || ld < V || !s || !s->uniform ||
+      !tokens)
+    return SPEC_EINVAL;
+  if (M > SAMPLE_ROWS_MAX || V > SAMPLE_V_MAX) return SPEC_EUNSUPPORTED;
+  if (sample_rows(sample_args(dtype, logits, ld, M, V, *s, tokens, probs), 0, (cudaStream_t)stream) < 0)
+    return SPEC_ECUDA;
+  return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ECUDA;
+}
+
+spec_status spec_accept_sampled(int32_t dtype, const void* logits, int64_t ld, int32_t B, int32_t k, int32_t V,
+                                const int32_t* drafts, const spec_sampling* s, int32_t* out_tokens,
+                                int32_t* n_emitted, float* probs, void* stream) {
+  if (B <= 0 || k < 0 || (k > 0 && !drafts) || !n_emitted) return SPEC_EINVAL;
+  if (k > 1023 || (long long)B * (k + 1) > SAMPLE_ROWS_MAX) return SPEC_EUNSUPPORTED;
+  const spec_status r = spec_sample(dtype, logits, ld, B * (k + 1), V, s, out_tokens, probs, stream);
+  if (r != SPEC_OK) return r;
+  AcceptSampledArgs a = {};
+  a.B = B; a.k = k; a.drafts = drafts; a.out_tokens = out_tokens; a.probs = probs; a.n_emitted = n_emitted;
+  if (accept_sampled(a, (cudaStream_t)stream) < 0) return SPEC_ECUDA;
   return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ECUDA;
 }
 

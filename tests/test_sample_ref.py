@@ -1,0 +1,77 @@
+"""The 64-bit sampling reference against closed forms, and the host-side
+refusals of the sampling entry points (no GPU)."""
+import ctypes as C
+
+import numpy as np
+import pytest
+import torch
+
+from speculative_decoding_spec_gb300 import binding
+from tests import sampling_ref as ref
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from speculative_decoding_spec_gb300 import build
+    build.build()
+    return binding.lib()
+
+
+def test_frequencies_are_the_softmax():
+    l = np.array([0.0, 1.0, -2.0, 1.0, 3.0])
+    n = 20000
+    got = np.bincount([ref.row(l, (i + 0.5) / n, 0.7)[0] for i in range(n)], minlength=5) / n
+    w = np.exp(l / 0.7)
+    # an inverse CDF on n equal steps is within one step of each probability
+    assert np.abs(got - w / w.sum()).max() <= 1.0 / n
+
+
+def test_filters_by_hand():
+    l = np.log([0.1, 0.4, 0.2, 0.2, 0.1])
+    assert [ref.row(l, u, k=2)[0] for u in (0.0, 0.6, 0.7, 0.99)] == [1, 1, 2, 2]      # the tie at 0.2: lower index
+    assert {ref.row(l, u, p=0.5)[0] for u in np.linspace(0, 0.999, 50)} == {1, 2}      # 0.4 < 0.5, 0.6 reaches it
+    assert {ref.row(l, u, p=0.0)[0] for u in np.linspace(0, 0.999, 50)} == {1}
+    assert {ref.row(l, u, q=0.49)[0] for u in np.linspace(0, 0.999, 50)} == {1, 2, 3}  # at least 0.49 * 0.4
+    assert ref.row(l, 0.3, T=0.0)[:2] == (1, 1.0)
+    assert abs(ref.row(l, 0.3, k=2)[1] - 0.4 / 0.6) < 1e-12
+
+
+def test_rows_without_a_distribution():
+    inf = np.inf
+    assert ref.row(np.array([-inf, -inf]), 0.5)[0] == -1
+    assert ref.row(np.array([0.0, np.nan]), 0.5)[0] == -1
+    assert ref.row(np.array([0.0, 1.0]), 0.5, T=-1.0)[0] == -1
+    assert ref.row(np.array([0.0, inf, 3.0, inf]), 0.6)[0] == 3
+
+
+def test_accept_walk():
+    t = np.array([[5, 6, 7], [5, 6, 7], [-1, 6, 7], [5, -1, 7]])
+    d = np.array([[5, 6], [5, 9], [1, 2], [5, 6]])
+    out, n, _ = ref.accept(t, np.ones((4, 3)), d)
+    assert n.tolist() == [3, 2, 0, 1]
+    assert out.tolist() == [[5, 6, 7], [5, 6, -1], [-1, -1, -1], [5, -1, -1]]
+
+
+def test_host_refusals(lib):
+    E, U = binding.SPEC_EINVAL, binding.SPEC_EUNSUPPORTED
+    s = binding.spec_sampling(uniform=256)       # never read: every call below is refused on the host
+    none = binding.spec_sampling()
+    p = 256
+    sample = lambda dt=0, lg=p, ld=8, M=1, V=8, st=s, tok=p: lib.spec_sample(dt, lg, ld, M, V, C.byref(st), tok, p, None)
+    assert sample(dt=2) == E and sample(lg=None) == E and sample(ld=7) == E and sample(M=0) == E
+    assert sample(V=0) == E and sample(st=none) == E and sample(tok=None) == E
+    assert lib.spec_sample(0, p, 8, 1, 8, None, p, p, None) == E
+    assert sample(V=(1 << 21) + 1, ld=1 << 22) == U and sample(M=(1 << 20) + 1) == U
+    acc = lambda B=1, k=2, d=p, st=s, out=p, ne=p: lib.spec_accept_sampled(0, p, 8, B, k, 8, d, C.byref(st), out, ne,
+                                                                           None, None)
+    assert acc(B=0) == E and acc(k=-1) == E and acc(d=None) == E and acc(st=none) == E
+    assert acc(out=None) == E and acc(ne=None) == E and acc(k=1024) == U and acc(B=1 << 20) == U
+    assert lib.spec_verify_sampled(None, 1, None, 0, None, C.byref(s), None, None, None, None, None) == E
+
+
+def test_binding_refusals(lib):
+    x, u = torch.zeros(2, 8), torch.zeros(2)
+    with pytest.raises(binding.SpecError):
+        binding.spec_sample(x, u)                # not on a GPU
+    with pytest.raises(binding.SpecError):
+        binding.spec_accept_sampled(x, torch.zeros(1, 1, dtype=torch.int64), u)
