@@ -322,6 +322,33 @@ spec_status spec_linear(const spec_matrix *w, int32_t N, int32_t K, const float 
                         const float *gain, float eps, float *y, void *workspace, size_t ws_bytes,
                         void *stream);
 
+/* Low-rank adapters ("device"): a [n_adapters][rank][K], b [n_adapters][N][rank]
+ * in dtype (SPEC_F32 or SPEC_BF16), scale float [n_adapters] or NULL (1).
+ * rank a multiple of 8, 8..128 (adapters of a smaller rank are padded with
+ * zeros). */
+typedef struct {
+    int32_t dtype;
+    int32_t n_adapters;
+    int32_t rank;
+    const void *a;
+    const void *b;
+    const float *scale;
+} spec_lora;
+
+/* spec_linear with a low-rank adapter of its own for each row, as the requests
+ * of one batch bring them: y[m][n] = W[n] . xn[m] + scale_i * b_i[n] . (a_i xn[m])
+ * with i = ids[m] ("device" int32 [M]; -1: no adapter for this row). W is
+ * streamed once for all rows, an adapter once for the rows that use it. The
+ * adapter's sums are binary32. Arguments and limits otherwise as spec_linear;
+ * x, y, gain, a, b and the workspace are 16-byte aligned. workspace ("device",
+ * ws_bytes >= spec_linear_lora_workspace_bytes(N, K, M, rank)) needs no
+ * initialisation. An id outside [-1, n_adapters) counts as -1 and is recorded in
+ * the workspace's first int (SPEC_ECAPACITY's device code 2, else 0). */
+size_t spec_linear_lora_workspace_bytes(int32_t N, int32_t K, int32_t M, int32_t rank);
+spec_status spec_linear_lora(const spec_matrix *w, int32_t N, int32_t K, const float *x, int32_t M,
+                             const float *gain, float eps, const spec_lora *lora, const int32_t *ids,
+                             float *y, void *workspace, size_t ws_bytes, void *stream);
+
 /* spec_linear without a caller workspace, for callers that cannot allocate
  * device memory (a host application that owns the whole device-memory budget,
  * a plugin whose framework allocator must see every allocation, code that must

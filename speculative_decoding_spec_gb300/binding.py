@@ -24,7 +24,8 @@ EXPORTS = ["spec_workspace_bytes", "spec_init", "spec_prefill", "spec_draft", "s
            "spec_kernel_launches", "spec_status_str", "spec_destroy", "spec_linear",
            "spec_linear_workspace_bytes", "spec_linear_noalloc", "spec_set_option",
            "spec_attention_workspace_bytes", "spec_attention", "spec_verify_topm", "spec_verify_tree",
-           "spec_verify_sampled", "spec_sample", "spec_accept_sampled"]
+           "spec_verify_sampled", "spec_sample", "spec_accept_sampled",
+           "spec_linear_lora", "spec_linear_lora_workspace_bytes"]
 SPEC_OPT_GRAPHS, SPEC_OPT_PREFETCH, SPEC_OPT_TEST_ATTN_WAIT = 1, 4, 8
 SPEC_OPT_WIDE_TRACE = 7
 SPEC_LINEAR_NOALLOC_MAX_ROWS = 523776
@@ -78,6 +79,11 @@ class spec_stats_t(C.Structure):
 
 class spec_sampling(C.Structure):
     _fields_ = [(n, C.c_void_p) for n in ("temperature", "top_k", "top_p", "min_p", "uniform")]
+
+
+class spec_lora(C.Structure):
+    _fields_ = [("dtype", C.c_int32), ("n_adapters", C.c_int32), ("rank", C.c_int32), ("a", C.c_void_p),
+                ("b", C.c_void_p), ("scale", C.c_void_p)]
 
 
 _lib = None
@@ -141,6 +147,11 @@ def lib():
     L.spec_sample.argtypes = [i32, p, C.c_int64, i32, i32, C.POINTER(spec_sampling), p, p, p]
     L.spec_accept_sampled.restype = st
     L.spec_accept_sampled.argtypes = [i32, p, C.c_int64, i32, i32, i32, p, C.POINTER(spec_sampling), p, p, p, p]
+    L.spec_linear_lora_workspace_bytes.restype = C.c_size_t
+    L.spec_linear_lora_workspace_bytes.argtypes = [i32, i32, i32, i32]
+    L.spec_linear_lora.restype = st
+    L.spec_linear_lora.argtypes = [C.POINTER(spec_matrix), i32, i32, p, i32, p, C.c_float, C.POINTER(spec_lora), p, p,
+                                   p, C.c_size_t, p]
     L.spec_destroy.restype = None
     L.spec_destroy.argtypes = [p]
     _lib = L
@@ -332,6 +343,60 @@ def spec_accept_sampled(logits: torch.Tensor, drafts: torch.Tensor, uniform: tor
         check(fn, lib().spec_accept_sampled(dt, _ptr(logits), ld, B, k, V, _ptr(drafts) if k else None, C.byref(s),
                                             _ptr(out), _ptr(ne), _ptr(probs), st))
     return out, ne, probs
+
+
+class Lora:
+    """Low-rank adapters of one projection: a [n][rank][K] and b [n][N][rank]
+    (float32 or bfloat16), scale float32 [n] or None (1)."""
+
+    def __init__(self, a: torch.Tensor, b: torch.Tensor, scale: Optional[torch.Tensor] = None):
+        fn = "Lora"
+        _need(fn, a.dim() == 3 and b.dim() == 3 and a.dtype == b.dtype and a.dtype in _LOGIT_DTYPES and
+              a.shape[0] == b.shape[0] and a.shape[1] == b.shape[2],
+              "a [n][rank][K] and b [n][N][rank] must be float32 or bfloat16 and agree")
+        _need(fn, a.is_cuda and a.device == b.device and a.is_contiguous() and b.is_contiguous(),
+              "a and b must be contiguous on one GPU")
+        _need(fn, scale is None or (scale.dtype == torch.float32 and scale.shape == a.shape[:1] and
+                                    scale.is_contiguous() and scale.device == a.device),
+              "scale must be a contiguous float32 tensor [n] beside them")
+        self.a, self.b, self.scale = a, b, scale
+        self.n, self.rank, self.K = a.shape
+        self.N = b.shape[1]
+        self.desc = spec_lora(_LOGIT_DTYPES[a.dtype], self.n, self.rank, _ptr(a), _ptr(b), _ptr(scale))
+
+
+def spec_linear_lora(w, x: torch.Tensor, lora: Lora, ids: torch.Tensor, gain: Optional[torch.Tensor] = None,
+                     eps: float = 1e-6, layer: int = 0, y: Optional[torch.Tensor] = None,
+                     workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """spec_linear plus each row's own low-rank adapter: ids int32 [M] picks one
+    of lora's adapters for every row, -1 none (include/spec.h spec_linear_lora).
+    workspace (uint8, spec_linear_lora_workspace_bytes) is allocated on the
+    call's stream when not given; its first int records an id out of range."""
+    fn = "spec_linear_lora"
+    L = lib()
+    dev = x.device
+    _need(fn, x.is_cuda and x.dim() == 2 and x.dtype == torch.float32 and x.is_contiguous() and x.shape[1] == w.K,
+          "x must be a contiguous float32 CUDA tensor [M][K]")
+    M = x.shape[0]
+    _need(fn, lora.K == w.K and lora.N == w.N and lora.a.device == dev and w.data.device == dev,
+          "the adapters must have the projection's N and K, on its device")
+    _need(fn, ids.dtype == torch.int32 and ids.shape == (M,) and ids.is_contiguous() and ids.device == dev,
+          "ids must be a contiguous int32 tensor [M] beside x")
+    _need(fn, gain is None or (gain.dtype == torch.float32 and gain.shape == (w.K,) and gain.is_contiguous() and
+                               gain.device == dev), "gain must be a contiguous float32 tensor [K] beside x")
+    _need(fn, y is None or (y.dtype == torch.float32 and y.shape == (M, w.N) and y.is_contiguous() and
+                            y.device == dev), "y must be a contiguous float32 tensor [M][N] beside x")
+    _need(fn, 0 <= layer < w.L, "layer out of range")
+    m = spec_matrix(DTYPES[w.dtype], _ptr(w.data[layer]), _ptr(w.scales[layer]) if w.scales is not None else None)
+    with _on(x, stream) as st:
+        if y is None:
+            y = torch.empty((M, w.N), dtype=torch.float32, device=dev)
+        if workspace is None:
+            n = L.spec_linear_lora_workspace_bytes(w.N, w.K, M, lora.rank)
+            workspace = torch.empty(max(n, 1), dtype=torch.uint8, device=dev)
+        check(fn, L.spec_linear_lora(C.byref(m), w.N, w.K, _ptr(x), M, _ptr(gain), eps, C.byref(lora.desc), _ptr(ids),
+                                     _ptr(y), _ptr(workspace), workspace.numel(), st))
+    return y
 
 
 _LINEAR_WS = {}

@@ -246,6 +246,26 @@ struct AcceptSampledArgs {
 };
 int accept_sampled(const AcceptSampledArgs& a, cudaStream_t st);
 
+// Low-rank adapters beside a shared projection (lora.cu).
+struct LoraArgs {
+  int dtype;                   // of a and b: DT_F32 or DT_BF16
+  int M, N, K, rank, n_adapters;
+  const void *a, *b;           // [n_adapters][rank][K], [n_adapters][N][rank]
+  const float* scale;          // [n_adapters] or null (1)
+  const int32_t* ids;          // [M] adapter of each row, -1: none
+  const float* x;              // [M][K]
+  const float* gain;           // [K] or null
+  float eps;
+  float* t;                    // [M][rank] scratch
+  float* y;                    // [M][N]
+  int add;                     // expand: y += (else y =)
+  unsigned int* cnt;           // the projection's arrival counters, cleared by the shrink
+  int n_cnt;
+  int* err;                    // set by the shrink: an id out of range, or 0
+};
+int lora_shrink(const LoraArgs& a, cudaStream_t st);
+int lora_expand(const LoraArgs& a, cudaStream_t st);
+
 // Tree verify: the accepted path's K/V rows (all layers) moved from their
 // pass slots (seq_len_old + row) to consecutive positions (seq_len_old + j).
 // Skipped when the device error word is set (nothing was committed).

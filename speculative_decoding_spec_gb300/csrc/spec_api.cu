@@ -724,6 +724,34 @@ bool batch_ok(const spec_ctx* c, int B, const int32_t* seq_ids) {
   return c && B > 0 && B <= c->B_max && seq_ids;
 }
 
+// spec_linear's launch on its workspace
+size_t linear_counters(int N) { return (size_t)N / 8 + 64; }
+GemvArgs linear_args(const spec_matrix& w, int N, int K, const float* x, int M, const float* gain, float eps, float* y,
+                     void* workspace) {
+  GemvArgs g = {};
+  g.X = x; g.ldx = K; g.M = M; g.N = N; g.K = K; g.W = M_(w); g.gain = gain; g.eps = eps;
+  g.epi = EPI_STORE; g.Y = y; g.ldy = N; g.pdl = 0; g.prefetch = 0;
+  g.tc_fix = (float*)workspace;
+  g.tc_cnt = (unsigned int*)((char*)workspace + gemv_tc_fixup_bytes());
+  if (M > 8 || ((long long)N * K >= WIDE_MIN_ELEMS && K >= WIDE_MIN_K)) {
+    char* p = (char*)workspace + gemv_tc_fixup_bytes() +
+              (linear_counters(N) * sizeof(unsigned int) + 255) / 256 * 256 + 256;
+    g.wide.fix = (float*)p;
+    p += (gemv_wide_fix_bytes() + 255) / 256 * 256;
+    g.wide.xs = (uint16_t*)p;
+    p += (gemv_wide_xs_bytes(K) + 255) / 256 * 256;
+    g.wide.rms = (float*)p;
+    g.wide.kmax = K;
+  }
+  return g;
+}
+
+bool aligned16(std::initializer_list<const void*> ps) {
+  for (const void* p : ps)
+    if ((uintptr_t)p & 15) return false;
+  return true;
+}
+
 }  // namespace
 
 extern "C" {
@@ -941,23 +969,46 @@ spec_status spec_linear(const spec_matrix* w, int32_t N, int32_t K, const float*
                         float eps, float* y, void* workspace, size_t ws_bytes, void* stream) {
   if (!w || !x || !y || N <= 0 || K <= 0 || M <= 0 || M > 64 || !mat_ok(*w, K)) return SPEC_EINVAL;
   if (!workspace || ws_bytes < spec_linear_workspace_bytes(N, K, M)) return SPEC_ECAPACITY;
-  GemvArgs g = {};
-  g.X = x; g.ldx = K; g.M = M; g.N = N; g.K = K; g.W = M_(*w); g.gain = gain; g.eps = eps;
-  g.epi = EPI_STORE; g.Y = y; g.ldy = N; g.pdl = 0; g.prefetch = 0;
-  g.tc_fix = (float*)workspace;
-  g.tc_cnt = (unsigned int*)((char*)workspace + gemv_tc_fixup_bytes());
-  if (M > 8 || ((long long)N * K >= WIDE_MIN_ELEMS && K >= WIDE_MIN_K)) {
-    char* p = (char*)workspace + gemv_tc_fixup_bytes() +
-              (((size_t)N / 8 + 64) * sizeof(unsigned int) + 255) / 256 * 256 + 256;
-    g.wide.fix = (float*)p;
-    p += (gemv_wide_fix_bytes() + 255) / 256 * 256;
-    g.wide.xs = (uint16_t*)p;
-    p += (gemv_wide_xs_bytes(K) + 255) / 256 * 256;
-    g.wide.rms = (float*)p;
-    g.wide.kmax = K;
-  }
+  GemvArgs g = linear_args(*w, N, K, x, M, gain, eps, y, workspace);
   setup_device_attributes();
   if (gemv(g, (cudaStream_t)stream) < 0) return SPEC_ECUDA;
+  return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ECUDA;
+}
+
+// workspace: error word, the shrink's rows, spec_linear's workspace
+static size_t lora_head_bytes(int M, int rank) { return 256 + ((size_t)M * rank * sizeof(float) + 255) / 256 * 256; }
+
+size_t spec_linear_lora_workspace_bytes(int32_t N, int32_t K, int32_t M, int32_t rank) {
+  if (rank <= 0) return 0;
+  const size_t n = spec_linear_workspace_bytes(N, K, M);
+  return n ? n + lora_head_bytes(M, rank) : 0;
+}
+
+spec_status spec_linear_lora(const spec_matrix* w, int32_t N, int32_t K, const float* x, int32_t M, const float* gain,
+                             float eps, const spec_lora* lora, const int32_t* ids, float* y, void* workspace,
+                             size_t ws_bytes, void* stream) {
+  if (!w || !x || !y || N <= 0 || K <= 0 || M <= 0 || M > 64 || !mat_ok(*w, K) || !lora || !ids || !lora->a ||
+      !lora->b || lora->n_adapters <= 0 || lora->rank <= 0 ||
+      (lora->dtype != SPEC_F32 && lora->dtype != SPEC_BF16) ||
+      !aligned16({w->data, w->scales, x, y, gain, lora->a, lora->b, workspace}))
+    return SPEC_EINVAL;
+  if (lora->rank % 8 || lora->rank > 128) return SPEC_EUNSUPPORTED;
+  if (!workspace || ws_bytes < spec_linear_lora_workspace_bytes(N, K, M, lora->rank)) return SPEC_ECAPACITY;
+  cudaStream_t st = (cudaStream_t)stream;
+  GemvArgs g = linear_args(*w, N, K, x, M, gain, eps, y, (char*)workspace + lora_head_bytes(M, lora->rank));
+  LoraArgs a = {};
+  a.dtype = lora->dtype == SPEC_F32 ? DT_F32 : DT_BF16;
+  a.M = M; a.N = N; a.K = K; a.rank = lora->rank; a.n_adapters = lora->n_adapters;
+  a.a = lora->a; a.b = lora->b; a.scale = lora->scale; a.ids = ids; a.x = x; a.gain = gain; a.eps = eps;
+  a.err = (int*)workspace; a.t = (float*)((char*)workspace + 256); a.y = y;
+  a.cnt = g.tc_cnt; a.n_cnt = (int)linear_counters(N);
+  a.add = N % 4 != 0;
+  g.epi = a.add ? EPI_STORE : EPI_ADD;
+  setup_device_attributes();
+  if (lora_shrink(a, st) < 0) return SPEC_ECUDA;
+  if (!a.add && lora_expand(a, st) < 0) return SPEC_ECUDA;
+  if (gemv(g, st) < 0) return SPEC_ECUDA;
+  if (a.add && lora_expand(a, st) < 0) return SPEC_ECUDA;
   return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ECUDA;
 }
 

@@ -1,5 +1,5 @@
 """The 64-bit sampling reference against closed forms, and the host-side
-refusals of the sampling entry points (no GPU)."""
+refusals of the per-request entry points (no GPU)."""
 import ctypes as C
 
 import numpy as np
@@ -75,3 +75,22 @@ def test_binding_refusals(lib):
         binding.spec_sample(x, u)                # not on a GPU
     with pytest.raises(binding.SpecError):
         binding.spec_accept_sampled(x, torch.zeros(1, 1, dtype=torch.int64), u)
+
+
+def test_lora_host_refusals(lib):
+    E, U, CAP = binding.SPEC_EINVAL, binding.SPEC_EUNSUPPORTED, binding.SPEC_ECAPACITY
+    p = 256                                       # never read: every call below is refused on the host
+    w = binding.spec_matrix(1, p, None)
+
+    def call(w=w, N=64, K=64, x=p, M=4, gain=None, dt=1, n=2, r=8, a=p, b=p, ids=p, y=p, ws=p, nws=0):
+        lo = binding.spec_lora(dt, n, r, a, b, None)
+        return lib.spec_linear_lora(C.byref(w), N, K, x, M, gain, 1e-6, C.byref(lo), ids, y, ws, nws, None)
+    assert call() == CAP and call(ws=None) == CAP  # a workspace too small, or none
+    for kw in (dict(N=0), dict(K=0), dict(K=12), dict(x=None), dict(M=0), dict(M=65), dict(dt=2), dict(n=0), dict(r=0),
+               dict(a=None), dict(b=None), dict(ids=None), dict(y=None), dict(x=260), dict(a=264), dict(b=258),
+               dict(y=252), dict(gain=4), dict(ws=8)):
+        assert call(**kw) == E, kw
+    assert call(r=12) == U and call(r=136) == U
+    assert lib.spec_linear_lora(C.byref(w), 64, 64, p, 4, None, 1e-6, None, p, p, p, 1 << 30, None) == E
+    assert lib.spec_linear_lora_workspace_bytes(0, 64, 4, 8) == 0
+    assert lib.spec_linear_lora_workspace_bytes(64, 64, 4, 0) == 0
