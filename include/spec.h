@@ -178,7 +178,7 @@ typedef struct {
  *               mass (u below 0 or NaN counts as 0, u >= 1 takes the last kept
  *               token).
  * Values outside these ranges (NaN included) leave top_k, top_p and min_p off.
- * Weights are held in 40 fraction bits of the largest (smaller ones count as
+ * Weights are held in 44 fraction bits of the largest (smaller ones count as
  * zero) and their sums are exact, so a row's token depends on nothing but the
  * row. -inf logits are never chosen; +inf logits share the whole mass equally;
  * a row with a NaN, or with nothing above -inf, has no distribution. */
@@ -407,7 +407,7 @@ spec_status spec_attention(const spec_model_desc *m, const spec_kv_desc *kv, int
  * with its own settings. tokens ("device" int32 [M]) gets the token, -1 for a
  * row without a distribution; probs ("device" float [M], may be NULL) the
  * probability it had (its weight over the kept mass), 0 for such a row.
- * Needs no workspace. V <= 2^21, M <= 2^20. */
+ * Needs no workspace. V <= 2^19, M <= 2^20. */
 spec_status spec_sample(int32_t dtype, const void *logits, int64_t ld, int32_t M, int32_t V,
                         const spec_sampling *s, int32_t *tokens, float *probs, void *stream);
 

@@ -227,6 +227,7 @@ struct SampleArgs {
   int32_t* tokens;             // [M]
   float* probs;                // [M] or null
 };
+void setup_sample_attributes();
 int sample_rows(const SampleArgs& a, int pdl, cudaStream_t st);
 
 // Sampled accept: out_tokens holds every row's sample on entry, the emitted

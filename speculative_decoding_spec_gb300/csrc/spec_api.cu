@@ -254,7 +254,7 @@ int launch_attention(int kv_dtype, AttnArgs at, unsigned int* counters, int wait
   return attention(at, st);
 }
 
-constexpr int SAMPLE_V_MAX = 1 << 21;      // weights of 40 bits sum to less than 2^61
+constexpr int SAMPLE_V_MAX = 1 << 19;      // weights of 45 bits sum to less than 2^64
 constexpr int SAMPLE_ROWS_MAX = 1 << 20;
 
 SampleArgs sample_args(int dtype, const void* logits, long long ld, int M, int V, const spec_sampling& s,
@@ -286,6 +286,7 @@ void spec::setup_device_attributes() {
   setup_draft_attributes();
   setup_attn_flash_attributes();
   setup_moe_attributes();
+  setup_sample_attributes();
   done[dev] = true;
 }
 
@@ -1053,6 +1054,7 @@ spec_status spec_sample(int32_t dtype, const void* logits, int64_t ld, int32_t M
       !tokens)
     return SPEC_EINVAL;
   if (M > SAMPLE_ROWS_MAX || V > SAMPLE_V_MAX) return SPEC_EUNSUPPORTED;
+  setup_device_attributes();
   if (sample_rows(sample_args(dtype, logits, ld, M, V, *s, tokens, probs), 0, (cudaStream_t)stream) < 0)
     return SPEC_ECUDA;
   return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ECUDA;

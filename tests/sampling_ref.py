@@ -2,14 +2,15 @@
 (spec_sampling), written with library sorts and sums, and how near a row's
 decisions are to a border.
 
-The kernel evaluates a weight to a relative 2^-32 and an absolute 2^-40 (its
-unit; the largest weight is 1). A sum of up to V weights, compared with another
-one, is therefore off by at most 2 * (Z * 2^-32 + V * 2^-40), Z the whole mass: a
-draw is compared only where it is further from its borders than that, `slack`.
-Where top-p's cut is that near to a border, the kernel may cut up to 2 * slack of
-mass and one token earlier or later; the kept mass and each partial sum then move
-by no more, and the draw is compared where its borders are that much further. min-p compares logits, so its border is the rounding
-of a 64-bit logarithm: 2^-45 of the threshold."""
+The kernel evaluates a weight to a relative 2^-36 and rounds it down to its unit,
+an absolute 2^-44 (the largest weight is 1). A sum of up to V weights, compared
+with another one, is therefore off by at most 2 * (Z * 2^-36 + V * 2^-44), Z the
+whole mass: a draw is compared only where it is further from its borders than
+that, `slack`. Where top-p's cut is that near to a border, the kernel may cut up
+to 2 * slack of mass and one token earlier or later; the kept mass and each
+partial sum then move by no more, and the draw is compared where its borders are
+that much further. A row is compared where no weight is within
+2^-36 min_p + 2^-44 of min_p."""
 import numpy as np
 
 
@@ -31,7 +32,7 @@ def row(l, u, T=1.0, k=0, p=1.0, q=0.0):
     if T < 1e-5:
         return int(np.argmax(l)), 1.0, True
     w = weights(l, T)
-    slack = 2.0 * (w.sum() * 2.0 ** -32 + n * 2.0 ** -40)
+    slack = 2.0 * (w.sum() * 2.0 ** -36 + n * 2.0 ** -44)
     order = np.lexsort((np.arange(n), -l))
     if 0 < k < n:
         order = order[:k]
@@ -46,16 +47,16 @@ def row(l, u, T=1.0, k=0, p=1.0, q=0.0):
     keep = np.zeros(n, bool)
     keep[order] = True
     if q > 0.0:
-        thr = l.max() + T * np.log(min(q, 1.0))
-        finite = l[np.isfinite(l)]
-        decided &= q >= 1.0 or len(finite) == 0 or np.abs(finite - thr).min() > abs(thr) * 2.0 ** -45
-        keep &= l >= thr
-    at = np.flatnonzero(keep & (w > 2.0 ** -41))
+        q = min(q, 1.0)
+        decided &= q == 1.0 or np.abs(w - q).min() > q * 2.0 ** -36 + 2.0 ** -44
+        keep &= w >= q
+    at = np.flatnonzero(keep & (w > 2.0 ** -44))
     cum = np.cumsum(w[at])
     u = min(max(u, 0.0), 1.0) if u == u else 0.0
     t = u * cum[-1]
     j = min(int(np.searchsorted(cum, t, "right")), len(at) - 1)
     near = np.abs(cum[:-1] - t)
+    decided &= moved <= cum[-1] * 2.0 ** -24      # (the probability follows the kept mass)
     decided &= len(near) == 0 or u == 0.0 or u == 1.0 or near.min() > slack + 2.0 * moved
     return int(at[j]), float(w[at[j]] / cum[-1]), bool(decided)
 

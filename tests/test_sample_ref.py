@@ -61,7 +61,7 @@ def test_host_refusals(lib):
     assert sample(dt=2) == E and sample(lg=None) == E and sample(ld=7) == E and sample(M=0) == E
     assert sample(V=0) == E and sample(st=none) == E and sample(tok=None) == E
     assert lib.spec_sample(0, p, 8, 1, 8, None, p, p, None) == E
-    assert sample(V=(1 << 21) + 1, ld=1 << 22) == U and sample(M=(1 << 20) + 1) == U
+    assert sample(V=(1 << 19) + 1, ld=1 << 22) == U and sample(M=(1 << 20) + 1) == U
     acc = lambda B=1, k=2, d=p, st=s, out=p, ne=p: lib.spec_accept_sampled(0, p, 8, B, k, 8, d, C.byref(st), out, ne,
                                                                            None, None)
     assert acc(B=0) == E and acc(k=-1) == E and acc(d=None) == E and acc(st=none) == E
