@@ -15,8 +15,8 @@
 // sampling: it is kept with probability p(d), and a rejected position emits a
 // token distributed as p without d.
 //
-// Weights are integers: w_i in units of 2^-44 of the largest, rounded down (a
-// choice: tokens below 2^-44 of the most likely one count as zero). Their sums
+// Weights are integers: w_i in units of 2^-44 of the largest, rounded (a
+// choice: tokens below 2^-45 of the most likely one count as zero). Their sums
 // are exact, so the cut and the token do not depend on the order of the
 // additions, the number of CTAs or the other rows of the batch. The weight
 // itself is evaluated to about 2^-37 (the exponent as a float pair, a table of
@@ -30,13 +30,16 @@
 // Without top-k and top-p, scan 2 sums the weights and the warp that holds the
 // drawn mass finds the token. With them, scan 2 lists the tokens down to the
 // k-th largest segment maximum -- at least k tokens, and rarely many more -- (top-p
-// alone: down to the median one, and sums the weights too), and the first CTA
+// alone: down to the 128th, and sums the weights too), and the first CTA
 // sorts, cuts and draws among those alone. Where they are too many, or hold too
 // little mass for top-p, the cut is found in the whole row: a histogram of 2048
 // bins, linear in the exponent, of counts or of exact masses (three 15-bit
-// digits), then a radix search of the keys inside one bin.
+// digits), then the tokens of the one bin in which the cut lies are listed and
+// sorted (a radix search of their keys where they are too many).
 #include <cooperative_groups.h>
 
+#include <algorithm>
+#include <mutex>
 #include <utility>
 
 #include "common.cuh"
@@ -54,15 +57,20 @@ constexpr int NW = NT / 32;
 constexpr int BINS = 2048;
 constexpr int BPT = BINS / NT;      // consecutive bins of a thread
 constexpr int WBITS = 44;           // fraction bits of a weight
-constexpr int DIGIT = 15;           // bits of a mass digit: 2^17 tokens of a CTA sum in 32 bits
+constexpr int DIGIT = 15;           // bits of a mass digit
+constexpr int DIGIT_TOKENS = 120000;  // tokens of a CTA whose digits surely sum in 32 bits
 constexpr int TAB_LOG = 12;
 constexpr int TAB = 1 << TAB_LOG;   // 2^(-j/4096)
 constexpr int MAX_C = 16;           // CTAs on one row (a thread-block cluster)
 constexpr int LIST = 1024;          // tokens a CTA lists
 constexpr int FEW = 2048;           // tokens the first CTA sorts
+constexpr int COUNTED = NT / 2;     // at most so many are counted instead
 constexpr int SEG_MAX = 1024;       // segments of a row (the elements of 1, 2, 4 or 8 lanes)
 constexpr int SEG_BINS = NT;        // bins of the segment maxima
+constexpr int NUCLEUS = 128;        // tokens listed at first for top-p alone
 constexpr float Z_END = 46.f;       // weights are zero beyond this exponent
+constexpr int CHUNK = 8;            // vectors of a lane whose sum is kept apart, doubled until
+constexpr int CHUNKS = 32;          // a warp's part has at most 32 chunks
 constexpr int IDX_BITS = 19;        // V <= 2^19: an index and a 45-bit weight share a word
 
 // 2^(44 - j/4096), from the exponential series at compile time.
@@ -85,6 +93,13 @@ constexpr Table make_table() {
 }
 __device__ const Table g_table = make_table();
 
+// A cut of the order: tokens with a smaller key, and those of this key up to
+// this index, are kept.
+struct Cut {
+  uint32_t key;
+  int idx;
+};
+
 struct Shared {
   ull tab[TAB];
   union {
@@ -104,7 +119,8 @@ struct Shared {
   int gathered;              // first CTA: tokens listed by all
   int few;                   // the first CTA's verdict: the listed tokens suffice
   unsigned int seg_bins[SEG_BINS];
-  uint32_t threshold;        // largest rank key listed
+  Cut cut;                   // pushed by the first CTA: the cut of the row
+  ull chunk[NW][CHUNKS];     // sums of the warps' chunks
   ull wsum[NW];
   ull total;                 // this CTA's sum, read by the cluster
   int bin;                   // crossing bin
@@ -119,11 +135,17 @@ struct Shared {
 struct Scale {
   float m, sh, sl, bins;
   // Monotone in x (each rounding is), so bins are ranges of the order.
+  SPEC_DEV float place(float x) const { return (m - x) * sh * bins; }
   SPEC_DEV int bin(float x) const {
     if (m == INFINITY) return x == INFINITY ? 0 : BINS - 1;
-    return (int)fminf((m - x) * sh * bins, (float)(BINS - 1));
+    return (int)fminf(place(x), (float)(BINS - 1));
   }
 };
+
+// 2^(n-1), half a unit before the shift by n: a weight is rounded, not cut off.
+// (The bias of V cut-off weights would move a border among the unlikely tokens
+// by as much as their weights.) From n = 31 on a little less, within 32 bits.
+SPEC_DEV float half_unit(int n) { return __int_as_float((min(n, 30) << 23) + 0x3f000000); }
 
 // The weight of logit x in units of 2^-WBITS. z is formed as a float pair (an
 // exact difference, an exact product), split into n + j/4096 + g, and
@@ -134,25 +156,85 @@ SPEC_DEV ull weight(const Scale& r, const ull* tab, float x, float* val = nullpt
     if (val) *val = x == INFINITY ? 1.f : 0.f;
     return x == INFINITY ? 1ull << WBITS : 0ull;
   }
-  const float d = r.m - x;
-  const float bb = d - r.m;
-  const float e = (r.m - (d - bb)) + (-x - bb);       // d + e == m - x
-  float p = d * r.sh;
+  const float d = __fsub_rn(r.m, x);
+  const float bb = __fsub_rn(d, r.m);
+  const float e = __fadd_rn(__fsub_rn(r.m, __fsub_rn(d, bb)), __fsub_rn(-x, bb));   // d + e == m - x
+  float p = __fmul_rn(d, r.sh);
   const float pe = fmaf(e, r.sh, fmaf(d, r.sl, fmaf(d, r.sh, -p)));
   p = fminf(p, 63.f);
   // round(4096 p) in the low bits of p + 1.5 * 2^(23 - 12)
-  const float t = p + 12582912.f / TAB;
-  const int j = __float_as_int(t) & 0x3fffff;
-  const float g = (p - (t - 12582912.f / TAB)) + pe;  // |g| <= 2^-13
-  const float q = fmaf(g, 0.240226507f, -0.693147181f) * g;   // 2^-g - 1
+  const float t = __fadd_rn(p, 12582912.f / TAB);
+  const float g = __fadd_rn(__fsub_rn(p, __fsub_rn(t, 12582912.f / TAB)), pe);      // |g| <= 2^-13
+  const float q = __fmul_rn(fmaf(g, 0.240226507f, -0.693147181f), g);               // 2^-g - 1
+  const uint32_t j = __float_as_uint(t);
   const ull T = tab[j & (TAB - 1)];
-  const int n = j >> TAB_LOG;
+  const int n = (j >> TAB_LOG) & 63;
   // the table value as a float: its 24 leading bits (2^43 <= T <= 2^44)
   const float Tf = __uint_as_float((uint32_t)(T >> (WBITS - 24)) + 0x4a800000u) * (float)(1 << (WBITS - 24));
-  const ull v = T + (long long)__float2int_rn(Tf * q);
+  const ull v = T + (long long)__float2int_rn(fmaf(Tf, q, half_unit(n)));
   if (val) *val = fmaf(Tf, q, Tf) * __int_as_float((127 - WBITS - n) << 23);
   return v >> n;
 }
+
+// Two floats in one register pair, and Blackwell's packed operations on them.
+SPEC_DEV ull pk(float a, float b) {
+  ull r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+SPEC_DEV ull pk(float a) { return pk(a, a); }
+SPEC_DEV void upk(ull p, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p)); }
+SPEC_DEV ull fma2(ull a, ull b, ull c) {
+  ull r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+SPEC_DEV ull add2(ull a, ull b) {
+  ull r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+SPEC_DEV ull mul2(ull a, ull b) {
+  ull r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// weight() of two logits, operation for operation, in packed arithmetic (the
+// scans that weigh a whole row are bound by their instructions).
+SPEC_DEV void weight2(const Scale& r, const ull* tab, float x0, float x1, ull& w0, ull& w1) {
+  if (r.m == INFINITY) {
+    w0 = x0 == INFINITY ? 1ull << WBITS : 0ull;
+    w1 = x1 == INFINITY ? 1ull << WBITS : 0ull;
+    return;
+  }
+  constexpr float MAGIC = 12582912.f / TAB;
+  const ull m = pk(r.m), x = pk(x0, x1), neg = pk(-1.f), sh = pk(r.sh);
+  const ull d = fma2(x, neg, m), nb = fma2(d, neg, m);              // nb = -bb
+  const ull e = add2(fma2(add2(d, nb), neg, m), fma2(x, neg, nb));
+  ull np = mul2(d, pk(-r.sh));                                      // -p
+  const ull pe = fma2(e, sh, fma2(d, pk(r.sl), fma2(d, sh, np)));
+  float a, b;
+  upk(np, a, b);
+  np = pk(fmaxf(a, -63.f), fmaxf(b, -63.f));
+  const ull t = fma2(np, neg, pk(MAGIC));
+  const ull g = fma2(add2(np, add2(t, pk(-MAGIC))), neg, pe);
+  // 2^-g - 1, in units that make its product with the table's 24 leading bits one with weight()'s
+  constexpr float S = (float)(1 << (WBITS - 24));
+  const ull q = mul2(fma2(g, pk(0.240226507f * S), pk(-0.693147181f * S)), g);
+  upk(t, a, b);
+  const uint32_t j0 = __float_as_uint(a), j1 = __float_as_uint(b);
+  const ull T0 = tab[j0 & (TAB - 1)], T1 = tab[j1 & (TAB - 1)];
+  const ull Tf = pk(__uint_as_float((uint32_t)(T0 >> (WBITS - 24)) + 0x4a800000u),
+                    __uint_as_float((uint32_t)(T1 >> (WBITS - 24)) + 0x4a800000u));
+  const int n0 = (j0 >> TAB_LOG) & 63, n1 = (j1 >> TAB_LOG) & 63;
+  upk(fma2(Tf, q, pk(half_unit(n0), half_unit(n1))), a, b);
+  w0 = (T0 + (long long)__float2int_rn(a)) >> n0;
+  w1 = (T1 + (long long)__float2int_rn(b)) >> n1;
+}
+
+// The same out of line, where it is evaluated a few times.
+__device__ __noinline__ ull weight_once(Scale r, const ull* tab, float x, float* val) { return weight(r, tab, x, val); }
 
 // u * z for u in [0, 1), exactly, rounded down (up: rounded up).
 SPEC_DEV ull scaled(float u, ull z, bool up) {
@@ -205,39 +287,109 @@ struct Part {
     v0 = min(nvec, w * per);
     v1 = min(nvec, v0 + per);
   }
-  // f(index, value) for the elements of vector v
-  template <typename F>
-  SPEC_DEV void vec(int v, F& f) const {
-    const int i0 = v * E - mis;
-    if (i0 >= 0 && i0 + E <= V) {
-      const uint4 q = *reinterpret_cast<const uint4*>(p + i0);
+  // Vectors v, v + 32, ... of a lane, U in flight; q[j] is valid where the
+  // returned bit j is set (the others lie outside the part or on its edges).
+  SPEC_DEV unsigned int load(int v, uint4 (&q)[U]) const {
+    unsigned int ok = 0;
 #pragma unroll
-      for (int i = 0; i < E; ++i) f(i0 + i, get(q, i));
-    } else {
-      for (int i = max(0, -i0); i < E && i0 + i < V; ++i) f(i0 + i, one(p + i0 + i));
+    for (int j = 0; j < U; ++j) {
+      const int i0 = (v + 32 * j) * E - mis;
+      if (v + 32 * j < v1 && i0 >= 0 && i0 + E <= V) {
+        q[j] = *reinterpret_cast<const uint4*>(p + i0);
+        ok |= 1u << j;
+      }
     }
+    return ok;
+  }
+  // f(index, value) of the vectors that hold a value of at least x0.
+  template <typename F>
+  SPEC_DEV void each_above(float x0, F f) const {
+    if (v0 < v1) edge(v0, 0, f);
+#pragma unroll 1
+    for (int v = v0 + (int)(threadIdx.x & 31); v < v1; v += 32 * U) {
+      uint4 q[U];
+      const unsigned int ok = load(v, q);
+#pragma unroll
+      for (int j = 0; j < U; ++j) {
+        float mx = get(q[j], 0);
+#pragma unroll
+        for (int i = 1; i < E; ++i) mx = fmaxf(mx, get(q[j], i));
+        if ((ok & (1u << j)) && mx >= x0) {
+#pragma unroll 1
+          for (int i = 0; i < E; ++i) f((v + 32 * j) * E - mis + i, one(p + (v + 32 * j) * E - mis + i));
+        }
+      }
+    }
+    if (v0 < v1 - 1) edge(v1 - 1, 1, f);
   }
   template <typename F>
   SPEC_DEV void each(F f) const {
-    int v = v0 + (int)(threadIdx.x & 31);
-    for (; v + 32 * (U - 1) < v1 && v * E >= mis && (v + 32 * (U - 1)) * E - mis + E <= V; v += 32 * U) {
+    if (v0 < v1) edge(v0, 0, f);
+    for (int v = v0 + (int)(threadIdx.x & 31); v < v1; v += 32 * U) {
       uint4 q[U];
-#pragma unroll
-      for (int j = 0; j < U; ++j) q[j] = *reinterpret_cast<const uint4*>(p + (v + 32 * j) * E - mis);
+      const unsigned int ok = load(v, q);
 #pragma unroll
       for (int j = 0; j < U; ++j)
+        if (ok & (1u << j)) {
 #pragma unroll
-        for (int i = 0; i < E; ++i) f((v + 32 * j) * E - mis + i, get(q[j], i));
+          for (int i = 0; i < E; ++i) f((v + 32 * j) * E - mis + i, get(q[j], i));
+        }
     }
+    if (v0 < v1 - 1) edge(v1 - 1, 1, f);
+  }
+  // The same for a long f, in pairs: f.two(index, value, next value), or
+  // f(index, value) on the row's edges. One copy of it for a vector's pairs
+  // (the code of a scan that runs once comes from a cold instruction cache),
+  // two vectors ahead; done(vectors of the lane so far) after each vector.
+  template <typename F, typename D>
+  SPEC_DEV void each_rolled(int from, int to, F& f, D done) const {
+    const int lane = threadIdx.x & 31;
+    uint4 q[3];
+    bool ok[3];
+    auto get_vec = [&](int v, uint4& x) {
+      const int i0 = v * E - mis;
+      const bool in = v < to && i0 >= 0 && i0 + E <= V;
+      if (in) x = *reinterpret_cast<const uint4*>(p + i0);
+      return in;
+    };
+    ok[0] = get_vec(from + lane, q[0]);
+    ok[1] = get_vec(from + 32 + lane, q[1]);
+    int n = 0;
 #pragma unroll 1
-    for (; v < v1; v += 32) vec(v, f);
+    for (int v = from + lane; v - lane < to; v += 32) {
+      ok[2] = get_vec(v + 64, q[2]);
+      if (ok[0]) {
+#pragma unroll
+        for (int i = 0; i < E; i += 2) f.two(v * E - mis + i, get(q[0], i), get(q[0], i + 1));
+      } else if (v < to) {
+#pragma unroll 1
+        for (int i = max(0, mis - v * E); i < E && v * E - mis + i < V; ++i) f(v * E - mis + i, one(p + v * E - mis + i));
+      }
+      q[0] = q[1];
+      q[1] = q[2];
+      ok[0] = ok[1];
+      ok[1] = ok[2];
+      done(++n);
+    }
+  }
+  // The part's first or last vector, where the row does not fill it, in one
+  // lane (the first before and the last behind the others, in index order).
+  template <typename F>
+  SPEC_DEV void edge(int v, int lane, F& f) const {
+    const int i0 = v * E - mis;
+    if ((int)(threadIdx.x & 31) != lane || (i0 >= 0 && i0 + E <= V)) return;
+#pragma unroll 1
+    for (int i = max(0, -i0); i < E && i0 + i < V; ++i) f(i0 + i, one(p + i0 + i));
   }
 };
 
+// Warp sum of values below 2^63, three hardware reductions of 21 bits each.
 SPEC_DEV ull warp_sum_u64(ull v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(FULL, v, o);
-  return v;
+  constexpr unsigned int M = (1u << 21) - 1;
+  const ull a = __reduce_add_sync(FULL, (unsigned int)v & M);
+  const ull b = __reduce_add_sync(FULL, (unsigned int)(v >> 21) & M);
+  const ull c = __reduce_add_sync(FULL, (unsigned int)(v >> 42));
+  return a + (b << 21) + (c << 42);
 }
 SPEC_DEV ull warp_scan_u64(ull v) {  // inclusive
   const int lane = threadIdx.x & 31;
@@ -249,13 +401,49 @@ SPEC_DEV ull warp_scan_u64(ull v) {  // inclusive
   return v;
 }
 
-// A cut of the order: tokens with a smaller key, and those of this key up to
-// this index, are kept.
-struct Cut {
-  uint32_t key;
-  int idx;
-};
 SPEC_DEV bool kept(const Cut& c, uint32_t key, int i) { return key < c.key || (key == c.key && i <= c.idx); }
+
+// f(index, value) as a scan's functor.
+template <typename F>
+struct Single {
+  F f;
+  SPEC_DEV void operator()(int i, float x) { f(i, x); }
+  SPEC_DEV void two(int i, float x0, float x1) {
+    f(i, x0);
+    f(i + 1, x1);
+  }
+};
+// Amounts of tokens, summed by sum_part: one amount, or two together.
+template <typename F>
+struct Amount {
+  F f;
+  SPEC_DEV ull operator()(int i, float x) const { return f(i, x); }
+  SPEC_DEV ull two(int i, float x0, float x1) const { return f(i, x0) + f(i + 1, x1); }
+};
+template <typename F>
+struct Summing {
+  const F& f;
+  ull a;
+  SPEC_DEV void operator()(int i, float x) { a += f(i, x); }
+  SPEC_DEV void two(int i, float x0, float x1) { a += f.two(i, x0, x1); }
+};
+// The mass of the tokens inside a cut whose weight is at least qw.
+struct Mass {
+  Scale sc;
+  const ull* tab;
+  ull qw;
+  Cut cut;
+  bool cutting;
+  SPEC_DEV ull keep(int i, float x, ull w) const {
+    return w < qw || (cutting && !kept(cut, rank_key(x), i)) ? 0ull : w;
+  }
+  SPEC_DEV ull operator()(int i, float x) const { return keep(i, x, weight(sc, tab, x)); }
+  SPEC_DEV ull two(int i, float x0, float x1) const {
+    ull w0, w1;
+    weight2(sc, tab, x0, x1, w0, w1);
+    return keep(i, x0, w0) + keep(i + 1, x1, w1);
+  }
+};
 
 template <typename T>
 struct Sampler {
@@ -264,6 +452,14 @@ struct Sampler {
   int cta, C;
   Part<T> part;
   Scale sc;
+  static constexpr int PT = FEW / NT;   // sorted tokens of a thread
+
+  // f(index, value) of this CTA's tokens.
+  template <typename F>
+  SPEC_DEV void scan(const F& f) {
+    Single<F> one{f};
+    part.each_rolled(part.v0, part.v1, one, [](int) {});
+  }
 
   // Exclusive sum of v over the CTA's threads, in thread order.
   SPEC_DEV ull block_scan(ull v) {
@@ -272,17 +468,53 @@ struct Sampler {
     if ((threadIdx.x & 31) == 31) s.wsum[threadIdx.x >> 5] = inc;
     __syncthreads();
     ull b = inc - v;
-    for (int i = 0; i < (int)(threadIdx.x >> 5); ++i) b += s.wsum[i];
+#pragma unroll
+    for (int i = 0; i < NW; ++i)
+      if (i < (int)(threadIdx.x >> 5)) b += s.wsum[i];
     return b;
   }
 
-  // Sum of f(index, value) over the row; wsum holds the warps' parts, and
-  // `before` gets the sum of the cluster's earlier CTAs.
+  // This CTA's sum of f(index, value) in s.total, the warps' parts in wsum,
+  // their chunks' in chunk; ends with a barrier.
   template <typename F>
-  SPEC_DEV ull sum(F f, ull* before) {
-    ull a = 0;
-    part.each([&](int i, float x) { a += f(i, x); });
-    block_total(a);
+  SPEC_DEV void sum_part(const F& f) {
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, per = chunk_vectors();
+    ull all = 0;
+    int c = 0;
+    __syncthreads();
+    Summing<F> add{f, 0};
+    part.each_rolled(part.v0, part.v1, add, [&](int n) {
+      if ((n & (per - 1)) == 0) {
+        const ull a = warp_sum_u64(add.a);
+        if (lane == 0) s.chunk[w][c] = a;
+        ++c;
+        all += a;
+        add.a = 0;
+      }
+    });
+    const ull a = warp_sum_u64(add.a);
+    if (lane == 0) {
+      if (c < CHUNKS) s.chunk[w][c] = a;
+      s.wsum[w] = all + a;
+    }
+    __syncthreads();
+    if (threadIdx.x < 32) {
+      const ull t = warp_sum_u64(threadIdx.x < NW ? s.wsum[threadIdx.x] : 0ull);
+      if (threadIdx.x == 0) s.total = t;
+    }
+    __syncthreads();
+  }
+  // A power of two.
+  SPEC_DEV int chunk_vectors() const {
+    int per = CHUNK;
+    while (per * CHUNKS * 32 < part.v1 - part.v0) per *= 2;
+    return per;
+  }
+
+  // Sum of f(index, value) over the row, and that of the cluster's earlier CTAs.
+  template <typename F>
+  SPEC_DEV ull sum(const F& f, ull* before) {
+    sum_part(f);
     cl.sync();
     ull all = 0, b = 0;
     for (int c = 0; c < C; ++c) {
@@ -296,48 +528,54 @@ struct Sampler {
   }
 
   // Calls hit(index, value) in the lane that holds the lowest index at which
-  // the sum of f in index order exceeds t (t below the row's sum; wsum: the
-  // warps' parts, before: the sum of the earlier CTAs).
+  // the sum of f in index order exceeds t (t below the row's sum; the CTA's
+  // sums as sum_part left them, before: the sum of the earlier CTAs).
   template <typename F, typename H>
-  SPEC_DEV void find_in_order(F f, ull t, ull before, H hit) {
-    constexpr int U = 4;
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  SPEC_DEV void find_in_order(const F& f, ull t, ull before, H hit) {
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, per = chunk_vectors();
     ull b = before;
-    for (int i = 0; i < w; ++i) b += s.wsum[i];
+#pragma unroll
+    for (int i = 0; i < NW; ++i)
+      if (i < w) b += s.wsum[i];
     if (t < b || t >= b + s.wsum[w]) return;
-    for (int v0 = part.v0 + lane; v0 - lane < part.v1; v0 += 32 * U) {
-      ull a[U], inc[U];
-#pragma unroll
-      for (int j = 0; j < U; ++j) {
-        a[j] = 0;
-        auto add = [&](int i, float x) { a[j] += f(i, x); };
-        if (v0 + 32 * j < part.v1) part.vec(v0 + 32 * j, add);
+    // the chunk, then the vector, then the element
+    const ull mine = lane * per * 32 < part.v1 - part.v0 ? s.chunk[w][lane] : 0ull;
+    const ull upto = b + warp_scan_u64(mine);
+    const int c = __ffs(__ballot_sync(FULL, t < upto)) - 1;
+    b = __shfl_sync(FULL, upto - mine, c);
+    const int from = part.v0 + c * per * 32;
+    int v = from + lane;
+    bool over = false;
+    Summing<F> add{f, 0};
+    part.each_rolled(from, min(part.v1, from + per * 32), add, [&](int) {
+      const ull inc = warp_scan_u64(add.a);
+      const ull tot = __shfl_sync(FULL, inc, 31);
+      if (!over && t < b + tot) {
+        over = true;
+        const ull at = b + inc - add.a;
+        if (t >= at && t < at + add.a) walk(f, max(0, v * Part<T>::E - part.mis), t, at, hit);
       }
-#pragma unroll
-      for (int j = 0; j < U; ++j) inc[j] = warp_scan_u64(a[j]);
-#pragma unroll
-      for (int j = 0; j < U; ++j) {
-        const ull tot = __shfl_sync(FULL, inc[j], 31);
-        ull c = b + inc[j] - a[j];
-        if (t >= c && t < c + a[j]) {
-          bool done = false;
-          auto walk = [&](int i, float x) {
-            c += f(i, x);
-            if (!done && t < c) {
-              done = true;
-              hit(i, x);
-            }
-          };
-          part.vec(v0 + 32 * j, walk);
-        }
-        b += tot;
+      b += tot;
+      add.a = 0;
+      v += 32;
+    });
+  }
+  // From index i on, in one lane: the element at which the sum b passes t.
+  template <typename F, typename H>
+  SPEC_DEV void walk(const F& f, int i, ull t, ull b, H hit) {
+#pragma unroll 1
+    for (; i < part.V; ++i) {
+      const float x = Part<T>::one(part.p + i);
+      b += f(i, x);
+      if (t < b) {
+        hit(i, x);
+        return;
       }
-      if (t < b) return;
     }
   }
   // The same index in every CTA.
   template <typename F>
-  SPEC_DEV int find_all(F f, ull t, ull before) {
+  SPEC_DEV int find_all(const F& f, ull t, ull before) {
     find_in_order(f, t, before, [&](int i, float) {
       for (int r = 0; r < C; ++r) *cl.map_shared_rank(&s.found, r) = i;
     });
@@ -368,7 +606,7 @@ struct Sampler {
     constexpr int D = MASS ? 3 : 1;
     for (int i = threadIdx.x; i < D * BINS; i += NT) s.hist[0][i] = 0u;
     __syncthreads();
-    part.each([&](int i, float x) {
+    auto one = [&](int i, float x) {
       if (!keep(i, x)) return;
       const int b = sc.bin(x);
       if (MASS) {
@@ -382,7 +620,8 @@ struct Sampler {
       } else {
         atomicAdd(&s.hist[0][b], 1u);
       }
-    });
+    };
+    scan(one);
     cl.sync();
 #pragma unroll
     for (int j = 0; j < BPT; ++j) h[j] = 0;
@@ -432,12 +671,13 @@ struct Sampler {
       const int bits = level == 2 ? 10 : 11;
       for (int i = threadIdx.x; i < BINS; i += NT) s.mass[i] = 0ull;
       __syncthreads();
-      part.each([&](int i, float x) {
+      auto one = [&](int i, float x) {
         if (sc.bin(x) != bin) return;
         const uint32_t k = rank_key(x);
         if ((level > 0 && (k >> (shift + bits)) != pre) || !keep(i, x)) return;
         atomicAdd(&s.mass[(k >> shift) & ((1 << bits) - 1)], MASS ? weight(sc, s.tab, x) : 1ull);
-      });
+      };
+      scan(one);
       cl.sync();
       ull h[BPT] = {0, 0, 0, 0};
 #pragma unroll 4
@@ -452,11 +692,69 @@ struct Sampler {
     return pre;
   }
 
+  // The cut at which the amount in order (of the tokens kept so far) reaches
+  // `need`, in bin s.bin with s.before ahead of it.
+  template <bool MASS, typename K>
+  SPEC_DEV void cut_in_bin(Cut& cut, ull need, K keep) {
+    const int bin = s.bin;
+    const ull before = s.before;
+    if (threadIdx.x == 0) {
+      s.listed = 0;
+      s.gathered = 0;
+    }
+    __syncthreads();
+    const float lo = (float)bin, hi = bin < BINS - 1 ? (float)(bin + 1) : INFINITY;
+    auto one = [&](int i, float x) {
+      if (keep(i, x)) list(i, x, lo, hi);
+    };
+    scan(one);
+    cl.sync();
+    push_list();
+    cl.sync();
+    const int n = *cl.map_shared_rank(&s.gathered, 0);
+    if (n <= FEW) {
+      if (cta == 0) {
+        int n2 = 64;
+        while (n2 < n) n2 <<= 1;
+        for (int i = n + threadIdx.x; i < n2; i += NT) s.sort[i] = ~0ull;
+        __syncthreads();
+        sort(n2);
+        ull w[PT], t = 0;
+#pragma unroll
+        for (int j = 0; j < PT; ++j) {
+          const int i = threadIdx.x * PT + j;
+          w[j] = i >= n ? 0ull : MASS ? weight_once(sc, s.tab, rank_val((uint32_t)(s.sort[i] >> 32)), nullptr) : 1ull;
+          t += w[j];
+        }
+        ull b = before + block_scan(t);
+#pragma unroll
+        for (int j = 0; j < PT; ++j) {
+          if (b < need && need <= b + w[j]) {
+            const ull e = s.sort[threadIdx.x * PT + j];
+            for (int c = 0; c < C; ++c) *cl.map_shared_rank(&s.cut, c) = Cut{(uint32_t)(e >> 32), (int)(uint32_t)e};
+          }
+          b += w[j];
+        }
+        // (tokens at -inf are not listed: a count that ends among them cuts nothing)
+        if (threadIdx.x == NT - 1 && b < need)
+          for (int c = 0; c < C; ++c) *cl.map_shared_rank(&s.cut, c) = Cut{0xffffffffu, 0x7fffffff};
+      }
+      cl.sync();
+      cut = s.cut;
+      return;
+    }
+    cl.sync();
+    const uint32_t key = radix<MASS>(bin, need, before, keep);
+    const ull w = MASS ? weight_once(sc, s.tab, rank_val(key), nullptr) : 1ull;
+    cut_ties(cut, key, (need - s.before + w - 1) / w, s.at / w);
+  }
+
   // Narrows the cut to the `r` lowest indices among the `n` kept tokens of key.
   SPEC_DEV void cut_ties(Cut& cut, uint32_t key, ull r, ull n) {
     if (r < n) {
       const Cut old = cut;
-      auto eq = [&](int i, float x) { return rank_key(x) == key && kept(old, key, i) ? 1ull : 0ull; };
+      auto same = [=](int i, float x) { return rank_key(x) == key && kept(old, key, i) ? 1ull : 0ull; };
+      const Amount<decltype(same)> eq{same};
       ull before;
       sum(eq, &before);
       cut.idx = find_all(eq, r - 1, before);
@@ -466,22 +764,28 @@ struct Sampler {
     cut.key = key;
   }
 
-  // The rank key down to which at least `need` tokens of weight lie: that of the
-  // need-th largest segment maximum, found to a bin of them (and tokens
-  // without weight are never listed). Every CTA finds the same.
-  SPEC_DEV uint32_t threshold(int need, int n) {
-    if (threadIdx.x == 0) s.threshold = 0u;
-    const float end = sc.m == INFINITY ? sc.m : sc.m - Z_END / sc.sh;
+  // The bin (of SEG_BINS) down to which at least `need` tokens lie: that of the
+  // need-th largest of the row's n segment maxima. Every CTA finds the same.
+  SPEC_DEV int threshold(int need, int n) {
     for (int i = threadIdx.x; i < n; i += NT) atomicAdd(&s.seg_bins[sc.bin(s.seg[i]) / (BINS / SEG_BINS)], 1u);
     __syncthreads();
     const unsigned int c = s.seg_bins[threadIdx.x];
     const ull b = block_scan(c);
     if (b < (ull)need && (ull)need <= b + c) s.bin = threadIdx.x;
     __syncthreads();
-    for (int i = threadIdx.x; i < n; i += NT)
-      if (sc.bin(s.seg[i]) / (BINS / SEG_BINS) <= s.bin) atomicMax(&s.threshold, rank_key(s.seg[i]));
-    __syncthreads();
-    return min(s.threshold, rank_key(end));
+    return s.bin;
+  }
+
+  // Lists the tokens of exponents [lo, hi) in bin units.
+  SPEC_DEV void list(int i, float x, float lo, float hi) {
+    const float v = sc.m == INFINITY ? (x == INFINITY ? 0.f : INFINITY) : sc.place(x);
+    if (v < hi && v >= lo) {
+      const int at = atomicAdd(&s.listed, 1);
+      if (at < LIST) {
+        s.list_key[at] = rank_key(x);
+        s.list_idx[at] = i;
+      }
+    }
   }
 
   // Appends the listed tokens to the first CTA's; what does not fit is counted
@@ -497,7 +801,8 @@ struct Sampler {
     for (int i = threadIdx.x; i < n; i += NT) sort0[base + i] = ((ull)s.list_key[i] << 32) | (unsigned int)s.list_idx[i];
   }
 
-  // Ascending bitonic sort of s.sort[0, n2), n2 a power of two.
+  // Ascending bitonic sort of s.sort[0, n2), n2 a power of two, at least 64.
+  // A warp's pairs of a stride up to 32 stay inside 64 elements of its own.
   SPEC_DEV void sort(int n2) {
     for (int k = 2; k <= n2; k <<= 1)
       for (int j = k >> 1; j > 0; j >>= 1) {
@@ -509,8 +814,57 @@ struct Sampler {
             s.sort[l] = a;
           }
         }
-        __syncthreads();
+        if (j > 32 || (j == 1 && k >= 64)) __syncthreads();
+        else __syncwarp();
       }
+  }
+
+  // draw_few for at most COUNTED tokens, which are not sorted: two threads a
+  // token count the tokens (and their mass) ahead of it, in the order and then
+  // in the vocabulary.
+  SPEC_DEV int draw_counted(int n, int k, float p, ull qw, float u, ull mass, ull* kept_mass) {
+    ull* w = s.sort + COUNTED;
+    const int i = threadIdx.x >> 1, half = threadIdx.x & 1;
+    const ull e = i < n ? s.sort[i] : ~0ull;
+    const ull wi = i < n ? weight_once(sc, s.tab, rank_val((uint32_t)(e >> 32)), nullptr) : 0ull;
+    if (half == 0) w[i] = wi;
+    __syncthreads();
+    ull ahead = 0;
+    int rank = 0;
+    if (i < n) {
+#pragma unroll 4
+      for (int j = half; j < n; j += 2)
+        if (s.sort[j] < e) {
+          ahead += w[j];
+          ++rank;
+        }
+    }
+    ahead += __shfl_xor_sync(FULL, ahead, 1);
+    rank += __shfl_xor_sync(FULL, rank, 1);
+    bool keep = i < n && (k <= 0 || rank < k);
+    if (p < 1.f) {
+      block_total(keep && half == 0 ? wi : 0ull);
+      const ull need = top_p_mass(p, k > 0 ? s.total : mass);
+      if (need > s.total) return -1;
+      keep = keep && ahead < need;
+    }
+    keep = keep && wi >= qw;
+    const ull ki = keep ? wi : 0ull;
+    block_total(half == 0 ? ki : 0ull);
+    const ull z = s.total, d = drawn_mass(u, z);
+    if (half == 0) w[i] = ki;
+    __syncthreads();
+    if (ki) {
+      ahead = 0;
+#pragma unroll 4
+      for (int j = half; j < n; j += 2)
+        if ((uint32_t)s.sort[j] < (uint32_t)e) ahead += w[j];
+    }
+    ahead += __shfl_xor_sync(FULL, ahead, 1);
+    if (half == 0 && d >= ahead && d < ahead + ki) s.found = (int)(uint32_t)e;
+    __syncthreads();
+    *kept_mass = z;
+    return s.found;
   }
 
   // The first CTA's end of the usual case: the n listed tokens sorted by
@@ -518,13 +872,13 @@ struct Sampler {
   // mass (top-p without top-k). Returns the token, *kept_mass its kept mass; -1
   // if the listed tokens hold less than top-p's mass.
   SPEC_DEV int draw_few(int n, int k, float p, ull qw, float u, ull mass, ull* kept_mass) {
+    if (n <= COUNTED) return draw_counted(n, k, p, qw, u, mass, kept_mass);
     int n2 = 64;
     while (n2 < n) n2 <<= 1;
     for (int i = n + threadIdx.x; i < n2; i += NT) s.sort[i] = ~0ull;
     if (threadIdx.x == 0) s.r = k > 0 ? min(n, k) : n;
     __syncthreads();
     sort(n2);
-    constexpr int PT = FEW / NT;
     // weights of the first r tokens, PT consecutive ones a thread
     const int r1 = s.r;
     ull e[PT], w[PT], t = 0;
@@ -532,7 +886,7 @@ struct Sampler {
     for (int j = 0; j < PT; ++j) {
       const int i = threadIdx.x * PT + j;
       e[j] = i < r1 ? s.sort[i] : 0ull;
-      w[j] = i < r1 ? weight(sc, s.tab, rank_val((uint32_t)(e[j] >> 32))) : 0ull;
+      w[j] = i < r1 ? weight_once(sc, s.tab, rank_val((uint32_t)(e[j] >> 32)), nullptr) : 0ull;
       t += w[j];
     }
     const ull b0 = block_scan(t);
@@ -613,7 +967,8 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SampleArgs a) {
   const float u = a.uniform[row];
   S.part.bind((const T*)a.logits + (size_t)row * a.ld, a.V, cta, C);
   const bool greedy = temp < 1e-5f, cuts = k > 0 || p < 1.f;
-  const int seg_lanes = max(1, C * NT / SEG_MAX);
+  int seg_lanes = 1;
+  while (C * NT / seg_lanes > SEG_MAX) seg_lanes *= 2;
 
   // maximum with its lowest index, minimum, segment maxima; a NaN anywhere
   // leaves the row without a distribution
@@ -636,16 +991,18 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SampleArgs a) {
       if (o < seg_lanes) bx = fmaxf(bx, v);
     }
     const int per = 32 / seg_lanes;   // segments of a warp, pushed to every CTA
-    for (int j = lane; j < per * C; j += 32) {
-      const float v = __shfl_sync(FULL, bx, (j & (per - 1)) * seg_lanes);
-      cl.map_shared_rank(s.seg, j / per)[(cta * NW + warp) * per + (j & (per - 1))] = v;
+    for (int j0 = 0; j0 < per * C; j0 += 32) {
+      const int j = j0 + lane, g = j & (per - 1);
+      const float v = __shfl_sync(FULL, bx, g * seg_lanes);
+      if (j < per * C) cl.map_shared_rank(s.seg, j / per)[(cta * NW + warp) * per + g] = v;
     }
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const ull other = __shfl_xor_sync(FULL, best, o);
-    best = other > best ? other : best;
-    low = fminf(low, __shfl_xor_sync(FULL, low, o));
+  {
+    // the largest key of the warp, and its lowest index
+    const uint32_t key = __reduce_max_sync(FULL, (uint32_t)(best >> 32));
+    const uint32_t idx = __reduce_max_sync(FULL, (uint32_t)(best >> 32) == key ? (uint32_t)best : 0u);
+    best = ((ull)key << 32) | idx;
+    low = ord_val(__reduce_min_sync(FULL, ord_key(low)));
   }
   if (lane == 0) {
     s.wsum[warp] = best;
@@ -665,11 +1022,13 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SampleArgs a) {
   cl.sync();
   best = 0;
   nan = 0;
-  for (int c = 0; c < C; ++c) {
-    best = s.x_best[c] > best ? s.x_best[c] : best;
-    low = fminf(low, s.x_low[c]);
-    nan |= s.x_nan[c];
-  }
+#pragma unroll
+  for (int c = 0; c < MAX_C; ++c)
+    if (c < C) {
+      best = s.x_best[c] > best ? s.x_best[c] : best;
+      low = fminf(low, s.x_low[c]);
+      nan |= s.x_nan[c];
+    }
 
   auto write = [&](int token, float prob) {
     a.tokens[row] = token;
@@ -693,24 +1052,20 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SampleArgs a) {
   const ull qw = q > 0.f ? (q < 1.f ? scaled(q, 1ull << WBITS, true) : 1ull << WBITS) : 0ull;
   auto result = [&](int token, float x, ull z) {
     float v;
-    weight(S.sc, s.tab, x, &v);
+    weight_once(S.sc, s.tab, x, &v);
     write(token, v / ((float)z * (1.f / (float)(1ull << WBITS))));
   };
 
   if (!cuts) {
-    auto mass = [&](int, float x) {
-      const ull w = weight(S.sc, s.tab, x);
-      return w < qw ? 0ull : w;
-    };
-    ull t = 0;
-    S.part.each([&](int i, float x) { t += mass(i, x); });
-    S.block_total(t);
+    const Mass mass{S.sc, s.tab, qw, Cut{}, false};
+    S.sum_part(mass);
     if (threadIdx.x < C) *cl.map_shared_rank(&s.x_total[cta], threadIdx.x) = s.total;
     cl.sync();
     ull z = 0, before = 0;
-    for (int c = 0; c < C; ++c) {
+#pragma unroll
+    for (int c = 0; c < MAX_C; ++c) {
       if (c == cta) before = z;
-      z += s.x_total[c];
+      if (c < C) z += s.x_total[c];
     }
     S.find_in_order(mass, drawn_mass(u, z), before, [&](int i, float x) { result(i, x, z); });
     return;
@@ -718,29 +1073,22 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SampleArgs a) {
 
   // the tokens that may be kept, listed for the first CTA
   const bool by_mass = k == 0;
-  const int segs = C * NT / seg_lanes, need_k = by_mass ? segs / 2 : k;
+  const int segs = C * NT / seg_lanes, need_k = by_mass ? min(NUCLEUS, segs / 2) : k;
   if (need_k <= segs) {
-    const uint32_t thr = S.threshold(need_k, segs);
-    const float xthr = rank_val(thr);
-    auto add = [&](int i, float x) {
-      if (x >= xthr) {
-        const int at = atomicAdd(&s.listed, 1);
-        if (at < LIST) {
-          s.list_key[at] = rank_key(x);
-          s.list_idx[at] = i;
-        }
-      }
-    };
+    const int last = S.threshold(need_k, segs);
+    // (the last bin holds tokens without weight where the range was cut)
+    const float hi = last < SEG_BINS - 1 ? (float)((last + 1) * (BINS / SEG_BINS))
+                                         : range < Z_END ? INFINITY : (float)(BINS - 1);
+    // a little below any value listed
+    const float x0 = m == INFINITY ? m : hi == INFINITY || S.sc.bins == 0.f
+                         ? -INFINITY : m - hi / (sh * S.sc.bins) * 1.0001f - fabsf(m) * 1e-5f;
     if (by_mass) {
-      ull t = 0;
-      S.part.each([&](int i, float x) {
-        t += weight(S.sc, s.tab, x);
-        add(i, x);
-      });
-      S.block_total(t);
+      S.sum_part(Mass{S.sc, s.tab, 0ull, Cut{}, false});
+      S.part.each_above(x0, [&](int i, float x) { S.list(i, x, 0.f, hi); });
+      __syncthreads();
       if (threadIdx.x == 0) *cl.map_shared_rank(&s.x_total[cta], 0) = s.total;
     } else {
-      S.part.each(add);
+      S.part.each_above(x0, [&](int i, float x) { S.list(i, x, 0.f, hi); });
       __syncthreads();
     }
     S.push_list();
@@ -771,8 +1119,7 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SampleArgs a) {
   if (k > 0) {
     S.template histogram<false>(all, h);
     S.cross(h, (ull)k, 0ull);
-    const uint32_t key = S.template radix<false>(s.bin, (ull)k, s.before, all);
-    S.cut_ties(cut, key, (ull)k - s.before, s.at);
+    S.template cut_in_bin<false>(cut, (ull)k, all);
   }
   if (p < 1.f) {
     auto in = [&](int i, float x) { return kept(cut, rank_key(x), i); };
@@ -783,15 +1130,9 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SampleArgs a) {
     S.block_total(t);
     const ull need = top_p_mass(p, s.total);
     S.cross(h, need, 0ull);
-    const uint32_t key = S.template radix<true>(s.bin, need, s.before, in);
-    const ull w = weight(S.sc, s.tab, rank_val(key));
-    S.cut_ties(cut, key, (need - s.before + w - 1) / w, s.at / w);
+    S.template cut_in_bin<true>(cut, need, in);
   }
-  auto mass = [&](int i, float x) {
-    if (!kept(cut, rank_key(x), i)) return 0ull;
-    const ull w = weight(S.sc, s.tab, x);
-    return w < qw ? 0ull : w;
-  };
+  const Mass mass{S.sc, s.tab, qw, cut, true};
   const ull z = S.sum(mass, &before);
   S.find_in_order(mass, drawn_mass(u, z), before, [&](int i, float x) { result(i, x, z); });
 }
@@ -840,10 +1181,71 @@ __global__ void __launch_bounds__(256) accept_sampled_kernel(AcceptSampledArgs a
     for (int i = b0; i < a.B * R; i += step) a.best[i] = 0ull;
 }
 
+// Clusters of C CTAs of the kernel that the current device holds at once.
+template <typename T>
+int max_clusters(int C) {
+  static std::mutex mu;
+  static int cache[MAX_DEVICES][MAX_C + 1];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= MAX_DEVICES) return 0;
+  std::lock_guard<std::mutex> lk(mu);
+  int& n = cache[dev][C];
+  if (n == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(C);
+    cfg.blockDim = dim3(NT);
+    cfg.dynamicSmemBytes = sizeof(Shared);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = C;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, sample_kernel<T>, &cfg) != cudaSuccess || n < 1) {
+      cudaGetLastError();
+      n = -1;  // not on this device
+    }
+  }
+  return n;
+}
+
+// CTAs a row: the count with the least estimated time, waves of resident
+// clusters at a fixed cost of about 8 us (0.1 more a CTA of the exchanges) and
+// 0.17 ns a token of a CTA, twice that where two CTAs share an SM. 262144
+// tokens, measured: 1 row 13 us with 16 CTAs, 15 with 8, 58 with 1; 40 rows 40 us
+// with 6 (one wave), 50 with 8, 57 with 16.
+template <typename T>
+int cluster_size(int M, int V) {
+  int best = MAX_C;
+  double least = 1e30;
+  for (int C : {1, 2, 3, 4, 5, 6, 7, 8, 12, 16}) {
+    if (V / C > DIGIT_TOKENS) continue;
+    const int fit = max_clusters<T>(C);
+    if (fit < 1) continue;
+    double us = 0;
+    for (int left = M; left > 0; left -= fit) {
+      const int rows = std::min(left, fit);
+      const int share = (rows * C + num_sms() - 1) / num_sms();
+      const double wave = 8.0 + 0.1 * C + 0.17e-3 * share * V / C;
+      if (left > 8 * fit) {  // many waves: all but the last few at once
+        const int n = left / fit - 4;
+        us += n * wave;
+        left -= n * fit;
+      }
+      us += wave;
+    }
+    if (us < least) {
+      least = us;
+      best = C;
+    }
+  }
+  return best;
+}
+
 template <typename T>
 int launch_sample(const SampleArgs& a, int pdl, cudaStream_t st) {
-  int C = 1;
-  while (C < MAX_C && (long long)C * 8192 < a.V) C *= 2;
+  const int C = cluster_size<T>(a.M, a.V);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)a.M * C);
   cfg.blockDim = dim3(NT);

@@ -2,8 +2,8 @@
 (spec_sampling), written with library sorts and sums, and how near a row's
 decisions are to a border.
 
-The kernel evaluates a weight to a relative 2^-36 and rounds it down to its unit,
-an absolute 2^-44 (the largest weight is 1). A sum of up to V weights, compared
+The kernel evaluates a weight to a relative 2^-36 and rounds it to its unit,
+an absolute 2^-44 at most (the largest weight is 1). A sum of up to V weights, compared
 with another one, is therefore off by at most 2 * (Z * 2^-36 + V * 2^-44), Z the
 whole mass: a draw is compared only where it is further from its borders than
 that, `slack`. Where top-p's cut is that near to a border, the kernel may cut up
@@ -50,7 +50,7 @@ def row(l, u, T=1.0, k=0, p=1.0, q=0.0):
         q = min(q, 1.0)
         decided &= q == 1.0 or np.abs(w - q).min() > q * 2.0 ** -36 + 2.0 ** -44
         keep &= w >= q
-    at = np.flatnonzero(keep & (w > 2.0 ** -44))
+    at = np.flatnonzero(keep & (w > 2.0 ** -45))
     cum = np.cumsum(w[at])
     u = min(max(u, 0.0), 1.0) if u == u else 0.0
     t = u * cum[-1]
