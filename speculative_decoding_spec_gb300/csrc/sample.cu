@@ -28,14 +28,15 @@
 // their shared memory, so that a phase costs one cluster barrier. Scan 1 finds
 // the maximum and the maxima of the row's segments (up to 1024).
 // Without top-k and top-p, scan 2 sums the weights and the warp that holds the
-// drawn mass finds the token. With them, scan 2 lists the tokens down to the
-// k-th largest segment maximum -- at least k tokens, and rarely many more -- (top-p
-// alone: down to the 128th, and sums the weights too), and the first CTA
-// sorts, cuts and draws among those alone. Where they are too many, or hold too
-// little mass for top-p, the cut is found in the whole row: a histogram of 2048
-// bins, linear in the exponent, of counts or of exact masses (three 15-bit
-// digits), then the tokens of the one bin in which the cut lies are listed and
-// sorted (a radix search of their keys where they are too many).
+// drawn mass finds the token. With top-k, scan 2 lists the tokens down to the
+// k-th largest segment maximum -- at least k tokens, and rarely many more -- and
+// the first CTA cuts and draws among those alone. With top-p alone, scan 2 adds
+// up a histogram of 2048 bins, linear in the exponent, of exact masses (three
+// 15-bit digits), and the tokens up to the bin in which the cut lies are listed
+// and drawn from in the same way. Where the listed tokens are too many, those of
+// that bin alone are listed and sorted for the cut (a radix search of their keys
+// where even they are too many; top-k then has a histogram of counts), and a
+// last scan sums the kept weights.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -67,7 +68,6 @@ constexpr int FEW = 2048;           // tokens the first CTA sorts
 constexpr int COUNTED = NT / 2;     // at most so many are counted instead
 constexpr int SEG_MAX = 1024;       // segments of a row (the elements of 1, 2, 4 or 8 lanes)
 constexpr int SEG_BINS = NT;        // bins of the segment maxima
-constexpr int NUCLEUS = 128;        // tokens listed at first for top-p alone
 constexpr float Z_END = 46.f;       // weights are zero beyond this exponent
 constexpr int CHUNK = 8;            // vectors of a lane whose sum is kept apart, doubled until
 constexpr int CHUNKS = 32;          // a warp's part has at most 32 chunks
@@ -117,7 +117,6 @@ struct Shared {
   ull x_total[MAX_C];        // sum of the weights
   float seg[SEG_MAX];        // segment maxima
   int gathered;              // first CTA: tokens listed by all
-  int few;                   // the first CTA's verdict: the listed tokens suffice
   unsigned int seg_bins[SEG_BINS];
   Cut cut;                   // pushed by the first CTA: the cut of the row
   ull chunk[NW][CHUNKS];     // sums of the warps' chunks
@@ -439,9 +438,41 @@ struct Mass {
   }
   SPEC_DEV ull operator()(int i, float x) const { return keep(i, x, weight(sc, tab, x)); }
   SPEC_DEV ull two(int i, float x0, float x1) const {
+    if (cutting && rank_key(fmaxf(x0, x1)) > cut.key) return 0ull;
     ull w0, w1;
     weight2(sc, tab, x0, x1, w0, w1);
     return keep(i, x0, w0) + keep(i + 1, x1, w1);
+  }
+};
+
+// Counts or exact masses (in digits) of the kept tokens, by bin.
+template <bool MASS, typename K>
+struct Binned {
+  Scale sc;
+  const ull* tab;
+  unsigned int* hist;
+  K keep;
+  SPEC_DEV void put(float x, ull w) const {
+    unsigned int* h = hist + sc.bin(x);
+    if (!MASS) {
+      atomicAdd(h, 1u);
+      return;
+    }
+    constexpr unsigned int M = (1u << DIGIT) - 1;
+    if (w) atomicAdd(h, (unsigned int)w & M);
+    if (w >> DIGIT) atomicAdd(h + BINS, (unsigned int)(w >> DIGIT) & M);
+    if (w >> (2 * DIGIT)) atomicAdd(h + 2 * BINS, (unsigned int)(w >> (2 * DIGIT)));
+  }
+  SPEC_DEV void operator()(int i, float x) const {
+    if (keep(i, x)) put(x, MASS ? weight(sc, tab, x) : 0ull);
+  }
+  SPEC_DEV void two(int i, float x0, float x1) const {
+    const bool k0 = keep(i, x0), k1 = keep(i + 1, x1);
+    if (!k0 && !k1) return;
+    ull w0 = 0, w1 = 0;
+    if (MASS) weight2(sc, tab, x0, x1, w0, w1);
+    if (k0) put(x0, w0);
+    if (k1) put(x1, w1);
   }
 };
 
@@ -599,45 +630,65 @@ struct Sampler {
     __syncthreads();
   }
 
-  // Histogram of the kept tokens' counts or exact masses by bin, in every
-  // CTA: h[j] is the row's amount in bin threadIdx.x * BPT + j.
-  template <bool MASS, typename K>
-  SPEC_DEV void histogram(K keep, ull (&h)[BPT]) {
+  // The bin in which the count or exact mass of the kept tokens, in order,
+  // first reaches need(row's amount) >= 1: s.bin, with the amount before it and
+  // in it in s.before and s.at, the same in every CTA. Each CTA counts its
+  // tokens by bin, adds up the cluster's counts of a share of the bins, and the
+  // owner of the bin tells the others. Returns the row's amount; *last: need.
+  // Empties the lists.
+  template <bool MASS, typename K, typename N>
+  SPEC_DEV ull find_bin(K keep, N need, ull* last) {
     constexpr int D = MASS ? 3 : 1;
+    if (threadIdx.x == 0) {
+      s.listed = 0;
+      s.gathered = 0;
+    }
     for (int i = threadIdx.x; i < D * BINS; i += NT) s.hist[0][i] = 0u;
     __syncthreads();
-    auto one = [&](int i, float x) {
-      if (!keep(i, x)) return;
-      const int b = sc.bin(x);
-      if (MASS) {
-        const ull w = weight(sc, s.tab, x);
-        const unsigned int d0 = (unsigned int)w & ((1u << DIGIT) - 1),
-                           d1 = (unsigned int)(w >> DIGIT) & ((1u << DIGIT) - 1),
-                           d2 = (unsigned int)(w >> (2 * DIGIT));
-        if (w) atomicAdd(&s.hist[0][b], d0);
-        if (w >> DIGIT) atomicAdd(&s.hist[1][b], d1);
-        if (d2) atomicAdd(&s.hist[2][b], d2);
-      } else {
-        atomicAdd(&s.hist[0][b], 1u);
-      }
-    };
-    scan(one);
+    Binned<MASS, K> add{sc, s.tab, &s.hist[0][0], keep};
+    part.each_rolled(part.v0, part.v1, add, [](int) {});
     cl.sync();
+    const int share = (BINS + C - 1) / C, per = (share + NT - 1) / NT, b0 = cta * share + threadIdx.x * per;
+    const int b1 = min(min(b0 + per, (cta + 1) * share), BINS);
+    ull h[BPT], t = 0;
 #pragma unroll
-    for (int j = 0; j < BPT; ++j) h[j] = 0;
+    for (int j = 0; j < BPT; ++j) {
+      h[j] = 0;
+      if (b0 + j < b1) {
 #pragma unroll 4
-    for (int c = 0; c < C; ++c) {
-      const unsigned int* o = cl.map_shared_rank(&s.hist[0][0], c);
+        for (int c = 0; c < C; ++c) {
+          const unsigned int* o = cl.map_shared_rank(&s.hist[0][0], c) + b0 + j;
 #pragma unroll
-      for (int d = 0; d < D; ++d) {
-        const uint4 q = *reinterpret_cast<const uint4*>(o + d * BINS + threadIdx.x * BPT);
-        h[0] += (ull)q.x << (d * DIGIT);
-        h[1] += (ull)q.y << (d * DIGIT);
-        h[2] += (ull)q.z << (d * DIGIT);
-        h[3] += (ull)q.w << (d * DIGIT);
+          for (int d = 0; d < D; ++d) h[j] += (ull)o[d * BINS] << (d * DIGIT);
+        }
       }
+      t += h[j];
     }
-    cl.sync();  // read everywhere before it is written again
+    ull b = block_scan(t);
+    if (threadIdx.x == NT - 1) s.total = b + t;
+    __syncthreads();
+    if (threadIdx.x < C) *cl.map_shared_rank(&s.x_total[cta], threadIdx.x) = s.total;
+    cl.sync();
+    ull all = 0;
+#pragma unroll
+    for (int c = 0; c < MAX_C; ++c) {
+      if (c == cta) b += all;
+      if (c < C) all += s.x_total[c];
+    }
+    *last = need(all);
+#pragma unroll
+    for (int j = 0; j < BPT; ++j) {
+      if (b < *last && *last <= b + h[j])
+        for (int c = 0; c < C; ++c) {
+          Shared& o = *cl.map_shared_rank(&s, c);
+          o.bin = b0 + j;
+          o.before = b;
+          o.at = h[j];
+        }
+      b += h[j];
+    }
+    cl.sync();
+    return all;
   }
 
   // The bin in which the amount in order first reaches need >= 1 (s.bin), the
@@ -788,6 +839,19 @@ struct Sampler {
     }
   }
 
+  // Lists the tokens of the first bins in order, below `hi`, and hands them to
+  // the first CTA. Returns their number; more than FEW: they did not fit.
+  SPEC_DEV int list_below(float hi) {
+    // a little below any value listed
+    const float x0 = sc.m == INFINITY ? sc.m : hi == INFINITY || sc.bins == 0.f
+                         ? -INFINITY : sc.m - hi / (sc.sh * sc.bins) * 1.0001f - fabsf(sc.m) * 1e-5f;
+    part.each_above(x0, [&](int i, float x) { list(i, x, 0.f, hi); });
+    __syncthreads();
+    push_list();
+    cl.sync();
+    return *cl.map_shared_rank(&s.gathered, 0);
+  }
+
   // Appends the listed tokens to the first CTA's; what does not fit is counted
   // as more than FEW.
   SPEC_DEV void push_list() {
@@ -845,7 +909,6 @@ struct Sampler {
     if (p < 1.f) {
       block_total(keep && half == 0 ? wi : 0ull);
       const ull need = top_p_mass(p, k > 0 ? s.total : mass);
-      if (need > s.total) return -1;
       keep = keep && ahead < need;
     }
     keep = keep && wi >= qw;
@@ -869,8 +932,7 @@ struct Sampler {
 
   // The first CTA's end of the usual case: the n listed tokens sorted by
   // (key, index), cut, and drawn from in index order. mass: the row's whole
-  // mass (top-p without top-k). Returns the token, *kept_mass its kept mass; -1
-  // if the listed tokens hold less than top-p's mass.
+  // mass (top-p without top-k). Returns the token, *kept_mass its kept mass.
   SPEC_DEV int draw_few(int n, int k, float p, ull qw, float u, ull mass, ull* kept_mass) {
     if (n <= COUNTED) return draw_counted(n, k, p, qw, u, mass, kept_mass);
     int n2 = 64;
@@ -895,7 +957,6 @@ struct Sampler {
     int r = r1;
     if (p < 1.f) {
       const ull need = top_p_mass(p, k > 0 ? s.total : mass);
-      if (need > s.total) return -1;
       ull b = b0;
 #pragma unroll
       for (int j = 0; j < PT; ++j) {  // the token at which the mass reaches need is the last kept
@@ -1072,65 +1133,39 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SampleArgs a) {
   }
 
   // the tokens that may be kept, listed for the first CTA
-  const bool by_mass = k == 0;
-  const int segs = C * NT / seg_lanes, need_k = by_mass ? min(NUCLEUS, segs / 2) : k;
-  if (need_k <= segs) {
-    const int last = S.threshold(need_k, segs);
-    // (the last bin holds tokens without weight where the range was cut)
-    const float hi = last < SEG_BINS - 1 ? (float)((last + 1) * (BINS / SEG_BINS))
-                                         : range < Z_END ? INFINITY : (float)(BINS - 1);
-    // a little below any value listed
-    const float x0 = m == INFINITY ? m : hi == INFINITY || S.sc.bins == 0.f
-                         ? -INFINITY : m - hi / (sh * S.sc.bins) * 1.0001f - fabsf(m) * 1e-5f;
-    if (by_mass) {
-      S.sum_part(Mass{S.sc, s.tab, 0ull, Cut{}, false});
-      S.part.each_above(x0, [&](int i, float x) { S.list(i, x, 0.f, hi); });
-      __syncthreads();
-      if (threadIdx.x == 0) *cl.map_shared_rank(&s.x_total[cta], 0) = s.total;
-    } else {
-      S.part.each_above(x0, [&](int i, float x) { S.list(i, x, 0.f, hi); });
-      __syncthreads();
-    }
-    S.push_list();
-    cl.sync();
-    const int n = *cl.map_shared_rank(&s.gathered, 0);
-    int token = -1;
+  // the last bin holds tokens without weight where the range was cut: not listed
+  auto end_of = [&](int bins) { return bins < BINS ? (float)bins : range < Z_END ? INFINITY : (float)(BINS - 1); };
+  // the first CTA draws among the n tokens handed to it, if they fit
+  auto draw = [&](int n, ull all) {
     if (n <= FEW && cta == 0) {
-      ull mass = 0, z = 0;
-      if (by_mass)
-        for (int c = 0; c < C; ++c) mass += s.x_total[c];
-      token = S.draw_few(n, k, p, qw, u, mass, &z);
-      if (token >= 0 && threadIdx.x == 0)
-        result(token, Part<T>::one((const T*)a.logits + (size_t)row * a.ld + token), z);
+      ull z;
+      const int token = S.draw_few(n, k, p, qw, u, all, &z);
+      if (threadIdx.x == 0) result(token, Part<T>::one((const T*)a.logits + (size_t)row * a.ld + token), z);
     }
-    cl.sync();   // the first CTA's count is read, and its tokens are, before either changes
-    if (!by_mass && n <= FEW) return;
-    if (by_mass) {
-      if (cta == 0 && threadIdx.x < C) *cl.map_shared_rank(&s.few, threadIdx.x) = token >= 0;
-      cl.sync();
-      if (s.few) return;
-    }
-  }
-
-  // the cut in the whole row
-  auto all = [](int, float) { return true; };
+    cl.sync();   // its count is read, and its tokens are, before either changes
+    return n <= FEW;
+  };
+  auto every = [](int, float) { return true; };
+  auto k_of = [&](ull) { return (ull)k; };
+  auto p_of = [&](ull z) { return top_p_mass(p, z); };
   Cut cut{0xffffffffu, 0x7fffffff};
-  ull h[BPT], before;
+  ull need, before;
   if (k > 0) {
-    S.template histogram<false>(all, h);
-    S.cross(h, (ull)k, 0ull);
-    S.template cut_in_bin<false>(cut, (ull)k, all);
+    const int segs = C * NT / seg_lanes;
+    if (k <= segs && draw(S.list_below(end_of((S.threshold(k, segs) + 1) * (BINS / SEG_BINS))), 0ull)) return;
+    S.template find_bin<false>(every, k_of, &need);
+    S.template cut_in_bin<false>(cut, need, every);
   }
   if (p < 1.f) {
-    auto in = [&](int i, float x) { return kept(cut, rank_key(x), i); };
-    S.template histogram<true>(in, h);
-    ull t = 0;
-#pragma unroll
-    for (int j = 0; j < BPT; ++j) t += h[j];
-    S.block_total(t);
-    const ull need = top_p_mass(p, s.total);
-    S.cross(h, need, 0ull);
-    S.template cut_in_bin<true>(cut, need, in);
+    if (k == 0) {
+      const ull all = S.template find_bin<true>(every, p_of, &need);
+      if (draw(S.list_below(end_of(s.bin + 1)), all)) return;
+      S.template cut_in_bin<true>(cut, need, every);
+    } else {
+      auto in = [&](int i, float x) { return kept(cut, rank_key(x), i); };
+      S.template find_bin<true>(in, p_of, &need);
+      S.template cut_in_bin<true>(cut, need, in);
+    }
   }
   const Mass mass{S.sc, s.tab, qw, cut, true};
   const ull z = S.sum(mass, &before);
@@ -1213,14 +1248,17 @@ int max_clusters(int C) {
 // CTAs a row: the count with the least estimated time, waves of resident
 // clusters at a fixed cost of about 8 us (0.1 more a CTA of the exchanges) and
 // 0.17 ns a token of a CTA, twice that where two CTAs share an SM. 262144
-// tokens, measured: 1 row 13 us with 16 CTAs, 15 with 8, 58 with 1; 40 rows 40 us
-// with 6 (one wave), 50 with 8, 57 with 16.
+// tokens, measured: 1 row with top-k and top-p 13 us with 16 CTAs, 15 with 8, 58
+// with 1; 40 rows at temperature only 42 us with 6 (one wave), 51 with 8, 58 with
+// 16. Rows with filters differ in length (a broad nucleus takes up to four
+// scans), so they are spread over 8 CTAs at least where a CTA keeps 4096 tokens:
+// 64 rows with top-p 128 us with 8, 143 with 6, 164 with 4.
 template <typename T>
-int cluster_size(int M, int V) {
+int cluster_size(int M, int V, bool filters) {
   int best = MAX_C;
   double least = 1e30;
   for (int C : {1, 2, 3, 4, 5, 6, 7, 8, 12, 16}) {
-    if (V / C > DIGIT_TOKENS) continue;
+    if (V / C > DIGIT_TOKENS || (filters && C < std::min(8, V / 4096))) continue;
     const int fit = max_clusters<T>(C);
     if (fit < 1) continue;
     double us = 0;
@@ -1245,7 +1283,7 @@ int cluster_size(int M, int V) {
 
 template <typename T>
 int launch_sample(const SampleArgs& a, int pdl, cudaStream_t st) {
-  const int C = cluster_size<T>(a.M, a.V);
+  const int C = cluster_size<T>(a.M, a.V, a.top_k || a.top_p);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)a.M * C);
   cfg.blockDim = dim3(NT);
