@@ -266,6 +266,12 @@ struct LoraArgs {
 };
 int lora_shrink(const LoraArgs& a, cudaStream_t st);
 int lora_expand(const LoraArgs& a, cudaStream_t st);
+// The projection of bf16 weights w [N][K] and its bf16 adapters in one weight
+// stream (lora_gemm.cu); ws: lora_gemm_bytes().
+void setup_lora_attributes();
+size_t lora_gemm_bytes(int N, int K, int M, int rank);
+bool lora_gemm_ok(const LoraArgs& a, int w_dtype);
+int lora_gemm(LoraArgs a, const void* w, void* ws, cudaStream_t st);
 
 // Tree verify: the accepted path's K/V rows (all layers) moved from their
 // pass slots (seq_len_old + row) to consecutive positions (seq_len_old + j).

@@ -1,0 +1,678 @@
+// lora_gemm.cu -- a bf16 projection and its rows' low-rank adapters in one
+// weight stream on the fifth-generation tensor cores.
+//
+// y[m] = r_m (W (x_m * gain) + s_a B_a (A_a (x_m * gain))) with a = ids[m] and r_m
+// RMSNorm's 1/rms (1 without a gain). A preparation kernel writes the
+// activations and the shrunken rows t_m = s_a A_a (x_m * gain); the projection
+// then treats the adapters in use as more columns of W: a tile of 128 output
+// rows reduces over K / 64 chunks of W and, for every adapter in use, over the
+// chunks of B_a's 128 rows, against activation columns that hold t_m in the
+// rows of that adapter and zero elsewhere. y is written once, and W and each
+// B_a in use are read once: the operator's floor is those bytes.
+//
+// Precision. The activations enter as three bf16 planes (hi, mid, lo: 24 bits,
+// x to 2^-25) against exact bf16 weights with binary32 accumulation, so the
+// result is a binary32 projection's. (The projection kernels of a pass use two
+// planes, 2^-17.) The planes are consecutive rows of the MMA's B operand, so
+// each 16-column k-step is one MMA with N = 3 x rows.
+//
+// Work split: units are (tile, chunk of W) pairs in tile-major order, and CTA b
+// of G owns [U b / G, U (b + 1) / G); the CTA with a tile's last chunk also takes
+// the adapters' (counted on the device from the ids, by every CTA alike). A tile
+// cut between CTAs is summed by the last CTA to arrive, in CTA order. So a row's
+// result depends on neither timing, nor the other rows, nor their adapters (whose
+// chunks add exact zeros).
+//
+// Roles of a CTA's 6 warps, one CTA an SM: TMA producer (warp 0, one thread; a
+// ring of stages of a 128 x 64 weight tile and the activations' 64 columns, both
+// in the 128-byte-swizzled K-major layout; an adapter's columns past its rank
+// read as zero), MMA issue (warp 1, one thread; two accumulators alternate
+// between tiles), epilogue (warps 2-5: lane = output row,
+// so stores of an activation row are consecutive). Every wait is bounded; on a
+// timeout the CTA records it, drains its copies and MMAs and returns.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <mutex>
+
+#include "common.cuh"
+#include "mbar.cuh"
+
+namespace spec {
+
+namespace {
+
+constexpr int TM = 128;               // weight rows of a tile (MMA M)
+constexpr int KC = 64;                // columns of a chunk (one 128-byte swizzle row of bf16)
+constexpr int W_BYTES = TM * KC * 2;
+constexpr int ROWS = 64;              // activation rows of a call
+constexpr int PREP_COLS = 1024;       // columns of a preparation block
+constexpr int RMS_PARTS = 32;         // blocks of a row that leave a sum of squares (K <= 32768)
+constexpr int MAX_STAGES = 10;
+constexpr int SMEM_LIMIT = 227 * 1024;
+constexpr int NTHR = 192;
+constexpr int EPI0 = 64;              // first epilogue thread
+constexpr int TMEM_COLS = 512;
+constexpr int ACC_COLS = 256;         // columns of one of the two accumulators (up to 192 used)
+constexpr unsigned SPIN_LIMIT = 1u << 26;
+
+// The adapters in use, in order of first appearance, and each row's place
+// among them (-1: none). `n` is written by one thread; ends with a barrier.
+struct Slots {
+  int id[ROWS], slot[ROWS], used[ROWS], first[ROWS];
+  int n;
+};
+SPEC_DEV void find_slots(Slots& s, const int32_t* ids, int M, int n_adapters) {
+  const int t = threadIdx.x;
+  int id = -1;
+  if (t < M) {
+    id = ids[t];
+    if (id < 0 || id >= n_adapters) id = -1;
+    s.id[t] = id;
+  }
+  __syncthreads();
+  int lead = t;   // the first row of this row's adapter
+  if (t < M) {
+    for (int j = t - 1; j >= 0; --j) lead = s.id[j] == id ? j : lead;
+    s.first[t] = id >= 0 && lead == t;
+  }
+  __syncthreads();
+  if (t < M) {
+    int n = 0;
+    for (int j = 0; j < lead; ++j) n += s.first[j];
+    s.slot[t] = id < 0 ? -1 : n;
+    if (s.first[t]) s.used[n] = id;
+    if (t == M - 1) {
+      int all = 0;
+      for (int j = 0; j < M; ++j) all += s.first[j];
+      s.n = all;
+    }
+  }
+  __syncthreads();
+}
+
+// v as three bf16 numbers, hi + mid + lo = v to 2^-25.
+SPEC_DEV void split3(float v, uint16_t (&o)[3]) {
+  const __nv_bfloat16 h = __float2bfloat16_rn(v);
+  const float r = v - __bfloat162float(h);
+  const __nv_bfloat16 m = __float2bfloat16_rn(r);
+  o[0] = __bfloat16_as_ushort(h);
+  o[1] = __bfloat16_as_ushort(m);
+  o[2] = __bfloat16_as_ushort(__float2bfloat16_rn(r - __bfloat162float(m)));
+}
+
+// Blocks (m, y): y below the row's column blocks writes the planes of 1024
+// columns of row m and their sum of squares; the others take 8 ranks each of
+// row m's shrink and write its planes' adapter columns.
+__global__ void __launch_bounds__(128) lora_prep_kernel(LoraArgs a, int col_blocks, int MP, int KT, uint16_t* planes,
+                                                        float* rms) {
+  __shared__ Slots sl;
+  __shared__ float red[32];
+  grid_dep_launch();   // the projection starts on its weights
+  const int m = blockIdx.x, y = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const size_t plane = (size_t)MP * KT;
+  uint16_t* out = planes + (size_t)m * KT;
+  const float* x = a.x + (size_t)m * a.K;
+  if (y < col_blocks) {
+    if (m == 0 && y == 0) {
+      int bad = 0;
+      for (int i = threadIdx.x; i < a.M; i += blockDim.x) bad |= a.ids[i] < -1 || a.ids[i] >= a.n_adapters;
+      bad = __syncthreads_or(bad);
+      if (threadIdx.x == 0) *a.err = bad ? SPEC_ERR_CAPACITY : SPEC_ERR_NONE;
+      for (int i = threadIdx.x; i < a.n_cnt; i += blockDim.x) a.cnt[i] = 0u;
+    }
+    float ss = 0.f;
+    const int c = y * PREP_COLS + threadIdx.x * 8;
+    if (c < a.K) {
+      const float4 u0 = *reinterpret_cast<const float4*>(x + c), u1 = *reinterpret_cast<const float4*>(x + c + 4);
+      float v[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
+      if (a.gain) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          ss = fmaf(v[i], v[i], ss);
+          v[i] *= a.gain[c + i];
+        }
+      }
+      uint16_t o[8][3];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) split3(v[i], o[i]);
+#pragma unroll
+      for (int p = 0; p < 3; ++p) {
+        uint4 q;
+        q.x = o[0][p] | ((uint32_t)o[1][p] << 16);
+        q.y = o[2][p] | ((uint32_t)o[3][p] << 16);
+        q.z = o[4][p] | ((uint32_t)o[5][p] << 16);
+        q.w = o[6][p] | ((uint32_t)o[7][p] << 16);
+        *reinterpret_cast<uint4*>(out + p * plane + c) = q;
+      }
+    }
+    if (a.gain) {
+      const float tot = block_sum(ss, red);
+      if (threadIdx.x == 0) rms[m * RMS_PARTS + y] = tot;
+    }
+    return;
+  }
+  // ranks r0 .. r0 + 7 of row m: a warp takes two of them
+  find_slots(sl, a.ids, a.M, a.n_adapters);
+  const int r0 = (y - col_blocks) * 8, mine = sl.slot[m], rc = (a.rank + KC - 1) / KC;
+  __shared__ float t[8];
+  if (mine >= 0) {
+    const __nv_bfloat16* A = (const __nv_bfloat16*)a.a + ((size_t)sl.id[m] * a.rank + r0 + 2 * warp) * a.K;
+    float s0 = 0.f, s1 = 0.f;
+#pragma unroll 2
+    for (int c = lane * 8; c < a.K; c += 256) {
+      const uint4 w0 = ldg_stream(A + c), w1 = ldg_stream(A + a.K + c);
+      const float4 u0 = *reinterpret_cast<const float4*>(x + c), u1 = *reinterpret_cast<const float4*>(x + c + 4);
+      float v[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
+      if (a.gain) {
+        const float4 g0 = *reinterpret_cast<const float4*>(a.gain + c), g1 = *reinterpret_cast<const float4*>(a.gain + c + 4);
+        v[0] *= g0.x; v[1] *= g0.y; v[2] *= g0.z; v[3] *= g0.w;
+        v[4] *= g1.x; v[5] *= g1.y; v[6] *= g1.z; v[7] *= g1.w;
+      }
+      const uint32_t b0[4] = {w0.x, w0.y, w0.z, w0.w}, b1[4] = {w1.x, w1.y, w1.z, w1.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        s0 = fmaf(bf16lo(b0[i]), v[2 * i], fmaf(bf16hi(b0[i]), v[2 * i + 1], s0));
+        s1 = fmaf(bf16lo(b1[i]), v[2 * i], fmaf(bf16hi(b1[i]), v[2 * i + 1], s1));
+      }
+    }
+    s0 = warp_sum(s0);
+    s1 = warp_sum(s1);
+    const float sc = a.scale ? a.scale[sl.id[m]] : 1.f;
+    if (lane == 0) {
+      t[2 * warp] = s0 * sc;
+      t[2 * warp + 1] = s1 * sc;
+    }
+  }
+  __syncthreads();
+  // eight columns of every adapter in use: t in this row's, zero in the others;
+  // the last block also clears the columns up to a whole k-step
+  const int width = r0 + 8 >= a.rank && (a.rank & 15) ? 16 : 8;
+  for (int i = threadIdx.x; i < sl.n * 3 * (width / 8); i += blockDim.x) {
+    const int part = i % (width / 8), p = i / (width / 8) % 3, s = i / (width / 8) / 3;
+    uint32_t q[4] = {0, 0, 0, 0};
+    if (s == mine && part == 0)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        uint16_t o[3];
+        split3(t[j], o);
+        q[j >> 1] |= (uint32_t)(p == 0 ? o[0] : p == 1 ? o[1] : o[2]) << (16 * (j & 1));
+      }
+    *reinterpret_cast<uint4*>(out + p * plane + a.K + s * rc * KC + r0 + part * 8) = make_uint4(q[0], q[1], q[2], q[3]);
+  }
+}
+
+// ---- the projection ----------------------------------------------------------
+
+SPEC_DEV void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+SPEC_DEV void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// K-major operand in the 128-byte swizzle layout (8-row groups of 1024 bytes).
+SPEC_DEV uint64_t sw128_desc(uint32_t saddr) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) |
+         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+// kind::f16: fp32 accumulate, bf16 A and B, both K-major.
+__host__ __device__ constexpr uint32_t idesc_bf16(int M, int N) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+SPEC_DEV void mma_bf16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+SPEC_DEV void mma_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(sa(bar))
+               : "memory");
+}
+SPEC_DEV void tma_load(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+          sa(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(sa(bar))
+      : "memory");
+}
+// The same for weights, read once: first to leave L2.
+SPEC_DEV void tma_load_once(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, "
+      "%3}], [%4], %5;" ::"r"(sa(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(sa(bar)), "l"(policy)
+      : "memory");
+}
+SPEC_DEV uint64_t l2_evict_first() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+// 8 consecutive accumulator columns of this warp's 32 lanes.
+SPEC_DEV void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+SPEC_DEV void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+SPEC_DEV void epi_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
+SPEC_DEV bool wait_phase(uint64_t* b, unsigned parity, volatile int* abort_s, int* err) {
+  for (unsigned it = 0; it < SPIN_LIMIT; ++it) {
+    if (mbar_test(b, parity)) return true;
+    if (*abort_s) return false;
+  }
+  *abort_s = 1;
+  set_error(err, SPEC_ERR_TIMEOUT);
+  return false;
+}
+SPEC_DEV void drain_phase(uint64_t* b, unsigned parity) {
+  for (unsigned it = 0; it < SPIN_LIMIT; ++it)
+    if (mbar_test(b, parity)) return;
+}
+
+struct GemmArgs {
+  int M, N, K, rank, n_adapters, T, grid, stages;
+  const int32_t* ids;
+  bool norm;
+  float eps;
+  const float* rms;       // [M][RMS_PARTS]
+  float* y;               // [M][N]
+  float* fix;             // [grid][2][MP][TM]
+  unsigned int* cnt;      // [T]
+  int* err;
+};
+
+// MMA N: the three planes of MP rows.
+constexpr int mma_n(int MP) { return (3 * MP + 15) / 16 * 16; }
+
+template <int MP>
+struct Gemm {
+  static constexpr int NB = mma_n(MP);
+  static constexpr int X_BYTES = NB * KC * 2;
+  static constexpr int STAGE = W_BYTES + X_BYTES;
+  const GemmArgs& a;
+  const CUtensorMap *tmw, *tmb, *tmx;
+  const Slots& sl;
+  unsigned char* ring;
+  uint64_t *full, *empty, *accf, *acce, *drain;
+  float* rms_s;
+  volatile int* abort_s;
+  int* bc;
+  uint32_t tmem;
+  int CW, RC, E, U, u0, u1;   // chunks of a tile: CW of W, then RC of every adapter in use, E in all
+
+  // The (tile, chunk) pairs of the CTA, in the order they are streamed.
+  struct Items {
+    const Gemm& k;
+    int u, t, c, extra;
+    SPEC_DEV explicit Items(const Gemm& k_) : k(k_), u(k_.u0), t(0), c(0), extra(-1) {}
+    SPEC_DEV void next() {
+      if (extra >= 0) {
+        c = k.CW + extra;
+        if (++extra == k.E) extra = -1;
+        return;
+      }
+      t = u / k.CW;
+      c = u - t * k.CW;
+      ++u;
+      if (c == k.CW - 1 && k.E > 0) extra = 0;
+    }
+    // the pair just returned is the CTA's last of its tile
+    SPEC_DEV bool ends() const { return extra < 0 && (c >= k.CW - 1 || u == k.u1); }
+  };
+  SPEC_DEV int items() const { return u1 - u0 + E * (u1 / CW - u0 / CW); }
+
+  SPEC_DEV int unit_begin(int b) const { return (int)(((long long)b * U) / a.grid); }
+  SPEC_DEV int cta_of(int u) const {
+    int b = (int)((((long long)u + 1) * a.grid - 1) / U);
+    b = min(b, a.grid - 1);
+    while (b > 0 && unit_begin(b) > u) --b;
+    while (b + 1 < a.grid && unit_begin(b + 1) <= u) ++b;
+    return b;
+  }
+  // 16-column k-steps of chunk c
+  SPEC_DEV int steps(int c) const {
+    return c < CW ? KC / 16 : min(KC / 16, (a.rank - (c - CW) % RC * KC + 15) / 16);
+  }
+  SPEC_DEV unsigned char* stage(int s) const { return ring + (size_t)s * STAGE; }
+
+  SPEC_DEV void load_w(int s, const Items& it, uint64_t pol) const {
+    if (it.c < CW) {
+      tma_load_once(stage(s), tmw, it.c * KC, it.t * TM, &full[s], pol);
+    } else {
+      const int slot = (it.c - CW) / RC;
+      tma_load_once(stage(s), tmb, (it.c - CW - slot * RC) * KC, sl.used[slot] * a.N + it.t * TM, &full[s], pol);
+    }
+  }
+  SPEC_DEV void load_x(int s, const Items& it) const { tma_load(stage(s) + W_BYTES, tmx, it.c * KC, 0, &full[s]); }
+
+  SPEC_DEV void producer() {
+    const int nu = items(), pre = min(nu, a.stages);
+    const uint64_t pol = l2_evict_first();
+    Items iw(*this), ix(*this);
+    for (int n = 0; n < pre; ++n) {
+      iw.next();
+      mbar_expect_tx(&full[n], (unsigned)STAGE);
+      load_w(n, iw, pol);
+    }
+    grid_dep_wait();  // the activation planes come from the preparation
+    for (int n = 0; n < pre; ++n) {
+      ix.next();
+      load_x(n, ix);
+    }
+    int issued = pre;
+    for (int n = pre; n < nu; ++n) {
+      const int s = n % a.stages;
+      if (!wait_phase(&empty[s], ((n / a.stages) - 1) & 1, abort_s, a.err)) break;
+      iw.next();
+      mbar_expect_tx(&full[s], (unsigned)STAGE);
+      load_w(s, iw, pol);
+      load_x(s, iw);
+      issued = n + 1;
+    }
+    if (*abort_s)  // this CTA's copies land before its shared memory is released
+      for (int n = max(0, issued - a.stages); n < issued; ++n) drain_phase(&full[n % a.stages], (n / a.stages) & 1);
+  }
+
+  SPEC_DEV void mma_loop() {
+    constexpr uint32_t idesc = idesc_bf16(TM, NB);
+    const int nu = items();
+    Items it(*this);
+    int i = 0;             // segments (tiles) so far
+    bool first = true;     // first k-step of a segment
+    uint32_t d = tmem;
+    for (int n = 0; n < nu; ++n) {
+      it.next();
+      if (first) {
+        if (i >= 2 && !wait_phase(&acce[i & 1], ((i >> 1) - 1) & 1, abort_s, a.err)) break;
+        fence_after();
+        d = tmem + (uint32_t)((i & 1) * ACC_COLS);
+      }
+      const int s = n % a.stages;
+      if (!wait_phase(&full[s], (n / a.stages) & 1, abort_s, a.err)) break;
+      fence_after();
+      const uint32_t w = sa(stage(s)), x = w + (uint32_t)W_BYTES;
+      const int ns = steps(it.c);
+      for (int ks = 0; ks < ns; ++ks) {
+        mma_bf16(d, sw128_desc(w + 32 * ks), sw128_desc(x + 32 * ks), idesc, first ? 0u : 1u);
+        first = false;
+      }
+      mma_commit(&empty[s]);
+      if (it.ends()) {
+        mma_commit(&accf[i & 1]);
+        ++i;
+        first = true;
+      }
+    }
+    // every MMA of this CTA is complete before its tensor memory is freed
+    mma_commit(drain);
+    drain_phase(drain, 0);
+  }
+
+  // thread = output row n of the tile, lane by lane: a warp's stores of an
+  // activation row are consecutive
+  SPEC_DEV void finish(int t, int r, const float (&v)[MP]) const {
+    const int n = t * TM + r;
+    if (n >= a.N) return;
+#pragma unroll
+    for (int m = 0; m < MP; ++m)
+      if (m < a.M) a.y[(size_t)m * a.N + n] = v[m] * rms_s[m];
+  }
+
+  // A tile shared with other CTAs: publish this CTA's sums; the last to arrive
+  // adds all of them in CTA order and finishes the tile.
+  SPEC_DEV void partial(int t, int i, int r, int e, float (&v)[MP]) const {
+    const int b = blockIdx.x;
+    float* f = a.fix + (size_t)(b * 2 + (t == u0 / CW ? 0 : 1)) * MP * TM;
+#pragma unroll
+    for (int m = 0; m < MP; ++m) __stcg(f + m * TM + r, v[m]);
+    epi_sync();
+    if (e == 0) bc[2 + (i & 1)] = (int)atomic_add_acq_rel(a.cnt + t, 1u);
+    epi_sync();
+    const int bf = cta_of(t * CW), bl = cta_of(t * CW + CW - 1);
+    if (bc[2 + (i & 1)] != bl - bf) return;
+    __threadfence();
+#pragma unroll
+    for (int m = 0; m < MP; ++m) v[m] = 0.f;
+    for (int bb = bf; bb <= bl; ++bb) {
+      const float* g = a.fix + (size_t)(bb * 2 + (t == unit_begin(bb) / CW ? 0 : 1)) * MP * TM;
+      float o[MP];
+#pragma unroll
+      for (int m = 0; m < MP; ++m) o[m] = __ldcg(g + m * TM + r);
+#pragma unroll
+      for (int m = 0; m < MP; ++m) v[m] += o[m];
+    }
+    if (e == 0) a.cnt[t] = 0u;
+    finish(t, r, v);
+  }
+
+  SPEC_DEV void epilogue() {
+    const int e = threadIdx.x - EPI0, r = ((threadIdx.x >> 5) & 3) * 32 + (threadIdx.x & 31);
+    grid_dep_wait();
+    if (e < ROWS) {
+      float f = 1.f;
+      if (a.norm && e < a.M) {
+        float tot = 0.f;
+        for (int y = 0; y < (a.K + PREP_COLS - 1) / PREP_COLS; ++y) tot += __ldcg(a.rms + e * RMS_PARTS + y);
+        f = rsqrtf(tot / (float)a.K + a.eps);
+      }
+      rms_s[e] = f;
+    }
+    epi_sync();
+    int i = 0;
+    for (int u = u0; u < u1; ++i) {
+      const int t = u / CW, c0 = u - t * CW, ue = min(u1, (t + 1) * CW), c1 = ue - t * CW, acc = i & 1;
+      u = ue;
+      if (e == 0) bc[i & 1] = wait_phase(&accf[acc], (i >> 1) & 1, abort_s, a.err) ? 1 : 0;
+      epi_sync();
+      if (!bc[i & 1]) break;
+      fence_after();
+      const uint32_t taddr = tmem + ((uint32_t)(((threadIdx.x >> 5) & 3) * 32) << 16) + (uint32_t)(acc * ACC_COLS);
+      float v[MP];
+#pragma unroll
+      for (int j = 0; j < MP / 8; ++j) {
+        uint32_t q[3][8];
+#pragma unroll
+        for (int p = 0; p < 3; ++p) tmem_ld8(taddr + p * MP + 8 * j, q[p]);
+        tmem_wait_ld();
+#pragma unroll
+        for (int h = 0; h < 8; ++h)   // small terms first
+          v[8 * j + h] = (__uint_as_float(q[2][h]) + __uint_as_float(q[1][h])) + __uint_as_float(q[0][h]);
+      }
+      fence_before();
+      mbar_arrive(&acce[acc]);
+      if (c0 == 0 && c1 == CW) finish(t, r, v);
+      else partial(t, i, r, e, v);
+    }
+  }
+};
+
+template <int MP>
+__global__ void __launch_bounds__(NTHR, 1)
+    lora_gemm_kernel(const __grid_constant__ GemmArgs a, const __grid_constant__ CUtensorMap tmw,
+                     const __grid_constant__ CUtensorMap tmb, const __grid_constant__ CUtensorMap tmx) {
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  __shared__ Slots sl;
+  __shared__ __align__(8) uint64_t bars[2 * MAX_STAGES + 5];
+  __shared__ float rms_s[ROWS];
+  __shared__ uint32_t tmem_slot;
+  __shared__ int flags[5];
+  const uint32_t mis = sa(smem_raw) & 1023u;
+  Gemm<MP> k{a, &tmw, &tmb, &tmx, sl, smem_raw + (mis ? 1024 - mis : 0)};
+  k.full = bars;
+  k.empty = bars + MAX_STAGES;
+  k.accf = bars + 2 * MAX_STAGES;
+  k.acce = k.accf + 2;
+  k.drain = k.acce + 2;
+  k.rms_s = rms_s;
+  k.abort_s = flags;
+  k.bc = flags + 1;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < a.stages; ++s) {
+      mbar_init(&k.full[s], 1);
+      mbar_init(&k.empty[s], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&k.accf[i], 1);
+      mbar_init(&k.acce[i], 128);
+    }
+    mbar_init(k.drain, 1);
+    flags[0] = 0;
+    mbar_init_fence();
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sa(&tmem_slot)),
+                 "r"(TMEM_COLS)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  // (the ids are the call's input, complete before the preparation started)
+  find_slots(sl, a.ids, a.M, a.n_adapters);
+  fence_before();
+  __syncthreads();
+  fence_after();
+  k.tmem = tmem_slot;
+  k.CW = a.K / KC;
+  k.RC = (a.rank + KC - 1) / KC;
+  k.E = sl.n * k.RC;
+  k.U = a.T * k.CW;
+  k.u0 = k.unit_begin(blockIdx.x);
+  k.u1 = k.unit_begin(blockIdx.x + 1);
+  if (warp == 0) {
+    if (lane == 0) k.producer();
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) k.mma_loop();
+    __syncwarp();
+  } else {
+    k.epilogue();
+  }
+  fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(k.tmem), "r"(TMEM_COLS) : "memory");
+  }
+}
+
+// ---- host ----------------------------------------------------------------------
+
+PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
+std::once_flag g_once;
+
+void init_encode() {
+  void* fn = nullptr;
+  cudaDriverEntryPointQueryResult q;
+  if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+      q == cudaDriverEntryPointSuccess)
+    g_encode = (PFN_cuTensorMapEncodeTiled_v12000)fn;
+}
+
+// Row-major bf16 [rows][inner]; boxes of box_rows x 64 columns in the 128-byte
+// swizzle layout, zero past the ends.
+bool encode(CUtensorMap* m, const void* base, long long inner, long long rows, int box_rows) {
+  if (!g_encode || ((uintptr_t)base & 15) || (inner * 2) % 16) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)inner * 2};
+  const cuuint32_t box[2] = {(cuuint32_t)KC, (cuuint32_t)box_rows};
+  const cuuint32_t es[2] = {1, 1};
+  return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int rows_padded(int M) {
+  for (int mp : {8, 16, 32, 40, 48})
+    if (M <= mp) return mp;
+  return 64;
+}
+
+// Scratch of the fused path: sums of squares, counters, split-tile sums, planes.
+struct Scratch {
+  size_t rms, cnt, fix, planes, bytes;
+};
+Scratch scratch(int N, int K, int M, int rank) {
+  const int MP = rows_padded(M), rc = (rank + KC - 1) / KC;
+  auto up = [](size_t n) { return (n + 255) / 256 * 256; };
+  Scratch s;
+  s.rms = 0;
+  s.cnt = s.rms + up((size_t)ROWS * RMS_PARTS * sizeof(float));
+  s.fix = s.cnt + up((size_t)((N + TM - 1) / TM) * sizeof(unsigned int));
+  s.planes = s.fix + up((size_t)num_sms() * 2 * MP * TM * sizeof(float));
+  s.bytes = s.planes + up((size_t)mma_n(MP) * (K + (size_t)M * rc * KC) * 2);
+  return s;
+}
+
+template <int MP>
+cudaError_t launch_gemm(GemmArgs& g, const CUtensorMap& tmw, const CUtensorMap& tmb, const CUtensorMap& tmx,
+                        cudaStream_t st) {
+  g.stages = std::min(MAX_STAGES, (SMEM_LIMIT - 4096) / Gemm<MP>::STAGE);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(g.grid);
+  cfg.blockDim = dim3(NTHR);
+  cfg.dynamicSmemBytes = (size_t)g.stages * Gemm<MP>::STAGE + 1024;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, lora_gemm_kernel<MP>, g, tmw, tmb, tmx);
+}
+
+}  // namespace
+
+void setup_lora_attributes() {
+  const int n = SMEM_LIMIT - 3072;
+  cudaFuncSetAttribute(lora_gemm_kernel<8>, cudaFuncAttributeMaxDynamicSharedMemorySize, n);
+  cudaFuncSetAttribute(lora_gemm_kernel<16>, cudaFuncAttributeMaxDynamicSharedMemorySize, n);
+  cudaFuncSetAttribute(lora_gemm_kernel<32>, cudaFuncAttributeMaxDynamicSharedMemorySize, n);
+  cudaFuncSetAttribute(lora_gemm_kernel<40>, cudaFuncAttributeMaxDynamicSharedMemorySize, n);
+  cudaFuncSetAttribute(lora_gemm_kernel<48>, cudaFuncAttributeMaxDynamicSharedMemorySize, n);
+  cudaFuncSetAttribute(lora_gemm_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, n);
+}
+
+size_t lora_gemm_bytes(int N, int K, int M, int rank) { return scratch(N, K, M, rank).bytes; }
+
+bool lora_gemm_ok(const LoraArgs& a, int w_dtype) {
+  return w_dtype == DT_BF16 && a.dtype == DT_BF16 && a.K % KC == 0 && a.K <= PREP_COLS * RMS_PARTS &&
+         (long long)a.n_adapters * a.N + TM < (1ll << 31);
+}
+
+int lora_gemm(LoraArgs a, const void* w, void* ws, cudaStream_t st) {
+  std::call_once(g_once, init_encode);
+  const int MP = rows_padded(a.M), rc = (a.rank + KC - 1) / KC, KT = a.K + std::min(a.M, a.n_adapters) * rc * KC;
+  const Scratch s = scratch(a.N, a.K, a.M, a.rank);
+  char* base = (char*)ws;
+  uint16_t* planes = (uint16_t*)(base + s.planes);
+  GemmArgs g = {};
+  g.M = a.M; g.N = a.N; g.K = a.K; g.rank = a.rank; g.n_adapters = a.n_adapters;
+  g.T = (a.N + TM - 1) / TM;
+  g.grid = (int)std::min<long long>((long long)g.T * (a.K / KC), num_sms());
+  g.ids = a.ids; g.norm = a.gain != nullptr; g.eps = a.eps;
+  g.rms = (const float*)(base + s.rms); g.y = a.y; g.fix = (float*)(base + s.fix);
+  g.cnt = (unsigned int*)(base + s.cnt); g.err = a.err;
+  a.cnt = g.cnt;
+  a.n_cnt = g.T;
+  CUtensorMap tmw, tmb, tmx;
+  if (!encode(&tmw, w, a.K, a.N, TM) || !encode(&tmb, a.b, a.rank, (long long)a.n_adapters * a.N, TM) ||
+      !encode(&tmx, planes, KT, mma_n(MP), mma_n(MP)))
+    return -1;
+  const int col_blocks = (a.K + PREP_COLS - 1) / PREP_COLS;
+  lora_prep_kernel<<<dim3(a.M, col_blocks + a.rank / 8), 128, 0, st>>>(a, col_blocks, MP, KT, planes, (float*)(base + s.rms));
+  if (cudaGetLastError() != cudaSuccess) return -1;
+  cudaError_t e;
+  switch (MP) {
+    case 8: e = launch_gemm<8>(g, tmw, tmb, tmx, st); break;
+    case 16: e = launch_gemm<16>(g, tmw, tmb, tmx, st); break;
+    case 32: e = launch_gemm<32>(g, tmw, tmb, tmx, st); break;
+    case 40: e = launch_gemm<40>(g, tmw, tmb, tmx, st); break;
+    case 48: e = launch_gemm<48>(g, tmw, tmb, tmx, st); break;
+    default: e = launch_gemm<64>(g, tmw, tmb, tmx, st); break;
+  }
+  return e == cudaSuccess ? 2 : -1;
+}
+
+}  // namespace spec

@@ -287,6 +287,7 @@ void spec::setup_device_attributes() {
   setup_attn_flash_attributes();
   setup_moe_attributes();
   setup_sample_attributes();
+  setup_lora_attributes();
   done[dev] = true;
 }
 
@@ -982,7 +983,8 @@ static size_t lora_head_bytes(int M, int rank) { return 256 + ((size_t)M * rank 
 size_t spec_linear_lora_workspace_bytes(int32_t N, int32_t K, int32_t M, int32_t rank) {
   if (rank <= 0) return 0;
   const size_t n = spec_linear_workspace_bytes(N, K, M);
-  return n ? n + lora_head_bytes(M, rank) : 0;
+  if (n == 0 || M > 64) return 0;
+  return std::max(n + lora_head_bytes(M, rank), 256 + lora_gemm_bytes(N, K, M, rank));
 }
 
 spec_status spec_linear_lora(const spec_matrix* w, int32_t N, int32_t K, const float* x, int32_t M, const float* gain,
@@ -1002,10 +1004,14 @@ spec_status spec_linear_lora(const spec_matrix* w, int32_t N, int32_t K, const f
   a.M = M; a.N = N; a.K = K; a.rank = lora->rank; a.n_adapters = lora->n_adapters;
   a.a = lora->a; a.b = lora->b; a.scale = lora->scale; a.ids = ids; a.x = x; a.gain = gain; a.eps = eps;
   a.err = (int*)workspace; a.t = (float*)((char*)workspace + 256); a.y = y;
+  setup_device_attributes();
+  if (lora_gemm_ok(a, w->dtype)) {
+    if (lora_gemm(a, w->data, (char*)workspace + 256, st) < 0) return SPEC_ECUDA;
+    return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ECUDA;
+  }
   a.cnt = g.tc_cnt; a.n_cnt = (int)linear_counters(N);
   a.add = N % 4 != 0;
   g.epi = a.add ? EPI_STORE : EPI_ADD;
-  setup_device_attributes();
   if (lora_shrink(a, st) < 0) return SPEC_ECUDA;
   if (!a.add && lora_expand(a, st) < 0) return SPEC_ECUDA;
   if (gemv(g, st) < 0) return SPEC_ECUDA;

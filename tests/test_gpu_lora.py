@@ -87,23 +87,40 @@ def test_adapter_part_alone(adt, M, N, K, r, norm):
     assert np.linalg.norm(y - want) <= 1e-6 * np.linalg.norm(want) + 1e-30
 
 
-def test_rows_without_an_adapter_are_the_plain_projection():
-    """Bit for bit, whatever the other rows bring; unused adapters are not read
-    into any row."""
+@pytest.mark.parametrize("dtype", [configs.BF16, configs.Q4_0, configs.F32])
+@pytest.mark.parametrize("N,M", [(1024, 8), (1024, 40), (1023, 5), (20000, 12)])
+def test_rows_without_an_adapter(dtype, N, M):
+    """Bit for bit those of a call without adapters, whatever the other rows
+    bring; unused adapters are not read into any row."""
     g = _gen(2)
-    for N, M in ((1024, 8), (1024, 40), (1023, 5)):
-        w = synth.make_matrix(g, configs.BF16, 1, N, 512, 0.02, "cuda")
-        lora = _adapters(g, 4, 16, N, 512, torch.bfloat16)
-        lora.a[2] = float("nan")
-        lora.b[2] = float("inf")
-        x = torch.randn((M, 512), generator=g, device="cuda")
-        ids = torch.full((M,), -1, dtype=torch.int32, device="cuda")
-        ids[::3] = 1
-        plain = binding.spec_linear(w, x)
-        y = binding.spec_linear_lora(w, x, lora, ids)
-        assert torch.equal(y[ids < 0], plain[ids < 0]) and torch.isfinite(y).all()
-        none = binding.spec_linear_lora(w, x, lora, torch.full_like(ids, -1))
-        assert torch.equal(none, plain)
+    w = synth.make_matrix(g, dtype, 1, N, 512, 0.02, "cuda")
+    lora = _adapters(g, 4, 16, N, 512, torch.bfloat16)
+    lora.a[2] = float("nan")
+    lora.b[2] = float("inf")
+    x = torch.randn((M, 512), generator=g, device="cuda")
+    ids = torch.full((M,), -1, dtype=torch.int32, device="cuda")
+    none = binding.spec_linear_lora(w, x, lora, ids)
+    assert_rows_close(none.cpu().numpy(), _base(w, x, None), KTOL, "no adapters")
+    ids[::3] = 1
+    ids[1::3] = 3
+    y = binding.spec_linear_lora(w, x, lora, ids)
+    assert torch.equal(y[ids < 0], none[ids < 0]) and torch.isfinite(y).all()
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 4096, 1536), (12, 2560, 6144), (40, 3000, 2560), (64, 130, 24576)])
+def test_bf16_is_a_binary32_projection(M, N, K):
+    """bf16 weights and adapters: activations in three 16-bit planes (2^-25), exact
+    products, binary32 sums. A sum of n products of random sign is off by about
+    sqrt(n) * 2^-24 of a product's size times the number of roundings of a partial
+    sum, relative to a result of sqrt(n) such products: well below 2^-20."""
+    g = _gen(N)
+    w = synth.make_matrix(g, configs.BF16, 1, N, K, 0.02, "cuda")
+    lora = _adapters(g, 5, 16, N, K, torch.bfloat16)
+    ids = torch.randint(-1, 5, (M,), generator=g, device="cuda", dtype=torch.int32)
+    x = torch.randn((M, K), generator=g, device="cuda")
+    want = torch.as_tensor(_delta(x, lora, ids, None)[0], device="cuda") + x.double() @ w.data[0].double().t()
+    y = binding.spec_linear_lora(w, x, lora, ids).double()
+    assert (y - want).norm() <= 2.0 ** -20 * want.norm()
 
 
 def test_a_row_depends_on_its_adapter_only():
