@@ -256,49 +256,61 @@ _SETTINGS = (("temperature", torch.float32), ("top_k", torch.int32), ("top_p", t
              ("min_p", torch.float32), ("uniform", torch.float32))
 
 
-def _sampling(fn, device, M, *settings) -> spec_sampling:
-    """Settings of M rows (temperature, top_k, top_p, min_p, uniform; None: left out)."""
-    s = spec_sampling()
-    for (name, dtype), t in zip(_SETTINGS, settings):
-        if t is None:
-            _need(fn, name != "uniform", "uniform numbers are required")
-            continue
-        _need(fn, t.dtype == dtype and t.dim() == 1 and t.shape[0] == M and t.is_contiguous() and t.device == device,
-              "%s must be a contiguous %s tensor of %d rows on %s" % (name, dtype, M, device))
-        setattr(s, name, t.data_ptr())
-    return s
+def _row(fn, name, t, dtype, M, dev):
+    """Address of one setting of M rows on GPU `dev` (its index), None left out."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.dim() != 1 or t.numel() != M or t.get_device() != dev or not t.is_contiguous():
+        raise SpecError(fn, SPEC_EINVAL, "%s must be a contiguous %s tensor of %d rows beside the logits"
+                        % (name, dtype, M))
+    return t.data_ptr()
+
+
+def _sampling(fn, dev, M, temperature, top_k, top_p, min_p, uniform) -> spec_sampling:
+    """Settings of M rows, None leaves one out."""
+    _need(fn, uniform is not None, "uniform numbers are required")
+    f = torch.float32
+    return spec_sampling(_row(fn, "temperature", temperature, f, M, dev), _row(fn, "top_k", top_k, torch.int32, M, dev),
+                         _row(fn, "top_p", top_p, f, M, dev), _row(fn, "min_p", min_p, f, M, dev),
+                         _row(fn, "uniform", uniform, f, M, dev))
 
 
 _LOGIT_DTYPES = {torch.float32: 0, torch.bfloat16: 1}
 
 
-def _logits(fn, logits, rows=None):
-    """(dtype code, row stride) of a [M][V] logits tensor whose rows may be strided."""
-    _need(fn, logits.is_cuda and logits.dim() == 2 and logits.dtype in _LOGIT_DTYPES,
+def _logits(fn, logits):
+    """(rows, V, dtype code, row stride, GPU) of a [rows][V] tensor whose rows may be strided."""
+    dt = _LOGIT_DTYPES.get(logits.dtype)
+    _need(fn, logits.is_cuda and logits.dim() == 2 and dt is not None,
           "logits must be a float32 or bfloat16 CUDA tensor [rows][V]")
     M, V = logits.shape
-    _need(fn, M > 0 and V > 0 and (rows is None or M == rows), "logits must have %s rows" % (rows or "some"))
-    ld = logits.stride(0) if M > 1 else V
-    _need(fn, (V == 1 or logits.stride(1) == 1) and ld >= V, "the logits of a row must be contiguous")
-    return _LOGIT_DTYPES[logits.dtype], ld
+    _need(fn, M > 0 and V > 0, "no logits")
+    ld, step = logits.stride()
+    ld = ld if M > 1 else V
+    _need(fn, (V == 1 or step == 1) and ld >= V, "the logits of a row must be contiguous")
+    return M, V, dt, ld, logits.get_device()
+
+
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else \
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream
 
 
 class _on:
-    """The tensor's device made current for a call, and the stream it goes to:
-    the given one, or the device's current one. What the call allocates belongs
-    to that stream."""
+    """The GPU of a call's tensors made current, and the stream it goes to: the
+    given one, or the GPU's current one. What the call allocates belongs to that
+    stream."""
 
-    def __init__(self, t, stream):
-        self.ctx = None
+    def __init__(self, dev, stream):
+        self.dev, self.ctx = dev, None
         if stream is not None:
             self.ctx = torch.cuda.stream(stream)
-        elif t.device.index != torch.cuda.current_device():
-            self.ctx = torch.cuda.device(t.device)
+        elif dev != torch.cuda.current_device():
+            self.ctx = torch.cuda.device(dev)
 
     def __enter__(self):
         if self.ctx is not None:
             self.ctx.__enter__()
-        return torch.cuda.current_stream().cuda_stream
+        return _raw_stream(self.dev)
 
     def __exit__(self, *e):
         if self.ctx is not None:
@@ -313,13 +325,13 @@ def spec_sample(logits: torch.Tensor, uniform: torch.Tensor, temperature: Option
     include/spec.h spec_sampling). Returns (tokens int32 [M], probs float32 [M]);
     a row without a distribution gives token -1 and probability 0."""
     fn = "spec_sample"
-    dt, ld = _logits(fn, logits)
-    M, V = logits.shape
-    s = _sampling(fn, logits.device, M, temperature, top_k, top_p, min_p, uniform)
-    with _on(logits, stream) as st:
-        tokens = torch.empty(M, dtype=torch.int32, device=logits.device)
-        probs = torch.empty(M, dtype=torch.float32, device=logits.device)
-        check(fn, lib().spec_sample(dt, _ptr(logits), ld, M, V, C.byref(s), _ptr(tokens), _ptr(probs), st))
+    M, V, dt, ld, dev = _logits(fn, logits)
+    s = _sampling(fn, dev, M, temperature, top_k, top_p, min_p, uniform)
+    with _on(dev, stream) as st:
+        tokens = torch.empty_like(uniform, dtype=torch.int32)
+        probs = torch.empty_like(uniform)
+        rc = lib().spec_sample(dt, logits.data_ptr(), ld, M, V, C.byref(s), tokens.data_ptr(), probs.data_ptr(), st)
+    check(fn, rc)
     return tokens, probs
 
 
@@ -330,18 +342,19 @@ def spec_accept_sampled(logits: torch.Tensor, drafts: torch.Tensor, uniform: tor
     verify pass; the settings have a row for each row of logits. Returns
     (out_tokens int32 [B][k+1], n_emitted int32 [B], probs float32 [B][k+1])."""
     fn = "spec_accept_sampled"
-    _need(fn, drafts.dim() == 2 and drafts.dtype == torch.int32 and drafts.is_contiguous() and
-          drafts.device == logits.device, "drafts must be a contiguous int32 tensor [B][k] beside the logits")
+    M, V, dt, ld, dev = _logits(fn, logits)
+    _need(fn, drafts.dim() == 2 and drafts.dtype is torch.int32 and drafts.is_contiguous() and
+          drafts.get_device() == dev, "drafts must be a contiguous int32 tensor [B][k] beside the logits")
     B, k = drafts.shape
-    dt, ld = _logits(fn, logits, B * (k + 1))
-    M, V = logits.shape
-    s = _sampling(fn, logits.device, M, temperature, top_k, top_p, min_p, uniform)
-    with _on(logits, stream) as st:
-        out = torch.empty((B, k + 1), dtype=torch.int32, device=logits.device)
-        ne = torch.empty(B, dtype=torch.int32, device=logits.device)
-        probs = torch.empty((B, k + 1), dtype=torch.float32, device=logits.device)
-        check(fn, lib().spec_accept_sampled(dt, _ptr(logits), ld, B, k, V, _ptr(drafts) if k else None, C.byref(s),
-                                            _ptr(out), _ptr(ne), _ptr(probs), st))
+    _need(fn, M == B * (k + 1), "logits must have a row for every draft and one more of every sequence")
+    s = _sampling(fn, dev, M, temperature, top_k, top_p, min_p, uniform)
+    with _on(dev, stream) as st:
+        out = drafts.new_empty((B, k + 1))
+        ne = drafts.new_empty(B)
+        probs = uniform.new_empty((B, k + 1))
+        rc = lib().spec_accept_sampled(dt, logits.data_ptr(), ld, B, k, V, drafts.data_ptr() if k else None, C.byref(s),
+                                       out.data_ptr(), ne.data_ptr(), probs.data_ptr(), st)
+    check(fn, rc)
     return out, ne, probs
 
 
@@ -362,6 +375,7 @@ class Lora:
         self.a, self.b, self.scale = a, b, scale
         self.n, self.rank, self.K = a.shape
         self.N = b.shape[1]
+        self.dev = a.get_device()
         self.desc = spec_lora(_LOGIT_DTYPES[a.dtype], self.n, self.rank, _ptr(a), _ptr(b), _ptr(scale))
 
 
@@ -374,28 +388,32 @@ def spec_linear_lora(w, x: torch.Tensor, lora: Lora, ids: torch.Tensor, gain: Op
     call's stream when not given; its first int records an id out of range."""
     fn = "spec_linear_lora"
     L = lib()
-    dev = x.device
-    _need(fn, x.is_cuda and x.dim() == 2 and x.dtype == torch.float32 and x.is_contiguous() and x.shape[1] == w.K,
+    dev = x.get_device()
+    N, K = w.N, w.K
+    _need(fn, x.is_cuda and x.dim() == 2 and x.dtype is torch.float32 and x.is_contiguous() and x.shape[1] == K,
           "x must be a contiguous float32 CUDA tensor [M][K]")
     M = x.shape[0]
-    _need(fn, lora.K == w.K and lora.N == w.N and lora.a.device == dev and w.data.device == dev,
+    _need(fn, lora.K == K and lora.N == N and lora.dev == dev and w.data.get_device() == dev,
           "the adapters must have the projection's N and K, on its device")
-    _need(fn, ids.dtype == torch.int32 and ids.shape == (M,) and ids.is_contiguous() and ids.device == dev,
-          "ids must be a contiguous int32 tensor [M] beside x")
-    _need(fn, gain is None or (gain.dtype == torch.float32 and gain.shape == (w.K,) and gain.is_contiguous() and
-                               gain.device == dev), "gain must be a contiguous float32 tensor [K] beside x")
-    _need(fn, y is None or (y.dtype == torch.float32 and y.shape == (M, w.N) and y.is_contiguous() and
-                            y.device == dev), "y must be a contiguous float32 tensor [M][N] beside x")
+    _need(fn, ids.dtype is torch.int32 and ids.dim() == 1 and ids.numel() == M and ids.is_contiguous() and
+          ids.get_device() == dev, "ids must be a contiguous int32 tensor [M] beside x")
+    _need(fn, gain is None or (gain.dtype is torch.float32 and gain.dim() == 1 and gain.numel() == K and
+                               gain.is_contiguous() and gain.get_device() == dev),
+          "gain must be a contiguous float32 tensor [K] beside x")
+    _need(fn, y is None or (y.dtype is torch.float32 and y.shape == (M, N) and y.is_contiguous() and
+                            y.get_device() == dev), "y must be a contiguous float32 tensor [M][N] beside x")
     _need(fn, 0 <= layer < w.L, "layer out of range")
-    m = spec_matrix(DTYPES[w.dtype], _ptr(w.data[layer]), _ptr(w.scales[layer]) if w.scales is not None else None)
-    with _on(x, stream) as st:
+    m = spec_matrix(DTYPES[w.dtype], w.data[layer].data_ptr() if layer else w.data.data_ptr(),
+                    None if w.scales is None else w.scales[layer].data_ptr())
+    with _on(dev, stream) as st:
         if y is None:
-            y = torch.empty((M, w.N), dtype=torch.float32, device=dev)
+            y = x.new_empty((M, N))
         if workspace is None:
-            n = L.spec_linear_lora_workspace_bytes(w.N, w.K, M, lora.rank)
-            workspace = torch.empty(max(n, 1), dtype=torch.uint8, device=dev)
-        check(fn, L.spec_linear_lora(C.byref(m), w.N, w.K, _ptr(x), M, _ptr(gain), eps, C.byref(lora.desc), _ptr(ids),
-                                     _ptr(y), _ptr(workspace), workspace.numel(), st))
+            n = L.spec_linear_lora_workspace_bytes(N, K, M, lora.rank)
+            workspace = x.new_empty(max(n, 1), dtype=torch.uint8)
+        rc = L.spec_linear_lora(C.byref(m), N, K, x.data_ptr(), M, _ptr(gain), eps, C.byref(lora.desc), ids.data_ptr(),
+                                y.data_ptr(), workspace.data_ptr(), workspace.numel(), st)
+    check(fn, rc)
     return y
 
 
@@ -547,7 +565,7 @@ class Engine:
         # (the converted tensors live until leave() orders their reuse after the copies)
         given = [None if t is None else torch.as_tensor(t).reshape(-1).to(self.device, dtype)
                  for (_, dtype), t in zip(_SETTINGS, (temperature, top_k, top_p, min_p, uniform))]
-        s = _sampling("spec_verify_sampled", self.pool.device, M,
+        s = _sampling("spec_verify_sampled", self.pool.get_device(), M,
                       *(None if t is None else self._in(name, t) for (name, _), t in zip(_SETTINGS, given)))
         self.enter()
         out = self._buf("out_tokens", (B, k + 1))

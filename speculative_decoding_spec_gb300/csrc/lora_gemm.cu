@@ -11,10 +11,12 @@
 // B_a in use are read once: the operator's floor is those bytes.
 //
 // Precision. The activations enter as three bf16 planes (hi, mid, lo: 24 bits,
-// x to 2^-25) against exact bf16 weights with binary32 accumulation, so the
-// result is a binary32 projection's. (The projection kernels of a pass use two
-// planes, 2^-17.) The planes are consecutive rows of the MMA's B operand, so
-// each 16-column k-step is one MMA with N = 3 x rows.
+// x to 2^-25) against exact bf16 weights, and the tensor cores' sums, which
+// round towards zero, leave tensor memory every FLUSH chunks and are added up in
+// registers: the result is a binary32 projection's. (Measured at 40 x 49152 x
+// 6144 against 64 bits: 6.0e-6 with one sum over all of K. The projection
+// kernels of a pass use two planes, 2^-17.) The planes are consecutive rows of
+// the MMA's B operand, so each 16-column k-step is one MMA with N = 3 x rows.
 //
 // Work split: units are (tile, chunk of W) pairs in tile-major order, and CTA b
 // of G owns [U b / G, U (b + 1) / G); the CTA with a tile's last chunk also takes
@@ -24,11 +26,13 @@
 // chunks add exact zeros).
 //
 // Roles of a CTA's 6 warps, one CTA an SM: TMA producer (warp 0, one thread; a
-// ring of stages of a 128 x 64 weight tile and the activations' 64 columns, both
-// in the 128-byte-swizzled K-major layout; an adapter's columns past its rank
-// read as zero), MMA issue (warp 1, one thread; two accumulators alternate
-// between tiles), epilogue (warps 2-5: lane = output row,
-// so stores of an activation row are consecutive). Every wait is bounded; on a
+// ring of stages of a weight tile's 64 columns and the activations', both in the
+// 128-byte-swizzled K-major layout; an adapter's columns past its rank read as
+// zero), MMA issue (warp 1, one thread; two accumulators alternate where they
+// fit), epilogue (warps 2-5: lane = output row,
+// so stores of an activation row are consecutive). A tile of 256 rows is two MMAs
+// a k-step on one load of the activations: half their traffic out of L2, and half
+// the barrier work of the two single threads, which bound 128-row tiles. Every wait is bounded; on a
 // timeout the CTA records it, drains its copies and MMAs and returns.
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -43,9 +47,9 @@ namespace spec {
 
 namespace {
 
-constexpr int TM = 128;               // weight rows of a tile (MMA M)
+constexpr int TM = 128;               // weight rows of an MMA; a tile is one or two of them
 constexpr int KC = 64;                // columns of a chunk (one 128-byte swizzle row of bf16)
-constexpr int W_BYTES = TM * KC * 2;
+constexpr int SUB_BYTES = TM * KC * 2;
 constexpr int ROWS = 64;              // activation rows of a call
 constexpr int PREP_COLS = 1024;       // columns of a preparation block
 constexpr int RMS_PARTS = 32;         // blocks of a row that leave a sum of squares (K <= 32768)
@@ -54,40 +58,44 @@ constexpr int SMEM_LIMIT = 227 * 1024;
 constexpr int NTHR = 192;
 constexpr int EPI0 = 64;              // first epilogue thread
 constexpr int TMEM_COLS = 512;
-constexpr int ACC_COLS = 256;         // columns of one of the two accumulators (up to 192 used)
+constexpr int FLUSH = 8;              // chunks summed in tensor memory (a multiple of an adapter's chunks)
 constexpr unsigned SPIN_LIMIT = 1u << 26;
 
 // The adapters in use, in order of first appearance, and each row's place
-// among them (-1: none). `n` is written by one thread; ends with a barrier.
+// among them (-1: none). Called by every thread; ends with a barrier.
 struct Slots {
-  int id[ROWS], slot[ROWS], used[ROWS], first[ROWS];
+  int4 id[ROWS / 4];
+  int slot[ROWS], used[ROWS], lead[2];
   int n;
 };
 SPEC_DEV void find_slots(Slots& s, const int32_t* ids, int M, int n_adapters) {
   const int t = threadIdx.x;
   int id = -1;
-  if (t < M) {
-    id = ids[t];
-    if (id < 0 || id >= n_adapters) id = -1;
-    s.id[t] = id;
-  }
+  if (t < M) id = ids[t];
+  if (id < 0 || id >= n_adapters) id = -1;
+  if (t < ROWS) reinterpret_cast<int*>(s.id)[t] = id;
   __syncthreads();
-  int lead = t;   // the first row of this row's adapter
-  if (t < M) {
-    for (int j = t - 1; j >= 0; --j) lead = s.id[j] == id ? j : lead;
-    s.first[t] = id >= 0 && lead == t;
-  }
-  __syncthreads();
-  if (t < M) {
-    int n = 0;
-    for (int j = 0; j < lead; ++j) n += s.first[j];
-    s.slot[t] = id < 0 ? -1 : n;
-    if (s.first[t]) s.used[n] = id;
-    if (t == M - 1) {
-      int all = 0;
-      for (int j = 0; j < M; ++j) all += s.first[j];
-      s.n = all;
+  int lead = 0;   // the first row of this row's adapter
+  if (t < ROWS) {
+    unsigned int lo = 0, hi = 0;   // the rows of this adapter
+#pragma unroll
+    for (int j = 0; j < ROWS / 4; ++j) {
+      const int4 o = s.id[j];
+      const unsigned int bits = (o.x == id ? 1u : 0u) | (o.y == id ? 2u : 0u) | (o.z == id ? 4u : 0u) | (o.w == id ? 8u : 0u);
+      if (j < 8) lo |= bits << (4 * j);
+      else hi |= bits << (4 * (j - 8));
     }
+    lead = lo ? __ffs(lo) - 1 : 31 + __ffs(hi);
+    const unsigned int first = __ballot_sync(FULL, id >= 0 && lead == t);
+    if ((t & 31) == 0) s.lead[t >> 5] = (int)first;
+  }
+  __syncthreads();
+  if (t < ROWS) {
+    const unsigned int lo = (unsigned int)s.lead[0], hi = (unsigned int)s.lead[1];
+    const int n = lead < 32 ? __popc(lo & ((1u << lead) - 1)) : __popc(lo) + __popc(hi & ((1u << (lead - 32)) - 1));
+    s.slot[t] = id < 0 ? -1 : n;
+    if (id >= 0 && lead == t) s.used[n] = id;
+    if (t == 0) s.n = __popc(lo) + __popc(hi);
   }
   __syncthreads();
 }
@@ -104,11 +112,14 @@ SPEC_DEV void split3(float v, uint16_t (&o)[3]) {
 
 // Blocks (m, y): y below the row's column blocks writes the planes of 1024
 // columns of row m and their sum of squares; the others take 8 ranks each of
-// row m's shrink and write its planes' adapter columns.
-__global__ void __launch_bounds__(128) lora_prep_kernel(LoraArgs a, int col_blocks, int MP, int KT, uint16_t* planes,
-                                                        float* rms) {
+// row m's shrink, all warps together along K, and write its planes' adapter
+// columns. Rows that share an adapter read it from L2.
+constexpr int PREP_THR = 256;
+__global__ void __launch_bounds__(PREP_THR) lora_prep_kernel(LoraArgs a, int col_blocks, int MP, int KT, uint16_t* planes,
+                                                             float* rms) {
   __shared__ Slots sl;
   __shared__ float red[32];
+  __shared__ float sums[PREP_THR / 32][8];
   grid_dep_launch();   // the projection starts on its weights
   const int m = blockIdx.x, y = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const size_t plane = (size_t)MP * KT;
@@ -123,29 +134,22 @@ __global__ void __launch_bounds__(128) lora_prep_kernel(LoraArgs a, int col_bloc
       for (int i = threadIdx.x; i < a.n_cnt; i += blockDim.x) a.cnt[i] = 0u;
     }
     float ss = 0.f;
-    const int c = y * PREP_COLS + threadIdx.x * 8;
+    const int c = y * PREP_COLS + threadIdx.x * 4;
     if (c < a.K) {
-      const float4 u0 = *reinterpret_cast<const float4*>(x + c), u1 = *reinterpret_cast<const float4*>(x + c + 4);
-      float v[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
+      const float4 u = *reinterpret_cast<const float4*>(x + c);
+      float v[4] = {u.x, u.y, u.z, u.w};
       if (a.gain) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          ss = fmaf(v[i], v[i], ss);
-          v[i] *= a.gain[c + i];
-        }
+        const float4 g = *reinterpret_cast<const float4*>(a.gain + c);
+        ss = fmaf(v[0], v[0], fmaf(v[1], v[1], fmaf(v[2], v[2], v[3] * v[3])));
+        v[0] *= g.x; v[1] *= g.y; v[2] *= g.z; v[3] *= g.w;
       }
-      uint16_t o[8][3];
+      uint16_t o[4][3];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) split3(v[i], o[i]);
+      for (int i = 0; i < 4; ++i) split3(v[i], o[i]);
 #pragma unroll
-      for (int p = 0; p < 3; ++p) {
-        uint4 q;
-        q.x = o[0][p] | ((uint32_t)o[1][p] << 16);
-        q.y = o[2][p] | ((uint32_t)o[3][p] << 16);
-        q.z = o[4][p] | ((uint32_t)o[5][p] << 16);
-        q.w = o[6][p] | ((uint32_t)o[7][p] << 16);
-        *reinterpret_cast<uint4*>(out + p * plane + c) = q;
-      }
+      for (int p = 0; p < 3; ++p)
+        *reinterpret_cast<uint2*>(out + p * plane + c) =
+            make_uint2(o[0][p] | ((uint32_t)o[1][p] << 16), o[2][p] | ((uint32_t)o[3][p] << 16));
     }
     if (a.gain) {
       const float tot = block_sum(ss, red);
@@ -153,16 +157,17 @@ __global__ void __launch_bounds__(128) lora_prep_kernel(LoraArgs a, int col_bloc
     }
     return;
   }
-  // ranks r0 .. r0 + 7 of row m: a warp takes two of them
-  find_slots(sl, a.ids, a.M, a.n_adapters);
-  const int r0 = (y - col_blocks) * 8, mine = sl.slot[m], rc = (a.rank + KC - 1) / KC;
-  __shared__ float t[8];
-  if (mine >= 0) {
-    const __nv_bfloat16* A = (const __nv_bfloat16*)a.a + ((size_t)sl.id[m] * a.rank + r0 + 2 * warp) * a.K;
-    float s0 = 0.f, s1 = 0.f;
-#pragma unroll 2
-    for (int c = lane * 8; c < a.K; c += 256) {
-      const uint4 w0 = ldg_stream(A + c), w1 = ldg_stream(A + a.K + c);
+  const int r0 = (y - col_blocks) * 8, rc = (a.rank + KC - 1) / KC, id = a.ids[m];
+  const bool has = id >= 0 && id < a.n_adapters;
+  if (has) {
+    const __nv_bfloat16* A = (const __nv_bfloat16*)a.a + ((size_t)id * a.rank + r0) * a.K;
+    float acc[8];
+#pragma unroll
+    for (int r = 0; r < 8; ++r) acc[r] = 0.f;
+    for (int c = threadIdx.x * 8; c < a.K; c += PREP_THR * 8) {
+      uint4 w[8];
+#pragma unroll
+      for (int r = 0; r < 8; ++r) w[r] = *reinterpret_cast<const uint4*>(A + (size_t)r * a.K + c);
       const float4 u0 = *reinterpret_cast<const float4*>(x + c), u1 = *reinterpret_cast<const float4*>(x + c + 4);
       float v[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
       if (a.gain) {
@@ -170,22 +175,27 @@ __global__ void __launch_bounds__(128) lora_prep_kernel(LoraArgs a, int col_bloc
         v[0] *= g0.x; v[1] *= g0.y; v[2] *= g0.z; v[3] *= g0.w;
         v[4] *= g1.x; v[5] *= g1.y; v[6] *= g1.z; v[7] *= g1.w;
       }
-      const uint32_t b0[4] = {w0.x, w0.y, w0.z, w0.w}, b1[4] = {w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        s0 = fmaf(bf16lo(b0[i]), v[2 * i], fmaf(bf16hi(b0[i]), v[2 * i + 1], s0));
-        s1 = fmaf(bf16lo(b1[i]), v[2 * i], fmaf(bf16hi(b1[i]), v[2 * i + 1], s1));
+      for (int r = 0; r < 8; ++r) {
+        const uint32_t b[4] = {w[r].x, w[r].y, w[r].z, w[r].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[r] = fmaf(bf16lo(b[i]), v[2 * i], fmaf(bf16hi(b[i]), v[2 * i + 1], acc[r]));
       }
     }
-    s0 = warp_sum(s0);
-    s1 = warp_sum(s1);
-    const float sc = a.scale ? a.scale[sl.id[m]] : 1.f;
-    if (lane == 0) {
-      t[2 * warp] = s0 * sc;
-      t[2 * warp + 1] = s1 * sc;
+#pragma unroll
+    for (int r = 0; r < 8; ++r) acc[r] = warp_sum(acc[r]);
+    if (lane == 0)
+#pragma unroll
+      for (int r = 0; r < 8; ++r) sums[warp][r] = acc[r];
+    __syncthreads();
+    if (threadIdx.x < 8) {
+      float t = 0.f;
+      for (int w = 0; w < PREP_THR / 32; ++w) t += sums[w][threadIdx.x];
+      red[threadIdx.x] = t * (a.scale ? a.scale[id] : 1.f);
     }
   }
-  __syncthreads();
+  find_slots(sl, a.ids, a.M, a.n_adapters);
+  const int mine = sl.slot[m];
   // eight columns of every adapter in use: t in this row's, zero in the others;
   // the last block also clears the columns up to a whole k-step
   const int width = r0 + 8 >= a.rank && (a.rank & 15) ? 16 : 8;
@@ -196,7 +206,7 @@ __global__ void __launch_bounds__(128) lora_prep_kernel(LoraArgs a, int col_bloc
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         uint16_t o[3];
-        split3(t[j], o);
+        split3(red[j], o);
         q[j >> 1] |= (uint32_t)(p == 0 ? o[0] : p == 1 ? o[1] : o[2]) << (16 * (j & 1));
       }
     *reinterpret_cast<uint4*>(out + p * plane + a.K + s * rc * KC + r0 + part * 8) = make_uint4(q[0], q[1], q[2], q[3]);
@@ -278,7 +288,7 @@ struct GemmArgs {
   float eps;
   const float* rms;       // [M][RMS_PARTS]
   float* y;               // [M][N]
-  float* fix;             // [grid][2][MP][TM]
+  float* fix;             // [grid][2][tile rows / TM][MP][TM]
   unsigned int* cnt;      // [T]
   int* err;
 };
@@ -286,9 +296,14 @@ struct GemmArgs {
 // MMA N: the three planes of MP rows.
 constexpr int mma_n(int MP) { return (3 * MP + 15) / 16 * 16; }
 
-template <int MP>
+// NS: MMAs a k-step (128-row parts of a tile).
+template <int MP, int NS>
 struct Gemm {
   static constexpr int NB = mma_n(MP);
+  static constexpr int ACC_COLS = NB <= 128 ? 128 : 256;
+  static constexpr int SETS = NS * ACC_COLS <= TMEM_COLS / 2 ? 2 : 1;
+  static constexpr int ROWS_T = NS * TM;
+  static constexpr int W_BYTES = NS * SUB_BYTES;
   static constexpr int X_BYTES = NB * KC * 2;
   static constexpr int STAGE = W_BYTES + X_BYTES;
   const GemmArgs& a;
@@ -302,26 +317,41 @@ struct Gemm {
   uint32_t tmem;
   int CW, RC, E, U, u0, u1;   // chunks of a tile: CW of W, then RC of every adapter in use, E in all
 
-  // The (tile, chunk) pairs of the CTA, in the order they are streamed.
+  // The (tile, chunk) pairs of the CTA, in the order they are streamed. Counted
+  // up without a division: one thread issues a chunk every 700 cycles or so, and
+  // with divisions here and for the ring's slots (1200 cycles a chunk) the
+  // stream ran at half its rate.
   struct Items {
     const Gemm& k;
-    int u, t, c, extra;
-    SPEC_DEV explicit Items(const Gemm& k_) : k(k_), u(k_.u0), t(0), c(0), extra(-1) {}
+    int left, t, c;   // units of W left, the pair
+    SPEC_DEV explicit Items(const Gemm& k_) : k(k_), left(k_.u1 - k_.u0), t(k_.u0 / k_.CW), c(k_.u0 - t * k_.CW - 1) {}
     SPEC_DEV void next() {
-      if (extra >= 0) {
-        c = k.CW + extra;
-        if (++extra == k.E) extra = -1;
-        return;
+      if (c + 1 == k.CW + k.E) {   // the tile's last chunk, or its last adapter's
+        c = -1;
+        ++t;
       }
-      t = u / k.CW;
-      c = u - t * k.CW;
-      ++u;
-      if (c == k.CW - 1 && k.E > 0) extra = 0;
+      if (++c < k.CW) --left;
     }
     // the pair just returned is the CTA's last of its tile
-    SPEC_DEV bool ends() const { return extra < 0 && (c >= k.CW - 1 || u == k.u1); }
+    SPEC_DEV bool ends() const { return c == k.CW + k.E - 1 || (left == 0 && c < k.CW - 1); }
+    // and the last of a sum in tensor memory: the same chunks of W, and of a row's
+    // adapter, meet there whatever else the call holds
+    SPEC_DEV bool flushes() const {
+      return ends() || c == k.CW - 1 || ((c < k.CW ? c : c - k.CW) + 1) % FLUSH == 0;
+    }
   };
   SPEC_DEV int items() const { return u1 - u0 + E * (u1 / CW - u0 / CW); }
+  // A place in the ring, and the parity of its turn.
+  struct Slot {
+    int s = 0;
+    unsigned turn = 0;
+    SPEC_DEV void next(int stages) {
+      if (++s == stages) {
+        s = 0;
+        turn ^= 1;
+      }
+    }
+  };
 
   SPEC_DEV int unit_begin(int b) const { return (int)(((long long)b * U) / a.grid); }
   SPEC_DEV int cta_of(int u) const {
@@ -339,10 +369,10 @@ struct Gemm {
 
   SPEC_DEV void load_w(int s, const Items& it, uint64_t pol) const {
     if (it.c < CW) {
-      tma_load_once(stage(s), tmw, it.c * KC, it.t * TM, &full[s], pol);
+      tma_load_once(stage(s), tmw, it.c * KC, it.t * ROWS_T, &full[s], pol);
     } else {
       const int slot = (it.c - CW) / RC;
-      tma_load_once(stage(s), tmb, (it.c - CW - slot * RC) * KC, sl.used[slot] * a.N + it.t * TM, &full[s], pol);
+      tma_load_once(stage(s), tmb, (it.c - CW - slot * RC) * KC, sl.used[slot] * a.N + it.t * ROWS_T, &full[s], pol);
     }
   }
   SPEC_DEV void load_x(int s, const Items& it) const { tma_load(stage(s) + W_BYTES, tmx, it.c * KC, 0, &full[s]); }
@@ -362,13 +392,13 @@ struct Gemm {
       load_x(n, ix);
     }
     int issued = pre;
-    for (int n = pre; n < nu; ++n) {
-      const int s = n % a.stages;
-      if (!wait_phase(&empty[s], ((n / a.stages) - 1) & 1, abort_s, a.err)) break;
+    Slot at;
+    for (int n = pre; n < nu; ++n, at.next(a.stages)) {
+      if (!wait_phase(&empty[at.s], at.turn, abort_s, a.err)) break;
       iw.next();
-      mbar_expect_tx(&full[s], (unsigned)STAGE);
-      load_w(s, iw, pol);
-      load_x(s, iw);
+      mbar_expect_tx(&full[at.s], (unsigned)STAGE);
+      load_w(at.s, iw, pol);
+      load_x(at.s, iw);
       issued = n + 1;
     }
     if (*abort_s)  // this CTA's copies land before its shared memory is released
@@ -379,30 +409,40 @@ struct Gemm {
     constexpr uint32_t idesc = idesc_bf16(TM, NB);
     const int nu = items();
     Items it(*this);
-    int i = 0;             // segments (tiles) so far
-    bool first = true;     // first k-step of a segment
+    int i = 0, ks = 0;     // sums so far, k-steps of the current one
     uint32_t d = tmem;
-    for (int n = 0; n < nu; ++n) {
+    Slot at;
+    for (int n = 0; n < nu; ++n, at.next(a.stages)) {
       it.next();
-      if (first) {
-        if (i >= 2 && !wait_phase(&acce[i & 1], ((i >> 1) - 1) & 1, abort_s, a.err)) break;
+      if (ks == 0) {
+        const int set = i % SETS;
+        if (i >= SETS && !wait_phase(&acce[set], (i / SETS - 1) & 1, abort_s, a.err)) break;
         fence_after();
-        d = tmem + (uint32_t)((i & 1) * ACC_COLS);
+        d = tmem + (uint32_t)(set * NS * ACC_COLS);
       }
-      const int s = n % a.stages;
-      if (!wait_phase(&full[s], (n / a.stages) & 1, abort_s, a.err)) break;
+      if (!wait_phase(&full[at.s], at.turn, abort_s, a.err)) break;
       fence_after();
-      const uint32_t w = sa(stage(s)), x = w + (uint32_t)W_BYTES;
+      const uint32_t w = sa(stage(at.s)), x = w + (uint32_t)W_BYTES;
       const int ns = steps(it.c);
-      for (int ks = 0; ks < ns; ++ks) {
-        mma_bf16(d, sw128_desc(w + 32 * ks), sw128_desc(x + 32 * ks), idesc, first ? 0u : 1u);
-        first = false;
+      const uint64_t wd = sw128_desc(w), xd = sw128_desc(x);
+      auto step = [&](int j) {   // 32 bytes a k-step: 2 in the descriptors' units
+#pragma unroll
+        for (int h = 0; h < NS; ++h)
+          mma_bf16(d + (uint32_t)(h * ACC_COLS), wd + h * (SUB_BYTES >> 4) + 2 * j, xd + 2 * j, idesc,
+                   ks + j > 0 ? 1u : 0u);
+      };
+      if (ns == KC / 16) {
+#pragma unroll
+        for (int j = 0; j < KC / 16; ++j) step(j);
+      } else {
+        for (int j = 0; j < ns; ++j) step(j);
       }
-      mma_commit(&empty[s]);
-      if (it.ends()) {
-        mma_commit(&accf[i & 1]);
+      ks += ns;
+      mma_commit(&empty[at.s]);
+      if (it.flushes()) {
+        mma_commit(&accf[i % SETS]);
         ++i;
-        first = true;
+        ks = 0;
       }
     }
     // every MMA of this CTA is complete before its tensor memory is freed
@@ -410,23 +450,30 @@ struct Gemm {
     drain_phase(drain, 0);
   }
 
-  // thread = output row n of the tile, lane by lane: a warp's stores of an
-  // activation row are consecutive
-  SPEC_DEV void finish(int t, int r, const float (&v)[MP]) const {
-    const int n = t * TM + r;
-    if (n >= a.N) return;
+  // thread = output row n of the tile's parts, lane by lane: a warp's stores of
+  // an activation row are consecutive
+  SPEC_DEV void finish(int t, int r, const float (&v)[NS][MP]) const {
 #pragma unroll
-    for (int m = 0; m < MP; ++m)
-      if (m < a.M) a.y[(size_t)m * a.N + n] = v[m] * rms_s[m];
+    for (int h = 0; h < NS; ++h) {
+      const int n = t * ROWS_T + h * TM + r;
+      if (n >= a.N) break;
+#pragma unroll
+      for (int m = 0; m < MP; ++m)
+        if (m < a.M) a.y[(size_t)m * a.N + n] = v[h][m] * rms_s[m];
+    }
   }
 
+  SPEC_DEV float* slot(int b, int t) const {
+    return a.fix + (size_t)(b * 2 + (t == unit_begin(b) / CW ? 0 : 1)) * NS * MP * TM;
+  }
   // A tile shared with other CTAs: publish this CTA's sums; the last to arrive
-  // adds all of them in CTA order and finishes the tile.
-  SPEC_DEV void partial(int t, int i, int r, int e, float (&v)[MP]) const {
-    const int b = blockIdx.x;
-    float* f = a.fix + (size_t)(b * 2 + (t == u0 / CW ? 0 : 1)) * MP * TM;
+  // adds all of them in CTA order and finishes the tile. i: the CTA's tiles so far.
+  SPEC_DEV void partial(int t, int i, int r, int e, float (&v)[NS][MP]) const {
+    float* f = slot(blockIdx.x, t);
 #pragma unroll
-    for (int m = 0; m < MP; ++m) __stcg(f + m * TM + r, v[m]);
+    for (int h = 0; h < NS; ++h)
+#pragma unroll
+      for (int m = 0; m < MP; ++m) __stcg(f + (h * MP + m) * TM + r, v[h][m]);
     epi_sync();
     if (e == 0) bc[2 + (i & 1)] = (int)atomic_add_acq_rel(a.cnt + t, 1u);
     epi_sync();
@@ -434,14 +481,19 @@ struct Gemm {
     if (bc[2 + (i & 1)] != bl - bf) return;
     __threadfence();
 #pragma unroll
-    for (int m = 0; m < MP; ++m) v[m] = 0.f;
+    for (int h = 0; h < NS; ++h)
+#pragma unroll
+      for (int m = 0; m < MP; ++m) v[h][m] = 0.f;
     for (int bb = bf; bb <= bl; ++bb) {
-      const float* g = a.fix + (size_t)(bb * 2 + (t == unit_begin(bb) / CW ? 0 : 1)) * MP * TM;
-      float o[MP];
+      const float* g = slot(bb, t);
 #pragma unroll
-      for (int m = 0; m < MP; ++m) o[m] = __ldcg(g + m * TM + r);
+      for (int h = 0; h < NS; ++h) {
+        float o[MP];
 #pragma unroll
-      for (int m = 0; m < MP; ++m) v[m] += o[m];
+        for (int m = 0; m < MP; ++m) o[m] = __ldcg(g + (h * MP + m) * TM + r);
+#pragma unroll
+        for (int m = 0; m < MP; ++m) v[h][m] += o[m];
+      }
     }
     if (e == 0) a.cnt[t] = 0u;
     finish(t, r, v);
@@ -460,35 +512,53 @@ struct Gemm {
       rms_s[e] = f;
     }
     epi_sync();
-    int i = 0;
-    for (int u = u0; u < u1; ++i) {
-      const int t = u / CW, c0 = u - t * CW, ue = min(u1, (t + 1) * CW), c1 = ue - t * CW, acc = i & 1;
-      u = ue;
-      if (e == 0) bc[i & 1] = wait_phase(&accf[acc], (i >> 1) & 1, abort_s, a.err) ? 1 : 0;
+    const uint32_t lanes = tmem + ((uint32_t)(((threadIdx.x >> 5) & 3) * 32) << 16);
+    const int nu = items();
+    Items it(*this);
+    int i = 0, tile = 0, c0 = -1;
+    float v[NS][MP];
+    for (int n = 0; n < nu; ++n) {
+      it.next();
+      if (c0 < 0) {
+        c0 = it.c;
+#pragma unroll
+        for (int h = 0; h < NS; ++h)
+#pragma unroll
+          for (int m = 0; m < MP; ++m) v[h][m] = 0.f;
+      }
+      if (!it.flushes()) continue;
+      const int set = i % SETS;
+      if (e == 0) bc[i & 1] = wait_phase(&accf[set], (i / SETS) & 1, abort_s, a.err) ? 1 : 0;
       epi_sync();
       if (!bc[i & 1]) break;
       fence_after();
-      const uint32_t taddr = tmem + ((uint32_t)(((threadIdx.x >> 5) & 3) * 32) << 16) + (uint32_t)(acc * ACC_COLS);
-      float v[MP];
 #pragma unroll
-      for (int j = 0; j < MP / 8; ++j) {
-        uint32_t q[3][8];
+      for (int h = 0; h < NS; ++h) {
+        const uint32_t taddr = lanes + (uint32_t)((set * NS + h) * ACC_COLS);
 #pragma unroll
-        for (int p = 0; p < 3; ++p) tmem_ld8(taddr + p * MP + 8 * j, q[p]);
-        tmem_wait_ld();
+        for (int j = 0; j < MP / 8; ++j) {
+          uint32_t q[3][8];   // hi, mid, lo
 #pragma unroll
-        for (int h = 0; h < 8; ++h)   // small terms first
-          v[8 * j + h] = (__uint_as_float(q[2][h]) + __uint_as_float(q[1][h])) + __uint_as_float(q[0][h]);
+          for (int p = 0; p < 3; ++p) tmem_ld8(taddr + p * MP + 8 * j, q[p]);
+          tmem_wait_ld();
+#pragma unroll
+          for (int l = 0; l < 8; ++l)
+            v[h][8 * j + l] += __uint_as_float(q[0][l]) + (__uint_as_float(q[1][l]) + __uint_as_float(q[2][l]));
+        }
       }
       fence_before();
-      mbar_arrive(&acce[acc]);
-      if (c0 == 0 && c1 == CW) finish(t, r, v);
-      else partial(t, i, r, e, v);
+      mbar_arrive(&acce[set]);
+      ++i;
+      if (!it.ends()) continue;
+      if (c0 == 0 && it.c >= CW - 1) finish(it.t, r, v);
+      else partial(it.t, tile, r, e, v);
+      ++tile;
+      c0 = -1;
     }
   }
 };
 
-template <int MP>
+template <int MP, int NS>
 __global__ void __launch_bounds__(NTHR, 1)
     lora_gemm_kernel(const __grid_constant__ GemmArgs a, const __grid_constant__ CUtensorMap tmw,
                      const __grid_constant__ CUtensorMap tmb, const __grid_constant__ CUtensorMap tmx) {
@@ -499,7 +569,7 @@ __global__ void __launch_bounds__(NTHR, 1)
   __shared__ uint32_t tmem_slot;
   __shared__ int flags[5];
   const uint32_t mis = sa(smem_raw) & 1023u;
-  Gemm<MP> k{a, &tmw, &tmb, &tmx, sl, smem_raw + (mis ? 1024 - mis : 0)};
+  Gemm<MP, NS> k{a, &tmw, &tmb, &tmx, sl, smem_raw + (mis ? 1024 - mis : 0)};
   k.full = bars;
   k.empty = bars + MAX_STAGES;
   k.accf = bars + 2 * MAX_STAGES;
@@ -589,6 +659,11 @@ int rows_padded(int M) {
   return 64;
 }
 
+// Tiles of 256 rows where every SM has 16 of their chunks or more (80 MB of
+// weights), else of 128. 49152 x 6144, 40 rows, 8 adapters of rank 16: 111 us with
+// 256 (5.6 TB/s), 163 us with 128.
+int parts(int N, int K) { return (long long)N * K >= 16ll * num_sms() * 2 * TM * KC ? 2 : 1; }
+
 // Scratch of the fused path: sums of squares, counters, split-tile sums, planes.
 struct Scratch {
   size_t rms, cnt, fix, planes, bytes;
@@ -600,45 +675,51 @@ Scratch scratch(int N, int K, int M, int rank) {
   s.rms = 0;
   s.cnt = s.rms + up((size_t)ROWS * RMS_PARTS * sizeof(float));
   s.fix = s.cnt + up((size_t)((N + TM - 1) / TM) * sizeof(unsigned int));
-  s.planes = s.fix + up((size_t)num_sms() * 2 * MP * TM * sizeof(float));
+  s.planes = s.fix + up((size_t)num_sms() * 2 * 2 * MP * TM * sizeof(float));
   s.bytes = s.planes + up((size_t)mma_n(MP) * (K + (size_t)M * rc * KC) * 2);
   return s;
 }
 
-template <int MP>
+template <int MP, int NS>
 cudaError_t launch_gemm(GemmArgs& g, const CUtensorMap& tmw, const CUtensorMap& tmb, const CUtensorMap& tmx,
                         cudaStream_t st) {
-  g.stages = std::min(MAX_STAGES, (SMEM_LIMIT - 4096) / Gemm<MP>::STAGE);
+  g.stages = std::min(MAX_STAGES, (SMEM_LIMIT - 4096) / Gemm<MP, NS>::STAGE);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(g.grid);
   cfg.blockDim = dim3(NTHR);
-  cfg.dynamicSmemBytes = (size_t)g.stages * Gemm<MP>::STAGE + 1024;
+  cfg.dynamicSmemBytes = (size_t)g.stages * Gemm<MP, NS>::STAGE + 1024;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, lora_gemm_kernel<MP>, g, tmw, tmb, tmx);
+  return cudaLaunchKernelEx(&cfg, lora_gemm_kernel<MP, NS>, g, tmw, tmb, tmx);
+}
+
+template <int MP>
+void set_attributes() {
+  const int n = SMEM_LIMIT - 3072;
+  cudaFuncSetAttribute(lora_gemm_kernel<MP, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, n);
+  cudaFuncSetAttribute(lora_gemm_kernel<MP, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize, n);
 }
 
 }  // namespace
 
 void setup_lora_attributes() {
-  const int n = SMEM_LIMIT - 3072;
-  cudaFuncSetAttribute(lora_gemm_kernel<8>, cudaFuncAttributeMaxDynamicSharedMemorySize, n);
-  cudaFuncSetAttribute(lora_gemm_kernel<16>, cudaFuncAttributeMaxDynamicSharedMemorySize, n);
-  cudaFuncSetAttribute(lora_gemm_kernel<32>, cudaFuncAttributeMaxDynamicSharedMemorySize, n);
-  cudaFuncSetAttribute(lora_gemm_kernel<40>, cudaFuncAttributeMaxDynamicSharedMemorySize, n);
-  cudaFuncSetAttribute(lora_gemm_kernel<48>, cudaFuncAttributeMaxDynamicSharedMemorySize, n);
-  cudaFuncSetAttribute(lora_gemm_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, n);
+  set_attributes<8>();
+  set_attributes<16>();
+  set_attributes<32>();
+  set_attributes<40>();
+  set_attributes<48>();
+  set_attributes<64>();
 }
 
 size_t lora_gemm_bytes(int N, int K, int M, int rank) { return scratch(N, K, M, rank).bytes; }
 
 bool lora_gemm_ok(const LoraArgs& a, int w_dtype) {
   return w_dtype == DT_BF16 && a.dtype == DT_BF16 && a.K % KC == 0 && a.K <= PREP_COLS * RMS_PARTS &&
-         (long long)a.n_adapters * a.N + TM < (1ll << 31);
+         (long long)a.n_adapters * a.N + 2 * TM < (1ll << 31);
 }
 
 int lora_gemm(LoraArgs a, const void* w, void* ws, cudaStream_t st) {
@@ -649,7 +730,8 @@ int lora_gemm(LoraArgs a, const void* w, void* ws, cudaStream_t st) {
   uint16_t* planes = (uint16_t*)(base + s.planes);
   GemmArgs g = {};
   g.M = a.M; g.N = a.N; g.K = a.K; g.rank = a.rank; g.n_adapters = a.n_adapters;
-  g.T = (a.N + TM - 1) / TM;
+  const int ns = parts(a.N, a.K), rows_t = ns * TM;
+  g.T = (a.N + rows_t - 1) / rows_t;
   g.grid = (int)std::min<long long>((long long)g.T * (a.K / KC), num_sms());
   g.ids = a.ids; g.norm = a.gain != nullptr; g.eps = a.eps;
   g.rms = (const float*)(base + s.rms); g.y = a.y; g.fix = (float*)(base + s.fix);
@@ -657,20 +739,21 @@ int lora_gemm(LoraArgs a, const void* w, void* ws, cudaStream_t st) {
   a.cnt = g.cnt;
   a.n_cnt = g.T;
   CUtensorMap tmw, tmb, tmx;
-  if (!encode(&tmw, w, a.K, a.N, TM) || !encode(&tmb, a.b, a.rank, (long long)a.n_adapters * a.N, TM) ||
+  if (!encode(&tmw, w, a.K, a.N, rows_t) ||
+      !encode(&tmb, a.b, a.rank, (long long)a.n_adapters * a.N, rows_t) ||
       !encode(&tmx, planes, KT, mma_n(MP), mma_n(MP)))
     return -1;
   const int col_blocks = (a.K + PREP_COLS - 1) / PREP_COLS;
-  lora_prep_kernel<<<dim3(a.M, col_blocks + a.rank / 8), 128, 0, st>>>(a, col_blocks, MP, KT, planes, (float*)(base + s.rms));
+  lora_prep_kernel<<<dim3(a.M, col_blocks + a.rank / 8), PREP_THR, 0, st>>>(a, col_blocks, MP, KT, planes, (float*)(base + s.rms));
   if (cudaGetLastError() != cudaSuccess) return -1;
   cudaError_t e;
   switch (MP) {
-    case 8: e = launch_gemm<8>(g, tmw, tmb, tmx, st); break;
-    case 16: e = launch_gemm<16>(g, tmw, tmb, tmx, st); break;
-    case 32: e = launch_gemm<32>(g, tmw, tmb, tmx, st); break;
-    case 40: e = launch_gemm<40>(g, tmw, tmb, tmx, st); break;
-    case 48: e = launch_gemm<48>(g, tmw, tmb, tmx, st); break;
-    default: e = launch_gemm<64>(g, tmw, tmb, tmx, st); break;
+    case 8: e = ns == 2 ? launch_gemm<8, 2>(g, tmw, tmb, tmx, st) : launch_gemm<8, 1>(g, tmw, tmb, tmx, st); break;
+    case 16: e = ns == 2 ? launch_gemm<16, 2>(g, tmw, tmb, tmx, st) : launch_gemm<16, 1>(g, tmw, tmb, tmx, st); break;
+    case 32: e = ns == 2 ? launch_gemm<32, 2>(g, tmw, tmb, tmx, st) : launch_gemm<32, 1>(g, tmw, tmb, tmx, st); break;
+    case 40: e = ns == 2 ? launch_gemm<40, 2>(g, tmw, tmb, tmx, st) : launch_gemm<40, 1>(g, tmw, tmb, tmx, st); break;
+    case 48: e = ns == 2 ? launch_gemm<48, 2>(g, tmw, tmb, tmx, st) : launch_gemm<48, 1>(g, tmw, tmb, tmx, st); break;
+    default: e = ns == 2 ? launch_gemm<64, 2>(g, tmw, tmb, tmx, st) : launch_gemm<64, 1>(g, tmw, tmb, tmx, st); break;
   }
   return e == cudaSuccess ? 2 : -1;
 }

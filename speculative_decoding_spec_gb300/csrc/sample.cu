@@ -40,7 +40,7 @@
 #include <cooperative_groups.h>
 
 #include <algorithm>
-#include <mutex>
+#include <atomic>
 #include <utility>
 
 #include "common.cuh"
@@ -1216,15 +1216,12 @@ __global__ void __launch_bounds__(256) accept_sampled_kernel(AcceptSampledArgs a
     for (int i = b0; i < a.B * R; i += step) a.best[i] = 0ull;
 }
 
-// Clusters of C CTAs of the kernel that the current device holds at once.
+// Clusters of C CTAs of the kernel that device `dev`, the current one, holds at
+// once (asked once).
 template <typename T>
-int max_clusters(int C) {
-  static std::mutex mu;
-  static int cache[MAX_DEVICES][MAX_C + 1];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= MAX_DEVICES) return 0;
-  std::lock_guard<std::mutex> lk(mu);
-  int& n = cache[dev][C];
+int max_clusters(int dev, int C) {
+  static std::atomic<int> cache[MAX_DEVICES][MAX_C + 1];
+  int n = cache[dev][C].load(std::memory_order_relaxed);
   if (n == 0) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(C);
@@ -1241,6 +1238,7 @@ int max_clusters(int C) {
       cudaGetLastError();
       n = -1;  // not on this device
     }
+    cache[dev][C].store(n, std::memory_order_relaxed);
   }
   return n;
 }
@@ -1255,16 +1253,18 @@ int max_clusters(int C) {
 // 64 rows with top-p 128 us with 8, 143 with 6, 164 with 4.
 template <typename T>
 int cluster_size(int M, int V, bool filters) {
-  int best = MAX_C;
+  int best = MAX_C, dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= MAX_DEVICES) dev = 0;
+  const int sms = num_sms();
   double least = 1e30;
   for (int C : {1, 2, 3, 4, 5, 6, 7, 8, 12, 16}) {
     if (V / C > DIGIT_TOKENS || (filters && C < std::min(8, V / 4096))) continue;
-    const int fit = max_clusters<T>(C);
+    const int fit = max_clusters<T>(dev, C);
     if (fit < 1) continue;
     double us = 0;
     for (int left = M; left > 0; left -= fit) {
       const int rows = std::min(left, fit);
-      const int share = (rows * C + num_sms() - 1) / num_sms();
+      const int share = (rows * C + sms - 1) / sms;
       const double wave = 8.0 + 0.1 * C + 0.17e-3 * share * V / C;
       if (left > 8 * fit) {  // many waves: all but the last few at once
         const int n = left / fit - 4;

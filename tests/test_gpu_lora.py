@@ -88,7 +88,7 @@ def test_adapter_part_alone(adt, M, N, K, r, norm):
 
 
 @pytest.mark.parametrize("dtype", [configs.BF16, configs.Q4_0, configs.F32])
-@pytest.mark.parametrize("N,M", [(1024, 8), (1024, 40), (1023, 5), (20000, 12)])
+@pytest.mark.parametrize("N,M", [(1024, 8), (1024, 40), (1023, 5), (80001, 12)])
 def test_rows_without_an_adapter(dtype, N, M):
     """Bit for bit those of a call without adapters, whatever the other rows
     bring; unused adapters are not read into any row."""
@@ -107,7 +107,8 @@ def test_rows_without_an_adapter(dtype, N, M):
     assert torch.equal(y[ids < 0], none[ids < 0]) and torch.isfinite(y).all()
 
 
-@pytest.mark.parametrize("M,N,K", [(1, 4096, 1536), (12, 2560, 6144), (40, 3000, 2560), (64, 130, 24576)])
+@pytest.mark.parametrize("M,N,K", [(1, 4096, 1536), (12, 2560, 6144), (40, 3000, 2560), (64, 130, 24576),
+                                   (3, 26001, 2048), (37, 8201, 6144), (64, 7000, 6144)])
 def test_bf16_is_a_binary32_projection(M, N, K):
     """bf16 weights and adapters: activations in three 16-bit planes (2^-25), exact
     products, binary32 sums. A sum of n products of random sign is off by about
