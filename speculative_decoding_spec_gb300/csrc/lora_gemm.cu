@@ -115,8 +115,8 @@ SPEC_DEV void split3(float v, uint16_t (&o)[3]) {
 // row m's shrink, all warps together along K, and write its planes' adapter
 // columns. Rows that share an adapter read it from L2.
 constexpr int PREP_THR = 256;
-__global__ void __launch_bounds__(PREP_THR) lora_prep_kernel(LoraArgs a, int col_blocks, int MP, int KT, uint16_t* planes,
-                                                             float* rms) {
+__global__ void __launch_bounds__(PREP_THR) lora_prep_kernel(LoraArgs a, int col_blocks, int MP, int Kp, int KT,
+                                                             uint16_t* planes, float* rms) {
   __shared__ Slots sl;
   __shared__ float red[32];
   __shared__ float sums[PREP_THR / 32][8];
@@ -135,10 +135,10 @@ __global__ void __launch_bounds__(PREP_THR) lora_prep_kernel(LoraArgs a, int col
     }
     float ss = 0.f;
     const int c = y * PREP_COLS + threadIdx.x * 4;
-    if (c < a.K) {
-      const float4 u = *reinterpret_cast<const float4*>(x + c);
+    if (c < Kp) {   // (the columns up to a whole chunk are zero, as the weights' read)
+      const float4 u = c < a.K ? *reinterpret_cast<const float4*>(x + c) : make_float4(0.f, 0.f, 0.f, 0.f);
       float v[4] = {u.x, u.y, u.z, u.w};
-      if (a.gain) {
+      if (a.gain && c < a.K) {
         const float4 g = *reinterpret_cast<const float4*>(a.gain + c);
         ss = fmaf(v[0], v[0], fmaf(v[1], v[1], fmaf(v[2], v[2], v[3] * v[3])));
         v[0] *= g.x; v[1] *= g.y; v[2] *= g.z; v[3] *= g.w;
@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(PREP_THR) lora_prep_kernel(LoraArgs a, int col
         split3(red[j], o);
         q[j >> 1] |= (uint32_t)(p == 0 ? o[0] : p == 1 ? o[1] : o[2]) << (16 * (j & 1));
       }
-    *reinterpret_cast<uint4*>(out + p * plane + a.K + s * rc * KC + r0 + part * 8) = make_uint4(q[0], q[1], q[2], q[3]);
+    *reinterpret_cast<uint4*>(out + p * plane + Kp + s * rc * KC + r0 + part * 8) = make_uint4(q[0], q[1], q[2], q[3]);
   }
 }
 
@@ -604,7 +604,7 @@ __global__ void __launch_bounds__(NTHR, 1)
   __syncthreads();
   fence_after();
   k.tmem = tmem_slot;
-  k.CW = a.K / KC;
+  k.CW = (a.K + KC - 1) / KC;
   k.RC = (a.rank + KC - 1) / KC;
   k.E = sl.n * k.RC;
   k.U = a.T * k.CW;
@@ -676,7 +676,7 @@ Scratch scratch(int N, int K, int M, int rank) {
   s.cnt = s.rms + up((size_t)ROWS * RMS_PARTS * sizeof(float));
   s.fix = s.cnt + up((size_t)((N + TM - 1) / TM) * sizeof(unsigned int));
   s.planes = s.fix + up((size_t)num_sms() * 2 * 2 * MP * TM * sizeof(float));
-  s.bytes = s.planes + up((size_t)mma_n(MP) * (K + (size_t)M * rc * KC) * 2);
+  s.bytes = s.planes + up((size_t)mma_n(MP) * ((K + KC - 1) / KC * KC + (size_t)M * rc * KC) * 2);
   return s;
 }
 
@@ -718,13 +718,14 @@ void setup_lora_attributes() {
 size_t lora_gemm_bytes(int N, int K, int M, int rank) { return scratch(N, K, M, rank).bytes; }
 
 bool lora_gemm_ok(const LoraArgs& a, int w_dtype) {
-  return w_dtype == DT_BF16 && a.dtype == DT_BF16 && a.K % KC == 0 && a.K <= PREP_COLS * RMS_PARTS &&
+  return w_dtype == DT_BF16 && a.dtype == DT_BF16 && a.K % 8 == 0 && a.K <= PREP_COLS * RMS_PARTS &&
          (long long)a.n_adapters * a.N + 2 * TM < (1ll << 31);
 }
 
 int lora_gemm(LoraArgs a, const void* w, void* ws, cudaStream_t st) {
   std::call_once(g_once, init_encode);
-  const int MP = rows_padded(a.M), rc = (a.rank + KC - 1) / KC, KT = a.K + std::min(a.M, a.n_adapters) * rc * KC;
+  const int MP = rows_padded(a.M), rc = (a.rank + KC - 1) / KC, Kp = (a.K + KC - 1) / KC * KC;
+  const int KT = Kp + std::min(a.M, a.n_adapters) * rc * KC;
   const Scratch s = scratch(a.N, a.K, a.M, a.rank);
   char* base = (char*)ws;
   uint16_t* planes = (uint16_t*)(base + s.planes);
@@ -732,7 +733,7 @@ int lora_gemm(LoraArgs a, const void* w, void* ws, cudaStream_t st) {
   g.M = a.M; g.N = a.N; g.K = a.K; g.rank = a.rank; g.n_adapters = a.n_adapters;
   const int ns = parts(a.N, a.K), rows_t = ns * TM;
   g.T = (a.N + rows_t - 1) / rows_t;
-  g.grid = (int)std::min<long long>((long long)g.T * (a.K / KC), num_sms());
+  g.grid = (int)std::min<long long>((long long)g.T * (Kp / KC), num_sms());
   g.ids = a.ids; g.norm = a.gain != nullptr; g.eps = a.eps;
   g.rms = (const float*)(base + s.rms); g.y = a.y; g.fix = (float*)(base + s.fix);
   g.cnt = (unsigned int*)(base + s.cnt); g.err = a.err;
@@ -744,7 +745,7 @@ int lora_gemm(LoraArgs a, const void* w, void* ws, cudaStream_t st) {
       !encode(&tmx, planes, KT, mma_n(MP), mma_n(MP)))
     return -1;
   const int col_blocks = (a.K + PREP_COLS - 1) / PREP_COLS;
-  lora_prep_kernel<<<dim3(a.M, col_blocks + a.rank / 8), PREP_THR, 0, st>>>(a, col_blocks, MP, KT, planes, (float*)(base + s.rms));
+  lora_prep_kernel<<<dim3(a.M, col_blocks + a.rank / 8), PREP_THR, 0, st>>>(a, col_blocks, MP, Kp, KT, planes, (float*)(base + s.rms));
   if (cudaGetLastError() != cudaSuccess) return -1;
   cudaError_t e;
   switch (MP) {

@@ -1012,6 +1012,7 @@ spec_status spec_linear_lora(const spec_matrix* w, int32_t N, int32_t K, const f
   a.cnt = g.tc_cnt; a.n_cnt = (int)linear_counters(N);
   a.add = N % 4 != 0;
   g.epi = a.add ? EPI_STORE : EPI_ADD;
+  g.pdl = a.add ? 0 : 1;
   if (lora_shrink(a, st) < 0) return SPEC_ECUDA;
   if (!a.add && lora_expand(a, st) < 0) return SPEC_ECUDA;
   if (gemv(g, st) < 0) return SPEC_ECUDA;
