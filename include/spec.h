@@ -179,9 +179,10 @@ typedef struct {
  *               token).
  * Values outside these ranges (NaN included) leave top_k, top_p and min_p off.
  * Weights are held in 44 fraction bits of the largest (smaller ones count as
- * zero) and their sums are exact, so a row's token depends on nothing but the
- * row. -inf logits are never chosen; +inf logits share the whole mass equally;
- * a row with a NaN, or with nothing above -inf, has no distribution. */
+ * zero), to a relative 2^-36, and summed exactly: a result does not depend on
+ * timing, and is the 64-bit one unless u or a filter falls that near to a
+ * border. -inf logits are never chosen; +inf logits share the whole mass
+ * equally; a row with a NaN, or with nothing above -inf, has no distribution. */
 typedef struct {
     const float *temperature;
     const int32_t *top_k;
@@ -407,9 +408,14 @@ spec_status spec_attention(const spec_model_desc *m, const spec_kv_desc *kv, int
  * with its own settings. tokens ("device" int32 [M]) gets the token, -1 for a
  * row without a distribution; probs ("device" float [M], may be NULL) the
  * probability it had (its weight over the kept mass), 0 for such a row.
- * Needs no workspace. V <= 2^19, M <= 2^20. */
+ * workspace ("device", 16-byte aligned, ws_bytes >=
+ * spec_sample_workspace_bytes(M, V), no initialisation; may be NULL where that
+ * is 0) is written and read by the call; calls sharing one must not overlap.
+ * V <= 2^19, M <= 2^20. */
+size_t spec_sample_workspace_bytes(int32_t M, int32_t V);
 spec_status spec_sample(int32_t dtype, const void *logits, int64_t ld, int32_t M, int32_t V,
-                        const spec_sampling *s, int32_t *tokens, float *probs, void *stream);
+                        const spec_sampling *s, int32_t *tokens, float *probs, void *workspace,
+                        size_t ws_bytes, void *stream);
 
 /* Sampled accept of drafts from the logits of a verify pass ("device", B*(k+1)
  * rows: row j of sequence b, at b*(k+1) + j, scores the token after j drafts).
@@ -424,11 +430,12 @@ spec_status spec_sample(int32_t dtype, const void *logits, int64_t ld, int32_t M
  * ("device" int32 [B][k+1]) gets the emitted tokens, then -1; n_emitted
  * ("device" int32 [B]) their number, at least 1 unless the first row has no
  * distribution (such a row ends the emission before it); probs ("device" float
- * [B][k+1], may be NULL) their probabilities, 0 behind them.
- * k in [0, 1023], B * (k+1) <= 2^20. */
+ * [B][k+1], may be NULL) their probabilities, 0 behind them. workspace as for
+ * spec_sample with M = B * (k+1). k in [0, 1023], B * (k+1) <= 2^20. */
 spec_status spec_accept_sampled(int32_t dtype, const void *logits, int64_t ld, int32_t B, int32_t k,
                                 int32_t V, const int32_t *drafts, const spec_sampling *s,
-                                int32_t *out_tokens, int32_t *n_emitted, float *probs, void *stream);
+                                int32_t *out_tokens, int32_t *n_emitted, float *probs,
+                                void *workspace, size_t ws_bytes, void *stream);
 
 /* Copy one slot's counters to the host (synchronises `stream`). */
 spec_status spec_stats(spec_ctx *ctx, int32_t slot, spec_stats_t *out, void *stream);

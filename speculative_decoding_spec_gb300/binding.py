@@ -24,7 +24,7 @@ EXPORTS = ["spec_workspace_bytes", "spec_init", "spec_prefill", "spec_draft", "s
            "spec_kernel_launches", "spec_status_str", "spec_destroy", "spec_linear",
            "spec_linear_workspace_bytes", "spec_linear_noalloc", "spec_set_option",
            "spec_attention_workspace_bytes", "spec_attention", "spec_verify_topm", "spec_verify_tree",
-           "spec_verify_sampled", "spec_sample", "spec_accept_sampled",
+           "spec_verify_sampled", "spec_sample", "spec_sample_workspace_bytes", "spec_accept_sampled",
            "spec_linear_lora", "spec_linear_lora_workspace_bytes"]
 SPEC_OPT_GRAPHS, SPEC_OPT_PREFETCH, SPEC_OPT_TEST_ATTN_WAIT = 1, 4, 8
 SPEC_OPT_WIDE_TRACE = 7
@@ -144,9 +144,11 @@ def lib():
     L.spec_verify_sampled.restype = st
     L.spec_verify_sampled.argtypes = [p, i32, p, i32, p, C.POINTER(spec_sampling), p, p, p, p, p]
     L.spec_sample.restype = st
-    L.spec_sample.argtypes = [i32, p, C.c_int64, i32, i32, C.POINTER(spec_sampling), p, p, p]
+    L.spec_sample.argtypes = [i32, p, C.c_int64, i32, i32, C.POINTER(spec_sampling), p, p, p, C.c_size_t, p]
+    L.spec_sample_workspace_bytes.restype = C.c_size_t
+    L.spec_sample_workspace_bytes.argtypes = [i32, i32]
     L.spec_accept_sampled.restype = st
-    L.spec_accept_sampled.argtypes = [i32, p, C.c_int64, i32, i32, i32, p, C.POINTER(spec_sampling), p, p, p, p]
+    L.spec_accept_sampled.argtypes = [i32, p, C.c_int64, i32, i32, i32, p, C.POINTER(spec_sampling), p, p, p, p, C.c_size_t, p]
     L.spec_linear_lora_workspace_bytes.restype = C.c_size_t
     L.spec_linear_lora_workspace_bytes.argtypes = [i32, i32, i32, i32]
     L.spec_linear_lora.restype = st
@@ -317,6 +319,12 @@ class _on:
             self.ctx.__exit__(*e)
 
 
+def _sample_ws(L, logits, M, V):
+    """Scratch of a sampling call on its stream, where it needs any."""
+    n = L.spec_sample_workspace_bytes(M, V)
+    return (logits.new_empty(n, dtype=torch.uint8), n) if n else (None, 0)
+
+
 def spec_sample(logits: torch.Tensor, uniform: torch.Tensor, temperature: Optional[torch.Tensor] = None,
                 top_k: Optional[torch.Tensor] = None, top_p: Optional[torch.Tensor] = None,
                 min_p: Optional[torch.Tensor] = None, stream=None):
@@ -325,12 +333,15 @@ def spec_sample(logits: torch.Tensor, uniform: torch.Tensor, temperature: Option
     include/spec.h spec_sampling). Returns (tokens int32 [M], probs float32 [M]);
     a row without a distribution gives token -1 and probability 0."""
     fn = "spec_sample"
+    L = lib()
     M, V, dt, ld, dev = _logits(fn, logits)
     s = _sampling(fn, dev, M, temperature, top_k, top_p, min_p, uniform)
     with _on(dev, stream) as st:
         tokens = torch.empty_like(uniform, dtype=torch.int32)
         probs = torch.empty_like(uniform)
-        rc = lib().spec_sample(dt, logits.data_ptr(), ld, M, V, C.byref(s), tokens.data_ptr(), probs.data_ptr(), st)
+        ws, n = _sample_ws(L, logits, M, V)
+        rc = L.spec_sample(dt, logits.data_ptr(), ld, M, V, C.byref(s), tokens.data_ptr(), probs.data_ptr(), _ptr(ws),
+                           n, st)
     check(fn, rc)
     return tokens, probs
 
@@ -342,6 +353,7 @@ def spec_accept_sampled(logits: torch.Tensor, drafts: torch.Tensor, uniform: tor
     verify pass; the settings have a row for each row of logits. Returns
     (out_tokens int32 [B][k+1], n_emitted int32 [B], probs float32 [B][k+1])."""
     fn = "spec_accept_sampled"
+    L = lib()
     M, V, dt, ld, dev = _logits(fn, logits)
     _need(fn, drafts.dim() == 2 and drafts.dtype is torch.int32 and drafts.is_contiguous() and
           drafts.get_device() == dev, "drafts must be a contiguous int32 tensor [B][k] beside the logits")
@@ -352,8 +364,9 @@ def spec_accept_sampled(logits: torch.Tensor, drafts: torch.Tensor, uniform: tor
         out = drafts.new_empty((B, k + 1))
         ne = drafts.new_empty(B)
         probs = uniform.new_empty((B, k + 1))
-        rc = lib().spec_accept_sampled(dt, logits.data_ptr(), ld, B, k, V, drafts.data_ptr() if k else None, C.byref(s),
-                                       out.data_ptr(), ne.data_ptr(), probs.data_ptr(), st)
+        ws, n = _sample_ws(L, logits, M, V)
+        rc = L.spec_accept_sampled(dt, logits.data_ptr(), ld, B, k, V, drafts.data_ptr() if k else None, C.byref(s),
+                                   out.data_ptr(), ne.data_ptr(), probs.data_ptr(), _ptr(ws), n, st)
     check(fn, rc)
     return out, ne, probs
 

@@ -226,8 +226,10 @@ struct SampleArgs {
   const float* uniform;        // [M]
   int32_t* tokens;             // [M]
   float* probs;                // [M] or null
+  void* workspace;             // sample_workspace_bytes(M, V)
 };
 void setup_sample_attributes();
+size_t sample_workspace_bytes(int M, int V);  // 0 where none is needed
 int sample_rows(const SampleArgs& a, int pdl, cudaStream_t st);
 
 // Sampled accept: out_tokens holds every row's sample on entry, the emitted

@@ -18,13 +18,19 @@
 // Weights are integers: w_i in units of 2^-44 of the largest, rounded (a
 // choice: tokens below 2^-45 of the most likely one count as zero). Their sums
 // are exact, so the cut and the token do not depend on the order of the
-// additions, the number of CTAs or the other rows of the batch. The weight
+// additions or the number of CTAs. The weight
 // itself is evaluated to about 2^-37 (the exponent as a float pair, a table of
 // 4096 powers), because a token is decided by a sum of up to V weights next to
 // a border: at the 2^-24 of plain floats about one token in 10^4 would differ
 // from the 64-bit definition.
 //
-// A thread-block cluster takes a row; its CTAs push what the others need into
+// Large calls without filters: a first kernel takes the rows in chunks of 4096
+// tokens, one pass that leaves each chunk's maximum and the sum of its weights,
+// relative to that maximum; it loads the SMs evenly, with the next chunk's loads
+// in flight under the exponentials of the last. A CTA a row then adds the sums
+// up in the row's units, finds the drawn chunk and draws inside it.
+//
+// Otherwise a thread-block cluster takes a row; its CTAs push what the others need into
 // their shared memory, so that a phase costs one cluster barrier. Scan 1 finds
 // the maximum and the maxima of the row's segments (up to 1024).
 // Without top-k and top-p, scan 2 sums the weights and the warp that holds the
@@ -66,6 +72,9 @@ constexpr int MAX_C = 16;           // CTAs on one row (a thread-block cluster)
 constexpr int LIST = 1024;          // tokens a CTA lists
 constexpr int FEW = 2048;           // tokens the first CTA sorts
 constexpr int COUNTED = NT / 2;     // at most so many are counted instead
+constexpr int CHUNK_TOKENS = 4096;  // tokens of a chunk of the chunk kernel
+constexpr int CNT = 256;            // its threads
+constexpr int CNW = CNT / 32;
 constexpr int SEG_MAX = 1024;       // segments of a row (the elements of 1, 2, 4 or 8 lanes)
 constexpr int SEG_BINS = NT;        // bins of the segment maxima
 constexpr float Z_END = 46.f;       // weights are zero beyond this exponent
@@ -173,6 +182,33 @@ SPEC_DEV ull weight(const Scale& r, const ull* tab, float x, float* val = nullpt
   const ull v = T + (long long)__float2int_rn(fmaf(Tf, q, half_unit(n)));
   if (val) *val = fmaf(Tf, q, Tf) * __int_as_float((127 - WBITS - n) << 23);
   return v >> n;
+}
+
+// The factor of logit x's weight as v * 2^-(WBITS + n), not yet cut to units.
+SPEC_DEV ull weight_parts(const Scale& r, const ull* tab, float x, int& n) {
+  n = 0;
+  if (r.m == INFINITY) return x == INFINITY ? 1ull << WBITS : 0ull;
+  const float d = __fsub_rn(r.m, x);
+  const float bb = __fsub_rn(d, r.m);
+  const float e = __fadd_rn(__fsub_rn(r.m, __fsub_rn(d, bb)), __fsub_rn(-x, bb));
+  float p = __fmul_rn(d, r.sh);
+  const float pe = fmaf(e, r.sh, fmaf(d, r.sl, fmaf(d, r.sh, -p)));
+  if (!(p < 63.f)) return 0ull;
+  const float t = __fadd_rn(p, 12582912.f / TAB);
+  const float g = __fadd_rn(__fsub_rn(p, __fsub_rn(t, 12582912.f / TAB)), pe);
+  const float q = __fmul_rn(fmaf(g, 0.240226507f, -0.693147181f), g);
+  const uint32_t j = __float_as_uint(t);
+  const ull T = tab[j & (TAB - 1)];
+  n = (j >> TAB_LOG) & 63;
+  const float Tf = __uint_as_float((uint32_t)(T >> (WBITS - 24)) + 0x4a800000u) * (float)(1 << (WBITS - 24));
+  return T + (long long)__float2int_rn(__fmul_rn(Tf, q));
+}
+// A sum of weights relative to a chunk's maximum, in the row's units: times
+// v * 2^-(WBITS + n), rounded down. Monotone in the sum.
+SPEC_DEV ull in_row(ull sum, ull v, int n) {
+  const ull lo = sum * v, hi = __umul64hi(sum, v);
+  const int sh = WBITS + n;
+  return sh < 64 ? (hi << (64 - sh)) | (lo >> sh) : hi >> (sh - 64);
 }
 
 // Two floats in one register pair, and Blackwell's packed operations on them.
@@ -830,7 +866,7 @@ struct Sampler {
   // Lists the tokens of exponents [lo, hi) in bin units.
   SPEC_DEV void list(int i, float x, float lo, float hi) {
     const float v = sc.m == INFINITY ? (x == INFINITY ? 0.f : INFINITY) : sc.place(x);
-    if (v < hi && v >= lo) {
+    if (v < hi && v >= lo && *(volatile int*)&s.listed <= LIST) {   // (full: no more of them)
       const int at = atomicAdd(&s.listed, 1);
       if (at < LIST) {
         s.list_key[at] = rank_key(x);
@@ -1001,6 +1037,247 @@ struct Sampler {
   }
 };
 
+// What the chunk kernel leaves of a chunk.
+struct __align__(16) Record {
+  ull sum;         // weights relative to the chunk's maximum
+  ull best;        // packed maximum, 0: nothing above -inf
+  int nan;
+};
+
+// log2(e) / T as a float pair.
+SPEC_DEV void scale_of(float temp, float& sh, float& sl) {
+  constexpr float L = 1.44269502f;                                   // log2(e) rounded
+  constexpr float L_LO = (float)(1.4426950408889634 - (double)L);
+  sh = L / temp;
+  sl = (fmaf(-sh, temp, L) + L_LO) / temp;
+}
+
+// A vector of a row, -inf where the row does not fill it.
+template <typename T>
+SPEC_DEV uint4 row_vector(const T* p, int V, int mis, int v) {
+  constexpr int E = 16 / sizeof(T);
+  const int i0 = v * E - mis;
+  if (i0 >= 0 && i0 + E <= V) return *reinterpret_cast<const uint4*>(p + i0);
+  uint32_t w[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) w[j] = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;
+#pragma unroll
+  for (int i = 0; i < E; ++i)
+    if (i0 + i >= 0 && i0 + i < V) {
+      if (sizeof(T) == 4) {
+        w[i & 3] = *reinterpret_cast<const uint32_t*>(p + i0 + i);
+      } else {
+        const int sft = 16 * (i & 1);
+        w[(i >> 1) & 3] = (w[(i >> 1) & 3] & (0xffff0000u >> sft)) |
+                          ((uint32_t)*reinterpret_cast<const uint16_t*>(p + i0 + i) << sft);
+      }
+    }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Chunks per row: enough for any alignment of its first token.
+__host__ __device__ inline int row_chunks(int V) { return (V + 7 + CHUNK_TOKENS - 1) / CHUNK_TOKENS; }
+
+template <typename T>
+__global__ void __launch_bounds__(CNT, 4) chunk_kernel(SampleArgs a, Record* records) {
+  constexpr int E = 16 / sizeof(T), PER = CHUNK_TOKENS / E, NV = PER / CNT;
+  extern __shared__ __align__(16) unsigned char smem_raw[];
+  ull* tab = reinterpret_cast<ull*>(smem_raw);
+  __shared__ ull s_best[2][CNW], s_sum[2][CNW];
+  for (int i = threadIdx.x; i < TAB / 2; i += CNT) {
+    const unsigned int dst = (unsigned int)__cvta_generic_to_shared(tab + 2 * i);
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(g_table.v + 2 * i) : "memory");
+  }
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int n = row_chunks(a.V), items = a.M * n;
+  grid_dep_wait();
+  uint4 q[NV], next[NV];
+  float temp = 0.f, temp_next = 0.f;
+  auto load = [&](int item, uint4 (&v)[NV], float& t) {
+    if (item >= items) return;
+    const int row = item / n, c = item - row * n;
+    const T* p = (const T*)a.logits + (size_t)row * a.ld;
+    const int mis = (int)(((uintptr_t)p & 15) / sizeof(T));
+    const int i0 = c * CHUNK_TOKENS - mis;
+    if (i0 >= 0 && i0 + CHUNK_TOKENS <= a.V) {   // for the whole CTA: plain loads, nothing to merge
+#pragma unroll
+      for (int j = 0; j < NV; ++j) v[j] = reinterpret_cast<const uint4*>(p + i0)[j * CNT + threadIdx.x];
+    } else {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) v[j] = row_vector(p, a.V, mis, c * PER + j * CNT + threadIdx.x);
+    }
+    t = a.temperature ? a.temperature[row] : 1.f;
+  };
+  load(blockIdx.x, q, temp);
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncthreads();
+  int turn = 0;
+  for (int item = blockIdx.x; item < items; item += gridDim.x, turn ^= 1) {
+    load(item + gridDim.x, next, temp_next);
+    const int row = item / n, c = item - row * n;
+    const int mis = (int)(((uintptr_t)((const T*)a.logits + (size_t)row * a.ld) & 15) / sizeof(T));
+    float bx = -INFINITY;
+    int bi = -1, nan = 0;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        const float x = Part<T>::get(q[j], i);
+        nan |= x != x;
+        if (x > bx) {
+          bx = x;
+          bi = (c * PER + j * CNT + threadIdx.x) * E - mis + i;
+        }
+      }
+    ull best = bi >= 0 ? pack_best(bx + 0.f, (uint32_t)bi) : 0ull;
+    const uint32_t key = __reduce_max_sync(FULL, (uint32_t)(best >> 32));
+    const uint32_t idx = __reduce_max_sync(FULL, (uint32_t)(best >> 32) == key ? (uint32_t)best : 0u);
+    best = ((ull)key << 32) | idx;
+    if (lane == 0) s_best[turn][warp] = best;
+    nan = __syncthreads_or(nan);
+#pragma unroll
+    for (int w = 0; w < CNW; ++w) best = s_best[turn][w] > best ? s_best[turn][w] : best;
+    ull sum = 0;
+    if (best && !nan && temp >= 1e-5f && temp < INFINITY) {
+      Scale sc{best_value(best), 0.f, 0.f, 0.f};
+      scale_of(temp, sc.sh, sc.sl);
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int i = 0; i < E; i += 2) {
+          ull w0, w1;
+          weight2(sc, tab, Part<T>::get(q[j], i), Part<T>::get(q[j], i + 1), w0, w1);
+          sum += w0 + w1;
+        }
+      sum = warp_sum_u64(sum);
+    }
+    if (lane == 0) s_sum[turn][warp] = sum;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      sum = 0;
+#pragma unroll
+      for (int w = 0; w < CNW; ++w) sum += s_sum[turn][w];
+      Record& r = records[item];
+      r.sum = sum;
+      r.best = best;
+      r.nan = nan;
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j) q[j] = next[j];
+    temp = temp_next;
+  }
+}
+
+// A row of a call without filters, from its chunks' records: their sums in the
+// row's units, the chunk in which the drawn mass lies, and the token in it.
+template <typename T>
+__global__ void __launch_bounds__(NT) draw_kernel(SampleArgs a, const Record* records) {
+  extern __shared__ __align__(16) unsigned char smem_raw[];
+  ull* tab = reinterpret_cast<ull*>(smem_raw);
+  __shared__ ull wsum[NW], before, factor, total;
+  __shared__ int chunk, shift;
+  for (int i = threadIdx.x; i < TAB / 2; i += NT) {
+    const unsigned int dst = (unsigned int)__cvta_generic_to_shared(tab + 2 * i);
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(g_table.v + 2 * i) : "memory");
+  }
+  const int row = blockIdx.x, chunks = row_chunks(a.V), lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  grid_dep_wait();
+  const Record* rec = records + (size_t)row * chunks;
+  const float temp = a.temperature ? a.temperature[row] : 1.f, u = a.uniform[row];
+  auto scan = [&](ull v) {   // exclusive, in thread order
+    const ull inc = warp_scan_u64(v);
+    __syncthreads();
+    if (lane == 31) wsum[warp] = inc;
+    __syncthreads();
+    ull b = inc - v;
+#pragma unroll
+    for (int i = 0; i < NW; ++i)
+      if (i < warp) b += wsum[i];
+    return b;
+  };
+  ull best = 0, mine = 0;
+  int nan = 0;
+  if (threadIdx.x < chunks) {
+    mine = __ldcg(&rec[threadIdx.x].best);
+    nan = __ldcg(&rec[threadIdx.x].nan);
+  }
+  {
+    const uint32_t key = __reduce_max_sync(FULL, (uint32_t)(mine >> 32));
+    const uint32_t idx = __reduce_max_sync(FULL, (uint32_t)(mine >> 32) == key ? (uint32_t)mine : 0u);
+    if (lane == 0) wsum[warp] = ((ull)key << 32) | idx;
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  nan = __syncthreads_or(nan);
+#pragma unroll
+  for (int i = 0; i < NW; ++i) best = wsum[i] > best ? wsum[i] : best;
+  const bool greedy = temp < 1e-5f;
+  if (best == 0ull || nan || !(temp >= 0.f && temp < INFINITY) || greedy) {
+    const bool ok = best != 0ull && !nan && greedy && temp >= 0.f;   // else: no distribution
+    if (threadIdx.x == 0) {
+      a.tokens[row] = ok ? (int)best_index(best) : -1;
+      if (a.probs) a.probs[row] = ok ? 1.f : 0.f;
+    }
+    return;
+  }
+  Scale sc{best_value(best), 0.f, 0.f, 0.f};
+  scale_of(temp, sc.sh, sc.sl);
+  ull v = 0, mass = 0;
+  int n = 0;
+  if (mine) {
+    v = weight_parts(sc, tab, best_value(mine), n);
+    mass = in_row(__ldcg(&rec[threadIdx.x].sum), v, n);
+  }
+  const ull from = scan(mass);
+  if (threadIdx.x == NT - 1) total = from + mass;
+  __syncthreads();
+  const ull z = total, d = drawn_mass(u, z);
+  if (d >= from && d < from + mass) {
+    chunk = threadIdx.x;
+    before = from;
+    factor = v;
+    shift = n;
+  }
+  __syncthreads();
+  // the chunk again, NV consecutive vectors a thread
+  constexpr int E = Part<T>::E, PER = CHUNK_TOKENS / E, NV = PER / NT;
+  const int c = chunk;
+  const ull t = d - before;
+  v = factor;
+  n = shift;
+  const T* p = (const T*)a.logits + (size_t)row * a.ld;
+  const int mis = (int)(((uintptr_t)p & 15) / sizeof(T));
+  Scale in = sc;
+  in.m = best_value(__ldcg(&rec[c].best));
+  ull sum = 0;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const uint4 q = row_vector(p, a.V, mis, c * PER + threadIdx.x * NV + j);
+#pragma unroll
+    for (int i = 0; i < E; i += 2) {
+      ull w0, w1;
+      weight2(in, tab, Part<T>::get(q, i), Part<T>::get(q, i + 1), w0, w1);
+      sum += w0 + w1;
+    }
+  }
+  ull b = scan(sum);
+  if (in_row(b, v, n) <= t && t < in_row(b + sum, v, n)) {
+#pragma unroll 1
+    for (int i = 0; i < NV * E; ++i) {
+      const int at = (c * PER + threadIdx.x * NV) * E + i - mis;
+      if (at < 0 || at >= a.V) continue;
+      const float x = Part<T>::one(p + at);
+      b += weight(in, tab, x);
+      if (t < in_row(b, v, n)) {
+        float w;
+        weight(sc, tab, x, &w);
+        a.tokens[row] = at;
+        if (a.probs) a.probs[row] = w / ((float)z * (1.f / (float)(1ull << WBITS)));
+        break;
+      }
+    }
+  }
+}
+
 template <typename T>
 __global__ void __launch_bounds__(NT, 2) sample_kernel(SampleArgs a) {
   extern __shared__ __align__(16) unsigned char smem_raw[];
@@ -1102,10 +1379,8 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SampleArgs a) {
   }
 
   const float m = best_value(best);
-  // log2(e) / T as a float pair
-  constexpr float L = 1.44269502f;                                   // log2(e) rounded
-  constexpr float L_LO = (float)(1.4426950408889634 - (double)L);
-  const float sh = L / temp, sl = (fmaf(-sh, temp, L) + L_LO) / temp;
+  float sh, sl;
+  scale_of(temp, sh, sl);
   // finer bins where the row's range of exponents is less than the weights'
   const float range = fminf((m - low) * sh, Z_END);
   S.sc = Scale{m, sh, sl, range > 1e-30f ? (float)(BINS - 1) / range : 0.f};
@@ -1281,8 +1556,33 @@ int cluster_size(int M, int V, bool filters) {
   return best;
 }
 
+// Calls without filters of at least this many tokens take the chunk kernel:
+// 40 rows of 262144, 33 us against 43 us.
+constexpr long long CHUNKED_MIN = 1ll << 21;
+bool chunked(int M, int V) { return (long long)M * V >= CHUNKED_MIN && V >= 2 * CHUNK_TOKENS; }
+
+template <typename T>
+int launch_chunked(const SampleArgs& a, int pdl, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)std::min<long long>(4 * num_sms(), (long long)a.M * row_chunks(a.V)));
+  cfg.blockDim = dim3(CNT);
+  cfg.dynamicSmemBytes = TAB * sizeof(ull);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl ? 1 : 0;
+  if (cudaLaunchKernelEx(&cfg, chunk_kernel<T>, a, (Record*)a.workspace) != cudaSuccess) return -1;
+  cfg.gridDim = dim3(a.M);
+  cfg.blockDim = dim3(NT);
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, draw_kernel<T>, a, (const Record*)a.workspace) == cudaSuccess ? 2 : -1;
+}
+
 template <typename T>
 int launch_sample(const SampleArgs& a, int pdl, cudaStream_t st) {
+  if (chunked(a.M, a.V) && !a.top_k && !a.top_p && !a.min_p) return launch_chunked<T>(a, pdl, st);
   const int C = cluster_size<T>(a.M, a.V, a.top_k || a.top_p);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)a.M * C);
@@ -1305,6 +1605,8 @@ template <typename T>
 void set_attributes() {
   cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Shared));
   cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  cudaFuncSetAttribute(chunk_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(TAB * sizeof(ull)));
+  cudaFuncSetAttribute(draw_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(TAB * sizeof(ull)));
 }
 
 }  // namespace
@@ -1312,6 +1614,10 @@ void set_attributes() {
 void setup_sample_attributes() {
   set_attributes<float>();
   set_attributes<__nv_bfloat16>();
+}
+
+size_t sample_workspace_bytes(int M, int V) {
+  return chunked(M, V) ? (size_t)M * row_chunks(V) * sizeof(Record) : 0;
 }
 
 int sample_rows(const SampleArgs& a, int pdl, cudaStream_t st) {

@@ -39,6 +39,7 @@ struct Work {
   MoeArgs moe;              // mixture-of-experts buffers (null fields for a dense target)
   unsigned int* tmask;      // [M] tree verify: ancestor mask per row
   int32_t* path;            // [B_max][KMAX + 1] tree verify: accepted path rows
+  uint4* sample;            // sampled verify: the sampling kernels' records
   unsigned int *rank, *rank_cnt;
   float* tc_fix;
   unsigned int* tc_cnt;
@@ -97,6 +98,7 @@ Work carve(char* base, const spec_model_desc& m, const spec_drafter_desc* d, int
   w.rank = b.take<unsigned int>(base, (size_t)B_max * KMAX);
   w.rank_cnt = b.take<unsigned int>(base, 4);
   w.tmask = b.take<unsigned int>(base, M);
+  w.sample = b.take<uint4>(base, sample_workspace_bytes((int)M, m.vocab) / sizeof(uint4));
   if (m.n_experts > 0) {
     const int E = m.n_experts, K = m.top_k, ff = m.d_ff_expert;
     w.moe.E = E; w.moe.K = K; w.moe.d = m.d_model; w.moe.ff = ff;
@@ -258,8 +260,9 @@ constexpr int SAMPLE_V_MAX = 1 << 19;      // weights of 45 bits sum to less tha
 constexpr int SAMPLE_ROWS_MAX = 1 << 20;
 
 SampleArgs sample_args(int dtype, const void* logits, long long ld, int M, int V, const spec_sampling& s,
-                       int32_t* tokens, float* probs) {
+                       int32_t* tokens, float* probs, void* workspace) {
   SampleArgs a = {};
+  a.workspace = workspace;
   a.dtype = dtype == SPEC_F32 ? DT_F32 : DT_BF16;
   a.logits = logits; a.ld = ld; a.M = M; a.V = V;
   a.temperature = s.temperature; a.top_k = s.top_k; a.top_p = s.top_p; a.min_p = s.min_p;
@@ -544,7 +547,7 @@ int enqueue_pass(spec_ctx* c, int B, const int32_t* seq_ids, int R, int mode, co
     LAUNCH(topm_accept(ta, st));
   }
   if (sampling) {
-    LAUNCH(sample_rows(sample_args(SPEC_F32, g.Y, m.vocab, M, m.vocab, *sampling, out_tokens, probs), 1, st));
+    LAUNCH(sample_rows(sample_args(SPEC_F32, g.Y, m.vocab, M, m.vocab, *sampling, out_tokens, probs, w.sample), 1, st));
     AcceptSampledArgs aa = {};
     aa.B = B; aa.k = R - 1; aa.drafts = tokens; aa.out_tokens = out_tokens; aa.probs = probs;
     aa.n_emitted = n_emitted; aa.seq_ids = seq_ids; aa.seq_len = c->state.seq_len; aa.pending = c->state.pending;
@@ -1055,24 +1058,31 @@ spec_status spec_attention(const spec_model_desc* m, const spec_kv_desc* kv, int
   return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ECUDA;
 }
 
+size_t spec_sample_workspace_bytes(int32_t M, int32_t V) {
+  return M > 0 && V > 0 && M <= SAMPLE_ROWS_MAX && V <= SAMPLE_V_MAX ? sample_workspace_bytes(M, V) : 0;
+}
+
 spec_status spec_sample(int32_t dtype, const void* logits, int64_t ld, int32_t M, int32_t V, const spec_sampling* s,
-                        int32_t* tokens, float* probs, void* stream) {
+                        int32_t* tokens, float* probs, void* workspace, size_t ws_bytes, void* stream) {
   if ((dtype != SPEC_F32 && dtype != SPEC_BF16) || !logits || M <= 0 || V <= 0 || ld < V || !s || !s->uniform ||
       !tokens)
     return SPEC_EINVAL;
   if (M > SAMPLE_ROWS_MAX || V > SAMPLE_V_MAX) return SPEC_EUNSUPPORTED;
+  const size_t need = sample_workspace_bytes(M, V);
+  if (need && !aligned16({workspace})) return SPEC_EINVAL;
+  if (need && (!workspace || ws_bytes < need)) return SPEC_ECAPACITY;
   setup_device_attributes();
-  if (sample_rows(sample_args(dtype, logits, ld, M, V, *s, tokens, probs), 0, (cudaStream_t)stream) < 0)
+  if (sample_rows(sample_args(dtype, logits, ld, M, V, *s, tokens, probs, workspace), 0, (cudaStream_t)stream) < 0)
     return SPEC_ECUDA;
   return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ECUDA;
 }
 
 spec_status spec_accept_sampled(int32_t dtype, const void* logits, int64_t ld, int32_t B, int32_t k, int32_t V,
                                 const int32_t* drafts, const spec_sampling* s, int32_t* out_tokens,
-                                int32_t* n_emitted, float* probs, void* stream) {
+                                int32_t* n_emitted, float* probs, void* workspace, size_t ws_bytes, void* stream) {
   if (B <= 0 || k < 0 || (k > 0 && !drafts) || !n_emitted) return SPEC_EINVAL;
   if (k > 1023 || (long long)B * (k + 1) > SAMPLE_ROWS_MAX) return SPEC_EUNSUPPORTED;
-  const spec_status r = spec_sample(dtype, logits, ld, B * (k + 1), V, s, out_tokens, probs, stream);
+  const spec_status r = spec_sample(dtype, logits, ld, B * (k + 1), V, s, out_tokens, probs, workspace, ws_bytes, stream);
   if (r != SPEC_OK) return r;
   AcceptSampledArgs a = {};
   a.B = B; a.k = k; a.drafts = drafts; a.out_tokens = out_tokens; a.probs = probs; a.n_emitted = n_emitted;

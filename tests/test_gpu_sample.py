@@ -74,6 +74,36 @@ def test_strided_and_unaligned_rows(dtype, V, ld, off):
     _check(x, binding.spec_sample(x, u, T), u, T)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("M,V,ld,off", [(64, 32773, 32773, 0), (22, 100003, 100010, 3), (9, 262144, 262144, 0),
+                                         (5, 500000, 500003, 1), (40, 57344, 57344, 0)])
+def test_large_calls(dtype, M, V, ld, off):
+    """Calls that read their rows in chunks first: every row with settings of its
+    own (plain, filtered, greedy), with masks and without."""
+    g = _gen(M + V)
+    buf = (torch.randn(off + M * ld, generator=g, device="cuda") * 2.5).to(dtype)
+    x = buf[off:off + M * ld].view(M, ld)[:, :V]
+    x[:, torch.randint(0, V, (40,), generator=g, device="cuda")] += 9.0
+    x[1, torch.rand(V, generator=g, device="cuda") < 0.9] = -float("inf")
+    x[3, ::2] = torch.finfo(dtype).min
+    x[4, :V - 1] = -float("inf")
+    u = torch.rand(M, generator=g, device="cuda")
+    i = torch.arange(M, device="cuda")
+    T = torch.where(i % 7 == 6, 0.0, 0.5 + 0.1 * (i % 9)).contiguous()
+    k = torch.where(i % 4 == 1, 30 + i, torch.where(i % 4 == 3, 3000, 0)).to(torch.int32)
+    p = torch.where(i % 3 == 0, 1.0, 0.7 + 0.29 * (i % 5) / 4).contiguous()
+    q = torch.where(i % 5 == 2, 0.02, 0.0).contiguous()
+    assert binding.lib().spec_sample_workspace_bytes(M, V) > 0
+    _check(x, binding.spec_sample(x, u, T, k, p, q), u, T, k, p, q)
+    _check(x, binding.spec_sample(x, u, T), u, T)
+    _check(x, binding.spec_sample(x, u, T, None, p), u, T, None, p)
+    x[0, V // 2] = float("nan")
+    x[2, [5, V - 1]] = float("inf")
+    x[3] = -float("inf")
+    tok, prob = binding.spec_sample(x, u)
+    assert tok[0] == -1 and prob[0] == 0 and tok[2] == (5 if u[2] < 0.5 else V - 1) and prob[2] == 0.5 and tok[3] == -1
+
+
 def test_settings_differ_by_row():
     M, V = 64, 5003
     g = _gen(3)

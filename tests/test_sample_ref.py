@@ -53,17 +53,22 @@ def test_accept_walk():
 
 
 def test_host_refusals(lib):
-    E, U = binding.SPEC_EINVAL, binding.SPEC_EUNSUPPORTED
+    E, U, CAP = binding.SPEC_EINVAL, binding.SPEC_EUNSUPPORTED, binding.SPEC_ECAPACITY
     s = binding.spec_sampling(uniform=256)       # never read: every call below is refused on the host
     none = binding.spec_sampling()
     p = 256
-    sample = lambda dt=0, lg=p, ld=8, M=1, V=8, st=s, tok=p: lib.spec_sample(dt, lg, ld, M, V, C.byref(st), tok, p, None)
+    sample = lambda dt=0, lg=p, ld=8, M=1, V=8, st=s, tok=p, ws=None, nws=0: lib.spec_sample(dt, lg, ld, M, V, C.byref(st), tok, p, ws, nws, None)
     assert sample(dt=2) == E and sample(lg=None) == E and sample(ld=7) == E and sample(M=0) == E
     assert sample(V=0) == E and sample(st=none) == E and sample(tok=None) == E
-    assert lib.spec_sample(0, p, 8, 1, 8, None, p, p, None) == E
+    assert lib.spec_sample(0, p, 8, 1, 8, None, p, p, None, 0, None) == E
+    big = dict(M=64, V=1 << 18, ld=1 << 18)      # needs a workspace
+    need = lib.spec_sample_workspace_bytes(64, 1 << 18)
+    assert need > 0 and sample(**big) == CAP and sample(ws=p, nws=need - 1, **big) == CAP
+    assert sample(ws=p + 8, nws=need, **big) == E
+    assert lib.spec_sample_workspace_bytes(1, 4096) == 0 and lib.spec_sample_workspace_bytes(0, 8) == 0
     assert sample(V=(1 << 19) + 1, ld=1 << 22) == U and sample(M=(1 << 20) + 1) == U
     acc = lambda B=1, k=2, d=p, st=s, out=p, ne=p: lib.spec_accept_sampled(0, p, 8, B, k, 8, d, C.byref(st), out, ne,
-                                                                           None, None)
+                                                                           None, None, 0, None)
     assert acc(B=0) == E and acc(k=-1) == E and acc(d=None) == E and acc(st=none) == E
     assert acc(out=None) == E and acc(ne=None) == E and acc(k=1024) == U and acc(B=1 << 20) == U
     assert lib.spec_verify_sampled(None, 1, None, 0, None, C.byref(s), None, None, None, None, None) == E
