@@ -377,19 +377,18 @@ class Lora:
 
     def __init__(self, a: torch.Tensor, b: torch.Tensor, scale: Optional[torch.Tensor] = None):
         fn = "Lora"
-        _need(fn, a.dim() == 3 and b.dim() == 3 and a.dtype == b.dtype and a.dtype in _LOGIT_DTYPES and
-              a.shape[0] == b.shape[0] and a.shape[1] == b.shape[2],
-              "a [n][rank][K] and b [n][N][rank] must be float32 or bfloat16 and agree")
-        _need(fn, a.is_cuda and a.device == b.device and a.is_contiguous() and b.is_contiguous(),
+        dt, sa, sb, dev = _LOGIT_DTYPES.get(a.dtype), a.shape, b.shape, a.get_device()
+        _need(fn, dt is not None and b.dtype is a.dtype and len(sa) == 3 and len(sb) == 3 and sa[0] == sb[0] and
+              sa[1] == sb[2], "a [n][rank][K] and b [n][N][rank] must be float32 or bfloat16 and agree")
+        _need(fn, dev >= 0 and b.get_device() == dev and a.is_contiguous() and b.is_contiguous(),
               "a and b must be contiguous on one GPU")
-        _need(fn, scale is None or (scale.dtype == torch.float32 and scale.shape == a.shape[:1] and
-                                    scale.is_contiguous() and scale.device == a.device),
+        _need(fn, scale is None or (scale.dtype is torch.float32 and scale.shape == sa[:1] and
+                                    scale.is_contiguous() and scale.get_device() == dev),
               "scale must be a contiguous float32 tensor [n] beside them")
-        self.a, self.b, self.scale = a, b, scale
-        self.n, self.rank, self.K = a.shape
-        self.N = b.shape[1]
-        self.dev = a.get_device()
-        self.desc = spec_lora(_LOGIT_DTYPES[a.dtype], self.n, self.rank, _ptr(a), _ptr(b), _ptr(scale))
+        self.a, self.b, self.scale, self.dev = a, b, scale, dev
+        self.n, self.rank, self.K = sa
+        self.N = sb[1]
+        self.desc = spec_lora(dt, self.n, self.rank, a.data_ptr(), b.data_ptr(), _ptr(scale))
 
 
 def spec_linear_lora(w, x: torch.Tensor, lora: Lora, ids: torch.Tensor, gain: Optional[torch.Tensor] = None,
@@ -401,11 +400,11 @@ def spec_linear_lora(w, x: torch.Tensor, lora: Lora, ids: torch.Tensor, gain: Op
     call's stream when not given; its first int records an id out of range."""
     fn = "spec_linear_lora"
     L = lib()
-    dev = x.get_device()
+    dev, shape = x.get_device(), x.shape
     N, K = w.N, w.K
-    _need(fn, x.is_cuda and x.dim() == 2 and x.dtype is torch.float32 and x.is_contiguous() and x.shape[1] == K,
+    _need(fn, dev >= 0 and len(shape) == 2 and shape[1] == K and x.dtype is torch.float32 and x.is_contiguous(),
           "x must be a contiguous float32 CUDA tensor [M][K]")
-    M = x.shape[0]
+    M = shape[0]
     _need(fn, lora.K == K and lora.N == N and lora.dev == dev and w.data.get_device() == dev,
           "the adapters must have the projection's N and K, on its device")
     _need(fn, ids.dtype is torch.int32 and ids.dim() == 1 and ids.numel() == M and ids.is_contiguous() and

@@ -18,22 +18,22 @@
 // Weights are integers: w_i in units of 2^-44 of the largest, rounded (a
 // choice: tokens below 2^-45 of the most likely one count as zero). Their sums
 // are exact, so the cut and the token do not depend on the order of the
-// additions or the number of CTAs. The weight
-// itself is evaluated to about 2^-37 (the exponent as a float pair, a table of
-// 4096 powers), because a token is decided by a sum of up to V weights next to
-// a border: at the 2^-24 of plain floats about one token in 10^4 would differ
-// from the 64-bit definition.
+// additions or the number of CTAs. The weight itself is evaluated to about 2^-37
+// (the exponent as a float pair, a table of 4096 powers), because a token is
+// decided by a sum of up to V weights next to a border: at the 2^-24 of plain
+// floats about one token in 10^4 would differ from the 64-bit definition; here
+// none of 27600 rows of 4096 to 262144 tokens did.
 //
 // Large calls without filters: a first kernel takes the rows in chunks of 4096
-// tokens, one pass that leaves each chunk's maximum and the sum of its weights,
+// tokens, in one pass that leaves each chunk's maximum and the sum of its weights,
 // relative to that maximum; it loads the SMs evenly, with the next chunk's loads
 // in flight under the exponentials of the last. A CTA a row then adds the sums
 // up in the row's units, finds the drawn chunk and draws inside it.
 //
-// Otherwise a thread-block cluster takes a row; its CTAs push what the others need into
-// their shared memory, so that a phase costs one cluster barrier. Scan 1 finds
-// the maximum and the maxima of the row's segments (up to 1024).
-// Without top-k and top-p, scan 2 sums the weights and the warp that holds the
+// Otherwise a thread-block cluster takes a row; its CTAs push what the others
+// need into their shared memory, so that a phase costs one cluster barrier. Scan
+// 1 finds the maximum and the maxima of the row's segments (up to 1024). Without
+// top-k and top-p, scan 2 sums the weights and the warp that holds the
 // drawn mass finds the token. With top-k, scan 2 lists the tokens down to the
 // k-th largest segment maximum -- at least k tokens, and rarely many more -- and
 // the first CTA cuts and draws among those alone. With top-p alone, scan 2 adds
@@ -43,6 +43,13 @@
 // that bin alone are listed and sorted for the cut (a radix search of their keys
 // where even they are too many; top-k then has a histogram of counts), and a
 // last scan sums the kept weights.
+//
+// What bounds it: one row, latency (13 us with top-k, about 20 dependent phases of
+// 0.3 to 2 us); many rows, the weights: the table's random 8-byte reads of shared
+// memory (about 6 wavefronts a warp, 0.2 cycles a token of an SM) and the
+// histogram's atomics, not the 1 MB a row out of HBM. 262144 fp32 logits a row: 40
+// rows at temperature 28.5 us (1.5 TB/s; the bytes alone 6.2 us), with top-k 50 36
+// us; 64 rows with top-p of mixed breadth 104 us.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -474,7 +481,6 @@ struct Mass {
   }
   SPEC_DEV ull operator()(int i, float x) const { return keep(i, x, weight(sc, tab, x)); }
   SPEC_DEV ull two(int i, float x0, float x1) const {
-    if (cutting && rank_key(fmaxf(x0, x1)) > cut.key) return 0ull;
     ull w0, w1;
     weight2(sc, tab, x0, x1, w0, w1);
     return keep(i, x0, w0) + keep(i + 1, x1, w1);
@@ -873,6 +879,17 @@ struct Sampler {
         s.list_idx[at] = i;
       }
     }
+  }
+
+  // Whether the tokens of the bins before `bins` are few enough to be listed and
+  // sorted by one CTA: fewer than a quarter of the n segment maxima lie there, that
+  // is about 0.3 tokens a segment. (64 rows with top-p: 104 us; trying wherever
+  // they might fit, up to 7 of 8 of the segments, 114 us.)
+  SPEC_DEV bool listable(int bins, int n) {
+    int in = 0;
+    for (int i0 = 0; i0 < n; i0 += NT)
+      in += __syncthreads_count(i0 + (int)threadIdx.x < n && sc.bin(s.seg[min(i0 + (int)threadIdx.x, n - 1)]) < bins);
+    return in < n / 4;
   }
 
   // Lists the tokens of the first bins in order, below `hi`, and hands them to
@@ -1425,8 +1442,8 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SampleArgs a) {
   auto p_of = [&](ull z) { return top_p_mass(p, z); };
   Cut cut{0xffffffffu, 0x7fffffff};
   ull need, before;
+  const int segs = C * NT / seg_lanes;
   if (k > 0) {
-    const int segs = C * NT / seg_lanes;
     if (k <= segs && draw(S.list_below(end_of((S.threshold(k, segs) + 1) * (BINS / SEG_BINS))), 0ull)) return;
     S.template find_bin<false>(every, k_of, &need);
     S.template cut_in_bin<false>(cut, need, every);
@@ -1434,7 +1451,7 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SampleArgs a) {
   if (p < 1.f) {
     if (k == 0) {
       const ull all = S.template find_bin<true>(every, p_of, &need);
-      if (draw(S.list_below(end_of(s.bin + 1)), all)) return;
+      if (S.listable(s.bin + 1, segs) && draw(S.list_below(end_of(s.bin + 1)), all)) return;
       S.template cut_in_bin<true>(cut, need, every);
     } else {
       auto in = [&](int i, float x) { return kept(cut, rank_key(x), i); };
@@ -1556,9 +1573,9 @@ int cluster_size(int M, int V, bool filters) {
   return best;
 }
 
-// Calls without filters of at least this many tokens take the chunk kernel:
-// 40 rows of 262144, 33 us against 43 us.
-constexpr long long CHUNKED_MIN = 1ll << 21;
+// Calls without filters of at least this many tokens take the chunk kernel: of
+// 262144 tokens a row, 1 row 8.9 us (16.9 without), 40 rows 28.5 us (43).
+constexpr long long CHUNKED_MIN = 1ll << 17;
 bool chunked(int M, int V) { return (long long)M * V >= CHUNKED_MIN && V >= 2 * CHUNK_TOKENS; }
 
 template <typename T>
