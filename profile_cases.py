@@ -42,6 +42,15 @@ Each summary under profiles/ names the case and the ncu command it ran.
     python profile_cases.py verify_moe
         the mixture-of-experts workload (batch 8, context 4096, k = 4): two
         verify passes inside an NVTX range "verify".
+    python profile_cases.py lora_30b
+        the ~30B-class gate/up projection (49152 x 6144 bf16, 604 MB) of 40
+        rows with RMSNorm, eight adapters of rank 16 over them; three calls.
+    python profile_cases.py sample_topp
+        64 rows of 262144 fp32 logits, every row with its own temperature
+        and top-p; three calls.
+    python profile_cases.py sample_t
+        40 rows of 262144 fp32 logits at a temperature each, no filter; three
+        calls.
 
 Inputs are the seeded synthetic weights and caches of the workloads; nothing
 here checks results (the tests do).
@@ -187,11 +196,51 @@ def verify_moe(w):
     _steps(configs.WORKLOADS["moe_bf16_b8_ctx4096_k4"], "verify", 2, draft=False)
 
 
+def lora_30b(w):
+    t = configs.DENSE30B
+    M, adapters, r = 40, 8, 16
+    g = torch.Generator(device="cuda").manual_seed(7)
+    W = synth.make_matrix(g, t.wdtype, 1, 2 * t.ff, t.d, t.wstd, "cuda")
+    x = torch.randn((M, t.d), generator=g, device="cuda")
+    A = (torch.randn((adapters, r, t.d), generator=g, device="cuda") / t.d ** 0.5).to(torch.bfloat16)
+    B = (torch.randn((adapters, 2 * t.ff, r), generator=g, device="cuda") / r ** 0.5).to(torch.bfloat16)
+    lora = binding.Lora(A, B)
+    idx = (torch.arange(M, device="cuda", dtype=torch.int32) // 5) % adapters
+    y = torch.empty((M, W.N), device="cuda")
+    gain = torch.ones(t.d, device="cuda")
+    for _ in range(3):
+        binding.spec_linear_lora(W, x, lora, idx, gain=gain, y=y)
+    torch.cuda.synchronize()
+
+
+def _logits(rows, V):
+    g = torch.Generator(device="cuda").manual_seed(8)
+    z = torch.randn((rows, V), generator=g, device="cuda") * 3
+    T = torch.linspace(0.6, 1.2, rows, device="cuda")
+    return z, T, torch.rand(rows, generator=g, device="cuda")
+
+
+def sample_topp(w):
+    z, T, u = _logits(64, 262144)
+    p = torch.linspace(0.5, 0.99, 64, device="cuda")
+    for _ in range(3):
+        binding.spec_sample(z, u, temperature=T, top_p=p)
+    torch.cuda.synchronize()
+
+
+def sample_t(w):
+    z, T, u = _logits(40, 262144)
+    for _ in range(3):
+        binding.spec_sample(z, u, temperature=T)
+    torch.cuda.synchronize()
+
+
 CASES = {"projections": projections, "projections_wide": projections_wide, "projections_30b": projections_30b,
          "layer_and_head_30b": layer_and_head_30b,
          "projections_30b_m5": projections_30b_m5, "projections_wide_q4": projections_wide_q4,
          "verify_q4b4": verify_q4b4, "draft": draft, "verify": verify, "attention_30b": attention_30b,
-         "lmhead_30b": lmhead_30b, "step_30b_b8": step_30b_b8, "verify_moe": verify_moe}
+         "lmhead_30b": lmhead_30b, "step_30b_b8": step_30b_b8, "verify_moe": verify_moe,
+         "lora_30b": lora_30b, "sample_topp": sample_topp, "sample_t": sample_t}
 
 
 def main(argv):

@@ -33,23 +33,24 @@
 // Otherwise a thread-block cluster takes a row; its CTAs push what the others
 // need into their shared memory, so that a phase costs one cluster barrier. Scan
 // 1 finds the maximum and the maxima of the row's segments (up to 1024). Without
-// top-k and top-p, scan 2 sums the weights and the warp that holds the
-// drawn mass finds the token. With top-k, scan 2 lists the tokens down to the
-// k-th largest segment maximum -- at least k tokens, and rarely many more -- and
-// the first CTA cuts and draws among those alone. With top-p alone, scan 2 adds
-// up a histogram of 2048 bins, linear in the exponent, of exact masses (three
-// 15-bit digits), and the tokens up to the bin in which the cut lies are listed
-// and drawn from in the same way. Where the listed tokens are too many, those of
-// that bin alone are listed and sorted for the cut (a radix search of their keys
-// where even they are too many; top-k then has a histogram of counts), and a
-// last scan sums the kept weights.
+// top-k and top-p, scan 2 sums the weights and the warp that holds the drawn mass
+// finds the token. With top-k, scan 2 lists the tokens down to the k-th largest
+// segment maximum -- at least k tokens, and rarely many more -- and the first CTA
+// cuts and draws among those alone. With top-p alone, scan 2 counts the tokens in
+// 2048 bins, linear in the exponent, which bound the mass up to each well enough
+// to leave a few bins for the cut; scan 3 adds all weights up exactly, lists those
+// bins' tokens, and sums the tokens ahead of them in index order, so that the cut
+// and the draw follow from the list and those sums. (A nucleus of few tokens is
+// listed as a whole and drawn from as top-k's.) Where the listed tokens are too
+// many, the cut comes from a radix search of their keys, or min-p's end lies ahead
+// of it, and a last scan sums the kept weights.
 //
 // What bounds it: one row, latency (13 us with top-k, about 20 dependent phases of
-// 0.3 to 2 us); many rows, the weights: the table's random 8-byte reads of shared
-// memory (about 6 wavefronts a warp, 0.2 cycles a token of an SM) and the
-// histogram's atomics, not the 1 MB a row out of HBM. 262144 fp32 logits a row: 40
-// rows at temperature 28.5 us (1.5 TB/s; the bytes alone 6.2 us), with top-k 50 36
-// us; 64 rows with top-p of mixed breadth 104 us.
+// 0.3 to 2 us); many rows, the weights: about 50 instructions a token, among them
+// random 8-byte reads of the table in shared memory, not the 1 MB a row out of
+// HBM. 262144 fp32 logits a row: 40 rows at temperature 28.5 us (1.5 TB/s; the
+// bytes alone 6.2 us), with top-k 50 26 us; 64 rows with top-p of mixed breadth 93
+// us.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -71,23 +72,21 @@ constexpr int NW = NT / 32;
 constexpr int BINS = 2048;
 constexpr int BPT = BINS / NT;      // consecutive bins of a thread
 constexpr int WBITS = 44;           // fraction bits of a weight
-constexpr int DIGIT = 15;           // bits of a mass digit
-constexpr int DIGIT_TOKENS = 120000;  // tokens of a CTA whose digits surely sum in 32 bits
 constexpr int TAB_LOG = 12;
 constexpr int TAB = 1 << TAB_LOG;   // 2^(-j/4096)
 constexpr int MAX_C = 16;           // CTAs on one row (a thread-block cluster)
-constexpr int LIST = 1024;          // tokens a CTA lists
-constexpr int FEW = 2048;           // tokens the first CTA sorts
+constexpr int FEW = 2048;           // tokens a CTA lists, and the first one cuts
 constexpr int COUNTED = NT / 2;     // at most so many are counted instead
 constexpr int CHUNK_TOKENS = 4096;  // tokens of a chunk of the chunk kernel
 constexpr int CNT = 256;            // its threads
 constexpr int CNW = CNT / 32;
 constexpr int SEG_MAX = 1024;       // segments of a row (the elements of 1, 2, 4 or 8 lanes)
 constexpr int SEG_BINS = NT;        // bins of the segment maxima
+constexpr int FINE = NT;            // finer bins of listed tokens, one a thread
+constexpr int TIED = 64;            // of one such bin, so many are counted
 constexpr float Z_END = 46.f;       // weights are zero beyond this exponent
 constexpr int CHUNK = 8;            // vectors of a lane whose sum is kept apart, doubled until
 constexpr int CHUNKS = 32;          // a warp's part has at most 32 chunks
-constexpr int IDX_BITS = 19;        // V <= 2^19: an index and a 45-bit weight share a word
 
 // 2^(44 - j/4096), from the exponential series at compile time.
 struct Table {
@@ -119,19 +118,26 @@ struct Cut {
 struct Shared {
   ull tab[TAB];
   union {
-    unsigned int hist[3][BINS];  // counts, or the masses' digits
-    ull mass[BINS];              // radix search inside a bin
-    ull sort[FEW];               // first CTA: the listed tokens
+    unsigned int hist[BINS];     // counts
+    ull mass[BINS];              // radix search inside some bins
+    ull sort[FEW];               // first CTA: the tokens all listed
   };
-  uint32_t list_key[LIST];
-  int list_idx[LIST];
-  int listed;                // tokens this CTA listed (more than LIST: they did not fit)
+  uint32_t list_key[FEW];
+  int list_idx[FEW];
+  int listed;                // tokens this CTA listed (more than FEW: they did not fit)
   // pushed by every CTA of the cluster
   ull x_best[MAX_C];         // packed maximum
   float x_low[MAX_C];        // minimum
   int x_nan[MAX_C];
   ull x_total[MAX_C];        // sum of the weights
-  float seg[SEG_MAX];        // segment maxima
+  union {
+    float seg[SEG_MAX];      // segment maxima
+    ull fine[FINE];          // first CTA: amounts of the listed tokens, by finer bins
+  };
+  ull tied[TIED][2];         // tokens of one of those, and their amounts
+  ull word;                  // the selected one
+  uint32_t key_lo, key_hi;
+  int n_tied;
   int gathered;              // first CTA: tokens listed by all
   unsigned int seg_bins[SEG_BINS];
   Cut cut;                   // pushed by the first CTA: the cut of the row
@@ -140,6 +146,10 @@ struct Shared {
   ull total;                 // this CTA's sum, read by the cluster
   int bin;                   // crossing bin
   ull before, at;            // amount before it, and in it
+  ull x_bins[MAX_C][3];      // pushed: counts, least and largest mass of a share of the bins
+  ull scan[NW][3];
+  ull all;                   // this CTA's mass
+  int lo, hi, n_lo, n_hi;    // pushed: bins in which a cut may lie, tokens before and through them
   int found;                 // index found by find_in_order, written by its owner
   int base;
   int r;                     // tokens kept of the sorted ones
@@ -150,11 +160,10 @@ struct Shared {
 struct Scale {
   float m, sh, sl, bins;
   // Monotone in x (each rounding is), so bins are ranges of the order.
-  SPEC_DEV float place(float x) const { return (m - x) * sh * bins; }
-  SPEC_DEV int bin(float x) const {
-    if (m == INFINITY) return x == INFINITY ? 0 : BINS - 1;
-    return (int)fminf(place(x), (float)(BINS - 1));
+  SPEC_DEV float place(float x) const {
+    return m == INFINITY ? (x == INFINITY ? 0.f : INFINITY) : (m - x) * sh * bins;
   }
+  SPEC_DEV int bin(float x) const { return (int)fminf(place(x), (float)(BINS - 1)); }
 };
 
 // 2^(n-1), half a unit before the shift by n: a weight is rounded, not cut off.
@@ -308,7 +317,7 @@ SPEC_DEV float rank_val(uint32_t k) { return ord_val(~k); }
 template <typename T>
 struct Part {
   const T* p;
-  int V, mis, v0, v1;   // vectors [v0, v1); vector v holds elements v * E - mis ...
+  int V, mis, per, nvec, v0, v1;   // vectors [v0, v1); vector v holds elements v * E - mis ...
   static constexpr int E = 16 / sizeof(T);
   static constexpr int U = 4;           // vectors a lane has in flight
   SPEC_DEV static float get(const uint4& q, int i) {
@@ -323,8 +332,8 @@ struct Part {
     p = row;
     V = V_;
     mis = (int)(((uintptr_t)row & 15) / sizeof(T));
-    const int nvec = (V + mis + E - 1) / E;
-    const int per = (nvec + C * NW - 1) / (C * NW);
+    nvec = (V + mis + E - 1) / E;
+    per = (nvec + C * NW - 1) / (C * NW);
     const int w = cta * NW + (threadIdx.x >> 5);
     v0 = min(nvec, w * per);
     v1 = min(nvec, v0 + per);
@@ -380,38 +389,49 @@ struct Part {
     if (v0 < v1 - 1) edge(v1 - 1, 1, f);
   }
   // The same for a long f, in pairs: f.two(index, value, next value), or
-  // f(index, value) on the row's edges. One copy of it for a vector's pairs
-  // (the code of a scan that runs once comes from a cold instruction cache),
-  // two vectors ahead; done(vectors of the lane so far) after each vector.
-  template <typename F, typename D>
+  // f(index, value) on the row's edges. W vectors of a lane a step, the next ones
+  // in flight; one copy of f for them (the code of a scan that runs once comes
+  // from a cold instruction cache). done(vectors of the lane so far) after each step.
+  template <int W, typename F, typename D>
   SPEC_DEV void each_rolled(int from, int to, F& f, D done) const {
+    constexpr int B = W == 1 ? 3 : 2 * W;   // buffers
     const int lane = threadIdx.x & 31;
-    uint4 q[3];
-    bool ok[3];
-    auto get_vec = [&](int v, uint4& x) {
+    uint4 q[B];
+    bool ok[B];
+    auto get_vec = [&](int v, int j) {
       const int i0 = v * E - mis;
-      const bool in = v < to && i0 >= 0 && i0 + E <= V;
-      if (in) x = *reinterpret_cast<const uint4*>(p + i0);
-      return in;
+      ok[j] = v < to && i0 >= 0 && i0 + E <= V;
+      if (ok[j]) q[j] = *reinterpret_cast<const uint4*>(p + i0);
     };
-    ok[0] = get_vec(from + lane, q[0]);
-    ok[1] = get_vec(from + 32 + lane, q[1]);
+#pragma unroll
+    for (int j = 0; j < B - W; ++j) get_vec(from + lane + 32 * j, j);
     int n = 0;
 #pragma unroll 1
-    for (int v = from + lane; v - lane < to; v += 32) {
-      ok[2] = get_vec(v + 64, q[2]);
-      if (ok[0]) {
+    for (int v = from + lane; v - lane < to; v += 32 * W) {
 #pragma unroll
-        for (int i = 0; i < E; i += 2) f.two(v * E - mis + i, get(q[0], i), get(q[0], i + 1));
-      } else if (v < to) {
+      for (int j = B - W; j < B; ++j) get_vec(v + 32 * j, j);
+      bool all = true;
+#pragma unroll
+      for (int j = 0; j < W; ++j) all = all && ok[j];
+      if (all) {
+#pragma unroll
+        for (int j = 0; j < W; ++j)
+#pragma unroll
+          for (int i = 0; i < E; i += 2) f.two((v + 32 * j) * E - mis + i, get(q[j], i), get(q[j], i + 1));
+      } else {
 #pragma unroll 1
-        for (int i = max(0, mis - v * E); i < E && v * E - mis + i < V; ++i) f(v * E - mis + i, one(p + v * E - mis + i));
+        for (int j = 0; j < W; ++j) {
+          const int i0 = (v + 32 * j) * E - mis;
+#pragma unroll 1
+          for (int i = max(0, -i0); i < E && i0 + i < V && v + 32 * j < to; ++i) f(i0 + i, one(p + i0 + i));
+        }
       }
-      q[0] = q[1];
-      q[1] = q[2];
-      ok[0] = ok[1];
-      ok[1] = ok[2];
-      done(++n);
+#pragma unroll
+      for (int j = 0; j < B - W; ++j) {
+        q[j] = q[j + W];
+        ok[j] = ok[j + W];
+      }
+      done(n += W);
     }
   }
   // The part's first or last vector, where the row does not fill it, in one
@@ -464,7 +484,7 @@ struct Amount {
 };
 template <typename F>
 struct Summing {
-  const F& f;
+  F& f;
   ull a;
   SPEC_DEV void operator()(int i, float x) { a += f(i, x); }
   SPEC_DEV void two(int i, float x0, float x1) { a += f.two(i, x0, x1); }
@@ -487,34 +507,53 @@ struct Mass {
   }
 };
 
-// Counts or exact masses (in digits) of the kept tokens, by bin.
-template <bool MASS, typename K>
+// One more of the tokens a CTA lists (when full, only their number is known).
+SPEC_DEV void append(Shared& s, int i, float x) {
+  if (*(volatile int*)&s.listed > FEW) return;
+  const int at = atomicAdd(&s.listed, 1);
+  if (at < FEW) {
+    s.list_key[at] = rank_key(x);
+    s.list_idx[at] = i;
+  }
+}
+
+// Top-p's scan of the tokens inside a cut: adds all their weights up, lists those
+// of exponents [lo, hi) in bin units, and returns the mass of those below lo.
+struct Nucleus {
+  Scale sc;
+  Shared& s;
+  Cut cut;
+  bool cutting;
+  float lo, hi;
+  ull all;
+  SPEC_DEV ull take(int i, float x, ull w) {
+    if (cutting && !kept(cut, rank_key(x), i)) return 0ull;
+    all += w;
+    const float v = sc.place(x);
+    if (v < lo) return w;
+    if (v < hi) append(s, i, x);
+    return 0ull;
+  }
+  SPEC_DEV ull operator()(int i, float x) { return take(i, x, weight(sc, s.tab, x)); }
+  SPEC_DEV ull two(int i, float x0, float x1) {
+    ull w0, w1;
+    weight2(sc, s.tab, x0, x1, w0, w1);
+    return take(i, x0, w0) + take(i + 1, x1, w1);
+  }
+};
+
+// Counts of the tokens inside a cut, by bin.
 struct Binned {
   Scale sc;
-  const ull* tab;
   unsigned int* hist;
-  K keep;
-  SPEC_DEV void put(float x, ull w) const {
-    unsigned int* h = hist + sc.bin(x);
-    if (!MASS) {
-      atomicAdd(h, 1u);
-      return;
-    }
-    constexpr unsigned int M = (1u << DIGIT) - 1;
-    if (w) atomicAdd(h, (unsigned int)w & M);
-    if (w >> DIGIT) atomicAdd(h + BINS, (unsigned int)(w >> DIGIT) & M);
-    if (w >> (2 * DIGIT)) atomicAdd(h + 2 * BINS, (unsigned int)(w >> (2 * DIGIT)));
-  }
+  Cut cut;
+  bool cutting;
   SPEC_DEV void operator()(int i, float x) const {
-    if (keep(i, x)) put(x, MASS ? weight(sc, tab, x) : 0ull);
+    if (!cutting || kept(cut, rank_key(x), i)) atomicAdd(hist + sc.bin(x), 1u);
   }
   SPEC_DEV void two(int i, float x0, float x1) const {
-    const bool k0 = keep(i, x0), k1 = keep(i + 1, x1);
-    if (!k0 && !k1) return;
-    ull w0 = 0, w1 = 0;
-    if (MASS) weight2(sc, tab, x0, x1, w0, w1);
-    if (k0) put(x0, w0);
-    if (k1) put(x1, w1);
+    (*this)(i, x0);
+    (*this)(i + 1, x1);
   }
 };
 
@@ -525,13 +564,15 @@ struct Sampler {
   int cta, C;
   Part<T> part;
   Scale sc;
+  static constexpr int WIDE = 8 / Part<T>::E;   // vectors a step
+  float range;      // of the row's exponents, up to Z_END
   static constexpr int PT = FEW / NT;   // sorted tokens of a thread
 
   // f(index, value) of this CTA's tokens.
   template <typename F>
   SPEC_DEV void scan(const F& f) {
     Single<F> one{f};
-    part.each_rolled(part.v0, part.v1, one, [](int) {});
+    part.template each_rolled<1>(part.v0, part.v1, one, [](int) {});
   }
 
   // Exclusive sum of v over the CTA's threads, in thread order.
@@ -550,13 +591,13 @@ struct Sampler {
   // This CTA's sum of f(index, value) in s.total, the warps' parts in wsum,
   // their chunks' in chunk; ends with a barrier.
   template <typename F>
-  SPEC_DEV void sum_part(const F& f) {
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, per = chunk_vectors();
+  SPEC_DEV void sum_part(F& f) {
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, per = chunk_vectors(part.v1 - part.v0);
     ull all = 0;
     int c = 0;
     __syncthreads();
     Summing<F> add{f, 0};
-    part.each_rolled(part.v0, part.v1, add, [&](int n) {
+    part.template each_rolled<WIDE>(part.v0, part.v1, add, [&](int n) {
       if ((n & (per - 1)) == 0) {
         const ull a = warp_sum_u64(add.a);
         if (lane == 0) s.chunk[w][c] = a;
@@ -577,35 +618,38 @@ struct Sampler {
     }
     __syncthreads();
   }
-  // A power of two.
-  SPEC_DEV int chunk_vectors() const {
+  // A lane's vectors in a chunk of a warp's n: a power of two.
+  SPEC_DEV static int chunk_vectors(int n) {
     int per = CHUNK;
-    while (per * CHUNKS * 32 < part.v1 - part.v0) per *= 2;
+    while (per * CHUNKS * 32 < n) per *= 2;
     return per;
   }
 
+  // The cluster's sum of the CTAs' v, and that of the earlier CTAs.
+  SPEC_DEV ull cluster_sum(ull v, ull* before) {
+    if (threadIdx.x < C) *cl.map_shared_rank(&s.x_total[cta], threadIdx.x) = v;
+    cl.sync();
+    ull all = 0;
+#pragma unroll
+    for (int c = 0; c < MAX_C; ++c) {
+      if (c == cta) *before = all;
+      if (c < C) all += s.x_total[c];
+    }
+    return all;
+  }
   // Sum of f(index, value) over the row, and that of the cluster's earlier CTAs.
   template <typename F>
-  SPEC_DEV ull sum(const F& f, ull* before) {
+  SPEC_DEV ull sum(F& f, ull* before) {
     sum_part(f);
-    cl.sync();
-    ull all = 0, b = 0;
-    for (int c = 0; c < C; ++c) {
-      const ull t = *cl.map_shared_rank(&s.total, c);
-      if (c < cta) b += t;
-      all += t;
-    }
-    cl.sync();
-    *before = b;
-    return all;
+    return cluster_sum(s.total, before);
   }
 
   // Calls hit(index, value) in the lane that holds the lowest index at which
   // the sum of f in index order exceeds t (t below the row's sum; the CTA's
   // sums as sum_part left them, before: the sum of the earlier CTAs).
   template <typename F, typename H>
-  SPEC_DEV void find_in_order(const F& f, ull t, ull before, H hit) {
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, per = chunk_vectors();
+  SPEC_DEV void find_in_order(F& f, ull t, ull before, H hit) {
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, per = chunk_vectors(part.v1 - part.v0);
     ull b = before;
 #pragma unroll
     for (int i = 0; i < NW; ++i)
@@ -620,7 +664,7 @@ struct Sampler {
     int v = from + lane;
     bool over = false;
     Summing<F> add{f, 0};
-    part.each_rolled(from, min(part.v1, from + per * 32), add, [&](int) {
+    part.template each_rolled<1>(from, min(part.v1, from + per * 32), add, [&](int) {
       const ull inc = warp_scan_u64(add.a);
       const ull tot = __shfl_sync(FULL, inc, 31);
       if (!over && t < b + tot) {
@@ -635,7 +679,7 @@ struct Sampler {
   }
   // From index i on, in one lane: the element at which the sum b passes t.
   template <typename F, typename H>
-  SPEC_DEV void walk(const F& f, int i, ull t, ull b, H hit) {
+  SPEC_DEV void walk(F& f, int i, ull t, ull b, H hit) {
 #pragma unroll 1
     for (; i < part.V; ++i) {
       const float x = Part<T>::one(part.p + i);
@@ -648,7 +692,7 @@ struct Sampler {
   }
   // The same index in every CTA.
   template <typename F>
-  SPEC_DEV int find_all(const F& f, ull t, ull before) {
+  SPEC_DEV int find_all(F& f, ull t, ull before) {
     find_in_order(f, t, before, [&](int i, float) {
       for (int r = 0; r < C; ++r) *cl.map_shared_rank(&s.found, r) = i;
     });
@@ -672,65 +716,113 @@ struct Sampler {
     __syncthreads();
   }
 
-  // The bin in which the count or exact mass of the kept tokens, in order,
-  // first reaches need(row's amount) >= 1: s.bin, with the amount before it and
-  // in it in s.before and s.at, the same in every CTA. Each CTA counts its
-  // tokens by bin, adds up the cluster's counts of a share of the bins, and the
-  // owner of the bin tells the others. Returns the row's amount; *last: need.
-  // Empties the lists.
-  template <bool MASS, typename K, typename N>
-  SPEC_DEV ull find_bin(K keep, N need, ull* last) {
-    constexpr int D = MASS ? 3 : 1;
+  // Where in the order of bins the tokens inside `cut` reach k tokens, or the
+  // mass p of them (k = 0), the same in every CTA: in one of the bins s.lo to
+  // s.hi, with s.n_lo tokens before those and s.n_hi through them. A bin's tokens
+  // weigh the same to 1.6%, so their count bounds their mass; the cut may lie in a
+  // bin unless the bounds of the mass up to it and of the mass behind it say
+  // otherwise -- few bins, as the same error in both nearly cancels. Each CTA
+  // counts its tokens by bin, adds up the cluster's counts of a share of the
+  // bins, and the owners of the two bins tell the others. Empties the lists.
+  // (Exact masses by bin, in three 15-bit digits, took three atomics and a weight
+  // a token, and a further scan for the list: 64 rows of 262144 with a broad nucleus
+  // took 154 us, 95 now.)
+  SPEC_DEV void find_bins(const Cut& cut, bool cutting, int k, float p) {
     if (threadIdx.x == 0) {
+      s.all = 0;
       s.listed = 0;
       s.gathered = 0;
     }
-    for (int i = threadIdx.x; i < D * BINS; i += NT) s.hist[0][i] = 0u;
+    for (int i = threadIdx.x; i < BINS; i += NT) s.hist[i] = 0u;
     __syncthreads();
-    Binned<MASS, K> add{sc, s.tab, &s.hist[0][0], keep};
-    part.each_rolled(part.v0, part.v1, add, [](int) {});
+    Binned add{sc, s.hist, cut, cutting};
+    part.template each_rolled<WIDE>(part.v0, part.v1, add, [](int) {});
     cl.sync();
+    // (rolled loops: what runs once comes from a cold instruction cache)
     const int share = (BINS + C - 1) / C, per = (share + NT - 1) / NT, b0 = cta * share + threadIdx.x * per;
     const int b1 = min(min(b0 + per, (cta + 1) * share), BINS);
-    ull h[BPT], t = 0;
-#pragma unroll
-    for (int j = 0; j < BPT; ++j) {
-      h[j] = 0;
-      if (b0 + j < b1) {
+    ull t[3] = {0, 0, 0};   // tokens, their least and largest mass
+#pragma unroll 1
+    for (int b = b0; b < b1; ++b) {
+      unsigned int n = 0;
 #pragma unroll 4
-        for (int c = 0; c < C; ++c) {
-          const unsigned int* o = cl.map_shared_rank(&s.hist[0][0], c) + b0 + j;
+      for (int c = 0; c < C; ++c) n += cl.map_shared_rank(s.hist, c)[b];
+      s.list_key[b - cta * share] = n;
+      add_bin(t, b, n);
+    }
+    ull at[3];
 #pragma unroll
-          for (int d = 0; d < D; ++d) h[j] += (ull)o[d * BINS] << (d * DIGIT);
+    for (int i = 0; i < 3; ++i) {
+      at[i] = warp_scan_u64(t[i]);
+      if ((threadIdx.x & 31) == 31) s.scan[threadIdx.x >> 5][i] = at[i];
+      at[i] -= t[i];
+    }
+    __syncthreads();
+    if (threadIdx.x < 3 * C) {   // a sum to each CTA
+      const int i = threadIdx.x % 3;
+      ull all = 0;
+#pragma unroll 4
+      for (int w = 0; w < NW; ++w) all += s.scan[w][i];
+      cl.map_shared_rank(&s, threadIdx.x / 3)->x_bins[cta][i] = all;
+    }
+    for (int w = 0; w < (int)(threadIdx.x >> 5); ++w)
+#pragma unroll
+      for (int i = 0; i < 3; ++i) at[i] += s.scan[w][i];
+    cl.sync();
+    ull all[3] = {0, 0, 0};
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        if (c == cta) at[i] += all[i];
+        all[i] += s.x_bins[c][i];
+      }
+    // Up to a bin: may the cut lie there or before (x), must it (y)?
+    bool x0 = true, y0 = true;
+#pragma unroll 1
+    for (int b = b0 - 1; b < b1; ++b) {
+      const int n0 = (int)at[0];
+      if (b >= b0) add_bin(at, b, s.list_key[b - cta * share]);
+      const bool x = k > 0 ? at[0] >= (ull)k : at[2] >= top_p_mass(p, at[2] + (all[1] - at[1]));
+      const bool y = k > 0 ? x : at[1] >= top_p_mass(p, at[1] + (all[2] - at[2]));
+      for (int c = 0; c < C; ++c) {
+        Shared& o = *cl.map_shared_rank(&s, c);
+        if (x && !x0) {
+          o.lo = b;
+          o.n_lo = n0;
+        }
+        if (y && !y0) {
+          o.hi = b;
+          o.n_hi = (int)at[0];
         }
       }
-      t += h[j];
-    }
-    ull b = block_scan(t);
-    if (threadIdx.x == NT - 1) s.total = b + t;
-    __syncthreads();
-    if (threadIdx.x < C) *cl.map_shared_rank(&s.x_total[cta], threadIdx.x) = s.total;
-    cl.sync();
-    ull all = 0;
-#pragma unroll
-    for (int c = 0; c < MAX_C; ++c) {
-      if (c == cta) b += all;
-      if (c < C) all += s.x_total[c];
-    }
-    *last = need(all);
-#pragma unroll
-    for (int j = 0; j < BPT; ++j) {
-      if (b < *last && *last <= b + h[j])
-        for (int c = 0; c < C; ++c) {
-          Shared& o = *cl.map_shared_rank(&s, c);
-          o.bin = b0 + j;
-          o.before = b;
-          o.at = h[j];
-        }
-      b += h[j];
+      x0 = x;
+      y0 = y;
     }
     cl.sync();
-    return all;
+  }
+  // n tokens of bin b to a count and its bounds of mass.
+  SPEC_DEV void add_bin(ull (&t)[3], int b, unsigned int n) const {
+    ull least, most;
+    bounds(b, least, most);
+    t[0] += n;
+    t[1] += n * least;
+    t[2] += n * most;
+  }
+
+  // Bounds of the weight of a token in a bin.
+  SPEC_DEV void bounds(int bin, ull& least, ull& most) const {
+    if (sc.m == INFINITY) {
+      least = most = bin == 0 ? 1ull << WBITS : 0ull;
+      return;
+    }
+    // (place() is off by 4 roundings, 2e-5 in the exponent at most; the factors are 1 -+ 1e-4)
+    const float step = sc.bins > 0.f ? 1.f / sc.bins : 0.f;
+    most = (ull)(exp2f(WBITS - bin * step) * 1.0001f) + 1;
+    least = (ull)(exp2f(WBITS - (bin + 1) * step) * 0.9999f);
+    if (bin == BINS - 1) {   // ends with the least weight of all, or beyond all weights
+      least = 0;
+      if (range >= Z_END) most = 0;
+    }
   }
 
   // The bin in which the amount in order first reaches need >= 1 (s.bin), the
@@ -752,11 +844,11 @@ struct Sampler {
     __syncthreads();
   }
 
-  // The key in bin `bin` at which the amount in order first reaches `need`
-  // (`before` the bin): three levels of 11, 11 and 10 key bits. Returns the
+  // The key in bins lo to hi at which the amount in order first reaches `need`
+  // (`before` those bins): three levels of 11, 11 and 10 key bits. Returns the
   // key; s.before: amount strictly before it, s.at: amount of its tokens.
   template <bool MASS, typename K>
-  SPEC_DEV uint32_t radix(int bin, ull need, ull before, K keep) {
+  SPEC_DEV uint32_t radix(int lo, int hi, ull need, ull before, K keep) {
     uint32_t pre = 0;
 #pragma unroll 1
     for (int level = 0; level < 3; ++level) {
@@ -765,7 +857,8 @@ struct Sampler {
       for (int i = threadIdx.x; i < BINS; i += NT) s.mass[i] = 0ull;
       __syncthreads();
       auto one = [&](int i, float x) {
-        if (sc.bin(x) != bin) return;
+        const int b = sc.bin(x);
+        if (b < lo || b > hi) return;
         const uint32_t k = rank_key(x);
         if ((level > 0 && (k >> (shift + bits)) != pre) || !keep(i, x)) return;
         atomicAdd(&s.mass[(k >> shift) & ((1 << bits) - 1)], MASS ? weight(sc, s.tab, x) : 1ull);
@@ -785,61 +878,134 @@ struct Sampler {
     return pre;
   }
 
-  // The cut at which the amount in order (of the tokens kept so far) reaches
-  // `need`, in bin s.bin with s.before ahead of it.
-  template <bool MASS, typename K>
-  SPEC_DEV void cut_in_bin(Cut& cut, ull need, K keep) {
-    const int bin = s.bin;
-    const ull before = s.before;
+  // The n tokens handed to the first CTA, PT a thread: their order (key, index)
+  // and weight (1 where they are counted); s.key_lo and s.key_hi: their keys' range.
+  template <bool MASS>
+  SPEC_DEV void take_listed(int n, ull (&e)[PT], ull (&w)[PT]) {
     if (threadIdx.x == 0) {
-      s.listed = 0;
-      s.gathered = 0;
+      s.key_lo = 0xffffffffu;
+      s.key_hi = 0u;
     }
     __syncthreads();
+    uint32_t lo = 0xffffffffu, hi = 0u;
+#pragma unroll
+    for (int j = 0; j < PT; ++j) {
+      const int i = threadIdx.x + j * NT;
+      e[j] = i < n ? s.sort[i] : ~0ull;
+      const uint32_t key = (uint32_t)(e[j] >> 32);
+      w[j] = i >= n ? 0ull : MASS ? weight_once(sc, s.tab, rank_val(key), nullptr) : 1ull;
+      if (i < n) {
+        lo = min(lo, key);
+        hi = max(hi, key);
+      }
+    }
+    lo = __reduce_min_sync(FULL, lo);
+    hi = __reduce_max_sync(FULL, hi);
+    if ((threadIdx.x & 31) == 0) {
+      atomicMin(&s.key_lo, lo);
+      atomicMax(&s.key_hi, hi);
+    }
+    __syncthreads();
+  }
+
+  // Of the first CTA's words in [lo, hi] with an amount, that at which the sum of
+  // the amounts in the words' order, `before` ahead of all, reaches need >= 1 (~0:
+  // nowhere); *ahead: the sum before it, *at: its amount. FINE bins of the range at
+  // a time, until one holds few words, which are counted (sorting 700 tokens took
+  // 10 us, one level of bins takes 1).
+  SPEC_DEV ull select(const ull (&word)[PT], const ull (&amount)[PT], ull lo, ull hi, ull need, ull before,
+                      ull* ahead, ull* at) {
+#pragma unroll 1
+    for (;;) {
+      const int shift = max(0, 55 - __clzll((long long)((hi - lo) | 1)));
+      s.fine[threadIdx.x] = 0ull;
+      if (threadIdx.x == 0) {
+        s.n_tied = 0;
+        s.bin = -1;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < PT; ++j)
+        if (amount[j] && word[j] >= lo && word[j] <= hi) atomicAdd(&s.fine[(word[j] - lo) >> shift], amount[j]);
+      __syncthreads();
+      const ull h = s.fine[threadIdx.x], b = before + block_scan(h);
+      if (b < need && need <= b + h) {
+        s.bin = threadIdx.x;
+        s.before = b;
+      }
+      __syncthreads();
+      const int bin = s.bin;
+      if (bin < 0) return ~0ull;
+      before = s.before;
+      lo += (ull)bin << shift;
+      hi = min(hi, lo + ((1ull << shift) - 1));
+#pragma unroll
+      for (int j = 0; j < PT; ++j)
+        if (amount[j] && word[j] >= lo && word[j] <= hi) {
+          const int i = atomicAdd(&s.n_tied, 1);
+          if (i < TIED) {
+            s.tied[i][0] = word[j];
+            s.tied[i][1] = amount[j];
+          }
+        }
+      __syncthreads();
+      const int ties = s.n_tied;
+      if (ties <= TIED) {
+        if ((int)threadIdx.x < ties) {
+          const ull mine = s.tied[threadIdx.x][0], own = s.tied[threadIdx.x][1];
+          ull a = before;
+          for (int j = 0; j < ties; ++j)
+            if (s.tied[j][0] < mine) a += s.tied[j][1];
+          if (a < need && need <= a + own) {
+            s.word = mine;
+            s.before = a;
+            s.at = own;
+          }
+        }
+        __syncthreads();
+        *ahead = s.before;
+        *at = s.at;
+        const ull r = s.word;
+        __syncthreads();
+        return r;
+      }
+      __syncthreads();
+    }
+  }
+
+  // The token of the n handed to the first CTA at which the amount in order,
+  // `before` ahead of them, reaches `need`; the same cut in every CTA.
+  template <bool MASS>
+  SPEC_DEV void cut_listed(Cut& cut, int n, ull need, ull before) {
+    if (cta == 0) {
+      ull e[PT], w[PT], ahead, at;
+      take_listed<MASS>(n, e, w);
+      // (tokens without weight are not listed: a count that ends among them cuts nothing)
+      const ull word = select(e, w, (ull)s.key_lo << 32, ((ull)s.key_hi << 32) | 0xffffffffu, need, before, &ahead, &at);
+      const Cut found = word == ~0ull ? Cut{0xffffffffu, 0x7fffffff} : Cut{(uint32_t)(word >> 32), (int)(uint32_t)word};
+      if (threadIdx.x < C) *cl.map_shared_rank(&s.cut, threadIdx.x) = found;
+    }
+    cl.sync();
+    cut = s.cut;
+  }
+
+  // The cut behind k tokens, which lies in bin s.lo with s.n_lo ahead of it.
+  SPEC_DEV void cut_count(Cut& cut, int k) {
+    const int bin = s.lo;
+    const ull before = s.n_lo;
     const float lo = (float)bin, hi = bin < BINS - 1 ? (float)(bin + 1) : INFINITY;
-    auto one = [&](int i, float x) {
-      if (keep(i, x)) list(i, x, lo, hi);
-    };
-    scan(one);
+    scan([&](int i, float x) { list(i, x, lo, hi); });
     cl.sync();
     push_list();
     cl.sync();
     const int n = *cl.map_shared_rank(&s.gathered, 0);
     if (n <= FEW) {
-      if (cta == 0) {
-        int n2 = 64;
-        while (n2 < n) n2 <<= 1;
-        for (int i = n + threadIdx.x; i < n2; i += NT) s.sort[i] = ~0ull;
-        __syncthreads();
-        sort(n2);
-        ull w[PT], t = 0;
-#pragma unroll
-        for (int j = 0; j < PT; ++j) {
-          const int i = threadIdx.x * PT + j;
-          w[j] = i >= n ? 0ull : MASS ? weight_once(sc, s.tab, rank_val((uint32_t)(s.sort[i] >> 32)), nullptr) : 1ull;
-          t += w[j];
-        }
-        ull b = before + block_scan(t);
-#pragma unroll
-        for (int j = 0; j < PT; ++j) {
-          if (b < need && need <= b + w[j]) {
-            const ull e = s.sort[threadIdx.x * PT + j];
-            for (int c = 0; c < C; ++c) *cl.map_shared_rank(&s.cut, c) = Cut{(uint32_t)(e >> 32), (int)(uint32_t)e};
-          }
-          b += w[j];
-        }
-        // (tokens at -inf are not listed: a count that ends among them cuts nothing)
-        if (threadIdx.x == NT - 1 && b < need)
-          for (int c = 0; c < C; ++c) *cl.map_shared_rank(&s.cut, c) = Cut{0xffffffffu, 0x7fffffff};
-      }
-      cl.sync();
-      cut = s.cut;
+      cut_listed<false>(cut, n, k, before);
       return;
     }
     cl.sync();
-    const uint32_t key = radix<MASS>(bin, need, before, keep);
-    const ull w = MASS ? weight_once(sc, s.tab, rank_val(key), nullptr) : 1ull;
-    cut_ties(cut, key, (need - s.before + w - 1) / w, s.at / w);
+    const uint32_t key = radix<false>(bin, bin, k, before, [](int, float) { return true; });
+    cut_ties(cut, key, k - s.before, s.at);
   }
 
   // Narrows the cut to the `r` lowest indices among the `n` kept tokens of key.
@@ -847,7 +1013,7 @@ struct Sampler {
     if (r < n) {
       const Cut old = cut;
       auto same = [=](int i, float x) { return rank_key(x) == key && kept(old, key, i) ? 1ull : 0ull; };
-      const Amount<decltype(same)> eq{same};
+      Amount<decltype(same)> eq{same};
       ull before;
       sum(eq, &before);
       cut.idx = find_all(eq, r - 1, before);
@@ -871,25 +1037,83 @@ struct Sampler {
 
   // Lists the tokens of exponents [lo, hi) in bin units.
   SPEC_DEV void list(int i, float x, float lo, float hi) {
-    const float v = sc.m == INFINITY ? (x == INFINITY ? 0.f : INFINITY) : sc.place(x);
-    if (v < hi && v >= lo && *(volatile int*)&s.listed <= LIST) {   // (full: no more of them)
-      const int at = atomicAdd(&s.listed, 1);
-      if (at < LIST) {
-        s.list_key[at] = rank_key(x);
-        s.list_idx[at] = i;
-      }
-    }
+    const float v = sc.place(x);
+    if (v < hi && v >= lo) append(s, i, x);
   }
 
-  // Whether the tokens of the bins before `bins` are few enough to be listed and
-  // sorted by one CTA: fewer than a quarter of the n segment maxima lie there, that
-  // is about 0.3 tokens a segment. (64 rows with top-p: 104 us; trying wherever
-  // they might fit, up to 7 of 8 of the segments, 114 us.)
-  SPEC_DEV bool listable(int bins, int n) {
-    int in = 0;
-    for (int i0 = 0; i0 < n; i0 += NT)
-      in += __syncthreads_count(i0 + (int)threadIdx.x < n && sc.bin(s.seg[min(i0 + (int)threadIdx.x, n - 1)]) < bins);
-    return in < n / 4;
+  // Top-p: the cut at which the tokens inside the present one reach the mass p, in
+  // the bins of find_bins. SUMMED: *kept_mass and *before are sum()'s of the tokens
+  // that the cut and min-p (weights from qw on) keep; DRAWN: a nucleus of few tokens
+  // has been drawn from by draw(their number, the mass).
+  enum Outcome { CUT, SUMMED, DRAWN };
+  template <typename D>
+  SPEC_DEV Outcome cut_mass(Cut& cut, bool cutting, float p, ull qw, D draw, ull* kept_mass, ull* before) {
+    const int lo = s.lo, hi = s.hi;
+    const bool few = s.n_hi <= COUNTED;
+    ull least, most;
+    bounds(lo, least, most);
+    if (!few && qw > most) return CUT;   // min-p keeps fewer
+    Nucleus f{sc, s, cut, cutting, few ? 0.f : (float)lo, end_of(hi + 1), 0ull};
+    sum_part(f);
+    const ull w = warp_sum_u64(f.all);
+    if ((threadIdx.x & 31) == 0) atomicAdd(&s.all, w);
+    push_list();
+    if (threadIdx.x < C) {
+      ull* o = *cl.map_shared_rank(&s.x_bins[cta], threadIdx.x);
+      o[0] = s.total;
+      o[1] = s.all;
+    }
+    cl.sync();
+    ull ahead = 0, all = 0;
+    for (int c = 0; c < C; ++c) {
+      ahead += s.x_bins[c][0];
+      all += s.x_bins[c][1];
+    }
+    const int n = *cl.map_shared_rank(&s.gathered, 0);
+    if (few) {
+      draw(n, all);
+      return DRAWN;
+    }
+    const ull need = top_p_mass(p, all);
+    if (n > FEW) {
+      cl.sync();
+      const Cut old = cut;
+      const uint32_t key = radix<true>(lo, hi, need, ahead, [=](int i, float x) { return kept(old, rank_key(x), i); });
+      const ull v = weight_once(sc, s.tab, rank_val(key), nullptr);
+      cut_ties(cut, key, (need - s.before + v - 1) / v, s.at / v);
+      return CUT;
+    }
+    cut_listed<true>(cut, n, need, ahead);
+    if (lo > 0) {
+      bounds(lo - 1, least, most);
+      if (qw > least) return CUT;   // min-p's end may lie ahead of bin lo
+    }
+    // the sums ahead of bin lo, and the listed tokens that are kept
+    for (int j = threadIdx.x; j < s.listed; j += NT) {
+      const uint32_t key = s.list_key[j];
+      const int i = s.list_idx[j];
+      const ull v = kept(cut, key, i) ? weight_once(sc, s.tab, rank_val(key), nullptr) : 0ull;
+      if (v == 0 || v < qw) continue;
+      const int vec = (i + part.mis) / Part<T>::E, warp = vec / part.per;
+      const int from = warp * part.per, len = min(part.nvec, from + part.per) - from;
+      atomicAdd(&s.chunk[warp - cta * NW][(vec - from) / (32 * chunk_vectors(len))], v);
+    }
+    __syncthreads();
+    const int len = part.v1 - part.v0, lane = threadIdx.x & 31;
+    const ull sum = warp_sum_u64(lane * 32 * chunk_vectors(len) < len ? s.chunk[threadIdx.x >> 5][lane] : 0ull);
+    if (lane == 0) s.wsum[threadIdx.x >> 5] = sum;
+    __syncthreads();
+    ull total = 0;
+#pragma unroll 4
+    for (int i = 0; i < NW; ++i) total += s.wsum[i];
+    *kept_mass = cluster_sum(total, before);
+    return SUMMED;
+  }
+
+  // Where the bins before `bins` end. The last bin holds tokens without weight
+  // where the range was cut: not listed.
+  SPEC_DEV float end_of(int bins) const {
+    return bins < BINS ? (float)bins : range < Z_END ? INFINITY : (float)(BINS - 1);
   }
 
   // Lists the tokens of the first bins in order, below `hi`, and hands them to
@@ -910,30 +1134,12 @@ struct Sampler {
   SPEC_DEV void push_list() {
     const int n = s.listed;
     int* gathered = cl.map_shared_rank(&s.gathered, 0);
-    if (threadIdx.x == 0) s.base = atomicAdd(gathered, n <= LIST ? n : FEW + 1);
+    if (threadIdx.x == 0) s.base = atomicAdd(gathered, n <= FEW ? n : FEW + 1);
     __syncthreads();
     const int base = s.base;
-    if (n > LIST || base + n > FEW) return;
+    if (n > FEW || base + n > FEW) return;
     ull* sort0 = cl.map_shared_rank(s.sort, 0);
     for (int i = threadIdx.x; i < n; i += NT) sort0[base + i] = ((ull)s.list_key[i] << 32) | (unsigned int)s.list_idx[i];
-  }
-
-  // Ascending bitonic sort of s.sort[0, n2), n2 a power of two, at least 64.
-  // A warp's pairs of a stride up to 32 stay inside 64 elements of its own.
-  SPEC_DEV void sort(int n2) {
-    for (int k = 2; k <= n2; k <<= 1)
-      for (int j = k >> 1; j > 0; j >>= 1) {
-        for (int t = threadIdx.x; t < n2 / 2; t += NT) {
-          const int i = 2 * t - (t & (j - 1)), l = i + j;
-          const ull a = s.sort[i], b = s.sort[l];
-          if ((a > b) == ((i & k) == 0)) {
-            s.sort[i] = b;
-            s.sort[l] = a;
-          }
-        }
-        if (j > 32 || (j == 1 && k >= 64)) __syncthreads();
-        else __syncwarp();
-      }
   }
 
   // draw_few for at most COUNTED tokens, which are not sorted: two threads a
@@ -983,74 +1189,38 @@ struct Sampler {
     return s.found;
   }
 
-  // The first CTA's end of the usual case: the n listed tokens sorted by
-  // (key, index), cut, and drawn from in index order. mass: the row's whole
-  // mass (top-p without top-k). Returns the token, *kept_mass its kept mass.
+  // The first CTA's end of the usual case: the n listed tokens, the row's best, are
+  // cut and drawn from in index order. mass: the row's whole mass (top-p without
+  // top-k). Returns the token, *kept_mass its kept mass.
   SPEC_DEV int draw_few(int n, int k, float p, ull qw, float u, ull mass, ull* kept_mass) {
     if (n <= COUNTED) return draw_counted(n, k, p, qw, u, mass, kept_mass);
-    int n2 = 64;
-    while (n2 < n) n2 <<= 1;
-    for (int i = n + threadIdx.x; i < n2; i += NT) s.sort[i] = ~0ull;
-    if (threadIdx.x == 0) s.r = k > 0 ? min(n, k) : n;
-    __syncthreads();
-    sort(n2);
-    // weights of the first r tokens, PT consecutive ones a thread
-    const int r1 = s.r;
-    ull e[PT], w[PT], t = 0;
+    ull e[PT], w[PT], t[PT], ahead, at, last = ~0ull;
+    take_listed<true>(n, e, w);
+    const ull lo = (ull)s.key_lo << 32, hi = ((ull)s.key_hi << 32) | 0xffffffffu;
+    if (k > 0 && k < n) {
 #pragma unroll
-    for (int j = 0; j < PT; ++j) {
-      const int i = threadIdx.x * PT + j;
-      e[j] = i < r1 ? s.sort[i] : 0ull;
-      w[j] = i < r1 ? weight_once(sc, s.tab, rank_val((uint32_t)(e[j] >> 32)), nullptr) : 0ull;
-      t += w[j];
+      for (int j = 0; j < PT; ++j) t[j] = e[j] != ~0ull;
+      last = select(e, t, lo, hi, k, 0ull, &ahead, &at);
     }
-    const ull b0 = block_scan(t);
-    if (threadIdx.x == NT - 1) s.total = b0 + t;
-    __syncthreads();
-    int r = r1;
-    if (p < 1.f) {
-      const ull need = top_p_mass(p, k > 0 ? s.total : mass);
-      ull b = b0;
+    auto keep = [&](ull least) {   // in t, of weight `least` at least; returns their mass
+      ull sum = 0;
 #pragma unroll
-      for (int j = 0; j < PT; ++j) {  // the token at which the mass reaches need is the last kept
-        if (b < need && need <= b + w[j]) s.r = threadIdx.x * PT + j + 1;
-        b += w[j];
+      for (int j = 0; j < PT; ++j) {
+        t[j] = e[j] <= last && w[j] >= least ? w[j] : 0ull;
+        sum += t[j];
       }
-      __syncthreads();
-      r = s.r;
+      block_total(sum);
+      return s.total;
+    };
+    if (p < 1.f) {
+      const ull z = keep(0ull);
+      last = select(e, t, lo, hi, top_p_mass(p, k > 0 ? z : mass), 0ull, &ahead, &at);
     }
-    ull z = 0;
+    const ull z = keep(qw);
+    *kept_mass = z;
 #pragma unroll
-    for (int j = 0; j < PT; ++j) {
-      const int i = threadIdx.x * PT + j;
-      if (i >= r || w[j] < qw) w[j] = 0ull;
-      z += w[j];
-      // index and weight in one word; tokens not kept go behind
-      if (i < n2) s.sort[i] = w[j] ? ((e[j] & 0xffffffffull) << (64 - IDX_BITS)) | w[j] : ~0ull;
-    }
-    const ull zb = block_scan(z);
-    if (threadIdx.x == NT - 1) s.total = zb + z;
-    __syncthreads();
-    *kept_mass = s.total;
-    const ull d = drawn_mass(u, s.total);
-    while (n2 > 64 && n2 / 2 >= r) n2 >>= 1;
-    sort(n2);
-    t = 0;
-#pragma unroll
-    for (int j = 0; j < PT; ++j) {
-      const int i = threadIdx.x * PT + j;
-      e[j] = i < n2 ? s.sort[i] : ~0ull;
-      w[j] = e[j] == ~0ull ? 0ull : e[j] & ((1ull << (64 - IDX_BITS)) - 1);
-      t += w[j];
-    }
-    ull b = block_scan(t);
-#pragma unroll
-    for (int j = 0; j < PT; ++j) {
-      if (d >= b && d < b + w[j]) s.found = (int)(e[j] >> (64 - IDX_BITS));
-      b += w[j];
-    }
-    __syncthreads();
-    return s.found;
+    for (int j = 0; j < PT; ++j) e[j] = (uint32_t)e[j];
+    return (int)select(e, t, 0ull, (ull)(part.V - 1), drawn_mass(u, z) + 1, 0ull, &ahead, &at);
   }
 };
 
@@ -1339,7 +1509,7 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SampleArgs a) {
   });
   ull best = bi >= 0 ? pack_best(bx + 0.f, (uint32_t)bi) : 0ull;
   cl.barrier_wait(std::move(started));
-  if (cuts && !greedy) {
+  if (k > 0 && !greedy) {   // (top-k alone looks at them)
 #pragma unroll
     for (int o = 1; o < 8; o <<= 1) {
       const float v = __shfl_xor_sync(FULL, bx, o);
@@ -1400,6 +1570,7 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SampleArgs a) {
   scale_of(temp, sh, sl);
   // finer bins where the row's range of exponents is less than the weights'
   const float range = fminf((m - low) * sh, Z_END);
+  S.range = range;
   S.sc = Scale{m, sh, sl, range > 1e-30f ? (float)(BINS - 1) / range : 0.f};
   // min-p's smallest weight
   const ull qw = q > 0.f ? (q < 1.f ? scaled(q, 1ull << WBITS, true) : 1ull << WBITS) : 0ull;
@@ -1410,57 +1581,42 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SampleArgs a) {
   };
 
   if (!cuts) {
-    const Mass mass{S.sc, s.tab, qw, Cut{}, false};
-    S.sum_part(mass);
-    if (threadIdx.x < C) *cl.map_shared_rank(&s.x_total[cta], threadIdx.x) = s.total;
-    cl.sync();
-    ull z = 0, before = 0;
-#pragma unroll
-    for (int c = 0; c < MAX_C; ++c) {
-      if (c == cta) before = z;
-      if (c < C) z += s.x_total[c];
-    }
+    Mass mass{S.sc, s.tab, qw, Cut{}, false};
+    ull before;
+    const ull z = S.sum(mass, &before);
     S.find_in_order(mass, drawn_mass(u, z), before, [&](int i, float x) { result(i, x, z); });
     return;
   }
 
-  // the tokens that may be kept, listed for the first CTA
-  // the last bin holds tokens without weight where the range was cut: not listed
-  auto end_of = [&](int bins) { return bins < BINS ? (float)bins : range < Z_END ? INFINITY : (float)(BINS - 1); };
   // the first CTA draws among the n tokens handed to it, if they fit
-  auto draw = [&](int n, ull all) {
+  auto draw = [&](int n, ull mass) {
     if (n <= FEW && cta == 0) {
       ull z;
-      const int token = S.draw_few(n, k, p, qw, u, all, &z);
+      const int token = S.draw_few(n, k, p, qw, u, mass, &z);
       if (threadIdx.x == 0) result(token, Part<T>::one((const T*)a.logits + (size_t)row * a.ld + token), z);
     }
     cl.sync();   // its count is read, and its tokens are, before either changes
     return n <= FEW;
   };
-  auto every = [](int, float) { return true; };
-  auto k_of = [&](ull) { return (ull)k; };
-  auto p_of = [&](ull z) { return top_p_mass(p, z); };
   Cut cut{0xffffffffu, 0x7fffffff};
-  ull need, before;
-  const int segs = C * NT / seg_lanes;
+  ull z = 0, before = 0;
+  bool summed = false;
   if (k > 0) {
-    if (k <= segs && draw(S.list_below(end_of((S.threshold(k, segs) + 1) * (BINS / SEG_BINS))), 0ull)) return;
-    S.template find_bin<false>(every, k_of, &need);
-    S.template cut_in_bin<false>(cut, need, every);
+    const int segs = C * NT / seg_lanes;
+    if (k <= segs && draw(S.list_below(S.end_of((S.threshold(k, segs) + 1) * (BINS / SEG_BINS))), 0ull)) return;
+    S.find_bins(cut, false, k, 1.f);
+    S.cut_count(cut, k);
+    k = 0;   // (the cut holds it)
   }
   if (p < 1.f) {
-    if (k == 0) {
-      const ull all = S.template find_bin<true>(every, p_of, &need);
-      if (S.listable(s.bin + 1, segs) && draw(S.list_below(end_of(s.bin + 1)), all)) return;
-      S.template cut_in_bin<true>(cut, need, every);
-    } else {
-      auto in = [&](int i, float x) { return kept(cut, rank_key(x), i); };
-      S.template find_bin<true>(in, p_of, &need);
-      S.template cut_in_bin<true>(cut, need, in);
-    }
+    const bool cutting = cut.idx != 0x7fffffff || cut.key != 0xffffffffu;
+    S.find_bins(cut, cutting, 0, p);
+    const auto outcome = S.cut_mass(cut, cutting, p, qw, draw, &z, &before);
+    if (outcome == Sampler<T>::DRAWN) return;
+    summed = outcome == Sampler<T>::SUMMED;
   }
-  const Mass mass{S.sc, s.tab, qw, cut, true};
-  const ull z = S.sum(mass, &before);
+  Mass mass{S.sc, s.tab, qw, cut, true};
+  if (!summed) z = S.sum(mass, &before);
   S.find_in_order(mass, drawn_mass(u, z), before, [&](int i, float x) { result(i, x, z); });
 }
 
@@ -1536,28 +1692,24 @@ int max_clusters(int dev, int C) {
 }
 
 // CTAs a row: the count with the least estimated time, waves of resident
-// clusters at a fixed cost of about 8 us (0.1 more a CTA of the exchanges) and
-// 0.17 ns a token of a CTA, twice that where two CTAs share an SM. 262144
-// tokens, measured: 1 row with top-k and top-p 13 us with 16 CTAs, 15 with 8, 58
-// with 1; 40 rows at temperature only 42 us with 6 (one wave), 51 with 8, 58 with
-// 16. Rows with filters differ in length (a broad nucleus takes up to four
-// scans), so they are spread over 8 CTAs at least where a CTA keeps 4096 tokens:
-// 64 rows with top-p 128 us with 8, 143 with 6, 164 with 4.
+// clusters at a fixed cost of about 9 us (0.2 more a CTA of the exchanges) and
+// 0.25 ns a token of a CTA, up to 0.5 ns as the SMs hold two CTAs each. Measured,
+// 262144 tokens a row: 1 row with top-k 50 13 us with 16 CTAs, 15 with 8, 60 with
+// 1; 64 rows with top-k 50 32 us with 4 CTAs, 46 with 2, 39 with 8, with top-p of
+// mixed breadth 93, 114 (3), 100.
 template <typename T>
-int cluster_size(int M, int V, bool filters) {
+int cluster_size(int M, int V) {
   int best = MAX_C, dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= MAX_DEVICES) dev = 0;
   const int sms = num_sms();
   double least = 1e30;
-  for (int C : {1, 2, 3, 4, 5, 6, 7, 8, 12, 16}) {
-    if (V / C > DIGIT_TOKENS || (filters && C < std::min(8, V / 4096))) continue;
+  for (int C : {1, 2, 3, 4, 6, 8, 16}) {
     const int fit = max_clusters<T>(dev, C);
     if (fit < 1) continue;
     double us = 0;
     for (int left = M; left > 0; left -= fit) {
-      const int rows = std::min(left, fit);
-      const int share = (rows * C + sms - 1) / sms;
-      const double wave = 8.0 + 0.1 * C + 0.17e-3 * share * V / C;
+      const double held = (double)std::min(left, fit) * C / sms;
+      const double wave = 9.0 + 0.2 * C + (0.25 + 0.12 * held) * 1e-3 * V / C;
       if (left > 8 * fit) {  // many waves: all but the last few at once
         const int n = left / fit - 4;
         us += n * wave;
@@ -1600,7 +1752,7 @@ int launch_chunked(const SampleArgs& a, int pdl, cudaStream_t st) {
 template <typename T>
 int launch_sample(const SampleArgs& a, int pdl, cudaStream_t st) {
   if (chunked(a.M, a.V) && !a.top_k && !a.top_p && !a.min_p) return launch_chunked<T>(a, pdl, st);
-  const int C = cluster_size<T>(a.M, a.V, a.top_k || a.top_p);
+  const int C = cluster_size<T>(a.M, a.V);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)a.M * C);
   cfg.blockDim = dim3(NT);

@@ -61,6 +61,58 @@ def test_sample_matches_reference(dtype, V, name):
     _check(x, binding.spec_sample(x, u, T, k, p, q), u, T, k, p, q)
 
 
+# Top-p's cut found in a few bins: nuclei from a token to most of the row, values so
+# coarse that thousands of tokens share one, and min-p's end around top-p's.
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V", [2500, 32003, 262144])
+@pytest.mark.parametrize("kind", ["smooth", "coarse", "halves", "equal", "masked", "inf", "huge"])
+def test_nuclei(dtype, V, kind):
+    M = 12
+    g = _gen(V + len(kind))
+    x = torch.randn((M, V), generator=g, device="cuda") * 2.5
+    if kind == "coarse":
+        x = (x * 2).round() / 2
+    elif kind == "halves":
+        x = (x > 0).float() * 1.5
+    elif kind == "equal":
+        x.fill_(3.25)
+    elif kind == "masked":
+        x[torch.rand((M, V), generator=g, device="cuda") < 0.97] = -float("inf")
+        x[:, V // 2] = 1.0
+    elif kind == "inf":
+        x[torch.rand((M, V), generator=g, device="cuda") < 0.3] = float("inf")
+        x[:, V // 2] = float("inf")
+    elif kind == "huge":
+        x = x * 1e37
+    x = x.to(dtype)
+    u = torch.rand(M, generator=g, device="cuda")
+    T = torch.linspace(0.4, 3.0, M, device="cuda")
+    if kind == "huge":
+        T = T * 1e37
+    p = torch.tensor([0.9, 0.5, 0.05, 0.99, 0.9999, 0.7, 0.2, 0.95, 0.999, 0.31, 0.83, 0.61], device="cuda")
+    _check(x, binding.spec_sample(x, u, T, None, p), u, T, None, p, most_undecided=0.1)
+    q = torch.tensor([0.5, 0.3, 0.9, 1e-4, 1e-9, 0.1, 0.03, 0.01, 0.003, 0.6, 0.2, 0.05], device="cuda")
+    _check(x, binding.spec_sample(x, u, T, None, p, q), u, T, None, p, q, most_undecided=0.1)
+    k = torch.randint(1, V, (M,), generator=g, device="cuda").int()
+    _check(x, binding.spec_sample(x, u, T, k, p, q), u, T, k, p, q, most_undecided=0.1)
+    _check(x, binding.spec_sample(x, u, T, k, p), u, T, k, p, most_undecided=0.1)
+    _check(x, binding.spec_sample(x, u, T, k), u, T, k, most_undecided=0.1)
+
+
+# min-p's end moved across the bins in which top-p's cut lies
+def test_min_p_around_the_nucleus():
+    V, M = 100003, 96
+    g = _gen(5)
+    x = (torch.randn((1, V), generator=g, device="cuda") * 2.5).expand(M, V)
+    u = torch.rand(M, generator=g, device="cuda")
+    T, p = _vec(1.0, M), _vec(0.8, M)
+    w = torch.sort(torch.exp((x[0] - x[0].max()).double()), descending=True).values
+    at = w[int((torch.cumsum(w, 0) < 0.8 * w.sum()).sum())].item()   # the weight of the last token of the nucleus
+    q = (at * torch.exp(torch.linspace(-0.08, 0.08, M, dtype=torch.float64))).float().cuda()
+    x = x.contiguous()
+    _check(x, binding.spec_sample(x, u, T, None, p, q), u, T, None, p, q)
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("V,ld,off", [(1000, 1003, 0), (4097, 4097, 1), (32003, 32010, 3), (50001, 50001, 7)])
 def test_strided_and_unaligned_rows(dtype, V, ld, off):
