@@ -23,7 +23,8 @@
 // the adapters' (counted on the device from the ids, by every CTA alike). A tile
 // cut between CTAs is summed by the last CTA to arrive, in CTA order. So a row's
 // result depends on neither timing, nor the other rows, nor their adapters (whose
-// chunks add exact zeros).
+// chunks add exact zeros; where one holds infinities or NaN, the elements of the
+// other rows that meet them are summed again, one by one).
 //
 // What bounds it: HBM from about 80 MB of weights on (49152 x 6144, 40 rows, 8
 // adapters of rank 16: 112 us, 5.6 TB/s; 262144 x 2560, rank 64: 262 us, 6.1 TB/s,
@@ -296,7 +297,40 @@ struct GemmArgs {
   float* fix;             // [grid][2][tile rows / TM][MP][TM]
   unsigned int* cnt;      // [T]
   int* err;
+  // for the elements that are summed again
+  const __nv_bfloat16 *w, *b;   // [N][K], [n_adapters][N][rank]
+  const uint16_t* planes;       // [3][MP][KT], the adapters' columns from Kp on
+  int KT, Kp;
 };
+
+// The elements of weight rows n, n + TM, ... that are NaN, each by itself: W's part
+// and that of the row's own adapter, in the activations' values (a plane of an
+// infinity has NaN behind it).
+template <int MP>
+__device__ __noinline__ void mend(const GemmArgs& a, const Slots& sl, const float* rms_s, int n0, int n1) {
+  const size_t plane = (size_t)MP * a.KT;
+  for (int i = 0; i < a.M * 2; ++i) {
+    const int m = i >> 1, n = n0 + (i & 1) * TM, slot = sl.slot[m];
+    if (n >= n1) continue;
+    float* y = a.y + (size_t)m * a.N + n;
+    if (*(volatile float*)y == *(volatile float*)y) continue;
+    const uint16_t* x = a.planes + (size_t)m * a.KT;
+    auto val = [](uint16_t u) { return __bfloat162float(__ushort_as_bfloat16(u)); };
+    auto dot = [&](const __nv_bfloat16* w, int at, int cols) {
+      double sum = 0.0;
+      for (int c = 0; c < cols; ++c) {
+        const uint16_t* q = x + at + c;
+        const float h = val(q[0]);
+        sum += (double)__bfloat162float(w[c]) * (isfinite(h) ? h + (val(q[plane]) + val(q[2 * plane])) : h);
+      }
+      return sum;
+    };
+    double sum = dot(a.w + (size_t)n * a.K, 0, a.K);
+    if (slot >= 0)
+      sum += dot(a.b + ((size_t)sl.used[slot] * a.N + n) * a.rank, a.Kp + slot * ((a.rank + KC - 1) / KC * KC), a.rank);
+    *y = (float)sum * rms_s[m];
+  }
+}
 
 // MMA N: the three planes of MP rows.
 constexpr int mma_n(int MP) { return (3 * MP + 15) / 16 * 16; }
@@ -458,14 +492,21 @@ struct Gemm {
   // thread = output row n of the tile's parts, lane by lane: a warp's stores of
   // an activation row are consecutive
   SPEC_DEV void finish(int t, int r, const float (&v)[NS][MP]) const {
+    int nan = 0;
 #pragma unroll
     for (int h = 0; h < NS; ++h) {
       const int n = t * ROWS_T + h * TM + r;
       if (n >= a.N) break;
 #pragma unroll
       for (int m = 0; m < MP; ++m)
-        if (m < a.M) a.y[(size_t)m * a.N + n] = v[h][m] * rms_s[m];
+        if (m < a.M) {
+          a.y[(size_t)m * a.N + n] = v[h][m] * rms_s[m];
+          nan |= v[h][m] != v[h][m];
+        }
     }
+    // A NaN may come from another row's adapter (its infinities and NaN meet this
+    // row's zeros), or stand for an infinity: these elements are summed again.
+    if (nan) mend<MP>(a, sl, rms_s, t * ROWS_T + r, min(a.N, (t + 1) * ROWS_T));
   }
 
   SPEC_DEV float* slot(int b, int t) const {
@@ -742,6 +783,7 @@ int lora_gemm(LoraArgs a, const void* w, void* ws, cudaStream_t st) {
   g.ids = a.ids; g.norm = a.gain != nullptr; g.eps = a.eps;
   g.rms = (const float*)(base + s.rms); g.y = a.y; g.fix = (float*)(base + s.fix);
   g.cnt = (unsigned int*)(base + s.cnt); g.err = a.err;
+  g.w = (const __nv_bfloat16*)w; g.b = (const __nv_bfloat16*)a.b; g.planes = planes; g.KT = KT; g.Kp = Kp;
   a.cnt = g.cnt;
   a.n_cnt = g.T;
   CUtensorMap tmw, tmb, tmx;

@@ -1488,7 +1488,7 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SampleArgs a) {
   int k = a.top_k ? a.top_k[row] : 0;
   if (k >= a.V) k = 0;
   const float p = a.top_p ? a.top_p[row] : 1.f;
-  const float q = a.min_p ? fminf(a.min_p[row], 1.f) : 0.f;
+  const float q = a.min_p ? a.min_p[row] : 0.f;
   const float u = a.uniform[row];
   S.part.bind((const T*)a.logits + (size_t)row * a.ld, a.V, cta, C);
   const bool greedy = temp < 1e-5f, cuts = k > 0 || p < 1.f;

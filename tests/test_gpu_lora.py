@@ -174,6 +174,28 @@ def test_infinities_stay_in_their_rows():
     assert torch.equal(z[0], y[0]) and torch.equal(z[3], y[3]) and torch.isnan(z[1]).all()
 
 
+# An adapter with infinities and NaN is its own rows' trouble.
+@pytest.mark.parametrize("dtype,adt", [(configs.BF16, torch.bfloat16), (configs.Q4_0, torch.bfloat16),
+                                       (configs.BF16, torch.float32)])
+@pytest.mark.parametrize("M,N,K,r", [(7, 300, 256, 16), (40, 1001, 1536, 72), (20, 130, 24576, 8)])
+def test_a_broken_adapter_stays_in_its_rows(dtype, adt, M, N, K, r):
+    g = _gen(N)
+    w = synth.make_matrix(g, dtype, 1, N, K, 0.02, "cuda")
+    lora = _adapters(g, 3, r, N, K, adt)
+    ids = torch.arange(M, device="cuda", dtype=torch.int32) % 4 - 1
+    x = torch.randn((M, K), generator=g, device="cuda")
+    want = _base(w, x, None) + _delta(x, lora, ids, None)[0]
+    lora.b[1, ::2, 0] = float("nan")
+    lora.b[1, 1::3, r - 1] = float("inf")
+    lora.a[2, r // 2, K // 2] = float("-inf")
+    y = binding.spec_linear_lora(w, x, lora, ids).cpu().numpy()
+    rows = (ids.cpu().numpy() < 1)
+    assert_rows_close(y[rows], want[rows], KTOL, "rows of sound adapters")
+    one = y[ids.cpu().numpy() == 1]
+    assert np.isnan(one[:, ::2]).all() and np.isfinite(np.delete(one, np.r_[0:N:2, 1:N:3], 1)).all()
+    assert not np.isfinite(y[ids.cpu().numpy() == 2]).any()
+
+
 def test_other_stream_captured_graph_and_layers():
     g = _gen(6)
     N, K, M = 1536, 512, 20

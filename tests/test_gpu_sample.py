@@ -229,6 +229,19 @@ def test_settings_out_of_range():
     _check(x[6:7], (tok[6:7], prob[6:7]), torch.tensor([1.0]), T[6:7], None, p[6:7])
 
 
+@pytest.mark.parametrize("V", [100, 262144])
+def test_min_p_out_of_range_is_off(V):
+    x = torch.randn((4, V), generator=_gen(3), device="cuda") * 2.5
+    q = torch.tensor([float("nan"), -0.5, 0.0, -float("inf")], device="cuda")
+    u = torch.rand(4, generator=_gen(4), device="cuda")
+    plain, got = binding.spec_sample(x, u), binding.spec_sample(x, u, None, None, None, q)
+    _check(x, got, u)
+    assert torch.equal(plain[0], got[0])
+    one = binding.spec_sample(x, u, None, None, None, torch.full((4,), 7.0, device="cuda"))
+    assert torch.equal(one[0].long(), x.argmax(1)) and one[1].tolist() == [1.0] * 4   # at most 1
+
+
+
 def test_a_row_depends_on_nothing_else():
     """Bit-identical tokens and probabilities alone, in a batch, at another
     alignment, and from run to run."""
