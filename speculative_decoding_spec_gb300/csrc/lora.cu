@@ -9,8 +9,10 @@
 // makes one trip less than with the adapters added behind the projection, and
 // each kernel of the chain starts while the one before it runs. (Rows of y that
 // do not start on 16 bytes, N % 4 != 0, take the other order: the residual-add
-// epilogue prefetches y in 16-byte pieces.) Bound by the launches' latency:
-// Q4_0 12288 x 1536, 20 rows, 4 adapters of rank 32.
+// epilogue prefetches y in 16-byte pieces.) Bound by the Q4_0 projection: 12288 x
+// 1536, 20 rows, 4 adapters of rank 32 31 us, 25 of them the projection's kernel.
+#include <algorithm>
+
 #include "common.cuh"
 
 namespace spec {
@@ -97,26 +99,27 @@ __global__ void __launch_bounds__(SHRINK_THR) shrink_kernel(LoraArgs a) {
   }
 }
 
-// y[m][n] (= or +=) B_a[n] . t[m]: a thread a column, the rows of t in shared
+// y[m][n] (= or +=) B_a[n] . t[m]: a thread a column, `rows` rows of t in shared
 // memory. Up to HELD ranks of B stay in registers over the rows of a request.
 template <typename T>
-__global__ void __launch_bounds__(EXPAND_THR) expand_kernel(LoraArgs a) {
+__global__ void __launch_bounds__(EXPAND_THR) expand_kernel(LoraArgs a, int rows) {
   extern __shared__ __align__(16) float ts[];
   __shared__ int ids[64];
   grid_dep_launch();
-  if (threadIdx.x < a.M) {   // (the call's input: complete before the shrink)
-    const int id = a.ids[threadIdx.x];
+  const int m0 = blockIdx.y * rows, nr = min(rows, a.M - m0);
+  if (threadIdx.x < nr) {   // (the call's input: complete before the shrink)
+    const int id = a.ids[m0 + threadIdx.x];
     ids[threadIdx.x] = id < 0 || id >= a.n_adapters ? -1 : id;
   }
   grid_dep_wait();
-  for (int i = threadIdx.x * 4; i < a.M * a.rank; i += blockDim.x * 4)
-    *reinterpret_cast<float4*>(ts + i) = __ldcg(reinterpret_cast<const float4*>(a.t + i));
+  for (int i = threadIdx.x * 4; i < nr * a.rank; i += blockDim.x * 4)
+    *reinterpret_cast<float4*>(ts + i) = __ldcg(reinterpret_cast<const float4*>(a.t + (size_t)m0 * a.rank + i));
   __syncthreads();
   const int n = blockIdx.x * blockDim.x + threadIdx.x;
   if (n >= a.N) return;
   float w[HELD / 8][8];
   int held = -1;
-  for (int m = 0; m < a.M; ++m) {
+  for (int m = 0; m < nr; ++m) {
     const int id = ids[m];
     if (id < 0 && a.add) continue;
     float acc = 0.f;
@@ -144,7 +147,7 @@ __global__ void __launch_bounds__(EXPAND_THR) expand_kernel(LoraArgs a) {
         }
       }
     }
-    float* y = a.y + (size_t)m * a.N + n;
+    float* y = a.y + (size_t)(m0 + m) * a.N + n;
     *y = a.add ? *y + acc : acc;
   }
 }
@@ -158,16 +161,20 @@ int shrink(const LoraArgs& a, cudaStream_t st) {
 template <typename T>
 int expand(const LoraArgs& a, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((a.N + EXPAND_THR - 1) / EXPAND_THR);
+  // rows of a block: all, where the columns alone give every SM four blocks, else
+  // fewer (12288 columns, 20 rows of 4 adapters: 4.0 us, 7 with all rows a block)
+  const int cols = (a.N + EXPAND_THR - 1) / EXPAND_THR;
+  const int rows = std::min(a.M, std::max(1, (int)((long long)a.M * cols / (4 * num_sms()))));
+  cfg.gridDim = dim3(cols, (a.M + rows - 1) / rows);
   cfg.blockDim = dim3(EXPAND_THR);
-  cfg.dynamicSmemBytes = (size_t)a.M * a.rank * sizeof(float);
+  cfg.dynamicSmemBytes = (size_t)rows * a.rank * sizeof(float);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = a.add ? 0 : 1;   // behind the projection: an ordinary launch
-  return cudaLaunchKernelEx(&cfg, expand_kernel<T>, a) == cudaSuccess ? 1 : -1;
+  return cudaLaunchKernelEx(&cfg, expand_kernel<T>, a, rows) == cudaSuccess ? 1 : -1;
 }
 
 }  // namespace

@@ -29,7 +29,7 @@
 // What bounds it: HBM from about 80 MB of weights on (49152 x 6144, 40 rows, 8
 // adapters of rank 16: 112 us, 5.6 TB/s; 262144 x 2560, rank 64: 262 us, 6.1 TB/s,
 // measured copy 6.8); below that the chain of preparation, stream, split tiles'
-// sums (2560 x 1536: 21 us, 0.4 TB/s).
+// sums (2560 x 1536, 4 rows: 17 us, 0.5 TB/s).
 //
 // Roles of a CTA's 6 warps, one CTA an SM: TMA producer (warp 0, one thread; a
 // ring of stages of a weight tile's 64 columns and the activations', both in the
@@ -117,15 +117,18 @@ SPEC_DEV void split3(float v, uint16_t (&o)[3]) {
 }
 
 // Blocks (m, y): y below the row's column blocks writes the planes of 1024
-// columns of row m and their sum of squares; the others take 8 ranks each of
-// row m's shrink, all warps together along K, and write its planes' adapter
-// columns. Rows that share an adapter read it from L2.
+// columns of row m and their sum of squares; the others take RB ranks each of
+// row m's shrink, all warps together along K, two steps of loads in flight, and
+// write its planes' adapter columns. Rows that share an adapter read it from L2.
+// (A latency chain beside the weight stream's start: 40 rows, K = 6144, rank 16
+// 5.7 us; 8 ranks a block and one step in flight 8.1 us.)
 constexpr int PREP_THR = 256;
+constexpr int RB = 4;
 __global__ void __launch_bounds__(PREP_THR) lora_prep_kernel(LoraArgs a, int col_blocks, int MP, int Kp, int KT,
                                                              uint16_t* planes, float* rms) {
   __shared__ Slots sl;
   __shared__ float red[32];
-  __shared__ float sums[PREP_THR / 32][8];
+  __shared__ float sums[PREP_THR / 32][RB];
   grid_dep_launch();   // the projection starts on its weights
   const int m = blockIdx.x, y = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const size_t plane = (size_t)MP * KT;
@@ -163,38 +166,52 @@ __global__ void __launch_bounds__(PREP_THR) lora_prep_kernel(LoraArgs a, int col
     }
     return;
   }
-  const int r0 = (y - col_blocks) * 8, rc = (a.rank + KC - 1) / KC, id = a.ids[m];
+  const int r0 = (y - col_blocks) * RB, rc = (a.rank + KC - 1) / KC, id = a.ids[m];
   const bool has = id >= 0 && id < a.n_adapters;
   if (has) {
     const __nv_bfloat16* A = (const __nv_bfloat16*)a.a + ((size_t)id * a.rank + r0) * a.K;
-    float acc[8];
+    float acc[RB];
 #pragma unroll
-    for (int r = 0; r < 8; ++r) acc[r] = 0.f;
-    for (int c = threadIdx.x * 8; c < a.K; c += PREP_THR * 8) {
-      uint4 w[8];
+    for (int r = 0; r < RB; ++r) acc[r] = 0.f;
+    constexpr int STEP = PREP_THR * 8;
+    for (int c0 = threadIdx.x * 8; c0 < a.K; c0 += 2 * STEP) {
+      uint4 w[2][RB];
+      float4 u[2][2], g[2][2];
 #pragma unroll
-      for (int r = 0; r < 8; ++r) w[r] = *reinterpret_cast<const uint4*>(A + (size_t)r * a.K + c);
-      const float4 u0 = *reinterpret_cast<const float4*>(x + c), u1 = *reinterpret_cast<const float4*>(x + c + 4);
-      float v[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
-      if (a.gain) {
-        const float4 g0 = *reinterpret_cast<const float4*>(a.gain + c), g1 = *reinterpret_cast<const float4*>(a.gain + c + 4);
-        v[0] *= g0.x; v[1] *= g0.y; v[2] *= g0.z; v[3] *= g0.w;
-        v[4] *= g1.x; v[5] *= g1.y; v[6] *= g1.z; v[7] *= g1.w;
+      for (int i = 0; i < 2; ++i) {
+        const int c = c0 + i * STEP;
+        if (c >= a.K) break;
+#pragma unroll
+        for (int r = 0; r < RB; ++r) w[i][r] = *reinterpret_cast<const uint4*>(A + (size_t)r * a.K + c);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          u[i][j] = *reinterpret_cast<const float4*>(x + c + 4 * j);
+          if (a.gain) g[i][j] = *reinterpret_cast<const float4*>(a.gain + c + 4 * j);
+        }
       }
 #pragma unroll
-      for (int r = 0; r < 8; ++r) {
-        const uint32_t b[4] = {w[r].x, w[r].y, w[r].z, w[r].w};
+      for (int i = 0; i < 2; ++i) {
+        if (c0 + i * STEP >= a.K) break;
+        float v[8] = {u[i][0].x, u[i][0].y, u[i][0].z, u[i][0].w, u[i][1].x, u[i][1].y, u[i][1].z, u[i][1].w};
+        if (a.gain) {
+          v[0] *= g[i][0].x; v[1] *= g[i][0].y; v[2] *= g[i][0].z; v[3] *= g[i][0].w;
+          v[4] *= g[i][1].x; v[5] *= g[i][1].y; v[6] *= g[i][1].z; v[7] *= g[i][1].w;
+        }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[r] = fmaf(bf16lo(b[i]), v[2 * i], fmaf(bf16hi(b[i]), v[2 * i + 1], acc[r]));
+        for (int r = 0; r < RB; ++r) {
+          const uint32_t b[4] = {w[i][r].x, w[i][r].y, w[i][r].z, w[i][r].w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[r] = fmaf(bf16lo(b[j]), v[2 * j], fmaf(bf16hi(b[j]), v[2 * j + 1], acc[r]));
+        }
       }
     }
 #pragma unroll
-    for (int r = 0; r < 8; ++r) acc[r] = warp_sum(acc[r]);
+    for (int r = 0; r < RB; ++r) acc[r] = warp_sum(acc[r]);
     if (lane == 0)
 #pragma unroll
-      for (int r = 0; r < 8; ++r) sums[warp][r] = acc[r];
+      for (int r = 0; r < RB; ++r) sums[warp][r] = acc[r];
     __syncthreads();
-    if (threadIdx.x < 8) {
+    if (threadIdx.x < RB) {
       float t = 0.f;
       for (int w = 0; w < PREP_THR / 32; ++w) t += sums[w][threadIdx.x];
       red[threadIdx.x] = t * (a.scale ? a.scale[id] : 1.f);
@@ -202,20 +219,20 @@ __global__ void __launch_bounds__(PREP_THR) lora_prep_kernel(LoraArgs a, int col
   }
   find_slots(sl, a.ids, a.M, a.n_adapters);
   const int mine = sl.slot[m];
-  // eight columns of every adapter in use: t in this row's, zero in the others;
-  // the last block also clears the columns up to a whole k-step
-  const int width = r0 + 8 >= a.rank && (a.rank & 15) ? 16 : 8;
-  for (int i = threadIdx.x; i < sl.n * 3 * (width / 8); i += blockDim.x) {
-    const int part = i % (width / 8), p = i / (width / 8) % 3, s = i / (width / 8) / 3;
-    uint32_t q[4] = {0, 0, 0, 0};
+  // RB columns of every adapter in use: t in this row's, zero in the others; the
+  // last block also clears the columns up to a whole k-step
+  const int width = r0 + RB >= a.rank && (a.rank & 15) ? 1 + 8 / RB : 1;
+  for (int i = threadIdx.x; i < sl.n * 3 * width; i += blockDim.x) {
+    const int part = i % width, p = i / width % 3, s = i / width / 3;
+    uint32_t q[RB / 2] = {};
     if (s == mine && part == 0)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
+      for (int j = 0; j < RB; ++j) {
         uint16_t o[3];
         split3(red[j], o);
         q[j >> 1] |= (uint32_t)(p == 0 ? o[0] : p == 1 ? o[1] : o[2]) << (16 * (j & 1));
       }
-    *reinterpret_cast<uint4*>(out + p * plane + Kp + s * rc * KC + r0 + part * 8) = make_uint4(q[0], q[1], q[2], q[3]);
+    *reinterpret_cast<uint2*>(out + p * plane + Kp + s * rc * KC + r0 + part * RB) = make_uint2(q[0], q[1]);
   }
 }
 
@@ -792,7 +809,7 @@ int lora_gemm(LoraArgs a, const void* w, void* ws, cudaStream_t st) {
       !encode(&tmx, planes, KT, mma_n(MP), mma_n(MP)))
     return -1;
   const int col_blocks = (a.K + PREP_COLS - 1) / PREP_COLS;
-  lora_prep_kernel<<<dim3(a.M, col_blocks + a.rank / 8), PREP_THR, 0, st>>>(a, col_blocks, MP, Kp, KT, planes, (float*)(base + s.rms));
+  lora_prep_kernel<<<dim3(a.M, col_blocks + a.rank / RB), PREP_THR, 0, st>>>(a, col_blocks, MP, Kp, KT, planes, (float*)(base + s.rms));
   if (cudaGetLastError() != cudaSuccess) return -1;
   cudaError_t e;
   switch (MP) {
