@@ -126,9 +126,8 @@ struct Shared {
   int list_idx[FEW];
   int listed;                // tokens this CTA listed (more than FEW: they did not fit)
   // pushed by every CTA of the cluster
-  ull x_best[MAX_C];         // packed maximum
+  uint32_t x_best[MAX_C];    // key of the maximum, 0: nothing above -inf
   float x_low[MAX_C];        // minimum
-  int x_nan[MAX_C];
   ull x_total[MAX_C];        // sum of the weights
   union {
     float seg[SEG_MAX];      // segment maxima
@@ -148,7 +147,7 @@ struct Shared {
   ull before, at;            // amount before it, and in it
   ull x_bins[MAX_C][3];      // pushed: counts, least and largest mass of a share of the bins
   ull scan[NW][3];
-  ull all;                   // this CTA's mass
+  ull all;                   // this CTA's mass from bin lo on
   int lo, hi, n_lo, n_hi;    // pushed: bins in which a cut may lie, tokens before and through them
   int found;                 // index found by find_in_order, written by its owner
   int base;
@@ -253,8 +252,11 @@ SPEC_DEV ull mul2(ull a, ull b) {
 
 // weight() of two logits, operation for operation, in packed arithmetic (the
 // scans that weigh a whole row are bound by their instructions).
-SPEC_DEV void weight2(const Scale& r, const ull* tab, float x0, float x1, ull& w0, ull& w1) {
+// v0, v1: their place().
+SPEC_DEV void weight2(const Scale& r, const ull* tab, float x0, float x1, ull& w0, ull& w1, float& v0, float& v1) {
   if (r.m == INFINITY) {
+    v0 = r.place(x0);
+    v1 = r.place(x1);
     w0 = x0 == INFINITY ? 1ull << WBITS : 0ull;
     w1 = x1 == INFINITY ? 1ull << WBITS : 0ull;
     return;
@@ -267,6 +269,8 @@ SPEC_DEV void weight2(const Scale& r, const ull* tab, float x0, float x1, ull& w
   const ull pe = fma2(e, sh, fma2(d, pk(r.sl), fma2(d, sh, np)));
   float a, b;
   upk(np, a, b);
+  v0 = a * -r.bins;
+  v1 = b * -r.bins;
   np = pk(fmaxf(a, -63.f), fmaxf(b, -63.f));
   const ull t = fma2(np, neg, pk(MAGIC));
   const ull g = fma2(add2(np, add2(t, pk(-MAGIC))), neg, pe);
@@ -282,6 +286,11 @@ SPEC_DEV void weight2(const Scale& r, const ull* tab, float x0, float x1, ull& w
   upk(fma2(Tf, q, pk(half_unit(n0), half_unit(n1))), a, b);
   w0 = (T0 + (long long)__float2int_rn(a)) >> n0;
   w1 = (T1 + (long long)__float2int_rn(b)) >> n1;
+}
+
+SPEC_DEV void weight2(const Scale& r, const ull* tab, float x0, float x1, ull& w0, ull& w1) {
+  float v0, v1;
+  weight2(r, tab, x0, x1, w0, w1, v0, v1);
 }
 
 // The same out of line, where it is evaluated a few times.
@@ -311,6 +320,13 @@ SPEC_DEV ull drawn_mass(float u, ull z) { return u > 0.f ? (u < 1.f ? scaled(u, 
 // Order-preserving key, ascending from the best token: -0 counts as +0.
 SPEC_DEV uint32_t rank_key(float x) { return ~ord_key(x + 0.f); }
 SPEC_DEV float rank_val(uint32_t k) { return ord_val(~k); }
+
+// The larger value, NaN if either is.
+SPEC_DEV float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
 
 // The part of a row one warp owns, 16-byte vectors in index order; rows may
 // start at any element, the first and last vectors are read element by element.
@@ -517,28 +533,28 @@ SPEC_DEV void append(Shared& s, int i, float x) {
   }
 }
 
-// Top-p's scan of the tokens inside a cut: adds all their weights up, lists those
-// of exponents [lo, hi) in bin units, and returns the mass of those below lo.
+// Top-p's scan of the tokens inside a cut: returns the mass of those below lo, in
+// bin units, adds the others' up, and lists those of them below hi.
 struct Nucleus {
   Scale sc;
   Shared& s;
   Cut cut;
   bool cutting;
   float lo, hi;
-  ull all;
-  SPEC_DEV ull take(int i, float x, ull w) {
+  ull all;   // the others'
+  SPEC_DEV ull take(int i, float x, float v, ull w) {
     if (cutting && !kept(cut, rank_key(x), i)) return 0ull;
-    all += w;
-    const float v = sc.place(x);
     if (v < lo) return w;
+    all += w;
     if (v < hi) append(s, i, x);
     return 0ull;
   }
-  SPEC_DEV ull operator()(int i, float x) { return take(i, x, weight(sc, s.tab, x)); }
+  SPEC_DEV ull operator()(int i, float x) { return take(i, x, sc.place(x), weight(sc, s.tab, x)); }
   SPEC_DEV ull two(int i, float x0, float x1) {
     ull w0, w1;
-    weight2(sc, s.tab, x0, x1, w0, w1);
-    return take(i, x0, w0) + take(i + 1, x1, w1);
+    float v0, v1;
+    weight2(sc, s.tab, x0, x1, w0, w1, v0, v1);
+    return take(i, x0, v0, w0) + take(i + 1, x1, v1, w1);
   }
 };
 
@@ -1067,7 +1083,7 @@ struct Sampler {
     ull ahead = 0, all = 0;
     for (int c = 0; c < C; ++c) {
       ahead += s.x_bins[c][0];
-      all += s.x_bins[c][1];
+      all += s.x_bins[c][0] + s.x_bins[c][1];
     }
     const int n = *cl.map_shared_rank(&s.gathered, 0);
     if (few) {
@@ -1270,7 +1286,8 @@ __global__ void __launch_bounds__(CNT, 4) chunk_kernel(SampleArgs a, Record* rec
   constexpr int E = 16 / sizeof(T), PER = CHUNK_TOKENS / E, NV = PER / CNT;
   extern __shared__ __align__(16) unsigned char smem_raw[];
   ull* tab = reinterpret_cast<ull*>(smem_raw);
-  __shared__ ull s_best[2][CNW], s_sum[2][CNW];
+  __shared__ ull s_sum[2][CNW];
+  __shared__ uint32_t s_key[2][CNW], s_at[2][CNW];
   for (int i = threadIdx.x; i < TAB / 2; i += CNT) {
     const unsigned int dst = (unsigned int)__cvta_generic_to_shared(tab + 2 * i);
     asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(g_table.v + 2 * i) : "memory");
@@ -1304,26 +1321,31 @@ __global__ void __launch_bounds__(CNT, 4) chunk_kernel(SampleArgs a, Record* rec
     const int row = item / n, c = item - row * n;
     const int mis = (int)(((uintptr_t)((const T*)a.logits + (size_t)row * a.ld) & 15) / sizeof(T));
     float bx = -INFINITY;
-    int bi = -1, nan = 0;
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
-      for (int i = 0; i < E; ++i) {
-        const float x = Part<T>::get(q[j], i);
-        nan |= x != x;
-        if (x > bx) {
-          bx = x;
-          bi = (c * PER + j * CNT + threadIdx.x) * E - mis + i;
-        }
-      }
-    ull best = bi >= 0 ? pack_best(bx + 0.f, (uint32_t)bi) : 0ull;
-    const uint32_t key = __reduce_max_sync(FULL, (uint32_t)(best >> 32));
-    const uint32_t idx = __reduce_max_sync(FULL, (uint32_t)(best >> 32) == key ? (uint32_t)best : 0u);
-    best = ((ull)key << 32) | idx;
-    if (lane == 0) s_best[turn][warp] = best;
-    nan = __syncthreads_or(nan);
+      for (int i = 0; i < E; ++i) bx = max_nan(bx, Part<T>::get(q[j], i));
+    uint32_t key = bx > -INFINITY ? ord_key(bx + 0.f) : 0u;
+    key = __reduce_max_sync(FULL, key);
+    if (lane == 0) s_key[turn][warp] = key;
+    const int nan = __syncthreads_or(bx != bx);
 #pragma unroll
-    for (int w = 0; w < CNW; ++w) best = s_best[turn][w] > best ? s_best[turn][w] : best;
+    for (int w = 0; w < CNW; ++w) key = max(key, s_key[turn][w]);
+    ull best = key ? pack_best(ord_val(key), 0u) : 0ull;
+    if (key && temp < 1e-5f) {   // (greedy: the whole CTA) the lowest index of the maximum
+      uint32_t at = 0xffffffffu;
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int i = 0; i < E; ++i)
+          if (Part<T>::get(q[j], i) == ord_val(key)) at = min(at, (uint32_t)((c * PER + j * CNT + threadIdx.x) * E - mis + i));
+      at = __reduce_min_sync(FULL, at);
+      if (lane == 0) s_at[turn][warp] = at;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < CNW; ++w) at = min(at, s_at[turn][w]);
+      best = pack_best(ord_val(key), at);
+    }
     ull sum = 0;
     if (best && !nan && temp >= 1e-5f && temp < INFINITY) {
       Scale sc{best_value(best), 0.f, 0.f, 0.f};
@@ -1495,19 +1517,15 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SampleArgs a) {
   int seg_lanes = 1;
   while (C * NT / seg_lanes > SEG_MAX) seg_lanes *= 2;
 
-  // maximum with its lowest index, minimum, segment maxima; a NaN anywhere
-  // leaves the row without a distribution
+  // maximum, minimum, segment maxima; a NaN anywhere leaves the row without a
+  // distribution
   float bx = -INFINITY, low = INFINITY;
-  int bi = -1, nan = 0;
-  S.part.each([&](int i, float x) {
-    nan |= x != x;
+  S.part.each([&](int, float x) {
     low = fminf(low, x);
-    if (x > bx) {
-      bx = x;
-      bi = i;
-    }
+    bx = max_nan(bx, x);
   });
-  ull best = bi >= 0 ? pack_best(bx + 0.f, (uint32_t)bi) : 0ull;
+  int nan = bx != bx;
+  uint32_t key = bx > -INFINITY ? ord_key(bx + 0.f) : 0u;
   cl.barrier_wait(std::move(started));
   if (k > 0 && !greedy) {   // (top-k alone looks at them)
 #pragma unroll
@@ -1522,50 +1540,61 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SampleArgs a) {
       if (j < per * C) cl.map_shared_rank(s.seg, j / per)[(cta * NW + warp) * per + g] = v;
     }
   }
-  {
-    // the largest key of the warp, and its lowest index
-    const uint32_t key = __reduce_max_sync(FULL, (uint32_t)(best >> 32));
-    const uint32_t idx = __reduce_max_sync(FULL, (uint32_t)(best >> 32) == key ? (uint32_t)best : 0u);
-    best = ((ull)key << 32) | idx;
-    low = ord_val(__reduce_min_sync(FULL, ord_key(low)));
-  }
+  key = __reduce_max_sync(FULL, key);
+  low = ord_val(__reduce_min_sync(FULL, ord_key(low)));
   if (lane == 0) {
-    s.wsum[warp] = best;
+    s.list_key[warp] = key;
     reinterpret_cast<float*>(s.list_idx)[warp] = low;
   }
   nan = __syncthreads_or(nan);
   if (threadIdx.x < C) {
     for (int i = 0; i < NW; ++i) {
-      best = s.wsum[i] > best ? s.wsum[i] : best;
+      key = max(key, s.list_key[i]);
       low = fminf(low, reinterpret_cast<float*>(s.list_idx)[i]);
     }
-    *cl.map_shared_rank(&s.x_best[cta], threadIdx.x) = best;
+    *cl.map_shared_rank(&s.x_best[cta], threadIdx.x) = nan ? 0xffffffffu : key;   // (no value's key)
     *cl.map_shared_rank(&s.x_low[cta], threadIdx.x) = low;
-    *cl.map_shared_rank(&s.x_nan[cta], threadIdx.x) = nan;
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
   cl.sync();
-  best = 0;
-  nan = 0;
+  key = 0;
 #pragma unroll
   for (int c = 0; c < MAX_C; ++c)
     if (c < C) {
-      best = s.x_best[c] > best ? s.x_best[c] : best;
+      key = max(key, s.x_best[c]);
       low = fminf(low, s.x_low[c]);
-      nan |= s.x_nan[c];
     }
 
   auto write = [&](int token, float prob) {
     a.tokens[row] = token;
     if (a.probs) a.probs[row] = prob;
   };
-  if (best == 0ull || nan || !(temp >= 0.f && temp < INFINITY) || greedy) {
-    const bool ok = best != 0ull && !nan && greedy && temp >= 0.f;   // else: no distribution
-    if (cta == 0 && threadIdx.x == 0) write(ok ? (int)best_index(best) : -1, ok ? 1.f : 0.f);
+  const float m = ord_val(key);
+  if (key == 0u || key == 0xffffffffu || !(temp >= 0.f && temp < INFINITY)) {   // no distribution
+    if (cta == 0 && threadIdx.x == 0) write(-1, 0.f);
+    return;
+  }
+  if (greedy) {   // the lowest index of the maximum
+    uint32_t at = 0xffffffffu;
+    S.part.each([&](int i, float x) {
+      if (x == m) at = min(at, (uint32_t)i);
+    });
+    at = __reduce_min_sync(FULL, at);
+    if (lane == 0) s.list_key[warp] = at;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      for (int i = 0; i < NW; ++i) at = min(at, s.list_key[i]);
+      *cl.map_shared_rank(&s.x_total[cta], 0) = at;
+    }
+    cl.sync();
+    if (cta == 0 && threadIdx.x == 0) {
+      ull first = s.x_total[0];
+      for (int c = 1; c < C; ++c) first = min(first, s.x_total[c]);
+      write((int)first, 1.f);
+    }
     return;
   }
 
-  const float m = best_value(best);
   float sh, sl;
   scale_of(temp, sh, sl);
   // finer bins where the row's range of exponents is less than the weights'
