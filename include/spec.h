@@ -179,7 +179,7 @@ typedef struct {
  *               token).
  * Values outside these ranges (NaN included) leave top_k, top_p and min_p off.
  * Weights are held in 44 fraction bits of the largest (smaller ones count as
- * zero), to a relative 2^-36, and summed exactly: a result does not depend on
+ * zero), to a relative 2^-36 (at temperatures up to 1e30), and summed exactly: a result does not depend on
  * timing, and is the 64-bit one unless u or a filter falls that near to a
  * border. -inf logits are never chosen; +inf logits share the whole mass
  * equally; a row with a NaN, or with nothing above -inf, has no distribution. */

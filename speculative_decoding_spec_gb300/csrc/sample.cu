@@ -46,10 +46,10 @@
 // of it, and a last scan sums the kept weights.
 //
 // What bounds it: one row, latency (13 us with top-k, about 20 dependent phases of
-// 0.3 to 2 us); many rows, the weights: about 50 instructions a token, among them
+// 0.3 to 2 us); many rows, the weights: about 45 instructions a token, among them
 // random 8-byte reads of the table in shared memory, not the 1 MB a row out of
-// HBM. 262144 fp32 logits a row: 40 rows at temperature 28.5 us (1.5 TB/s; the
-// bytes alone 6.2 us), with top-k 50 26 us; 64 rows with top-p of mixed breadth 93
+// HBM. 262144 fp32 logits a row: 40 rows at temperature 25.9 us (1.6 TB/s; the
+// bytes alone 6.2 us), with top-k 50 26 us; 64 rows with top-p of mixed breadth 91
 // us.
 #include <cooperative_groups.h>
 
@@ -1755,7 +1755,7 @@ int cluster_size(int M, int V) {
 }
 
 // Calls without filters of at least this many tokens take the chunk kernel: of
-// 262144 tokens a row, 1 row 8.9 us (16.9 without), 40 rows 28.5 us (43).
+// 262144 tokens a row, 1 row 8.9 us (16.9 without), 40 rows 25.9 us (43).
 constexpr long long CHUNKED_MIN = 1ll << 17;
 bool chunked(int M, int V) { return (long long)M * V >= CHUNKED_MIN && V >= 2 * CHUNK_TOKENS; }
 
