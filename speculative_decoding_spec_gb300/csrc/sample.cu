@@ -36,21 +36,24 @@
 // top-k and top-p, scan 2 sums the weights and the warp that holds the drawn mass
 // finds the token. With top-k, scan 2 lists the tokens down to the k-th largest
 // segment maximum -- at least k tokens, and rarely many more -- and the first CTA
-// cuts and draws among those alone. With top-p alone, scan 2 counts the tokens in
-// 2048 bins, linear in the exponent, which bound the mass up to each well enough
-// to leave a few bins for the cut; scan 3 adds all weights up exactly, lists those
-// bins' tokens, and sums the tokens ahead of them in index order, so that the cut
-// and the draw follow from the list and those sums. (A nucleus of few tokens is
-// listed as a whole and drawn from as top-k's.) Where the listed tokens are too
-// many, the cut comes from a radix search of their keys, or min-p's end lies ahead
-// of it, and a last scan sums the kept weights.
+// cuts and draws among those alone. With top-p alone, where the segment maxima
+// promise a narrow nucleus, scan 2 lists the likeliest tokens and adds the others up
+// in plain floats: bounds of the tail's mass that nearly always leave one cut. Else,
+// or where they leave two, a scan counts the tokens in 2048 bins, linear in the
+// exponent, which bound the mass up to each well enough to leave a few bins for the
+// cut; the next adds all weights up exactly, lists those bins' tokens, and sums the
+// tokens ahead of them in index order, so that the cut and the draw follow from the
+// list and those sums. (A nucleus of few tokens is listed as a whole and drawn from
+// as top-k's.) Where the listed tokens are too many, the cut comes from a radix
+// search of their keys, or min-p's end lies ahead of it, and a last scan sums the
+// kept weights.
 //
 // What bounds it: one row, latency (13 us with top-k, about 20 dependent phases of
 // 0.3 to 2 us); many rows, the weights: about 45 instructions a token, among them
 // random 8-byte reads of the table in shared memory, not the 1 MB a row out of
 // HBM. 262144 fp32 logits a row: 40 rows at temperature 25.9 us (1.6 TB/s; the
-// bytes alone 6.2 us), with top-k 50 26 us; 64 rows with top-p of mixed breadth 91
-// us.
+// bytes alone 6.2 us), with top-k 50 26 us; 64 rows with top-p of mixed breadth 85
+// us, 40 with few likely tokens 33 us.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -77,6 +80,7 @@ constexpr int TAB = 1 << TAB_LOG;   // 2^(-j/4096)
 constexpr int MAX_C = 16;           // CTAs on one row (a thread-block cluster)
 constexpr int FEW = 2048;           // tokens a CTA lists, and the first one cuts
 constexpr int COUNTED = NT / 2;     // at most so many are counted instead
+constexpr int HEAD = 128;           // segment maxima among which top-p looks first
 constexpr int CHUNK_TOKENS = 4096;  // tokens of a chunk of the chunk kernel
 constexpr int CNT = 256;            // its threads
 constexpr int CNW = CNT / 32;
@@ -136,6 +140,8 @@ struct Shared {
   ull tied[TIED][2];         // tokens of one of those, and their amounts
   ull word;                  // the selected one
   uint32_t key_lo, key_hi;
+  int undecided;             // pushed by the first CTA
+  float seen[2];             // weights of the listed segment maxima, and of all
   int n_tied;
   int gathered;              // first CTA: tokens listed by all
   unsigned int seg_bins[SEG_BINS];
@@ -555,6 +561,27 @@ struct Nucleus {
     float v0, v1;
     weight2(sc, s.tab, x0, x1, w0, w1, v0, v1);
     return take(i, x0, v0, w0) + take(i + 1, x1, v1, w1);
+  }
+};
+
+// The scan for a nucleus among the first few tokens: lists those below `end`, in
+// bin units, and adds the weights of the others up in plain floats, a step's at a time.
+struct Tail {
+  Scale sc;
+  Shared& s;
+  float end, some;
+  ull all;
+  SPEC_DEV void operator()(int i, float x) {
+    if (sc.place(x) < end) append(s, i, x);
+    else some += exp2f((x - sc.m) * sc.sh);
+  }
+  SPEC_DEV void two(int i, float x0, float x1) {
+    (*this)(i, x0);
+    (*this)(i + 1, x1);
+  }
+  SPEC_DEV void step() {
+    all += (ull)(some * (float)(1ull << WBITS));
+    some = 0.f;
   }
 };
 
@@ -1057,10 +1084,65 @@ struct Sampler {
     if (v < hi && v >= lo) append(s, i, x);
   }
 
+  // Whether top-p's nucleus probably lies among the tokens of the bins before `bins`,
+  // as far as the row's n segment maxima tell: those behind hold at most a quarter of
+  // the 1 - p that may be cut. (64 rows of 262144 of mixed breadth 85 us, 89 with a
+  // half, 94 with all of it, 91 without looking; 40 rows with few likely tokens 33 us,
+  // 64 without; 40 rows with a broad nucleus 82 us, 79 without.)
+  SPEC_DEV bool promising(int bins, int n, float p) {
+    if (threadIdx.x < 2) s.seen[threadIdx.x] = 0.f;
+    __syncthreads();
+    float in = 0.f, all = 0.f;
+    for (int i = threadIdx.x; i < n; i += NT) {
+      const float w = sc.m == INFINITY ? (s.seg[i] == INFINITY ? 1.f : 0.f) : exp2f((s.seg[i] - sc.m) * sc.sh);
+      all += w;
+      if (sc.bin(s.seg[i]) < bins) in += w;
+    }
+    in = warp_sum(in);
+    all = warp_sum(all);
+    if ((threadIdx.x & 31) == 0) {
+      s.scan[threadIdx.x >> 5][0] = __float_as_uint(in);
+      s.scan[threadIdx.x >> 5][1] = __float_as_uint(all);
+    }
+    __syncthreads();
+    if (threadIdx.x < 2) {
+      float t = 0.f;
+      for (int w = 0; w < NW; ++w) t += __uint_as_float((uint32_t)s.scan[w][threadIdx.x]);
+      s.seen[threadIdx.x] = t;
+    }
+    __syncthreads();
+    return s.seen[1] - s.seen[0] <= 0.25f * (1.f - p) * s.seen[1];
+  }
+
+  // Lists the tokens of the first bins in order, below `end`, for the first CTA,
+  // with bounds of the mass of the tokens behind them. Returns their number.
+  // (A weight of the tail is off by three roundings of its exponent, 4e-6 up to
+  // 2^-32 of the largest weight, and by 1e-6 for the exponential and a step's sum:
+  // below 2^-17 together. Smaller ones, their rounding to units and the steps' are
+  // below a unit a token and 2^-30.)
+  SPEC_DEV int list_head(float end, ull* tail_least, ull* tail_most) {
+    if (threadIdx.x == 0) s.all = 0;
+    __syncthreads();
+    Tail f{sc, s, end, 0.f, 0ull};
+    part.template each_rolled<WIDE>(part.v0, part.v1, f, [&](int) { f.step(); });
+    const ull w = warp_sum_u64(f.all);
+    if ((threadIdx.x & 31) == 0) atomicAdd(&s.all, w);
+    __syncthreads();
+    push_list();
+    if (threadIdx.x < C) cl.map_shared_rank(&s, threadIdx.x)->x_bins[cta][0] = s.all;
+    cl.sync();
+    ull tail = 0;
+    for (int c = 0; c < C; ++c) tail += s.x_bins[c][0];
+    const ull off = (tail >> 17) + part.V + (1ull << (WBITS - 30));
+    *tail_least = tail > off ? tail - off : 0ull;
+    *tail_most = tail + off;
+    return *cl.map_shared_rank(&s.gathered, 0);
+  }
+
   // Top-p: the cut at which the tokens inside the present one reach the mass p, in
   // the bins of find_bins. SUMMED: *kept_mass and *before are sum()'s of the tokens
   // that the cut and min-p (weights from qw on) keep; DRAWN: a nucleus of few tokens
-  // has been drawn from by draw(their number, the mass).
+  // has been drawn from by draw(their number, false, the mass, the mass).
   enum Outcome { CUT, SUMMED, DRAWN };
   template <typename D>
   SPEC_DEV Outcome cut_mass(Cut& cut, bool cutting, float p, ull qw, D draw, ull* kept_mass, ull* before) {
@@ -1087,7 +1169,7 @@ struct Sampler {
     }
     const int n = *cl.map_shared_rank(&s.gathered, 0);
     if (few) {
-      draw(n, all);
+      draw(n, false, all, all);
       return DRAWN;
     }
     const ull need = top_p_mass(p, all);
@@ -1161,7 +1243,7 @@ struct Sampler {
   // draw_few for at most COUNTED tokens, which are not sorted: two threads a
   // token count the tokens (and their mass) ahead of it, in the order and then
   // in the vocabulary.
-  SPEC_DEV int draw_counted(int n, int k, float p, ull qw, float u, ull mass, ull* kept_mass) {
+  SPEC_DEV int draw_counted(int n, int k, float p, ull qw, float u, bool tail, ull least, ull most, ull* kept_mass) {
     ull* w = s.sort + COUNTED;
     const int i = threadIdx.x >> 1, half = threadIdx.x & 1;
     const ull e = i < n ? s.sort[i] : ~0ull;
@@ -1183,7 +1265,8 @@ struct Sampler {
     bool keep = i < n && (k <= 0 || rank < k);
     if (p < 1.f) {
       block_total(keep && half == 0 ? wi : 0ull);
-      const ull need = top_p_mass(p, k > 0 ? s.total : mass);
+      const ull z = tail ? s.total : 0ull, need = top_p_mass(p, z + least), last = top_p_mass(p, z + most);
+      if (__syncthreads_or(last > s.total || (keep && (ahead < need) != (ahead < last)))) return -1;
       keep = keep && ahead < need;
     }
     keep = keep && wi >= qw;
@@ -1206,10 +1289,13 @@ struct Sampler {
   }
 
   // The first CTA's end of the usual case: the n listed tokens, the row's best, are
-  // cut and drawn from in index order. mass: the row's whole mass (top-p without
-  // top-k). Returns the token, *kept_mass its kept mass.
-  SPEC_DEV int draw_few(int n, int k, float p, ull qw, float u, ull mass, ull* kept_mass) {
-    if (n <= COUNTED) return draw_counted(n, k, p, qw, u, mass, kept_mass);
+  // cut and drawn from in index order. Top-p takes the row's whole mass between
+  // least and most, or with `tail` that of the tokens behind those (0: top-k); -1
+  // where the cut depends on which, or lies behind them. Returns the token,
+  // *kept_mass its kept mass.
+  SPEC_DEV int draw_few(int n, int k, float p, ull qw, float u, bool tail, ull least, ull most,
+                        ull* kept_mass) {
+    if (n <= COUNTED) return draw_counted(n, k, p, qw, u, tail, least, most, kept_mass);
     ull e[PT], w[PT], t[PT], ahead, at, last = ~0ull;
     take_listed<true>(n, e, w);
     const ull lo = (ull)s.key_lo << 32, hi = ((ull)s.key_hi << 32) | 0xffffffffu;
@@ -1218,19 +1304,21 @@ struct Sampler {
       for (int j = 0; j < PT; ++j) t[j] = e[j] != ~0ull;
       last = select(e, t, lo, hi, k, 0ull, &ahead, &at);
     }
-    auto keep = [&](ull least) {   // in t, of weight `least` at least; returns their mass
+    auto keep = [&](ull from) {   // in t, those of weight `from` on; returns their mass
       ull sum = 0;
 #pragma unroll
       for (int j = 0; j < PT; ++j) {
-        t[j] = e[j] <= last && w[j] >= least ? w[j] : 0ull;
+        t[j] = e[j] <= last && w[j] >= from ? w[j] : 0ull;
         sum += t[j];
       }
       block_total(sum);
       return s.total;
     };
     if (p < 1.f) {
-      const ull z = keep(0ull);
-      last = select(e, t, lo, hi, top_p_mass(p, k > 0 ? z : mass), 0ull, &ahead, &at);
+      const ull z = keep(0ull), need = top_p_mass(p, least + (tail ? z : 0ull)), far = top_p_mass(p, most + (tail ? z : 0ull));
+      if (far > z) return -1;
+      last = select(e, t, lo, hi, need, 0ull, &ahead, &at);
+      if (far > ahead + at) return -1;
     }
     const ull z = keep(qw);
     *kept_mass = z;
@@ -1527,7 +1615,7 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SampleArgs a) {
   int nan = bx != bx;
   uint32_t key = bx > -INFINITY ? ord_key(bx + 0.f) : 0u;
   cl.barrier_wait(std::move(started));
-  if (k > 0 && !greedy) {   // (top-k alone looks at them)
+  if (cuts && !greedy) {
 #pragma unroll
     for (int o = 1; o < 8; o <<= 1) {
       const float v = __shfl_xor_sync(FULL, bx, o);
@@ -1617,25 +1705,33 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SampleArgs a) {
     return;
   }
 
-  // the first CTA draws among the n tokens handed to it, if they fit
-  auto draw = [&](int n, ull mass) {
+  // the first CTA draws among the n tokens handed to it, if they fit and decide it
+  auto draw = [&](int n, bool tail, ull least, ull most) {
     if (n <= FEW && cta == 0) {
       ull z;
-      const int token = S.draw_few(n, k, p, qw, u, mass, &z);
-      if (threadIdx.x == 0) result(token, Part<T>::one((const T*)a.logits + (size_t)row * a.ld + token), z);
+      const int token = S.draw_few(n, k, p, qw, u, tail, least, most, &z);
+      if (threadIdx.x == 0 && token >= 0) result(token, Part<T>::one((const T*)a.logits + (size_t)row * a.ld + token), z);
+      if (threadIdx.x < C) *cl.map_shared_rank(&s.undecided, threadIdx.x) = token < 0;
     }
     cl.sync();   // its count is read, and its tokens are, before either changes
-    return n <= FEW;
+    return n <= FEW && !s.undecided;
   };
   Cut cut{0xffffffffu, 0x7fffffff};
   ull z = 0, before = 0;
   bool summed = false;
+  const int segs = C * NT / seg_lanes;
   if (k > 0) {
-    const int segs = C * NT / seg_lanes;
-    if (k <= segs && draw(S.list_below(S.end_of((S.threshold(k, segs) + 1) * (BINS / SEG_BINS))), 0ull)) return;
+    if (k <= segs && draw(S.list_below(S.end_of((S.threshold(k, segs) + 1) * (BINS / SEG_BINS))), true, 0ull, 0ull)) return;
     S.find_bins(cut, false, k, 1.f);
     S.cut_count(cut, k);
     k = 0;   // (the cut holds it)
+  } else {
+    const int bins = (S.threshold(HEAD, segs) + 1) * (BINS / SEG_BINS);
+    if (S.promising(bins, segs, p)) {
+      ull least, most;
+      const int n = S.list_head(S.end_of(bins), &least, &most);
+      if (draw(n, true, least, most)) return;
+    }
   }
   if (p < 1.f) {
     const bool cutting = cut.idx != 0x7fffffff || cut.key != 0xffffffffu;
@@ -1724,8 +1820,7 @@ int max_clusters(int dev, int C) {
 // clusters at a fixed cost of about 9 us (0.2 more a CTA of the exchanges) and
 // 0.25 ns a token of a CTA, up to 0.5 ns as the SMs hold two CTAs each. Measured,
 // 262144 tokens a row: 1 row with top-k 50 13 us with 16 CTAs, 15 with 8, 60 with
-// 1; 64 rows with top-k 50 32 us with 4 CTAs, 46 with 2, 39 with 8, with top-p of
-// mixed breadth 93, 114 (3), 100.
+// 1; 64 rows with top-k 50 32 us with 4 CTAs, 46 with 2, 39 with 8.
 template <typename T>
 int cluster_size(int M, int V) {
   int best = MAX_C, dev = 0;

@@ -113,6 +113,21 @@ def test_min_p_around_the_nucleus():
     _check(x, binding.spec_sample(x, u, T, None, p, q), u, T, None, p, q)
 
 
+# top_p a rounding away from where a token enters the nucleus: nearer than the plain
+# float sums that decide most narrow nuclei can tell.
+@pytest.mark.parametrize("V", [4099, 262144])
+def test_top_p_beside_a_border(V):
+    M = 96
+    g = _gen(V)
+    x = (torch.randn((1, V), generator=g, device="cuda") * 9).repeat(M, 1)
+    u = torch.rand(M, generator=g, device="cuda")
+    w = torch.sort(torch.exp((x[0].double() - x[0].max().double())), descending=True).values
+    at = (torch.cumsum(w, 0) / w.sum())[1:33].repeat_interleave(3).float()
+    p = torch.nextafter(at, torch.tensor([0.0, 2.0, 1.0], device="cuda").repeat(32))
+    p[2::3] = at[2::3] * (1 - 2.0 ** -19)
+    _check(x, binding.spec_sample(x, u, None, None, p), u, None, None, p, most_undecided=0.1)
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("V,ld,off", [(1000, 1003, 0), (4097, 4097, 1), (32003, 32010, 3), (50001, 50001, 7)])
 def test_strided_and_unaligned_rows(dtype, V, ld, off):
