@@ -410,7 +410,8 @@ spec_status spec_attention(const spec_model_desc *m, const spec_kv_desc *kv, int
  * probability it had (its weight over the kept mass), 0 for such a row.
  * workspace ("device", 16-byte aligned, ws_bytes >=
  * spec_sample_workspace_bytes(M, V), no initialisation; may be NULL where that
- * is 0) is written and read by the call; calls sharing one must not overlap.
+ * is 0, or top_k, top_p or min_p is given) is written and read by the call; calls
+ * sharing one must not overlap.
  * V <= 2^19, M <= 2^20. */
 size_t spec_sample_workspace_bytes(int32_t M, int32_t V);
 spec_status spec_sample(int32_t dtype, const void *logits, int64_t ld, int32_t M, int32_t V,

@@ -295,6 +295,7 @@ def _logits(fn, logits):
 
 _raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else \
     lambda dev: torch.cuda.current_stream(dev).cuda_stream
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 class _on:
@@ -306,7 +307,7 @@ class _on:
         self.dev, self.ctx = dev, None
         if stream is not None:
             self.ctx = torch.cuda.stream(stream)
-        elif dev != torch.cuda.current_device():
+        elif dev != _current_device():
             self.ctx = torch.cuda.device(dev)
 
     def __enter__(self):
@@ -319,8 +320,10 @@ class _on:
             self.ctx.__exit__(*e)
 
 
-def _sample_ws(L, logits, M, V):
-    """Scratch of a sampling call on its stream, where it needs any."""
+def _sample_ws(L, logits, M, V, s):
+    """Scratch of a sampling call on its stream, where it needs any (calls with filters do not)."""
+    if s.top_k or s.top_p or s.min_p:
+        return None, 0
     n = L.spec_sample_workspace_bytes(M, V)
     return (logits.new_empty(n, dtype=torch.uint8), n) if n else (None, 0)
 
@@ -339,7 +342,7 @@ def spec_sample(logits: torch.Tensor, uniform: torch.Tensor, temperature: Option
     with _on(dev, stream) as st:
         tokens = torch.empty_like(uniform, dtype=torch.int32)
         probs = torch.empty_like(uniform)
-        ws, n = _sample_ws(L, logits, M, V)
+        ws, n = _sample_ws(L, logits, M, V, s)
         rc = L.spec_sample(dt, logits.data_ptr(), ld, M, V, C.byref(s), tokens.data_ptr(), probs.data_ptr(), _ptr(ws),
                            n, st)
     check(fn, rc)
@@ -364,7 +367,7 @@ def spec_accept_sampled(logits: torch.Tensor, drafts: torch.Tensor, uniform: tor
         out = drafts.new_empty((B, k + 1))
         ne = drafts.new_empty(B)
         probs = uniform.new_empty((B, k + 1))
-        ws, n = _sample_ws(L, logits, M, V)
+        ws, n = _sample_ws(L, logits, M, V, s)
         rc = L.spec_accept_sampled(dt, logits.data_ptr(), ld, B, k, V, drafts.data_ptr() if k else None, C.byref(s),
                                    out.data_ptr(), ne.data_ptr(), probs.data_ptr(), _ptr(ws), n, st)
     check(fn, rc)

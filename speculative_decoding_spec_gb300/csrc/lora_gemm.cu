@@ -762,7 +762,7 @@ cudaError_t launch_gemm(GemmArgs& g, const CUtensorMap& tmw, const CUtensorMap& 
 
 template <int MP>
 void set_attributes() {
-  const int n = SMEM_LIMIT - 3072;
+  const int n = SMEM_LIMIT - 3 * 1024;
   cudaFuncSetAttribute(lora_gemm_kernel<MP, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, n);
   cudaFuncSetAttribute(lora_gemm_kernel<MP, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize, n);
 }

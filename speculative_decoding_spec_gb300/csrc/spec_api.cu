@@ -1068,7 +1068,7 @@ spec_status spec_sample(int32_t dtype, const void* logits, int64_t ld, int32_t M
       !tokens)
     return SPEC_EINVAL;
   if (M > SAMPLE_ROWS_MAX || V > SAMPLE_V_MAX) return SPEC_EUNSUPPORTED;
-  const size_t need = sample_workspace_bytes(M, V);
+  const size_t need = s->top_k || s->top_p || s->min_p ? 0 : sample_workspace_bytes(M, V);
   if (need && !aligned16({workspace})) return SPEC_EINVAL;
   if (need && (!workspace || ws_bytes < need)) return SPEC_ECAPACITY;
   setup_device_attributes();
