@@ -228,6 +228,22 @@ def test_other_stream_captured_graph_and_layers():
             assert torch.equal(out, binding.spec_linear_lora(w, x, lora, ids, layer=l))
 
 
+@pytest.mark.parametrize("dtype", [configs.BF16, configs.Q4_0])
+def test_two_calls_at_once(dtype):
+    g = _gen(12)
+    N, K, M = 5000, 2048, 24
+    w = synth.make_matrix(g, dtype, 1, N, K, 0.02, "cuda")
+    lora = _adapters(g, 4, 16, N, K, torch.bfloat16)
+    x = [torch.randn((M, K), generator=g, device="cuda") for _ in range(2)]
+    ids = [torch.randint(-1, 4, (M,), generator=g, device="cuda", dtype=torch.int32) for _ in range(2)]
+    alone = [binding.spec_linear_lora(w, x[i], lora, ids[i]) for i in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[binding.spec_linear_lora(w, x[i], lora, ids[i], stream=streams[i]) for i in range(2)] for _ in range(8)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(both[i], alone[i]) for both in got for i in range(2))
+
+
 def test_refusals():
     g = _gen(7)
     w = synth.make_matrix(g, configs.BF16, 1, 64, 64, 0.02, "cuda")

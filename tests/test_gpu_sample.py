@@ -343,6 +343,24 @@ def test_other_stream_and_captured_graph():
         assert all(torch.equal(a, b) for a, b in zip(t2, binding.spec_accept_sampled(x, d, u, T, None, p)))
 
 
+def test_two_calls_at_once():
+    """Calls on two streams, large enough to overlap, leave what each leaves alone."""
+    g = _gen(11)
+    x = [torch.randn((24, 100003), generator=g, device="cuda") * 2.5 for _ in range(2)]
+    u = [torch.rand(24, generator=g, device="cuda") for _ in range(2)]
+    p = _vec(0.9, 24)
+    for top_p in (None, p):
+        alone = [binding.spec_sample(x[i], u[i], None, None, top_p) for i in range(2)]
+        streams = [torch.cuda.Stream() for _ in range(2)]
+        torch.cuda.synchronize()
+        got = [[binding.spec_sample(x[i], u[i], None, None, top_p, stream=streams[i]) for i in range(2)]
+               for _ in range(8)]
+        torch.cuda.synchronize()
+        for both in got:
+            for i in range(2):
+                assert torch.equal(both[i][0], alone[i][0]) and torch.equal(both[i][1], alone[i][1])
+
+
 def test_refusals():
     x, u = torch.zeros((2, 8), device="cuda"), torch.zeros(2, device="cuda")
     bad = [
