@@ -19,7 +19,7 @@
 // the MMA's B operand, so each 16-column k-step is one MMA with N = 3 x rows.
 //
 // Work split: units are (tile, chunk of W) pairs in tile-major order, and CTA b
-// of G owns [U b / G, U (b + 1) / G); the CTA with a tile's last chunk also takes
+// of G owns [U b / G, U (b + 1) / G), of small matrices whole shares of a tile; the CTA with a tile's last chunk also takes
 // the adapters' (counted on the device from the ids, by every CTA alike). A tile
 // cut between CTAs is summed by the last CTA to arrive, in CTA order. So a row's
 // result depends on neither timing, nor the other rows, nor their adapters (whose
@@ -29,7 +29,7 @@
 // What bounds it: HBM from about 80 MB of weights on (49152 x 6144, 40 rows, 8
 // adapters of rank 16: 112 us, 5.6 TB/s; 262144 x 2560, rank 64: 262 us, 6.1 TB/s,
 // measured copy 6.8); below that the chain of preparation, stream, split tiles'
-// sums (2560 x 1536, 4 rows: 17 us, 0.5 TB/s).
+// sums (2560 x 1536, 4 rows: 13.4 us, 0.6 TB/s).
 //
 // Roles of a CTA's 6 warps, one CTA an SM: TMA producer (warp 0, one thread; a
 // ring of stages of a weight tile's 64 columns and the activations', both in the
@@ -44,6 +44,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <cmath>
 #include <mutex>
 
 #include "common.cuh"
@@ -547,6 +548,7 @@ struct Gemm {
     for (int h = 0; h < NS; ++h)
 #pragma unroll
       for (int m = 0; m < MP; ++m) v[h][m] = 0.f;
+#pragma unroll NS == 1 ? 2 : 1
     for (int bb = bf; bb <= bl; ++bb) {
       const float* g = slot(bb, t);
 #pragma unroll
@@ -727,6 +729,18 @@ int rows_padded(int M) {
 // 256 (5.6 TB/s), 163 us with 128.
 int parts(int N, int K) { return (long long)N * K >= 16ll * num_sms() * 2 * TM * KC ? 2 : 1; }
 
+// CTAs of T tiles of CW chunks: whole shares of a tile each, as many as the SMs hold
+// and no more than pay for their part of the tile's sum (a chunk takes a CTA about
+// 0.4 us, a share 0.3 to 0.8 us of the last one); every SM where that would leave
+// more than 40% of them idle. In us, with every SM: 333 x 7392, 60 rows 43 (107);
+// 2560 x 1536, 4 rows 13.4 (15.5); 4096 x 4096, 40 rows 24.6 (29.9); 12288 x 1536,
+// 20 rows 23.2 (25.4); but 10240 x 2560, 4 rows 26.6 (23.6), 53% of the SMs.
+int ctas(int T, int CW) {
+  const int sms = num_sms(), fit = sms / T, pays = std::max(1, (int)(0.75 * std::sqrt((double)CW) + 0.5));
+  if (fit >= 1 && (pays < fit || 10 * fit * T >= 6 * sms)) return T * std::min(fit, pays);
+  return (int)std::min<long long>((long long)T * CW, sms);
+}
+
 // Scratch of the fused path: sums of squares, counters, split-tile sums, planes.
 struct Scratch {
   size_t rms, cnt, fix, planes, bytes;
@@ -796,7 +810,7 @@ int lora_gemm(LoraArgs a, const void* w, void* ws, cudaStream_t st) {
   g.M = a.M; g.N = a.N; g.K = a.K; g.rank = a.rank; g.n_adapters = a.n_adapters;
   const int ns = parts(a.N, a.K), rows_t = ns * TM;
   g.T = (a.N + rows_t - 1) / rows_t;
-  g.grid = (int)std::min<long long>((long long)g.T * (Kp / KC), num_sms());
+  g.grid = ctas(g.T, Kp / KC);
   g.ids = a.ids; g.norm = a.gain != nullptr; g.eps = a.eps;
   g.rms = (const float*)(base + s.rms); g.y = a.y; g.fix = (float*)(base + s.fix);
   g.cnt = (unsigned int*)(base + s.cnt); g.err = a.err;
