@@ -52,8 +52,8 @@
 // 0.3 to 2 us); many rows, the weights: about 45 instructions a token, among them
 // random 8-byte reads of the table in shared memory, not the 1 MB a row out of
 // HBM. 262144 fp32 logits a row: 40 rows at temperature 25.9 us (1.6 TB/s; the
-// bytes alone 6.2 us), with top-k 50 26 us; 64 rows with top-p of mixed breadth 85
-// us, 40 with few likely tokens 33 us.
+// bytes alone 6.2 us), with top-k 50 26 us; 64 rows with top-p of mixed breadth 72
+// to 97 us, 40 with few likely tokens 33 us.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -1086,9 +1086,10 @@ struct Sampler {
 
   // Whether top-p's nucleus probably lies among the tokens of the bins before `bins`,
   // as far as the row's n segment maxima tell: those behind hold at most a quarter of
-  // the 1 - p that may be cut. (64 rows of 262144 of mixed breadth 85 us, 89 with a
-  // half, 94 with all of it, 91 without looking; 40 rows with few likely tokens 33 us,
-  // 64 without; 40 rows with a broad nucleus 82 us, 79 without.)
+  // the 1 - p that may be cut. (64 rows of 262144 of mixed breadth, mean of 12 draws of
+  // the rows: 81 us, 82 with an eighth, 88 with a fiftieth, 90 without looking; one
+  // draw: 85 with a quarter, 89 with a half, 94 with all of it. 40 rows with few likely
+  // tokens 33 us, 64 without; 40 rows with a broad nucleus 82 us, 79 without.)
   SPEC_DEV bool promising(int bins, int n, float p) {
     if (threadIdx.x < 2) s.seen[threadIdx.x] = 0.f;
     __syncthreads();
