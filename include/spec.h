@@ -175,13 +175,17 @@ typedef struct {
  *  min_p        > 0: of those, the tokens with w_i >= min_p (at most 1);
  *  uniform      u in [0, 1), required: the token is the lowest index at which
  *               the kept mass, summed in index order, exceeds u times the kept
- *               mass (u below 0 or NaN counts as 0, u >= 1 takes the last kept
- *               token).
+ *               mass (u below 0 or NaN counts as 0, u >= 1 takes the last token
+ *               that adds to it).
  * Values outside these ranges (NaN included) leave top_k, top_p and min_p off.
- * Weights are held in 44 fraction bits of the largest (smaller ones count as
- * zero), to a relative 2^-36 (at temperatures up to 1e30), and summed exactly: a result does not depend on
- * timing, and is the 64-bit one unless u or a filter falls that near to a
- * border. -inf logits are never chosen; +inf logits share the whole mass
+ * Weights are held to a relative 2^-36 (at temperatures up to 1e30), in 44
+ * fraction bits of the largest (smaller ones count as zero), and summed exactly.
+ * (In a row that no filter cuts, the 44 bits are those of the largest of its 4096
+ * tokens from a multiple of 4096 on, and the mass of each such part up to a token
+ * is rounded down to 44 bits of the row's largest.) A result is the 64-bit one
+ * unless u or a filter falls that near to a border; it depends neither on timing
+ * nor on the other rows, the row's address or filters that leave the row as it
+ * is. -inf logits are never chosen; +inf logits share the whole mass
  * equally; a row with a NaN, or with nothing above -inf, has no distribution. */
 typedef struct {
     const float *temperature;

@@ -16,16 +16,19 @@
 // token distributed as p without d.
 //
 // Weights are integers: w_i in units of 2^-44 of the largest, rounded (a
-// choice: tokens below 2^-45 of the most likely one count as zero). Their sums
+// choice: tokens below 2^-45 of the most likely one count as zero). In rows without
+// filters they are in units of 2^-44 of the largest of their chunk, the 4096 tokens
+// from a multiple of 4096 on, and the mass up to a token is rounded down to the row's
+// units in its chunk: a chunk's sum needs no other chunk's maximum. The sums
 // are exact, so the cut and the token do not depend on the order of the
-// additions or the number of CTAs. The weight itself is evaluated to about 2^-37
+// additions, the number of CTAs, the other rows or the row's address. The weight itself is evaluated to about 2^-37
 // (the exponent as a float pair, a table of 4096 powers), because a token is
 // decided by a sum of up to V weights next to a border: at the 2^-24 of plain
 // floats about one token in 10^4 would differ from the 64-bit definition; here
 // none of 27600 rows of 4096 to 262144 tokens did.
 //
-// Large calls without filters: a first kernel takes the rows in chunks of 4096
-// tokens, in one pass that leaves each chunk's maximum and the sum of its weights,
+// Large calls without filters: a first kernel takes the rows' chunks, in one pass
+// that leaves each chunk's maximum and the sum of its weights,
 // relative to that maximum; it loads the SMs evenly, with the next chunk's loads
 // in flight under the exponentials of the last. A CTA a row then adds the sums
 // up in the row's units, finds the drawn chunk and draws inside it.
@@ -33,7 +36,8 @@
 // Otherwise a thread-block cluster takes a row; its CTAs push what the others
 // need into their shared memory, so that a phase costs one cluster barrier. Scan
 // 1 finds the maximum and the maxima of the row's segments (up to 1024). Without
-// top-k and top-p, scan 2 sums the weights and the warp that holds the drawn mass
+// filters, the CTAs share the row's chunks and the first one draws, as above. With
+// min-p alone, scan 2 sums the weights and the warp that holds the drawn mass
 // finds the token. With top-k, scan 2 lists the tokens down to the k-th largest
 // segment maximum -- at least k tokens, and rarely many more -- and the first CTA
 // cuts and draws among those alone. With top-p alone, where the segment maxima
@@ -81,7 +85,9 @@ constexpr int MAX_C = 16;           // CTAs on one row (a thread-block cluster)
 constexpr int FEW = 2048;           // tokens a CTA lists, and the first one cuts
 constexpr int COUNTED = NT / 2;     // at most so many are counted instead
 constexpr int HEAD = 128;           // segment maxima among which top-p looks first
-constexpr int CHUNK_TOKENS = 4096;  // tokens of a chunk of the chunk kernel
+constexpr int CHUNK_TOKENS = 4096;  // tokens of a chunk of a row without filters
+constexpr int MAX_CHUNKS = (1 << 19) / CHUNK_TOKENS;
+static_assert(MAX_CHUNKS <= NT, "a thread a chunk draws");
 constexpr int CNT = 256;            // its threads
 constexpr int CNW = CNT / 32;
 constexpr int SEG_MAX = 1024;       // segments of a row (the elements of 1, 2, 4 or 8 lanes)
@@ -119,12 +125,25 @@ struct Cut {
   int idx;
 };
 
+// What a CTA shares while it draws from a row's chunks.
+struct Drawn {
+  ull wsum[NW];
+  ull before, factor, total;   // mass ahead of the drawn chunk, its units, the row's mass
+  uint32_t top;                // key of the chunk's maximum
+  int chunk, shift;
+};
+
 struct Shared {
   ull tab[TAB];
   union {
     unsigned int hist[BINS];     // counts
     ull mass[BINS];              // radix search inside some bins
     ull sort[FEW];               // first CTA: the tokens all listed
+    struct {                     // first CTA of a row without filters
+      ull sum[MAX_CHUNKS];       // pushed: its chunks' sums
+      uint32_t top[MAX_CHUNKS];  // and keys of their maxima
+      Drawn drawn;
+    } chunks;
   };
   uint32_t list_key[FEW];
   int list_idx[FEW];
@@ -466,6 +485,67 @@ struct Part {
     for (int i = max(0, -i0); i < E && i0 + i < V; ++i) f(i0 + i, one(p + i0 + i));
   }
 };
+
+// What the chunk kernel leaves of a chunk.
+struct __align__(16) Record {
+  ull sum;         // weights relative to the chunk's maximum
+  ull best;        // packed maximum, 0: nothing above -inf (its index in greedy rows only)
+  int nan;
+};
+
+// A vector of a row, -inf where the row does not fill it.
+template <typename T>
+SPEC_DEV uint4 row_vector(const T* p, int V, int mis, int v) {
+  constexpr int E = 16 / sizeof(T);
+  const int i0 = v * E - mis;
+  if (i0 >= 0 && i0 + E <= V) return *reinterpret_cast<const uint4*>(p + i0);
+  uint32_t w[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) w[j] = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;
+#pragma unroll
+  for (int i = 0; i < E; ++i)
+    if (i0 + i >= 0 && i0 + i < V) {
+      if (sizeof(T) == 4) {
+        w[i & 3] = *reinterpret_cast<const uint32_t*>(p + i0 + i);
+      } else {
+        const int sft = 16 * (i & 1);
+        w[(i >> 1) & 3] = (w[(i >> 1) & 3] & (0xffff0000u >> sft)) |
+                          ((uint32_t)*reinterpret_cast<const uint16_t*>(p + i0 + i) << sft);
+      }
+    }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// The first n elements of b, then a's from n on.
+template <typename T>
+SPEC_DEV uint4 merge(const uint4& a, const uint4& b, int n) {
+  auto word = [&](uint32_t x, uint32_t y, int j) {
+    const int by = n * (int)sizeof(T) - 4 * j;   // bytes of b in this word
+    return by <= 0 ? x : by >= 4 ? y : (y & 0xffffu) | (x & 0xffff0000u);
+  };
+  return make_uint4(word(a.x, b.x, 0), word(a.y, b.y, 1), word(a.z, b.z, 2), word(a.w, b.w, 3));
+}
+
+// Tokens v * E to (v + 1) * E - 1 of a row whose first one lies `mis` elements behind
+// a 16-byte boundary, -inf past its end.
+template <typename T>
+SPEC_DEV uint4 token_vector(const T* p, int V, int mis, int v) {
+  const uint4 a = row_vector(p, V, mis, v);
+  if (mis == 0) return a;
+  const uint4 b = row_vector(p, V, mis, v + 1);
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  const int by = mis * (int)sizeof(T), words = by >> 2;
+  uint32_t x[5];
+#pragma unroll
+  for (int i = 0; i < 5; ++i) x[i] = words == 0 ? w[i] : words == 1 ? w[i + 1] : words == 2 ? w[i + 2] : w[i + 3];
+  const int bits = (by & 2) * 8;
+  return make_uint4(__funnelshift_r(x[0], x[1], bits), __funnelshift_r(x[1], x[2], bits),
+                    __funnelshift_r(x[2], x[3], bits), __funnelshift_r(x[3], x[4], bits));
+}
+
+// Chunks of a row: of the tokens, wherever the row starts.
+__host__ __device__ inline int row_chunks(int V) { return (V + CHUNK_TOKENS - 1) / CHUNK_TOKENS; }
+
 
 // Warp sum of values below 2^63, three hardware reductions of 21 bits each.
 SPEC_DEV ull warp_sum_u64(ull v) {
@@ -1289,6 +1369,59 @@ struct Sampler {
     return s.found;
   }
 
+  // Of a row without filters: the sums of this CTA's chunks and the keys of their
+  // maxima, pushed to the first CTA, as the chunk kernel leaves them.
+  SPEC_DEV void chunk_sums() {
+    constexpr int E = Part<T>::E, PER = CHUNK_TOKENS / E, NV = PER / NT;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, chunks = row_chunks(part.V);
+    auto& to = cl.map_shared_rank(&s, 0)->chunks;
+    uint4 q[NV], next[NV];
+    auto load = [&](int c, uint4 (&v)[NV]) {
+      if (c >= chunks) return;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) v[j] = token_vector(part.p, part.V, part.mis, c * PER + j * NT + threadIdx.x);
+    };
+    load(cta, q);
+#pragma unroll 1
+    for (int c = cta; c < chunks; c += C) {
+      load(c + C, next);
+      float bx = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int i = 0; i < E; ++i) bx = fmaxf(bx, Part<T>::get(q[j], i));
+      uint32_t key = __reduce_max_sync(FULL, bx > -INFINITY ? ord_key(bx + 0.f) : 0u);
+      if (lane == 0) s.list_key[warp] = key;
+      __syncthreads();
+      key = __reduce_max_sync(FULL, s.list_key[lane & (NW - 1)]);
+      ull sum = 0;
+      if (key) {
+        Scale in = sc;
+        in.m = ord_val(key);
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+          for (int i = 0; i < E; i += 2) {
+            ull w0, w1;
+            weight2(in, s.tab, Part<T>::get(q[j], i), Part<T>::get(q[j], i + 1), w0, w1);
+            sum += w0 + w1;
+          }
+        sum = warp_sum_u64(sum);
+      }
+      if (lane == 0) s.wsum[warp] = sum;
+      __syncthreads();
+      if (warp == 0) {
+        sum = warp_sum_u64(lane < NW ? s.wsum[lane] : 0ull);
+        if (lane == 0) {
+          to.sum[c] = sum;
+          to.top[c] = key;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < NV; ++j) q[j] = next[j];
+    }
+  }
+
   // The first CTA's end of the usual case: the n listed tokens, the row's best, are
   // cut and drawn from in index order. Top-p takes the row's whole mass between
   // least and most, or with `tail` that of the tokens behind those (0: top-k); -1
@@ -1329,13 +1462,6 @@ struct Sampler {
   }
 };
 
-// What the chunk kernel leaves of a chunk.
-struct __align__(16) Record {
-  ull sum;         // weights relative to the chunk's maximum
-  ull best;        // packed maximum, 0: nothing above -inf
-  int nan;
-};
-
 // log2(e) / T as a float pair.
 SPEC_DEV void scale_of(float temp, float& sh, float& sl) {
   constexpr float L = 1.44269502f;                                   // log2(e) rounded
@@ -1344,33 +1470,8 @@ SPEC_DEV void scale_of(float temp, float& sh, float& sl) {
   sl = (fmaf(-sh, temp, L) + L_LO) / temp;
 }
 
-// A vector of a row, -inf where the row does not fill it.
-template <typename T>
-SPEC_DEV uint4 row_vector(const T* p, int V, int mis, int v) {
-  constexpr int E = 16 / sizeof(T);
-  const int i0 = v * E - mis;
-  if (i0 >= 0 && i0 + E <= V) return *reinterpret_cast<const uint4*>(p + i0);
-  uint32_t w[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) w[j] = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;
-#pragma unroll
-  for (int i = 0; i < E; ++i)
-    if (i0 + i >= 0 && i0 + i < V) {
-      if (sizeof(T) == 4) {
-        w[i & 3] = *reinterpret_cast<const uint32_t*>(p + i0 + i);
-      } else {
-        const int sft = 16 * (i & 1);
-        w[(i >> 1) & 3] = (w[(i >> 1) & 3] & (0xffff0000u >> sft)) |
-                          ((uint32_t)*reinterpret_cast<const uint16_t*>(p + i0 + i) << sft);
-      }
-    }
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-// Chunks per row: enough for any alignment of its first token.
-__host__ __device__ inline int row_chunks(int V) { return (V + 7 + CHUNK_TOKENS - 1) / CHUNK_TOKENS; }
-
-template <typename T>
+// ALIGNED: every row starts on 16 bytes.
+template <typename T, bool ALIGNED>
 __global__ void __launch_bounds__(CNT, 4) chunk_kernel(SampleArgs a, Record* records) {
   constexpr int E = 16 / sizeof(T), PER = CHUNK_TOKENS / E, NV = PER / CNT;
   extern __shared__ __align__(16) unsigned char smem_raw[];
@@ -1384,13 +1485,16 @@ __global__ void __launch_bounds__(CNT, 4) chunk_kernel(SampleArgs a, Record* rec
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int n = row_chunks(a.V), items = a.M * n;
   grid_dep_wait();
-  uint4 q[NV], next[NV];
+  // A chunk's vectors, as they lie in memory. Where its first token does not start one,
+  // the first vector begins with tokens of the chunk before, and as many of this one's
+  // are left in the vector behind the last (`tail`): they take those places.
+  uint4 q[NV], next[NV], tail = {}, tail_next = {};
   float temp = 0.f, temp_next = 0.f;
-  auto load = [&](int item, uint4 (&v)[NV], float& t) {
+  auto load = [&](int item, uint4 (&v)[NV], uint4& behind, float& t) {
     if (item >= items) return;
     const int row = item / n, c = item - row * n;
     const T* p = (const T*)a.logits + (size_t)row * a.ld;
-    const int mis = (int)(((uintptr_t)p & 15) / sizeof(T));
+    const int mis = ALIGNED ? 0 : (int)(((uintptr_t)p & 15) / sizeof(T));
     const int i0 = c * CHUNK_TOKENS - mis;
     if (i0 >= 0 && i0 + CHUNK_TOKENS <= a.V) {   // for the whole CTA: plain loads, nothing to merge
 #pragma unroll
@@ -1399,16 +1503,18 @@ __global__ void __launch_bounds__(CNT, 4) chunk_kernel(SampleArgs a, Record* rec
 #pragma unroll
       for (int j = 0; j < NV; ++j) v[j] = row_vector(p, a.V, mis, c * PER + j * CNT + threadIdx.x);
     }
+    if (mis && threadIdx.x == 0) behind = row_vector(p, a.V, mis, (c + 1) * PER);
     t = a.temperature ? a.temperature[row] : 1.f;
   };
-  load(blockIdx.x, q, temp);
+  load(blockIdx.x, q, tail, temp);
   asm volatile("cp.async.wait_all;" ::: "memory");
   __syncthreads();
   int turn = 0;
   for (int item = blockIdx.x; item < items; item += gridDim.x, turn ^= 1) {
-    load(item + gridDim.x, next, temp_next);
+    load(item + gridDim.x, next, tail_next, temp_next);
     const int row = item / n, c = item - row * n;
-    const int mis = (int)(((uintptr_t)((const T*)a.logits + (size_t)row * a.ld) & 15) / sizeof(T));
+    const int mis = ALIGNED ? 0 : (int)(((uintptr_t)((const T*)a.logits + (size_t)row * a.ld) & 15) / sizeof(T));
+    if (mis && threadIdx.x == 0) q[0] = merge<T>(q[0], tail, mis);
     float bx = -INFINITY;
 #pragma unroll
     for (int j = 0; j < NV; ++j)
@@ -1427,7 +1533,10 @@ __global__ void __launch_bounds__(CNT, 4) chunk_kernel(SampleArgs a, Record* rec
       for (int j = 0; j < NV; ++j)
 #pragma unroll
         for (int i = 0; i < E; ++i)
-          if (Part<T>::get(q[j], i) == ord_val(key)) at = min(at, (uint32_t)((c * PER + j * CNT + threadIdx.x) * E - mis + i));
+          if (Part<T>::get(q[j], i) == ord_val(key)) {
+            const int place = (j * CNT + threadIdx.x) * E - mis + i;
+            at = min(at, (uint32_t)(c * CHUNK_TOKENS + (place < 0 ? place + CHUNK_TOKENS : place)));
+          }
       at = __reduce_min_sync(FULL, at);
       if (lane == 0) s_at[turn][warp] = at;
       __syncthreads();
@@ -1462,18 +1571,91 @@ __global__ void __launch_bounds__(CNT, 4) chunk_kernel(SampleArgs a, Record* rec
     }
 #pragma unroll
     for (int j = 0; j < NV; ++j) q[j] = next[j];
+    tail = tail_next;
     temp = temp_next;
   }
 }
 
-// A row of a call without filters, from its chunks' records: their sums in the
-// row's units, the chunk in which the drawn mass lies, and the token in it.
+// Draws from a row without filters: its chunks' sums in the row's units, the chunk in
+// which the drawn mass lies, and the token in it. Thread c brings chunk c's sum and the
+// key of its maximum (0: nothing above -inf, or no such chunk).
+template <typename T>
+SPEC_DEV void draw_row(const SampleArgs& a, int row, const ull* tab, const Scale& sc, float u, ull sum, uint32_t key,
+                       Drawn& d) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  auto scan = [&](ull v) {   // exclusive, in thread order
+    const ull inc = warp_scan_u64(v);
+    __syncthreads();
+    if (lane == 31) d.wsum[warp] = inc;
+    __syncthreads();
+    ull b = inc - v;
+#pragma unroll
+    for (int i = 0; i < NW; ++i)
+      if (i < warp) b += d.wsum[i];
+    return b;
+  };
+  ull v = 0, mass = 0;
+  int n = 0;
+  if (key) {
+    v = weight_parts(sc, tab, ord_val(key), n);
+    mass = in_row(sum, v, n);
+  }
+  const ull from = scan(mass);
+  if (threadIdx.x == NT - 1) d.total = from + mass;
+  __syncthreads();
+  const ull z = d.total, drawn = drawn_mass(u, z);
+  if (drawn >= from && drawn < from + mass) {
+    d.chunk = threadIdx.x;
+    d.top = key;
+    d.before = from;
+    d.factor = v;
+    d.shift = n;
+  }
+  __syncthreads();
+  // the chunk again, NV consecutive vectors a thread
+  constexpr int E = Part<T>::E, PER = CHUNK_TOKENS / E, NV = PER / NT;
+  const int c = d.chunk;
+  const ull t = drawn - d.before;
+  v = d.factor;
+  n = d.shift;
+  const T* p = (const T*)a.logits + (size_t)row * a.ld;
+  const int mis = (int)(((uintptr_t)p & 15) / sizeof(T));
+  Scale in = sc;
+  in.m = ord_val(d.top);
+  sum = 0;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const uint4 q = token_vector(p, a.V, mis, c * PER + threadIdx.x * NV + j);
+#pragma unroll
+    for (int i = 0; i < E; i += 2) {
+      ull w0, w1;
+      weight2(in, tab, Part<T>::get(q, i), Part<T>::get(q, i + 1), w0, w1);
+      sum += w0 + w1;
+    }
+  }
+  ull b = scan(sum);
+  if (in_row(b, v, n) <= t && t < in_row(b + sum, v, n)) {
+#pragma unroll 1
+    for (int i = (c * PER + threadIdx.x * NV) * E; i < a.V; ++i) {
+      const float x = Part<T>::one(p + i);
+      b += weight(in, tab, x);
+      if (t < in_row(b, v, n)) {
+        float w;
+        weight(sc, tab, x, &w);
+        a.tokens[row] = i;
+        if (a.probs) a.probs[row] = w / ((float)z * (1.f / (float)(1ull << WBITS)));
+        break;
+      }
+    }
+  }
+}
+
+// A row of a call without filters, from its chunks' records.
 template <typename T>
 __global__ void __launch_bounds__(NT) draw_kernel(SampleArgs a, const Record* records) {
   extern __shared__ __align__(16) unsigned char smem_raw[];
   ull* tab = reinterpret_cast<ull*>(smem_raw);
-  __shared__ ull wsum[NW], before, factor, total;
-  __shared__ int chunk, shift;
+  __shared__ Drawn d;
   for (int i = threadIdx.x; i < TAB / 2; i += NT) {
     const unsigned int dst = (unsigned int)__cvta_generic_to_shared(tab + 2 * i);
     asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(g_table.v + 2 * i) : "memory");
@@ -1482,32 +1664,22 @@ __global__ void __launch_bounds__(NT) draw_kernel(SampleArgs a, const Record* re
   grid_dep_wait();
   const Record* rec = records + (size_t)row * chunks;
   const float temp = a.temperature ? a.temperature[row] : 1.f, u = a.uniform[row];
-  auto scan = [&](ull v) {   // exclusive, in thread order
-    const ull inc = warp_scan_u64(v);
-    __syncthreads();
-    if (lane == 31) wsum[warp] = inc;
-    __syncthreads();
-    ull b = inc - v;
-#pragma unroll
-    for (int i = 0; i < NW; ++i)
-      if (i < warp) b += wsum[i];
-    return b;
-  };
-  ull best = 0, mine = 0;
+  ull best = 0, mine = 0, sum = 0;
   int nan = 0;
   if (threadIdx.x < chunks) {
     mine = __ldcg(&rec[threadIdx.x].best);
+    sum = __ldcg(&rec[threadIdx.x].sum);
     nan = __ldcg(&rec[threadIdx.x].nan);
   }
   {
     const uint32_t key = __reduce_max_sync(FULL, (uint32_t)(mine >> 32));
     const uint32_t idx = __reduce_max_sync(FULL, (uint32_t)(mine >> 32) == key ? (uint32_t)mine : 0u);
-    if (lane == 0) wsum[warp] = ((ull)key << 32) | idx;
+    if (lane == 0) d.wsum[warp] = ((ull)key << 32) | idx;
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
   nan = __syncthreads_or(nan);
 #pragma unroll
-  for (int i = 0; i < NW; ++i) best = wsum[i] > best ? wsum[i] : best;
+  for (int i = 0; i < NW; ++i) best = d.wsum[i] > best ? d.wsum[i] : best;
   const bool greedy = temp < 1e-5f;
   if (best == 0ull || nan || !(temp >= 0.f && temp < INFINITY) || greedy) {
     const bool ok = best != 0ull && !nan && greedy && temp >= 0.f;   // else: no distribution
@@ -1519,61 +1691,7 @@ __global__ void __launch_bounds__(NT) draw_kernel(SampleArgs a, const Record* re
   }
   Scale sc{best_value(best), 0.f, 0.f, 0.f};
   scale_of(temp, sc.sh, sc.sl);
-  ull v = 0, mass = 0;
-  int n = 0;
-  if (mine) {
-    v = weight_parts(sc, tab, best_value(mine), n);
-    mass = in_row(__ldcg(&rec[threadIdx.x].sum), v, n);
-  }
-  const ull from = scan(mass);
-  if (threadIdx.x == NT - 1) total = from + mass;
-  __syncthreads();
-  const ull z = total, d = drawn_mass(u, z);
-  if (d >= from && d < from + mass) {
-    chunk = threadIdx.x;
-    before = from;
-    factor = v;
-    shift = n;
-  }
-  __syncthreads();
-  // the chunk again, NV consecutive vectors a thread
-  constexpr int E = Part<T>::E, PER = CHUNK_TOKENS / E, NV = PER / NT;
-  const int c = chunk;
-  const ull t = d - before;
-  v = factor;
-  n = shift;
-  const T* p = (const T*)a.logits + (size_t)row * a.ld;
-  const int mis = (int)(((uintptr_t)p & 15) / sizeof(T));
-  Scale in = sc;
-  in.m = best_value(__ldcg(&rec[c].best));
-  ull sum = 0;
-#pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const uint4 q = row_vector(p, a.V, mis, c * PER + threadIdx.x * NV + j);
-#pragma unroll
-    for (int i = 0; i < E; i += 2) {
-      ull w0, w1;
-      weight2(in, tab, Part<T>::get(q, i), Part<T>::get(q, i + 1), w0, w1);
-      sum += w0 + w1;
-    }
-  }
-  ull b = scan(sum);
-  if (in_row(b, v, n) <= t && t < in_row(b + sum, v, n)) {
-#pragma unroll 1
-    for (int i = 0; i < NV * E; ++i) {
-      const int at = (c * PER + threadIdx.x * NV) * E + i - mis;
-      if (at < 0 || at >= a.V) continue;
-      const float x = Part<T>::one(p + at);
-      b += weight(in, tab, x);
-      if (t < in_row(b, v, n)) {
-        float w;
-        weight(sc, tab, x, &w);
-        a.tokens[row] = at;
-        if (a.probs) a.probs[row] = w / ((float)z * (1.f / (float)(1ull << WBITS)));
-        break;
-      }
-    }
-  }
+  draw_row<T>(a, row, tab, sc, u, sum, (uint32_t)(mine >> 32), d);
 }
 
 template <typename T>
@@ -1698,6 +1816,16 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SampleArgs a) {
     write(token, v / ((float)z * (1.f / (float)(1ull << WBITS))));
   };
 
+  if (!cuts && qw == 0) {   // no filter: as a call without any gives it
+    S.chunk_sums();
+    cl.sync();
+    if (cta == 0) {
+      const bool mine = threadIdx.x < row_chunks(a.V);
+      draw_row<T>(a, row, s.tab, S.sc, u, mine ? s.chunks.sum[threadIdx.x] : 0ull, mine ? s.chunks.top[threadIdx.x] : 0u,
+                  s.chunks.drawn);
+    }
+    return;
+  }
   if (!cuts) {
     Mass mass{S.sc, s.tab, qw, Cut{}, false};
     ull before;
@@ -1867,7 +1995,10 @@ int launch_chunked(const SampleArgs& a, int pdl, cudaStream_t st) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = pdl ? 1 : 0;
-  if (cudaLaunchKernelEx(&cfg, chunk_kernel<T>, a, (Record*)a.workspace) != cudaSuccess) return -1;
+  const bool aligned = (uintptr_t)a.logits % 16 == 0 && (a.M == 1 || a.ld * sizeof(T) % 16 == 0);
+  if (cudaLaunchKernelEx(&cfg, aligned ? chunk_kernel<T, true> : chunk_kernel<T, false>, a, (Record*)a.workspace) !=
+      cudaSuccess)
+    return -1;
   cfg.gridDim = dim3(a.M);
   cfg.blockDim = dim3(NT);
   cfg.numAttrs = 1;
@@ -1899,7 +2030,8 @@ template <typename T>
 void set_attributes() {
   cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Shared));
   cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  cudaFuncSetAttribute(chunk_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(TAB * sizeof(ull)));
+  cudaFuncSetAttribute(chunk_kernel<T, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(TAB * sizeof(ull)));
+  cudaFuncSetAttribute(chunk_kernel<T, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(TAB * sizeof(ull)));
   cudaFuncSetAttribute(draw_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(TAB * sizeof(ull)));
 }
 
