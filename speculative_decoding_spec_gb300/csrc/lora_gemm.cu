@@ -22,9 +22,13 @@
 // of G owns [U b / G, U (b + 1) / G), of small matrices whole shares of a tile; the CTA with a tile's last chunk also takes
 // the adapters' (counted on the device from the ids, by every CTA alike). A tile
 // cut between CTAs is summed by the last CTA to arrive, in CTA order. So a row's
-// result depends on neither timing, nor the other rows, nor their adapters (whose
-// chunks add exact zeros; where one holds infinities or NaN, the elements of the
-// other rows that meet them are summed again, one by one).
+// result depends on neither timing, nor the other rows, nor their adapters, whose
+// chunks add exact zeros to it. Infinities and NaN among the activations, the weights
+// or an adapter come out of the planes as NaN, an adapter's in every row: a tile with
+// a sum that is not finite is taken again, by its CTA and behind its others, where the
+// leading plane's infinities and NaN count alone and each adapter has a sum of its own
+// that only the rows that bring it take. (All of that from the start: 49152 x 6144, 64
+// rows of 64 adapters 311 us instead of 188.)
 //
 // What bounds it: HBM from about 80 MB of weights on (49152 x 6144, 40 rows, 8
 // adapters of rank 16: 112 us, 5.6 TB/s; 262144 x 2560, rank 64: 262 us, 6.1 TB/s,
@@ -73,6 +77,7 @@ constexpr unsigned SPIN_LIMIT = 1u << 26;
 struct Slots {
   int4 id[ROWS / 4];
   int slot[ROWS], used[ROWS], lead[2];
+  uint2 rows[ROWS];   // of each adapter in use: a bit a row
   int n;
 };
 SPEC_DEV void find_slots(Slots& s, const int32_t* ids, int M, int n_adapters) {
@@ -83,8 +88,8 @@ SPEC_DEV void find_slots(Slots& s, const int32_t* ids, int M, int n_adapters) {
   if (t < ROWS) reinterpret_cast<int*>(s.id)[t] = id;
   __syncthreads();
   int lead = 0;   // the first row of this row's adapter
+  unsigned int lo = 0, hi = 0;   // the rows of this adapter
   if (t < ROWS) {
-    unsigned int lo = 0, hi = 0;   // the rows of this adapter
 #pragma unroll
     for (int j = 0; j < ROWS / 4; ++j) {
       const int4 o = s.id[j];
@@ -98,18 +103,23 @@ SPEC_DEV void find_slots(Slots& s, const int32_t* ids, int M, int n_adapters) {
   }
   __syncthreads();
   if (t < ROWS) {
-    const unsigned int lo = (unsigned int)s.lead[0], hi = (unsigned int)s.lead[1];
-    const int n = lead < 32 ? __popc(lo & ((1u << lead) - 1)) : __popc(lo) + __popc(hi & ((1u << (lead - 32)) - 1));
+    const unsigned int l0 = (unsigned int)s.lead[0], l1 = (unsigned int)s.lead[1];
+    const int n = lead < 32 ? __popc(l0 & ((1u << lead) - 1)) : __popc(l0) + __popc(l1 & ((1u << (lead - 32)) - 1));
     s.slot[t] = id < 0 ? -1 : n;
-    if (id >= 0 && lead == t) s.used[n] = id;
-    if (t == 0) s.n = __popc(lo) + __popc(hi);
+    if (id >= 0 && lead == t) {
+      s.used[n] = id;
+      s.rows[n] = make_uint2(lo, hi);
+    }
+    if (t == 0) s.n = __popc(l0) + __popc(l1);
   }
   __syncthreads();
 }
 
-// v as three bf16 numbers, hi + mid + lo = v to 2^-25.
+// v as three bf16 numbers, hi + mid + lo = v to 2^-25 (hi rounds to an infinity for
+// an infinity alone).
 SPEC_DEV void split3(float v, uint16_t (&o)[3]) {
-  const __nv_bfloat16 h = __float2bfloat16_rn(v);
+  const float most = 3.38953139e38f;   // bf16's largest number
+  const __nv_bfloat16 h = __float2bfloat16_rn(fabsf(v) < INFINITY ? fmaxf(-most, fminf(v, most)) : v);
   const float r = v - __bfloat162float(h);
   const __nv_bfloat16 m = __float2bfloat16_rn(r);
   o[0] = __bfloat16_as_ushort(h);
@@ -290,6 +300,15 @@ SPEC_DEV void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
 }
 SPEC_DEV void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 SPEC_DEV void epi_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+SPEC_DEV bool epi_any(bool v) {
+  unsigned int any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(any)
+      : "r"(v ? 1u : 0u)
+      : "memory");
+  return any != 0;
+}
 
 SPEC_DEV bool wait_phase(uint64_t* b, unsigned parity, volatile int* abort_s, int* err) {
   for (unsigned it = 0; it < SPIN_LIMIT; ++it) {
@@ -313,41 +332,24 @@ struct GemmArgs {
   const float* rms;       // [M][RMS_PARTS]
   float* y;               // [M][N]
   float* fix;             // [grid][2][tile rows / TM][MP][TM]
-  unsigned int* cnt;      // [T]
+  unsigned int* cnt;      // [T] arrivals, [T] tiles to be taken again
   int* err;
-  // for the elements that are summed again
-  const __nv_bfloat16 *w, *b;   // [N][K], [n_adapters][N][rank]
-  const uint16_t* planes;       // [3][MP][KT], the adapters' columns from Kp on
-  int KT, Kp;
 };
 
-// The elements of weight rows n, n + TM, ... that are NaN, each by itself: W's part
-// and that of the row's own adapter, in the activations' values (a plane of an
-// infinity has NaN behind it).
-template <int MP>
-__device__ __noinline__ void mend(const GemmArgs& a, const Slots& sl, const float* rms_s, int n0, int n1) {
-  const size_t plane = (size_t)MP * a.KT;
-  for (int i = 0; i < a.M * 2; ++i) {
-    const int m = i >> 1, n = n0 + (i & 1) * TM, slot = sl.slot[m];
-    if (n >= n1) continue;
-    float* y = a.y + (size_t)m * a.N + n;
-    if (*(volatile float*)y == *(volatile float*)y) continue;
-    const uint16_t* x = a.planes + (size_t)m * a.KT;
-    auto val = [](uint16_t u) { return __bfloat162float(__ushort_as_bfloat16(u)); };
-    auto dot = [&](const __nv_bfloat16* w, int at, int cols) {
-      double sum = 0.0;
-      for (int c = 0; c < cols; ++c) {
-        const uint16_t* q = x + at + c;
-        const float h = val(q[0]);
-        sum += (double)__bfloat162float(w[c]) * (isfinite(h) ? h + (val(q[plane]) + val(q[2 * plane])) : h);
-      }
-      return sum;
-    };
-    double sum = dot(a.w + (size_t)n * a.K, 0, a.K);
-    if (slot >= 0)
-      sum += dot(a.b + ((size_t)sl.used[slot] * a.N + n) * a.rank, a.Kp + slot * ((a.rank + KC - 1) / KC * KC), a.rank);
-    *y = (float)sum * rms_s[m];
-  }
+// The larger magnitude, NaN if either is.
+SPEC_DEV float max_abs(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(fabsf(b)));
+  return r;
+}
+
+// A sum from its planes' sums. Where that of the leading plane is not finite it is the
+// result: an infinity among the activations or the weights has NaN in the other
+// planes (their zeros meet it, and the infinity's remainder is one).
+template <bool ODD>
+SPEC_DEV float join(uint32_t hi, uint32_t mid, uint32_t lo) {
+  const float h = __uint_as_float(hi), s = h + (__uint_as_float(mid) + __uint_as_float(lo));
+  return !ODD || fabsf(h) < INFINITY ? s : h;
 }
 
 // MMA N: the three planes of MP rows.
@@ -369,7 +371,7 @@ struct Gemm {
   unsigned char* ring;
   uint64_t *full, *empty, *accf, *acce, *drain;
   float* rms_s;
-  volatile int* abort_s;
+  volatile int *abort_s, *redo;
   int* bc;
   uint32_t tmem;
   int CW, RC, E, U, u0, u1;   // chunks of a tile: CW of W, then RC of every adapter in use, E in all
@@ -380,24 +382,42 @@ struct Gemm {
   // stream ran at half its rate.
   struct Items {
     const Gemm& k;
-    int left, t, c;   // units of W left, the pair
-    SPEC_DEV explicit Items(const Gemm& k_) : k(k_), left(k_.u1 - k_.u0), t(k_.u0 / k_.CW), c(k_.u0 - t * k_.CW - 1) {}
-    SPEC_DEV void next() {
-      if (c + 1 == k.CW + k.E) {   // the tile's last chunk, or its last adapter's
-        c = -1;
-        ++t;
+    const bool again;   // tiles to be taken again only
+    int t, c, last;     // the pair, and the CTA's last chunk of its tile
+    SPEC_DEV Items(const Gemm& k_, bool again_) : k(k_), again(again_), t(k_.u0 / k_.CW - 1), c(0), last(0) {}
+    SPEC_DEV bool next() {
+      if (c != last) {
+        ++c;
+        return true;
       }
-      if (++c < k.CW) --left;
+      for (;;) {
+        const int at = ++t * k.CW;
+        if (at >= k.u1) return false;
+        c = max(0, k.u0 - at);
+        last = at + k.CW <= k.u1 ? k.CW + k.E - 1 : k.u1 - at - 1;
+        if (!again || k.marked(t, last)) return true;
+      }
     }
-    // the pair just returned is the CTA's last of its tile
-    SPEC_DEV bool ends() const { return c == k.CW + k.E - 1 || (left == 0 && c < k.CW - 1); }
-    // and the last of a sum in tensor memory: the same chunks of W, and of a row's
-    // adapter, meet there whatever else the call holds
+    SPEC_DEV bool ends() const { return c == last; }
+    // the last of a sum in tensor memory: the same chunks of W, and of a row's adapter,
+    // meet there whatever else the call holds
     SPEC_DEV bool flushes() const {
-      return ends() || c == k.CW - 1 || ((c < k.CW ? c : c - k.CW) + 1) % FLUSH == 0;
+      if (c == last || c == k.CW - 1) return true;
+      if (c < k.CW) return (c + 1) % FLUSH == 0;
+      return again ? k.part_of(c) == k.RC - 1 : (c - k.CW + 1) % FLUSH == 0;
     }
   };
-  SPEC_DEV int items() const { return u1 - u0 + E * (u1 / CW - u0 / CW); }
+  // Tiles to be taken again: a word each behind the arrival counters, written and read
+  // by the CTA with the tile's last chunk of W; of a CTA that ends inside a tile, its
+  // part of that one (redo[1]).
+  SPEC_DEV bool marked(int t, int last) const {
+    return last < CW - 1 ? redo[1] != 0 : *(volatile unsigned int*)(a.cnt + a.T + t) != 0u;
+  }
+  SPEC_DEV void mark(int t, int last) const {
+    redo[0] = 1;
+    if (last < CW - 1) redo[1] = 1;
+    else *(volatile unsigned int*)(a.cnt + a.T + t) = 1u;
+  }
   // A place in the ring, and the parity of its turn.
   struct Slot {
     int s = 0;
@@ -420,66 +440,79 @@ struct Gemm {
   }
   // 16-column k-steps of chunk c
   SPEC_DEV int steps(int c) const {
-    return c < CW ? KC / 16 : min(KC / 16, (a.rank - (c - CW) % RC * KC + 15) / 16);
+    return c < CW ? KC / 16 : min(KC / 16, (a.rank - part_of(c) * KC + 15) / 16);
   }
+  // chunk c's adapter among those in use, and its place in it (RC is 1 or 2: ranks to 128)
+  SPEC_DEV int slot_of(int c) const { return (c - CW) >> (RC - 1); }
+  SPEC_DEV int part_of(int c) const { return (c - CW) & (RC - 1); }
   SPEC_DEV unsigned char* stage(int s) const { return ring + (size_t)s * STAGE; }
 
   SPEC_DEV void load_w(int s, const Items& it, uint64_t pol) const {
     if (it.c < CW) {
       tma_load_once(stage(s), tmw, it.c * KC, it.t * ROWS_T, &full[s], pol);
     } else {
-      const int slot = (it.c - CW) / RC;
-      tma_load_once(stage(s), tmb, (it.c - CW - slot * RC) * KC, sl.used[slot] * a.N + it.t * ROWS_T, &full[s], pol);
+      tma_load_once(stage(s), tmb, part_of(it.c) * KC, sl.used[slot_of(it.c)] * a.N + it.t * ROWS_T, &full[s], pol);
     }
   }
   SPEC_DEV void load_x(int s, const Items& it) const { tma_load(stage(s) + W_BYTES, tmx, it.c * KC, 0, &full[s]); }
 
-  SPEC_DEV void producer() {
-    const int nu = items(), pre = min(nu, a.stages);
-    const uint64_t pol = l2_evict_first();
-    Items iw(*this), ix(*this);
-    for (int n = 0; n < pre; ++n) {
-      iw.next();
-      mbar_expect_tx(&full[n], (unsigned)STAGE);
-      load_w(n, iw, pol);
-    }
-    grid_dep_wait();  // the activation planes come from the preparation
-    for (int n = 0; n < pre; ++n) {
-      ix.next();
-      load_x(n, ix);
-    }
-    int issued = pre;
+  // Where a role stands: chunks, or sums, so far, and the next place in the ring (for
+  // the producer, the next one to be emptied).
+  struct Role {
+    int n = 0;
     Slot at;
-    for (int n = pre; n < nu; ++n, at.next(a.stages)) {
-      if (!wait_phase(&empty[at.s], at.turn, abort_s, a.err)) break;
-      iw.next();
-      mbar_expect_tx(&full[at.s], (unsigned)STAGE);
-      load_w(at.s, iw, pol);
-      load_x(at.s, iw);
-      issued = n + 1;
+  };
+
+  SPEC_DEV void producer(Role& p, bool again) {
+    const uint64_t pol = l2_evict_first();
+    Items it(*this, again);
+    bool more = it.next();
+    if (!again) {   // the ring filled: the weights, and behind the wait the activations
+      Items ix(*this, false);
+      while (more && p.n < a.stages) {
+        mbar_expect_tx(&full[p.n], (unsigned)STAGE);
+        load_w(p.n++, it, pol);
+        more = it.next();
+      }
+      grid_dep_wait();  // the activation planes come from the preparation
+      for (int n = 0; n < p.n; ++n) {
+        ix.next();
+        load_x(n, ix);
+      }
+    }
+    while (more) {
+      int s = p.n;
+      if (s >= a.stages) {
+        s = p.at.s;
+        if (!wait_phase(&empty[s], p.at.turn, abort_s, a.err)) break;
+        p.at.next(a.stages);
+      }
+      mbar_expect_tx(&full[s], (unsigned)STAGE);
+      load_w(s, it, pol);
+      load_x(s, it);
+      ++p.n;
+      more = it.next();
     }
     if (*abort_s)  // this CTA's copies land before its shared memory is released
-      for (int n = max(0, issued - a.stages); n < issued; ++n) drain_phase(&full[n % a.stages], (n / a.stages) & 1);
+      for (int n = max(0, p.n - a.stages); n < p.n; ++n) drain_phase(&full[n % a.stages], (n / a.stages) & 1);
   }
 
-  SPEC_DEV void mma_loop() {
+  SPEC_DEV void mma_loop(Role& p, bool again) {
     constexpr uint32_t idesc = idesc_bf16(TM, NB);
-    const int nu = items();
-    Items it(*this);
-    int i = 0, ks = 0;     // sums so far, k-steps of the current one
+    Items it(*this, again);
+    int& i = p.n;      // sums so far
+    int ks = 0;        // k-steps of the current one
     uint32_t d = tmem;
-    Slot at;
-    for (int n = 0; n < nu; ++n, at.next(a.stages)) {
-      it.next();
+    for (; it.next(); p.at.next(a.stages)) {
       if (ks == 0) {
         const int set = i % SETS;
         if (i >= SETS && !wait_phase(&acce[set], (i / SETS - 1) & 1, abort_s, a.err)) break;
         fence_after();
         d = tmem + (uint32_t)(set * NS * ACC_COLS);
       }
-      if (!wait_phase(&full[at.s], at.turn, abort_s, a.err)) break;
+      if (!wait_phase(&full[p.at.s], p.at.turn, abort_s, a.err)) break;
       fence_after();
-      const uint32_t w = sa(stage(at.s)), x = w + (uint32_t)W_BYTES;
+      const uint32_t w = sa(stage(p.at.s)), x = w + (uint32_t)W_BYTES;
       const int ns = steps(it.c);
       const uint64_t wd = sw128_desc(w), xd = sw128_desc(x);
       auto step = [&](int j) {   // 32 bytes a k-step: 2 in the descriptors' units
@@ -495,14 +528,16 @@ struct Gemm {
         for (int j = 0; j < ns; ++j) step(j);
       }
       ks += ns;
-      mma_commit(&empty[at.s]);
+      mma_commit(&empty[p.at.s]);
       if (it.flushes()) {
         mma_commit(&accf[i % SETS]);
         ++i;
         ks = 0;
       }
     }
-    // every MMA of this CTA is complete before its tensor memory is freed
+  }
+  // Every MMA of this CTA is complete before its tensor memory is freed.
+  SPEC_DEV void mma_drain() const {
     mma_commit(drain);
     drain_phase(drain, 0);
   }
@@ -510,21 +545,14 @@ struct Gemm {
   // thread = output row n of the tile's parts, lane by lane: a warp's stores of
   // an activation row are consecutive
   SPEC_DEV void finish(int t, int r, const float (&v)[NS][MP]) const {
-    int nan = 0;
 #pragma unroll
     for (int h = 0; h < NS; ++h) {
       const int n = t * ROWS_T + h * TM + r;
       if (n >= a.N) break;
 #pragma unroll
       for (int m = 0; m < MP; ++m)
-        if (m < a.M) {
-          a.y[(size_t)m * a.N + n] = v[h][m] * rms_s[m];
-          nan |= v[h][m] != v[h][m];
-        }
+        if (m < a.M) a.y[(size_t)m * a.N + n] = v[h][m] * rms_s[m];
     }
-    // A NaN may come from another row's adapter (its infinities and NaN meet this
-    // row's zeros), or stand for an infinity: these elements are summed again.
-    if (nan) mend<MP>(a, sl, rms_s, t * ROWS_T + r, min(a.N, (t + 1) * ROWS_T));
   }
 
   SPEC_DEV float* slot(int b, int t) const {
@@ -564,8 +592,8 @@ struct Gemm {
     finish(t, r, v);
   }
 
-  SPEC_DEV void epilogue() {
-    const int e = threadIdx.x - EPI0, r = ((threadIdx.x >> 5) & 3) * 32 + (threadIdx.x & 31);
+  SPEC_DEV void row_scales() const {
+    const int e = threadIdx.x - EPI0;
     grid_dep_wait();
     if (e < ROWS) {
       float f = 1.f;
@@ -577,13 +605,59 @@ struct Gemm {
       rms_s[e] = f;
     }
     epi_sync();
+  }
+
+  // The rows that take the sum over adapters that ends with chunk c: those that bring
+  // one of them.
+  SPEC_DEV uint2 takers(int c, bool again) const {
+    const int s1 = slot_of(c);
+    uint2 r = make_uint2(0u, 0u);
+    for (int i = again ? s1 : slot_of(CW + (c - CW) / FLUSH * FLUSH); i <= s1; ++i) {
+      r.x |= sl.rows[i].x;
+      r.y |= sl.rows[i].y;
+    }
+    return r;
+  }
+  // This thread's sums of a tile's rows, from tensor memory, added to v; of those
+  // with a bit in `take` (ALL: every row).
+  template <bool ODD, bool ALL>
+  SPEC_DEV void add_sums(uint32_t acc, uint2 rows, float (&v)[NS][MP]) const {
+#pragma unroll
+    for (int h = 0; h < NS; ++h)
+#pragma unroll
+      for (int j = 0; j < MP / 8; ++j) {
+        const unsigned int take = ALL ? 0xffu : (j < 4 ? rows.x : rows.y) >> (8 * (j & 3)) & 0xffu;
+        if (!ALL && take == 0) continue;
+        uint32_t q[3][8];   // hi, mid, lo
+#pragma unroll
+        for (int p = 0; p < 3; ++p) tmem_ld8(acc + h * ACC_COLS + p * MP + 8 * j, q[p]);
+        tmem_wait_ld();
+#pragma unroll
+        for (int l = 0; l < 8; ++l)
+          if (ALL || take >> l & 1) v[h][8 * j + l] += join<ODD>(q[0][l], q[1][l], q[2][l]);
+      }
+  }
+
+  SPEC_DEV bool finite(const float (&v)[NS][MP]) const {
+    float top = 0.f;
+#pragma unroll
+    for (int m = 0; m < MP; ++m)
+      if (m < a.M)
+#pragma unroll
+        for (int h = 0; h < NS; ++h) top = max_abs(top, v[h][m]);
+    return top < INFINITY;
+  }
+
+  // p.n: sums so far, p.at.s: tiles so far
+  SPEC_DEV void epilogue(Role& p, bool again) const {
+    const int e = threadIdx.x - EPI0, r = ((threadIdx.x >> 5) & 3) * 32 + (threadIdx.x & 31);
     const uint32_t lanes = tmem + ((uint32_t)(((threadIdx.x >> 5) & 3) * 32) << 16);
-    const int nu = items();
-    Items it(*this);
-    int i = 0, tile = 0, c0 = -1;
+    Items it(*this, again);
+    int& i = p.n;
+    int& tile = p.at.s;
+    int c0 = -1;
     float v[NS][MP];
-    for (int n = 0; n < nu; ++n) {
-      it.next();
+    while (it.next()) {
       if (c0 < 0) {
         c0 = it.c;
 #pragma unroll
@@ -597,27 +671,25 @@ struct Gemm {
       epi_sync();
       if (!bc[i & 1]) break;
       fence_after();
-#pragma unroll
-      for (int h = 0; h < NS; ++h) {
-        const uint32_t taddr = lanes + (uint32_t)((set * NS + h) * ACC_COLS);
-#pragma unroll
-        for (int j = 0; j < MP / 8; ++j) {
-          uint32_t q[3][8];   // hi, mid, lo
-#pragma unroll
-          for (int p = 0; p < 3; ++p) tmem_ld8(taddr + p * MP + 8 * j, q[p]);
-          tmem_wait_ld();
-#pragma unroll
-          for (int l = 0; l < 8; ++l)
-            v[h][8 * j + l] += __uint_as_float(q[0][l]) + (__uint_as_float(q[1][l]) + __uint_as_float(q[2][l]));
-        }
+      const uint32_t acc = lanes + (uint32_t)(set * NS * ACC_COLS);
+      if (it.c < CW) {
+        if (again) add_sums<true, true>(acc, make_uint2(0u, 0u), v);
+        else add_sums<false, true>(acc, make_uint2(0u, 0u), v);
+      } else {
+        if (again) add_sums<true, false>(acc, takers(it.c, true), v);
+        else add_sums<false, false>(acc, takers(it.c, false), v);
       }
       fence_before();
       mbar_arrive(&acce[set]);
       ++i;
       if (!it.ends()) continue;
-      if (c0 == 0 && it.c >= CW - 1) finish(it.t, r, v);
-      else partial(it.t, tile, r, e, v);
-      ++tile;
+      if (!again && epi_any(!finite(v))) {
+        if (e == 0) mark(it.t, it.c);
+      } else {
+        if (c0 == 0 && it.c >= CW - 1) finish(it.t, r, v);
+        else partial(it.t, tile, r, e, v);
+        ++tile;
+      }
       c0 = -1;
     }
   }
@@ -632,7 +704,7 @@ __global__ void __launch_bounds__(NTHR, 1)
   __shared__ __align__(8) uint64_t bars[2 * MAX_STAGES + 5];
   __shared__ float rms_s[ROWS];
   __shared__ uint32_t tmem_slot;
-  __shared__ int flags[5];
+  __shared__ int flags[7];
   const uint32_t mis = sa(smem_raw) & 1023u;
   Gemm<MP, NS> k{a, &tmw, &tmb, &tmx, sl, smem_raw + (mis ? 1024 - mis : 0)};
   k.full = bars;
@@ -642,7 +714,8 @@ __global__ void __launch_bounds__(NTHR, 1)
   k.drain = k.acce + 2;
   k.rms_s = rms_s;
   k.abort_s = flags;
-  k.bc = flags + 1;
+  k.redo = flags + 1;
+  k.bc = flags + 3;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < a.stages; ++s) {
@@ -654,7 +727,7 @@ __global__ void __launch_bounds__(NTHR, 1)
       mbar_init(&k.acce[i], 128);
     }
     mbar_init(k.drain, 1);
-    flags[0] = 0;
+    flags[0] = flags[1] = flags[2] = 0;
     mbar_init_fence();
   }
   if (warp == 1) {
@@ -675,15 +748,24 @@ __global__ void __launch_bounds__(NTHR, 1)
   k.U = a.T * k.CW;
   k.u0 = k.unit_begin(blockIdx.x);
   k.u1 = k.unit_begin(blockIdx.x + 1);
-  if (warp == 0) {
-    if (lane == 0) k.producer();
-    __syncwarp();
-  } else if (warp == 1) {
-    if (lane == 0) k.mma_loop();
-    __syncwarp();
-  } else {
-    k.epilogue();
+  typename Gemm<MP, NS>::Role role;
+  if (warp >= 2) k.row_scales();
+#pragma unroll 1
+  for (int again = 0; again < 2; ++again) {
+    if (warp == 0) {
+      if (lane == 0) k.producer(role, again);
+      __syncwarp();
+    } else if (warp == 1) {
+      if (lane == 0) k.mma_loop(role, again);
+      __syncwarp();
+    } else {
+      k.epilogue(role, again);
+    }
+    __syncthreads();
+    if (!k.redo[0] || *k.abort_s) break;
   }
+  if (threadIdx.x == 32) k.mma_drain();
+  __syncwarp();
   fence_before();
   __syncthreads();
   if (warp == 1) {
@@ -751,7 +833,7 @@ Scratch scratch(int N, int K, int M, int rank) {
   Scratch s;
   s.rms = 0;
   s.cnt = s.rms + up((size_t)ROWS * RMS_PARTS * sizeof(float));
-  s.fix = s.cnt + up((size_t)((N + TM - 1) / TM) * sizeof(unsigned int));
+  s.fix = s.cnt + up((size_t)((N + TM - 1) / TM) * 2 * sizeof(unsigned int));
   s.planes = s.fix + up((size_t)num_sms() * 2 * 2 * MP * TM * sizeof(float));
   s.bytes = s.planes + up((size_t)mma_n(MP) * ((K + KC - 1) / KC * KC + (size_t)M * rc * KC) * 2);
   return s;
@@ -814,9 +896,8 @@ int lora_gemm(LoraArgs a, const void* w, void* ws, cudaStream_t st) {
   g.ids = a.ids; g.norm = a.gain != nullptr; g.eps = a.eps;
   g.rms = (const float*)(base + s.rms); g.y = a.y; g.fix = (float*)(base + s.fix);
   g.cnt = (unsigned int*)(base + s.cnt); g.err = a.err;
-  g.w = (const __nv_bfloat16*)w; g.b = (const __nv_bfloat16*)a.b; g.planes = planes; g.KT = KT; g.Kp = Kp;
   a.cnt = g.cnt;
-  a.n_cnt = g.T;
+  a.n_cnt = 2 * g.T;
   CUtensorMap tmw, tmb, tmx;
   if (!encode(&tmw, w, a.K, a.N, rows_t) ||
       !encode(&tmb, a.b, a.rank, (long long)a.n_adapters * a.N, rows_t) ||
