@@ -344,11 +344,16 @@ typedef struct {
  * of one batch bring them: y[m][n] = W[n] . xn[m] + scale_i * b_i[n] . (a_i xn[m])
  * with i = ids[m] ("device" int32 [M]; -1: no adapter for this row). W is
  * streamed once for all rows, an adapter once for the rows that use it. The
- * adapter's sums are binary32. Arguments and limits otherwise as spec_linear;
+ * adapter's sums are binary32. With bf16 weights and bf16 adapters so is the
+ * projection (activations to 2^-25), and a row's result follows from its own x and
+ * adapter alone, bit for bit; with other types, float adapters beside bf16 weights
+ * among them, it is spec_linear's (activations to 2^-17). Arguments and limits otherwise as spec_linear;
  * x, y, gain, a, b and the workspace are 16-byte aligned. workspace ("device",
  * ws_bytes >= spec_linear_lora_workspace_bytes(N, K, M, rank)) needs no
- * initialisation. An id outside [-1, n_adapters) counts as -1 and is recorded in
- * the workspace's first int (SPEC_ECAPACITY's device code 2, else 0). */
+ * initialisation. The call leaves its outcome in the workspace's first int: 0; 2
+ * (SPEC_ECAPACITY's device code) where an id was outside [-1, n_adapters), which
+ * counts as -1; 4 (SPEC_ETIMEOUT's) where a wait inside a kernel ran out: y is
+ * then undefined. */
 size_t spec_linear_lora_workspace_bytes(int32_t N, int32_t K, int32_t M, int32_t rank);
 spec_status spec_linear_lora(const spec_matrix *w, int32_t N, int32_t K, const float *x, int32_t M,
                              const float *gain, float eps, const spec_lora *lora, const int32_t *ids,

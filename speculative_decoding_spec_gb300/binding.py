@@ -18,6 +18,7 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libspec_gb3
 
 SPEC_OK, SPEC_EINVAL, SPEC_ECAPACITY, SPEC_ESTATE, SPEC_ECUDA, SPEC_ETIMEOUT, SPEC_EUNSUPPORTED = range(7)
 DTYPES = {F32: 0, BF16: 1, Q4_0: 2}
+_DEVICE_ERRORS = {0: SPEC_OK, 2: SPEC_ECAPACITY, 4: SPEC_ETIMEOUT}   # a workspace's error word
 
 EXPORTS = ["spec_workspace_bytes", "spec_init", "spec_prefill", "spec_draft", "spec_verify", "spec_step",
            "spec_decode", "spec_inject_drafts", "spec_stats", "spec_sync", "spec_set_graphs",
@@ -396,7 +397,7 @@ class Lora:
 
 def spec_linear_lora(w, x: torch.Tensor, lora: Lora, ids: torch.Tensor, gain: Optional[torch.Tensor] = None,
                      eps: float = 1e-6, layer: int = 0, y: Optional[torch.Tensor] = None,
-                     workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+                     workspace: Optional[torch.Tensor] = None, stream=None, sync: bool = False) -> torch.Tensor:
     """spec_linear plus each row's own low-rank adapter: ids int32 [M] picks one
     of lora's adapters for every row, -1 none (include/spec.h spec_linear_lora).
     workspace (uint8, spec_linear_lora_workspace_bytes) is allocated on the
@@ -428,7 +429,9 @@ def spec_linear_lora(w, x: torch.Tensor, lora: Lora, ids: torch.Tensor, gain: Op
             workspace = x.new_empty(max(n, 1), dtype=torch.uint8)
         rc = L.spec_linear_lora(C.byref(m), N, K, x.data_ptr(), M, _ptr(gain), eps, C.byref(lora.desc), ids.data_ptr(),
                                 y.data_ptr(), workspace.data_ptr(), workspace.numel(), st)
-    check(fn, rc)
+        check(fn, rc)
+        if sync:
+            check(fn, _DEVICE_ERRORS.get(int(workspace[:4].view(torch.int32)), SPEC_EINVAL))
     return y
 
 

@@ -76,8 +76,10 @@ SPEC_DEV void st_release(unsigned int* p, unsigned int v) {
   asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
 }
 
+// The first error stays, but for a timeout, which leaves the results undefined.
 SPEC_DEV void set_error(int* err, int code) {
-  if (err) atomicCAS(err, 0, code);
+  if (err && code == SPEC_ERR_TIMEOUT) atomicMax(err, code);
+  else if (err) atomicCAS(err, 0, code);
 }
 
 // Programmatic dependent launch: a kernel launched with the PDL attribute may

@@ -1012,6 +1012,7 @@ spec_status spec_linear_lora(const spec_matrix* w, int32_t N, int32_t K, const f
     if (lora_gemm(a, w->data, (char*)workspace + 256, st) < 0) return SPEC_ECUDA;
     return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ECUDA;
   }
+  g.wide.err = a.err;
   a.cnt = g.tc_cnt; a.n_cnt = (int)linear_counters(N);
   a.add = N % 4 != 0;
   g.epi = a.add ? EPI_STORE : EPI_ADD;
