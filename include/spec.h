@@ -226,7 +226,11 @@ spec_status spec_init(const spec_model_desc *model, const spec_weights *weights,
  * R <= rows_max; prompts longer than a pass (see spec_workspace_bytes) run as
  * consecutive causal passes within the call. seq_ids ("device" int32 [B])
  * name distinct slots. A caller that filled the cache itself sets seq_len
- * first and feeds the last prompt token with R = 1. */
+ * first and feeds the last prompt token with R = 1. The choice left pending is
+ * greedy. A caller that samples its first token too feeds all prompt tokens but
+ * the last (none of a prompt of one), writes that one into the slot's pending and
+ * calls spec_verify_sampled with k = 0, which emits the sampled token and leaves it
+ * pending. */
 spec_status spec_prefill(spec_ctx *ctx, int32_t B, const int32_t *seq_ids, int32_t R,
                          const int32_t *tokens, void *stream);
 

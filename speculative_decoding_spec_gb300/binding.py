@@ -401,7 +401,9 @@ def spec_linear_lora(w, x: torch.Tensor, lora: Lora, ids: torch.Tensor, gain: Op
     """spec_linear plus each row's own low-rank adapter: ids int32 [M] picks one
     of lora's adapters for every row, -1 none (include/spec.h spec_linear_lora).
     workspace (uint8, spec_linear_lora_workspace_bytes) is allocated on the
-    call's stream when not given; its first int records an id out of range."""
+    call's stream when not given; its first int records an id out of range, which
+    counts as none, or a wait that ran out. sync=True waits for the call and raises
+    what it recorded."""
     fn = "spec_linear_lora"
     L = lib()
     dev, shape = x.get_device(), x.shape
@@ -537,6 +539,9 @@ class Engine:
 
     # -- the C ABI --------------------------------------------------------------
     def spec_prefill(self, seq_ids: torch.Tensor, tokens: torch.Tensor):
+        """Feeds the prompts and leaves the greedy next token pending. To sample the
+        first token too: all prompt tokens but the last here, that one into
+        self.pending, then spec_verify_sampled with drafts of width 0."""
         self.enter()
         B, R = tokens.shape
         check("spec_prefill", lib().spec_prefill(self.ctx, B, _ptr(seq_ids), R, _ptr(tokens),
@@ -577,7 +582,8 @@ class Engine:
     def spec_verify_sampled(self, seq_ids, drafts: torch.Tensor, uniform: torch.Tensor, temperature=None, top_k=None,
                             top_p=None, min_p=None, logits: Optional[torch.Tensor] = None):
         """Sampled verify: settings [B][k+1] (or flat), None leaves one out.
-        Returns (out_tokens, n_emitted, probs)."""
+        Returns (out_tokens, n_emitted, probs). With drafts of width 0 it samples the
+        row behind the pending token, a request's first token among them."""
         B, k = drafts.shape
         M = B * (k + 1)
         # (the converted tensors live until leave() orders their reuse after the copies)
