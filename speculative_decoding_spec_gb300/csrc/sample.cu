@@ -176,7 +176,6 @@ struct Shared {
   int lo, hi, n_lo, n_hi;    // pushed: bins in which a cut may lie, tokens before and through them
   int found;                 // index found by find_in_order, written by its owner
   int base;
-  int r;                     // tokens kept of the sorted ones
 };
 
 // Scale of a row: weights are 2^-z with z = (m - x) * (sh + sl); bins are
