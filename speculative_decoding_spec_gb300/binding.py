@@ -584,18 +584,26 @@ class Engine:
         """Sampled verify: settings [B][k+1] (or flat), None leaves one out.
         Returns (out_tokens, n_emitted, probs). With drafts of width 0 it samples the
         row behind the pending token, a request's first token among them."""
+        fn, dev = "spec_verify_sampled", self.pool.get_device()
+        _need(fn, drafts.dim() == 2 and drafts.dtype is torch.int32 and drafts.is_contiguous() and
+              drafts.get_device() == dev, "drafts must be a contiguous int32 tensor [B][k] on the engine's GPU")
         B, k = drafts.shape
         M = B * (k + 1)
+        _need(fn, seq_ids.dtype is torch.int32 and seq_ids.numel() >= B and seq_ids.is_contiguous() and
+              seq_ids.get_device() == dev, "seq_ids must be a contiguous int32 tensor [B] on the engine's GPU")
+        _need(fn, logits is None or (logits.dtype is torch.float32 and logits.numel() >= M * self.shape.V and
+                                     logits.is_contiguous() and logits.get_device() == dev),
+              "logits must be a contiguous float32 tensor [B*(k+1)][V] on the engine's GPU")
         # (the converted tensors live until leave() orders their reuse after the copies)
         given = [None if t is None else torch.as_tensor(t).reshape(-1).to(self.device, dtype)
                  for (_, dtype), t in zip(_SETTINGS, (temperature, top_k, top_p, min_p, uniform))]
-        s = _sampling("spec_verify_sampled", self.pool.get_device(), M,
+        s = _sampling(fn, dev, M,
                       *(None if t is None else self._in(name, t) for (name, _), t in zip(_SETTINGS, given)))
         self.enter()
         out = self._buf("out_tokens", (B, k + 1))
         ne = self._buf("n_emitted", (B,))
         probs = self._buf("probs", (B, k + 1), torch.float32)
-        check("spec_verify_sampled", lib().spec_verify_sampled(
+        check(fn, lib().spec_verify_sampled(
             self.ctx, B, _ptr(seq_ids), k, _ptr(drafts) if k else None, C.byref(s), _ptr(out), _ptr(ne), _ptr(probs),
             _ptr(logits), self.stream.cuda_stream))
         self.leave()
