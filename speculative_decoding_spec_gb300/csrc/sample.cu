@@ -16,13 +16,13 @@
 // token distributed as p without d.
 //
 // Weights are integers: w_i in units of 2^-44 of the largest, rounded (a
-// choice: tokens below 2^-45 of the most likely one count as zero). In rows without
-// filters they are in units of 2^-44 of the largest of their chunk, the 4096 tokens
-// from a multiple of 4096 on, and the mass up to a token is rounded down to the row's
-// units in its chunk: a chunk's sum needs no other chunk's maximum. The sums
-// are exact, so the cut and the token do not depend on the order of the
-// additions, the number of CTAs, the other rows or the row's address. The weight itself is evaluated to about 2^-37
-// (the exponent as a float pair, a table of 4096 powers), because a token is
+// choice; those below 2^13 units are cut off, and below one unit count as zero). In
+// rows without filters they are in units of 2^-44 of the largest of their chunk, the
+// 4096 tokens from a multiple of 4096 on, and the mass up to a token is rounded down
+// to the row's units in its chunk: a chunk's sum needs no other chunk's maximum. The
+// sums are exact, so the cut and the token do not depend on the order of the
+// additions, the number of CTAs, the other rows or the row's address. The weight
+// itself is evaluated to about 2^-37 (the exponent as a float pair, a table of 4096 powers), because a token is
 // decided by a sum of up to V weights next to a border: at the 2^-24 of plain
 // floats about one token in 10^4 would differ from the 64-bit definition; here
 // none of 27600 rows of 4096 to 262144 tokens did.
@@ -52,10 +52,10 @@
 // search of their keys, or min-p's end lies ahead of it, and a last scan sums the
 // kept weights.
 //
-// What bounds it: one row, latency (13 us with top-k, about 20 dependent phases of
+// What bounds it: one row, latency (12 us with top-k, about 20 dependent phases of
 // 0.3 to 2 us); many rows, the weights: about 45 instructions a token, among them
 // random 8-byte reads of the table in shared memory, not the 1 MB a row out of
-// HBM. 262144 fp32 logits a row: 40 rows at temperature 25.9 us (1.6 TB/s; the
+// HBM. 262144 fp32 logits a row: 40 rows at temperature 24.9 us (1.7 TB/s; the
 // bytes alone 6.2 us), with top-k 50 26 us; 64 rows with top-p of mixed breadth 72
 // to 97 us, 40 with few likely tokens 33 us.
 #include <cooperative_groups.h>
@@ -191,7 +191,8 @@ struct Scale {
 
 // 2^(n-1), half a unit before the shift by n: a weight is rounded, not cut off.
 // (The bias of V cut-off weights would move a border among the unlikely tokens
-// by as much as their weights.) From n = 31 on a little less, within 32 bits.
+// by as much as their weights.) From n = 31 on, weights below 2^13 units, a fixed
+// amount within 32 bits: next to nothing.
 SPEC_DEV float half_unit(int n) { return __int_as_float((min(n, 30) << 23) + 0x3f000000); }
 
 // The weight of logit x in units of 2^-WBITS. z is formed as a float pair (an
@@ -1378,7 +1379,9 @@ struct Sampler {
     auto load = [&](int c, uint4 (&v)[NV]) {
       if (c >= chunks) return;
 #pragma unroll
-      for (int j = 0; j < NV; ++j) v[j] = token_vector(part.p, part.V, part.mis, c * PER + j * NT + threadIdx.x);
+      for (int j = 0; j < NV; ++j) v[j] = row_vector(part.p, part.V, part.mis, c * PER + j * NT + threadIdx.x);
+      if (part.mis && threadIdx.x == 0)   // (as the chunk kernel)
+        v[0] = merge<T>(v[0], row_vector(part.p, part.V, part.mis, (c + 1) * PER), part.mis);
     };
     load(cta, q);
 #pragma unroll 1
@@ -1815,7 +1818,9 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SampleArgs a) {
     write(token, v / ((float)z * (1.f / (float)(1ull << WBITS))));
   };
 
-  if (!cuts && qw == 0) {   // no filter: as a call without any gives it
+  // no filter: as a call without any gives it (of a row of one chunk the sum below is
+  // the same, by all CTAs: 1 x 4096 8.1 us, 9.1 by the first one alone)
+  if (!cuts && qw == 0 && a.V > CHUNK_TOKENS) {
     S.chunk_sums();
     cl.sync();
     if (cta == 0) {
@@ -1978,7 +1983,7 @@ int cluster_size(int M, int V) {
 }
 
 // Calls without filters of at least this many tokens take the chunk kernel: of
-// 262144 tokens a row, 1 row 8.9 us (16.9 without), 40 rows 25.9 us (43).
+// 262144 tokens a row, 1 row 8.2 us (15.7 without), 40 rows 24.9 us (36).
 constexpr long long CHUNKED_MIN = 1ll << 17;
 bool chunked(int M, int V) { return (long long)M * V >= CHUNKED_MIN && V >= 2 * CHUNK_TOKENS; }
 
