@@ -10,7 +10,7 @@
 // each kernel of the chain starts while the one before it runs. (Rows of y that
 // do not start on 16 bytes, N % 4 != 0, take the other order: the residual-add
 // epilogue prefetches y in 16-byte pieces.) Bound by the Q4_0 projection: 12288 x
-// 1536, 20 rows, 4 adapters of rank 32 31 us, 25 of them the projection's kernel.
+// 1536, 20 rows, 4 adapters of rank 32 30 us, 25 of them the projection's kernel.
 #include <algorithm>
 
 #include "common.cuh"

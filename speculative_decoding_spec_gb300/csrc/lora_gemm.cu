@@ -28,12 +28,12 @@
 // a sum that is not finite is taken again, by its CTA and behind its others, where the
 // leading plane's infinities and NaN count alone and each adapter has a sum of its own
 // that only the rows that bring it take. (All of that from the start: 49152 x 6144, 64
-// rows of 64 adapters 311 us instead of 188.)
+// rows of 64 adapters 311 us instead of 191.)
 //
 // What bounds it: HBM from about 80 MB of weights on (49152 x 6144, 40 rows, 8
-// adapters of rank 16: 112 us, 5.6 TB/s; 262144 x 2560, rank 64: 262 us, 6.1 TB/s,
-// measured copy 6.8); below that the chain of preparation, stream, split tiles'
-// sums (2560 x 1536, 4 rows: 13.4 us, 0.6 TB/s).
+// adapters of rank 16: 109 to 112 us, 5.7 TB/s; 262144 x 2560, rank 64: 255 to 260 us,
+// 6.2 TB/s, measured copy 6.8); below that the chain of preparation, stream, split tiles'
+// sums (2560 x 1536, 4 rows: 12.7 us, 0.6 TB/s).
 //
 // Roles of a CTA's 6 warps, one CTA an SM: TMA producer (warp 0, one thread; a
 // ring of stages of a weight tile's 64 columns and the activations', both in the

@@ -53,7 +53,7 @@
 // kept weights.
 //
 // What bounds it: one row, latency (12 us with top-k, about 20 dependent phases of
-// 0.3 to 2 us); many rows, the weights: about 45 instructions a token, among them
+// 0.3 to 2 us); many rows, the weights: about 42 instructions a token, among them
 // random 8-byte reads of the table in shared memory, not the 1 MB a row out of
 // HBM. 262144 fp32 logits a row: 40 rows at temperature 24.9 us (1.7 TB/s; the
 // bytes alone 6.2 us), with top-k 50 26 us; 64 rows with top-p of mixed breadth 72
@@ -1983,7 +1983,7 @@ int cluster_size(int M, int V) {
 }
 
 // Calls without filters of at least this many tokens take the chunk kernel: of
-// 262144 tokens a row, 1 row 8.2 us (15.7 without), 40 rows 24.9 us (36).
+// 262144 tokens a row, 1 row 8.3 us (14.0 without), 40 rows 23.1 us (33.6).
 constexpr long long CHUNKED_MIN = 1ll << 17;
 bool chunked(int M, int V) { return (long long)M * V >= CHUNKED_MIN && V >= 2 * CHUNK_TOKENS; }
 
