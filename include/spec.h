@@ -451,6 +451,142 @@ spec_status spec_accept_sampled(int32_t dtype, const void *logits, int64_t ld, i
                                 int32_t *out_tokens, int32_t *n_emitted, float *probs,
                                 void *workspace, size_t ws_bytes, void *stream);
 
+/* Attention of the rows of drafted trees over the paged cache (a kernel-level
+ * entry beside spec_attention, for trees larger than a pass of spec_verify_tree
+ * takes, rows in bf16 and sequences with trees of different sizes; "Accelerating
+ * Gemini Nano on Pixel with frozen multi-token prediction" (ai-news-spoon),
+ * "Future directions", explores branches in parallel and gives no algorithm).
+ * Sequence b has n_rows[b] rows (R where n_rows is NULL); the key and value of
+ * row r are in the cache at position len + r, len = seq_len[seq_ids[b]]. Row r
+ * attends the len committed keys, its ancestors' and its own: parents ("device"
+ * int32 [B][R]) holds each row's parent row, an earlier one, or -1; NULL is a
+ * chain (parent r - 1). Scores are q.k / sqrt(head_dim), sums and statistics
+ * binary32; with bf16 rows the probabilities enter the products in bf16 (and
+ * their sum is that of the rounded ones), with float rows to 2^-17.
+ *  m: head_dim, n_kv_heads, kv_dtype and n_layers describe the cache.
+ *  q ("device" float or bf16, q_dtype, row b*R + r at stride ldq elements, head h
+ *     at column h*head_dim, already rotated) and out (the same type, stride ldo):
+ *     16-byte aligned, strides multiples of 8, at least n_q_heads * head_dim. Rows
+ *     from n_rows on are left as they were.
+ *  workspace ("device", 16-byte aligned, ws_bytes >=
+ *     spec_attention_tree_workspace_bytes(...)) needs no initialisation; calls
+ *     sharing one must not overlap. Its first int gets the call's outcome: 0; 2
+ *     (SPEC_ECAPACITY's device code) where a slot id, a length or a row count was
+ *     out of range (that sequence's outputs stay as they were), a parent was not
+ *     an earlier row (it counts as -1) or a page id was out of range (rows of that
+ *     sequence are then undefined); 4 (SPEC_ETIMEOUT's) where a wait inside a
+ *     kernel ran out: out is then undefined.
+ * B <= 1024, R <= 64, head_dim a multiple of 8, at most 256. What lies behind a
+ * sequence's last key, and the values of rows that a row does not see, do not
+ * reach it, infinities and NaN included. */
+size_t spec_attention_tree_workspace_bytes(const spec_model_desc *m, int32_t B, int32_t R, int32_t n_q_heads,
+                                           int32_t max_pages_per_seq);
+spec_status spec_attention_tree(const spec_model_desc *m, const spec_kv_desc *kv, int32_t layer, int32_t B,
+                                const int32_t *seq_ids, const int32_t *seq_len, int32_t R, int32_t n_q_heads,
+                                const int32_t *parents, const int32_t *n_rows, int32_t q_dtype, const void *q,
+                                int64_t ldq, void *out, int64_t ldo, void *workspace, size_t ws_bytes, void *stream);
+
+/* The accepted rows of a tree moved together: position len + rows[b][i] of
+ * sequence b to len + i for i < n_keep[b], len = seq_len[seq_ids[b]], in every
+ * layer (rows "device" int32 [B][n], ascending; n_keep "device" int32 [B]). The
+ * lengths stay as they are. workspace ("device", ws_bytes >= 256): its first int
+ * gets 0, or 2 where a slot, a count, a row or a page was out of range, rows did
+ * not ascend or a slot was named twice; such a sequence is left as it was.
+ * head_dim times the type's size a multiple of 16. B <= 1024, n <= 64. */
+spec_status spec_rows_keep(const spec_model_desc *m, const spec_kv_desc *kv, int32_t B, const int32_t *seq_ids,
+                           const int32_t *seq_len, int32_t n, const int32_t *rows, const int32_t *n_keep,
+                           void *workspace, size_t ws_bytes, void *stream);
+
+/* Pages handed out, shared, given back and moved. A slot's row of the block table
+ * (which these calls write) names its pages in order, then -1; refs ("device"
+ * int32 [n_pages]) counts for each page how often tables name it, and a page that
+ * nothing names is free. Free pages are handed out lowest number first, in the
+ * order of the call's slots and their positions. A page named more than once must
+ * not be written: a forked slot shares only pages that are full, and goes on in
+ * pages of its own (a slot cut back into a shared page is forked before it is
+ * written again).
+ * Every call plans on the GPU, needs no answer from the host and can be captured.
+ * A call with a slot out of range or named twice, a table entry out of range, or
+ * more pages to hand out than are free or fit a table changes nothing; workspace
+ * ("device", 16-byte aligned, ws_bytes >= spec_pages_workspace_bytes(n_pages, n),
+ * no initialisation) gets in its first int 0, or 2 for such a call. n <= 1024
+ * slots, n_pages <= 2^20.
+ *  reserve: slot ids[i] gets pages until it has those of lens[i] positions.
+ *  release: slot ids[i] keeps the pages of its first lens[i] positions (none where
+ *    lens is NULL) and gives the others back.
+ *  fork: slot dst[i] gives its pages back and continues slot src[i] (several may
+ *    continue one; none is both): it shares the pages of seq_len[src[i]] positions
+ *    that are full and gets a page of its own, with the rows there are, for the
+ *    last one that is not. state: seq_len, pending and hid ([n_slots][m->d_model])
+ *    are copied too; pending and hid may be NULL, stats is not used.
+ *  compact: with n pages in use, those numbered n or above move to the free
+ *    numbers below, both in ascending order, in every layer. table_out and
+ *    refs_out get the tables afterwards (they may be kv->block_table and refs);
+ *    moved ("device" int32 [n_pages]) each page's new number, -1 for one that was
+ *    free; n_live ("device" int32 [1]) n. */
+size_t spec_pages_workspace_bytes(int32_t n_pages, int32_t n);
+spec_status spec_pages_reserve(const spec_kv_desc *kv, int32_t *refs, int32_t n, const int32_t *ids,
+                               const int32_t *lens, void *workspace, size_t ws_bytes, void *stream);
+spec_status spec_pages_release(const spec_kv_desc *kv, int32_t *refs, int32_t n, const int32_t *ids,
+                               const int32_t *lens, void *workspace, size_t ws_bytes, void *stream);
+spec_status spec_pages_fork(const spec_model_desc *m, const spec_kv_desc *kv, int32_t *refs, const spec_state *state,
+                            int32_t n, const int32_t *src, const int32_t *dst, void *workspace, size_t ws_bytes,
+                            void *stream);
+spec_status spec_pages_compact(const spec_model_desc *m, const spec_kv_desc *kv, int32_t *refs, int32_t *table_out,
+                               int32_t *refs_out, int32_t *moved, int32_t *n_live, void *workspace, size_t ws_bytes,
+                               void *stream);
+
+/* What changes the logits of B sequences with R rows each before they are
+ * sampled ("device"; NULL leaves a part out). Row r of sequence b follows the
+ * first hist_len[b] tokens of history row b and the tokens of the rows on its
+ * path, itself included.
+ *  history     [B] rows of n_history tokens at stride ld_history; those before
+ *              prompt_len[b] (0 where NULL) are the prompt, the others output, as
+ *              the pass's own tokens are. hist_len NULL: n_history. Entries outside
+ *              [0, V) are padding;
+ *  tokens      [B][R] the tokens fed at the pass's rows (row 0: the pending one);
+ *  parents     [B][R] as for spec_attention_tree; NULL: a chain;
+ *  repetition  [B] > 0: a token that occurs, in the prompt or the output, has
+ *              x / repetition in place of x > 0, else x * repetition;
+ *  frequency   [B] then x - count * frequency, count its occurrences in the output;
+ *  presence    [B] then x - presence where count > 0;
+ *  bias        [B][n_bias] tokens (outside [0, V): padding; of several entries for
+ *              one token the last counts) and what is added to their logits; a bias
+ *              of -inf forbids its token, NaN is none;
+ *  mask        [n_masks] rows of ceil(V / 32) words at stride ld_mask: token t is
+ *              allowed where bit t % 32 of word t / 32 is set. mask_ids [B*R] picks a
+ *              row's mask, -1 none; NULL: row m has mask m;
+ *  status      [1] set to 2 where a length, a parent or a mask id was out of range
+ *              (taken to the nearest length, as -1); else left as it was.
+ * Settings out of range or not finite are off. Forbidden tokens get -inf; a logit
+ * of -inf stays so. */
+typedef struct {
+    const int32_t *history;
+    int64_t ld_history;
+    int32_t n_history;
+    const int32_t *hist_len, *prompt_len;
+    const int32_t *tokens, *parents;
+    const float *repetition, *frequency, *presence;
+    const int32_t *bias_tokens;
+    const float *bias_values;
+    int32_t n_bias;
+    const uint32_t *mask;
+    int64_t ld_mask;
+    int32_t n_masks;
+    const int32_t *mask_ids;
+    int32_t *status;
+} spec_adjust;
+
+/* The logits ("device", dtype SPEC_F32 or SPEC_BF16, B*R rows of V at a stride of
+ * ld >= V elements) of a pass, changed as spec_adjust says, in binary32, to out (the
+ * same type, stride ld_out >= V; the logits themselves, with the same stride, or
+ * memory that does not overlap them): what spec_sample and spec_accept_sampled
+ * read next. In place, logits that stay as they are are neither read nor written.
+ * V <= 2^19, R <= 1024 (64 with parents), B <= 65535, n_history < 2^19 - 1024,
+ * n_bias <= 4095. */
+spec_status spec_adjust_logits(int32_t dtype, const void *logits, int64_t ld, int32_t B, int32_t R, int32_t V,
+                               const spec_adjust *adjust, void *out, int64_t ld_out, void *stream);
+
 /* Copy one slot's counters to the host (synchronises `stream`). */
 spec_status spec_stats(spec_ctx *ctx, int32_t slot, spec_stats_t *out, void *stream);
 

@@ -26,7 +26,10 @@ EXPORTS = ["spec_workspace_bytes", "spec_init", "spec_prefill", "spec_draft", "s
            "spec_linear_workspace_bytes", "spec_linear_noalloc", "spec_set_option",
            "spec_attention_workspace_bytes", "spec_attention", "spec_verify_topm", "spec_verify_tree",
            "spec_verify_sampled", "spec_sample", "spec_sample_workspace_bytes", "spec_accept_sampled",
-           "spec_linear_lora", "spec_linear_lora_workspace_bytes"]
+           "spec_linear_lora", "spec_linear_lora_workspace_bytes",
+           "spec_attention_tree", "spec_attention_tree_workspace_bytes", "spec_rows_keep",
+           "spec_pages_workspace_bytes", "spec_pages_reserve", "spec_pages_release", "spec_pages_fork",
+           "spec_pages_compact", "spec_adjust_logits"]
 SPEC_OPT_GRAPHS, SPEC_OPT_PREFETCH, SPEC_OPT_TEST_ATTN_WAIT = 1, 4, 8
 SPEC_OPT_WIDE_TRACE = 7
 SPEC_LINEAR_NOALLOC_MAX_ROWS = 523776
@@ -85,6 +88,14 @@ class spec_sampling(C.Structure):
 class spec_lora(C.Structure):
     _fields_ = [("dtype", C.c_int32), ("n_adapters", C.c_int32), ("rank", C.c_int32), ("a", C.c_void_p),
                 ("b", C.c_void_p), ("scale", C.c_void_p)]
+
+
+class spec_adjust(C.Structure):
+    _fields_ = [("history", C.c_void_p), ("ld_history", C.c_int64), ("n_history", C.c_int32), ("hist_len", C.c_void_p),
+                ("prompt_len", C.c_void_p), ("tokens", C.c_void_p), ("parents", C.c_void_p),
+                ("repetition", C.c_void_p), ("frequency", C.c_void_p), ("presence", C.c_void_p),
+                ("bias_tokens", C.c_void_p), ("bias_values", C.c_void_p), ("n_bias", C.c_int32), ("mask", C.c_void_p),
+                ("ld_mask", C.c_int64), ("n_masks", C.c_int32), ("mask_ids", C.c_void_p), ("status", C.c_void_p)]
 
 
 _lib = None
@@ -155,6 +166,24 @@ def lib():
     L.spec_linear_lora.restype = st
     L.spec_linear_lora.argtypes = [C.POINTER(spec_matrix), i32, i32, p, i32, p, C.c_float, C.POINTER(spec_lora), p, p,
                                    p, C.c_size_t, p]
+    z, i64 = C.c_size_t, C.c_int64
+    md, kv = C.POINTER(spec_model_desc), C.POINTER(spec_kv_desc)
+    L.spec_attention_tree_workspace_bytes.restype = z
+    L.spec_attention_tree_workspace_bytes.argtypes = [md, i32, i32, i32, i32]
+    L.spec_attention_tree.restype = st
+    L.spec_attention_tree.argtypes = [md, kv, i32, i32, p, p, i32, i32, p, p, i32, p, i64, p, i64, p, z, p]
+    L.spec_rows_keep.restype = st
+    L.spec_rows_keep.argtypes = [md, kv, i32, p, p, i32, p, p, p, z, p]
+    L.spec_pages_workspace_bytes.restype = z
+    L.spec_pages_workspace_bytes.argtypes = [i32, i32]
+    L.spec_pages_reserve.restype = L.spec_pages_release.restype = st
+    L.spec_pages_reserve.argtypes = L.spec_pages_release.argtypes = [kv, p, i32, p, p, p, z, p]
+    L.spec_pages_fork.restype = st
+    L.spec_pages_fork.argtypes = [md, kv, p, C.POINTER(spec_state), i32, p, p, p, z, p]
+    L.spec_pages_compact.restype = st
+    L.spec_pages_compact.argtypes = [md, kv, p, p, p, p, p, p, z, p]
+    L.spec_adjust_logits.restype = st
+    L.spec_adjust_logits.argtypes = [i32, p, i64, i32, i32, i32, C.POINTER(spec_adjust), p, i64, p]
     L.spec_destroy.restype = None
     L.spec_destroy.argtypes = [p]
     _lib = L
@@ -435,6 +464,265 @@ def spec_linear_lora(w, x: torch.Tensor, lora: Lora, ids: torch.Tensor, gain: Op
         if sync:
             check(fn, _DEVICE_ERRORS.get(int(workspace[:4].view(torch.int32)), SPEC_EINVAL))
     return y
+
+
+class Cache:
+    """A paged KV cache: pool [L][n_pages][2][nkv][64][hd] (float32 or bfloat16),
+    block_table int32 [n_slots][max_pages], and, for the calls that hand out
+    pages, refs int32 [n_pages] (include/spec.h spec_pages_reserve)."""
+
+    def __init__(self, pool: torch.Tensor, block_table: torch.Tensor, refs: Optional[torch.Tensor] = None):
+        fn = "Cache"
+        dt, dev = _LOGIT_DTYPES.get(pool.dtype), pool.get_device()
+        _need(fn, dev >= 0 and dt is not None and pool.dim() == 6 and pool.shape[2] == 2 and pool.shape[4] == PAGE and
+              pool.is_contiguous() and pool.numel() > 0,
+              "pool must be a contiguous float32 or bfloat16 CUDA tensor [L][n_pages][2][nkv][64][hd]")
+        _need(fn, block_table.dtype is torch.int32 and block_table.dim() == 2 and block_table.is_contiguous() and
+              block_table.get_device() == dev and block_table.numel() > 0,
+              "block_table must be a contiguous int32 tensor [n_slots][max_pages] beside the pool")
+        _need(fn, refs is None or (refs.dtype is torch.int32 and refs.shape == pool.shape[1:2] and refs.is_contiguous() and
+                                   refs.get_device() == dev), "refs must be a contiguous int32 tensor [n_pages]")
+        self.pool, self.block_table, self.refs, self.dev = pool, block_table, refs, dev
+        self.L, self.n_pages, _, self.nkv, _, self.hd = pool.shape
+        self.n_slots, self.max_pages = block_table.shape
+        self.model = spec_model_desc(self.L, 8, self.nkv, self.nkv, self.hd, 8, 2, dt, dt, 1e-6, 1e4, 0, 0, 0)
+        self.kv = spec_kv_desc(pool.data_ptr(), self.n_pages, PAGE, block_table.data_ptr(), self.max_pages, self.n_slots)
+        self.model_ref, self.kv_ref = C.byref(self.model), C.byref(self.kv)
+        self._bytes = {}
+
+    def _size(self, what, *shape):
+        """Bytes of a call's workspace, looked up once a shape."""
+        n = self._bytes.get(shape)
+        if n is None:
+            n = self._bytes[shape] = what(*shape)
+        return n
+
+
+def _ints(fn, name, t, n, dev):
+    """Address of int32 [n] (or of that many in all) on GPU `dev`."""
+    if t.dtype is not torch.int32 or t.numel() != n or t.get_device() != dev or not t.is_contiguous():
+        raise SpecError(fn, SPEC_EINVAL, "%s must be a contiguous int32 tensor of %d on the cache's GPU" % (name, n))
+    return t.data_ptr()
+
+
+def _workspace(fn, like, given, n):
+    if given is None:
+        return like.new_empty(max(n, 1), dtype=torch.uint8)
+    _need(fn, given.dtype is torch.uint8 and given.is_contiguous() and given.get_device() == like.get_device() and
+          given.numel() >= n, "workspace must be a contiguous uint8 tensor of %d bytes beside the inputs" % n)
+    return given
+
+
+def _outcome(fn, workspace):
+    check(fn, _DEVICE_ERRORS.get(int(workspace[:4].view(torch.int32)), SPEC_EINVAL))
+
+
+def spec_attention_tree(cache: Cache, layer: int, seq_ids: torch.Tensor, seq_len: torch.Tensor, q: torch.Tensor,
+                        parents: Optional[torch.Tensor] = None, n_rows: Optional[torch.Tensor] = None,
+                        out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None,
+                        sync: bool = False) -> torch.Tensor:
+    """Attention of the rows of drafted trees (include/spec.h): q [B*R][nq*hd]
+    (float32 or bfloat16, rows may be strided), parents int32 [B][R] (None: a
+    chain), n_rows int32 [B] (None: R each). Returns out in q's type; rows from
+    n_rows on are left as they were (zero where out is not given). sync=True waits
+    and raises what the call recorded."""
+    fn = "spec_attention_tree"
+    L = lib()
+    dev, B = cache.dev, seq_ids.numel()
+    dt = _LOGIT_DTYPES.get(q.dtype)
+    _need(fn, dt is not None and q.dim() == 2 and q.get_device() == dev and q.shape[0] > 0 and B > 0 and
+          q.shape[0] % B == 0 and q.shape[1] % (cache.hd * cache.nkv) == 0 and q.shape[1] > 0,
+          "q must be a float32 or bfloat16 tensor [B*R][nq*hd] beside the cache")
+    M, W = q.shape
+    R = M // B
+    ldq, step = q.stride()
+    _need(fn, step == 1 or W == 1, "the values of a row must be contiguous")
+    ldq = ldq if M > 1 else W
+    ids = _ints(fn, "seq_ids", seq_ids, B, dev)
+    lens = _ints(fn, "seq_len", seq_len, cache.n_slots, dev)
+    par = None if parents is None else _ints(fn, "parents", parents, M, dev)
+    rows = None if n_rows is None else _ints(fn, "n_rows", n_rows, B, dev)
+    with _on(dev, stream) as st:
+        if out is None:
+            out = q.new_empty((M, W)) if n_rows is None else q.new_zeros((M, W))
+        else:
+            _need(fn, out.dtype is q.dtype and out.shape == q.shape and out.get_device() == dev and
+                  (out.stride(1) == 1 or W == 1), "out must be like q")
+        n = cache._size(lambda *s: L.spec_attention_tree_workspace_bytes(cache.model_ref, *s), B, R, W // cache.hd,
+                        cache.max_pages)
+        if n == 0:
+            raise SpecError(fn, SPEC_EUNSUPPORTED)
+        workspace = _workspace(fn, q, workspace, n)
+        rc = L.spec_attention_tree(cache.model_ref, cache.kv_ref, layer, B, ids, lens, R, W // cache.hd, par, rows, dt,
+                                   q.data_ptr(), ldq, out.data_ptr(), out.stride(0) if M > 1 else W,
+                                   workspace.data_ptr(), workspace.numel(), st)
+        check(fn, rc)
+        if sync:
+            _outcome(fn, workspace)
+    return out
+
+
+def spec_rows_keep(cache: Cache, seq_ids: torch.Tensor, seq_len: torch.Tensor, rows: torch.Tensor,
+                   n_keep: torch.Tensor, workspace: Optional[torch.Tensor] = None, stream=None, sync: bool = False):
+    """The accepted rows of a tree moved together in every layer (include/spec.h):
+    rows int32 [B][n] ascending, n_keep int32 [B] of them used. seq_len stays."""
+    fn = "spec_rows_keep"
+    L = lib()
+    dev, B = cache.dev, seq_ids.numel()
+    _need(fn, rows.dim() == 2 and rows.shape[0] == B and rows.numel() > 0, "rows must be an int32 tensor [B][n]")
+    n = rows.shape[1]
+    ids, lens = _ints(fn, "seq_ids", seq_ids, B, dev), _ints(fn, "seq_len", seq_len, cache.n_slots, dev)
+    r, k = _ints(fn, "rows", rows, B * n, dev), _ints(fn, "n_keep", n_keep, B, dev)
+    with _on(dev, stream) as st:
+        workspace = _workspace(fn, rows, workspace, 256)
+        check(fn, L.spec_rows_keep(cache.model_ref, cache.kv_ref, B, ids, lens, n, r, k, workspace.data_ptr(),
+                                   workspace.numel(), st))
+        if sync:
+            _outcome(fn, workspace)
+
+
+def _pages(fn, cache, n, workspace):
+    L = lib()
+    _need(fn, cache.refs is not None, "the cache has no counts of references")
+    size = cache._size(L.spec_pages_workspace_bytes, cache.n_pages, max(n, 1))
+    if n < 1 or size == 0:
+        raise SpecError(fn, SPEC_EINVAL if n < 1 else SPEC_EUNSUPPORTED)
+    return L, _workspace(fn, cache.refs, workspace, size)
+
+
+def _pages_call(fn, cache, ids, lens, workspace, stream, sync):
+    n, dev = ids.numel(), cache.dev
+    i = _ints(fn, "seq_ids", ids, n, dev)
+    k = None if lens is None else _ints(fn, "lens", lens, n, dev)
+    with _on(dev, stream) as st:
+        L, ws = _pages(fn, cache, n, workspace)
+        check(fn, getattr(L, fn)(cache.kv_ref, cache.refs.data_ptr(), n, i, k, ws.data_ptr(), ws.numel(), st))
+        if sync:
+            _outcome(fn, ws)
+
+
+def spec_pages_reserve(cache: Cache, seq_ids: torch.Tensor, lens: torch.Tensor, workspace=None, stream=None,
+                       sync: bool = False):
+    """Slots seq_ids get pages until they have those of lens (int32 [n]) positions
+    (include/spec.h); the block table and the counts are written."""
+    _pages_call("spec_pages_reserve", cache, seq_ids, lens, workspace, stream, sync)
+
+
+def spec_pages_release(cache: Cache, seq_ids: torch.Tensor, lens: Optional[torch.Tensor] = None, workspace=None,
+                       stream=None, sync: bool = False):
+    """Slots seq_ids keep the pages of their first lens positions (None: none) and
+    give the others back."""
+    _pages_call("spec_pages_release", cache, seq_ids, lens, workspace, stream, sync)
+
+
+def spec_pages_fork(cache: Cache, seq_len: torch.Tensor, src: torch.Tensor, dst: torch.Tensor,
+                    pending: Optional[torch.Tensor] = None, hid: Optional[torch.Tensor] = None,
+                    workspace=None, stream=None, sync: bool = False):
+    """Slots dst continue slots src (int32 [n] each; include/spec.h): full pages are
+    shared, the rows of the last one copied; seq_len, pending (int32 [n_slots]) and
+    hid (float32 [n_slots][d]) are copied too."""
+    fn = "spec_pages_fork"
+    n, dev, S = dst.numel(), cache.dev, cache.n_slots
+    s, d = _ints(fn, "src", src, n, dev), _ints(fn, "dst", dst, n, dev)
+    _need(fn, hid is None or (hid.dtype is torch.float32 and hid.dim() == 2 and hid.shape[0] == S and
+                              hid.shape[1] % 8 == 0 and hid.is_contiguous() and hid.get_device() == dev),
+          "hid must be a contiguous float32 tensor [n_slots][d], d a multiple of 8, beside the cache")
+    state = spec_state(_ints(fn, "seq_len", seq_len, S, dev),
+                       None if pending is None else _ints(fn, "pending", pending, S, dev), _ptr(hid), None)
+    model = cache.model
+    if hid is not None and hid.shape[1] != model.d_model:
+        model = spec_model_desc.from_buffer_copy(model)
+        model.d_model = hid.shape[1]
+    with _on(dev, stream) as st:
+        L, ws = _pages(fn, cache, n, workspace)
+        check(fn, L.spec_pages_fork(C.byref(model), cache.kv_ref, cache.refs.data_ptr(), C.byref(state), n, s, d,
+                                    ws.data_ptr(), ws.numel(), st))
+        if sync:
+            _outcome(fn, ws)
+
+
+def spec_pages_compact(cache: Cache, block_table: Optional[torch.Tensor] = None, refs: Optional[torch.Tensor] = None,
+                       workspace=None, stream=None):
+    """The pages in use moved to the lowest numbers (include/spec.h). The tables
+    afterwards go to block_table and refs (None: the cache's own). Returns (moved
+    int32 [n_pages], n_live int32 [1])."""
+    fn = "spec_pages_compact"
+    dev = cache.dev
+    _need(fn, cache.refs is not None, "the cache has no counts of references")
+    block_table = cache.block_table if block_table is None else block_table
+    refs = cache.refs if refs is None else refs
+    t = _ints(fn, "block_table", block_table, cache.block_table.numel(), dev)
+    r = _ints(fn, "refs", refs, cache.n_pages, dev)
+    with _on(dev, stream) as st:
+        L, ws = _pages(fn, cache, 1, workspace)
+        moved, n_live = refs.new_empty(cache.n_pages), refs.new_empty(1)
+        check(fn, L.spec_pages_compact(cache.model_ref, cache.kv_ref, cache.refs.data_ptr(), t, r, moved.data_ptr(),
+                                       n_live.data_ptr(), ws.data_ptr(), ws.numel(), st))
+    return moved, n_live
+
+
+def _floats(fn, name, t, n, dev):
+    if t is None:
+        return None
+    if t.dtype is not torch.float32 or t.numel() != n or t.get_device() != dev or not t.is_contiguous():
+        raise SpecError(fn, SPEC_EINVAL, "%s must be a contiguous float32 tensor of %d beside the logits" % (name, n))
+    return t.data_ptr()
+
+
+def spec_adjust_logits(logits: torch.Tensor, R: int = 1, tokens: Optional[torch.Tensor] = None,
+                       parents: Optional[torch.Tensor] = None, history: Optional[torch.Tensor] = None,
+                       hist_len: Optional[torch.Tensor] = None, prompt_len: Optional[torch.Tensor] = None,
+                       repetition: Optional[torch.Tensor] = None, presence: Optional[torch.Tensor] = None,
+                       frequency: Optional[torch.Tensor] = None, bias_tokens: Optional[torch.Tensor] = None,
+                       bias_values: Optional[torch.Tensor] = None, mask: Optional[torch.Tensor] = None,
+                       mask_ids: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                       status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Penalties, biases and masks on the logits [B*R][V] of a pass (float32 or
+    bfloat16, rows may be strided): include/spec.h spec_adjust. history int32 [B][H]
+    (rows may be strided), bias_tokens / bias_values [B][n], mask int32 [n_masks]
+    [ceil(V/32)], the others [B] or [B*R]. Returns out (a new tensor where not
+    given, its rows on 16-byte boundaries; the logits themselves: in place)."""
+    fn = "spec_adjust_logits"
+    M, V, dt, ld, dev = _logits(fn, logits)
+    _need(fn, R >= 1 and M % R == 0, "the logits must have R rows for every sequence")
+    B = M // R
+    ints = lambda name, t, n: None if t is None else _ints(fn, name, t, n, dev)
+    s = spec_adjust()
+    if history is not None:
+        _need(fn, history.dtype is torch.int32 and history.dim() == 2 and history.shape[0] == B and
+              history.get_device() == dev and (history.stride(1) == 1 or history.shape[1] <= 1),
+              "history must be an int32 tensor [B][n] beside the logits, the tokens of a row contiguous")
+        s.history, s.n_history = history.data_ptr(), history.shape[1]
+        s.ld_history = history.stride(0) if B > 1 else history.shape[1]
+    _need(fn, (bias_tokens is None) == (bias_values is None), "bias_tokens and bias_values go together")
+    if bias_tokens is not None:
+        n = bias_tokens.numel()
+        _need(fn, n % B == 0, "bias_tokens must have a row for every sequence")
+        s.bias_tokens, s.bias_values = _ints(fn, "bias_tokens", bias_tokens, n, dev), _floats(fn, "bias_values", bias_values, n, dev)
+        s.n_bias = n // B
+    if mask is not None:
+        _need(fn, mask.dtype is torch.int32 and mask.dim() == 2 and mask.get_device() == dev and
+              mask.shape[0] > 0 and mask.shape[1] >= (V + 31) // 32 and (mask.stride(1) == 1 or mask.shape[1] == 1),
+              "mask must be an int32 tensor [n_masks][ceil(V/32)] beside the logits")
+        s.mask, s.n_masks = mask.data_ptr(), mask.shape[0]
+        s.ld_mask = mask.stride(0) if mask.shape[0] > 1 else mask.shape[1]
+        _need(fn, s.ld_mask >= (V + 31) // 32, "the masks must not overlap")
+        s.mask_ids = ints("mask_ids", mask_ids, M)
+    s.hist_len, s.prompt_len = ints("hist_len", hist_len, B), ints("prompt_len", prompt_len, B)
+    s.tokens, s.parents = ints("tokens", tokens, M), ints("parents", parents, M)
+    s.repetition, s.presence = _floats(fn, "repetition", repetition, B, dev), _floats(fn, "presence", presence, B, dev)
+    s.frequency, s.status = _floats(fn, "frequency", frequency, B, dev), ints("status", status, 1)
+    with _on(dev, stream) as st:
+        if out is None:
+            per = 16 // logits.element_size()
+            out = logits.new_empty((M, -(-V // per) * per))[:, :V]
+        else:
+            _need(fn, out.dtype is logits.dtype and out.shape == logits.shape and out.get_device() == dev and
+                  (V == 1 or out.stride(1) == 1) and (M == 1 or out.stride(0) >= V), "out must be like the logits")
+        rc = lib().spec_adjust_logits(dt, logits.data_ptr(), ld, B, R, V, C.byref(s), out.data_ptr(),
+                                      out.stride(0) if M > 1 else V if out is not logits else ld, st)
+    check(fn, rc)
+    return out
 
 
 _LINEAR_WS = {}

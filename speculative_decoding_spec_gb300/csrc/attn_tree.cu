@@ -1,0 +1,423 @@
+// attn_tree.cu -- attention of the rows of drafted trees over the paged cache:
+// the CUDA-core kernel (fp32 caches, head dims other than 64 and 128), and the
+// kernel that joins units cut between CTAs (attn_tree.cuh says how).
+//
+// Row r of sequence b, its own key and value already at position n + r of the
+// cache, attends the n committed keys and those of the rows on its path:
+//   o_r = sum_j p_j v_j / sum_j p_j,  p_j = exp(q_r . k_j / sqrt(hd) - m_r),
+// one pass over the keys with the running maximum m_r, sum and row of o, in fp32.
+//
+// A CTA of 256 threads holds 16 * TR query rows and walks its pages: the scores
+// of a page are a TR x 4 tile a thread (K transposed in shared memory, so a
+// step of the head dim is two vector loads for 4 * TR products), the
+// probabilities go through shared memory, the output is TR rows x 4 dims x NJ
+// a thread. 16 rows a tile where a KV head has no more.
+#include <algorithm>
+
+#include "attn_tree.cuh"
+
+namespace spec {
+namespace tree {
+namespace {
+
+constexpr int NTHR = 256;
+
+SPEC_DEV float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+SPEC_DEV float4 load4(const __nv_bfloat16* p) {
+  const uint2 w = *reinterpret_cast<const uint2*>(p);
+  return make_float4(bf16lo(w.x), bf16hi(w.x), bf16lo(w.y), bf16hi(w.y));
+}
+SPEC_DEV void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
+SPEC_DEV void store4(__nv_bfloat16* p, float4 v) {
+  __nv_bfloat162 x = __floats2bfloat162_rn(v.x, v.y), y = __floats2bfloat162_rn(v.z, v.w);
+  *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<uint32_t*>(&x), *reinterpret_cast<uint32_t*>(&y));
+}
+SPEC_DEV float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+constexpr int KLD = PAGE + 4;  // row of the transposed keys, a multiple of 16 bytes
+size_t cc_smem(int hd, int TR) {
+  const int rows = 16 * TR;
+  return ((size_t)hd * rows + (size_t)hd * KLD + (size_t)PAGE * hd + (size_t)PAGE * (rows + 4)) * 4;
+}
+
+template <typename QT, typename KT, int TR, int NJ>
+__global__ void __launch_bounds__(NTHR) tree_cc_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Plan p) {
+  constexpr int ROWS = 16 * TR, PLD = ROWS + 4;
+  extern __shared__ __align__(16) float sm[];
+  __shared__ long long pre[TREE_B_MAX + 1];
+  __shared__ unsigned long long path[64];
+  __shared__ int up[64];
+  grid_dep_launch();
+  const int t = threadIdx.x, tx = t & 15, ty = t >> 4, hd = a.hd, G = a.nq / a.nkv;
+  float* qs = sm;                 // [hd][ROWS]
+  float* ks = qs + hd * ROWS;     // [hd][KLD]
+  float* vs = ks + hd * KLD;      // [PAGE][hd]
+  float* ps = vs + PAGE * hd;     // [PAGE][PLD]
+  if (t < 32) prefix(a, p, pre);
+  __syncthreads();
+  if (blockIdx.x == 0) {
+    const int bad = __syncthreads_or(bad_input(a, t, NTHR));
+    if (t == 0) *a.err = bad ? SPEC_ERR_CAPACITY : 0;
+  }
+  const long long total = pre[a.B];
+  const int ctas = ctas_of(p, total);
+  if ((int)blockIdx.x >= ctas || total == 0) return;
+  long long x = part_start(total, blockIdx.x, ctas);
+  const long long x1 = part_start(total, blockIdx.x + 1, ctas);
+  const float scale2 = LOG2E / sqrtf((float)hd);
+
+  while (x < x1) {
+    const Unit n = unit_at(a, p, pre, x);
+    const int k0 = first_block(n, x), k1 = first_block(n, x1);
+    x = n.start + (long long)n.nb * n.w;
+    if (k0 >= k1) continue;
+    const Seq s = seq_of(a, n.b);
+    const int row0 = n.u * ROWS, nrow = min(ROWS, s.rows * G - row0);
+    __syncthreads();
+    paths(a, n.b, s.rows, path, up, t, [] { __syncthreads(); });
+    for (int i = t; i < ROWS * (hd / 4); i += NTHR) {
+      const int r = i / (hd / 4), c = (i % (hd / 4)) * 4;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (r < nrow) {
+        const int qr = (row0 + r) / G, g = (row0 + r) % G;
+        v = load4((const QT*)a.q + ((size_t)n.b * a.R + qr) * a.ldq + (size_t)(n.kvh * G + g) * hd + c);
+      }
+      qs[(c + 0) * ROWS + r] = v.x * scale2;
+      qs[(c + 1) * ROWS + r] = v.y * scale2;
+      qs[(c + 2) * ROWS + r] = v.z * scale2;
+      qs[(c + 3) * ROWS + r] = v.w * scale2;
+    }
+    float m[TR], l[TR], o[TR][NJ][4];
+#pragma unroll
+    for (int i = 0; i < TR; ++i) {
+      m[i] = -INFINITY;
+      l[i] = 0.f;
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[i][j][e] = 0.f;
+    }
+    for (int k = k0; k < k1; ++k) {
+      const size_t base = ((size_t)page_of(a, s.slot, k) * 2 * a.nkv + n.kvh) * PAGE * hd;
+      const KT* kp = (const KT*)a.pool + base;
+      const KT* vp = kp + (size_t)a.nkv * PAGE * hd;
+      const int valid = min(PAGE, s.len + s.rows - k * PAGE);  // keys that are there; behind them the page holds anything
+      __syncthreads();
+      for (int i = t; i < PAGE * (hd / 4); i += NTHR) {
+        const int key = i / (hd / 4), c = (i % (hd / 4)) * 4;
+        float4 kv = make_float4(0.f, 0.f, 0.f, 0.f), vv = kv;
+        if (key < valid) {
+          kv = load4(kp + (size_t)key * hd + c);
+          vv = load4(vp + (size_t)key * hd + c);
+        }
+        ks[(c + 0) * KLD + key] = kv.x;
+        ks[(c + 1) * KLD + key] = kv.y;
+        ks[(c + 2) * KLD + key] = kv.z;
+        ks[(c + 3) * KLD + key] = kv.w;
+        *reinterpret_cast<float4*>(vs + key * hd + c) = vv;
+      }
+      __syncthreads();
+      float acc[TR][4];
+#pragma unroll
+      for (int i = 0; i < TR; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
+#pragma unroll 4
+      for (int d = 0; d < hd; ++d) {
+        const float4 kk = *reinterpret_cast<const float4*>(ks + d * KLD + 4 * tx);
+        float qq[TR];
+        if constexpr (TR == 4) {
+          const float4 v = *reinterpret_cast<const float4*>(qs + d * ROWS + 4 * ty);
+          qq[0] = v.x; qq[1] = v.y; qq[2] = v.z; qq[3] = v.w;
+        } else {
+          qq[0] = qs[d * ROWS + ty];
+        }
+#pragma unroll
+        for (int i = 0; i < TR; ++i) {
+          acc[i][0] = fmaf(qq[i], kk.x, acc[i][0]);
+          acc[i][1] = fmaf(qq[i], kk.y, acc[i][1]);
+          acc[i][2] = fmaf(qq[i], kk.z, acc[i][2]);
+          acc[i][3] = fmaf(qq[i], kk.w, acc[i][3]);
+        }
+      }
+      const bool all = (k + 1) * PAGE <= s.len;  // no key of this page is a row of the tree
+#pragma unroll
+      for (int i = 0; i < TR; ++i) {
+        const int r = ty * TR + i;
+        const unsigned long long vis =
+            r < nrow ? (all ? ~0ull : visible(path[(row0 + r) / G], s.len, k * PAGE)) : 0ull;
+        float mx = -INFINITY;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (!((vis >> (4 * tx + e)) & 1)) acc[i][e] = -INFINITY;
+          mx = fmaxf(mx, acc[i][e]);
+        }
+#pragma unroll
+        for (int w = 8; w > 0; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, w));
+        const float mn = fmaxf(m[i], mx);
+        // (nothing above -inf so far: no weights yet; a row that ends so has 0 / 0, as in the formula)
+        const float f = m[i] == -INFINITY ? 0.f : ex2(m[i] - mn), mb = mn == -INFINITY ? 0.f : mn;
+        float sum = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float pr = ex2(acc[i][e] - mb);
+          sum += pr;
+          ps[(4 * tx + e) * PLD + r] = pr;
+        }
+#pragma unroll
+        for (int w = 8; w > 0; w >>= 1) sum += __shfl_xor_sync(FULL, sum, w);
+        l[i] = l[i] * f + sum;
+        m[i] = mn;
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[i][j][e] *= f;
+      }
+      __syncthreads();
+      auto values = [&](bool some) {  // some: a row may not see a key, whose value is then left out (it may be infinite)
+        unsigned long long vis[TR];
+#pragma unroll
+        for (int i = 0; i < TR; ++i) {
+          const int r = ty * TR + i;
+          vis[i] = some && r < nrow ? visible(path[(row0 + r) / G], s.len, k * PAGE) : ~0ull;
+        }
+#pragma unroll 2
+        for (int key = 0; key < valid; ++key) {
+          float pp[TR];
+          if constexpr (TR == 4) {
+            const float4 v = *reinterpret_cast<const float4*>(ps + key * PLD + 4 * ty);
+            pp[0] = v.x; pp[1] = v.y; pp[2] = v.z; pp[3] = v.w;
+          } else {
+            pp[0] = ps[key * PLD + ty];
+          }
+#pragma unroll
+          for (int j = 0; j < NJ; ++j) {
+            const int d = 4 * tx + 64 * j;
+            if (NJ * 64 != hd && d >= hd) break;
+            const float4 v = *reinterpret_cast<const float4*>(vs + key * hd + d);
+#pragma unroll
+            for (int i = 0; i < TR; ++i) {
+              if (some && !((vis[i] >> key) & 1)) continue;
+              o[i][j][0] = fmaf(pp[i], v.x, o[i][j][0]);
+              o[i][j][1] = fmaf(pp[i], v.y, o[i][j][1]);
+              o[i][j][2] = fmaf(pp[i], v.z, o[i][j][2]);
+              o[i][j][3] = fmaf(pp[i], v.w, o[i][j][3]);
+            }
+          }
+        }
+      };
+      if (all) values(false);
+      else values(true);
+    }
+    const bool whole = k0 == 0 && k1 == n.nb;
+    const size_t slot = (size_t)(2 * blockIdx.x + (k0 == 0)) * ROWS;
+#pragma unroll
+    for (int i = 0; i < TR; ++i) {
+      const int r = ty * TR + i;
+      if (r >= nrow) continue;
+      const int qr = (row0 + r) / G, g = (row0 + r) % G;
+      const float inv = whole ? 1.f / l[i] : 1.f;
+      if (!whole && tx == 0) a.part_ml[slot + r] = make_float2(m[i], l[i]);
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        const int d = 4 * tx + 64 * j;
+        if (d >= hd) break;
+        const float4 v = make_float4(o[i][j][0] * inv, o[i][j][1] * inv, o[i][j][2] * inv, o[i][j][3] * inv);
+        if (whole) store4((QT*)a.out + ((size_t)n.b * a.R + qr) * a.ldo + (size_t)(n.kvh * G + g) * hd + d, v);
+        else store4(a.part_o + (slot + r) * hd + d, v);
+      }
+    }
+  }
+}
+
+// A warp per query row: rows of units that one CTA finished are left alone.
+template <typename QT>
+__global__ void __launch_bounds__(NTHR) tree_join_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Plan p) {
+  __shared__ long long pre[TREE_B_MAX + 1];
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, G = a.nq / a.nkv, hd = a.hd;
+  if (w == 0) prefix(a, p, pre);  // (the call's inputs are not written by the kernel before this one)
+  __syncthreads();
+  const long long total = pre[a.B];
+  const int ctas = ctas_of(p, total);
+  grid_dep_wait();
+  if (total == 0 || ctas == 1) return;
+  const int urows = p.tile * p.tpu;
+  for (long long row = (long long)blockIdx.x * (NTHR / 32) + w; row < (long long)a.B * a.R * a.nq;
+       row += (long long)gridDim.x * (NTHR / 32)) {
+    const int h = (int)(row % a.nq), r = (int)(row / a.nq % a.R), b = (int)(row / a.nq / a.R);
+    const Seq s = seq_of(a, b);
+    if (r >= s.rows) continue;
+    const int kvh = h / G, q = r * G + h % G, T = tiles_of(p, G, s.rows), nb = blocks_of(p, s);
+    Unit n;
+    n.b = b;
+    n.kvh = kvh;
+    n.u = q / urows;
+    n.nb = nb;
+    n.w = min(p.tpu, T - n.u * p.tpu);
+    n.start = pre[b] + (long long)kvh * nb * T + (long long)n.u * nb * p.tpu;
+    const long long end = n.start + (long long)nb * n.w;
+    // the first and last CTA whose parts meet the unit
+    int c0 = (int)(n.start * ctas / total), c1 = (int)((end - 1) * ctas / total);
+    while (part_start(total, c0 + 1, ctas) <= n.start) ++c0;
+    while (c1 + 1 < ctas && part_start(total, c1 + 1, ctas) < end) ++c1;
+    if (c0 == c1) continue;
+    const int at = q - n.u * urows;
+    // the pieces' maxima and sums: lane i takes the pieces i, i + 32, ...
+    float M = -INFINITY;
+    bool any = false;
+    for (int c = c0 + lane; c <= c1; c += 32) {
+      const int k0 = first_block(n, part_start(total, c, ctas)), k1 = first_block(n, part_start(total, c + 1, ctas));
+      if (k0 >= k1 || (k0 == 0 && k1 == nb)) continue;
+      M = fmaxf(M, a.part_ml[(size_t)(2 * c + (k0 == 0)) * urows + at].x);
+      any = true;
+    }
+    if (!__any_sync(FULL, any)) continue;  // one CTA had all of its blocks
+    M = warp_max(M);
+    float L = 0.f;
+    float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+    for (int c = c0; c <= c1; c += 32) {
+      const int mine = c + lane;
+      float f = 0.f, fl = 0.f;
+      int first = 0;
+      if (mine <= c1) {
+        const int k0 = first_block(n, part_start(total, mine, ctas)), k1 = first_block(n, part_start(total, mine + 1, ctas));
+        if (k0 < k1) {
+          first = k0 == 0;
+          const float2 v = a.part_ml[(size_t)(2 * mine + first) * urows + at];
+          f = v.x == -INFINITY ? 0.f : ex2(v.x - M);
+          fl = f * v.y;
+        } else {
+          first = -1;
+        }
+      }
+      L += warp_sum(fl);
+      for (int i = 0; i < 32 && c + i <= c1; ++i) {
+        const float fi = __shfl_sync(FULL, f, i);
+        const int fs = __shfl_sync(FULL, first, i);
+        if (fs < 0) continue;
+        const float* src = a.part_o + ((size_t)(2 * (c + i) + fs) * urows + at) * hd;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int d = 4 * lane + 128 * j;
+          if (d >= hd) break;
+          const float4 v = *reinterpret_cast<const float4*>(src + d);
+          acc[j].x = fmaf(fi, v.x, acc[j].x);
+          acc[j].y = fmaf(fi, v.y, acc[j].y);
+          acc[j].z = fmaf(fi, v.z, acc[j].z);
+          acc[j].w = fmaf(fi, v.w, acc[j].w);
+        }
+      }
+    }
+    const float inv = 1.f / L;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int d = 4 * lane + 128 * j;
+      if (d < hd)
+        store4((QT*)a.out + ((size_t)b * a.R + r) * a.ldo + (size_t)h * hd + d,
+               make_float4(acc[j].x * inv, acc[j].y * inv, acc[j].z * inv, acc[j].w * inv));
+    }
+  }
+}
+
+template <typename QT, typename KT, int TR>
+const void* cc_kernel(int hd) {
+  return hd <= 64 ? (const void*)tree_cc_kernel<QT, KT, TR, 1>
+                  : hd <= 128 ? (const void*)tree_cc_kernel<QT, KT, TR, 2> : (const void*)tree_cc_kernel<QT, KT, TR, 4>;
+}
+const void* cc_pick(int q_dtype, int kv_dtype, int TR, int hd) {
+  if (q_dtype == DT_F32 && kv_dtype == DT_F32)
+    return TR == 1 ? cc_kernel<float, float, 1>(hd) : cc_kernel<float, float, 4>(hd);
+  if (q_dtype == DT_F32)
+    return TR == 1 ? cc_kernel<float, __nv_bfloat16, 1>(hd) : cc_kernel<float, __nv_bfloat16, 4>(hd);
+  if (kv_dtype == DT_F32)
+    return TR == 1 ? cc_kernel<__nv_bfloat16, float, 1>(hd) : cc_kernel<__nv_bfloat16, float, 4>(hd);
+  return TR == 1 ? cc_kernel<__nv_bfloat16, __nv_bfloat16, 1>(hd) : cc_kernel<__nv_bfloat16, __nv_bfloat16, 4>(hd);
+}
+int cc_rows(const TreeArgs& a) { return a.R * (a.nq / a.nkv) <= 16 ? 1 : 4; }
+
+Plan cc_plan(const TreeArgs& a) {
+  Plan p;
+  const int TR = cc_rows(a);
+  p.blk = PAGE;
+  p.tile = 16 * TR;
+  p.tpu = 1;
+  const int per_sm = std::max(1, std::min(4, (int)(220 * 1024 / cc_smem(a.hd, TR))));
+  p.grid = num_sms() * per_sm;
+  p.min_cost = 2;
+  return p;
+}
+
+Plan plan_of(const TreeArgs& a) {
+  Plan p = cc_plan(a);
+  // no more CTAs than the axis can have blocks
+  const long long T = (a.R * (a.nq / a.nkv) + p.tile - 1) / p.tile;
+  const long long most = (long long)a.B * a.nkv * T * (((long long)a.max_pages * PAGE + p.blk - 1) / p.blk);
+  p.grid = (int)std::max<long long>(1, std::min<long long>(p.grid, (most + p.min_cost - 1) / p.min_cost));
+  return p;
+}
+
+}  // namespace
+}  // namespace tree
+
+using namespace tree;
+
+static TreeArgs shape_args(int B, int R, int nq, int nkv, int hd, int max_pages, int q_dtype, int kv_dtype) {
+  TreeArgs a = {};
+  a.B = B; a.R = R; a.nq = nq; a.nkv = nkv; a.hd = hd; a.max_pages = max_pages;
+  a.q_dtype = q_dtype; a.kv_dtype = kv_dtype;
+  return a;
+}
+static size_t part_rows(const Plan& p) { return (size_t)2 * p.grid * p.tile * p.tpu; }
+
+// error word (256 bytes), maxima and sums, rows
+size_t attn_tree_bytes(int B, int R, int nq, int nkv, int hd, int max_pages) {
+  size_t most = 0;
+  for (int q : {DT_F32, DT_BF16})
+    for (int kv : {DT_F32, DT_BF16}) {
+      const size_t rows = part_rows(plan_of(shape_args(B, R, nq, nkv, hd, max_pages, q, kv)));
+      most = std::max(most, 256 + rows * (sizeof(float2) + (size_t)hd * sizeof(float)));
+    }
+  return most;
+}
+
+void setup_attn_tree_attributes() {
+  for (int q : {DT_F32, DT_BF16})
+    for (int kv : {DT_F32, DT_BF16})
+      for (int TR : {1, 4})
+        for (int hd : {64, 128, 256})
+          cudaFuncSetAttribute(cc_pick(q, kv, TR, hd), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cc_smem(hd, TR));
+}
+
+int attn_tree(TreeArgs a, void* ws, cudaStream_t st) {
+  const Plan p = plan_of(a);
+  a.err = (int*)ws;
+  a.part_ml = (float2*)((char*)ws + 256);
+  a.part_o = (float*)(a.part_ml + part_rows(p));
+  const int TR = cc_rows(a);
+  void* args[] = {(void*)&a, (void*)&p};
+  if (cudaLaunchKernel(cc_pick(a.q_dtype, a.kv_dtype, TR, a.hd), dim3(p.grid), dim3(NTHR), args, cc_smem(a.hd, TR), st) !=
+      cudaSuccess)
+    return -1;
+  const int r = 1;
+  // a unit of at most min_cost / tiles blocks is never cut where it starts a part; with one CTA nothing is
+  if (p.grid == 1) return r;
+  cudaLaunchConfig_t cfg = {};
+  const long long rows = (long long)a.B * a.R * a.nq;
+  cfg.gridDim = dim3((unsigned)std::min<long long>((rows + NTHR / 32 - 1) / (NTHR / 32), 4ll * num_sms()));
+  cfg.blockDim = dim3(NTHR);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = a.q_dtype == DT_F32 ? cudaLaunchKernelEx(&cfg, tree_join_kernel<float>, a, p)
+                                            : cudaLaunchKernelEx(&cfg, tree_join_kernel<__nv_bfloat16>, a, p);
+  return e == cudaSuccess ? r + 1 : -1;
+}
+
+}  // namespace spec

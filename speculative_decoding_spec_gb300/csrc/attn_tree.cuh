@@ -1,0 +1,180 @@
+// attn_tree.cuh -- how the attention of drafted trees is cut into pieces, shared
+// by its kernels (attn_tree.cu, attn_tree_tc.cu) and the one that joins them.
+//
+// Sequence b has n rows, so n * G query rows on each KV head (G query heads a
+// KV head; query row i*G + g), in tiles of `tile` rows; `tpu` tiles make a unit,
+// which reads its KV head's blocks of `blk` keys once. The units of all
+// sequences, in order (sequence, KV head, unit), lie on one axis on which a
+// block of a unit has the length of the unit's tiles. CTA c takes the c-th of
+// `ctas` equal parts of that axis, so every CTA gets the same work whatever the
+// lengths; a part may end inside a unit, and may hold several.
+//
+// A unit that lies in one part is finished there. Of a unit that is cut, each
+// CTA leaves its rows' sums unnormalised, with their maxima and sums, in one of
+// its two slots (slot 2c: a piece that does not start the unit; 2c + 1: one that
+// does; a part can hold one of each), and tree_join_kernel adds them up.
+#pragma once
+#include "common.cuh"
+
+namespace spec {
+namespace tree {
+
+constexpr int PAGE = 64;
+constexpr float LOG2E = 1.4426950408889634f;
+
+struct Plan {
+  int blk, tile, tpu, grid;  // keys a block, rows a tile, tiles a unit, CTAs
+  int min_cost;              // a part is not made shorter than this
+};
+
+// Sequence b of a call: slot, committed length, rows in use. A sequence whose
+// numbers are out of range has no rows: its outputs stay as they are.
+struct Seq {
+  int slot, len, rows;
+  bool ok;
+};
+SPEC_DEV Seq seq_of(const TreeArgs& a, int b) {
+  Seq s;
+  s.slot = a.seq_ids[b];
+  s.ok = s.slot >= 0 && s.slot < a.n_slots;
+  s.len = s.ok ? a.seq_len[s.slot] : 0;
+  s.rows = a.n_rows ? a.n_rows[b] : a.R;
+  s.ok = s.ok && s.len >= 0 && s.rows >= 0 && s.rows <= a.R && (long long)s.len + s.rows <= (long long)a.max_pages * PAGE;
+  if (!s.ok) s.rows = 0;
+  return s;
+}
+SPEC_DEV int tiles_of(const Plan& p, int G, int rows) { return (rows * G + p.tile - 1) / p.tile; }
+SPEC_DEV int blocks_of(const Plan& p, const Seq& s) { return s.rows ? (s.len + s.rows + p.blk - 1) / p.blk : 0; }
+
+// pre[b] = start of sequence b on the axis, pre[B] its end. By the first warp.
+SPEC_DEV void prefix(const TreeArgs& a, const Plan& p, long long* pre) {
+  const int lane = threadIdx.x & 31;
+  const int G = a.nq / a.nkv;
+  long long run = 0;
+  for (int b0 = 0; b0 < a.B; b0 += 32) {
+    const int b = b0 + lane;
+    long long c = 0;
+    if (b < a.B) {
+      const Seq s = seq_of(a, b);
+      c = (long long)a.nkv * blocks_of(p, s) * tiles_of(p, G, s.rows);
+    }
+    long long incl = c;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(FULL, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (b < a.B) pre[b] = run + incl - c;
+    run += __shfl_sync(FULL, incl, 31);
+  }
+  if (lane == 0) pre[a.B] = run;
+}
+SPEC_DEV int ctas_of(const Plan& p, long long total) {
+  const long long most = (total + p.min_cost - 1) / p.min_cost;
+  return (int)(most < p.grid ? (most < 1 ? 1 : most) : p.grid);
+}
+SPEC_DEV long long part_start(long long total, int c, int ctas) { return total * c / ctas; }
+
+// A unit: its place on the axis and what it covers.
+struct Unit {
+  int b, kvh, u;       // sequence, KV head, unit of the pair
+  int nb, w;           // blocks, tiles
+  long long start;
+};
+SPEC_DEV int upper(const long long* pre, int B, long long x) {  // the last sequence that starts at or before x and is not empty
+  int lo = 0, hi = B;  // first index with pre > x
+  while (lo < hi) {
+    const int m = (lo + hi) >> 1;
+    if (pre[m] > x) hi = m;
+    else lo = m + 1;
+  }
+  return lo - 1;
+}
+// The unit that holds position x (< total).
+SPEC_DEV Unit unit_at(const TreeArgs& a, const Plan& p, const long long* pre, long long x) {
+  Unit n;
+  n.b = upper(pre, a.B, x);
+  const Seq s = seq_of(a, n.b);
+  const int T = tiles_of(p, a.nq / a.nkv, s.rows);
+  n.nb = blocks_of(p, s);
+  const long long pair = (long long)n.nb * T, off = x - pre[n.b];
+  n.kvh = (int)(off / pair);
+  const long long in = off - n.kvh * pair;
+  n.u = (int)(in / ((long long)n.nb * p.tpu));
+  n.w = min(p.tpu, T - n.u * p.tpu);
+  n.start = pre[n.b] + n.kvh * pair + (long long)n.u * n.nb * p.tpu;
+  return n;
+}
+// The blocks of unit n in [x0, x1) of the axis.
+SPEC_DEV int first_block(const Unit& n, long long x) {
+  if (x <= n.start) return 0;
+  const long long k = (x - n.start + n.w - 1) / n.w;
+  return k < n.nb ? (int)k : n.nb;
+}
+
+// Bit j of path[r]: row j is row r or an ancestor of it (rows below 64). By
+// threads 0 .. 63 of the CTA between barriers of all of them: `sync`. A parent
+// that is not an earlier row counts as none.
+template <class Sync>
+SPEC_DEV void paths(const TreeArgs& a, int b, int rows, unsigned long long* path, int* up, int t, Sync sync) {
+  if (t < 64) {
+    int p = -1;
+    if (t < rows) {
+      p = a.parents ? a.parents[(size_t)b * a.R + t] : t - 1;
+      if (p < 0 || p >= t) p = -1;
+    }
+    path[t] = 1ull << t;
+    up[t] = p;
+  }
+  sync();
+  for (int step = 1; step < rows; step <<= 1) {  // (pointer jumping: a path of 2^i rows after i steps)
+    unsigned long long m = 0;
+    int p = -1;
+    if (t < 64 && up[t] >= 0) {
+      m = path[up[t]];
+      p = up[up[t]];
+    }
+    sync();
+    if (t < 64) {
+      path[t] |= m;
+      up[t] = p;
+    }
+    sync();
+  }
+}
+// Which of the 64 keys from `key0` on a row with this path sees.
+SPEC_DEV unsigned long long visible(unsigned long long path, int len, int key0) {
+  const long long off = (long long)len - key0;  // committed keys from key0 on
+  if (off >= 64) return ~0ull;
+  if (off >= 0) return ((1ull << off) - 1) | (path << off);
+  return off > -64 ? path >> -off : 0ull;
+}
+
+// What a call finds wrong, by `nthr` threads (t) of one warp or CTA: sequences
+// out of range, parents that are not earlier rows, pages that are not there.
+SPEC_DEV bool bad_input(const TreeArgs& a, int t, int nthr) {
+  bool bad = false;
+  for (int b = 0; b < a.B; ++b) {
+    const Seq s = seq_of(a, b);
+    bad |= !s.ok;
+    if (a.parents)
+      for (int r = t; r < s.rows; r += nthr) {
+        const int p = a.parents[(size_t)b * a.R + r];
+        bad |= p < -1 || p >= r;
+      }
+    const int pages = s.rows ? (s.len + s.rows + PAGE - 1) / PAGE : 0;
+    for (int i = t; i < pages; i += nthr) {
+      const int g = a.block_table[(size_t)s.slot * a.max_pages + i];
+      bad |= g < 0 || g >= a.n_pages;
+    }
+  }
+  return bad;
+}
+// A page id that is out of range reads page 0 (the call records it).
+SPEC_DEV int page_of(const TreeArgs& a, int slot, int i) {
+  const int g = a.block_table[(size_t)slot * a.max_pages + i];
+  return g < 0 || g >= a.n_pages ? 0 : g;
+}
+
+}  // namespace tree
+}  // namespace spec

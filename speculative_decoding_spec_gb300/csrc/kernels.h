@@ -415,4 +415,86 @@ constexpr int ATTN_FLASH_PART_ROWS = 256 * 32;
 bool attention_flash_ok(const AttnArgs& a);
 int attention_flash(const AttnArgs& a, unsigned int* counters, int wait_extra, cudaStream_t st);
 
+// Attention of the rows of drafted trees (attn_tree.cu, attn_tree_tc.cu).
+struct TreeArgs {
+  int B, R, nq, nkv, hd;
+  int q_dtype, kv_dtype;       // DT_F32 or DT_BF16
+  const void* q;               // [B*R] rows of nq*hd at stride ldq
+  long long ldq;
+  void* out;                   // [B*R] rows of nq*hd at stride ldo, q's type
+  long long ldo;
+  const void* pool;            // this layer's pages
+  int n_pages, max_pages, n_slots;
+  const int32_t* block_table;
+  const int32_t *seq_ids, *seq_len;
+  const int32_t* parents;      // [B][R] or null (a chain)
+  const int32_t* n_rows;       // [B] or null (R)
+  int* err;
+  float* part_o;               // partial rows of split units (attn_tree.cuh)
+  float2* part_ml;
+};
+constexpr int TREE_ROWS_MAX = 64, TREE_B_MAX = 1024;
+size_t attn_tree_bytes(int B, int R, int nq, int nkv, int hd, int max_pages);
+void setup_attn_tree_attributes();
+int attn_tree(TreeArgs a, void* ws, cudaStream_t st);
+
+// Penalties, biases and masks on logits (adjust.cu).
+struct AdjustArgs {
+  int dtype, B, R, V;
+  const void* logits;
+  long long ld;
+  void* out;
+  long long ld_out;
+  const int32_t *tokens, *parents;       // [B][R] or null
+  const int32_t* history;                // [B] rows of n_history at stride ld_history, or null
+  long long ld_history;
+  int n_history;
+  const int32_t *hist_len, *prompt_len;  // [B] or null
+  const float *repetition, *presence, *frequency;  // [B] or null
+  const int32_t* bias_tokens;            // [B][n_bias]
+  const float* bias_values;
+  int n_bias;
+  const uint32_t* mask;                  // [n_masks] rows of words at stride ld_mask, or null
+  long long ld_mask;
+  int n_masks;
+  const int32_t* mask_ids;               // [B*R] or null
+  int* status;
+  int chunk;                             // tokens of a CTA (set by the launcher)
+};
+void setup_adjust_attributes();
+int adjust_logits(AdjustArgs a, cudaStream_t st);
+
+// Pages of the cache (pages.cu).
+struct PagesArgs {
+  int n, n_pages, max_pages, n_slots;
+  int32_t* table;              // [n_slots][max_pages], -1 behind a slot's last page
+  int32_t* refs;               // [n_pages]
+  const int32_t* ids;          // [n] slots (fork: the slots forked to)
+  const int32_t* src;          // fork: [n] the slots forked from
+  const int32_t* lens;         // reserve, release: [n] or null
+  int32_t *seq_len, *pending;  // fork: [n_slots]
+  float* hid;                  // fork: [n_slots][d] or null
+  int d;
+  int32_t *table_out, *refs_out, *moved, *n_live;  // compact
+  char* pool;
+  long long layer_bytes;       // of a layer of the pool
+  int L, page_bytes;           // layers; bytes of a page in one layer
+  int planes, row_bytes;       // 2 * n_kv_heads planes of 64 rows
+  int* ws;                     // pages_bytes(): error word, job count, jobs
+};
+size_t pages_bytes(int n_pages, int n);
+int pages_reserve(const PagesArgs& a, cudaStream_t st);
+int pages_release(const PagesArgs& a, cudaStream_t st);
+int pages_fork(const PagesArgs& a, cudaStream_t st);
+int pages_compact(const PagesArgs& a, cudaStream_t st);
+// Accepted rows of a pass moved together: position seq_len + rows[i] to seq_len + i.
+struct KeepArgs {
+  int B, n, L, planes, row_bytes, n_pages, max_pages, n_slots;
+  const int32_t *seq_ids, *seq_len, *rows, *n_keep, *table;
+  char* pool;
+  long long layer_bytes;
+  int* err;
+};
+int rows_keep(const KeepArgs& a, cudaStream_t st);
+
 }  // namespace spec

@@ -291,6 +291,8 @@ void spec::setup_device_attributes() {
   setup_moe_attributes();
   setup_sample_attributes();
   setup_lora_attributes();
+  setup_attn_tree_attributes();
+  setup_adjust_attributes();
   done[dev] = true;
 }
 
@@ -757,6 +759,33 @@ bool aligned16(std::initializer_list<const void*> ps) {
   return true;
 }
 
+bool kv_ok(const spec_kv_desc* kv) {
+  return kv && kv->pool && kv->block_table && kv->page_size == 64 && kv->n_pages > 0 && kv->max_pages_per_seq > 0 &&
+         kv->n_slots > 0;
+}
+size_t kv_size(const spec_model_desc& m) { return m.kv_dtype == SPEC_F32 ? 4 : 2; }
+
+// The pages' part of a call; false where something is missing.
+bool pages_args(PagesArgs& a, const spec_kv_desc* kv, int32_t* refs, int32_t n, const int32_t* ids, void* ws) {
+  if (!kv || !kv->block_table || kv->n_pages <= 0 || kv->max_pages_per_seq <= 0 || kv->n_slots <= 0 || !refs || n <= 0 ||
+      !ids || !ws || !aligned16({ws}))
+    return false;
+  a.n = n; a.n_pages = kv->n_pages; a.max_pages = kv->max_pages_per_seq; a.n_slots = kv->n_slots;
+  a.table = const_cast<int32_t*>(kv->block_table); a.refs = refs; a.ids = ids; a.ws = (int*)ws;
+  return true;
+}
+void pages_pool(PagesArgs& a, const spec_model_desc& m, const spec_kv_desc& kv) {
+  a.pool = (char*)kv.pool; a.L = m.n_layers; a.planes = 2 * m.n_kv_heads;
+  a.row_bytes = (int)(m.head_dim * kv_size(m));
+  a.page_bytes = a.planes * 64 * a.row_bytes;
+  a.layer_bytes = (long long)kv.n_pages * a.page_bytes;
+}
+constexpr int PAGES_N_MAX = 1024, PAGES_MAX = 1 << 20;
+bool rows_copy_ok(const spec_model_desc& m, const spec_kv_desc& kv) {  // copies go by 16 bytes, offsets in a page in 31 bits
+  return m.head_dim * kv_size(m) % 16 == 0 && aligned16({kv.pool}) &&
+         (long long)2 * m.n_kv_heads * 64 * m.head_dim * (long long)kv_size(m) < (1ll << 31);
+}
+
 }  // namespace
 
 extern "C" {
@@ -1088,6 +1117,135 @@ spec_status spec_accept_sampled(int32_t dtype, const void* logits, int64_t ld, i
   AcceptSampledArgs a = {};
   a.B = B; a.k = k; a.drafts = drafts; a.out_tokens = out_tokens; a.probs = probs; a.n_emitted = n_emitted;
   if (accept_sampled(a, (cudaStream_t)stream) < 0) return SPEC_ECUDA;
+  return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ECUDA;
+}
+
+size_t spec_attention_tree_workspace_bytes(const spec_model_desc* m, int32_t B, int32_t R, int32_t n_q_heads,
+                                           int32_t max_pages_per_seq) {
+  if (!m || !model_ok(*m) || B <= 0 || B > TREE_B_MAX || R <= 0 || R > TREE_ROWS_MAX || n_q_heads <= 0 ||
+      n_q_heads % m->n_kv_heads || m->head_dim % 8 || max_pages_per_seq <= 0)
+    return 0;
+  return attn_tree_bytes(B, R, n_q_heads, m->n_kv_heads, m->head_dim, max_pages_per_seq);
+}
+
+spec_status spec_attention_tree(const spec_model_desc* m, const spec_kv_desc* kv, int32_t layer, int32_t B,
+                                const int32_t* seq_ids, const int32_t* seq_len, int32_t R, int32_t n_q_heads,
+                                const int32_t* parents, const int32_t* n_rows, int32_t q_dtype, const void* q,
+                                int64_t ldq, void* out, int64_t ldo, void* workspace, size_t ws_bytes, void* stream) {
+  if (!m || !model_ok(*m) || !kv_ok(kv) || layer < 0 || layer >= m->n_layers || B <= 0 || !seq_ids || !seq_len || R <= 0 ||
+      n_q_heads <= 0 || n_q_heads % m->n_kv_heads || (q_dtype != SPEC_F32 && q_dtype != SPEC_BF16) || !q || !out ||
+      !workspace || !aligned16({q, out, workspace, kv->pool}) || ldq % 8 || ldo % 8 ||
+      ldq < (int64_t)n_q_heads * m->head_dim || ldo < (int64_t)n_q_heads * m->head_dim)
+    return SPEC_EINVAL;
+  if (B > TREE_B_MAX || R > TREE_ROWS_MAX || m->head_dim % 8) return SPEC_EUNSUPPORTED;
+  if (ws_bytes < attn_tree_bytes(B, R, n_q_heads, m->n_kv_heads, m->head_dim, kv->max_pages_per_seq))
+    return SPEC_ECAPACITY;
+  TreeArgs a = {};
+  a.B = B; a.R = R; a.nq = n_q_heads; a.nkv = m->n_kv_heads; a.hd = m->head_dim;
+  a.q_dtype = q_dtype == SPEC_F32 ? DT_F32 : DT_BF16;
+  a.kv_dtype = m->kv_dtype == SPEC_F32 ? DT_F32 : DT_BF16;
+  a.q = q; a.ldq = ldq; a.out = out; a.ldo = ldo;
+  a.pool = (const char*)kv->pool + (size_t)layer * kv->n_pages * 2 * m->n_kv_heads * 64 * m->head_dim * kv_size(*m);
+  a.n_pages = kv->n_pages; a.max_pages = kv->max_pages_per_seq; a.n_slots = kv->n_slots;
+  a.block_table = kv->block_table; a.seq_ids = seq_ids; a.seq_len = seq_len; a.parents = parents; a.n_rows = n_rows;
+  setup_device_attributes();
+  if (attn_tree(a, workspace, (cudaStream_t)stream) < 0) return SPEC_ECUDA;
+  return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ECUDA;
+}
+
+spec_status spec_rows_keep(const spec_model_desc* m, const spec_kv_desc* kv, int32_t B, const int32_t* seq_ids,
+                           const int32_t* seq_len, int32_t n, const int32_t* rows, const int32_t* n_keep,
+                           void* workspace, size_t ws_bytes, void* stream) {
+  if (!m || !model_ok(*m) || !kv_ok(kv) || B <= 0 || !seq_ids || !seq_len || n <= 0 || !rows || !n_keep || !workspace)
+    return SPEC_EINVAL;
+  if (B > TREE_B_MAX || n > TREE_ROWS_MAX || !rows_copy_ok(*m, *kv)) return SPEC_EUNSUPPORTED;
+  if (ws_bytes < 256) return SPEC_ECAPACITY;
+  KeepArgs a = {};
+  a.B = B; a.n = n; a.L = m->n_layers; a.planes = 2 * m->n_kv_heads; a.row_bytes = (int)(m->head_dim * kv_size(*m));
+  a.n_pages = kv->n_pages; a.max_pages = kv->max_pages_per_seq; a.n_slots = kv->n_slots; a.seq_ids = seq_ids;
+  a.seq_len = seq_len; a.rows = rows; a.n_keep = n_keep; a.table = kv->block_table; a.pool = (char*)kv->pool;
+  a.layer_bytes = (long long)kv->n_pages * a.planes * 64 * a.row_bytes; a.err = (int*)workspace;
+  if (rows_keep(a, (cudaStream_t)stream) < 0) return SPEC_ECUDA;
+  return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ECUDA;
+}
+
+size_t spec_pages_workspace_bytes(int32_t n_pages, int32_t n) {
+  return n_pages > 0 && n_pages <= PAGES_MAX && n > 0 && n <= PAGES_N_MAX ? pages_bytes(n_pages, n) : 0;
+}
+
+spec_status spec_pages_reserve(const spec_kv_desc* kv, int32_t* refs, int32_t n, const int32_t* ids,
+                               const int32_t* lens, void* workspace, size_t ws_bytes, void* stream) {
+  PagesArgs a = {};
+  if (!pages_args(a, kv, refs, n, ids, workspace) || !lens) return SPEC_EINVAL;
+  if (n > PAGES_N_MAX || kv->n_pages > PAGES_MAX) return SPEC_EUNSUPPORTED;
+  if (ws_bytes < pages_bytes(kv->n_pages, n)) return SPEC_ECAPACITY;
+  a.lens = lens;
+  if (pages_reserve(a, (cudaStream_t)stream) < 0) return SPEC_ECUDA;
+  return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ECUDA;
+}
+
+spec_status spec_pages_release(const spec_kv_desc* kv, int32_t* refs, int32_t n, const int32_t* ids,
+                               const int32_t* lens, void* workspace, size_t ws_bytes, void* stream) {
+  PagesArgs a = {};
+  if (!pages_args(a, kv, refs, n, ids, workspace)) return SPEC_EINVAL;
+  if (n > PAGES_N_MAX || kv->n_pages > PAGES_MAX) return SPEC_EUNSUPPORTED;
+  if (ws_bytes < pages_bytes(kv->n_pages, n)) return SPEC_ECAPACITY;
+  a.lens = lens;
+  if (pages_release(a, (cudaStream_t)stream) < 0) return SPEC_ECUDA;
+  return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ECUDA;
+}
+
+spec_status spec_pages_fork(const spec_model_desc* m, const spec_kv_desc* kv, int32_t* refs, const spec_state* state,
+                            int32_t n, const int32_t* src, const int32_t* dst, void* workspace, size_t ws_bytes,
+                            void* stream) {
+  PagesArgs a = {};
+  if (!m || !model_ok(*m) || !kv_ok(kv) || !pages_args(a, kv, refs, n, dst, workspace) || !src || !state ||
+      !state->seq_len)
+    return SPEC_EINVAL;
+  if (n > PAGES_N_MAX || kv->n_pages > PAGES_MAX || !rows_copy_ok(*m, *kv)) return SPEC_EUNSUPPORTED;
+  if (ws_bytes < pages_bytes(kv->n_pages, n)) return SPEC_ECAPACITY;
+  pages_pool(a, *m, *kv);
+  a.src = src; a.seq_len = state->seq_len; a.pending = state->pending; a.hid = state->hid; a.d = m->d_model;
+  if (pages_fork(a, (cudaStream_t)stream) < 0) return SPEC_ECUDA;
+  return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ECUDA;
+}
+
+spec_status spec_pages_compact(const spec_model_desc* m, const spec_kv_desc* kv, int32_t* refs, int32_t* table_out,
+                               int32_t* refs_out, int32_t* moved, int32_t* n_live, void* workspace, size_t ws_bytes,
+                               void* stream) {
+  PagesArgs a = {};
+  if (!m || !model_ok(*m) || !kv_ok(kv) || !pages_args(a, kv, refs, 1, refs, workspace) || !table_out || !refs_out ||
+      !moved || !n_live)
+    return SPEC_EINVAL;
+  if (kv->n_pages > PAGES_MAX || !rows_copy_ok(*m, *kv)) return SPEC_EUNSUPPORTED;
+  if (ws_bytes < pages_bytes(kv->n_pages, 1)) return SPEC_ECAPACITY;
+  pages_pool(a, *m, *kv);
+  a.ids = nullptr; a.table_out = table_out; a.refs_out = refs_out; a.moved = moved; a.n_live = n_live;
+  if (pages_compact(a, (cudaStream_t)stream) < 0) return SPEC_ECUDA;
+  return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ECUDA;
+}
+
+spec_status spec_adjust_logits(int32_t dtype, const void* logits, int64_t ld, int32_t B, int32_t R, int32_t V,
+                               const spec_adjust* s, void* out, int64_t ld_out, void* stream) {
+  if ((dtype != SPEC_F32 && dtype != SPEC_BF16) || !logits || B <= 0 || R <= 0 || V <= 0 || ld < V || !s || !out ||
+      ld_out < V || (out == logits && ld_out != ld) || s->n_history < 0 || s->n_bias < 0 ||
+      (s->history && s->ld_history < s->n_history) || (s->n_bias > 0 && (!s->bias_tokens || !s->bias_values)) ||
+      (s->mask && (s->n_masks <= 0 || s->ld_mask < (V + 31) / 32 || (!s->mask_ids && s->n_masks < (int64_t)B * R))) ||
+      ((uintptr_t)logits | (uintptr_t)out) & (dtype == SPEC_F32 ? 3 : 1))
+    return SPEC_EINVAL;
+  if (V > SAMPLE_V_MAX || R > 1024 || (s->parents && R > TREE_ROWS_MAX) || B > 65535 ||
+      s->n_history >= (1 << 19) - 1024 || s->n_bias > 4095)
+    return SPEC_EUNSUPPORTED;
+  AdjustArgs a = {};
+  a.dtype = dtype == SPEC_F32 ? DT_F32 : DT_BF16;
+  a.B = B; a.R = R; a.V = V; a.logits = logits; a.ld = ld; a.out = out; a.ld_out = ld_out;
+  a.tokens = s->tokens; a.parents = s->parents; a.history = s->n_history > 0 ? s->history : nullptr;
+  a.ld_history = s->ld_history; a.n_history = s->n_history; a.hist_len = s->hist_len; a.prompt_len = s->prompt_len;
+  a.repetition = s->repetition; a.presence = s->presence; a.frequency = s->frequency;
+  a.bias_tokens = s->bias_tokens; a.bias_values = s->bias_values; a.n_bias = s->n_bias;
+  a.mask = s->mask; a.ld_mask = s->ld_mask; a.n_masks = s->n_masks; a.mask_ids = s->mask_ids; a.status = s->status;
+  setup_device_attributes();
+  if (adjust_logits(a, (cudaStream_t)stream) < 0) return SPEC_ECUDA;
   return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ECUDA;
 }
 

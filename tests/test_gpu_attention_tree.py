@@ -1,0 +1,302 @@
+"""spec_attention_tree against the 64-bit reference (tests/branch_ref.py).
+
+Tolerances, per output o = sum p v / sum p with A = sum p |v| / sum p and S the
+largest sum |q k| / sqrt(hd) of the row:
+ - a score is off by at most (hd + 8) 2^-23 S (hd products and sums, of which a
+   tensor core may cut instead of round, and the scaling), its exponential by 2^-21
+   more (the hardware's exponential and its argument's rounding up to scores of 16);
+   that moves a weight, and twice that an output, relative to A;
+ - sums over n keys: n 2^-23 A;
+ - float rows on a bf16 cache: probabilities to 2^-16 (two bf16 planes): 2 * 2^-16 A;
+ - bf16 rows: probabilities rounded to bf16 (2^-8) in both sums, 2 * 2^-8 A, and
+   the result's rounding 2^-8 |o|."""
+import numpy as np
+import pytest
+import torch
+
+from speculative_decoding_spec_gb300 import binding
+from tests import branch_ref as ref
+
+pytestmark = pytest.mark.gpu
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+
+
+def _np(t):
+    return t.detach().double().cpu().numpy()
+
+
+class Case:
+    def __init__(self, nq, nkv, hd, lens, R, q="f32", kv="bf16", rows=None, parents="tree", layers=2, seed=0, spare=3,
+                 scale=1.5, garbage=True):
+        rng = np.random.default_rng(seed)
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        B = len(lens)
+        self.B, self.R, self.nq, self.hd = B, R, nq, hd
+        rows = [R] * B if rows is None else rows
+        need = [-(-(n + r) // 64) for n, r in zip(lens, rows)]
+        P, pages = max(max(need), 1) + 1, sum(need) + spare
+        pool = torch.randn((layers, pages, 2, nkv, 64, hd), generator=g, device="cuda").to(DT[kv])
+        ids = rng.permutation(pages)
+        slots = rng.permutation(B + 1)[:B]          # a slot that no sequence of the call has
+        table, at = np.full((B + 1, P), -1, np.int32), 0
+        for b, n in enumerate(need):
+            table[slots[b], :n] = ids[at:at + n]
+            at += n
+        if garbage:                                  # what lies behind a sequence's last key, and pages of nobody
+            for b in range(B):
+                n = lens[b] + rows[b]
+                if n % 64:
+                    pool[:, int(table[slots[b], n // 64]), :, :, n % 64:] = float("nan")
+            pool[:, torch.from_numpy(ids[at:].copy()).cuda()] = float("inf")
+        seq_len = np.zeros(B + 1, np.int32)
+        seq_len[slots] = lens
+        self.parents = None if parents is None else ref.random_parents(rng, B, R) if parents == "tree" else np.array(parents, np.int32)
+        self.rows = np.array(rows, np.int32)
+        cu = lambda x: torch.from_numpy(np.ascontiguousarray(x, np.int32)).cuda()
+        self.pool, self.table, self.seq_ids, self.seq_len = pool, cu(table), cu(slots), cu(seq_len)
+        self.q = (torch.randn((B * R, nq * hd), generator=g, device="cuda") * scale).to(DT[q])
+        self.cache = binding.Cache(pool, self.table)
+        self.layer = layers - 1
+        self.alive = []
+
+    def call(self, **kw):
+        par = None if self.parents is None else torch.from_numpy(self.parents).cuda()
+        kw.setdefault("n_rows", torch.from_numpy(self.rows).cuda())
+        self.alive.append((par, kw["n_rows"]))     # (a call on another stream may still read them)
+        return binding.spec_attention_tree(self.cache, self.layer, self.seq_ids, self.seq_len, self.q, par, **kw)
+
+    def want(self):
+        return ref.attention(_np(self.pool[self.layer]), self.table.cpu().numpy(), self.seq_ids.cpu().numpy(),
+                             self.seq_len.cpu().numpy(), _np(self.q), self.nq, self.parents, self.rows)
+
+    def tol(self, o, A, S, n):
+        t = A * (2 * ((self.hd + 8) * 2.0 ** -23 * S + 2.0 ** -21) + (n + 16) * 2.0 ** -23)
+        if self.q.dtype is torch.bfloat16:
+            return t + A * 2 * 2.0 ** -8 + 2.0 ** -8 * np.abs(o)
+        return t + (A * 2 * 2.0 ** -16 if self.pool.dtype is torch.bfloat16 else 0)
+
+    def check(self, out=None):
+        out = self.call(sync=True) if out is None else out
+        o, A, S, n = self.want()
+        got, used = _np(out), ~np.isnan(o)
+        assert np.isfinite(got[used]).all()
+        err, tol = np.abs(got - o)[used], self.tol(o, A, S, n)[used]
+        assert (err <= tol).all(), "worst %.3g of its tolerance" % (err / tol).max()
+        return out
+
+
+KINDS = [("f32", "bf16"), ("bf16", "bf16"), ("f32", "f32"), ("bf16", "f32")]
+HEADS = [(12, 4, 128), (20, 4, 128), (48, 8, 128), (4, 4, 64), (16, 8, 128)]
+
+
+@pytest.mark.parametrize("q,kv", KINDS)
+@pytest.mark.parametrize("heads", HEADS)
+@pytest.mark.parametrize("n,R", [(0, 1), (1, 1), (62, 1), (63, 1), (64, 1), (0, 2), (60, 5), (63, 2), (127, 7), (128, 16), (500, 33), (1000, 64)])
+def test_one_sequence(q, kv, heads, n, R):
+    Case(*heads, [n], R, q, kv, seed=n + R).check()
+
+
+@pytest.mark.parametrize("q,kv", KINDS)
+@pytest.mark.parametrize("heads", [(6, 2, 96), (5, 1, 40), (3, 3, 8), (8, 1, 256), (32, 4, 64), (71, 1, 64), (16, 1, 128)])
+@pytest.mark.parametrize("n,R", [(3, 1), (130, 9), (300, 40)])
+def test_other_heads(q, kv, heads, n, R):
+    Case(*heads, [n], R, q, kv, seed=n).check()
+
+
+@pytest.mark.parametrize("q,kv", KINDS)
+@pytest.mark.parametrize("heads", [(12, 4, 128), (48, 8, 128), (4, 4, 64)])
+@pytest.mark.parametrize("R,rows", [(24, [24, 1, 0, 13, 7, 24]), (64, [64, 22, 43, 1, 0, 64]), (3, [3, 3, 1, 2, 0, 3])])
+def test_ragged_batch(q, kv, heads, R, rows):
+    c = Case(*heads, [0, 700, 65, 1283, 64, 40], R, q, kv, rows=rows, seed=R)
+    out = torch.full_like(c.q, 7.0)
+    assert c.call(out=out, sync=True) is out
+    c.check(out)
+    free = torch.from_numpy(np.arange(R)[None] >= c.rows[:, None]).reshape(-1).cuda()
+    assert (out[free] == 7.0).all()                         # rows that are not in use stay as they are
+    made = c.call()
+    assert (made[free] == 0).all() and torch.equal(made[~free], out[~free])
+
+
+@pytest.mark.parametrize("q,kv", KINDS[:3])
+def test_long_context_and_many_sequences(q, kv):
+    hd = 128 if kv == "bf16" else 64
+    Case(4, 2, hd, [20000], 5, q, kv, layers=1, seed=1).check()
+    Case(4, 2, hd, [(i * 37) % 211 for i in range(70)], 3, q, kv, layers=1, seed=2).check()
+
+
+@pytest.mark.parametrize("q,kv", KINDS)
+def test_chain_and_star(q, kv):
+    heads = (12, 4, 128)
+    chain = Case(*heads, [333, 64], 9, q, kv, parents=None)
+    star = [[-1] + [0] * 8] * 2
+    forest = [[-1] * 9, [-1, -1, 0, 1, 1, 2, -1, 6, 7]]
+    a = chain.check()
+    chain.parents = np.array([[r - 1 for r in range(9)]] * 2, np.int32)
+    assert torch.equal(a, chain.call())
+    Case(*heads, [333, 64], 9, q, kv, parents=star).check()
+    Case(*heads, [333, 64], 9, q, kv, parents=forest).check()
+
+
+@pytest.mark.parametrize("q,kv", KINDS)
+@pytest.mark.parametrize("n", [0, 100, 127])
+def test_values_of_unseen_rows_do_not_count(q, kv, n):
+    """Infinities and NaN in a row's key and value reach only the rows that see it."""
+    c = Case(12, 4, 128, [n], 6, q, kv, parents=[[-1, 0, 0, 1, 2, 0]])
+    want = c.check()
+    for plane in (0, 1):
+        for bad in (float("inf"), float("-inf"), float("nan")):
+            pool = c.pool.clone()
+            at = n + 2
+            pool[:, int(c.table[int(c.seq_ids[0]), at // 64]), plane, :, at % 64, 3::5] = bad
+            c.cache = binding.Cache(pool, c.table)
+            got = c.call(sync=True)
+            clean = [0, 1, 3, 5]
+            assert torch.isfinite(got[clean]).all()
+            o, A, S, k = c.want()
+            assert (np.abs(_np(got) - o)[clean] <= c.tol(o, A, S, k)[clean]).all()
+            touched = got[[2, 4]].view(2, 12, 128)
+            if plane == 0:
+                assert torch.isnan(touched).any(-1).all() or bad == float("-inf") or bad == float("inf")
+            else:
+                assert not torch.isfinite(touched[..., 3::5]).any()
+                assert torch.isfinite(touched[..., 0::5]).all()
+
+
+@pytest.mark.parametrize("q,kv", KINDS)
+def test_strided_rows(q, kv):
+    c = Case(12, 4, 128, [77, 300], 5, q, kv)
+    want = c.call()
+    wide = torch.full((10, 12 * 128 + 24), float("nan"), dtype=c.q.dtype, device="cuda")
+    wide[:, 8:8 + 12 * 128] = c.q
+    c.q = wide[:, 8:8 + 12 * 128]
+    out = torch.full((10, 12 * 128 + 40), 3.0, dtype=c.q.dtype, device="cuda")
+    got = c.call(out=out[:, 16:16 + 12 * 128])
+    assert torch.equal(got, want) and (out[:, :16] == 3).all() and (out[:, 16 + 12 * 128:] == 3).all()
+
+
+@pytest.mark.parametrize("q,kv", KINDS)
+def test_large_scores(q, kv):
+    """Peaked rows: one key takes nearly all of the weight, and the maximum moves often."""
+    c = Case(12, 4, 128, [900], 8, q, kv, scale=12.0)
+    c.check()
+    c = Case(4, 4, 64, [900], 8, q, kv, scale=0.0)          # all scores equal
+    c.check()
+
+
+@pytest.mark.parametrize("q,kv", KINDS)
+def test_recorded_errors(q, kv):
+    c = Case(12, 4, 128, [100, 200, 300], 4, q, kv)
+    want = c.check()
+    mark = lambda: torch.full_like(want, 5.0)
+    rows = torch.from_numpy(c.rows).cuda()
+
+    def run(out, **kw):
+        ws = torch.full((1 << 26,), 0xAB, dtype=torch.uint8, device="cuda")
+        c.call(out=out, workspace=ws, **kw)
+        return int(ws[:4].view(torch.int32))
+
+    out = mark()
+    assert run(out) == 0 and torch.equal(out, want)
+    for bad in (-1, 5, 1 << 30, -(1 << 31)):               # a row count: that sequence stays as it was
+        r = rows.clone()
+        r[1] = bad
+        out = mark()
+        assert run(out, n_rows=r) == 2
+        assert (out[4:8] == 5).all() and torch.equal(out[:4], want[:4]) and torch.equal(out[8:], want[8:])
+    keep = c.seq_ids
+    for bad in (-1, 4, 1 << 30):
+        c.seq_ids = keep.clone()
+        c.seq_ids[2] = bad
+        out = mark()
+        assert run(out) == 2 and (out[8:] == 5).all() and torch.equal(out[:8], want[:8])
+    c.seq_ids = keep
+    lens = c.seq_len
+    for bad in (-1, c.cache.max_pages * 64 - 3, (1 << 31) - 1):
+        c.seq_len = lens.clone()
+        c.seq_len[int(keep[0])] = bad
+        out = mark()
+        assert run(out) == 2 and (out[:4] == 5).all() and torch.equal(out[4:], want[4:])
+    c.seq_len = lens
+    for bad in (4, 3, -2, 1 << 30):                         # a parent that is no earlier row counts as none
+        c.parents[1, 3] = -1
+        fixed = c.call()
+        c.parents[1, 3] = bad
+        out = mark()
+        assert run(out) == 2 and torch.equal(out, fixed)
+    c.parents[1, 3] = -1
+    fixed = c.call()
+    table = c.table.clone()
+    for bad in (-1, c.cache.n_pages, 1 << 30):
+        c.table.copy_(table)
+        c.table[int(keep[1]), 1] = bad
+        out = mark()
+        assert run(out) == 2 and torch.equal(out[:4], fixed[:4]) and torch.equal(out[8:], fixed[8:])
+        with pytest.raises(binding.SpecError) as e:
+            c.call(sync=True)
+        assert e.value.code == binding.SPEC_ECAPACITY
+
+
+@pytest.mark.parametrize("q,kv", KINDS)
+def test_graph_streams_and_two_at_once(q, kv):
+    c = Case(48, 8, 128, [700, 90, 1500], 12, q, kv)
+    d = Case(48, 8, 128, [10, 4000], 5, q, kv, seed=9)
+    a, b = c.call(), d.call()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = [(c.call(stream=s1), d.call(stream=s2)) for _ in range(4)]
+    torch.cuda.synchronize()
+    for x, y in got:
+        assert torch.equal(x, a) and torch.equal(y, b)
+    rows, par = torch.from_numpy(c.rows).cuda(), torch.from_numpy(c.parents).cuda()
+    out = torch.zeros_like(a)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        binding.spec_attention_tree(c.cache, c.layer, c.seq_ids, c.seq_len, c.q, par, n_rows=rows, out=out)
+    for shift in (0, 1, 64):                                # other lengths on replay
+        c.seq_len -= shift
+        want = c.call()
+        out.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+
+
+def test_offsets_past_32_bits():
+    """A pool of more than 2^32 bytes (and elements), pages from its end."""
+    nkv, hd = 8, 128
+    page = 2 * nkv * 64 * hd
+    n = (1 << 32) // page + 9
+    pool = torch.empty((1, n, 2, nkv, 64, hd), dtype=torch.bfloat16, device="cuda")
+    c = Case(16, nkv, hd, [150, 100], 6, "bf16", "bf16", layers=1, garbage=False)
+    k = c.pool.shape[1]
+    pool[:, n - k:] = c.pool
+    table = torch.where(c.table >= 0, c.table + (n - k), -1).to(torch.int32)
+    want = c.check()
+    c.cache = binding.Cache(pool, table)
+    assert torch.equal(c.call(sync=True), want)
+
+
+def test_refusals():
+    c = Case(12, 4, 128, [100, 200], 4)
+    run = binding.spec_attention_tree
+    a = (c.cache, 0, c.seq_ids, c.seq_len)
+    bad = [
+        lambda: run(*a, c.q.half()), lambda: run(*a, c.q.cpu()), lambda: run(*a, c.q[:7]), lambda: run(*a, c.q[:, :-128]),
+        lambda: run(*a, c.q.t().contiguous().t()), lambda: run(*a, c.q[:0]), lambda: run(c.cache, 2, *a[2:], c.q),
+        lambda: run(c.cache, -1, *a[2:], c.q), lambda: run(*a, c.q, torch.zeros((2, 3), dtype=torch.int32, device="cuda")),
+        lambda: run(*a, c.q, torch.zeros((2, 4), device="cuda")), lambda: run(*a, c.q, n_rows=c.seq_len),
+        lambda: run(*a, c.q, out=torch.empty_like(c.q, dtype=torch.bfloat16)), lambda: run(*a, c.q, out=c.q[:4]),
+        lambda: run(c.cache, 0, c.seq_ids.long(), c.seq_len, c.q), lambda: run(c.cache, 0, c.seq_ids, c.seq_len[:2], c.q),
+        lambda: run(*a, torch.zeros((8, 12 * 128 + 4), device="cuda")[:, 2:-2]),
+        lambda: run(*a, torch.zeros((8, 12 * 128 + 4), device="cuda")[:, :-4]),
+        lambda: run(*a, c.q, workspace=torch.empty(64, dtype=torch.uint8, device="cuda")),
+        lambda: run(*a, torch.zeros((130, 12 * 128), device="cuda")),
+        lambda: binding.Cache(c.pool[0], c.table), lambda: binding.Cache(c.pool.half(), c.table),
+        lambda: binding.Cache(c.pool, c.table.long()), lambda: binding.Cache(c.pool, c.table.cpu()),
+        lambda: binding.Cache(c.pool[:, :, :, ::2], c.table), lambda: binding.Cache(c.pool, c.table, c.seq_len),
+    ]
+    for i, f in enumerate(bad):
+        with pytest.raises(binding.SpecError):
+            f()
+            pytest.fail("call %d was not refused" % i)
+    c.check()
