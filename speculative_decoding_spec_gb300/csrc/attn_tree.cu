@@ -352,7 +352,7 @@ Plan cc_plan(const TreeArgs& a) {
 }
 
 Plan plan_of(const TreeArgs& a) {
-  Plan p = cc_plan(a);
+  Plan p = tc_ok(a) ? tc_plan(a) : cc_plan(a);
   // no more CTAs than the axis can have blocks
   const long long T = (a.R * (a.nq / a.nkv) + p.tile - 1) / p.tile;
   const long long most = (long long)a.B * a.nkv * T * (((long long)a.max_pages * PAGE + p.blk - 1) / p.blk);
@@ -390,6 +390,7 @@ void setup_attn_tree_attributes() {
       for (int TR : {1, 4})
         for (int hd : {64, 128, 256})
           cudaFuncSetAttribute(cc_pick(q, kv, TR, hd), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cc_smem(hd, TR));
+  tc_setup();
 }
 
 int attn_tree(TreeArgs a, void* ws, cudaStream_t st) {
@@ -397,12 +398,17 @@ int attn_tree(TreeArgs a, void* ws, cudaStream_t st) {
   a.err = (int*)ws;
   a.part_ml = (float2*)((char*)ws + 256);
   a.part_o = (float*)(a.part_ml + part_rows(p));
-  const int TR = cc_rows(a);
-  void* args[] = {(void*)&a, (void*)&p};
-  if (cudaLaunchKernel(cc_pick(a.q_dtype, a.kv_dtype, TR, a.hd), dim3(p.grid), dim3(NTHR), args, cc_smem(a.hd, TR), st) !=
-      cudaSuccess)
-    return -1;
-  const int r = 1;
+  int r = 1;
+  if (tc_ok(a)) {
+    r = tc_launch(a, p, st);
+  } else {
+    const int TR = cc_rows(a);
+    void* args[] = {(void*)&a, (void*)&p};
+    if (cudaLaunchKernel(cc_pick(a.q_dtype, a.kv_dtype, TR, a.hd), dim3(p.grid), dim3(NTHR), args, cc_smem(a.hd, TR), st) !=
+        cudaSuccess)
+      r = -1;
+  }
+  if (r < 0) return r;
   // a unit of at most min_cost / tiles blocks is never cut where it starts a part; with one CTA nothing is
   if (p.grid == 1) return r;
   cudaLaunchConfig_t cfg = {};

@@ -176,5 +176,11 @@ SPEC_DEV int page_of(const TreeArgs& a, int slot, int i) {
   return g < 0 || g >= a.n_pages ? 0 : g;
 }
 
+// The tcgen05 kernel (attn_tree_tc.cu).
+bool tc_ok(const TreeArgs& a);
+Plan tc_plan(const TreeArgs& a);
+void tc_setup();
+int tc_launch(const TreeArgs& a, const Plan& p, cudaStream_t st);
+
 }  // namespace tree
 }  // namespace spec

@@ -1,0 +1,780 @@
+// attn_tree_tc.cu -- attention of the rows of drafted trees on the fifth-
+// generation tensor cores: bf16 caches, head dims 64 and 128.
+//
+//   S = Q K^T       (M = 128 query rows, N = 128 keys, K = head dim)
+//   O += P V        (M = 128 query rows, N = head dim, K = 128 keys)
+//
+// with P = exp(S - m) written back over S in tensor memory, where the second
+// product takes it from. A thread owns a query row (a lane of tensor memory),
+// so maxima and sums need no exchange between threads. Q is bf16, or three bf16
+// planes of a float row (exact), P bf16, or two planes (to 2^-17), K and V as
+// they lie in the cache: pages arrive by TMA in the 128-byte swizzle layout, K
+// a K-major operand, V (stored [key][dim]) an MN-major one.
+//
+// Few rows leave most of the 128 lanes idle, and may: a block of 128 keys is 64 KB
+// at head dim 128, about 2800 cycles at an SM's share of the HBM rate, while its
+// products take 1024 (2560 with planes) and its softmax about 600 a warp. Warps
+// whose lanes hold no row skip the softmax.
+//
+// Two streams hide the softmax behind the products: while one stream's softmax
+// runs, the tensor cores work on the other's. With one tile of query rows the
+// streams take alternate blocks of keys and keep a maximum, a sum and an O each,
+// added up at the end; with two tiles a unit (bf16 rows, more than 128 on a KV
+// head) each stream is a tile and a block is read once for both.
+//
+// Roles (384 threads, one CTA an SM): warp 0 loads (a ring of tiles, K and V in
+// the order in which they are used), warp 1 issues the products, warp 2 of CTA 0
+// checks the arguments, warps 4-7 and 8-11 are the streams' softmax. Waits are
+// bounded; one that runs out sets SPEC_ERR_TIMEOUT and an abort flag that lets
+// every other wait pass, so that the CTA drains its copies and ends.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <mutex>
+
+#include "attn_tree.cuh"
+#include "mbar.cuh"
+
+namespace spec {
+namespace tree {
+namespace {
+
+constexpr int BK = 128;                 // keys a block: two pages
+constexpr int ROWS = 128;               // query rows a tile
+constexpr int NTHR = 384, NSM = 256;    // threads; softmax threads
+constexpr int HALF = BK * 128;          // 64 dims of a tile: 128 rows of 128 bytes
+constexpr int BOX = PAGE * 128;
+constexpr int ST_MAX = 12;
+constexpr float TAU = 8.f;              // the running maximum is raised past a growth of 2^8
+constexpr unsigned SPIN_LIMIT = 1u << 26;
+
+// Shared memory: small items in the first 3 KB, then the query tiles and the ring.
+struct Small {
+  uint64_t full[ST_MAX], empty[ST_MAX], sfull[2], pfull[2], odone[2], qfull, drain;
+  uint32_t tmem;
+  int abort;
+  unsigned long long bad;               // rows of the tree whose values are not finite
+  float2 ml[2][ROWS];                   // the streams' maxima and sums
+  int up[64];                           // parents
+};
+constexpr size_t SMALL = 3072, SMEM_MAX = 227 * 1024;
+static_assert(sizeof(Small) <= SMALL, "");
+
+struct Shape {
+  int stages, tiles;                    // of the ring; query tiles a CTA
+  float scale2;
+};
+
+SPEC_DEV void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+SPEC_DEV void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+SPEC_DEV void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+SPEC_DEV void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+SPEC_DEV void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+SPEC_DEV void sm_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+// Operands in the 128-byte swizzle layout (bits 61-63 = 2, 46-48 = 0b001), groups
+// of 8 rows 1024 bytes apart; MN-major: halves of 64 elements `lbo` bytes apart.
+SPEC_DEV uint64_t desc_k(uint32_t at) {
+  return (uint64_t)((at & 0x3FFFFu) >> 4) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) |
+         ((uint64_t)2 << 61);
+}
+SPEC_DEV uint64_t desc_mn(uint32_t at, uint32_t lbo) {
+  return (uint64_t)((at & 0x3FFFFu) >> 4) | ((uint64_t)(lbo >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+// fp32 accumulators, bf16 operands; bit 16: B is MN-major.
+constexpr uint32_t idesc(int M, int N, bool b_mn) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (b_mn ? (1u << 16) : 0u) | ((uint32_t)(N >> 3) << 17) |
+         ((uint32_t)(M >> 4) << 24);
+}
+SPEC_DEV void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, bool acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"((uint32_t)acc)
+      : "memory");
+}
+// A in tensor memory: a lane's 32-bit column holds two consecutive elements of its row.
+SPEC_DEV void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, bool acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(id), "r"((uint32_t)acc)
+      : "memory");
+}
+SPEC_DEV void commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(sa(bar)) : "memory");
+}
+SPEC_DEV void tma_2d(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+          sa(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(sa(bar))
+      : "memory");
+}
+SPEC_DEV void ld32(uint32_t at, float* v) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(at));
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+SPEC_DEV void st16(uint32_t at, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(at),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+SPEC_DEV float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+SPEC_DEV uint32_t pack2(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// Byte offset of (row, byte) in 128-byte rows: 16-byte chunk c of row r lies at c ^ (r % 8).
+SPEC_DEV uint32_t swz(int row, int byte) { return (uint32_t)(row * 128 + ((((byte >> 4) ^ (row & 7)) << 4) | (byte & 15))); }
+
+SPEC_DEV bool wait_phase(uint64_t* b, unsigned parity, volatile int* abort, int* err) {
+  for (unsigned it = 0; it < SPIN_LIMIT; ++it) {
+    if (mbar_test(b, parity)) return true;
+    if (*abort) return false;
+  }
+  *abort = 1;
+  set_error(err, SPEC_ERR_TIMEOUT);
+  return false;
+}
+SPEC_DEV void drain_phase(uint64_t* b, unsigned parity) {
+  for (unsigned it = 0; it < SPIN_LIMIT; ++it)
+    if (mbar_test(b, parity)) return;
+}
+
+// The pieces of units in this CTA's part, one after the other.
+struct Walk {
+  Unit n;
+  Seq s;
+  int k0, N;                            // first block, blocks
+  long long x, x1;
+  SPEC_DEV bool pieces(const TreeArgs& a, const Plan& p) {  // from unit n on: the next one with blocks here
+    for (;;) {
+      if (x >= x1) return false;
+      k0 = first_block(n, x);
+      N = first_block(n, x1) - k0;
+      if (N > 0) return true;
+      step(a, p);
+    }
+  }
+  SPEC_DEV void step(const TreeArgs& a, const Plan& p) {
+    x = n.start + (long long)n.nb * n.w;
+    n.start = x;
+    if (x >= x1) return;
+    const int G = a.nq / a.nkv;
+    int T = tiles_of(p, G, s.rows);
+    if ((n.u + 1) * p.tpu < T) {
+      ++n.u;
+    } else {
+      n.u = 0;
+      if (++n.kvh == a.nkv) {
+        n.kvh = 0;
+        do s = seq_of(a, ++n.b);        // (x < x1 <= the axis's end: there is one)
+        while (s.rows == 0);
+        T = tiles_of(p, G, s.rows);
+        n.nb = blocks_of(p, s);
+      }
+    }
+    n.w = min(p.tpu, T - n.u * p.tpu);
+  }
+};
+
+// Places in the ring of a piece's tiles. One tile of rows: K0 K1 V0 K2 V1 ..; two: K0 V0 K1 V1 ..
+SPEC_DEV int place_k(int n, bool pair) { return pair ? 2 * n : n < 2 ? n : 2 * n - 1; }
+SPEC_DEV int place_v(int n, int N, bool pair) { return pair ? 2 * n + 1 : min(N, n + 2) + n; }
+
+template <int HD, bool F32>
+struct Cta {
+  static constexpr int NH = HD / 64, TILE = NH * HALF;
+  static constexpr int QPL = F32 ? 3 : 1;
+  static constexpr uint32_t O_COL = 256;
+  const TreeArgs& a;
+  const Plan& p;
+  const Shape& sh;
+  const CUtensorMap* tm;
+  Small* sm;
+  unsigned char *qt, *ring;
+  uint32_t tmem;
+  Walk w;
+
+  SPEC_DEV bool wait(uint64_t* b, unsigned parity) { return wait_phase(b, parity, (volatile int*)&sm->abort, a.err); }
+  SPEC_DEV unsigned char* stage(unsigned i) { return ring + (size_t)(i % sh.stages) * TILE; }
+  SPEC_DEV unsigned parity(unsigned i) { return (i / sh.stages) & 1; }
+
+  // ---- warp 0 ----
+  SPEC_DEV void load(unsigned i, int page0, int page1, int plane) {
+    const int s = i % sh.stages;
+    unsigned char* dst = stage(i);
+    const int r0 = ((page0 * 2 + plane) * a.nkv + w.n.kvh) * PAGE, r1 = ((page1 * 2 + plane) * a.nkv + w.n.kvh) * PAGE;
+    // (a second page that is not there is left out: nothing in it is seen, and its values are cleared)
+    mbar_expect_tx(&sm->full[s], page1 >= 0 ? TILE : TILE / 2);
+#pragma unroll
+    for (int h = 0; h < NH; ++h) {
+      tma_2d(dst + h * HALF, tm, 64 * h, r0, &sm->full[s]);
+      if (page1 >= 0) tma_2d(dst + h * HALF + BOX, tm, 64 * h, r1, &sm->full[s]);
+    }
+  }
+  SPEC_DEV void producer() {
+    const int lane = threadIdx.x & 31;
+    unsigned t0 = 0, issued = 0;
+    bool ok = true;
+    while (ok && w.pieces(a, p)) {
+      const bool pair = w.n.w == 2;
+      const int pages = (w.s.len + w.s.rows + PAGE - 1) / PAGE;
+      // page ids: a window of 16 blocks in the lanes of `cur`, the next one in `nxt`
+      auto window = [&](int i) {
+        const int pg = 2 * (w.k0 + 16 * i) + lane;
+        return pg < pages ? page_of(a, w.s.slot, pg) : -1;
+      };
+      int win = 0, cur = window(0), nxt = window(1);
+      auto tile = [&](int n, int plane, int place) {
+        const int from = n / 16 == win ? cur : nxt;
+        const int p0 = __shfl_sync(FULL, from, 2 * (n & 15)), p1 = __shfl_sync(FULL, from, 2 * (n & 15) + 1);
+        const unsigned i = t0 + place;
+        if (lane == 0) {
+          ok = i < (unsigned)sh.stages || wait(&sm->empty[i % sh.stages], parity(i) ^ 1);
+          if (ok) load(i, p0, p1, plane);
+        }
+        ok = __shfl_sync(FULL, ok, 0);
+        if (ok) issued = i + 1;
+      };
+      tile(0, 0, 0);
+      if (ok && !pair && w.N > 1) tile(1, 0, 1);
+      for (int n = 0; ok && n < w.N; ++n) {
+        if (n / 16 != win) {
+          ++win;
+          cur = nxt;
+          nxt = window(win + 1);
+        }
+        tile(n, 1, place_v(n, w.N, pair));
+        const int k = n + (pair ? 1 : 2);
+        if (ok && k < w.N) tile(k, 0, place_k(k, pair));
+      }
+      t0 += 2 * w.N;
+      w.step(a, p);
+    }
+    // what was issued lands before the shared memory goes (normally it was all consumed)
+    if (lane == 0)
+      for (unsigned i = issued > (unsigned)sh.stages ? issued - sh.stages : 0; i < issued; ++i)
+        drain_phase(&sm->full[i % sh.stages], parity(i));
+  }
+
+  // ---- warp 1, one thread ----
+  SPEC_DEV bool issue_s(int s, int t, unsigned i, bool last) {
+    if (!wait(&sm->full[i % sh.stages], parity(i))) return false;
+    fence_after();
+    const uint32_t kb = sa(stage(i)), qb = sa(qt) + (uint32_t)(t * QPL * TILE);
+#pragma unroll
+    for (int pl = 0; pl < QPL; ++pl)
+#pragma unroll
+      for (int ks = 0; ks < HD / 16; ++ks) {
+        const uint32_t off = (ks >> 2) * HALF + 32 * (ks & 3);
+        mma_ss(tmem + s * 128, desc_k(qb + pl * TILE + off), desc_k(kb + off), idesc(ROWS, BK, false), pl > 0 || ks > 0);
+      }
+    commit(&sm->sfull[s]);
+    if (last) commit(&sm->empty[i % sh.stages]);
+    return true;
+  }
+  SPEC_DEV bool issue_pv(int s, unsigned i, unsigned round, bool first, bool last) {
+    if (!wait(&sm->pfull[s], round & 1) || !wait(&sm->full[i % sh.stages], parity(i))) return false;
+    fence_after();
+    const uint32_t vb = sa(stage(i)), pb = tmem + s * 128, ob = tmem + O_COL + s * HD;
+#pragma unroll
+    for (int ks = 0; ks < BK / 16; ++ks) {  // 16 keys: two groups of 8 rows of V, 8 columns of P
+      const uint64_t v = desc_mn(vb + 2048 * ks, HALF);
+      if (F32) {  // (a chunk of 32 keys: its leading parts, then the rest)
+        const uint32_t at = pb + 32 * (ks >> 1) + 8 * (ks & 1);
+        mma_ts(ob, at, v, idesc(ROWS, HD, true), !first || ks > 0);
+        mma_ts(ob, at + 16, v, idesc(ROWS, HD, true), true);
+      } else {
+        mma_ts(ob, pb + 8 * ks, v, idesc(ROWS, HD, true), !first || ks > 0);
+      }
+    }
+    commit(&sm->odone[s]);
+    if (last) commit(&sm->empty[i % sh.stages]);
+    return true;
+  }
+  SPEC_DEV void products() {
+    unsigned t0 = 0, piece = 0, round[2] = {0, 0};
+    bool ok = true;
+    while (ok && w.pieces(a, p)) {
+      const bool pair = w.n.w == 2;
+      const int N = w.N;
+      ok = wait(&sm->qfull, piece & 1);
+      fence_after();
+      if (pair) {
+        ok = ok && issue_s(0, 0, t0, false) && issue_s(1, 1, t0, true);
+        for (int n = 0; ok && n < N; ++n)
+          for (int s = 0; ok && s < 2; ++s) {
+            ok = issue_pv(s, t0 + place_v(n, N, true), round[s]++, n == 0, s == 1);
+            if (ok && n + 1 < N) ok = issue_s(s, s, t0 + place_k(n + 1, true), s == 1);
+          }
+      } else {
+        ok = ok && issue_s(0, 0, t0, true) && (N < 2 || issue_s(1, 0, t0 + 1, true));
+        for (int n = 0; ok && n < N; ++n) {
+          const int s = n & 1;
+          ok = issue_pv(s, t0 + place_v(n, N, false), round[s]++, n < 2, true);
+          if (ok && n + 2 < N) ok = issue_s(s, 0, t0 + place_k(n + 2, false), true);
+        }
+      }
+      t0 += 2 * N;
+      ++piece;
+      w.step(a, p);
+    }
+    commit(&sm->drain);  // every product done before tensor memory is freed
+    drain_phase(&sm->drain, 0);
+  }
+
+  // ---- warps 4-11: thread = row of a tile ----
+  SPEC_DEV void load_q(int row0, int nrow) {
+    const int t = threadIdx.x - 128, G = a.nq / a.nkv;
+    const int tiles = w.n.w;
+    for (int i = t; i < tiles * ROWS * (HD / 8); i += NSM) {
+      const int c = i % (HD / 8), r = i / (HD / 8), ti = r / ROWS, rr = r % ROWS;
+      unsigned char* dst = qt + (size_t)ti * QPL * TILE + (c >> 3) * HALF + swz(rr, (c & 7) * 16);
+      const bool in = r < nrow;
+      const int gr = row0 + r, qi = gr / G, g = gr - qi * G;
+      const size_t at = ((size_t)w.n.b * a.R + qi) * a.ldq + (size_t)(w.n.kvh * G + g) * HD + 8 * c;
+      if (!F32) {
+        const uint4 v = in ? *reinterpret_cast<const uint4*>((const __nv_bfloat16*)a.q + at) : make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint4*>(dst) = v;
+      } else {
+        float f[8];
+        if (in) {
+          const float4 u = *reinterpret_cast<const float4*>((const float*)a.q + at);
+          const float4 v = *reinterpret_cast<const float4*>((const float*)a.q + at + 4);
+          f[0] = u.x; f[1] = u.y; f[2] = u.z; f[3] = u.w; f[4] = v.x; f[5] = v.y; f[6] = v.z; f[7] = v.w;
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) f[e] = 0.f;
+        }
+#pragma unroll
+        for (int pl = 0; pl < 3; ++pl) {  // x = hi + mid + lo: 24 bits in three times 8
+          uint32_t o[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            o[e] = pack2(f[2 * e], f[2 * e + 1]);
+            f[2 * e] -= bf16lo(o[e]);
+            f[2 * e + 1] -= bf16hi(o[e]);
+          }
+          *reinterpret_cast<uint4*>(dst + pl * TILE) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+      }
+    }
+  }
+
+  // What lies behind the sequence's last key is anything, and a row of the tree
+  // that some rows do not see may be anything: their probabilities are zero, and
+  // so that zero times infinity stays out, their values are cleared; rows of the
+  // tree with values that are not finite are noted and added to the rows that see
+  // them at the end.
+  SPEC_DEV void clean_values(unsigned i, int key0) {
+    wait(&sm->full[i % sh.stages], parity(i));
+    const int r = (threadIdx.x - 128) & 127, key = key0 + r, j = key - w.s.len;
+    if (j < 0) return;
+    uint4* row = reinterpret_cast<uint4*>(stage(i) + (size_t)r * 128);
+    bool clear = j >= w.s.rows;
+    if (!clear) {
+#pragma unroll
+      for (int h = 0; h < NH; ++h)
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const uint4 v = row[h * (HALF / 16) + c];
+          const uint32_t e[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) clear |= (e[k] & 0x7f80u) == 0x7f80u || (e[k] & 0x7f800000u) == 0x7f800000u;
+        }
+      if (clear) atomicOr(&sm->bad, 1ull << j);
+    }
+    if (clear)
+#pragma unroll
+      for (int h = 0; h < NH; ++h)
+#pragma unroll
+        for (int c = 0; c < 8; ++c) row[h * (HALF / 16) + c] = make_uint4(0, 0, 0, 0);
+  }
+
+  // A key that was noted: its probability for this row, from the definition.
+  SPEC_DEV float noted(size_t qat, int j, float M, const __nv_bfloat16** v) {
+    const int pos = w.s.len + j;
+    const __nv_bfloat16* k = (const __nv_bfloat16*)a.pool +
+                             (((size_t)page_of(a, w.s.slot, pos / PAGE) * 2 * a.nkv + w.n.kvh) * PAGE + pos % PAGE) * HD;
+    *v = k + (size_t)a.nkv * PAGE * HD;
+    float s = 0.f;
+    for (int d = 0; d < HD; ++d)
+      s = fmaf(F32 ? ((const float*)a.q)[qat + d] : __bfloat162float(((const __nv_bfloat16*)a.q)[qat + d]),
+               __bfloat162float(k[d]), s);
+    return ex2(fmaf(s, sh.scale2, -M));
+  }
+
+  SPEC_DEV void softmax() {
+    const int t = threadIdx.x - 128, s = t >> 7, r = t & 127, lane = t & 31, G = a.nq / a.nkv;
+    const uint32_t lanes = (uint32_t)(r & ~31) << 16;
+    const uint32_t sb = tmem + lanes + s * 128, ob = tmem + lanes + O_COL + s * HD;
+    unsigned t0 = 0, round[2] = {0, 0};
+    while (w.pieces(a, p)) {
+      const bool pair = w.n.w == 2;
+      const int N = w.N;
+      const int row0 = w.n.u * p.tpu * ROWS, nrow = min(w.n.w * ROWS, w.s.rows * G - row0);
+      sm_sync();                         // the piece before is read out
+      if (t < 64) {
+        int q = -1;
+        if (t < w.s.rows) q = a.parents ? a.parents[(size_t)w.n.b * a.R + t] : t - 1;
+        sm->up[t] = q < t ? q : -1;
+      }
+      if (t == 0) sm->bad = 0;
+      load_q(row0, nrow);
+      fence_async();
+      fence_before();
+      mbar_arrive(&sm->qfull);
+      sm_sync();
+      const int mine = pair ? s * ROWS + r : r;                       // row of the unit
+      const bool work = (mine & ~31) < nrow;                          // this warp holds a row
+      const int gr = row0 + mine, qi = mine < nrow ? gr / G : 0, g = gr - gr / G * G;
+      unsigned long long path = 0;
+      for (int q = qi; q >= 0; q = sm->up[q]) path |= 1ull << q;
+      float m = -INFINITY, l = 0.f;
+      const int n0 = pair ? 0 : s, dn = pair ? 1 : 2;
+      for (int n = n0; n < N; n += dn) {
+        wait(&sm->sfull[s], round[s] & 1);
+        fence_after();
+        const int key0 = (w.k0 + n) * BK;
+        const bool edge = key0 + BK > w.s.len;                        // rows of the tree, or the end, in this block
+        if (work) {
+          uint32_t vis[4] = {~0u, ~0u, ~0u, ~0u};
+          if (edge) {
+            const unsigned long long v0 = visible(path, w.s.len, key0), v1 = visible(path, w.s.len, key0 + 64);
+            vis[0] = (uint32_t)v0;
+            vis[1] = (uint32_t)(v0 >> 32);
+            vis[2] = (uint32_t)v1;
+            vis[3] = (uint32_t)(v1 >> 32);
+          }
+          float mx = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            float v[32];
+            ld32(sb + 32 * c, v);
+            wait_ld();
+            if (edge) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) v[e] = (vis[c] >> e) & 1 ? v[e] : -INFINITY;
+            }
+            float m0 = v[0], m1 = v[1], m2 = v[2], m3 = v[3];
+#pragma unroll
+            for (int e = 4; e < 32; e += 4) {
+              m0 = fmaxf(m0, v[e]);
+              m1 = fmaxf(m1, v[e + 1]);
+              m2 = fmaxf(m2, v[e + 2]);
+              m3 = fmaxf(m3, v[e + 3]);
+            }
+            mx = fmaxf(mx, fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)));
+          }
+          mx *= sh.scale2;
+          const bool raise = mx > m + TAU || (m == -INFINITY && mx > -INFINITY);
+          if (__any_sync(FULL, raise)) {
+            const float f = !raise ? 1.f : m == -INFINITY ? 0.f : ex2(m - mx);
+            if (raise) m = mx;
+            l *= f;
+            if (n != n0) {
+              wait(&sm->odone[s], (round[s] & 1) ^ 1);
+              fence_after();
+#pragma unroll
+              for (int c = 0; c < HD / 32; ++c) {
+                float v[32];
+                ld32(ob + 32 * c, v);
+                wait_ld();
+                uint32_t u[32];
+#pragma unroll
+                for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(v[e] * f);
+                st16(ob + 32 * c, u);
+                st16(ob + 32 * c + 16, u + 16);
+              }
+            }
+          }
+          const float mb = m == -INFINITY ? 0.f : m;
+          float l0 = 0.f, l1 = 0.f;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            float v[32];
+            ld32(sb + 32 * c, v);
+            wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              v[e] = ex2(fmaf(v[e], sh.scale2, -mb));
+              if (edge) v[e] = (vis[c] >> e) & 1 ? v[e] : 0.f;
+            }
+            uint32_t hi[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) hi[e] = pack2(v[2 * e], v[2 * e + 1]);
+            if (F32) {
+              uint32_t lo[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                l0 += v[2 * e];
+                l1 += v[2 * e + 1];
+                lo[e] = pack2(v[2 * e] - bf16lo(hi[e]), v[2 * e + 1] - bf16hi(hi[e]));
+              }
+              st16(sb + 32 * c, hi);
+              st16(sb + 32 * c + 16, lo);
+            } else {
+              // the sum of the rounded weights: a rounding then moves a value's share, not the rows' scale
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                l0 += bf16lo(hi[e]);
+                l1 += bf16hi(hi[e]);
+              }
+              st16(sb + 16 * c, hi);
+            }
+          }
+          l += l0 + l1;
+          wait_st();
+        }
+        if (edge && (!pair || s == 0)) {
+          clean_values(t0 + place_v(n, N, pair), key0);
+          fence_async();
+        }
+        fence_before();
+        mbar_arrive(&sm->pfull[s]);
+        ++round[s];
+      }
+      // (the other stream's rounds are known too: both streams' O are read below)
+      const int left = pair ? N : s == 0 ? N / 2 : (N + 1) / 2;
+      round[s ^ 1] += left;
+      sm->ml[s][r] = make_float2(m, l);
+      const bool both = pair || N > 1;
+      wait(&sm->odone[s], (round[s] & 1) ^ 1);
+      if (!pair && both) wait(&sm->odone[s ^ 1], (round[s ^ 1] & 1) ^ 1);
+      sm_sync();
+      fence_after();
+      if (work) {
+        const bool whole = w.k0 == 0 && N == w.n.nb;
+        float f[2] = {1.f, 1.f}, M = m, L = l;
+        if (!pair) {
+          const float2 u = sm->ml[0][r], v = sm->ml[1][r];
+          M = fmaxf(u.x, v.x);
+          f[0] = u.x == -INFINITY ? 0.f : ex2(u.x - M);
+          f[1] = v.x == -INFINITY ? 0.f : ex2(v.x - M);
+          L = f[0] * u.y + f[1] * v.y;
+        }
+        const unsigned long long bad = sm->bad & path;
+        const float inv = whole ? 1.f / L : 1.f;
+        const int c0 = pair ? 0 : s * (HD / 64), c1 = pair ? HD / 32 : c0 + HD / 64;
+        const size_t qat = ((size_t)w.n.b * a.R + qi) * a.ldq + (size_t)(w.n.kvh * G + g) * HD;
+        const size_t oat = ((size_t)w.n.b * a.R + qi) * a.ldo + (size_t)(w.n.kvh * G + g) * HD;
+        const size_t slot = (size_t)(2 * blockIdx.x + (w.k0 == 0)) * (p.tile * p.tpu) + mine;
+        for (int c = c0; c < c1; ++c) {
+          float v[32];
+          if (pair) {
+            ld32(ob + 32 * c, v);
+            wait_ld();
+          } else {
+            const uint32_t o0 = tmem + lanes + O_COL + 32 * c;
+            ld32(o0, v);
+            wait_ld();
+            if (both) {
+              float u[32];
+              ld32(o0 + HD, u);
+              wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) v[e] = f[0] * v[e] + f[1] * u[e];
+            }
+          }
+          if (mine < nrow) {
+            if (bad && key_here(bad)) {
+              for (unsigned long long b = bad; b; b &= b - 1) {
+                const int j = __ffsll((long long)b) - 1;
+                if (!in_piece(j)) continue;
+                const __nv_bfloat16* val;
+                const float pr = noted(qat, j, M == -INFINITY ? 0.f : M, &val);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) v[e] = fmaf(pr, __bfloat162float(val[32 * c + e]), v[e]);
+              }
+            }
+            if (!whole) {
+              float4* dst = reinterpret_cast<float4*>(a.part_o + slot * HD + 32 * c);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) dst[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+            } else if (F32) {
+              float4* dst = reinterpret_cast<float4*>((float*)a.out + oat + 32 * c);
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                dst[e] = make_float4(v[4 * e] * inv, v[4 * e + 1] * inv, v[4 * e + 2] * inv, v[4 * e + 3] * inv);
+            } else {
+              uint4* dst = reinterpret_cast<uint4*>((__nv_bfloat16*)a.out + oat + 32 * c);
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                dst[e] = make_uint4(pack2(v[8 * e] * inv, v[8 * e + 1] * inv), pack2(v[8 * e + 2] * inv, v[8 * e + 3] * inv),
+                                    pack2(v[8 * e + 4] * inv, v[8 * e + 5] * inv), pack2(v[8 * e + 6] * inv, v[8 * e + 7] * inv));
+            }
+          }
+        }
+        if (!whole && mine < nrow && (pair || s == 0)) a.part_ml[slot] = make_float2(M, L);
+      }
+      fence_before();
+      t0 += 2 * N;
+      w.step(a, p);
+    }
+  }
+  // Whether key len + j lies in this piece's blocks.
+  SPEC_DEV bool in_piece(int j) const {
+    const int k = (w.s.len + j) / BK - w.k0;
+    return k >= 0 && k < w.N;
+  }
+  SPEC_DEV bool key_here(unsigned long long b) const {
+    for (; b; b &= b - 1)
+      if (in_piece(__ffsll((long long)b) - 1)) return true;
+    return false;
+  }
+};
+
+template <int HD, bool F32>
+__global__ void __launch_bounds__(NTHR, 1)
+    tree_tc_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Plan p, const __grid_constant__ Shape sh,
+                   const __grid_constant__ CUtensorMap tm) {
+  extern __shared__ __align__(1024) unsigned char smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  Small* sm = reinterpret_cast<Small*>(smem);
+  Cta<HD, F32> k{a, p, sh, &tm, sm};
+  k.qt = smem + SMALL;
+  k.ring = k.qt + (size_t)sh.tiles * Cta<HD, F32>::QPL * Cta<HD, F32>::TILE;
+  grid_dep_launch();
+  long long* pre = reinterpret_cast<long long*>(k.ring);   // (before the first tile arrives there)
+  if (warp == 0) prefix(a, p, pre);
+  if (blockIdx.x == 0 && warp == 2) {
+    const bool bad = __any_sync(FULL, bad_input(a, lane, 32));
+    if (lane == 0) *a.err = bad ? SPEC_ERR_CAPACITY : 0;
+  }
+  __syncthreads();
+  const long long total = pre[a.B];
+  const int ctas = ctas_of(p, total);
+  if ((int)blockIdx.x >= ctas || total == 0) return;
+  k.w.x = part_start(total, blockIdx.x, ctas);
+  k.w.x1 = part_start(total, blockIdx.x + 1, ctas);
+  k.w.n = unit_at(a, p, pre, k.w.x);
+  k.w.s = seq_of(a, k.w.n.b);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < sh.stages; ++i) {
+      mbar_init(&sm->full[i], 1);
+      mbar_init(&sm->empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm->sfull[i], 1);
+      mbar_init(&sm->pfull[i], 128);
+      mbar_init(&sm->odone[i], 1);
+    }
+    mbar_init(&sm->qfull, NSM);
+    mbar_init(&sm->drain, 1);
+    sm->abort = 0;
+    mbar_init_fence();
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&tm) : "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(sa(&sm->tmem)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  fence_async();                                            // (the prefix's writes, before copies land on them)
+  fence_before();
+  __syncthreads();
+  fence_after();
+  k.tmem = sm->tmem;
+  if (warp == 0) {
+    k.producer();
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) k.products();
+    __syncwarp();
+  } else if (warp >= 4) {
+    k.softmax();
+  }
+  fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(k.tmem) : "memory");
+  }
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
+std::once_flag g_once;
+void init_encode() {
+  void* fn = nullptr;
+  cudaDriverEntryPointQueryResult q;
+  if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+      q == cudaDriverEntryPointSuccess)
+    g_encode = (PFN_cuTensorMapEncodeTiled_v12000)fn;
+}
+// A layer of the pool as rows of head-dim elements, boxes of a page's 64 rows x 64 dims.
+bool encode(CUtensorMap* m, const TreeArgs& a) {
+  if (!g_encode) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)a.hd, (cuuint64_t)a.n_pages * 2 * a.nkv * PAGE};
+  const cuuint64_t strides[1] = {(cuuint64_t)a.hd * 2};
+  const cuuint32_t box[2] = {64, PAGE}, es[2] = {1, 1};
+  return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(a.pool), dims, strides, box, es,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+const void* kernel_of(int hd, bool f32) {
+  return hd == 64 ? (f32 ? (const void*)tree_tc_kernel<64, true> : (const void*)tree_tc_kernel<64, false>)
+                  : (f32 ? (const void*)tree_tc_kernel<128, true> : (const void*)tree_tc_kernel<128, false>);
+}
+
+}  // namespace
+
+bool tc_ok(const TreeArgs& a) {
+  return a.kv_dtype == DT_BF16 && (a.hd == 64 || a.hd == 128) &&
+         (long long)a.n_pages * 2 * a.nkv * PAGE <= 0x7fffffffll;
+}
+
+Plan tc_plan(const TreeArgs& a) {
+  Plan p;
+  p.blk = BK;
+  p.tile = ROWS;
+  // two tiles share a block's reads; three planes of each do not fit beside a ring
+  p.tpu = a.q_dtype == DT_BF16 && a.R * (a.nq / a.nkv) > ROWS ? 2 : 1;
+  p.grid = num_sms();
+  p.min_cost = 1;
+  return p;
+}
+
+void tc_setup() {
+  std::call_once(g_once, init_encode);
+  for (int hd : {64, 128})
+    for (bool f : {false, true}) cudaFuncSetAttribute(kernel_of(hd, f), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_MAX);
+}
+
+int tc_launch(const TreeArgs& a, const Plan& p, cudaStream_t st) {
+  const bool f32 = a.q_dtype == DT_F32;
+  const int tile = a.hd * BK * 2;
+  Shape sh;
+  sh.tiles = p.tpu;
+  const size_t q = (size_t)sh.tiles * (f32 ? 3 : 1) * tile;
+  sh.stages = std::min(ST_MAX, (int)((SMEM_MAX - SMALL - q) / tile));
+  sh.scale2 = LOG2E / sqrtf((float)a.hd);
+  CUtensorMap tm;
+  if (!encode(&tm, a)) return -1;
+  void* args[] = {(void*)&a, (void*)&p, (void*)&sh, (void*)&tm};
+  return cudaLaunchKernel(kernel_of(a.hd, f32), dim3(p.grid), dim3(NTHR), args, SMALL + q + (size_t)sh.stages * tile, st) ==
+                 cudaSuccess
+             ? 1
+             : -1;
+}
+
+}  // namespace tree
+}  // namespace spec
