@@ -47,7 +47,7 @@ constexpr int HALF = BK * 128;          // 64 dims of a tile: 128 rows of 128 by
 constexpr int BOX = PAGE * 128;
 constexpr int ST_MAX = 12;
 constexpr float TAU = 8.f;              // the running maximum is raised past a growth of 2^8
-constexpr unsigned SPIN_LIMIT = 1u << 26;
+constexpr unsigned long long WAIT_NS = 1000000000ull;  // a wait's limit: 1 s
 
 // Shared memory: small items in the first 3 KB, then the query tiles and the ring.
 struct Small {
@@ -138,6 +138,23 @@ SPEC_DEV float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// Two products and sums at once.
+SPEC_DEV float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+      "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+SPEC_DEV float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tadd.rn.f32x2 w, x, y;\n\t"
+      "mov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
 SPEC_DEV uint32_t pack2(float a, float b) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -145,18 +162,31 @@ SPEC_DEV uint32_t pack2(float a, float b) {
 // Byte offset of (row, byte) in 128-byte rows: 16-byte chunk c of row r lies at c ^ (r % 8).
 SPEC_DEV uint32_t swz(int row, int byte) { return (uint32_t)(row * 128 + ((((byte >> 4) ^ (row & 7)) << 4) | (byte & 15))); }
 
+// (a try suspends the thread for a while, so that waiting warps leave the issue slots to others)
+SPEC_DEV bool mbar_try(uint64_t* b, unsigned parity) {
+  unsigned ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(sa(b)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 SPEC_DEV bool wait_phase(uint64_t* b, unsigned parity, volatile int* abort, int* err) {
-  for (unsigned it = 0; it < SPIN_LIMIT; ++it) {
-    if (mbar_test(b, parity)) return true;
+  if (mbar_try(b, parity)) return true;
+  const unsigned long long t0 = globaltimer();
+  do {
+    if (mbar_try(b, parity)) return true;
     if (*abort) return false;
-  }
+  } while (globaltimer() - t0 < WAIT_NS);
   *abort = 1;
   set_error(err, SPEC_ERR_TIMEOUT);
   return false;
 }
 SPEC_DEV void drain_phase(uint64_t* b, unsigned parity) {
-  for (unsigned it = 0; it < SPIN_LIMIT; ++it)
-    if (mbar_test(b, parity)) return;
+  const unsigned long long t0 = globaltimer();
+  while (!mbar_try(b, parity) && globaltimer() - t0 < WAIT_NS) {
+  }
 }
 
 // The pieces of units in this CTA's part, one after the other.
@@ -423,6 +453,79 @@ struct Cta {
     return ex2(fmaf(s, sh.scale2, -M));
   }
 
+  // A block's scores of this thread's row, 64 at a time: the largest one seen.
+  template <bool EDGE>
+  SPEC_DEV float row_max(uint32_t sb, const unsigned long long (&vis)[2]) const {
+    float mx = -INFINITY;
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) {
+      float v[64];
+      ld32(sb + 64 * h, v);
+      ld32(sb + 64 * h + 32, v + 32);
+      wait_ld();
+      if (EDGE) {
+        const unsigned long long b = h ? vis[1] : vis[0];
+#pragma unroll
+        for (int e = 0; e < 64; ++e) v[e] = (b >> e) & 1 ? v[e] : -INFINITY;
+      }
+      float m0 = v[0], m1 = v[1], m2 = v[2], m3 = v[3];
+#pragma unroll
+      for (int e = 4; e < 64; e += 4) {
+        m0 = fmaxf(m0, v[e]);
+        m1 = fmaxf(m1, v[e + 1]);
+        m2 = fmaxf(m2, v[e + 2]);
+        m3 = fmaxf(m3, v[e + 3]);
+      }
+      mx = fmaxf(mx, fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)));
+    }
+    return mx;
+  }
+  // Their weights over them, and the weights' sum. A bf16 row's sum is that of the
+  // rounded weights: a rounding then moves a value's share, not the row's scale.
+  template <bool EDGE>
+  SPEC_DEV float weights(uint32_t sb, const unsigned long long (&vis)[2], float m) const {
+    const float2 sc = make_float2(sh.scale2, sh.scale2), mm = make_float2(-m, -m);
+    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) {
+      float v[64];
+      ld32(sb + 64 * h, v);
+      ld32(sb + 64 * h + 32, v + 32);
+      wait_ld();
+      const unsigned long long b = h ? vis[1] : vis[0];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        uint32_t hi[16], lo[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int k = 32 * c + 2 * e;
+          float2 x = fma2(make_float2(v[k], v[k + 1]), sc, mm);
+          x.x = ex2(x.x);
+          x.y = ex2(x.y);
+          if (EDGE) {
+            x.x = (b >> k) & 1 ? x.x : 0.f;
+            x.y = (b >> (k + 1)) & 1 ? x.y : 0.f;
+          }
+          hi[e] = pack2(x.x, x.y);
+          const float2 r = make_float2(bf16lo(hi[e]), bf16hi(hi[e]));
+          if (F32) {
+            sum[e & 1] = add2(sum[e & 1], x);
+            lo[e] = pack2(x.x - r.x, x.y - r.y);
+          } else {
+            sum[e & 1] = add2(sum[e & 1], r);
+          }
+        }
+        if (F32) {
+          st16(sb + 64 * h + 32 * c, hi);
+          st16(sb + 64 * h + 32 * c + 16, lo);
+        } else {
+          st16(sb + 32 * h + 16 * c, hi);
+        }
+      }
+    }
+    return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+  }
+
   SPEC_DEV void softmax() {
     const int t = threadIdx.x - 128, s = t >> 7, r = t & 127, lane = t & 31, G = a.nq / a.nkv;
     const uint32_t lanes = (uint32_t)(r & ~31) << 16;
@@ -457,34 +560,12 @@ struct Cta {
         const int key0 = (w.k0 + n) * BK;
         const bool edge = key0 + BK > w.s.len;                        // rows of the tree, or the end, in this block
         if (work) {
-          uint32_t vis[4] = {~0u, ~0u, ~0u, ~0u};
+          unsigned long long vis[2] = {~0ull, ~0ull};
           if (edge) {
-            const unsigned long long v0 = visible(path, w.s.len, key0), v1 = visible(path, w.s.len, key0 + 64);
-            vis[0] = (uint32_t)v0;
-            vis[1] = (uint32_t)(v0 >> 32);
-            vis[2] = (uint32_t)v1;
-            vis[3] = (uint32_t)(v1 >> 32);
+            vis[0] = visible(path, w.s.len, key0);
+            vis[1] = visible(path, w.s.len, key0 + 64);
           }
-          float mx = -INFINITY;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            float v[32];
-            ld32(sb + 32 * c, v);
-            wait_ld();
-            if (edge) {
-#pragma unroll
-              for (int e = 0; e < 32; ++e) v[e] = (vis[c] >> e) & 1 ? v[e] : -INFINITY;
-            }
-            float m0 = v[0], m1 = v[1], m2 = v[2], m3 = v[3];
-#pragma unroll
-            for (int e = 4; e < 32; e += 4) {
-              m0 = fmaxf(m0, v[e]);
-              m1 = fmaxf(m1, v[e + 1]);
-              m2 = fmaxf(m2, v[e + 2]);
-              m3 = fmaxf(m3, v[e + 3]);
-            }
-            mx = fmaxf(mx, fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)));
-          }
+          float mx = edge ? row_max<true>(sb, vis) : row_max<false>(sb, vis);
           mx *= sh.scale2;
           const bool raise = mx > m + TAU || (m == -INFINITY && mx > -INFINITY);
           if (__any_sync(FULL, raise)) {
@@ -494,7 +575,7 @@ struct Cta {
             if (n != n0) {
               wait(&sm->odone[s], (round[s] & 1) ^ 1);
               fence_after();
-#pragma unroll
+#pragma unroll 1
               for (int c = 0; c < HD / 32; ++c) {
                 float v[32];
                 ld32(ob + 32 * c, v);
@@ -508,41 +589,7 @@ struct Cta {
             }
           }
           const float mb = m == -INFINITY ? 0.f : m;
-          float l0 = 0.f, l1 = 0.f;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            float v[32];
-            ld32(sb + 32 * c, v);
-            wait_ld();
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              v[e] = ex2(fmaf(v[e], sh.scale2, -mb));
-              if (edge) v[e] = (vis[c] >> e) & 1 ? v[e] : 0.f;
-            }
-            uint32_t hi[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) hi[e] = pack2(v[2 * e], v[2 * e + 1]);
-            if (F32) {
-              uint32_t lo[16];
-#pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                l0 += v[2 * e];
-                l1 += v[2 * e + 1];
-                lo[e] = pack2(v[2 * e] - bf16lo(hi[e]), v[2 * e + 1] - bf16hi(hi[e]));
-              }
-              st16(sb + 32 * c, hi);
-              st16(sb + 32 * c + 16, lo);
-            } else {
-              // the sum of the rounded weights: a rounding then moves a value's share, not the rows' scale
-#pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                l0 += bf16lo(hi[e]);
-                l1 += bf16hi(hi[e]);
-              }
-              st16(sb + 16 * c, hi);
-            }
-          }
-          l += l0 + l1;
+          l += edge ? weights<true>(sb, vis, mb) : weights<false>(sb, vis, mb);
           wait_st();
         }
         if (edge && (!pair || s == 0)) {
