@@ -48,7 +48,7 @@ template <typename QT, typename KT, int TR, int NJ>
 __global__ void __launch_bounds__(NTHR) tree_cc_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Plan p) {
   constexpr int ROWS = 16 * TR, PLD = ROWS + 4;
   extern __shared__ __align__(16) float sm[];
-  __shared__ long long pre[TREE_B_MAX + 1];
+  __shared__ int pre[TREE_B_MAX + 1];
   __shared__ unsigned long long path[64];
   __shared__ int up[64];
   grid_dep_launch();
@@ -63,17 +63,16 @@ __global__ void __launch_bounds__(NTHR) tree_cc_kernel(const __grid_constant__ T
     const int bad = __syncthreads_or(bad_input(a, t, NTHR));
     if (t == 0) *a.err = bad ? SPEC_ERR_CAPACITY : 0;
   }
-  const long long total = pre[a.B];
-  const int ctas = ctas_of(p, total);
-  if ((int)blockIdx.x >= ctas || total == 0) return;
-  long long x = part_start(total, blockIdx.x, ctas);
-  const long long x1 = part_start(total, blockIdx.x + 1, ctas);
+  const Cut cut(p, pre[a.B]);
+  if ((int)blockIdx.x >= cut.ctas) return;
+  int x = cut.start(blockIdx.x);
+  const int x1 = cut.start(blockIdx.x + 1);
   const float scale2 = LOG2E / sqrtf((float)hd);
 
   while (x < x1) {
     const Unit n = unit_at(a, p, pre, x);
     const int k0 = first_block(n, x), k1 = first_block(n, x1);
-    x = n.start + (long long)n.nb * n.w;
+    x = n.start + n.nb * n.w;
     if (k0 >= k1) continue;
     const Seq s = seq_of(a, n.b);
     const int row0 = n.u * ROWS, nrow = min(ROWS, s.rows * G - row0);
@@ -234,93 +233,115 @@ __global__ void __launch_bounds__(NTHR) tree_cc_kernel(const __grid_constant__ T
   }
 }
 
-// A warp per query row: rows of units that one CTA finished are left alone.
-template <typename QT>
+// A warp per query row: rows of units that one CTA finished are left alone. The
+// pieces' rows are read eight at a time; LN lanes hold a row, 32 / LN pieces go
+// side by side.
+template <typename QT, int LN, int NJ>
 __global__ void __launch_bounds__(NTHR) tree_join_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Plan p) {
-  __shared__ long long pre[TREE_B_MAX + 1];
+  __shared__ int pre[TREE_B_MAX + 1];
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, G = a.nq / a.nkv, hd = a.hd;
+  constexpr int SIDE = 32 / LN;
   if (w == 0) prefix(a, p, pre);  // (the call's inputs are not written by the kernel before this one)
   __syncthreads();
-  const long long total = pre[a.B];
-  const int ctas = ctas_of(p, total);
+  const Cut cut(p, pre[a.B]);
   grid_dep_wait();
-  if (total == 0 || ctas == 1) return;
-  const int urows = p.tile * p.tpu;
-  for (long long row = (long long)blockIdx.x * (NTHR / 32) + w; row < (long long)a.B * a.R * a.nq;
-       row += (long long)gridDim.x * (NTHR / 32)) {
-    const int h = (int)(row % a.nq), r = (int)(row / a.nq % a.R), b = (int)(row / a.nq / a.R);
+  if (cut.ctas == 1) return;
+  const int urows = p.tile * p.tpu, sub = lane / LN, ln = lane % LN;
+  for (int row = blockIdx.x * (NTHR / 32) + w; row < a.B * a.R * a.nq; row += gridDim.x * (NTHR / 32)) {
+    const int m = row / a.nq, h = row - m * a.nq, b = m / a.R, r = m - b * a.R;
     const Seq s = seq_of(a, b);
     if (r >= s.rows) continue;
-    const int kvh = h / G, q = r * G + h % G, T = tiles_of(p, G, s.rows), nb = blocks_of(p, s);
+    const int kvh = h / G, q = r * G + h - kvh * G, T = tiles_of(p, G, s.rows), nb = blocks_of(p, s);
     Unit n;
     n.b = b;
     n.kvh = kvh;
     n.u = q / urows;
     n.nb = nb;
     n.w = min(p.tpu, T - n.u * p.tpu);
-    n.start = pre[b] + (long long)kvh * nb * T + (long long)n.u * nb * p.tpu;
-    const long long end = n.start + (long long)nb * n.w;
+    n.start = pre[b] + (kvh * T + n.u * p.tpu) * nb;
     // the first and last CTA whose parts meet the unit
-    int c0 = (int)(n.start * ctas / total), c1 = (int)((end - 1) * ctas / total);
-    while (part_start(total, c0 + 1, ctas) <= n.start) ++c0;
-    while (c1 + 1 < ctas && part_start(total, c1 + 1, ctas) < end) ++c1;
+    const int c0 = cut.part_of(n.start), c1 = cut.part_of(n.start + nb * n.w - 1), at = q - n.u * urows;
     if (c0 == c1) continue;
-    const int at = q - n.u * urows;
-    // the pieces' maxima and sums: lane i takes the pieces i, i + 32, ...
-    float M = -INFINITY;
-    bool any = false;
-    for (int c = c0 + lane; c <= c1; c += 32) {
-      const int k0 = first_block(n, part_start(total, c, ctas)), k1 = first_block(n, part_start(total, c + 1, ctas));
-      if (k0 >= k1 || (k0 == 0 && k1 == nb)) continue;
-      M = fmaxf(M, a.part_ml[(size_t)(2 * c + (k0 == 0)) * urows + at].x);
-      any = true;
-    }
-    if (!__any_sync(FULL, any)) continue;  // one CTA had all of its blocks
-    M = warp_max(M);
-    float L = 0.f;
-    float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
-    for (int c = c0; c <= c1; c += 32) {
-      const int mine = c + lane;
-      float f = 0.f, fl = 0.f;
-      int first = 0;
-      if (mine <= c1) {
-        const int k0 = first_block(n, part_start(total, mine, ctas)), k1 = first_block(n, part_start(total, mine + 1, ctas));
-        if (k0 < k1) {
-          first = k0 == 0;
-          const float2 v = a.part_ml[(size_t)(2 * mine + first) * urows + at];
-          f = v.x == -INFINITY ? 0.f : ex2(v.x - M);
-          fl = f * v.y;
-        } else {
-          first = -1;
-        }
-      }
-      L += warp_sum(fl);
-      for (int i = 0; i < 32 && c + i <= c1; ++i) {
-        const float fi = __shfl_sync(FULL, f, i);
-        const int fs = __shfl_sync(FULL, first, i);
-        if (fs < 0) continue;
-        const float* src = a.part_o + ((size_t)(2 * (c + i) + fs) * urows + at) * hd;
+    float M = -INFINITY, L = 0.f;
+    float4 acc[NJ];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int d = 4 * lane + 128 * j;
-          if (d >= hd) break;
-          const float4 v = *reinterpret_cast<const float4*>(src + d);
-          acc[j].x = fmaf(fi, v.x, acc[j].x);
-          acc[j].y = fmaf(fi, v.y, acc[j].y);
-          acc[j].z = fmaf(fi, v.z, acc[j].z);
-          acc[j].w = fmaf(fi, v.w, acc[j].w);
+    for (int j = 0; j < NJ; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+    bool cutup = false;
+    for (int c = c0; c <= c1; c += 32) {
+      // lane i: the piece of CTA c + i, its maximum and sum
+      const int mine = c + lane;
+      int slot = -1;
+      float2 ml = make_float2(-INFINITY, 0.f);
+      if (mine <= c1) {
+        const int k0 = first_block(n, cut.start(mine)), k1 = first_block(n, cut.start(mine + 1));
+        if (k0 < k1 && k1 - k0 < nb) {
+          slot = (2 * mine + (k0 == 0)) * urows + at;
+          ml = a.part_ml[slot];
         }
       }
+      const unsigned have = __ballot_sync(FULL, slot >= 0);
+      if (!have) continue;
+      cutup = true;
+      const float mn = fmaxf(M, warp_max(ml.x));
+      const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - mn), old = M == -INFINITY ? 0.f : ex2(M - mn);
+      M = mn;
+      L = L * old + warp_sum(f * ml.y);
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        acc[j].x *= old; acc[j].y *= old; acc[j].z *= old; acc[j].w *= old;
+      }
+      const int last = min(32, c1 - c + 1);
+      for (int i0 = 0; i0 < last; i0 += 8 * SIDE) {
+        float4 v[8][NJ];
+        float fi[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int i = i0 + e * SIDE + sub;
+          const int si = __shfl_sync(FULL, slot, i & 31);
+          fi[e] = __shfl_sync(FULL, f, i & 31);
+          const bool in = i < last && si >= 0;
+#pragma unroll
+          for (int j = 0; j < NJ; ++j) {
+            const int d = 4 * ln + 4 * LN * j;
+            v[e][j] = in && d < hd ? *reinterpret_cast<const float4*>(a.part_o + (size_t)si * hd + d)
+                                   : make_float4(0.f, 0.f, 0.f, 0.f);
+          }
+          if (!in) fi[e] = 0.f;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+#pragma unroll
+          for (int j = 0; j < NJ; ++j) {
+            acc[j].x = fmaf(fi[e], v[e][j].x, acc[j].x);
+            acc[j].y = fmaf(fi[e], v[e][j].y, acc[j].y);
+            acc[j].z = fmaf(fi[e], v[e][j].z, acc[j].z);
+            acc[j].w = fmaf(fi[e], v[e][j].w, acc[j].w);
+          }
+      }
     }
+    if (!cutup) continue;  // one CTA had all of its blocks
     const float inv = 1.f / L;
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int d = 4 * lane + 128 * j;
-      if (d < hd)
-        store4((QT*)a.out + ((size_t)b * a.R + r) * a.ldo + (size_t)h * hd + d,
+    for (int j = 0; j < NJ; ++j) {
+#pragma unroll
+      for (int o = LN; o < 32; o <<= 1) {
+        acc[j].x += __shfl_xor_sync(FULL, acc[j].x, o);
+        acc[j].y += __shfl_xor_sync(FULL, acc[j].y, o);
+        acc[j].z += __shfl_xor_sync(FULL, acc[j].z, o);
+        acc[j].w += __shfl_xor_sync(FULL, acc[j].w, o);
+      }
+      const int d = 4 * ln + 4 * LN * j;
+      if (sub == 0 && d < hd)
+        store4((QT*)a.out + (size_t)m * a.ldo + (size_t)h * hd + d,
                make_float4(acc[j].x * inv, acc[j].y * inv, acc[j].z * inv, acc[j].w * inv));
     }
   }
+}
+
+template <typename QT>
+const void* join_kernel(int hd) {
+  return hd <= 64 ? (const void*)tree_join_kernel<QT, 16, 1>
+                  : hd <= 128 ? (const void*)tree_join_kernel<QT, 32, 1> : (const void*)tree_join_kernel<QT, 32, 2>;
 }
 
 template <typename QT, typename KT, int TR>
@@ -351,11 +372,16 @@ Plan cc_plan(const TreeArgs& a) {
   return p;
 }
 
+// The longest axis a call of this shape can have.
+long long axis_of(const TreeArgs& a, const Plan& p) {
+  const long long T = (a.R * (a.nq / a.nkv) + p.tile - 1) / p.tile;
+  return (long long)a.B * a.nkv * T * (((long long)a.max_pages * PAGE + p.blk - 1) / p.blk);
+}
+
 Plan plan_of(const TreeArgs& a) {
   Plan p = tc_ok(a) ? tc_plan(a) : cc_plan(a);
   // no more CTAs than the axis can have blocks
-  const long long T = (a.R * (a.nq / a.nkv) + p.tile - 1) / p.tile;
-  const long long most = (long long)a.B * a.nkv * T * (((long long)a.max_pages * PAGE + p.blk - 1) / p.blk);
+  const long long most = axis_of(a, p);
   p.grid = (int)std::max<long long>(1, std::min<long long>(p.grid, (most + p.min_cost - 1) / p.min_cost));
   return p;
 }
@@ -373,12 +399,16 @@ static TreeArgs shape_args(int B, int R, int nq, int nkv, int hd, int max_pages,
 }
 static size_t part_rows(const Plan& p) { return (size_t)2 * p.grid * p.tile * p.tpu; }
 
-// error word (256 bytes), maxima and sums, rows
+// error word (256 bytes), maxima and sums, rows; 0 where a kernel's axis (whose
+// numbers have 32 bits, slots of rows among them) may not hold the call
 size_t attn_tree_bytes(int B, int R, int nq, int nkv, int hd, int max_pages) {
   size_t most = 0;
   for (int q : {DT_F32, DT_BF16})
     for (int kv : {DT_F32, DT_BF16}) {
-      const size_t rows = part_rows(plan_of(shape_args(B, R, nq, nkv, hd, max_pages, q, kv)));
+      const TreeArgs a = shape_args(B, R, nq, nkv, hd, max_pages, q, kv);
+      const Plan p = plan_of(a);
+      if (axis_of(a, p) + 512 > 0x7fffffffll || (long long)B * R * nq > (1ll << 30)) return 0;
+      const size_t rows = part_rows(p);
       most = std::max(most, 256 + rows * (sizeof(float2) + (size_t)hd * sizeof(float)));
     }
   return most;
@@ -403,17 +433,16 @@ int attn_tree(TreeArgs a, void* ws, cudaStream_t st) {
     r = tc_launch(a, p, st);
   } else {
     const int TR = cc_rows(a);
-    void* args[] = {(void*)&a, (void*)&p};
-    if (cudaLaunchKernel(cc_pick(a.q_dtype, a.kv_dtype, TR, a.hd), dim3(p.grid), dim3(NTHR), args, cc_smem(a.hd, TR), st) !=
+    void* cargs[] = {(void*)&a, (void*)&p};
+    if (cudaLaunchKernel(cc_pick(a.q_dtype, a.kv_dtype, TR, a.hd), dim3(p.grid), dim3(NTHR), cargs, cc_smem(a.hd, TR), st) !=
         cudaSuccess)
       r = -1;
   }
   if (r < 0) return r;
-  // a unit of at most min_cost / tiles blocks is never cut where it starts a part; with one CTA nothing is
-  if (p.grid == 1) return r;
+  if (p.grid == 1) return r;  // nothing is cut
   cudaLaunchConfig_t cfg = {};
   const long long rows = (long long)a.B * a.R * a.nq;
-  cfg.gridDim = dim3((unsigned)std::min<long long>((rows + NTHR / 32 - 1) / (NTHR / 32), 4ll * num_sms()));
+  cfg.gridDim = dim3((unsigned)std::min<long long>((rows + NTHR / 32 - 1) / (NTHR / 32), 8ll * num_sms()));
   cfg.blockDim = dim3(NTHR);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -421,9 +450,9 @@ int attn_tree(TreeArgs a, void* ws, cudaStream_t st) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = a.q_dtype == DT_F32 ? cudaLaunchKernelEx(&cfg, tree_join_kernel<float>, a, p)
-                                            : cudaLaunchKernelEx(&cfg, tree_join_kernel<__nv_bfloat16>, a, p);
-  return e == cudaSuccess ? r + 1 : -1;
+  void* args[] = {(void*)&a, (void*)&p};
+  const void* f = a.q_dtype == DT_F32 ? join_kernel<float>(a.hd) : join_kernel<__nv_bfloat16>(a.hd);
+  return cudaLaunchKernelExC(&cfg, f, args) == cudaSuccess ? r + 1 : -1;
 }
 
 }  // namespace spec

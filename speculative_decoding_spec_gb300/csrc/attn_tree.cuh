@@ -47,21 +47,21 @@ SPEC_DEV int tiles_of(const Plan& p, int G, int rows) { return (rows * G + p.til
 SPEC_DEV int blocks_of(const Plan& p, const Seq& s) { return s.rows ? (s.len + s.rows + p.blk - 1) / p.blk : 0; }
 
 // pre[b] = start of sequence b on the axis, pre[B] its end. By the first warp.
-SPEC_DEV void prefix(const TreeArgs& a, const Plan& p, long long* pre) {
+SPEC_DEV void prefix(const TreeArgs& a, const Plan& p, int* pre) {
   const int lane = threadIdx.x & 31;
   const int G = a.nq / a.nkv;
-  long long run = 0;
+  int run = 0;  // (the launcher keeps the axis below 2^31)
   for (int b0 = 0; b0 < a.B; b0 += 32) {
     const int b = b0 + lane;
-    long long c = 0;
+    int c = 0;
     if (b < a.B) {
       const Seq s = seq_of(a, b);
-      c = (long long)a.nkv * blocks_of(p, s) * tiles_of(p, G, s.rows);
+      c = a.nkv * blocks_of(p, s) * tiles_of(p, G, s.rows);
     }
-    long long incl = c;
+    int incl = c;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long v = __shfl_up_sync(FULL, incl, o);
+      const int v = __shfl_up_sync(FULL, incl, o);
       if (lane >= o) incl += v;
     }
     if (b < a.B) pre[b] = run + incl - c;
@@ -69,19 +69,29 @@ SPEC_DEV void prefix(const TreeArgs& a, const Plan& p, long long* pre) {
   }
   if (lane == 0) pre[a.B] = run;
 }
-SPEC_DEV int ctas_of(const Plan& p, long long total) {
-  const long long most = (total + p.min_cost - 1) / p.min_cost;
-  return (int)(most < p.grid ? (most < 1 ? 1 : most) : p.grid);
-}
-SPEC_DEV long long part_start(long long total, int c, int ctas) { return total * c / ctas; }
+// The axis cut into parts: the first `more` of them are one longer than the others.
+struct Cut {
+  int total, ctas, base, more;
+  SPEC_DEV Cut(const Plan& p, int n) : total(n) {
+    const int most = n / p.min_cost + (n % p.min_cost != 0);
+    ctas = max(1, min(most, p.grid));
+    base = n / ctas;
+    more = n - base * ctas;
+  }
+  SPEC_DEV int start(int c) const { return base * c + min(c, more); }
+  SPEC_DEV int part_of(int x) const {  // x < total
+    const int edge = (base + 1) * more;
+    return x < edge ? x / (base + 1) : more + (x - edge) / base;
+  }
+};
 
 // A unit: its place on the axis and what it covers.
 struct Unit {
   int b, kvh, u;       // sequence, KV head, unit of the pair
   int nb, w;           // blocks, tiles
-  long long start;
+  int start;
 };
-SPEC_DEV int upper(const long long* pre, int B, long long x) {  // the last sequence that starts at or before x and is not empty
+SPEC_DEV int upper(const int* pre, int B, int x) {  // the last sequence that starts at or before x and is not empty
   int lo = 0, hi = B;  // first index with pre > x
   while (lo < hi) {
     const int m = (lo + hi) >> 1;
@@ -91,25 +101,23 @@ SPEC_DEV int upper(const long long* pre, int B, long long x) {  // the last sequ
   return lo - 1;
 }
 // The unit that holds position x (< total).
-SPEC_DEV Unit unit_at(const TreeArgs& a, const Plan& p, const long long* pre, long long x) {
+SPEC_DEV Unit unit_at(const TreeArgs& a, const Plan& p, const int* pre, int x) {
   Unit n;
   n.b = upper(pre, a.B, x);
   const Seq s = seq_of(a, n.b);
   const int T = tiles_of(p, a.nq / a.nkv, s.rows);
   n.nb = blocks_of(p, s);
-  const long long pair = (long long)n.nb * T, off = x - pre[n.b];
-  n.kvh = (int)(off / pair);
-  const long long in = off - n.kvh * pair;
-  n.u = (int)(in / ((long long)n.nb * p.tpu));
+  const int pair = n.nb * T, off = x - pre[n.b];
+  n.kvh = off / pair;
+  n.u = (off - n.kvh * pair) / (n.nb * p.tpu);
   n.w = min(p.tpu, T - n.u * p.tpu);
-  n.start = pre[n.b] + n.kvh * pair + (long long)n.u * n.nb * p.tpu;
+  n.start = pre[n.b] + n.kvh * pair + n.u * n.nb * p.tpu;
   return n;
 }
 // The blocks of unit n in [x0, x1) of the axis.
-SPEC_DEV int first_block(const Unit& n, long long x) {
-  if (x <= n.start) return 0;
-  const long long k = (x - n.start + n.w - 1) / n.w;
-  return k < n.nb ? (int)k : n.nb;
+SPEC_DEV int first_block(const Unit& n, int x) {
+  const int off = x - n.start;
+  return off <= 0 ? 0 : min(n.w == 1 ? off : (off + n.w - 1) / n.w, n.nb);
 }
 
 // Bit j of path[r]: row j is row r or an ancestor of it (rows below 64). By

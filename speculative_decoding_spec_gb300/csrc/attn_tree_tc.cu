@@ -62,7 +62,7 @@ constexpr size_t SMALL = 3072, SMEM_MAX = 227 * 1024;
 static_assert(sizeof(Small) <= SMALL, "");
 
 struct Shape {
-  int stages, tiles;                    // of the ring; query tiles a CTA
+  int stages, q_bytes;                  // of the ring; of the query tiles
   float scale2;
 };
 
@@ -88,19 +88,19 @@ constexpr uint32_t idesc(int M, int N, bool b_mn) {
   return (1u << 4) | (1u << 7) | (1u << 10) | (b_mn ? (1u << 16) : 0u) | ((uint32_t)(N >> 3) << 17) |
          ((uint32_t)(M >> 4) << 24);
 }
-SPEC_DEV void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, bool acc) {
+SPEC_DEV void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(id), "r"((uint32_t)acc)
+      "l"(a), "l"(b), "r"(id), "r"(acc)
       : "memory");
 }
 // A in tensor memory: a lane's 32-bit column holds two consecutive elements of its row.
-SPEC_DEV void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, bool acc) {
+SPEC_DEV void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(id), "r"((uint32_t)acc)
+      "r"(a), "l"(b), "r"(id), "r"(acc)
       : "memory");
 }
 SPEC_DEV void commit(uint64_t* bar) {
@@ -194,7 +194,7 @@ struct Walk {
   Unit n;
   Seq s;
   int k0, N;                            // first block, blocks
-  long long x, x1;
+  int x, x1;
   SPEC_DEV bool pieces(const TreeArgs& a, const Plan& p) {  // from unit n on: the next one with blocks here
     for (;;) {
       if (x >= x1) return false;
@@ -205,7 +205,7 @@ struct Walk {
     }
   }
   SPEC_DEV void step(const TreeArgs& a, const Plan& p) {
-    x = n.start + (long long)n.nb * n.w;
+    x = n.start + n.nb * n.w;
     n.start = x;
     if (x >= x1) return;
     const int G = a.nq / a.nkv;
@@ -307,104 +307,130 @@ struct Cta {
   }
 
   // ---- warp 1, one thread ----
-  SPEC_DEV bool issue_s(int s, int t, unsigned i, bool last) {
-    if (!wait(&sm->full[i % sh.stages], parity(i))) return false;
+  // A place in the ring, and the parity of its tile.
+  struct Place {
+    int s = 0;
+    unsigned ph = 0;
+  };
+  SPEC_DEV Place next(Place c) const {
+    if (++c.s == sh.stages) {
+      c.s = 0;
+      c.ph ^= 1;
+    }
+    return c;
+  }
+  // The loops stay rolled: what this thread executes for a product competes with
+  // eight softmax warps for the instruction caches (unrolled, a product took 160
+  // cycles to issue; the tensor cores need 64).
+  SPEC_DEV bool issue_s(int s, int t, Place k, bool last) {
+    if (!wait(&sm->full[k.s], k.ph)) return false;
     fence_after();
-    const uint32_t kb = sa(stage(i)), qb = sa(qt) + (uint32_t)(t * QPL * TILE);
+    uint64_t q = desc_k(sa(qt) + (uint32_t)(t * QPL * TILE));
+    const uint64_t kd = desc_k(sa(ring) + (uint32_t)(k.s * TILE));
+    const uint32_t d = tmem + s * 128;
+    uint32_t acc = 0;
+#pragma unroll 1
+    for (int i = 0; i < QPL * NH; ++i) {
+      const uint64_t kk = kd + (uint64_t)(i % NH) * (HALF >> 4);
 #pragma unroll
-    for (int pl = 0; pl < QPL; ++pl)
-#pragma unroll
-      for (int ks = 0; ks < HD / 16; ++ks) {
-        const uint32_t off = (ks >> 2) * HALF + 32 * (ks & 3);
-        mma_ss(tmem + s * 128, desc_k(qb + pl * TILE + off), desc_k(kb + off), idesc(ROWS, BK, false), pl > 0 || ks > 0);
+      for (int j = 0; j < 4; ++j) {
+        mma_ss(d, q + 2 * j, kk + 2 * j, idesc(ROWS, BK, false), acc);
+        acc = 1;
       }
+      q += HALF >> 4;
+    }
     commit(&sm->sfull[s]);
-    if (last) commit(&sm->empty[i % sh.stages]);
+    if (last) commit(&sm->empty[k.s]);
     return true;
   }
-  SPEC_DEV bool issue_pv(int s, unsigned i, unsigned round, bool first, bool last) {
-    if (!wait(&sm->pfull[s], round & 1) || !wait(&sm->full[i % sh.stages], parity(i))) return false;
+  SPEC_DEV bool issue_pv(int s, Place v, unsigned round, bool first, bool last) {
+    if (!wait(&sm->pfull[s], round & 1) || !wait(&sm->full[v.s], v.ph)) return false;
     fence_after();
-    const uint32_t vb = sa(stage(i)), pb = tmem + s * 128, ob = tmem + O_COL + s * HD;
+    uint64_t vd = desc_mn(sa(ring) + (uint32_t)(v.s * TILE), HALF);
+    uint32_t pb = tmem + s * 128;
+    const uint32_t ob = tmem + O_COL + s * HD;
+    uint32_t acc = !first;
+#pragma unroll 1
+    for (int c = 0; c < BK / 32; ++c) {  // 32 keys: four groups of 8 rows of V, 16 columns of P
 #pragma unroll
-    for (int ks = 0; ks < BK / 16; ++ks) {  // 16 keys: two groups of 8 rows of V, 8 columns of P
-      const uint64_t v = desc_mn(vb + 2048 * ks, HALF);
-      if (F32) {  // (a chunk of 32 keys: its leading parts, then the rest)
-        const uint32_t at = pb + 32 * (ks >> 1) + 8 * (ks & 1);
-        mma_ts(ob, at, v, idesc(ROWS, HD, true), !first || ks > 0);
-        mma_ts(ob, at + 16, v, idesc(ROWS, HD, true), true);
-      } else {
-        mma_ts(ob, pb + 8 * ks, v, idesc(ROWS, HD, true), !first || ks > 0);
+      for (int j = 0; j < 2; ++j) {
+        mma_ts(ob, pb + 8 * j, vd + j * (2048 >> 4), idesc(ROWS, HD, true), acc);
+        acc = 1;
+        if (F32) mma_ts(ob, pb + 16 + 8 * j, vd + j * (2048 >> 4), idesc(ROWS, HD, true), 1);  // (the weights' rest)
       }
+      pb += F32 ? 32 : 16;
+      vd += 4096 >> 4;
     }
     commit(&sm->odone[s]);
-    if (last) commit(&sm->empty[i % sh.stages]);
+    if (last) commit(&sm->empty[v.s]);
     return true;
   }
   SPEC_DEV void products() {
-    unsigned t0 = 0, piece = 0, round[2] = {0, 0};
+    unsigned piece = 0, round[2] = {0, 0};
+    Place at;  // the next tile
     bool ok = true;
     while (ok && w.pieces(a, p)) {
       const bool pair = w.n.w == 2;
       const int N = w.N;
       ok = wait(&sm->qfull, piece & 1);
       fence_after();
-      if (pair) {
-        ok = ok && issue_s(0, 0, t0, false) && issue_s(1, 1, t0, true);
-        for (int n = 0; ok && n < N; ++n)
-          for (int s = 0; ok && s < 2; ++s) {
-            ok = issue_pv(s, t0 + place_v(n, N, true), round[s]++, n == 0, s == 1);
-            if (ok && n + 1 < N) ok = issue_s(s, s, t0 + place_k(n + 1, true), s == 1);
-          }
-      } else {
-        ok = ok && issue_s(0, 0, t0, true) && (N < 2 || issue_s(1, 0, t0 + 1, true));
-        for (int n = 0; ok && n < N; ++n) {
-          const int s = n & 1;
-          ok = issue_pv(s, t0 + place_v(n, N, false), round[s]++, n < 2, true);
-          if (ok && n + 2 < N) ok = issue_s(s, 0, t0 + place_k(n + 2, false), true);
+      // the first scores of both streams, then in turn a stream's output and its next scores
+      for (int n = -2, s = 0; ok && n < (pair ? 2 * N : N); ++n, s ^= 1) {
+        // (two tiles: step n is block n / 2 of stream n & 1, and a tile of the ring serves two steps)
+        const bool shared = pair && s == 1;
+        if (n >= 0) {
+          if (!shared) vt = at, at = next(at);
+          ok = issue_pv(s, vt, round[s]++, n < 2, !pair || shared);
+        }
+        if (ok && n + 2 < (pair ? 2 * N : N)) {
+          if (!shared) kt = at, at = next(at);
+          ok = issue_s(s, pair ? s : 0, kt, !pair || shared);
         }
       }
-      t0 += 2 * N;
       ++piece;
       w.step(a, p);
     }
     commit(&sm->drain);  // every product done before tensor memory is freed
     drain_phase(&sm->drain, 0);
   }
+  Place kt, vt;
 
   // ---- warps 4-11: thread = row of a tile ----
   SPEC_DEV void load_q(int row0, int nrow) {
-    const int t = threadIdx.x - 128, G = a.nq / a.nkv;
-    const int tiles = w.n.w;
-    for (int i = t; i < tiles * ROWS * (HD / 8); i += NSM) {
-      const int c = i % (HD / 8), r = i / (HD / 8), ti = r / ROWS, rr = r % ROWS;
-      unsigned char* dst = qt + (size_t)ti * QPL * TILE + (c >> 3) * HALF + swz(rr, (c & 7) * 16);
-      const bool in = r < nrow;
-      const int gr = row0 + r, qi = gr / G, g = gr - qi * G;
-      const size_t at = ((size_t)w.n.b * a.R + qi) * a.ldq + (size_t)(w.n.kvh * G + g) * HD + 8 * c;
-      if (!F32) {
-        const uint4 v = in ? *reinterpret_cast<const uint4*>((const __nv_bfloat16*)a.q + at) : make_uint4(0, 0, 0, 0);
-        *reinterpret_cast<uint4*>(dst) = v;
-      } else {
-        float f[8];
-        if (in) {
-          const float4 u = *reinterpret_cast<const float4*>((const float*)a.q + at);
-          const float4 v = *reinterpret_cast<const float4*>((const float*)a.q + at + 4);
-          f[0] = u.x; f[1] = u.y; f[2] = u.z; f[3] = u.w; f[4] = v.x; f[5] = v.y; f[6] = v.z; f[7] = v.w;
+    const int t = threadIdx.x - 128, G = a.nq / a.nkv, c = t % (HD / 8);
+    constexpr int STEP = NSM / (HD / 8), U = F32 ? 4 : 8;  // rows a round, rounds in flight
+    for (int r0 = t / (HD / 8); r0 < w.n.w * ROWS; r0 += U * STEP) {
+      uint4 v[U][F32 ? 2 : 1];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int r = r0 + u * STEP, gr = row0 + r, qi = gr / G, g = gr - qi * G;
+        const size_t at = ((size_t)w.n.b * a.R + qi) * a.ldq + (size_t)(w.n.kvh * G + g) * HD + 8 * c;
+#pragma unroll
+        for (int e = 0; e < (F32 ? 2 : 1); ++e)
+          v[u][e] = r < nrow ? *reinterpret_cast<const uint4*>((const char*)a.q + at * (F32 ? 4 : 2) + 16 * e)
+                             : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int r = r0 + u * STEP;
+        unsigned char* dst = qt + (size_t)(r / ROWS) * QPL * TILE + (c >> 3) * HALF + swz(r % ROWS, (c & 7) * 16);
+        if (!F32) {
+          *reinterpret_cast<uint4*>(dst) = v[u][0];
         } else {
+          const uint4 x = v[u][0], y = v[u][F32 ? 1 : 0];
+          float f[8] = {__uint_as_float(x.x), __uint_as_float(x.y), __uint_as_float(x.z), __uint_as_float(x.w),
+                        __uint_as_float(y.x), __uint_as_float(y.y), __uint_as_float(y.z), __uint_as_float(y.w)};
 #pragma unroll
-          for (int e = 0; e < 8; ++e) f[e] = 0.f;
-        }
+          for (int pl = 0; pl < 3; ++pl) {  // x = hi + mid + lo: 24 bits in three times 8
+            uint32_t o[4];
 #pragma unroll
-        for (int pl = 0; pl < 3; ++pl) {  // x = hi + mid + lo: 24 bits in three times 8
-          uint32_t o[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            o[e] = pack2(f[2 * e], f[2 * e + 1]);
-            f[2 * e] -= bf16lo(o[e]);
-            f[2 * e + 1] -= bf16hi(o[e]);
+            for (int e = 0; e < 4; ++e) {
+              o[e] = pack2(f[2 * e], f[2 * e + 1]);
+              f[2 * e] -= bf16lo(o[e]);
+              f[2 * e + 1] -= bf16hi(o[e]);
+            }
+            *reinterpret_cast<uint4*>(dst + pl * TILE) = make_uint4(o[0], o[1], o[2], o[3]);
           }
-          *reinterpret_cast<uint4*>(dst + pl * TILE) = make_uint4(o[0], o[1], o[2], o[3]);
         }
       }
     }
@@ -625,6 +651,8 @@ struct Cta {
         const size_t qat = ((size_t)w.n.b * a.R + qi) * a.ldq + (size_t)(w.n.kvh * G + g) * HD;
         const size_t oat = ((size_t)w.n.b * a.R + qi) * a.ldo + (size_t)(w.n.kvh * G + g) * HD;
         const size_t slot = (size_t)(2 * blockIdx.x + (w.k0 == 0)) * (p.tile * p.tpu) + mine;
+        float4* stg = reinterpret_cast<float4*>(qt) + (t >> 5) * 256;
+#pragma unroll 1
         for (int c = c0; c < c1; ++c) {
           float v[32];
           if (pair) {
@@ -642,32 +670,41 @@ struct Cta {
               for (int e = 0; e < 32; ++e) v[e] = f[0] * v[e] + f[1] * u[e];
             }
           }
-          if (mine < nrow) {
-            if (bad && key_here(bad)) {
-              for (unsigned long long b = bad; b; b &= b - 1) {
-                const int j = __ffsll((long long)b) - 1;
-                if (!in_piece(j)) continue;
-                const __nv_bfloat16* val;
-                const float pr = noted(qat, j, M == -INFINITY ? 0.f : M, &val);
+          if (bad && mine < nrow && key_here(bad)) {
+            for (unsigned long long b = bad; b; b &= b - 1) {
+              const int j = __ffsll((long long)b) - 1;
+              if (!in_piece(j)) continue;
+              const __nv_bfloat16* val;
+              const float pr = noted(qat, j, M == -INFINITY ? 0.f : M, &val);
 #pragma unroll
-                for (int e = 0; e < 32; ++e) v[e] = fmaf(pr, __bfloat162float(val[32 * c + e]), v[e]);
-              }
+              for (int e = 0; e < 32; ++e) v[e] = fmaf(pr, __bfloat162float(val[32 * c + e]), v[e]);
             }
-            if (!whole) {
-              float4* dst = reinterpret_cast<float4*>(a.part_o + slot * HD + 32 * c);
+          }
+          // through shared memory (the query tiles are done with), so that stores are whole 128-byte (64: bf16) pieces of rows
+          __syncwarp();
 #pragma unroll
-              for (int e = 0; e < 8; ++e) dst[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
-            } else if (F32) {
-              float4* dst = reinterpret_cast<float4*>((float*)a.out + oat + 32 * c);
+          for (int e = 0; e < 8; ++e)
+            stg[lane * 8 + (e ^ (lane & 7))] = make_float4(v[4 * e] * inv, v[4 * e + 1] * inv, v[4 * e + 2] * inv, v[4 * e + 3] * inv);
+          __syncwarp();
+          const int w0 = mine & ~31;                                  // the warp's first row
+          if (F32 || !whole) {
 #pragma unroll
-              for (int e = 0; e < 8; ++e)
-                dst[e] = make_float4(v[4 * e] * inv, v[4 * e + 1] * inv, v[4 * e + 2] * inv, v[4 * e + 3] * inv);
-            } else {
-              uint4* dst = reinterpret_cast<uint4*>((__nv_bfloat16*)a.out + oat + 32 * c);
+            for (int i = 0; i < 8; ++i) {
+              const int rr = 4 * i + (lane >> 3), e = lane & 7;
+              const float4 x = stg[rr * 8 + (e ^ (rr & 7))];
+              const size_t to = __shfl_sync(FULL, (unsigned long long)oat, rr);
+              float* dst = whole ? (float*)a.out + to : a.part_o + (slot - lane + rr) * HD;
+              if (w0 + rr < nrow) *reinterpret_cast<float4*>(dst + 32 * c + 4 * e) = x;
+            }
+          } else {
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                dst[e] = make_uint4(pack2(v[8 * e] * inv, v[8 * e + 1] * inv), pack2(v[8 * e + 2] * inv, v[8 * e + 3] * inv),
-                                    pack2(v[8 * e + 4] * inv, v[8 * e + 5] * inv), pack2(v[8 * e + 6] * inv, v[8 * e + 7] * inv));
+            for (int i = 0; i < 4; ++i) {
+              const int rr = 8 * i + (lane >> 2), e = 2 * (lane & 3);
+              const float4 x = stg[rr * 8 + (e ^ (rr & 7))], y = stg[rr * 8 + ((e + 1) ^ (rr & 7))];
+              const size_t to = __shfl_sync(FULL, (unsigned long long)oat, rr);
+              if (w0 + rr < nrow)
+                *reinterpret_cast<uint4*>((__nv_bfloat16*)a.out + to + 32 * c + 4 * e) =
+                    make_uint4(pack2(x.x, x.y), pack2(x.z, x.w), pack2(y.x, y.y), pack2(y.z, y.w));
             }
           }
         }
@@ -699,23 +736,15 @@ __global__ void __launch_bounds__(NTHR, 1)
   Small* sm = reinterpret_cast<Small*>(smem);
   Cta<HD, F32> k{a, p, sh, &tm, sm};
   k.qt = smem + SMALL;
-  k.ring = k.qt + (size_t)sh.tiles * Cta<HD, F32>::QPL * Cta<HD, F32>::TILE;
+  k.ring = k.qt + sh.q_bytes;
   grid_dep_launch();
-  long long* pre = reinterpret_cast<long long*>(k.ring);   // (before the first tile arrives there)
-  if (warp == 0) prefix(a, p, pre);
-  if (blockIdx.x == 0 && warp == 2) {
-    const bool bad = __any_sync(FULL, bad_input(a, lane, 32));
-    if (lane == 0) *a.err = bad ? SPEC_ERR_CAPACITY : 0;
-  }
-  __syncthreads();
-  const long long total = pre[a.B];
-  const int ctas = ctas_of(p, total);
-  if ((int)blockIdx.x >= ctas || total == 0) return;
-  k.w.x = part_start(total, blockIdx.x, ctas);
-  k.w.x1 = part_start(total, blockIdx.x + 1, ctas);
-  k.w.n = unit_at(a, p, pre, k.w.x);
-  k.w.s = seq_of(a, k.w.n.b);
-  if (threadIdx.x == 0) {
+  int* pre = reinterpret_cast<int*>(k.ring);                // (before the first tile arrives there)
+  if (warp == 0) {
+    prefix(a, p, pre);
+  } else if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(sa(&sm->tmem)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  } else if (threadIdx.x == 64) {
     for (int i = 0; i < sh.stages; ++i) {
       mbar_init(&sm->full[i], 1);
       mbar_init(&sm->empty[i], 1);
@@ -731,22 +760,30 @@ __global__ void __launch_bounds__(NTHR, 1)
     mbar_init_fence();
     asm volatile("prefetch.tensormap [%0];" ::"l"(&tm) : "memory");
   }
-  if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(sa(&sm->tmem)) : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-  }
-  fence_async();                                            // (the prefix's writes, before copies land on them)
   fence_before();
   __syncthreads();
   fence_after();
   k.tmem = sm->tmem;
-  if (warp == 0) {
+  const Cut cut(p, pre[a.B]);
+  const bool work = (int)blockIdx.x < cut.ctas && cut.total > 0;
+  if (work) {
+    k.w.x = cut.start(blockIdx.x);
+    k.w.x1 = cut.start(blockIdx.x + 1);
+    k.w.n = unit_at(a, p, pre, k.w.x);
+    k.w.s = seq_of(a, k.w.n.b);
+  }
+  fence_async();                                            // (the prefix is read and gone, before copies land on it)
+  __syncthreads();
+  if (blockIdx.x == 0 && warp == 2) {
+    const bool bad = __any_sync(FULL, bad_input(a, lane, 32));
+    if (lane == 0) *a.err = bad ? SPEC_ERR_CAPACITY : 0;
+  } else if (work && warp == 0) {
     k.producer();
     __syncwarp();
-  } else if (warp == 1) {
+  } else if (work && warp == 1) {
     if (lane == 0) k.products();
     __syncwarp();
-  } else if (warp >= 4) {
+  } else if (work && warp >= 4) {
     k.softmax();
   }
   fence_before();
@@ -810,8 +847,8 @@ int tc_launch(const TreeArgs& a, const Plan& p, cudaStream_t st) {
   const bool f32 = a.q_dtype == DT_F32;
   const int tile = a.hd * BK * 2;
   Shape sh;
-  sh.tiles = p.tpu;
-  const size_t q = (size_t)sh.tiles * (f32 ? 3 : 1) * tile;
+  const size_t q = std::max((size_t)p.tpu * (f32 ? 3 : 1) * tile, (size_t)NSM * 128);  // (and a row of results a softmax thread)
+  sh.q_bytes = (int)q;
   sh.stages = std::min(ST_MAX, (int)((SMEM_MAX - SMALL - q) / tile));
   sh.scale2 = LOG2E / sqrtf((float)a.hd);
   CUtensorMap tm;

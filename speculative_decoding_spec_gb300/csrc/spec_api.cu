@@ -1138,8 +1138,9 @@ spec_status spec_attention_tree(const spec_model_desc* m, const spec_kv_desc* kv
       ldq < (int64_t)n_q_heads * m->head_dim || ldo < (int64_t)n_q_heads * m->head_dim)
     return SPEC_EINVAL;
   if (B > TREE_B_MAX || R > TREE_ROWS_MAX || m->head_dim % 8) return SPEC_EUNSUPPORTED;
-  if (ws_bytes < attn_tree_bytes(B, R, n_q_heads, m->n_kv_heads, m->head_dim, kv->max_pages_per_seq))
-    return SPEC_ECAPACITY;
+  const size_t need = attn_tree_bytes(B, R, n_q_heads, m->n_kv_heads, m->head_dim, kv->max_pages_per_seq);
+  if (need == 0) return SPEC_EUNSUPPORTED;
+  if (ws_bytes < need) return SPEC_ECAPACITY;
   TreeArgs a = {};
   a.B = B; a.R = R; a.nq = n_q_heads; a.nkv = m->n_kv_heads; a.hd = m->head_dim;
   a.q_dtype = q_dtype == SPEC_F32 ? DT_F32 : DT_BF16;
