@@ -48,7 +48,6 @@ template <typename QT, typename KT, int TR, int NJ>
 __global__ void __launch_bounds__(NTHR) tree_cc_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Plan p) {
   constexpr int ROWS = 16 * TR, PLD = ROWS + 4;
   extern __shared__ __align__(16) float sm[];
-  __shared__ int pre[TREE_B_MAX + 1];
   __shared__ unsigned long long path[64];
   __shared__ int up[64];
   grid_dep_launch();
@@ -57,20 +56,19 @@ __global__ void __launch_bounds__(NTHR) tree_cc_kernel(const __grid_constant__ T
   float* ks = qs + hd * ROWS;     // [hd][KLD]
   float* vs = ks + hd * KLD;      // [PAGE][hd]
   float* ps = vs + PAGE * hd;     // [PAGE][PLD]
-  if (t < 32) prefix(a, p, pre);
-  __syncthreads();
+  const Axis axis(a, p);
   if (blockIdx.x == 0) {
     const int bad = __syncthreads_or(bad_input(a, t, NTHR));
     if (t == 0) *a.err = bad ? SPEC_ERR_CAPACITY : 0;
   }
-  const Cut cut(p, pre[a.B]);
+  const Cut cut(p, axis.total);
   if ((int)blockIdx.x >= cut.ctas) return;
   int x = cut.start(blockIdx.x);
   const int x1 = cut.start(blockIdx.x + 1);
   const float scale2 = LOG2E / sqrtf((float)hd);
 
   while (x < x1) {
-    const Unit n = unit_at(a, p, pre, x);
+    const Unit n = unit_at(a, p, axis, x);
     const int k0 = first_block(n, x), k1 = first_block(n, x1);
     x = n.start + n.nb * n.w;
     if (k0 >= k1) continue;
@@ -233,6 +231,18 @@ __global__ void __launch_bounds__(NTHR) tree_cc_kernel(const __grid_constant__ T
   }
 }
 
+// pre[b] = where sequence b starts on the axis, pre[B] its end. By one warp.
+SPEC_DEV void starts(const TreeArgs& a, const Plan& p, int* pre) {
+  const int lane = threadIdx.x & 31;
+  int run = 0;
+  for (int b0 = 0; b0 < a.B; b0 += 32) {
+    const int c = b0 + lane < a.B ? cost_of(a, p, b0 + lane) : 0, end = run + scan32(c);
+    if (b0 + lane < a.B) pre[b0 + lane] = end - c;
+    run = __shfl_sync(FULL, end, 31);
+  }
+  if (lane == 0) pre[a.B] = run;
+}
+
 // A warp per query row: rows of units that one CTA finished are left alone. The
 // pieces' rows are read eight at a time; LN lanes hold a row, 32 / LN pieces go
 // side by side.
@@ -241,7 +251,7 @@ __global__ void __launch_bounds__(NTHR) tree_join_kernel(const __grid_constant__
   __shared__ int pre[TREE_B_MAX + 1];
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, G = a.nq / a.nkv, hd = a.hd;
   constexpr int SIDE = 32 / LN;
-  if (w == 0) prefix(a, p, pre);  // (the call's inputs are not written by the kernel before this one)
+  if (w == 0) starts(a, p, pre);  // (the call's inputs are not written by the kernel before this one)
   __syncthreads();
   const Cut cut(p, pre[a.B]);
   grid_dep_wait();

@@ -46,29 +46,52 @@ SPEC_DEV Seq seq_of(const TreeArgs& a, int b) {
 SPEC_DEV int tiles_of(const Plan& p, int G, int rows) { return (rows * G + p.tile - 1) / p.tile; }
 SPEC_DEV int blocks_of(const Plan& p, const Seq& s) { return s.rows ? (s.len + s.rows + p.blk - 1) / p.blk : 0; }
 
-// pre[b] = start of sequence b on the axis, pre[B] its end. By the first warp.
-SPEC_DEV void prefix(const TreeArgs& a, const Plan& p, int* pre) {
-  const int lane = threadIdx.x & 31;
-  const int G = a.nq / a.nkv;
-  int run = 0;  // (the launcher keeps the axis below 2^31)
-  for (int b0 = 0; b0 < a.B; b0 += 32) {
-    const int b = b0 + lane;
-    int c = 0;
-    if (b < a.B) {
-      const Seq s = seq_of(a, b);
-      c = a.nkv * blocks_of(p, s) * tiles_of(p, G, s.rows);
-    }
-    int incl = c;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(FULL, incl, o);
-      if (lane >= o) incl += v;
-    }
-    if (b < a.B) pre[b] = run + incl - c;
-    run += __shfl_sync(FULL, incl, 31);
-  }
-  if (lane == 0) pre[a.B] = run;
+SPEC_DEV int cost_of(const TreeArgs& a, const Plan& p, int b) {
+  const Seq s = seq_of(a, b);
+  return a.nkv * blocks_of(p, s) * tiles_of(p, a.nq / a.nkv, s.rows);  // (the launcher keeps the axis below 2^31)
 }
+// This lane's sequence of 32: where it ends, from the start of the first.
+SPEC_DEV int scan32(int c) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(FULL, c, o);
+    if (lane >= o) c += v;
+  }
+  return c;
+}
+// The sequences' places on the axis, by a whole warp: 32 of them in the lanes, the
+// others looked at again when they are asked for.
+struct Axis {
+  int mine, end0, total;  // this lane's sequence's end, the 32 sequences', the axis's
+  SPEC_DEV Axis(const TreeArgs& a, const Plan& p) {
+    const int lane = threadIdx.x & 31;
+    mine = scan32(lane < a.B ? cost_of(a, p, lane) : 0);
+    end0 = total = __shfl_sync(FULL, mine, 31);
+    for (int b0 = 32; b0 < a.B; b0 += 32) {
+      int c = b0 + lane < a.B ? cost_of(a, p, b0 + lane) : 0;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(FULL, c, o);
+      total += c;
+    }
+  }
+  // The sequence that holds x (< total), and where it starts.
+  SPEC_DEV int at(const TreeArgs& a, const Plan& p, int x, int& start) const {
+    const int lane = threadIdx.x & 31;
+    int base = 0, end = mine, b0 = 0, last = end0;
+    while (x >= last) {
+      b0 += 32;
+      base = last;
+      end = base + scan32(b0 + lane < a.B ? cost_of(a, p, b0 + lane) : 0);
+      last = __shfl_sync(FULL, end, 31);
+    }
+    const int i = __ffs(__ballot_sync(FULL, end > x)) - 1;
+    const int before = __shfl_sync(FULL, end, (i + 31) & 31);
+    start = i ? before : base;
+    return b0 + i;
+  }
+};
+
 // The axis cut into parts: the first `more` of them are one longer than the others.
 struct Cut {
   int total, ctas, base, more;
@@ -91,27 +114,19 @@ struct Unit {
   int nb, w;           // blocks, tiles
   int start;
 };
-SPEC_DEV int upper(const int* pre, int B, int x) {  // the last sequence that starts at or before x and is not empty
-  int lo = 0, hi = B;  // first index with pre > x
-  while (lo < hi) {
-    const int m = (lo + hi) >> 1;
-    if (pre[m] > x) hi = m;
-    else lo = m + 1;
-  }
-  return lo - 1;
-}
-// The unit that holds position x (< total).
-SPEC_DEV Unit unit_at(const TreeArgs& a, const Plan& p, const int* pre, int x) {
+// The unit that holds position x (< total). By a whole warp.
+SPEC_DEV Unit unit_at(const TreeArgs& a, const Plan& p, const Axis& axis, int x) {
   Unit n;
-  n.b = upper(pre, a.B, x);
+  int start;
+  n.b = axis.at(a, p, x, start);
   const Seq s = seq_of(a, n.b);
   const int T = tiles_of(p, a.nq / a.nkv, s.rows);
   n.nb = blocks_of(p, s);
-  const int pair = n.nb * T, off = x - pre[n.b];
+  const int pair = n.nb * T, off = x - start;
   n.kvh = off / pair;
   n.u = (off - n.kvh * pair) / (n.nb * p.tpu);
   n.w = min(p.tpu, T - n.u * p.tpu);
-  n.start = pre[n.b] + n.kvh * pair + n.u * n.nb * p.tpu;
+  n.start = start + n.kvh * pair + n.u * n.nb * p.tpu;
   return n;
 }
 // The blocks of unit n in [x0, x1) of the axis.

@@ -47,7 +47,7 @@ constexpr int HALF = BK * 128;          // 64 dims of a tile: 128 rows of 128 by
 constexpr int BOX = PAGE * 128;
 constexpr int ST_MAX = 12;
 constexpr float TAU = 8.f;              // the running maximum is raised past a growth of 2^8
-constexpr unsigned long long WAIT_NS = 1000000000ull;  // a wait's limit: 1 s
+constexpr long long WAIT_CYCLES = 2000000000ll;  // a wait's limit: a second or so
 
 // Shared memory: small items in the first 3 KB, then the query tiles and the ring.
 struct Small {
@@ -72,6 +72,12 @@ SPEC_DEV void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: 
 SPEC_DEV void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 SPEC_DEV void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 SPEC_DEV void sm_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+// Warps 0-3 set up and go on; warps 4-11 wait for that when they first need it.
+SPEC_DEV void set_up() {
+  asm volatile("bar.sync 2, 128;" ::: "memory");
+  asm volatile("bar.arrive 3, 384;" ::: "memory");
+}
+SPEC_DEV void all_ready() { asm volatile("bar.sync 3, 384;" ::: "memory"); }
 
 // Operands in the 128-byte swizzle layout (bits 61-63 = 2, 46-48 = 0b001), groups
 // of 8 rows 1024 bytes apart; MN-major: halves of 64 elements `lbo` bytes apart.
@@ -88,23 +94,35 @@ constexpr uint32_t idesc(int M, int N, bool b_mn) {
   return (1u << 4) | (1u << 7) | (1u << 10) | (b_mn ? (1u << 16) : 0u) | ((uint32_t)(N >> 3) << 17) |
          ((uint32_t)(M >> 4) << 24);
 }
-SPEC_DEV void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+// The whole warp comes here with the same operands, which stay in uniform
+// registers that way; the lane with `go` issues (a product takes 35 cycles to issue
+// so, 55 where one thread alone runs the loop; a commit 4, else 50).
+SPEC_DEV void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc, uint32_t go) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(id), "r"(acc)
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"(acc), "r"(go)
       : "memory");
 }
 // A in tensor memory: a lane's 32-bit column holds two consecutive elements of its row.
-SPEC_DEV void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
+SPEC_DEV void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc, uint32_t go) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(id), "r"(acc)
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(id), "r"(acc), "r"(go)
       : "memory");
 }
-SPEC_DEV void commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(sa(bar)) : "memory");
+SPEC_DEV void commit(uint64_t* bar, uint32_t go) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(sa(bar)),
+      "r"(go)
+      : "memory");
+}
+SPEC_DEV uint32_t elect() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(e));
+  return e;
 }
 SPEC_DEV void tma_2d(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
   asm volatile(
@@ -174,18 +192,18 @@ SPEC_DEV bool mbar_try(uint64_t* b, unsigned parity) {
 }
 SPEC_DEV bool wait_phase(uint64_t* b, unsigned parity, volatile int* abort, int* err) {
   if (mbar_try(b, parity)) return true;
-  const unsigned long long t0 = globaltimer();
+  const long long t0 = clock64();
   do {
     if (mbar_try(b, parity)) return true;
     if (*abort) return false;
-  } while (globaltimer() - t0 < WAIT_NS);
+  } while (clock64() - t0 < WAIT_CYCLES);
   *abort = 1;
   set_error(err, SPEC_ERR_TIMEOUT);
   return false;
 }
 SPEC_DEV void drain_phase(uint64_t* b, unsigned parity) {
-  const unsigned long long t0 = globaltimer();
-  while (!mbar_try(b, parity) && globaltimer() - t0 < WAIT_NS) {
+  const long long t0 = clock64();
+  while (!mbar_try(b, parity) && clock64() - t0 < WAIT_CYCLES) {
   }
 }
 
@@ -306,94 +324,89 @@ struct Cta {
         drain_phase(&sm->full[i % sh.stages], parity(i));
   }
 
-  // ---- warp 1, one thread ----
+  // ---- warp 1 ----
   // A place in the ring, and the parity of its tile.
   struct Place {
     int s = 0;
     unsigned ph = 0;
   };
   SPEC_DEV Place next(Place c) const {
-    if (++c.s == sh.stages) {
-      c.s = 0;
-      c.ph ^= 1;
-    }
+    const bool wrap = c.s + 1 == sh.stages;
+    c.s = wrap ? 0 : c.s + 1;
+    c.ph ^= wrap;
     return c;
   }
-  // The loops stay rolled: what this thread executes for a product competes with
-  // eight softmax warps for the instruction caches (unrolled, a product took 160
-  // cycles to issue; the tensor cores need 64).
-  SPEC_DEV bool issue_s(int s, int t, Place k, bool last) {
+  SPEC_DEV bool issue_s(int s, int t, Place k, bool last, uint32_t go) {
     if (!wait(&sm->full[k.s], k.ph)) return false;
     fence_after();
     uint64_t q = desc_k(sa(qt) + (uint32_t)(t * QPL * TILE));
     const uint64_t kd = desc_k(sa(ring) + (uint32_t)(k.s * TILE));
     const uint32_t d = tmem + s * 128;
-    uint32_t acc = 0;
 #pragma unroll 1
-    for (int i = 0; i < QPL * NH; ++i) {
-      const uint64_t kk = kd + (uint64_t)(i % NH) * (HALF >> 4);
+    for (int pl = 0; pl < QPL; ++pl) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        mma_ss(d, q + 2 * j, kk + 2 * j, idesc(ROWS, BK, false), acc);
-        acc = 1;
+      for (int i = 0; i < HD / 16; ++i) {
+        const uint32_t off = (i >> 2) * (HALF >> 4) + 2 * (i & 3);
+        mma_ss(d, q + off, kd + off, idesc(ROWS, BK, false), i > 0 || pl > 0, go);
       }
-      q += HALF >> 4;
+      q += TILE >> 4;
     }
-    commit(&sm->sfull[s]);
-    if (last) commit(&sm->empty[k.s]);
+    commit(&sm->sfull[s], go);
+    commit(&sm->empty[k.s], go && last);
     return true;
   }
-  SPEC_DEV bool issue_pv(int s, Place v, unsigned round, bool first, bool last) {
-    if (!wait(&sm->pfull[s], round & 1) || !wait(&sm->full[v.s], v.ph)) return false;
+  SPEC_DEV bool issue_pv(int s, Place v, unsigned ph, bool first, bool last, uint32_t go) {
+    if (!wait(&sm->pfull[s], ph) || !wait(&sm->full[v.s], v.ph)) return false;
     fence_after();
-    uint64_t vd = desc_mn(sa(ring) + (uint32_t)(v.s * TILE), HALF);
-    uint32_t pb = tmem + s * 128;
-    const uint32_t ob = tmem + O_COL + s * HD;
-    uint32_t acc = !first;
-#pragma unroll 1
-    for (int c = 0; c < BK / 32; ++c) {  // 32 keys: four groups of 8 rows of V, 16 columns of P
+    const uint64_t vd = desc_mn(sa(ring) + (uint32_t)(v.s * TILE), HALF);
+    const uint32_t pb = tmem + s * 128, ob = tmem + O_COL + s * HD;
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        mma_ts(ob, pb + 8 * j, vd + j * (2048 >> 4), idesc(ROWS, HD, true), acc);
-        acc = 1;
-        if (F32) mma_ts(ob, pb + 16 + 8 * j, vd + j * (2048 >> 4), idesc(ROWS, HD, true), 1);  // (the weights' rest)
-      }
-      pb += F32 ? 32 : 16;
-      vd += 4096 >> 4;
+    for (int i = 0; i < BK / 16; ++i) {  // 16 keys: two groups of 8 rows of V, 8 columns of P
+      const uint32_t at = F32 ? pb + 32 * (i >> 1) + 8 * (i & 1) : pb + 8 * i;
+      mma_ts(ob, at, vd + i * (2048 >> 4), idesc(ROWS, HD, true), i > 0 || !first, go);
+      if (F32) mma_ts(ob, at + 16, vd + i * (2048 >> 4), idesc(ROWS, HD, true), 1, go);  // (the weights' rest)
     }
-    commit(&sm->odone[s]);
-    if (last) commit(&sm->empty[v.s]);
+    commit(&sm->odone[s], go);
+    commit(&sm->empty[v.s], go && last);
     return true;
   }
   SPEC_DEV void products() {
-    unsigned piece = 0, round[2] = {0, 0};
-    Place at;  // the next tile
+    const uint32_t go = elect();
+    unsigned piece = 0, round = 0;       // bit s of round: parity of stream s's next output
+    Place at, kt, vt;                    // the next tile, the ones in use
     bool ok = true;
     while (ok && w.pieces(a, p)) {
       const bool pair = w.n.w == 2;
-      const int N = w.N;
+      const int steps = pair ? 2 * w.N : w.N;
       ok = wait(&sm->qfull, piece & 1);
       fence_after();
       // the first scores of both streams, then in turn a stream's output and its next scores
-      for (int n = -2, s = 0; ok && n < (pair ? 2 * N : N); ++n, s ^= 1) {
+#pragma unroll 1
+      for (int n = -2, s = 0; ok && n < steps; ++n, s ^= 1) {
         // (two tiles: step n is block n / 2 of stream n & 1, and a tile of the ring serves two steps)
-        const bool shared = pair && s == 1;
+        const bool shared = pair && s == 1, last = !pair || shared;
         if (n >= 0) {
-          if (!shared) vt = at, at = next(at);
-          ok = issue_pv(s, vt, round[s]++, n < 2, !pair || shared);
+          if (!shared) {
+            vt = at;
+            at = next(at);
+          }
+          ok = issue_pv(s, vt, (round >> s) & 1, n < 2, last, go);
+          round ^= 1u << s;
         }
-        if (ok && n + 2 < (pair ? 2 * N : N)) {
-          if (!shared) kt = at, at = next(at);
-          ok = issue_s(s, pair ? s : 0, kt, !pair || shared);
+        if (ok && n + 2 < steps) {
+          if (!shared) {
+            kt = at;
+            at = next(at);
+          }
+          ok = issue_s(s, pair ? s : 0, kt, last, go);
         }
       }
       ++piece;
       w.step(a, p);
     }
-    commit(&sm->drain);  // every product done before tensor memory is freed
+    commit(&sm->drain, go);  // every product done before tensor memory is freed
     drain_phase(&sm->drain, 0);
   }
-  Place kt, vt;
 
   // ---- warps 4-11: thread = row of a tile ----
   SPEC_DEV void load_q(int row0, int nrow) {
@@ -555,8 +568,8 @@ struct Cta {
   SPEC_DEV void softmax() {
     const int t = threadIdx.x - 128, s = t >> 7, r = t & 127, lane = t & 31, G = a.nq / a.nkv;
     const uint32_t lanes = (uint32_t)(r & ~31) << 16;
-    const uint32_t sb = tmem + lanes + s * 128, ob = tmem + lanes + O_COL + s * HD;
-    unsigned t0 = 0, round[2] = {0, 0};
+    unsigned t0 = 0, round = 0, other = 0;  // this stream's blocks so far, the other's
+    bool begun = false;
     while (w.pieces(a, p)) {
       const bool pair = w.n.w == 2;
       const int N = w.N;
@@ -570,9 +583,16 @@ struct Cta {
       if (t == 0) sm->bad = 0;
       load_q(row0, nrow);
       fence_async();
+      if (!begun) {                      // the barriers are set up, and tensor memory is there
+        all_ready();
+        tmem = sm->tmem;
+        begun = true;
+      }
       fence_before();
-      mbar_arrive(&sm->qfull);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm->qfull);
       sm_sync();
+      const uint32_t sb = tmem + lanes + s * 128, ob = tmem + lanes + O_COL + s * HD;
       const int mine = pair ? s * ROWS + r : r;                       // row of the unit
       const bool work = (mine & ~31) < nrow;                          // this warp holds a row
       const int gr = row0 + mine, qi = mine < nrow ? gr / G : 0, g = gr - gr / G * G;
@@ -581,7 +601,7 @@ struct Cta {
       float m = -INFINITY, l = 0.f;
       const int n0 = pair ? 0 : s, dn = pair ? 1 : 2;
       for (int n = n0; n < N; n += dn) {
-        wait(&sm->sfull[s], round[s] & 1);
+        wait(&sm->sfull[s], round & 1);
         fence_after();
         const int key0 = (w.k0 + n) * BK;
         const bool edge = key0 + BK > w.s.len;                        // rows of the tree, or the end, in this block
@@ -599,7 +619,7 @@ struct Cta {
             if (raise) m = mx;
             l *= f;
             if (n != n0) {
-              wait(&sm->odone[s], (round[s] & 1) ^ 1);
+              wait(&sm->odone[s], (round & 1) ^ 1);
               fence_after();
 #pragma unroll 1
               for (int c = 0; c < HD / 32; ++c) {
@@ -623,16 +643,16 @@ struct Cta {
           fence_async();
         }
         fence_before();
-        mbar_arrive(&sm->pfull[s]);
-        ++round[s];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm->pfull[s]);
+        ++round;
       }
       // (the other stream's rounds are known too: both streams' O are read below)
-      const int left = pair ? N : s == 0 ? N / 2 : (N + 1) / 2;
-      round[s ^ 1] += left;
+      other += pair ? N : s == 0 ? N / 2 : (N + 1) / 2;
       sm->ml[s][r] = make_float2(m, l);
       const bool both = pair || N > 1;
-      wait(&sm->odone[s], (round[s] & 1) ^ 1);
-      if (!pair && both) wait(&sm->odone[s ^ 1], (round[s ^ 1] & 1) ^ 1);
+      wait(&sm->odone[s], (round & 1) ^ 1);
+      if (!pair && both) wait(&sm->odone[s ^ 1], (other & 1) ^ 1);
       sm_sync();
       fence_after();
       if (work) {
@@ -738,10 +758,7 @@ __global__ void __launch_bounds__(NTHR, 1)
   k.qt = smem + SMALL;
   k.ring = k.qt + sh.q_bytes;
   grid_dep_launch();
-  int* pre = reinterpret_cast<int*>(k.ring);                // (before the first tile arrives there)
-  if (warp == 0) {
-    prefix(a, p, pre);
-  } else if (warp == 1) {
+  if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(sa(&sm->tmem)) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   } else if (threadIdx.x == 64) {
@@ -751,29 +768,30 @@ __global__ void __launch_bounds__(NTHR, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm->sfull[i], 1);
-      mbar_init(&sm->pfull[i], 128);
+      mbar_init(&sm->pfull[i], 4);
       mbar_init(&sm->odone[i], 1);
     }
-    mbar_init(&sm->qfull, NSM);
+    mbar_init(&sm->qfull, NSM / 32);
     mbar_init(&sm->drain, 1);
     sm->abort = 0;
     mbar_init_fence();
     asm volatile("prefetch.tensormap [%0];" ::"l"(&tm) : "memory");
   }
-  fence_before();
-  __syncthreads();
-  fence_after();
-  k.tmem = sm->tmem;
-  const Cut cut(p, pre[a.B]);
+  const Axis axis(a, p);                                    // (every warp for itself)
+  const Cut cut(p, axis.total);
   const bool work = (int)blockIdx.x < cut.ctas && cut.total > 0;
   if (work) {
     k.w.x = cut.start(blockIdx.x);
     k.w.x1 = cut.start(blockIdx.x + 1);
-    k.w.n = unit_at(a, p, pre, k.w.x);
+    k.w.n = unit_at(a, p, axis, k.w.x);
     k.w.s = seq_of(a, k.w.n.b);
+    if (warp < 4) {
+      fence_before();
+      set_up();
+      fence_after();
+      k.tmem = sm->tmem;
+    }
   }
-  fence_async();                                            // (the prefix is read and gone, before copies land on it)
-  __syncthreads();
   if (blockIdx.x == 0 && warp == 2) {
     const bool bad = __any_sync(FULL, bad_input(a, lane, 32));
     if (lane == 0) *a.err = bad ? SPEC_ERR_CAPACITY : 0;
@@ -781,7 +799,7 @@ __global__ void __launch_bounds__(NTHR, 1)
     k.producer();
     __syncwarp();
   } else if (work && warp == 1) {
-    if (lane == 0) k.products();
+    k.products();
     __syncwarp();
   } else if (work && warp >= 4) {
     k.softmax();
@@ -790,7 +808,7 @@ __global__ void __launch_bounds__(NTHR, 1)
   __syncthreads();
   if (warp == 1) {
     fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(k.tmem) : "memory");
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(sm->tmem) : "memory");
   }
 }
 
