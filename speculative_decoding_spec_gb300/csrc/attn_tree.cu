@@ -51,7 +51,7 @@ __global__ void __launch_bounds__(NTHR) tree_cc_kernel(const __grid_constant__ T
   __shared__ unsigned long long path[64];
   __shared__ int up[64];
   grid_dep_launch();
-  const int t = threadIdx.x, tx = t & 15, ty = t >> 4, hd = a.hd, G = a.nq / a.nkv;
+  const int t = threadIdx.x, tx = t & 15, ty = t >> 4, hd = a.hd, G = p.G;
   float* qs = sm;                 // [hd][ROWS]
   float* ks = qs + hd * ROWS;     // [hd][KLD]
   float* vs = ks + hd * KLD;      // [PAGE][hd]
@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(NTHR) tree_cc_kernel(const __grid_constant__ T
       const int r = i / (hd / 4), c = (i % (hd / 4)) * 4;
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
       if (r < nrow) {
-        const int qr = (row0 + r) / G, g = (row0 + r) % G;
+        const int qr = p.row_of(row0 + r), g = row0 + r - qr * G;
         v = load4((const QT*)a.q + ((size_t)n.b * a.R + qr) * a.ldq + (size_t)(n.kvh * G + g) * hd + c);
       }
       qs[(c + 0) * ROWS + r] = v.x * scale2;
@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(NTHR) tree_cc_kernel(const __grid_constant__ T
       for (int i = 0; i < TR; ++i) {
         const int r = ty * TR + i;
         const unsigned long long vis =
-            r < nrow ? (all ? ~0ull : visible(path[(row0 + r) / G], s.len, k * PAGE)) : 0ull;
+            r < nrow ? (all ? ~0ull : visible(path[p.row_of(row0 + r)], s.len, k * PAGE)) : 0ull;
         float mx = -INFINITY;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(NTHR) tree_cc_kernel(const __grid_constant__ T
 #pragma unroll
         for (int i = 0; i < TR; ++i) {
           const int r = ty * TR + i;
-          vis[i] = some && r < nrow ? visible(path[(row0 + r) / G], s.len, k * PAGE) : ~0ull;
+          vis[i] = some && r < nrow ? visible(path[p.row_of(row0 + r)], s.len, k * PAGE) : ~0ull;
         }
 #pragma unroll 2
         for (int key = 0; key < valid; ++key) {
@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(NTHR) tree_cc_kernel(const __grid_constant__ T
     for (int i = 0; i < TR; ++i) {
       const int r = ty * TR + i;
       if (r >= nrow) continue;
-      const int qr = (row0 + r) / G, g = (row0 + r) % G;
+      const int qr = p.row_of(row0 + r), g = row0 + r - qr * G;
       const float inv = whole ? 1.f / l[i] : 1.f;
       if (!whole && tx == 0) a.part_ml[slot + r] = make_float2(m[i], l[i]);
 #pragma unroll
@@ -245,23 +245,25 @@ SPEC_DEV void starts(const TreeArgs& a, const Plan& p, int* pre) {
 
 // A warp per query row: rows of units that one CTA finished are left alone. The
 // pieces' rows are read eight at a time; LN lanes hold a row, 32 / LN pieces go
-// side by side.
-template <typename QT, int LN, int NJ>
+// side by side. ALL: the CTA's eight warps share a row's pieces.
+template <typename QT, int LN, int NJ, bool ALL>
 __global__ void __launch_bounds__(NTHR) tree_join_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Plan p) {
   __shared__ int pre[TREE_B_MAX + 1];
-  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, G = a.nq / a.nkv, hd = a.hd;
+  __shared__ float2 wml[8];
+  __shared__ float4 wacc[ALL ? 8 : 1][32][NJ];
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, G = p.G, hd = a.hd;
   constexpr int SIDE = 32 / LN;
   if (w == 0) starts(a, p, pre);  // (the call's inputs are not written by the kernel before this one)
   __syncthreads();
   const Cut cut(p, pre[a.B]);
   grid_dep_wait();
   if (cut.ctas == 1) return;
-  const int urows = p.tile * p.tpu, sub = lane / LN, ln = lane % LN;
-  for (int row = blockIdx.x * (NTHR / 32) + w; row < a.B * a.R * a.nq; row += gridDim.x * (NTHR / 32)) {
+  const int urows = p.tpu << p.tile, sub = lane / LN, ln = lane % LN;
+  for (int row = ALL ? blockIdx.x : blockIdx.x * 8 + w; row < a.B * a.R * a.nq; row += gridDim.x * (ALL ? 1 : 8)) {
     const int m = row / a.nq, h = row - m * a.nq, b = m / a.R, r = m - b * a.R;
     const Seq s = seq_of(a, b);
     if (r >= s.rows) continue;
-    const int kvh = h / G, q = r * G + h - kvh * G, T = tiles_of(p, G, s.rows), nb = blocks_of(p, s);
+    const int kvh = h / G, q = r * G + h - kvh * G, T = tiles_of(p, s.rows), nb = blocks_of(p, s);
     Unit n;
     n.b = b;
     n.kvh = kvh;
@@ -277,9 +279,9 @@ __global__ void __launch_bounds__(NTHR) tree_join_kernel(const __grid_constant__
 #pragma unroll
     for (int j = 0; j < NJ; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
     bool cutup = false;
-    for (int c = c0; c <= c1; c += 32) {
-      // lane i: the piece of CTA c + i, its maximum and sum
-      const int mine = c + lane;
+    for (int c = c0 + (ALL ? w : 0); c <= c1; c += ALL ? 256 : 32) {
+      // lane i: the piece of CTA c + i (c + 8 i), its maximum and sum
+      const int mine = c + lane * (ALL ? 8 : 1);
       int slot = -1;
       float2 ml = make_float2(-INFINITY, 0.f);
       if (mine <= c1) {
@@ -300,7 +302,7 @@ __global__ void __launch_bounds__(NTHR) tree_join_kernel(const __grid_constant__
       for (int j = 0; j < NJ; ++j) {
         acc[j].x *= old; acc[j].y *= old; acc[j].z *= old; acc[j].w *= old;
       }
-      const int last = min(32, c1 - c + 1);
+      const int last = min(32, (ALL ? (c1 - c) >> 3 : c1 - c) + 1);
       for (int i0 = 0; i0 < last; i0 += 8 * SIDE) {
         float4 v[8][NJ];
         float fi[8];
@@ -329,10 +331,9 @@ __global__ void __launch_bounds__(NTHR) tree_join_kernel(const __grid_constant__
           }
       }
     }
-    if (!cutup) continue;  // one CTA had all of its blocks
-    const float inv = 1.f / L;
+    if (ALL ? !__syncthreads_or(cutup) : !cutup) continue;  // one CTA had all of its blocks
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) {
+    for (int j = 0; j < NJ; ++j)
 #pragma unroll
       for (int o = LN; o < 32; o <<= 1) {
         acc[j].x += __shfl_xor_sync(FULL, acc[j].x, o);
@@ -340,18 +341,47 @@ __global__ void __launch_bounds__(NTHR) tree_join_kernel(const __grid_constant__
         acc[j].z += __shfl_xor_sync(FULL, acc[j].z, o);
         acc[j].w += __shfl_xor_sync(FULL, acc[j].w, o);
       }
-      const int d = 4 * ln + 4 * LN * j;
-      if (sub == 0 && d < hd)
-        store4((QT*)a.out + (size_t)m * a.ldo + (size_t)h * hd + d,
-               make_float4(acc[j].x * inv, acc[j].y * inv, acc[j].z * inv, acc[j].w * inv));
+    if (ALL) {
+      if (lane == 0) wml[w] = make_float2(M, L);
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) wacc[w][lane][j] = acc[j];
+      __syncthreads();
+      if (w == 0) {
+        for (int i = 0; i < 8; ++i) M = fmaxf(M, wml[i].x);
+        L = 0.f;
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i = 0; i < 8; ++i) {
+          const float f = wml[i].x == -INFINITY ? 0.f : ex2(wml[i].x - M);
+          L = fmaf(f, wml[i].y, L);
+#pragma unroll
+          for (int j = 0; j < NJ; ++j) {
+            const float4 v = wacc[i][lane][j];
+            acc[j].x = fmaf(f, v.x, acc[j].x);
+            acc[j].y = fmaf(f, v.y, acc[j].y);
+            acc[j].z = fmaf(f, v.z, acc[j].z);
+            acc[j].w = fmaf(f, v.w, acc[j].w);
+          }
+        }
+      }
     }
+    const float inv = 1.f / L;
+    if (!ALL || w == 0)
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        const int d = 4 * ln + 4 * LN * j;
+        if (sub == 0 && d < hd)
+          store4((QT*)a.out + (size_t)m * a.ldo + (size_t)h * hd + d,
+                 make_float4(acc[j].x * inv, acc[j].y * inv, acc[j].z * inv, acc[j].w * inv));
+      }
+    if (ALL) __syncthreads();
   }
 }
 
-template <typename QT>
+template <typename QT, bool ALL>
 const void* join_kernel(int hd) {
-  return hd <= 64 ? (const void*)tree_join_kernel<QT, 16, 1>
-                  : hd <= 128 ? (const void*)tree_join_kernel<QT, 32, 1> : (const void*)tree_join_kernel<QT, 32, 2>;
+  return hd <= 64 ? (const void*)tree_join_kernel<QT, 16, 1, ALL>
+                  : hd <= 128 ? (const void*)tree_join_kernel<QT, 32, 1, ALL> : (const void*)tree_join_kernel<QT, 32, 2, ALL>;
 }
 
 template <typename QT, typename KT, int TR>
@@ -373,19 +403,20 @@ int cc_rows(const TreeArgs& a) { return a.R * (a.nq / a.nkv) <= 16 ? 1 : 4; }
 Plan cc_plan(const TreeArgs& a) {
   Plan p;
   const int TR = cc_rows(a);
-  p.blk = PAGE;
-  p.tile = 16 * TR;
+  p.blk = 6;
+  p.tile = TR == 1 ? 4 : 6;
   p.tpu = 1;
   const int per_sm = std::max(1, std::min(4, (int)(220 * 1024 / cc_smem(a.hd, TR))));
   p.grid = num_sms() * per_sm;
   p.min_cost = 2;
+  plan_heads(p, a);
   return p;
 }
 
 // The longest axis a call of this shape can have.
 long long axis_of(const TreeArgs& a, const Plan& p) {
-  const long long T = (a.R * (a.nq / a.nkv) + p.tile - 1) / p.tile;
-  return (long long)a.B * a.nkv * T * (((long long)a.max_pages * PAGE + p.blk - 1) / p.blk);
+  const long long T = (a.R * p.G + (1 << p.tile) - 1) >> p.tile;
+  return (long long)a.B * a.nkv * T * (((long long)a.max_pages * PAGE + (1 << p.blk) - 1) >> p.blk);
 }
 
 Plan plan_of(const TreeArgs& a) {
@@ -407,7 +438,7 @@ static TreeArgs shape_args(int B, int R, int nq, int nkv, int hd, int max_pages,
   a.q_dtype = q_dtype; a.kv_dtype = kv_dtype;
   return a;
 }
-static size_t part_rows(const Plan& p) { return (size_t)2 * p.grid * p.tile * p.tpu; }
+static size_t part_rows(const Plan& p) { return (size_t)2 * p.grid * p.tpu << p.tile; }
 
 // error word (256 bytes), maxima and sums, rows; 0 where a kernel's axis (whose
 // numbers have 32 bits, slots of rows among them) may not hold the call
@@ -452,7 +483,9 @@ int attn_tree(TreeArgs a, void* ws, cudaStream_t st) {
   if (p.grid == 1) return r;  // nothing is cut
   cudaLaunchConfig_t cfg = {};
   const long long rows = (long long)a.B * a.R * a.nq;
-  cfg.gridDim = dim3((unsigned)std::min<long long>((rows + NTHR / 32 - 1) / (NTHR / 32), 8ll * num_sms()));
+  // few rows are cut into many pieces: a CTA a row then (84 rows of 38 pieces: XX us, a warp a row YY)
+  const bool all = rows <= 4 * num_sms();
+  cfg.gridDim = dim3((unsigned)std::min<long long>(all ? rows : (rows + 7) / 8, 8ll * num_sms()));
   cfg.blockDim = dim3(NTHR);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -461,7 +494,8 @@ int attn_tree(TreeArgs a, void* ws, cudaStream_t st) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   void* args[] = {(void*)&a, (void*)&p};
-  const void* f = a.q_dtype == DT_F32 ? join_kernel<float>(a.hd) : join_kernel<__nv_bfloat16>(a.hd);
+  const void* f = a.q_dtype == DT_F32 ? (all ? join_kernel<float, true>(a.hd) : join_kernel<float, false>(a.hd))
+                                      : (all ? join_kernel<__nv_bfloat16, true>(a.hd) : join_kernel<__nv_bfloat16, false>(a.hd));
   return cudaLaunchKernelExC(&cfg, f, args) == cudaSuccess ? r + 1 : -1;
 }
 

@@ -23,9 +23,17 @@ constexpr int PAGE = 64;
 constexpr float LOG2E = 1.4426950408889634f;
 
 struct Plan {
-  int blk, tile, tpu, grid;  // keys a block, rows a tile, tiles a unit, CTAs
+  int blk, tile;             // keys a block, rows a tile: powers of two, as shifts
+  int tpu, grid;             // tiles a unit (1 or 2), CTAs
   int min_cost;              // a part is not made shorter than this
+  int G;                     // query heads a KV head
+  uint32_t inv_g;            // ceil(2^32 / G): rows below 2^16 are divided by G with a product
+  SPEC_DEV int row_of(int q) const { return G == 1 ? q : (int)__umulhi((uint32_t)q, inv_g); }
 };
+inline void plan_heads(Plan& p, const TreeArgs& a) {
+  p.G = a.nq / a.nkv;
+  p.inv_g = (uint32_t)(((1ull << 32) + p.G - 1) / p.G);
+}
 
 // Sequence b of a call: slot, committed length, rows in use. A sequence whose
 // numbers are out of range has no rows: its outputs stay as they are.
@@ -43,12 +51,12 @@ SPEC_DEV Seq seq_of(const TreeArgs& a, int b) {
   if (!s.ok) s.rows = 0;
   return s;
 }
-SPEC_DEV int tiles_of(const Plan& p, int G, int rows) { return (rows * G + p.tile - 1) / p.tile; }
-SPEC_DEV int blocks_of(const Plan& p, const Seq& s) { return s.rows ? (s.len + s.rows + p.blk - 1) / p.blk : 0; }
+SPEC_DEV int tiles_of(const Plan& p, int rows) { return (rows * p.G + (1 << p.tile) - 1) >> p.tile; }
+SPEC_DEV int blocks_of(const Plan& p, const Seq& s) { return s.rows ? (s.len + s.rows + (1 << p.blk) - 1) >> p.blk : 0; }
 
 SPEC_DEV int cost_of(const TreeArgs& a, const Plan& p, int b) {
   const Seq s = seq_of(a, b);
-  return a.nkv * blocks_of(p, s) * tiles_of(p, a.nq / a.nkv, s.rows);  // (the launcher keeps the axis below 2^31)
+  return a.nkv * blocks_of(p, s) * tiles_of(p, s.rows);  // (the launcher keeps the axis below 2^31)
 }
 // This lane's sequence of 32: where it ends, from the start of the first.
 SPEC_DEV int scan32(int c) {
@@ -96,8 +104,7 @@ struct Axis {
 struct Cut {
   int total, ctas, base, more;
   SPEC_DEV Cut(const Plan& p, int n) : total(n) {
-    const int most = n / p.min_cost + (n % p.min_cost != 0);
-    ctas = max(1, min(most, p.grid));
+    ctas = max(1, min((n + p.min_cost - 1) / p.min_cost, p.grid));
     base = n / ctas;
     more = n - base * ctas;
   }
@@ -120,7 +127,7 @@ SPEC_DEV Unit unit_at(const TreeArgs& a, const Plan& p, const Axis& axis, int x)
   int start;
   n.b = axis.at(a, p, x, start);
   const Seq s = seq_of(a, n.b);
-  const int T = tiles_of(p, a.nq / a.nkv, s.rows);
+  const int T = tiles_of(p, s.rows);
   n.nb = blocks_of(p, s);
   const int pair = n.nb * T, off = x - start;
   n.kvh = off / pair;
@@ -132,7 +139,7 @@ SPEC_DEV Unit unit_at(const TreeArgs& a, const Plan& p, const Axis& axis, int x)
 // The blocks of unit n in [x0, x1) of the axis.
 SPEC_DEV int first_block(const Unit& n, int x) {
   const int off = x - n.start;
-  return off <= 0 ? 0 : min(n.w == 1 ? off : (off + n.w - 1) / n.w, n.nb);
+  return off <= 0 ? 0 : min((off + n.w - 1) >> (n.w - 1), n.nb);
 }
 
 // Bit j of path[r]: row j is row r or an ancestor of it (rows below 64). By

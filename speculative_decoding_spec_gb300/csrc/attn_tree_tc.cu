@@ -226,8 +226,7 @@ struct Walk {
     x = n.start + n.nb * n.w;
     n.start = x;
     if (x >= x1) return;
-    const int G = a.nq / a.nkv;
-    int T = tiles_of(p, G, s.rows);
+    int T = tiles_of(p, s.rows);
     if ((n.u + 1) * p.tpu < T) {
       ++n.u;
     } else {
@@ -236,7 +235,7 @@ struct Walk {
         n.kvh = 0;
         do s = seq_of(a, ++n.b);        // (x < x1 <= the axis's end: there is one)
         while (s.rows == 0);
-        T = tiles_of(p, G, s.rows);
+        T = tiles_of(p, s.rows);
         n.nb = blocks_of(p, s);
       }
     }
@@ -410,13 +409,14 @@ struct Cta {
 
   // ---- warps 4-11: thread = row of a tile ----
   SPEC_DEV void load_q(int row0, int nrow) {
-    const int t = threadIdx.x - 128, G = a.nq / a.nkv, c = t % (HD / 8);
-    constexpr int STEP = NSM / (HD / 8), U = F32 ? 4 : 8;  // rows a round, rounds in flight
-    for (int r0 = t / (HD / 8); r0 < w.n.w * ROWS; r0 += U * STEP) {
+    const int t = threadIdx.x - 128, G = p.G, c = t % (HD / 8);
+    constexpr int STEP = NSM / (HD / 8), U = F32 ? 2 : 4;  // rows a round, rounds in flight
+    #pragma unroll 1
+    for (int r0 = t / (HD / 8); r0 < nrow; r0 += U * STEP) {  // (other rows stay what they are: a row's results are its own)
       uint4 v[U][F32 ? 2 : 1];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int r = r0 + u * STEP, gr = row0 + r, qi = gr / G, g = gr - qi * G;
+        const int r = r0 + u * STEP, gr = row0 + r, qi = p.row_of(gr), g = gr - qi * G;
         const size_t at = ((size_t)w.n.b * a.R + qi) * a.ldq + (size_t)(w.n.kvh * G + g) * HD + 8 * c;
 #pragma unroll
         for (int e = 0; e < (F32 ? 2 : 1); ++e)
@@ -426,6 +426,7 @@ struct Cta {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int r = r0 + u * STEP;
+        if (r >= nrow) break;
         unsigned char* dst = qt + (size_t)(r / ROWS) * QPL * TILE + (c >> 3) * HALF + swz(r % ROWS, (c & 7) * 16);
         if (!F32) {
           *reinterpret_cast<uint4*>(dst) = v[u][0];
@@ -492,24 +493,37 @@ struct Cta {
     return ex2(fmaf(s, sh.scale2, -M));
   }
 
-  // A block's scores of this thread's row, 64 at a time: the largest one seen.
-  template <bool EDGE>
-  SPEC_DEV float row_max(uint32_t sb, const unsigned long long (&vis)[2]) const {
+  // The loops over a block's 128 scores of this thread's row take 32 a turn and
+  // stay rolled: an instruction that runs once costs 20 to 40 cycles, as the caches
+  // are cold at a launch.
+  // Scores that the row does not see: -inf.
+  SPEC_DEV void hide(uint32_t sb, unsigned long long lo, unsigned long long hi) const {
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+      const uint32_t b = (uint32_t)((c < 2 ? lo : hi) >> (32 * (c & 1)));
+      if (__all_sync(FULL, b == ~0u)) continue;
+      float v[32];
+      ld32(sb + 32 * c, v);
+      wait_ld();
+      uint32_t u[32];
+#pragma unroll
+      for (int e = 0; e < 32; ++e) u[e] = (b >> e) & 1 ? __float_as_uint(v[e]) : 0xff800000u;
+      st16(sb + 32 * c, u);
+      st16(sb + 32 * c + 16, u + 16);
+    }
+    wait_st();
+  }
+  // The largest.
+  SPEC_DEV float row_max(uint32_t sb) const {
     float mx = -INFINITY;
 #pragma unroll 1
-    for (int h = 0; h < 2; ++h) {
-      float v[64];
-      ld32(sb + 64 * h, v);
-      ld32(sb + 64 * h + 32, v + 32);
+    for (int c = 0; c < 4; ++c) {
+      float v[32];
+      ld32(sb + 32 * c, v);
       wait_ld();
-      if (EDGE) {
-        const unsigned long long b = h ? vis[1] : vis[0];
-#pragma unroll
-        for (int e = 0; e < 64; ++e) v[e] = (b >> e) & 1 ? v[e] : -INFINITY;
-      }
       float m0 = v[0], m1 = v[1], m2 = v[2], m3 = v[3];
 #pragma unroll
-      for (int e = 4; e < 64; e += 4) {
+      for (int e = 4; e < 32; e += 4) {
         m0 = fmaxf(m0, v[e]);
         m1 = fmaxf(m1, v[e + 1]);
         m2 = fmaxf(m2, v[e + 2]);
@@ -521,52 +535,41 @@ struct Cta {
   }
   // Their weights over them, and the weights' sum. A bf16 row's sum is that of the
   // rounded weights: a rounding then moves a value's share, not the row's scale.
-  template <bool EDGE>
-  SPEC_DEV float weights(uint32_t sb, const unsigned long long (&vis)[2], float m) const {
+  SPEC_DEV float weights(uint32_t sb, float m) const {
     const float2 sc = make_float2(sh.scale2, sh.scale2), mm = make_float2(-m, -m);
     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll 1
-    for (int h = 0; h < 2; ++h) {
-      float v[64];
-      ld32(sb + 64 * h, v);
-      ld32(sb + 64 * h + 32, v + 32);
+    for (int c = 0; c < 4; ++c) {
+      float v[32];
+      ld32(sb + 32 * c, v);
       wait_ld();
-      const unsigned long long b = h ? vis[1] : vis[0];
+      uint32_t hi[16], lo[16];
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint32_t hi[16], lo[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int k = 32 * c + 2 * e;
-          float2 x = fma2(make_float2(v[k], v[k + 1]), sc, mm);
-          x.x = ex2(x.x);
-          x.y = ex2(x.y);
-          if (EDGE) {
-            x.x = (b >> k) & 1 ? x.x : 0.f;
-            x.y = (b >> (k + 1)) & 1 ? x.y : 0.f;
-          }
-          hi[e] = pack2(x.x, x.y);
-          const float2 r = make_float2(bf16lo(hi[e]), bf16hi(hi[e]));
-          if (F32) {
-            sum[e & 1] = add2(sum[e & 1], x);
-            lo[e] = pack2(x.x - r.x, x.y - r.y);
-          } else {
-            sum[e & 1] = add2(sum[e & 1], r);
-          }
-        }
+      for (int e = 0; e < 16; ++e) {
+        float2 x = fma2(make_float2(v[2 * e], v[2 * e + 1]), sc, mm);
+        x.x = ex2(x.x);
+        x.y = ex2(x.y);
+        hi[e] = pack2(x.x, x.y);
+        const float2 r = make_float2(bf16lo(hi[e]), bf16hi(hi[e]));
         if (F32) {
-          st16(sb + 64 * h + 32 * c, hi);
-          st16(sb + 64 * h + 32 * c + 16, lo);
+          sum[e & 1] = add2(sum[e & 1], x);
+          lo[e] = pack2(x.x - r.x, x.y - r.y);
         } else {
-          st16(sb + 32 * h + 16 * c, hi);
+          sum[e & 1] = add2(sum[e & 1], r);
         }
+      }
+      if (F32) {
+        st16(sb + 32 * c, hi);
+        st16(sb + 32 * c + 16, lo);
+      } else {
+        st16(sb + 16 * c, hi);
       }
     }
     return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
   }
 
   SPEC_DEV void softmax() {
-    const int t = threadIdx.x - 128, s = t >> 7, r = t & 127, lane = t & 31, G = a.nq / a.nkv;
+    const int t = threadIdx.x - 128, s = t >> 7, r = t & 127, lane = t & 31, G = p.G;
     const uint32_t lanes = (uint32_t)(r & ~31) << 16;
     unsigned t0 = 0, round = 0, other = 0;  // this stream's blocks so far, the other's
     bool begun = false;
@@ -595,7 +598,7 @@ struct Cta {
       const uint32_t sb = tmem + lanes + s * 128, ob = tmem + lanes + O_COL + s * HD;
       const int mine = pair ? s * ROWS + r : r;                       // row of the unit
       const bool work = (mine & ~31) < nrow;                          // this warp holds a row
-      const int gr = row0 + mine, qi = mine < nrow ? gr / G : 0, g = gr - gr / G * G;
+      const int gr = row0 + mine, qi = mine < nrow ? p.row_of(gr) : 0, g = gr - qi * G;
       unsigned long long path = 0;
       for (int q = qi; q >= 0; q = sm->up[q]) path |= 1ull << q;
       float m = -INFINITY, l = 0.f;
@@ -606,12 +609,8 @@ struct Cta {
         const int key0 = (w.k0 + n) * BK;
         const bool edge = key0 + BK > w.s.len;                        // rows of the tree, or the end, in this block
         if (work) {
-          unsigned long long vis[2] = {~0ull, ~0ull};
-          if (edge) {
-            vis[0] = visible(path, w.s.len, key0);
-            vis[1] = visible(path, w.s.len, key0 + 64);
-          }
-          float mx = edge ? row_max<true>(sb, vis) : row_max<false>(sb, vis);
+          if (edge) hide(sb, visible(path, w.s.len, key0), visible(path, w.s.len, key0 + 64));
+          float mx = row_max(sb);
           mx *= sh.scale2;
           const bool raise = mx > m + TAU || (m == -INFINITY && mx > -INFINITY);
           if (__any_sync(FULL, raise)) {
@@ -635,7 +634,7 @@ struct Cta {
             }
           }
           const float mb = m == -INFINITY ? 0.f : m;
-          l += edge ? weights<true>(sb, vis, mb) : weights<false>(sb, vis, mb);
+          l += weights(sb, mb);
           wait_st();
         }
         if (edge && (!pair || s == 0)) {
@@ -670,7 +669,7 @@ struct Cta {
         const int c0 = pair ? 0 : s * (HD / 64), c1 = pair ? HD / 32 : c0 + HD / 64;
         const size_t qat = ((size_t)w.n.b * a.R + qi) * a.ldq + (size_t)(w.n.kvh * G + g) * HD;
         const size_t oat = ((size_t)w.n.b * a.R + qi) * a.ldo + (size_t)(w.n.kvh * G + g) * HD;
-        const size_t slot = (size_t)(2 * blockIdx.x + (w.k0 == 0)) * (p.tile * p.tpu) + mine;
+        const size_t slot = (size_t)(2 * blockIdx.x + (w.k0 == 0)) * (p.tpu << p.tile) + mine;
         float4* stg = reinterpret_cast<float4*>(qt) + (t >> 5) * 256;
 #pragma unroll 1
         for (int c = c0; c < c1; ++c) {
@@ -846,8 +845,9 @@ bool tc_ok(const TreeArgs& a) {
 
 Plan tc_plan(const TreeArgs& a) {
   Plan p;
-  p.blk = BK;
-  p.tile = ROWS;
+  p.blk = 7;
+  p.tile = 7;
+  plan_heads(p, a);
   // two tiles share a block's reads; three planes of each do not fit beside a ring
   p.tpu = a.q_dtype == DT_BF16 && a.R * (a.nq / a.nkv) > ROWS ? 2 : 1;
   p.grid = num_sms();
