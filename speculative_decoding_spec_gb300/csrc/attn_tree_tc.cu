@@ -335,9 +335,7 @@ struct Cta {
     c.ph ^= wrap;
     return c;
   }
-  SPEC_DEV bool issue_s(int s, int t, Place k, bool last, uint32_t go) {
-    if (!wait(&sm->full[k.s], k.ph)) return false;
-    fence_after();
+  SPEC_DEV void issue_s(int s, int t, Place k, bool last, uint32_t go) {
     uint64_t q = desc_k(sa(qt) + (uint32_t)(t * QPL * TILE));
     const uint64_t kd = desc_k(sa(ring) + (uint32_t)(k.s * TILE));
     const uint32_t d = tmem + s * 128;
@@ -352,11 +350,8 @@ struct Cta {
     }
     commit(&sm->sfull[s], go);
     commit(&sm->empty[k.s], go && last);
-    return true;
   }
-  SPEC_DEV bool issue_pv(int s, Place v, unsigned ph, bool first, bool last, uint32_t go) {
-    if (!wait(&sm->pfull[s], ph) || !wait(&sm->full[v.s], v.ph)) return false;
-    fence_after();
+  SPEC_DEV void issue_pv(int s, Place v, bool first, bool last, uint32_t go) {
     const uint64_t vd = desc_mn(sa(ring) + (uint32_t)(v.s * TILE), HALF);
     const uint32_t pb = tmem + s * 128, ob = tmem + O_COL + s * HD;
 #pragma unroll
@@ -367,7 +362,6 @@ struct Cta {
     }
     commit(&sm->odone[s], go);
     commit(&sm->empty[v.s], go && last);
-    return true;
   }
   SPEC_DEV void products() {
     const uint32_t go = elect();
@@ -384,21 +378,26 @@ struct Cta {
       for (int n = -2, s = 0; ok && n < steps; ++n, s ^= 1) {
         // (two tiles: step n is block n / 2 of stream n & 1, and a tile of the ring serves two steps)
         const bool shared = pair && s == 1, last = !pair || shared;
-        if (n >= 0) {
-          if (!shared) {
-            vt = at;
-            at = next(at);
-          }
-          ok = issue_pv(s, vt, (round >> s) & 1, n < 2, last, go);
+        // (the tiles' arrivals first: with the weights there, 16 products go out without a wait)
+        const bool v = n >= 0, k = n + 2 < steps;
+        if (v && !shared) {
+          vt = at;
+          at = next(at);
+          ok = wait(&sm->full[vt.s], vt.ph);
+        }
+        if (k && !shared) {
+          kt = at;
+          at = next(at);
+          ok = ok && wait(&sm->full[kt.s], kt.ph);
+        }
+        if (v) {
+          ok = ok && wait(&sm->pfull[s], (round >> s) & 1);
           round ^= 1u << s;
         }
-        if (ok && n + 2 < steps) {
-          if (!shared) {
-            kt = at;
-            at = next(at);
-          }
-          ok = issue_s(s, pair ? s : 0, kt, last, go);
-        }
+        if (!ok) break;
+        fence_after();
+        if (v) issue_pv(s, vt, n < 2, last, go);
+        if (k) issue_s(s, pair ? s : 0, kt, last, go);
       }
       ++piece;
       w.step(a, p);

@@ -459,7 +459,8 @@ struct AdjustArgs {
   int n_masks;
   const int32_t* mask_ids;               // [B*R] or null
   int* status;
-  int chunk;                             // tokens of a CTA (set by the launcher)
+  // set by the launcher: tokens and rows of a CTA; slots of a hash table, CTAs a sequence
+  int chunk, rows, slots, parts;
 };
 void setup_adjust_attributes();
 int adjust_logits(AdjustArgs a, cudaStream_t st);

@@ -103,20 +103,25 @@ SPEC_DEV bool ids_bad(const PagesArgs& a) {
   return __syncthreads_or(bad);
 }
 
-// Entries of the named slots from keep(i) on: `by` added to their pages' counts.
+// f(i, k) for the entries k >= keep(i) of every named slot's row: a warp a slot,
+// so that a call's slots wait for memory together.
+template <class Keep, class F>
+SPEC_DEV void each_entry(const PagesArgs& a, Keep keep, F f) {
+  for (int i = threadIdx.x >> 5; i < a.n; i += PT / 32)
+    for (int k = keep(i) + (threadIdx.x & 31); k < a.max_pages; k += 32) f(i, k);
+}
+// Entries of the named slots from keep(i) on: `by` added to their pages' counts
+// (0: whether one is out of range, or a page that nothing names).
 template <class Keep>
 SPEC_DEV bool count_entries(const PagesArgs& a, int by, Keep keep) {
   bool bad = false;
-  for (int i = 0; i < a.n; ++i) {
-    const int32_t* row = a.table + (size_t)a.ids[i] * a.max_pages;
-    for (int k = keep(i) + threadIdx.x; k < a.max_pages; k += PT) {
-      const int p = row[k];
-      if (p < 0) continue;
-      if (!page_ok(a, p)) bad = true;
-      else if (by) atomicAdd(&a.refs[p], by);
-      else bad |= a.refs[p] <= 0;
-    }
-  }
+  each_entry(a, keep, [&](int i, int k) {
+    const int p = a.table[(size_t)a.ids[i] * a.max_pages + k];
+    if (p < 0) return;
+    if (!page_ok(a, p)) bad = true;
+    else if (by) atomicAdd(&a.refs[p], by);
+    else bad |= a.refs[p] <= 0;
+  });
   return __syncthreads_or(bad);
 }
 
@@ -145,9 +150,9 @@ __global__ void __launch_bounds__(PT) reserve_kernel(const __grid_constant__ Pag
         __syncthreads();
         if (threadIdx.x < a.n) want[threadIdx.x] = at;
         __syncthreads();
-        for (int i = 0; i < a.n; ++i) {
+        for (int i = threadIdx.x >> 5; i < a.n; i += PT / 32) {
           const int first = want[i], last = i + 1 < a.n ? want[i + 1] : need;
-          for (int k = first + threadIdx.x; k < last; k += PT) {
+          for (int k = first + (threadIdx.x & 31); k < last; k += 32) {
             a.table[(size_t)a.ids[i] * a.max_pages + have[i] + k - first] = list[k];
             a.refs[list[k]] = 1;
           }
@@ -169,8 +174,7 @@ __global__ void __launch_bounds__(PT) release_kernel(const __grid_constant__ Pag
   if (!bad) bad = count_entries(a, 0, keep);
   if (!bad) {
     count_entries(a, -1, keep);
-    for (int i = 0; i < a.n; ++i)
-      for (int k = keep(i) + threadIdx.x; k < a.max_pages; k += PT) a.table[(size_t)a.ids[i] * a.max_pages + k] = -1;
+    each_entry(a, keep, [&](int i, int k) { a.table[(size_t)a.ids[i] * a.max_pages + k] = -1; });
   }
   if (threadIdx.x == 0) *a.ws = bad ? SPEC_ERR_CAPACITY : 0;
 }
@@ -196,16 +200,17 @@ __global__ void __launch_bounds__(PT) fork_kernel(const __grid_constant__ PagesA
     }
     bad = __syncthreads_or(b);
   }
+  auto all = [](int) { return 0; };
   if (!bad) {
     bool b = false;
-    for (int i = 0; i < a.n; ++i) {
-      const int32_t* row = a.table + (size_t)a.src[i] * a.max_pages;
-      for (int k = threadIdx.x; k < pages_for(len[i]); k += PT) b |= !page_ok(a, row[k]) || a.refs[row[k]] <= 0;
-    }
+    each_entry(a, all, [&](int i, int k) {
+      const int p = k < pages_for(len[i]) ? a.table[(size_t)a.src[i] * a.max_pages + k] : 0;
+      const int q = a.table[(size_t)a.ids[i] * a.max_pages + k];
+      b |= k < pages_for(len[i]) && (!page_ok(a, p) || a.refs[p] <= 0);
+      b |= q >= 0 && (!page_ok(a, q) || a.refs[q] <= 0);
+    });
     bad = __syncthreads_or(b);
   }
-  auto all = [](int) { return 0; };
-  if (!bad) bad = count_entries(a, 0, all);
   int need = 0;
   if (!bad) {
     count_entries(a, -1, all);
@@ -221,25 +226,24 @@ __global__ void __launch_bounds__(PT) fork_kernel(const __grid_constant__ PagesA
   }
   __syncthreads();
   if (!bad) {
-    for (int i = 0; i < a.n; ++i) {
+    each_entry(a, all, [&](int i, int k) {
       const int full = len[i] / PAGE;
-      const int32_t* from = a.table + (size_t)a.src[i] * a.max_pages;
-      int32_t* to = a.table + (size_t)a.ids[i] * a.max_pages;
-      for (int k = threadIdx.x; k < a.max_pages; k += PT) {
-        int p = -1;
+      int p = -1;
+      if (k <= full) {
+        const int from = k < full || at[i] >= 0 ? a.table[(size_t)a.src[i] * a.max_pages + k] : -1;
         if (k < full) {
-          p = from[k];
+          p = from;
           atomicAdd(&a.refs[p], 1);
-        } else if (k == full && at[i] >= 0) {
+        } else if (at[i] >= 0) {
           p = list[at[i]];
           a.refs[p] = 1;
-          w.jobs[3 * at[i]] = from[k];
+          w.jobs[3 * at[i]] = from;
           w.jobs[3 * at[i] + 1] = p;
           w.jobs[3 * at[i] + 2] = len[i] % PAGE;
         }
-        to[k] = p;
       }
-    }
+      a.table[(size_t)a.ids[i] * a.max_pages + k] = p;
+    });
     for (int i = threadIdx.x; i < a.n; i += PT) {
       a.seq_len[a.ids[i]] = len[i];
       if (a.pending) a.pending[a.ids[i]] = a.pending[a.src[i]];
@@ -251,40 +255,46 @@ __global__ void __launch_bounds__(PT) fork_kernel(const __grid_constant__ PagesA
   }
 }
 
-// Rows [0, rows) of page `from` to page `to`, all layers, planes and heads: the
-// list's copies, 16 bytes a thread, four in flight.
-SPEC_DEV void copy_rows(const PagesArgs& a, int from, int to, int rows, long long i0, long long step) {
-  const int vec = a.row_bytes / 16, per = rows * vec;      // of a plane
-  const long long n = (long long)a.L * a.planes * per;
-  const size_t plane = (size_t)PAGE * a.row_bytes;
-  auto off = [&](long long i, int page) {
-    const int in = (int)(i % per);
-    const long long pl = i / per;
-    return (size_t)(pl / a.planes) * a.layer_bytes + (size_t)page * a.page_bytes + (size_t)(pl % a.planes) * plane +
-           (size_t)in * 16;
-  };
-  long long i = i0;
-  for (; i + 3 * step < n; i += 4 * step) {
-    uint4 v[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = *reinterpret_cast<const uint4*>(a.pool + off(i + j * step, from));
-#pragma unroll
-    for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(a.pool + off(i + j * step, to)) = v[j];
-  }
-  for (; i < n; i += step) *reinterpret_cast<uint4*>(a.pool + off(i, to)) = *reinterpret_cast<const uint4*>(a.pool + off(i, from));
-}
-
-__global__ void __launch_bounds__(256) fork_copy_kernel(const __grid_constant__ PagesArgs a) {
+// The list's copies: the first rows of a page, in all layers, planes and heads. The
+// rows of a plane are one piece of up to 64 rows; half of it is a CTA's unit (128
+// threads, four 16-byte reads in flight, no division in the loop). Copies of one
+// page follow each other in the list (slots forked from one source): the first of
+// them reads, and writes for all.
+__global__ void __launch_bounds__(128) fork_copy_kernel(const __grid_constant__ PagesArgs a) {
   grid_dep_wait();
   const Ws w = ws_of(a.ws);
   const int n = w.err[1];
   if (n < 0) return;
   if (a.hid)
-    for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < (long long)a.n * a.d; i += (long long)gridDim.x * 256)
-      a.hid[(size_t)a.ids[i / a.d] * a.d + i % a.d] = a.hid[(size_t)a.src[i / a.d] * a.d + i % a.d];
-  for (int j = 0; j < n; ++j)
-    copy_rows(a, w.jobs[3 * j], w.jobs[3 * j + 1], w.jobs[3 * j + 2], (long long)blockIdx.x * 256 + threadIdx.x,
-              (long long)gridDim.x * 256);
+    for (int i = blockIdx.x; i < a.n; i += gridDim.x) {
+      const float *from = a.hid + (size_t)a.src[i] * a.d;
+      float* to = a.hid + (size_t)a.ids[i] * a.d;
+      for (int k = threadIdx.x; k < a.d; k += 128) to[k] = from[k];
+    }
+  const size_t plane = (size_t)PAGE * a.row_bytes;
+  const int pieces = 2 * a.L * a.planes;
+  for (long long u = blockIdx.x; u < (long long)n * pieces; u += gridDim.x) {
+    const int j = (int)(u / pieces), k = (int)(u - (long long)j * pieces), pl = k >> 1;
+    const int from = w.jobs[3 * j], rows = w.jobs[3 * j + 2];
+    if (j && w.jobs[3 * j - 3] == from) continue;
+    int last = j + 1;
+    while (last < n && w.jobs[3 * last] == from) ++last;
+    const int vecs = rows * (a.row_bytes / 16), mid = vecs / 2, v1 = k & 1 ? vecs : mid;
+    char* base = a.pool + (size_t)(pl / a.planes) * a.layer_bytes + (size_t)(pl % a.planes) * plane;
+    const uint4* src = reinterpret_cast<const uint4*>(base + (size_t)from * a.page_bytes);
+    for (int v = (k & 1 ? mid : 0) + threadIdx.x; v < v1; v += 4 * 128) {
+      uint4 x[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (v + e * 128 < v1) x[e] = src[v + e * 128];
+      for (int i = j; i < last; ++i) {
+        uint4* dst = reinterpret_cast<uint4*>(base + (size_t)w.jobs[3 * i + 1] * a.page_bytes);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (v + e * 128 < v1) dst[v + e * 128] = x[e];
+      }
+    }
+  }
 }
 
 // With n pages in use, those numbered n or higher go to the free ones below, both
@@ -418,10 +428,10 @@ __global__ void __launch_bounds__(256) rows_keep_kernel(const __grid_constant__ 
   }
 }
 
-cudaError_t launch_after(const void* f, int grid, const PagesArgs& a, cudaStream_t st) {
+cudaError_t launch_after(const void* f, int grid, int threads, const PagesArgs& a, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(256);
+  cfg.blockDim = dim3(threads);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -450,12 +460,12 @@ int pages_release(const PagesArgs& a, cudaStream_t st) {
 int pages_fork(const PagesArgs& a, cudaStream_t st) {
   fork_kernel<<<1, PT, 0, st>>>(a);
   if (cudaPeekAtLastError() != cudaSuccess) return -1;
-  return launch_after((const void*)fork_copy_kernel, 8 * num_sms(), a, st) == cudaSuccess ? 2 : -1;
+  return launch_after((const void*)fork_copy_kernel, (int)std::min<long long>(16ll * num_sms(), 2ll * a.n * a.L * a.planes), 128, a, st) == cudaSuccess ? 2 : -1;
 }
 int pages_compact(const PagesArgs& a, cudaStream_t st) {
   compact_kernel<<<1, PT, 0, st>>>(a);
   if (cudaPeekAtLastError() != cudaSuccess) return -1;
-  return launch_after((const void*)compact_copy_kernel, 8 * num_sms(), a, st) == cudaSuccess ? 2 : -1;
+  return launch_after((const void*)compact_copy_kernel, 8 * num_sms(), 256, a, st) == cudaSuccess ? 2 : -1;
 }
 int rows_keep(const KeepArgs& a, cudaStream_t st) {
   const long long vecs = (long long)a.L * a.planes * (a.row_bytes / 16);
