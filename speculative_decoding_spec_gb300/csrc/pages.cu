@@ -19,9 +19,10 @@ constexpr int PAGE = 64;
 constexpr int PT = 1024;      // threads of a planning CTA
 constexpr int N_MAX = 1024;   // slots of a call
 
-// Workspace: [0] error word, [1] copies (-1: the call changes nothing), from [64]
+// Workspace: [0] error word, [1] copies (-1: the call changes nothing), [2] runs, from [64]
 // on the copies (fork: source page, page, rows; compact: from, to) and, behind a
-// fork's, the pages handed out (reserve: those alone).
+// fork's, the pages handed out (reserve: those alone) and where runs of copies of
+// one page begin.
 struct Ws {
   int *err, *jobs;
 };
@@ -249,50 +250,61 @@ __global__ void __launch_bounds__(PT) fork_kernel(const __grid_constant__ PagesA
       if (a.pending) a.pending[a.ids[i]] = a.pending[a.src[i]];
     }
   }
+  // copies of one page follow each other in the list (slots forked from one
+  // source): where each such run begins
+  __syncthreads();
+  const bool first = !bad && threadIdx.x < need &&
+                     (threadIdx.x == 0 || w.jobs[3 * threadIdx.x] != w.jobs[3 * threadIdx.x - 3]);
+  int runs;
+  const int run = scan(first, red, &runs);
+  if (first) list[N_MAX + run] = threadIdx.x;
   if (threadIdx.x == 0) {
     *w.err = bad ? SPEC_ERR_CAPACITY : 0;
     w.err[1] = bad ? -1 : need;
+    w.err[2] = runs;
   }
 }
 
 // The list's copies: the first rows of a page, in all layers, planes and heads. The
 // rows of a plane are one piece of up to 64 rows; half of it is a CTA's unit (128
-// threads, four 16-byte reads in flight, no division in the loop). Copies of one
-// page follow each other in the list (slots forked from one source): the first of
-// them reads, and writes for all.
+// threads, four 16-byte reads in flight, no division in the loop), read once for all
+// slots forked from one source. Behind those units the hidden states'.
+constexpr int HID = 4 * 128 * 4;  // floats a unit
 __global__ void __launch_bounds__(128) fork_copy_kernel(const __grid_constant__ PagesArgs a) {
   grid_dep_wait();
   const Ws w = ws_of(a.ws);
-  const int n = w.err[1];
+  const int n = w.err[1], runs = w.err[2], t = threadIdx.x;
   if (n < 0) return;
-  if (a.hid)
-    for (int i = blockIdx.x; i < a.n; i += gridDim.x) {
-      const float *from = a.hid + (size_t)a.src[i] * a.d;
-      float* to = a.hid + (size_t)a.ids[i] * a.d;
-      for (int k = threadIdx.x; k < a.d; k += 128) to[k] = from[k];
-    }
   const size_t plane = (size_t)PAGE * a.row_bytes;
-  const int pieces = 2 * a.L * a.planes;
-  for (long long u = blockIdx.x; u < (long long)n * pieces; u += gridDim.x) {
-    const int j = (int)(u / pieces), k = (int)(u - (long long)j * pieces), pl = k >> 1;
-    const int from = w.jobs[3 * j], rows = w.jobs[3 * j + 2];
-    if (j && w.jobs[3 * j - 3] == from) continue;
-    int last = j + 1;
-    while (last < n && w.jobs[3 * last] == from) ++last;
-    const int vecs = rows * (a.row_bytes / 16), mid = vecs / 2, v1 = k & 1 ? vecs : mid;
-    char* base = a.pool + (size_t)(pl / a.planes) * a.layer_bytes + (size_t)(pl % a.planes) * plane;
-    const uint4* src = reinterpret_cast<const uint4*>(base + (size_t)from * a.page_bytes);
-    for (int v = (k & 1 ? mid : 0) + threadIdx.x; v < v1; v += 4 * 128) {
+  const int pieces = 2 * a.L * a.planes, hids = a.hid ? (a.d + HID - 1) / HID : 0;
+  const long long copies = (long long)runs * pieces, units = copies + (long long)a.n * hids;
+  auto move = [&](const uint4* src, int v0, int v1, auto each) {  // [v0, v1) of src to each() of them
+    for (int v = v0 + t; v < v1; v += 4 * 128) {
       uint4 x[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e)
         if (v + e * 128 < v1) x[e] = src[v + e * 128];
-      for (int i = j; i < last; ++i) {
-        uint4* dst = reinterpret_cast<uint4*>(base + (size_t)w.jobs[3 * i + 1] * a.page_bytes);
+      each([&](uint4* dst) {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           if (v + e * 128 < v1) dst[v + e * 128] = x[e];
-      }
+      });
+    }
+  };
+  for (long long u = blockIdx.x; u < units; u += gridDim.x) {
+    if (u < copies) {
+      const int r = (int)(u / pieces), k = (int)(u - (long long)r * pieces), pl = k >> 1;
+      const int j = w.jobs[4 * N_MAX + r], last = r + 1 < runs ? w.jobs[4 * N_MAX + r + 1] : n;
+      const int vecs = w.jobs[3 * j + 2] * (a.row_bytes / 16), mid = vecs / 2;
+      char* base = a.pool + (size_t)(pl / a.planes) * a.layer_bytes + (size_t)(pl % a.planes) * plane;
+      move(reinterpret_cast<const uint4*>(base + (size_t)w.jobs[3 * j] * a.page_bytes), k & 1 ? mid : 0, k & 1 ? vecs : mid,
+           [&](auto put) {
+             for (int i = j; i < last; ++i) put(reinterpret_cast<uint4*>(base + (size_t)w.jobs[3 * i + 1] * a.page_bytes));
+           });
+    } else {
+      const int i = (int)((u - copies) / hids), c = (int)((u - copies) % hids);
+      move(reinterpret_cast<const uint4*>(a.hid + (size_t)a.src[i] * a.d), c * HID / 4, min((c + 1) * HID, a.d) / 4,
+           [&](auto put) { put(reinterpret_cast<uint4*>(a.hid + (size_t)a.ids[i] * a.d)); });
     }
   }
 }
@@ -445,8 +457,8 @@ cudaError_t launch_after(const void* f, int grid, int threads, const PagesArgs& 
 }  // namespace
 
 size_t pages_bytes(int n_pages, int n) {
-  // the head; three words a copy and one a page handed out (fork), one a page (reserve), two a page (compact)
-  return (size_t)4 * (64 + std::max(4 * N_MAX, 2 * n_pages));
+  // the head; three words a copy, one a page handed out and one a run (fork), one a page (reserve), two a page (compact)
+  return (size_t)4 * (64 + std::max(5 * N_MAX, 2 * n_pages));
 }
 
 int pages_reserve(const PagesArgs& a, cudaStream_t st) {
@@ -460,7 +472,7 @@ int pages_release(const PagesArgs& a, cudaStream_t st) {
 int pages_fork(const PagesArgs& a, cudaStream_t st) {
   fork_kernel<<<1, PT, 0, st>>>(a);
   if (cudaPeekAtLastError() != cudaSuccess) return -1;
-  return launch_after((const void*)fork_copy_kernel, (int)std::min<long long>(16ll * num_sms(), 2ll * a.n * a.L * a.planes), 128, a, st) == cudaSuccess ? 2 : -1;
+  return launch_after((const void*)fork_copy_kernel, (int)std::min<long long>(16ll * num_sms(), (2ll * a.L * a.planes + a.d / HID + 1) * a.n), 128, a, st) == cudaSuccess ? 2 : -1;
 }
 int pages_compact(const PagesArgs& a, cudaStream_t st) {
   compact_kernel<<<1, PT, 0, st>>>(a);

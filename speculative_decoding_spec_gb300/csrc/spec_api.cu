@@ -1201,7 +1201,7 @@ spec_status spec_pages_fork(const spec_model_desc* m, const spec_kv_desc* kv, in
                             void* stream) {
   PagesArgs a = {};
   if (!m || !model_ok(*m) || !kv_ok(kv) || !pages_args(a, kv, refs, n, dst, workspace) || !src || !state ||
-      !state->seq_len)
+      !state->seq_len || !aligned16({state->hid}))
     return SPEC_EINVAL;
   if (n > PAGES_N_MAX || kv->n_pages > PAGES_MAX || !rows_copy_ok(*m, *kv)) return SPEC_EUNSUPPORTED;
   if (ws_bytes < pages_bytes(kv->n_pages, n)) return SPEC_ECAPACITY;
