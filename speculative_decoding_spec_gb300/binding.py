@@ -488,34 +488,42 @@ class Cache:
         self.model = spec_model_desc(self.L, 8, self.nkv, self.nkv, self.hd, 8, 2, dt, dt, 1e-6, 1e4, 0, 0, 0)
         self.kv = spec_kv_desc(pool.data_ptr(), self.n_pages, PAGE, block_table.data_ptr(), self.max_pages, self.n_slots)
         self.model_ref, self.kv_ref = C.byref(self.model), C.byref(self.kv)
-        self._bytes = {}
-
-    def _size(self, what, *shape):
-        """Bytes of a call's workspace, looked up once a shape."""
-        n = self._bytes.get(shape)
-        if n is None:
-            n = self._bytes[shape] = what(*shape)
-        return n
+        self.width = self.nkv * self.hd
+        self.sizes = {}     # bytes of scratch by a call's shape
 
 
 def _ints(fn, name, t, n, dev):
     """Address of int32 [n] (or of that many in all) on GPU `dev`."""
-    if t.dtype is not torch.int32 or t.numel() != n or t.get_device() != dev or not t.is_contiguous():
-        raise SpecError(fn, SPEC_EINVAL, "%s must be a contiguous int32 tensor of %d on the cache's GPU" % (name, n))
-    return t.data_ptr()
+    if t.dtype is _I32 and t.numel() == n and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    raise SpecError(fn, SPEC_EINVAL, "%s must be a contiguous int32 tensor of %d on the call's GPU" % (name, n))
+
+
+def _floats(fn, name, t, n, dev):
+    if t.dtype is _F32 and t.numel() == n and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    raise SpecError(fn, SPEC_EINVAL, "%s must be a contiguous float32 tensor of %d on the call's GPU" % (name, n))
+
+
+_I32, _F32, _U8 = torch.int32, torch.float32, torch.uint8
 
 
 def _workspace(fn, like, given, n):
+    """The caller's scratch of n bytes, or some that belongs to the call's stream."""
     if given is None:
-        return like.new_empty(max(n, 1), dtype=torch.uint8)
-    _need(fn, given.dtype is torch.uint8 and given.is_contiguous() and given.get_device() == like.get_device() and
-          given.numel() >= n, "workspace must be a contiguous uint8 tensor of %d bytes beside the inputs" % n)
-    return given
+        return like.new_empty(n, dtype=_U8)
+    if given.dtype is _U8 and given.is_contiguous() and given.get_device() == like.get_device() and given.numel() >= n:
+        return given
+    raise SpecError(fn, SPEC_EINVAL, "workspace must be a contiguous uint8 tensor of %d bytes beside the inputs" % n)
 
 
 def _outcome(fn, workspace):
     check(fn, _DEVICE_ERRORS.get(int(workspace[:4].view(torch.int32)), SPEC_EINVAL))
 
+
+# (The functions below are called once a layer or step, on tensors whose kernels
+# take a few microseconds: a call on the current GPU and stream goes straight
+# through, any other makes them current first and calls again.)
 
 def spec_attention_tree(cache: Cache, layer: int, seq_ids: torch.Tensor, seq_len: torch.Tensor, q: torch.Tensor,
                         parents: Optional[torch.Tensor] = None, n_rows: Optional[torch.Tensor] = None,
@@ -526,39 +534,41 @@ def spec_attention_tree(cache: Cache, layer: int, seq_ids: torch.Tensor, seq_len
     chain), n_rows int32 [B] (None: R each). Returns out in q's type; rows from
     n_rows on are left as they were (zero where out is not given). sync=True waits
     and raises what the call recorded."""
-    fn = "spec_attention_tree"
-    L = lib()
-    dev, B = cache.dev, seq_ids.numel()
-    dt = _LOGIT_DTYPES.get(q.dtype)
-    _need(fn, dt is not None and q.dim() == 2 and q.get_device() == dev and q.shape[0] > 0 and B > 0 and
-          q.shape[0] % B == 0 and q.shape[1] % (cache.hd * cache.nkv) == 0 and q.shape[1] > 0,
-          "q must be a float32 or bfloat16 tensor [B*R][nq*hd] beside the cache")
-    M, W = q.shape
-    R = M // B
+    fn, dev = "spec_attention_tree", cache.dev
+    if stream is not None or dev != _current_device():
+        with _on(dev, stream):
+            return spec_attention_tree(cache, layer, seq_ids, seq_len, q, parents, n_rows, out, workspace, None, sync)
+    dt, shape, B = _LOGIT_DTYPES.get(q.dtype), q.shape, seq_ids.numel()
+    if dt is None or len(shape) != 2 or q.get_device() != dev or B == 0 or shape[0] == 0 or shape[0] % B or \
+            shape[1] == 0 or shape[1] % cache.width:
+        raise SpecError(fn, SPEC_EINVAL, "q must be a float32 or bfloat16 tensor [B*R][nq*hd] beside the cache")
+    M, W = shape
+    R, heads = M // B, W // cache.hd
     ldq, step = q.stride()
-    _need(fn, step == 1 or W == 1, "the values of a row must be contiguous")
-    ldq = ldq if M > 1 else W
-    ids = _ints(fn, "seq_ids", seq_ids, B, dev)
-    lens = _ints(fn, "seq_len", seq_len, cache.n_slots, dev)
+    ids, lens = _ints(fn, "seq_ids", seq_ids, B, dev), _ints(fn, "seq_len", seq_len, cache.n_slots, dev)
     par = None if parents is None else _ints(fn, "parents", parents, M, dev)
     rows = None if n_rows is None else _ints(fn, "n_rows", n_rows, B, dev)
-    with _on(dev, stream) as st:
-        if out is None:
-            out = q.new_empty((M, W)) if n_rows is None else q.new_zeros((M, W))
-        else:
-            _need(fn, out.dtype is q.dtype and out.shape == q.shape and out.get_device() == dev and
-                  (out.stride(1) == 1 or W == 1), "out must be like q")
-        n = cache._size(lambda *s: L.spec_attention_tree_workspace_bytes(cache.model_ref, *s), B, R, W // cache.hd,
-                        cache.max_pages)
-        if n == 0:
-            raise SpecError(fn, SPEC_EUNSUPPORTED)
-        workspace = _workspace(fn, q, workspace, n)
-        rc = L.spec_attention_tree(cache.model_ref, cache.kv_ref, layer, B, ids, lens, R, W // cache.hd, par, rows, dt,
-                                   q.data_ptr(), ldq, out.data_ptr(), out.stride(0) if M > 1 else W,
-                                   workspace.data_ptr(), workspace.numel(), st)
-        check(fn, rc)
-        if sync:
-            _outcome(fn, workspace)
+    if out is None:
+        out = q.new_empty(shape) if n_rows is None else q.new_zeros(shape)
+    elif out.dtype is not q.dtype or out.shape != shape or out.get_device() != dev:
+        raise SpecError(fn, SPEC_EINVAL, "out must be like q")
+    ldo, ostep = out.stride()
+    if step != 1 or ostep != 1:
+        raise SpecError(fn, SPEC_EINVAL, "the values of a row must be contiguous")
+    n = cache.sizes.get((B, R, heads))
+    if n is None:
+        n = cache.sizes[B, R, heads] = lib().spec_attention_tree_workspace_bytes(cache.model_ref, B, R, heads,
+                                                                                 cache.max_pages)
+    if n == 0:
+        raise SpecError(fn, SPEC_EUNSUPPORTED)
+    ws = _workspace(fn, q, workspace, n)
+    rc = lib().spec_attention_tree(cache.model_ref, cache.kv_ref, layer, B, ids, lens, R, heads, par, rows, dt, q.data_ptr(),
+                                   ldq if M > 1 else W, out.data_ptr(), ldo if M > 1 else W, ws.data_ptr(), ws.numel(),
+                                   _raw_stream(dev))
+    if rc:
+        raise SpecError(fn, rc)
+    if sync:
+        _outcome(fn, ws)
     return out
 
 
@@ -566,39 +576,51 @@ def spec_rows_keep(cache: Cache, seq_ids: torch.Tensor, seq_len: torch.Tensor, r
                    n_keep: torch.Tensor, workspace: Optional[torch.Tensor] = None, stream=None, sync: bool = False):
     """The accepted rows of a tree moved together in every layer (include/spec.h):
     rows int32 [B][n] ascending, n_keep int32 [B] of them used. seq_len stays."""
-    fn = "spec_rows_keep"
-    L = lib()
-    dev, B = cache.dev, seq_ids.numel()
-    _need(fn, rows.dim() == 2 and rows.shape[0] == B and rows.numel() > 0, "rows must be an int32 tensor [B][n]")
+    fn, dev = "spec_rows_keep", cache.dev
+    if stream is not None or dev != _current_device():
+        with _on(dev, stream):
+            return spec_rows_keep(cache, seq_ids, seq_len, rows, n_keep, workspace, None, sync)
+    B = seq_ids.numel()
+    if rows.dim() != 2 or rows.shape[0] != B or rows.numel() == 0:
+        raise SpecError(fn, SPEC_EINVAL, "rows must be an int32 tensor [B][n]")
     n = rows.shape[1]
     ids, lens = _ints(fn, "seq_ids", seq_ids, B, dev), _ints(fn, "seq_len", seq_len, cache.n_slots, dev)
     r, k = _ints(fn, "rows", rows, B * n, dev), _ints(fn, "n_keep", n_keep, B, dev)
-    with _on(dev, stream) as st:
-        workspace = _workspace(fn, rows, workspace, 256)
-        check(fn, L.spec_rows_keep(cache.model_ref, cache.kv_ref, B, ids, lens, n, r, k, workspace.data_ptr(),
-                                   workspace.numel(), st))
-        if sync:
-            _outcome(fn, workspace)
+    ws = _workspace(fn, rows, workspace, 256)
+    rc = lib().spec_rows_keep(cache.model_ref, cache.kv_ref, B, ids, lens, n, r, k, ws.data_ptr(), ws.numel(),
+                              _raw_stream(dev))
+    if rc:
+        raise SpecError(fn, rc)
+    if sync:
+        _outcome(fn, ws)
 
 
 def _pages(fn, cache, n, workspace):
-    L = lib()
-    _need(fn, cache.refs is not None, "the cache has no counts of references")
-    size = cache._size(L.spec_pages_workspace_bytes, cache.n_pages, max(n, 1))
-    if n < 1 or size == 0:
+    """The counts' address and the scratch of a call on n slots."""
+    if cache.refs is None:
+        raise SpecError(fn, SPEC_EINVAL, "the cache has no counts of references")
+    size = cache.sizes.get(n)
+    if size is None:
+        size = cache.sizes[n] = lib().spec_pages_workspace_bytes(cache.n_pages, n)
+    if size == 0:
         raise SpecError(fn, SPEC_EINVAL if n < 1 else SPEC_EUNSUPPORTED)
-    return L, _workspace(fn, cache.refs, workspace, size)
+    return cache.refs.data_ptr(), _workspace(fn, cache.refs, workspace, size)
 
 
 def _pages_call(fn, cache, ids, lens, workspace, stream, sync):
-    n, dev = ids.numel(), cache.dev
+    dev = cache.dev
+    if stream is not None or dev != _current_device():
+        with _on(dev, stream):
+            return _pages_call(fn, cache, ids, lens, workspace, None, sync)
+    n = ids.numel()
     i = _ints(fn, "seq_ids", ids, n, dev)
     k = None if lens is None else _ints(fn, "lens", lens, n, dev)
-    with _on(dev, stream) as st:
-        L, ws = _pages(fn, cache, n, workspace)
-        check(fn, getattr(L, fn)(cache.kv_ref, cache.refs.data_ptr(), n, i, k, ws.data_ptr(), ws.numel(), st))
-        if sync:
-            _outcome(fn, ws)
+    refs, ws = _pages(fn, cache, n, workspace)
+    rc = getattr(lib(), fn)(cache.kv_ref, refs, n, i, k, ws.data_ptr(), ws.numel(), _raw_stream(dev))
+    if rc:
+        raise SpecError(fn, rc)
+    if sync:
+        _outcome(fn, ws)
 
 
 def spec_pages_reserve(cache: Cache, seq_ids: torch.Tensor, lens: torch.Tensor, workspace=None, stream=None,
@@ -621,24 +643,31 @@ def spec_pages_fork(cache: Cache, seq_len: torch.Tensor, src: torch.Tensor, dst:
     """Slots dst continue slots src (int32 [n] each; include/spec.h): full pages are
     shared, the rows of the last one copied; seq_len, pending (int32 [n_slots]) and
     hid (float32 [n_slots][d]) are copied too."""
-    fn = "spec_pages_fork"
-    n, dev, S = dst.numel(), cache.dev, cache.n_slots
+    fn, dev = "spec_pages_fork", cache.dev
+    if stream is not None or dev != _current_device():
+        with _on(dev, stream):
+            return spec_pages_fork(cache, seq_len, src, dst, pending, hid, workspace, None, sync)
+    n, slots, model = dst.numel(), cache.n_slots, cache.model
     s, d = _ints(fn, "src", src, n, dev), _ints(fn, "dst", dst, n, dev)
-    _need(fn, hid is None or (hid.dtype is torch.float32 and hid.dim() == 2 and hid.shape[0] == S and
-                              hid.shape[1] % 8 == 0 and hid.is_contiguous() and hid.get_device() == dev),
-          "hid must be a contiguous float32 tensor [n_slots][d], d a multiple of 8, beside the cache")
-    state = spec_state(_ints(fn, "seq_len", seq_len, S, dev),
-                       None if pending is None else _ints(fn, "pending", pending, S, dev), _ptr(hid), None)
-    model = cache.model
-    if hid is not None and hid.shape[1] != model.d_model:
-        model = spec_model_desc.from_buffer_copy(model)
-        model.d_model = hid.shape[1]
-    with _on(dev, stream) as st:
-        L, ws = _pages(fn, cache, n, workspace)
-        check(fn, L.spec_pages_fork(C.byref(model), cache.kv_ref, cache.refs.data_ptr(), C.byref(state), n, s, d,
-                                    ws.data_ptr(), ws.numel(), st))
-        if sync:
-            _outcome(fn, ws)
+    state = spec_state(_ints(fn, "seq_len", seq_len, slots, dev),
+                       None if pending is None else _ints(fn, "pending", pending, slots, dev))
+    if hid is not None:
+        shape = hid.shape
+        if hid.dtype is not _F32 or len(shape) != 2 or shape[0] != slots or shape[1] % 8 or not hid.is_contiguous() or \
+                hid.get_device() != dev:
+            raise SpecError(fn, SPEC_EINVAL, "hid must be a contiguous float32 tensor [n_slots][d], d a multiple of 8, "
+                            "beside the cache")
+        state.hid = hid.data_ptr()
+        if shape[1] != model.d_model:
+            model = spec_model_desc.from_buffer_copy(model)
+            model.d_model = shape[1]
+    refs, ws = _pages(fn, cache, n, workspace)
+    rc = lib().spec_pages_fork(C.byref(model), cache.kv_ref, refs, C.byref(state), n, s, d, ws.data_ptr(), ws.numel(),
+                               _raw_stream(dev))
+    if rc:
+        raise SpecError(fn, rc)
+    if sync:
+        _outcome(fn, ws)
 
 
 def spec_pages_compact(cache: Cache, block_table: Optional[torch.Tensor] = None, refs: Optional[torch.Tensor] = None,
@@ -646,27 +675,20 @@ def spec_pages_compact(cache: Cache, block_table: Optional[torch.Tensor] = None,
     """The pages in use moved to the lowest numbers (include/spec.h). The tables
     afterwards go to block_table and refs (None: the cache's own). Returns (moved
     int32 [n_pages], n_live int32 [1])."""
-    fn = "spec_pages_compact"
-    dev = cache.dev
-    _need(fn, cache.refs is not None, "the cache has no counts of references")
-    block_table = cache.block_table if block_table is None else block_table
-    refs = cache.refs if refs is None else refs
-    t = _ints(fn, "block_table", block_table, cache.block_table.numel(), dev)
-    r = _ints(fn, "refs", refs, cache.n_pages, dev)
-    with _on(dev, stream) as st:
-        L, ws = _pages(fn, cache, 1, workspace)
-        moved, n_live = refs.new_empty(cache.n_pages), refs.new_empty(1)
-        check(fn, L.spec_pages_compact(cache.model_ref, cache.kv_ref, cache.refs.data_ptr(), t, r, moved.data_ptr(),
-                                       n_live.data_ptr(), ws.data_ptr(), ws.numel(), st))
+    fn, dev = "spec_pages_compact", cache.dev
+    if stream is not None or dev != _current_device():
+        with _on(dev, stream):
+            return spec_pages_compact(cache, block_table, refs, workspace, None)
+    counts, ws = _pages(fn, cache, 1, workspace)
+    t = _ints(fn, "block_table", cache.block_table if block_table is None else block_table, cache.n_slots * cache.max_pages,
+              dev)
+    r = _ints(fn, "refs", cache.refs if refs is None else refs, cache.n_pages, dev)
+    moved, n_live = cache.refs.new_empty(cache.n_pages), cache.refs.new_empty(1)
+    rc = lib().spec_pages_compact(cache.model_ref, cache.kv_ref, counts, t, r, moved.data_ptr(), n_live.data_ptr(),
+                                  ws.data_ptr(), ws.numel(), _raw_stream(dev))
+    if rc:
+        raise SpecError(fn, rc)
     return moved, n_live
-
-
-def _floats(fn, name, t, n, dev):
-    if t is None:
-        return None
-    if t.dtype is not torch.float32 or t.numel() != n or t.get_device() != dev or not t.is_contiguous():
-        raise SpecError(fn, SPEC_EINVAL, "%s must be a contiguous float32 tensor of %d beside the logits" % (name, n))
-    return t.data_ptr()
 
 
 def spec_adjust_logits(logits: torch.Tensor, R: int = 1, tokens: Optional[torch.Tensor] = None,
@@ -682,46 +704,70 @@ def spec_adjust_logits(logits: torch.Tensor, R: int = 1, tokens: Optional[torch.
     (rows may be strided), bias_tokens / bias_values [B][n], mask int32 [n_masks]
     [ceil(V/32)], the others [B] or [B*R]. Returns out (a new tensor where not
     given, its rows on 16-byte boundaries; the logits themselves: in place)."""
-    fn = "spec_adjust_logits"
+    fn, dev = "spec_adjust_logits", logits.get_device()
+    if stream is not None or dev != _current_device():
+        _need(fn, dev >= 0, "logits must be a float32 or bfloat16 CUDA tensor [rows][V]")
+        with _on(dev, stream):
+            return spec_adjust_logits(logits, R, tokens, parents, history, hist_len, prompt_len, repetition, presence,
+                                      frequency, bias_tokens, bias_values, mask, mask_ids, out, status, None)
     M, V, dt, ld, dev = _logits(fn, logits)
-    _need(fn, R >= 1 and M % R == 0, "the logits must have R rows for every sequence")
+    if R < 1 or M % R:
+        raise SpecError(fn, SPEC_EINVAL, "the logits must have R rows for every sequence")
     B = M // R
-    ints = lambda name, t, n: None if t is None else _ints(fn, name, t, n, dev)
     s = spec_adjust()
     if history is not None:
-        _need(fn, history.dtype is torch.int32 and history.dim() == 2 and history.shape[0] == B and
-              history.get_device() == dev and (history.stride(1) == 1 or history.shape[1] <= 1),
-              "history must be an int32 tensor [B][n] beside the logits, the tokens of a row contiguous")
-        s.history, s.n_history = history.data_ptr(), history.shape[1]
-        s.ld_history = history.stride(0) if B > 1 else history.shape[1]
-    _need(fn, (bias_tokens is None) == (bias_values is None), "bias_tokens and bias_values go together")
+        shape = history.shape
+        if history.dtype is not _I32 or len(shape) != 2 or shape[0] != B or history.get_device() != dev or \
+                (shape[1] > 1 and history.stride(1) != 1):
+            raise SpecError(fn, SPEC_EINVAL, "history must be an int32 tensor [B][n] beside the logits, the tokens of a row "
+                            "contiguous")
+        s.history, s.n_history = history.data_ptr(), shape[1]
+        s.ld_history = history.stride(0) if B > 1 else shape[1]
+        if hist_len is not None:
+            s.hist_len = _ints(fn, "hist_len", hist_len, B, dev)
+        if prompt_len is not None:
+            s.prompt_len = _ints(fn, "prompt_len", prompt_len, B, dev)
+    if (bias_tokens is None) != (bias_values is None):
+        raise SpecError(fn, SPEC_EINVAL, "bias_tokens and bias_values go together")
     if bias_tokens is not None:
         n = bias_tokens.numel()
-        _need(fn, n % B == 0, "bias_tokens must have a row for every sequence")
+        if n % B:
+            raise SpecError(fn, SPEC_EINVAL, "bias_tokens must have a row for every sequence")
         s.bias_tokens, s.bias_values = _ints(fn, "bias_tokens", bias_tokens, n, dev), _floats(fn, "bias_values", bias_values, n, dev)
         s.n_bias = n // B
     if mask is not None:
-        _need(fn, mask.dtype is torch.int32 and mask.dim() == 2 and mask.get_device() == dev and
-              mask.shape[0] > 0 and mask.shape[1] >= (V + 31) // 32 and (mask.stride(1) == 1 or mask.shape[1] == 1),
-              "mask must be an int32 tensor [n_masks][ceil(V/32)] beside the logits")
-        s.mask, s.n_masks = mask.data_ptr(), mask.shape[0]
-        s.ld_mask = mask.stride(0) if mask.shape[0] > 1 else mask.shape[1]
-        _need(fn, s.ld_mask >= (V + 31) // 32, "the masks must not overlap")
-        s.mask_ids = ints("mask_ids", mask_ids, M)
-    s.hist_len, s.prompt_len = ints("hist_len", hist_len, B), ints("prompt_len", prompt_len, B)
-    s.tokens, s.parents = ints("tokens", tokens, M), ints("parents", parents, M)
-    s.repetition, s.presence = _floats(fn, "repetition", repetition, B, dev), _floats(fn, "presence", presence, B, dev)
-    s.frequency, s.status = _floats(fn, "frequency", frequency, B, dev), ints("status", status, 1)
-    with _on(dev, stream) as st:
-        if out is None:
-            per = 16 // logits.element_size()
-            out = logits.new_empty((M, -(-V // per) * per))[:, :V]
-        else:
-            _need(fn, out.dtype is logits.dtype and out.shape == logits.shape and out.get_device() == dev and
-                  (V == 1 or out.stride(1) == 1) and (M == 1 or out.stride(0) >= V), "out must be like the logits")
-        rc = lib().spec_adjust_logits(dt, logits.data_ptr(), ld, B, R, V, C.byref(s), out.data_ptr(),
-                                      out.stride(0) if M > 1 else V if out is not logits else ld, st)
-    check(fn, rc)
+        shape, words = mask.shape, (V + 31) // 32
+        if mask.dtype is not _I32 or len(shape) != 2 or mask.get_device() != dev or shape[0] == 0 or shape[1] < words or \
+                (shape[1] > 1 and mask.stride(1) != 1) or (shape[0] > 1 and mask.stride(0) < words):
+            raise SpecError(fn, SPEC_EINVAL, "mask must be an int32 tensor [n_masks][ceil(V/32)] beside the logits")
+        s.mask, s.n_masks = mask.data_ptr(), shape[0]
+        s.ld_mask = mask.stride(0) if shape[0] > 1 else shape[1]
+        if mask_ids is not None:
+            s.mask_ids = _ints(fn, "mask_ids", mask_ids, M, dev)
+    if tokens is not None:
+        s.tokens = _ints(fn, "tokens", tokens, M, dev)
+    if parents is not None:
+        s.parents = _ints(fn, "parents", parents, M, dev)
+    if repetition is not None:
+        s.repetition = _floats(fn, "repetition", repetition, B, dev)
+    if presence is not None:
+        s.presence = _floats(fn, "presence", presence, B, dev)
+    if frequency is not None:
+        s.frequency = _floats(fn, "frequency", frequency, B, dev)
+    if status is not None:
+        s.status = _ints(fn, "status", status, 1, dev)
+    if out is None:
+        per = 7 if dt else 3
+        ldo = V + per & ~per
+        out = logits.new_empty((M, V)) if ldo == V else logits.new_empty_strided((M, V), (ldo, 1))
+    else:
+        if out.dtype is not logits.dtype or out.shape != logits.shape or out.get_device() != dev or \
+                (V > 1 and out.stride(1) != 1):
+            raise SpecError(fn, SPEC_EINVAL, "out must be like the logits")
+        ldo = out.stride(0) if M > 1 else ld
+    rc = lib().spec_adjust_logits(dt, logits.data_ptr(), ld, B, R, V, C.byref(s), out.data_ptr(), ldo, _raw_stream(dev))
+    if rc:
+        raise SpecError(fn, rc)
     return out
 
 
@@ -740,20 +786,30 @@ def _linear_ws(device, nbytes):
 
 class Engine:
     """Owns the torch allocations (KV pool, block table, slot state, workspace)
-    around one spec_ctx and forwards calls to the C ABI on its own stream."""
+    around one spec_ctx and forwards calls to the C ABI on its own stream. Every
+    slot has its pages from the start, or, with n_pages given, none: they are then
+    handed out of a pool of n_pages by spec_pages_reserve (a pass needs those of
+    seq_len + its rows), shared by spec_pages_fork and given back by
+    spec_pages_release."""
 
     def __init__(self, tw, dw=None, n_slots=1, B_max=1, rows_max=4, max_ctx=256, shuffle_pages=False,
-                 device="cuda", graphs=True):
+                 device="cuda", graphs=True, n_pages=None):
         L = lib()
         t = tw.shape
         self.tw, self.dw, self.shape = tw, dw, t
         self.device = device
         self.pages_per_seq = int(math.ceil(max_ctx / PAGE))
-        self.n_pages = n_slots * self.pages_per_seq
+        self.n_pages = n_slots * self.pages_per_seq if n_pages is None else int(n_pages)
         kvdt = torch.float32 if t.kvdtype == F32 else torch.bfloat16
         self.pool = torch.zeros((t.L, self.n_pages, 2, t.nkv, PAGE, t.hd), dtype=kvdt, device=device)
-        self.block_table = synth.make_page_table(n_slots, self.pages_per_seq, self.n_pages, shuffle_pages,
-                                                 device=device)
+        if n_pages is None:
+            self.block_table = synth.make_page_table(n_slots, self.pages_per_seq, self.n_pages, shuffle_pages,
+                                                     device=device)
+            self.page_refs = None
+        else:
+            self.block_table = torch.full((n_slots, self.pages_per_seq), -1, dtype=torch.int32, device=device)
+            self.page_refs = torch.zeros(self.n_pages, dtype=torch.int32, device=device)
+        self.cache = Cache(self.pool, self.block_table, self.page_refs)
         self.seq_len = torch.zeros(n_slots, dtype=torch.int32, device=device)
         self.pending = torch.zeros(n_slots, dtype=torch.int32, device=device)
         self.hid = torch.zeros((n_slots, t.d), dtype=torch.float32, device=device)
@@ -926,6 +982,29 @@ class Engine:
             self.ctx, B, _ptr(seq_ids), k, _ptr(drafts), _ptr(ref), ref.shape[1], float(alpha), _ptr(draws),
             _ptr(offsets), self.stream.cuda_stream))
         self.leave()
+
+    def _page_call(self, f, *args, **kw):
+        """A call on the engine's cache, on its stream; raises what it recorded."""
+        self.enter()
+        r = f(self.cache, *args, stream=self.stream, **kw)
+        self.leave()
+        return r
+
+    def spec_pages_reserve(self, seq_ids, lens: torch.Tensor):
+        """Pages for the first lens (int32 [B]) positions of the slots."""
+        self._page_call(spec_pages_reserve, seq_ids, lens, sync=True)
+
+    def spec_pages_release(self, seq_ids, lens: Optional[torch.Tensor] = None):
+        """The slots' pages behind their first lens positions (None: all) given back."""
+        self._page_call(spec_pages_release, seq_ids, lens, sync=True)
+
+    def spec_pages_fork(self, src, dst):
+        """Slots dst continue slots src: pages, length, pending token and hidden state."""
+        self._page_call(spec_pages_fork, self.seq_len, src, dst, pending=self.pending, hid=self.hid, sync=True)
+
+    def spec_pages_compact(self):
+        """The pages in use moved to the lowest numbers; returns (moved, n_live)."""
+        return self._page_call(spec_pages_compact)
 
     def spec_stats(self, slot: int) -> spec_stats_t:
         s = spec_stats_t()

@@ -259,3 +259,50 @@ def test_refusals():
             f()
             pytest.fail("call %d was not refused" % i)
     _check(x, a)
+
+
+# Calls of a megabyte and more, whose tokens are counted in hash tables beside the copy.
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V,pad", [(300032, 0), (300007, 1), (300007, 2)])
+@pytest.mark.parametrize("mask", [False, True])
+def test_large_in_place_and_given_outputs(dtype, V, pad, mask):
+    x, a = _case(2, 3, V, dtype, tree=True, pad=pad, seed=13, mask=mask, hist=3000, bias=50)
+    want = _call(x, a)
+    _check(x, a, want)
+    full = torch.full((6, V + pad + 9), 3.0, dtype=x.dtype, device="cuda")
+    for at in (0, 1, 8):
+        full.fill_(3.0)
+        assert torch.equal(_call(x, a, out=full[:, at:at + V]), want)
+        assert (full[:, :at] == 3).all() and (full[:, at + V:] == 3).all()
+    for at in (0, 3):
+        full.fill_(2.0)
+        mine = full[:, at:at + V]
+        mine.copy_(x)
+        _call(mine, a, out=mine)
+        assert torch.equal(mine, want) and (full[:, :at] == 2).all() and (full[:, at + V:] == 2).all()
+
+
+@pytest.mark.parametrize("R,tree", [(64, True), (64, False), (65, False)])
+def test_large_with_many_rows(R, tree):
+    x, a = _case(1, R, 20011, "f32", tree=tree, seed=14, hist=400)
+    a["tokens"][0, 1::2] = a["tokens"][0, 0]              # the same token on many paths
+    a["history"][0, :200] = a["tokens"][0, 0]
+    _check(x, a)
+
+
+@pytest.mark.parametrize("hist", [1, 12000, 12288, 12300])
+def test_large_with_as_many_tokens_as_a_table_holds(hist):
+    V = 262144
+    x, a = _case(2, 2, V, "f32", seed=15, hist=hist, bias=0, mask=False)
+    a["history"] = (torch.arange(2 * hist, device="cuda", dtype=torch.int32) * 21 % V).view(2, hist)   # all different
+    a["hist_len"] = a["prompt_len"] = None
+    _check(x, a)
+    a["history"].zero_()                                  # all the same
+    _check(x, a)
+    nan, inf = float("nan"), float("inf")
+    a["rep"][0], a["pres"][0], a["freq"][0] = 1.0, 0.0, nan   # a sequence that leaves all out, beside one that does not
+    x[:, 7] = inf
+    x[:, 0] = nan
+    a["bias_tokens"] = torch.tensor([[5, 7, 5, -1], [0, V, 9, 9]], dtype=torch.int32, device="cuda")
+    a["bias_values"] = torch.tensor([[1.0, -inf, nan, 2.0], [3.0, 1.0, -inf, 2.0]], device="cuda")
+    _check(x, a)
