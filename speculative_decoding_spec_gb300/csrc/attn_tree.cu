@@ -56,23 +56,18 @@ __global__ void __launch_bounds__(NTHR) tree_cc_kernel(const __grid_constant__ T
   float* ks = qs + hd * ROWS;     // [hd][KLD]
   float* vs = ks + hd * KLD;      // [PAGE][hd]
   float* ps = vs + PAGE * hd;     // [PAGE][PLD]
-  const Axis axis(a, p);
   if (blockIdx.x == 0) {
     const int bad = __syncthreads_or(bad_input(a, t, NTHR));
     if (t == 0) *a.err = bad ? SPEC_ERR_CAPACITY : 0;
   }
-  const Cut cut(p, axis.total);
-  if ((int)blockIdx.x >= cut.ctas) return;
-  int x = cut.start(blockIdx.x);
-  const int x1 = cut.start(blockIdx.x + 1);
+  Walk part;
+  if (!part.begin(a, p)) return;
   const float scale2 = LOG2E / sqrtf((float)hd);
 
-  while (x < x1) {
-    const Unit n = unit_at(a, p, axis, x);
-    const int k0 = first_block(n, x), k1 = first_block(n, x1);
-    x = n.start + n.nb * n.w;
-    if (k0 >= k1) continue;
-    const Seq s = seq_of(a, n.b);
+  for (; part.pieces(a, p); part.step(a, p)) {
+    const Unit n = part.n;
+    const Seq s = part.s;
+    const int k0 = part.k0, k1 = k0 + part.N;
     const int row0 = n.u * ROWS, nrow = min(ROWS, s.rows * G - row0);
     __syncthreads();
     paths(a, n.b, s.rows, path, up, t, [] { __syncthreads(); });
@@ -243,137 +238,154 @@ SPEC_DEV void starts(const TreeArgs& a, const Plan& p, int* pre) {
   if (lane == 0) pre[a.B] = run;
 }
 
-// A warp per query row: rows of units that one CTA finished are left alone. The
-// pieces' rows are read eight at a time; LN lanes hold a row, 32 / LN pieces go
-// side by side. ALL: the CTA's eight warps share a row's pieces.
+// What a lane knows of the pieces of a unit: lane i has CTA c + i's (c + 8 i's).
+SPEC_DEV int piece_slot(const Unit& n, const Cut& cut, int c, int c1) {
+  if (c > c1) return -1;
+  const int k0 = first_block(n, cut.start(c)), k1 = first_block(n, cut.start(c + 1));
+  return k0 < k1 && k1 - k0 < n.nb ? 2 * c + (k0 == 0) : -1;
+}
+
+// Units that one CTA finished are left alone; of the others a warp joins four
+// query rows (ALL: the CTA's eight warps one row, each an eighth of its pieces). LN
+// lanes hold a row, 32 / LN pieces go side by side, ROUND of them in flight.
 template <typename QT, int LN, int NJ, bool ALL>
 __global__ void __launch_bounds__(NTHR) tree_join_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Plan p) {
+  constexpr int SIDE = 32 / LN, RW = ALL ? 1 : 4, ROUND = ALL ? 8 : 2;
   __shared__ int pre[TREE_B_MAX + 1];
   __shared__ float2 wml[8];
   __shared__ float4 wacc[ALL ? 8 : 1][32][NJ];
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, G = p.G, hd = a.hd;
-  constexpr int SIDE = 32 / LN;
   if (w == 0) starts(a, p, pre);  // (the call's inputs are not written by the kernel before this one)
   __syncthreads();
   const Cut cut(p, pre[a.B]);
   grid_dep_wait();
   if (cut.ctas == 1) return;
   const int urows = p.tpu << p.tile, sub = lane / LN, ln = lane % LN;
-  for (int row = ALL ? blockIdx.x : blockIdx.x * 8 + w; row < a.B * a.R * a.nq; row += gridDim.x * (ALL ? 1 : 8)) {
-    const int m = row / a.nq, h = row - m * a.nq, b = m / a.R, r = m - b * a.R;
+  const int groups = (a.R * G + RW - 1) / RW;  // of a (sequence, KV head) pair's rows (a group lies in one unit)
+  for (int i = ALL ? blockIdx.x : blockIdx.x * 8 + w; i < a.B * a.nkv * groups; i += gridDim.x * (ALL ? 1 : 8)) {
+    const int pair = i / groups, q0 = (i - pair * groups) * RW, b = pair / a.nkv, kvh = pair - b * a.nkv;
     const Seq s = seq_of(a, b);
-    if (r >= s.rows) continue;
-    const int kvh = h / G, q = r * G + h - kvh * G, T = tiles_of(p, s.rows), nb = blocks_of(p, s);
+    const int nrow = min(RW, s.rows * G - q0);
+    if (nrow <= 0) continue;
+    const int T = tiles_of(p, s.rows), nb = blocks_of(p, s);
     Unit n;
-    n.b = b;
-    n.kvh = kvh;
-    n.u = q / urows;
+    n.u = q0 / urows;
     n.nb = nb;
     n.w = min(p.tpu, T - n.u * p.tpu);
     n.start = pre[b] + (kvh * T + n.u * p.tpu) * nb;
     // the first and last CTA whose parts meet the unit
-    const int c0 = cut.part_of(n.start), c1 = cut.part_of(n.start + nb * n.w - 1), at = q - n.u * urows;
+    const int c0 = cut.part_of(n.start), c1 = cut.part_of(n.start + nb * n.w - 1), at = q0 - n.u * urows;
     if (c0 == c1) continue;
-    float M = -INFINITY, L = 0.f;
-    float4 acc[NJ];
+    float M[RW], L[RW];
+    float4 acc[RW][NJ];
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int r = 0; r < RW; ++r) {
+      M[r] = -INFINITY;
+      L[r] = 0.f;
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) acc[r][j] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
     bool cutup = false;
     for (int c = c0 + (ALL ? w : 0); c <= c1; c += ALL ? 256 : 32) {
-      // lane i: the piece of CTA c + i (c + 8 i), its maximum and sum
-      const int mine = c + lane * (ALL ? 8 : 1);
-      int slot = -1;
-      float2 ml = make_float2(-INFINITY, 0.f);
-      if (mine <= c1) {
-        const int k0 = first_block(n, cut.start(mine)), k1 = first_block(n, cut.start(mine + 1));
-        if (k0 < k1 && k1 - k0 < nb) {
-          slot = (2 * mine + (k0 == 0)) * urows + at;
-          ml = a.part_ml[slot];
-        }
-      }
-      const unsigned have = __ballot_sync(FULL, slot >= 0);
-      if (!have) continue;
+      const int slot = piece_slot(n, cut, c + lane * (ALL ? 8 : 1), c1);
+      if (!__any_sync(FULL, slot >= 0)) continue;
       cutup = true;
-      const float mn = fmaxf(M, warp_max(ml.x));
-      const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - mn), old = M == -INFINITY ? 0.f : ex2(M - mn);
-      M = mn;
-      L = L * old + warp_sum(f * ml.y);
+      float f[RW];
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) {
-        acc[j].x *= old; acc[j].y *= old; acc[j].z *= old; acc[j].w *= old;
+      for (int r = 0; r < RW; ++r) {
+        const float2 ml = slot >= 0 && r < nrow ? a.part_ml[(size_t)slot * urows + at + r] : make_float2(-INFINITY, 0.f);
+        const float mn = fmaxf(M[r], warp_max(ml.x));
+        f[r] = ml.x == -INFINITY ? 0.f : ex2(ml.x - mn);
+        const float old = M[r] == -INFINITY ? 0.f : ex2(M[r] - mn);
+        M[r] = mn;
+        L[r] = L[r] * old + warp_sum(f[r] * ml.y);
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          acc[r][j].x *= old; acc[r][j].y *= old; acc[r][j].z *= old; acc[r][j].w *= old;
+        }
       }
       const int last = min(32, (ALL ? (c1 - c) >> 3 : c1 - c) + 1);
-      for (int i0 = 0; i0 < last; i0 += 8 * SIDE) {
-        float4 v[8][NJ];
-        float fi[8];
+      for (int i0 = 0; i0 < last; i0 += ROUND * SIDE) {
+        float4 v[ROUND][RW][NJ];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int i = i0 + e * SIDE + sub;
-          const int si = __shfl_sync(FULL, slot, i & 31);
-          fi[e] = __shfl_sync(FULL, f, i & 31);
-          const bool in = i < last && si >= 0;
+        for (int e = 0; e < ROUND; ++e) {
+          const int k = i0 + e * SIDE + sub, si = __shfl_sync(FULL, slot, k & 31);
+          const float* src = a.part_o + ((size_t)si * urows + at) * hd;
 #pragma unroll
-          for (int j = 0; j < NJ; ++j) {
-            const int d = 4 * ln + 4 * LN * j;
-            v[e][j] = in && d < hd ? *reinterpret_cast<const float4*>(a.part_o + (size_t)si * hd + d)
-                                   : make_float4(0.f, 0.f, 0.f, 0.f);
-          }
-          if (!in) fi[e] = 0.f;
+          for (int r = 0; r < RW; ++r)
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) {
+              const int d = 4 * ln + 4 * LN * j;
+              v[e][r][j] = k < last && si >= 0 && r < nrow && d < hd ? *reinterpret_cast<const float4*>(src + r * hd + d)
+                                                                     : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
         }
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
+        for (int e = 0; e < ROUND; ++e) {
+          const int k = i0 + e * SIDE + sub;
 #pragma unroll
-          for (int j = 0; j < NJ; ++j) {
-            acc[j].x = fmaf(fi[e], v[e][j].x, acc[j].x);
-            acc[j].y = fmaf(fi[e], v[e][j].y, acc[j].y);
-            acc[j].z = fmaf(fi[e], v[e][j].z, acc[j].z);
-            acc[j].w = fmaf(fi[e], v[e][j].w, acc[j].w);
+          for (int r = 0; r < RW; ++r) {
+            const float fk = __shfl_sync(FULL, f[r], k & 31), x = k < last ? fk : 0.f;
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) {
+              acc[r][j].x = fmaf(x, v[e][r][j].x, acc[r][j].x);
+              acc[r][j].y = fmaf(x, v[e][r][j].y, acc[r][j].y);
+              acc[r][j].z = fmaf(x, v[e][r][j].z, acc[r][j].z);
+              acc[r][j].w = fmaf(x, v[e][r][j].w, acc[r][j].w);
+            }
           }
+        }
       }
     }
     if (ALL ? !__syncthreads_or(cutup) : !cutup) continue;  // one CTA had all of its blocks
 #pragma unroll
-    for (int j = 0; j < NJ; ++j)
+    for (int r = 0; r < RW; ++r)
 #pragma unroll
-      for (int o = LN; o < 32; o <<= 1) {
-        acc[j].x += __shfl_xor_sync(FULL, acc[j].x, o);
-        acc[j].y += __shfl_xor_sync(FULL, acc[j].y, o);
-        acc[j].z += __shfl_xor_sync(FULL, acc[j].z, o);
-        acc[j].w += __shfl_xor_sync(FULL, acc[j].w, o);
-      }
+      for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int o = LN; o < 32; o <<= 1) {
+          acc[r][j].x += __shfl_xor_sync(FULL, acc[r][j].x, o);
+          acc[r][j].y += __shfl_xor_sync(FULL, acc[r][j].y, o);
+          acc[r][j].z += __shfl_xor_sync(FULL, acc[r][j].z, o);
+          acc[r][j].w += __shfl_xor_sync(FULL, acc[r][j].w, o);
+        }
     if (ALL) {
-      if (lane == 0) wml[w] = make_float2(M, L);
+      if (lane == 0) wml[w] = make_float2(M[0], L[0]);
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) wacc[w][lane][j] = acc[j];
+      for (int j = 0; j < NJ; ++j) wacc[w][lane][j] = acc[0][j];
       __syncthreads();
       if (w == 0) {
-        for (int i = 0; i < 8; ++i) M = fmaxf(M, wml[i].x);
-        L = 0.f;
+        for (int k = 0; k < 8; ++k) M[0] = fmaxf(M[0], wml[k].x);
+        L[0] = 0.f;
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int i = 0; i < 8; ++i) {
-          const float f = wml[i].x == -INFINITY ? 0.f : ex2(wml[i].x - M);
-          L = fmaf(f, wml[i].y, L);
+        for (int j = 0; j < NJ; ++j) acc[0][j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k = 0; k < 8; ++k) {
+          const float f = wml[k].x == -INFINITY ? 0.f : ex2(wml[k].x - M[0]);
+          L[0] = fmaf(f, wml[k].y, L[0]);
 #pragma unroll
           for (int j = 0; j < NJ; ++j) {
-            const float4 v = wacc[i][lane][j];
-            acc[j].x = fmaf(f, v.x, acc[j].x);
-            acc[j].y = fmaf(f, v.y, acc[j].y);
-            acc[j].z = fmaf(f, v.z, acc[j].z);
-            acc[j].w = fmaf(f, v.w, acc[j].w);
+            const float4 v = wacc[k][lane][j];
+            acc[0][j].x = fmaf(f, v.x, acc[0][j].x);
+            acc[0][j].y = fmaf(f, v.y, acc[0][j].y);
+            acc[0][j].z = fmaf(f, v.z, acc[0][j].z);
+            acc[0][j].w = fmaf(f, v.w, acc[0][j].w);
           }
         }
       }
     }
-    const float inv = 1.f / L;
-    if (!ALL || w == 0)
+#pragma unroll
+    for (int r = 0; r < RW; ++r) {
+      if (r >= nrow || (ALL && w)) break;
+      const float inv = 1.f / L[r];
+      const int qr = p.row_of(q0 + r), g = q0 + r - qr * G;
 #pragma unroll
       for (int j = 0; j < NJ; ++j) {
         const int d = 4 * ln + 4 * LN * j;
         if (sub == 0 && d < hd)
-          store4((QT*)a.out + (size_t)m * a.ldo + (size_t)h * hd + d,
-                 make_float4(acc[j].x * inv, acc[j].y * inv, acc[j].z * inv, acc[j].w * inv));
+          store4((QT*)a.out + ((size_t)b * a.R + qr) * a.ldo + (size_t)(kvh * G + g) * hd + d,
+                 make_float4(acc[r][j].x * inv, acc[r][j].y * inv, acc[r][j].z * inv, acc[r][j].w * inv));
       }
+    }
     if (ALL) __syncthreads();
   }
 }
@@ -409,6 +421,7 @@ Plan cc_plan(const TreeArgs& a) {
   const int per_sm = std::max(1, std::min(4, (int)(220 * 1024 / cc_smem(a.hd, TR))));
   p.grid = num_sms() * per_sm;
   p.min_cost = 2;
+  p.units = 0;
   plan_heads(p, a);
   return p;
 }
@@ -423,6 +436,13 @@ Plan plan_of(const TreeArgs& a) {
   Plan p = tc_ok(a) ? tc_plan(a) : cc_plan(a);
   // no more CTAs than the axis can have blocks
   const long long most = axis_of(a, p);
+  const long long T = (a.R * p.G + (1 << p.tile) - 1) >> p.tile;
+  // no cuts up to 256 keys: they cost a second kernel (4 x 68 keys, fp32: XX us, YY with)
+  if ((long long)a.max_pages * PAGE <= 256) {
+    p.units = (int)((T + p.tpu - 1) / p.tpu);
+    p.grid = a.B * a.nkv * p.units;
+    return p;
+  }
   p.grid = (int)std::max<long long>(1, std::min<long long>(p.grid, (most + p.min_cost - 1) / p.min_cost));
   return p;
 }
@@ -438,7 +458,7 @@ static TreeArgs shape_args(int B, int R, int nq, int nkv, int hd, int max_pages,
   a.q_dtype = q_dtype; a.kv_dtype = kv_dtype;
   return a;
 }
-static size_t part_rows(const Plan& p) { return (size_t)2 * p.grid * p.tpu << p.tile; }
+static size_t part_rows(const Plan& p) { return p.units ? 0 : (size_t)2 * p.grid * p.tpu << p.tile; }
 
 // error word (256 bytes), maxima and sums, rows; 0 where a kernel's axis (whose
 // numbers have 32 bits, slots of rows among them) may not hold the call
@@ -480,12 +500,12 @@ int attn_tree(TreeArgs a, void* ws, cudaStream_t st) {
       r = -1;
   }
   if (r < 0) return r;
-  if (p.grid == 1) return r;  // nothing is cut
+  if (p.units || p.grid == 1) return r;  // nothing is cut
   cudaLaunchConfig_t cfg = {};
   const long long rows = (long long)a.B * a.R * a.nq;
   // few rows are cut into many pieces: a CTA a row then (84 rows of 38 pieces: XX us, a warp a row YY)
   const bool all = rows <= 4 * num_sms();
-  cfg.gridDim = dim3((unsigned)std::min<long long>(all ? rows : (rows + 7) / 8, 8ll * num_sms()));
+  cfg.gridDim = dim3((unsigned)std::min<long long>(all ? rows : (rows + 31) / 32, 8ll * num_sms()));
   cfg.blockDim = dim3(NTHR);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];

@@ -26,6 +26,7 @@ struct Plan {
   int blk, tile;             // keys a block, rows a tile: powers of two, as shifts
   int tpu, grid;             // tiles a unit (1 or 2), CTAs
   int min_cost;              // a part is not made shorter than this
+  int units;                 // > 0: no cuts, a CTA a unit, so many a KV head
   int G;                     // query heads a KV head
   uint32_t inv_g;            // ceil(2^32 / G): rows below 2^16 are divided by G with a product
   SPEC_DEV int row_of(int q) const { return G == 1 ? q : (int)__umulhi((uint32_t)q, inv_g); }
@@ -141,6 +142,66 @@ SPEC_DEV int first_block(const Unit& n, int x) {
   const int off = x - n.start;
   return off <= 0 ? 0 : min((off + n.w - 1) >> (n.w - 1), n.nb);
 }
+
+// The pieces of units in this CTA's part, one after the other.
+// Without cuts (p.units) a CTA has one unit, on an axis of its own.
+struct Walk {
+  Unit n;
+  Seq s;
+  int k0, N;                            // first block, blocks
+  int x, x1;
+  // This CTA's part; false where there is none. By a whole warp.
+  SPEC_DEV bool begin(const TreeArgs& a, const Plan& p) {
+    if (p.units) {
+      const int pair = blockIdx.x / p.units;
+      n.u = blockIdx.x - pair * p.units;
+      n.b = pair / a.nkv;
+      n.kvh = pair - n.b * a.nkv;
+      s = seq_of(a, n.b);
+      n.w = min(p.tpu, tiles_of(p, s.rows) - n.u * p.tpu);
+      n.nb = blocks_of(p, s);
+      n.start = x = 0;
+      x1 = n.nb * n.w;
+      return n.w > 0;
+    }
+    const Axis axis(a, p);
+    const Cut cut(p, axis.total);
+    if ((int)blockIdx.x >= cut.ctas || cut.total == 0) return false;
+    x = cut.start(blockIdx.x);
+    x1 = cut.start(blockIdx.x + 1);
+    n = unit_at(a, p, axis, x);
+    s = seq_of(a, n.b);
+    return true;
+  }
+  SPEC_DEV bool pieces(const TreeArgs& a, const Plan& p) {  // from unit n on: the next one with blocks here
+    for (;;) {
+      if (x >= x1) return false;
+      k0 = first_block(n, x);
+      N = first_block(n, x1) - k0;
+      if (N > 0) return true;
+      step(a, p);
+    }
+  }
+  SPEC_DEV void step(const TreeArgs& a, const Plan& p) {
+    x = n.start + n.nb * n.w;
+    n.start = x;
+    if (x >= x1) return;
+    int T = tiles_of(p, s.rows);
+    if ((n.u + 1) * p.tpu < T) {
+      ++n.u;
+    } else {
+      n.u = 0;
+      if (++n.kvh == a.nkv) {
+        n.kvh = 0;
+        do s = seq_of(a, ++n.b);        // (x < x1 <= the axis's end: there is one)
+        while (s.rows == 0);
+        T = tiles_of(p, s.rows);
+        n.nb = blocks_of(p, s);
+      }
+    }
+    n.w = min(p.tpu, T - n.u * p.tpu);
+  }
+};
 
 // Bit j of path[r]: row j is row r or an ancestor of it (rows below 64). By
 // threads 0 .. 63 of the CTA between barriers of all of them: `sync`. A parent

@@ -51,7 +51,7 @@ constexpr long long WAIT_CYCLES = 2000000000ll;  // a wait's limit: a second or 
 
 // Shared memory: small items in the first 3 KB, then the query tiles and the ring.
 struct Small {
-  uint64_t full[ST_MAX], empty[ST_MAX], sfull[2], pfull[2], odone[2], qfull, drain;
+  uint64_t full[ST_MAX], empty[ST_MAX], sfull[2], pfull[2][2], odone[2], qfull, drain;
   uint32_t tmem;
   int abort;
   unsigned long long bad;               // rows of the tree whose values are not finite
@@ -144,6 +144,25 @@ SPEC_DEV void ld32(uint32_t at, float* v) {
 #pragma unroll
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
+// The largest of 32 columns of this thread's lane (the load reduces them on its
+// way; what it loads is not looked at, and waited for in the same breath).
+SPEC_DEV float ldmax32(uint32_t at) {
+  uint32_t r[32];
+  float m;
+  asm volatile(
+      "tcgen05.ld.red.sync.aligned.32x32b.x32.max.f32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%2"
+      "7,%28,%29,%30,%31}, %32, [%33];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+        "=f"(m)
+      : "r"(at)
+      : "memory");
+  (void)r[0];
+  return m;
+}
 SPEC_DEV void st16(uint32_t at, const uint32_t* v) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(at),
@@ -206,42 +225,6 @@ SPEC_DEV void drain_phase(uint64_t* b, unsigned parity) {
   while (!mbar_try(b, parity) && clock64() - t0 < WAIT_CYCLES) {
   }
 }
-
-// The pieces of units in this CTA's part, one after the other.
-struct Walk {
-  Unit n;
-  Seq s;
-  int k0, N;                            // first block, blocks
-  int x, x1;
-  SPEC_DEV bool pieces(const TreeArgs& a, const Plan& p) {  // from unit n on: the next one with blocks here
-    for (;;) {
-      if (x >= x1) return false;
-      k0 = first_block(n, x);
-      N = first_block(n, x1) - k0;
-      if (N > 0) return true;
-      step(a, p);
-    }
-  }
-  SPEC_DEV void step(const TreeArgs& a, const Plan& p) {
-    x = n.start + n.nb * n.w;
-    n.start = x;
-    if (x >= x1) return;
-    int T = tiles_of(p, s.rows);
-    if ((n.u + 1) * p.tpu < T) {
-      ++n.u;
-    } else {
-      n.u = 0;
-      if (++n.kvh == a.nkv) {
-        n.kvh = 0;
-        do s = seq_of(a, ++n.b);        // (x < x1 <= the axis's end: there is one)
-        while (s.rows == 0);
-        T = tiles_of(p, s.rows);
-        n.nb = blocks_of(p, s);
-      }
-    }
-    n.w = min(p.tpu, T - n.u * p.tpu);
-  }
-};
 
 // Places in the ring of a piece's tiles. One tile of rows: K0 K1 V0 K2 V1 ..; two: K0 V0 K1 V1 ..
 SPEC_DEV int place_k(int n, bool pair) { return pair ? 2 * n : n < 2 ? n : 2 * n - 1; }
@@ -351,17 +334,19 @@ struct Cta {
     commit(&sm->sfull[s], go);
     commit(&sm->empty[k.s], go && last);
   }
-  SPEC_DEV void issue_pv(int s, Place v, bool first, bool last, uint32_t go) {
-    const uint64_t vd = desc_mn(sa(ring) + (uint32_t)(v.s * TILE), HALF);
-    const uint32_t pb = tmem + s * 128, ob = tmem + O_COL + s * HD;
+  SPEC_DEV void issue_pv(int s, int h, Place v, bool first, bool last, uint32_t go) {  // half h of a block's keys
+    const uint64_t vd = desc_mn(sa(ring) + (uint32_t)(v.s * TILE + h * BOX), HALF);
+    const uint32_t pb = tmem + s * 128 + h * (F32 ? 64 : 32), ob = tmem + O_COL + s * HD;
 #pragma unroll
-    for (int i = 0; i < BK / 16; ++i) {  // 16 keys: two groups of 8 rows of V, 8 columns of P
+    for (int i = 0; i < PAGE / 16; ++i) {  // 16 keys: two groups of 8 rows of V, 8 columns of P
       const uint32_t at = F32 ? pb + 32 * (i >> 1) + 8 * (i & 1) : pb + 8 * i;
       mma_ts(ob, at, vd + i * (2048 >> 4), idesc(ROWS, HD, true), i > 0 || !first, go);
       if (F32) mma_ts(ob, at + 16, vd + i * (2048 >> 4), idesc(ROWS, HD, true), 1, go);  // (the weights' rest)
     }
-    commit(&sm->odone[s], go);
-    commit(&sm->empty[v.s], go && last);
+    if (h) {
+      commit(&sm->odone[s], go);
+      commit(&sm->empty[v.s], go && last);
+    }
   }
   SPEC_DEV void products() {
     const uint32_t go = elect();
@@ -391,12 +376,18 @@ struct Cta {
           ok = ok && wait(&sm->full[kt.s], kt.ph);
         }
         if (v) {
-          ok = ok && wait(&sm->pfull[s], (round >> s) & 1);
-          round ^= 1u << s;
+          ok = ok && wait(&sm->pfull[s][0], (round >> s) & 1);
         }
         if (!ok) break;
         fence_after();
-        if (v) issue_pv(s, vt, n < 2, last, go);
+        if (v) {
+          issue_pv(s, 0, vt, n < 2, last, go);
+          ok = wait(&sm->pfull[s][1], (round >> s) & 1);
+          round ^= 1u << s;
+          if (!ok) break;
+          fence_after();
+          issue_pv(s, 1, vt, false, last, go);
+        }
         if (k) issue_s(s, pair ? s : 0, kt, last, go);
       }
       ++piece;
@@ -512,29 +503,10 @@ struct Cta {
     }
     wait_st();
   }
-  // The largest.
-  SPEC_DEV float row_max(uint32_t sb) const {
-    float mx = -INFINITY;
-#pragma unroll 1
-    for (int c = 0; c < 4; ++c) {
-      float v[32];
-      ld32(sb + 32 * c, v);
-      wait_ld();
-      float m0 = v[0], m1 = v[1], m2 = v[2], m3 = v[3];
-#pragma unroll
-      for (int e = 4; e < 32; e += 4) {
-        m0 = fmaxf(m0, v[e]);
-        m1 = fmaxf(m1, v[e + 1]);
-        m2 = fmaxf(m2, v[e + 2]);
-        m3 = fmaxf(m3, v[e + 3]);
-      }
-      mx = fmaxf(mx, fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)));
-    }
-    return mx;
-  }
   // Their weights over them, and the weights' sum. A bf16 row's sum is that of the
   // rounded weights: a rounding then moves a value's share, not the row's scale.
-  SPEC_DEV float weights(uint32_t sb, float m) const {
+  // The products of the first 64 keys start while the others' weights are made.
+  SPEC_DEV float weights(uint32_t sb, float m, int s) const {
     const float2 sc = make_float2(sh.scale2, sh.scale2), mm = make_float2(-m, -m);
     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll 1
@@ -563,8 +535,17 @@ struct Cta {
       } else {
         st16(sb + 16 * c, hi);
       }
+      if (c & 1) hand_over(s, c >> 1);
     }
     return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+  }
+
+  // Half h of this warp's weights is in tensor memory.
+  SPEC_DEV void hand_over(int s, int h) const {
+    wait_st();
+    fence_before();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&sm->pfull[s][h]);
   }
 
   SPEC_DEV void softmax() {
@@ -607,9 +588,15 @@ struct Cta {
         fence_after();
         const int key0 = (w.k0 + n) * BK;
         const bool edge = key0 + BK > w.s.len;                        // rows of the tree, or the end, in this block
+        if (edge && (!pair || s == 0)) {
+          clean_values(t0 + place_v(n, N, pair), key0);
+          fence_async();
+        }
         if (work) {
           if (edge) hide(sb, visible(path, w.s.len, key0), visible(path, w.s.len, key0 + 64));
-          float mx = row_max(sb);
+          float mx = -INFINITY;
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) mx = fmaxf(mx, ldmax32(sb + 32 * c));
           mx *= sh.scale2;
           const bool raise = mx > m + TAU || (m == -INFINITY && mx > -INFINITY);
           if (__any_sync(FULL, raise)) {
@@ -633,16 +620,11 @@ struct Cta {
             }
           }
           const float mb = m == -INFINITY ? 0.f : m;
-          l += weights(sb, mb);
-          wait_st();
+          l += weights(sb, mb, s);
+        } else {
+          hand_over(s, 0);
+          hand_over(s, 1);
         }
-        if (edge && (!pair || s == 0)) {
-          clean_values(t0 + place_v(n, N, pair), key0);
-          fence_async();
-        }
-        fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm->pfull[s]);
         ++round;
       }
       // (the other stream's rounds are known too: both streams' O are read below)
@@ -766,7 +748,8 @@ __global__ void __launch_bounds__(NTHR, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm->sfull[i], 1);
-      mbar_init(&sm->pfull[i], 4);
+      mbar_init(&sm->pfull[i][0], 4);
+      mbar_init(&sm->pfull[i][1], 4);
       mbar_init(&sm->odone[i], 1);
     }
     mbar_init(&sm->qfull, NSM / 32);
@@ -775,20 +758,12 @@ __global__ void __launch_bounds__(NTHR, 1)
     mbar_init_fence();
     asm volatile("prefetch.tensormap [%0];" ::"l"(&tm) : "memory");
   }
-  const Axis axis(a, p);                                    // (every warp for itself)
-  const Cut cut(p, axis.total);
-  const bool work = (int)blockIdx.x < cut.ctas && cut.total > 0;
-  if (work) {
-    k.w.x = cut.start(blockIdx.x);
-    k.w.x1 = cut.start(blockIdx.x + 1);
-    k.w.n = unit_at(a, p, axis, k.w.x);
-    k.w.s = seq_of(a, k.w.n.b);
-    if (warp < 4) {
-      fence_before();
-      set_up();
-      fence_after();
-      k.tmem = sm->tmem;
-    }
+  const bool work = k.w.begin(a, p);                        // (every warp for itself)
+  if (work && warp < 4) {
+    fence_before();
+    set_up();
+    fence_after();
+    k.tmem = sm->tmem;
   }
   if (blockIdx.x == 0 && warp == 2) {
     const bool bad = __any_sync(FULL, bad_input(a, lane, 32));
@@ -846,6 +821,7 @@ Plan tc_plan(const TreeArgs& a) {
   Plan p;
   p.blk = 7;
   p.tile = 7;
+  p.units = 0;
   plan_heads(p, a);
   // two tiles share a block's reads; three planes of each do not fit beside a ring
   p.tpu = a.q_dtype == DT_BF16 && a.R * (a.nq / a.nkv) > ROWS ? 2 : 1;
