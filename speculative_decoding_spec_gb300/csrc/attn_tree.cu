@@ -56,10 +56,8 @@ __global__ void __launch_bounds__(NTHR) tree_cc_kernel(const __grid_constant__ T
   float* ks = qs + hd * ROWS;     // [hd][KLD]
   float* vs = ks + hd * KLD;      // [PAGE][hd]
   float* ps = vs + PAGE * hd;     // [PAGE][PLD]
-  if (blockIdx.x == 0) {
-    const int bad = __syncthreads_or(bad_input(a, t, NTHR));
-    if (t == 0) *a.err = bad ? SPEC_ERR_CAPACITY : 0;
-  }
+  const int bad = __syncthreads_or(bad_input(a, p, t, NTHR));
+  if (t == 0) found(a, p, bad);
   Walk part;
   if (!part.begin(a, p)) return;
   const float scale2 = LOG2E / sqrtf((float)hd);
@@ -239,9 +237,9 @@ SPEC_DEV void starts(const TreeArgs& a, const Plan& p, int* pre) {
 }
 
 // What a lane knows of the pieces of a unit: lane i has CTA c + i's (c + 8 i's).
-SPEC_DEV int piece_slot(const Unit& n, const Cut& cut, int c, int c1) {
+SPEC_DEV int piece_slot(const Plan& p, const Unit& n, const Cut& cut, int c, int c1) {
   if (c > c1) return -1;
-  const int k0 = first_block(n, cut.start(c)), k1 = first_block(n, cut.start(c + 1));
+  const int k0 = first_block(p, n, cut.start(c)), k1 = first_block(p, n, cut.start(c + 1));
   return k0 < k1 && k1 - k0 < n.nb ? 2 * c + (k0 == 0) : -1;
 }
 
@@ -259,6 +257,13 @@ __global__ void __launch_bounds__(NTHR) tree_join_kernel(const __grid_constant__
   __syncthreads();
   const Cut cut(p, pre[a.B]);
   grid_dep_wait();
+  if (blockIdx.x == 0 && w == 0) {  // the call's outcome: the worst of the CTAs'
+    int worst = 0;
+    for (int c = lane; c < p.grid; c += 32) worst = max(worst, a.flags[c]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) worst = max(worst, __shfl_xor_sync(FULL, worst, o));
+    if (lane == 0) *a.err = worst;
+  }
   if (cut.ctas == 1) return;
   const int urows = p.tpu << p.tile, sub = lane / LN, ln = lane % LN;
   const int groups = (a.R * G + RW - 1) / RW;  // of a (sequence, KV head) pair's rows (a group lies in one unit)
@@ -272,9 +277,9 @@ __global__ void __launch_bounds__(NTHR) tree_join_kernel(const __grid_constant__
     n.u = q0 / urows;
     n.nb = nb;
     n.w = min(p.tpu, T - n.u * p.tpu);
-    n.start = pre[b] + (kvh * T + n.u * p.tpu) * nb;
+    n.start = pre[b] + kvh * pair_length(p, T, nb) + n.u * (nb * p.tpu + p.head);
     // the first and last CTA whose parts meet the unit
-    const int c0 = cut.part_of(n.start), c1 = cut.part_of(n.start + nb * n.w - 1), at = q0 - n.u * urows;
+    const int c0 = cut.part_of(n.start), c1 = cut.part_of(n.start + p.head + nb * n.w - 1), at = q0 - n.u * urows;
     if (c0 == c1) continue;
     float M[RW], L[RW];
     float4 acc[RW][NJ];
@@ -287,7 +292,7 @@ __global__ void __launch_bounds__(NTHR) tree_join_kernel(const __grid_constant__
     }
     bool cutup = false;
     for (int c = c0 + (ALL ? w : 0); c <= c1; c += ALL ? 256 : 32) {
-      const int slot = piece_slot(n, cut, c + lane * (ALL ? 8 : 1), c1);
+      const int slot = piece_slot(p, n, cut, c + lane * (ALL ? 8 : 1), c1);
       if (!__any_sync(FULL, slot >= 0)) continue;
       cutup = true;
       float f[RW];
@@ -419,8 +424,9 @@ Plan cc_plan(const TreeArgs& a) {
   p.tile = TR == 1 ? 4 : 6;
   p.tpu = 1;
   const int per_sm = std::max(1, std::min(4, (int)(220 * 1024 / cc_smem(a.hd, TR))));
-  p.grid = num_sms() * per_sm;
+  p.grid = std::min(1024, num_sms() * per_sm);
   p.min_cost = 2;
+  p.head = 1;
   p.units = 0;
   plan_heads(p, a);
   return p;
@@ -429,7 +435,7 @@ Plan cc_plan(const TreeArgs& a) {
 // The longest axis a call of this shape can have.
 long long axis_of(const TreeArgs& a, const Plan& p) {
   const long long T = (a.R * p.G + (1 << p.tile) - 1) >> p.tile;
-  return (long long)a.B * a.nkv * T * (((long long)a.max_pages * PAGE + (1 << p.blk) - 1) >> p.blk);
+  return (long long)a.B * a.nkv * T * ((((long long)a.max_pages * PAGE + (1 << p.blk) - 1) >> p.blk) + p.head);
 }
 
 Plan plan_of(const TreeArgs& a) {
@@ -458,9 +464,10 @@ static TreeArgs shape_args(int B, int R, int nq, int nkv, int hd, int max_pages,
   a.q_dtype = q_dtype; a.kv_dtype = kv_dtype;
   return a;
 }
+constexpr size_t HEAD_BYTES = 256 + 4 * 1024;  // (no kernel has more than 1024 CTAs where it cuts)
 static size_t part_rows(const Plan& p) { return p.units ? 0 : (size_t)2 * p.grid * p.tpu << p.tile; }
 
-// error word (256 bytes), maxima and sums, rows; 0 where a kernel's axis (whose
+// error word (256 bytes), the CTAs' words, maxima and sums, rows; 0 where a kernel's axis (whose
 // numbers have 32 bits, slots of rows among them) may not hold the call
 size_t attn_tree_bytes(int B, int R, int nq, int nkv, int hd, int max_pages) {
   size_t most = 0;
@@ -470,7 +477,7 @@ size_t attn_tree_bytes(int B, int R, int nq, int nkv, int hd, int max_pages) {
       const Plan p = plan_of(a);
       if (axis_of(a, p) + 512 > 0x7fffffffll || (long long)B * R * nq > (1ll << 30)) return 0;
       const size_t rows = part_rows(p);
-      most = std::max(most, 256 + rows * (sizeof(float2) + (size_t)hd * sizeof(float)));
+      most = std::max(most, HEAD_BYTES + rows * (sizeof(float2) + (size_t)hd * sizeof(float)));
     }
   return most;
 }
@@ -487,7 +494,8 @@ void setup_attn_tree_attributes() {
 int attn_tree(TreeArgs a, void* ws, cudaStream_t st) {
   const Plan p = plan_of(a);
   a.err = (int*)ws;
-  a.part_ml = (float2*)((char*)ws + 256);
+  a.flags = (int*)((char*)ws + 256);
+  a.part_ml = (float2*)((char*)ws + HEAD_BYTES);
   a.part_o = (float*)(a.part_ml + part_rows(p));
   int r = 1;
   if (tc_ok(a)) {
@@ -500,7 +508,7 @@ int attn_tree(TreeArgs a, void* ws, cudaStream_t st) {
       r = -1;
   }
   if (r < 0) return r;
-  if (p.units || p.grid == 1) return r;  // nothing is cut
+  if (p.units) return r;  // nothing is cut
   cudaLaunchConfig_t cfg = {};
   const long long rows = (long long)a.B * a.R * a.nq;
   // few rows are cut into many pieces: a CTA a row then (84 rows of 38 pieces: XX us, a warp a row YY)

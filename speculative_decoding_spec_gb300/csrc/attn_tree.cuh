@@ -5,9 +5,10 @@
 // KV head; query row i*G + g), in tiles of `tile` rows; `tpu` tiles make a unit,
 // which reads its KV head's blocks of `blk` keys once. The units of all
 // sequences, in order (sequence, KV head, unit), lie on one axis on which a
-// block of a unit has the length of the unit's tiles. CTA c takes the c-th of
-// `ctas` equal parts of that axis, so every CTA gets the same work whatever the
-// lengths; a part may end inside a unit, and may hold several.
+// block of a unit has the length of the unit's tiles, and a unit's beginning that of
+// `head` tiles (its queries' way in and its results' way out take as long). CTA c
+// takes the c-th of `ctas` equal parts of that axis, so every CTA gets the same work
+// whatever the lengths; a part may end inside a unit, and may hold several.
 //
 // A unit that lies in one part is finished there. Of a unit that is cut, each
 // CTA leaves its rows' sums unnormalised, with their maxima and sums, in one of
@@ -25,7 +26,7 @@ constexpr float LOG2E = 1.4426950408889634f;
 struct Plan {
   int blk, tile;             // keys a block, rows a tile: powers of two, as shifts
   int tpu, grid;             // tiles a unit (1 or 2), CTAs
-  int min_cost;              // a part is not made shorter than this
+  int min_cost, head;        // a part is not made shorter than this; length of a unit's beginning
   int units;                 // > 0: no cuts, a CTA a unit, so many a KV head
   int G;                     // query heads a KV head
   uint32_t inv_g;            // ceil(2^32 / G): rows below 2^16 are divided by G with a product
@@ -55,9 +56,11 @@ SPEC_DEV Seq seq_of(const TreeArgs& a, int b) {
 SPEC_DEV int tiles_of(const Plan& p, int rows) { return (rows * p.G + (1 << p.tile) - 1) >> p.tile; }
 SPEC_DEV int blocks_of(const Plan& p, const Seq& s) { return s.rows ? (s.len + s.rows + (1 << p.blk) - 1) >> p.blk : 0; }
 
+// A KV head's part of the axis: T tiles of nb blocks.
+SPEC_DEV int pair_length(const Plan& p, int T, int nb) { return nb * T + (T + p.tpu - 1) / p.tpu * p.head; }
 SPEC_DEV int cost_of(const TreeArgs& a, const Plan& p, int b) {
   const Seq s = seq_of(a, b);
-  return a.nkv * blocks_of(p, s) * tiles_of(p, s.rows);  // (the launcher keeps the axis below 2^31)
+  return a.nkv * pair_length(p, tiles_of(p, s.rows), blocks_of(p, s));  // (the launcher keeps the axis below 2^31)
 }
 // This lane's sequence of 32: where it ends, from the start of the first.
 SPEC_DEV int scan32(int c) {
@@ -130,16 +133,16 @@ SPEC_DEV Unit unit_at(const TreeArgs& a, const Plan& p, const Axis& axis, int x)
   const Seq s = seq_of(a, n.b);
   const int T = tiles_of(p, s.rows);
   n.nb = blocks_of(p, s);
-  const int pair = n.nb * T, off = x - start;
+  const int pair = pair_length(p, T, n.nb), unit = n.nb * p.tpu + p.head, off = x - start;
   n.kvh = off / pair;
-  n.u = (off - n.kvh * pair) / (n.nb * p.tpu);
+  n.u = (off - n.kvh * pair) / unit;
   n.w = min(p.tpu, T - n.u * p.tpu);
-  n.start = start + n.kvh * pair + n.u * n.nb * p.tpu;
+  n.start = start + n.kvh * pair + n.u * unit;
   return n;
 }
 // The blocks of unit n in [x0, x1) of the axis.
-SPEC_DEV int first_block(const Unit& n, int x) {
-  const int off = x - n.start;
+SPEC_DEV int first_block(const Plan& p, const Unit& n, int x) {
+  const int off = x - n.start - p.head;
   return off <= 0 ? 0 : min((off + n.w - 1) >> (n.w - 1), n.nb);
 }
 
@@ -161,7 +164,7 @@ struct Walk {
       n.w = min(p.tpu, tiles_of(p, s.rows) - n.u * p.tpu);
       n.nb = blocks_of(p, s);
       n.start = x = 0;
-      x1 = n.nb * n.w;
+      x1 = n.nb * n.w + p.head;
       return n.w > 0;
     }
     const Axis axis(a, p);
@@ -176,14 +179,14 @@ struct Walk {
   SPEC_DEV bool pieces(const TreeArgs& a, const Plan& p) {  // from unit n on: the next one with blocks here
     for (;;) {
       if (x >= x1) return false;
-      k0 = first_block(n, x);
-      N = first_block(n, x1) - k0;
+      k0 = first_block(p, n, x);
+      N = first_block(p, n, x1) - k0;
       if (N > 0) return true;
       step(a, p);
     }
   }
   SPEC_DEV void step(const TreeArgs& a, const Plan& p) {
-    x = n.start + n.nb * n.w;
+    x = n.start + p.head + n.nb * n.w;
     n.start = x;
     if (x >= x1) return;
     int T = tiles_of(p, s.rows);
@@ -241,25 +244,35 @@ SPEC_DEV unsigned long long visible(unsigned long long path, int len, int key0) 
   return off > -64 ? path >> -off : 0ull;
 }
 
-// What a call finds wrong, by `nthr` threads (t) of one warp or CTA: sequences
-// out of range, parents that are not earlier rows, pages that are not there.
-SPEC_DEV bool bad_input(const TreeArgs& a, int t, int nthr) {
+// What a call finds wrong: sequences out of range, parents that are not earlier
+// rows, pages that are not there. By threads 0 .. nthr - 1 (t) for the sequences
+// first, first + step, ... With cuts a CTA looks at its share of them and leaves what
+// it found, or a wait that ran out, in a word of its own, and the join gathers those;
+// without, the first CTA looks at all.
+SPEC_DEV bool bad_input(const TreeArgs& a, const Plan& p, int t, int nthr) {
   bool bad = false;
-  for (int b = 0; b < a.B; ++b) {
+  if (p.units && blockIdx.x) return false;
+  for (int b = p.units ? 0 : blockIdx.x; b < a.B; b += p.units ? 1 : gridDim.x) {
     const Seq s = seq_of(a, b);
     bad |= !s.ok;
     if (a.parents)
       for (int r = t; r < s.rows; r += nthr) {
-        const int p = a.parents[(size_t)b * a.R + r];
-        bad |= p < -1 || p >= r;
+        const int q = a.parents[(size_t)b * a.R + r];
+        bad |= q < -1 || q >= r;
       }
     const int pages = s.rows ? (s.len + s.rows + PAGE - 1) / PAGE : 0;
+#pragma unroll 4
     for (int i = t; i < pages; i += nthr) {
       const int g = a.block_table[(size_t)s.slot * a.max_pages + i];
       bad |= g < 0 || g >= a.n_pages;
     }
   }
   return bad;
+}
+// Where this CTA's findings go.
+SPEC_DEV int* findings(const TreeArgs& a, const Plan& p) { return p.units ? a.err : a.flags + blockIdx.x; }
+SPEC_DEV void found(const TreeArgs& a, const Plan& p, bool bad) {  // by one thread
+  if (!p.units || blockIdx.x == 0) *findings(a, p) = bad ? SPEC_ERR_CAPACITY : 0;
 }
 // A page id that is out of range reads page 0 (the call records it).
 SPEC_DEV int page_of(const TreeArgs& a, int slot, int i) {

@@ -244,7 +244,7 @@ struct Cta {
   uint32_t tmem;
   Walk w;
 
-  SPEC_DEV bool wait(uint64_t* b, unsigned parity) { return wait_phase(b, parity, (volatile int*)&sm->abort, a.err); }
+  SPEC_DEV bool wait(uint64_t* b, unsigned parity) { return wait_phase(b, parity, (volatile int*)&sm->abort, findings(a, p)); }
   SPEC_DEV unsigned char* stage(unsigned i) { return ring + (size_t)(i % sh.stages) * TILE; }
   SPEC_DEV unsigned parity(unsigned i) { return (i / sh.stages) & 1; }
 
@@ -765,9 +765,9 @@ __global__ void __launch_bounds__(NTHR, 1)
     fence_after();
     k.tmem = sm->tmem;
   }
-  if (blockIdx.x == 0 && warp == 2) {
-    const bool bad = __any_sync(FULL, bad_input(a, lane, 32));
-    if (lane == 0) *a.err = bad ? SPEC_ERR_CAPACITY : 0;
+  if (warp == 2) {
+    const bool bad = __any_sync(FULL, bad_input(a, p, lane, 32));
+    if (lane == 0) found(a, p, bad);
   } else if (work && warp == 0) {
     k.producer();
     __syncwarp();
@@ -821,6 +821,7 @@ Plan tc_plan(const TreeArgs& a) {
   Plan p;
   p.blk = 7;
   p.tile = 7;
+  p.head = 5;
   p.units = 0;
   plan_heads(p, a);
   // two tiles share a block's reads; three planes of each do not fit beside a ring

@@ -429,7 +429,7 @@ struct TreeArgs {
   const int32_t *seq_ids, *seq_len;
   const int32_t* parents;      // [B][R] or null (a chain)
   const int32_t* n_rows;       // [B] or null (R)
-  int* err;
+  int *err, *flags;            // the call's outcome; each CTA's
   float* part_o;               // partial rows of split units (attn_tree.cuh)
   float2* part_ml;
 };
