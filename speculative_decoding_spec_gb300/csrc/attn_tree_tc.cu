@@ -821,7 +821,9 @@ Plan tc_plan(const TreeArgs& a) {
   Plan p;
   p.blk = 7;
   p.tile = 7;
-  p.head = 5;
+  // what a unit's beginning and end cost, in tiles (8 x 64 rows, 30B-class: 114 us at 12, 120 at 5; fp32 rows, whose
+  // tiles take longer, 8 x 24: 34.6 at 12, 32 at 5)
+  p.head = a.q_dtype == DT_BF16 ? 12 : 5;
   p.units = 0;
   plan_heads(p, a);
   // two tiles share a block's reads; three planes of each do not fit beside a ring
