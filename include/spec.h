@@ -462,7 +462,7 @@ spec_status spec_accept_sampled(int32_t dtype, const void *logits, int64_t ld, i
  * int32 [B][R]) holds each row's parent row, an earlier one, or -1; NULL is a
  * chain (parent r - 1). Scores are q.k / sqrt(head_dim), sums and statistics
  * binary32; with bf16 rows the probabilities enter the products in bf16 (and
- * their sum is that of the rounded ones), with float rows to 2^-17.
+ * their sum is that of the rounded ones), with float rows as binary32.
  *  m: head_dim, n_kv_heads, kv_dtype and n_layers describe the cache.
  *  q ("device" float or bf16, q_dtype, row b*R + r at stride ldq elements, head h
  *     at column h*head_dim, already rotated) and out (the same type, stride ldo):

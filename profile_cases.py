@@ -51,6 +51,12 @@ Each summary under profiles/ names the case and the ncu command it ran.
     python profile_cases.py sample_t
         40 rows of 262144 fp32 logits at a temperature each, no filter; three
         calls.
+    python profile_cases.py branching
+        what serves drafted trees and sequences that branch, each twice:
+        attention of 8 trees of 64 bf16 rows at context 8192 and of one of 7
+        rows at 131071, the logits of 8 x 5 rows of 262144, eight slots
+        forked from one of 2037 tokens (48 layers), a pool of 160 pages (32
+        layers) compacted. At most 0.7 GB of pool each.
 
 Inputs are the seeded synthetic weights and caches of the workloads; nothing
 here checks results (the tests do).
@@ -235,12 +241,23 @@ def sample_t(w):
     torch.cuda.synchronize()
 
 
+def branching(w):
+    from perf import more_operators
+    more_operators.own = True
+    for name in ("tree_8x64_30b_bf16", "tree_1x7_e2b_131072", "adjust_8x5x262144", "fork_1to8_30b", "compact_e4b"):
+        state = more_operators.prepare(next(c for c in more_operators.listed() if c["name"] == name), 1)
+        for _ in range(2):
+            more_operators.run(state)
+        torch.cuda.synchronize()
+
+
 CASES = {"projections": projections, "projections_wide": projections_wide, "projections_30b": projections_30b,
          "layer_and_head_30b": layer_and_head_30b,
          "projections_30b_m5": projections_30b_m5, "projections_wide_q4": projections_wide_q4,
          "verify_q4b4": verify_q4b4, "draft": draft, "verify": verify, "attention_30b": attention_30b,
          "lmhead_30b": lmhead_30b, "step_30b_b8": step_30b_b8, "verify_moe": verify_moe,
-         "lora_30b": lora_30b, "sample_topp": sample_topp, "sample_t": sample_t}
+         "lora_30b": lora_30b, "sample_topp": sample_topp, "sample_t": sample_t,
+         "branching": branching}
 
 
 def main(argv):

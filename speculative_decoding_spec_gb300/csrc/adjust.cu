@@ -240,7 +240,7 @@ struct Words {
   // f(i, word) for the words of [i0, i1) that are not zero (i0 a multiple of 16): 16
   // marks a thread. Few tokens of a vocabulary occur in a text, so a pass over the
   // marks costs less than a look at every word beside its logit, where one in 32
-  // sends the whole warp through the arithmetic (64 rows of 262144: 42 us; XX).
+  // sends the whole warp through the arithmetic.
   template <class F>
   SPEC_DEV void each_word(int i0, int i1, F f) const {
     if (!use) return;
@@ -408,8 +408,8 @@ __global__ void __launch_bounds__(NTHR, 8) adjust_copy_kernel(const __grid_const
 // The table has room for every token of the history, pass and list. The loops are
 // rolled and the tokens of a CTA's share are queued before they are counted: what
 // runs once pays for its instructions (20 to 40 cycles each out of cold caches: with
-// eight tokens unrolled the kernel took 17 us, XX now), and a warp that counts for
-// one lane waits as long as for all.
+// eight tokens unrolled the kernel took 17 us for 8 x 5 rows, 15 now), and a warp that
+// counts for one lane waits as long as for all.
 constexpr int HASH_MAX = 16384;  // slots; three quarters of them at most are used
 constexpr int WTHR = 512;        // (beside the copy's registers an SM has room for one such CTA of 48 a thread)
 constexpr int SCAN = 4;          // tokens a thread and round

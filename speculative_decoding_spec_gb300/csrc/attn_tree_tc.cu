@@ -1,20 +1,23 @@
 // attn_tree_tc.cu -- attention of the rows of drafted trees on the fifth-
 // generation tensor cores: bf16 caches, head dims 64 and 128.
 //
-//   S = Q K^T       (M = 128 query rows, N = 128 keys, K = head dim)
-//   O += P V        (M = 128 query rows, N = head dim, K = 128 keys)
+//   S = Q K^T       (M = 128 query rows, N = 128 keys, 64 with float rows, K = head dim)
+//   O += P V        (M = 128 query rows, N = head dim, K = those keys)
 //
 // with P = exp(S - m) written back over S in tensor memory, where the second
 // product takes it from. A thread owns a query row (a lane of tensor memory),
-// so maxima and sums need no exchange between threads. Q is bf16, or three bf16
-// planes of a float row (exact), P bf16, or two planes (to 2^-17), K and V as
-// they lie in the cache: pages arrive by TMA in the 128-byte swizzle layout, K
+// so maxima and sums need no exchange between threads. Q and P are bf16, or three
+// bf16 planes each of float rows and their weights (all 24 bits; with two planes of
+// P, whose blocks had 128 keys, an output was off by up to 3.6e-6 instead of 1.4e-6,
+// and 8 x 24 rows took 32 us instead of 41), K and V as they lie in the cache: pages arrive by TMA in the 128-byte swizzle layout, K
 // a K-major operand, V (stored [key][dim]) an MN-major one.
 //
-// Few rows leave most of the 128 lanes idle, and may: a block of 128 keys is 64 KB
-// at head dim 128, about 2800 cycles at an SM's share of the HBM rate, while its
-// products take 1024 (2560 with planes) and its softmax about 600 a warp. Warps
-// whose lanes hold no row skip the softmax.
+// Few rows leave most of the 128 lanes idle, and may: 128 keys are 64 KB at head
+// dim 128, about 2800 cycles at an SM's share of the HBM rate, while their products
+// take 1024 cycles and their softmax 1900 in either stream (500 for the maximum, 1400
+// for the weights; 8 x 64 rows are bound by that chain: 1750 cycles a block and tile).
+// Warps whose lanes hold no row skip the softmax. With three planes the products
+// take at least 3072 and bind.
 //
 // Two streams hide the softmax behind the products: while one stream's softmax
 // runs, the tensor cores work on the other's. With one tile of query rows the
@@ -40,12 +43,11 @@ namespace spec {
 namespace tree {
 namespace {
 
-constexpr int BK = 128;                 // keys a block: two pages
 constexpr int ROWS = 128;               // query rows a tile
 constexpr int NTHR = 384, NSM = 256;    // threads; softmax threads
-constexpr int HALF = BK * 128;          // 64 dims of a tile: 128 rows of 128 bytes
-constexpr int BOX = PAGE * 128;
-constexpr int ST_MAX = 12;
+constexpr int BOX = PAGE * 128;         // 64 dims of a page: 64 rows of 128 bytes
+constexpr int ST_MAX = 16;
+constexpr int keys_of(bool f32) { return f32 ? 64 : 128; }  // keys a block: a page or two
 constexpr float TAU = 8.f;              // the running maximum is raised past a growth of 2^8
 constexpr long long WAIT_CYCLES = 2000000000ll;  // a wait's limit: a second or so
 
@@ -232,8 +234,9 @@ SPEC_DEV int place_v(int n, int N, bool pair) { return pair ? 2 * n + 1 : min(N,
 
 template <int HD, bool F32>
 struct Cta {
-  static constexpr int NH = HD / 64, TILE = NH * HALF;
-  static constexpr int QPL = F32 ? 3 : 1;
+  static constexpr int BK = keys_of(F32), PPB = BK / PAGE;
+  static constexpr int NH = HD / 64, HALF = BK * 128, TILE = NH * HALF;      // of a block's keys or values
+  static constexpr int QPL = F32 ? 3 : 1, QHALF = ROWS * 128, QTILE = NH * QHALF;  // of a tile of query rows
   static constexpr uint32_t O_COL = 256;
   const TreeArgs& a;
   const Plan& p;
@@ -254,11 +257,12 @@ struct Cta {
     unsigned char* dst = stage(i);
     const int r0 = ((page0 * 2 + plane) * a.nkv + w.n.kvh) * PAGE, r1 = ((page1 * 2 + plane) * a.nkv + w.n.kvh) * PAGE;
     // (a second page that is not there is left out: nothing in it is seen, and its values are cleared)
-    mbar_expect_tx(&sm->full[s], page1 >= 0 ? TILE : TILE / 2);
+    const bool two = PPB == 2 && page1 >= 0;
+    mbar_expect_tx(&sm->full[s], (two ? 2 : 1) * NH * BOX);
 #pragma unroll
     for (int h = 0; h < NH; ++h) {
       tma_2d(dst + h * HALF, tm, 64 * h, r0, &sm->full[s]);
-      if (page1 >= 0) tma_2d(dst + h * HALF + BOX, tm, 64 * h, r1, &sm->full[s]);
+      if (two) tma_2d(dst + h * HALF + BOX, tm, 64 * h, r1, &sm->full[s]);
     }
   }
   SPEC_DEV void producer() {
@@ -268,15 +272,16 @@ struct Cta {
     while (ok && w.pieces(a, p)) {
       const bool pair = w.n.w == 2;
       const int pages = (w.s.len + w.s.rows + PAGE - 1) / PAGE;
-      // page ids: a window of 16 blocks in the lanes of `cur`, the next one in `nxt`
+      // page ids: a window of 32 pages in the lanes of `cur`, the next one in `nxt`
+      constexpr int WIN = 32 / PPB;  // in blocks
       auto window = [&](int i) {
-        const int pg = 2 * (w.k0 + 16 * i) + lane;
+        const int pg = PPB * (w.k0 + WIN * i) + lane;
         return pg < pages ? page_of(a, w.s.slot, pg) : -1;
       };
       int win = 0, cur = window(0), nxt = window(1);
       auto tile = [&](int n, int plane, int place) {
-        const int from = n / 16 == win ? cur : nxt;
-        const int p0 = __shfl_sync(FULL, from, 2 * (n & 15)), p1 = __shfl_sync(FULL, from, 2 * (n & 15) + 1);
+        const int from = n / WIN == win ? cur : nxt;
+        const int p0 = __shfl_sync(FULL, from, PPB * (n % WIN)), p1 = __shfl_sync(FULL, from, PPB * (n % WIN) + PPB - 1);
         const unsigned i = t0 + place;
         if (lane == 0) {
           ok = i < (unsigned)sh.stages || wait(&sm->empty[i % sh.stages], parity(i) ^ 1);
@@ -288,7 +293,7 @@ struct Cta {
       tile(0, 0, 0);
       if (ok && !pair && w.N > 1) tile(1, 0, 1);
       for (int n = 0; ok && n < w.N; ++n) {
-        if (n / 16 != win) {
+        if (n / WIN != win) {
           ++win;
           cur = nxt;
           nxt = window(win + 1);
@@ -319,30 +324,29 @@ struct Cta {
     return c;
   }
   SPEC_DEV void issue_s(int s, int t, Place k, bool last, uint32_t go) {
-    uint64_t q = desc_k(sa(qt) + (uint32_t)(t * QPL * TILE));
+    uint64_t q = desc_k(sa(qt) + (uint32_t)(t * QPL * QTILE));
     const uint64_t kd = desc_k(sa(ring) + (uint32_t)(k.s * TILE));
     const uint32_t d = tmem + s * 128;
 #pragma unroll 1
     for (int pl = 0; pl < QPL; ++pl) {
 #pragma unroll
       for (int i = 0; i < HD / 16; ++i) {
-        const uint32_t off = (i >> 2) * (HALF >> 4) + 2 * (i & 3);
-        mma_ss(d, q + off, kd + off, idesc(ROWS, BK, false), i > 0 || pl > 0, go);
+        const uint32_t h = i >> 2, off = 2 * (i & 3);
+        mma_ss(d, q + h * (QHALF >> 4) + off, kd + h * (HALF >> 4) + off, idesc(ROWS, BK, false), i > 0 || pl > 0, go);
       }
-      q += TILE >> 4;
+      q += QTILE >> 4;
     }
     commit(&sm->sfull[s], go);
     commit(&sm->empty[k.s], go && last);
   }
   SPEC_DEV void issue_pv(int s, int h, Place v, bool first, bool last, uint32_t go) {  // half h of a block's keys
-    const uint64_t vd = desc_mn(sa(ring) + (uint32_t)(v.s * TILE + h * BOX), HALF);
-    const uint32_t pb = tmem + s * 128 + h * (F32 ? 64 : 32), ob = tmem + O_COL + s * HD;
+    const uint64_t vd = desc_mn(sa(ring) + (uint32_t)(v.s * TILE + h * (BK / 2) * 128), HALF);
+    const uint32_t pb = tmem + s * 128 + weights_at(h * (BK / 64)), ob = tmem + O_COL + s * HD;
 #pragma unroll
-    for (int i = 0; i < PAGE / 16; ++i) {  // 16 keys: two groups of 8 rows of V, 8 columns of P
-      const uint32_t at = F32 ? pb + 32 * (i >> 1) + 8 * (i & 1) : pb + 8 * i;
-      mma_ts(ob, at, vd + i * (2048 >> 4), idesc(ROWS, HD, true), i > 0 || !first, go);
-      if (F32) mma_ts(ob, at + 16, vd + i * (2048 >> 4), idesc(ROWS, HD, true), 1, go);  // (the weights' rest)
-    }
+    for (int i = 0; i < BK / 32; ++i)  // 16 keys: two groups of 8 rows of V, 8 columns of P
+#pragma unroll
+      for (int pl = 0; pl < QPL; ++pl)
+        mma_ts(ob, pb + 16 * pl + 8 * i, vd + i * (2048 >> 4), idesc(ROWS, HD, true), i > 0 || pl > 0 || !first, go);
     if (h) {
       commit(&sm->odone[s], go);
       commit(&sm->empty[v.s], go && last);
@@ -417,7 +421,7 @@ struct Cta {
       for (int u = 0; u < U; ++u) {
         const int r = r0 + u * STEP;
         if (r >= nrow) break;
-        unsigned char* dst = qt + (size_t)(r / ROWS) * QPL * TILE + (c >> 3) * HALF + swz(r % ROWS, (c & 7) * 16);
+        unsigned char* dst = qt + (size_t)(r / ROWS) * QPL * QTILE + (c >> 3) * QHALF + swz(r % ROWS, (c & 7) * 16);
         if (!F32) {
           *reinterpret_cast<uint4*>(dst) = v[u][0];
         } else {
@@ -433,7 +437,7 @@ struct Cta {
               f[2 * e] -= bf16lo(o[e]);
               f[2 * e + 1] -= bf16hi(o[e]);
             }
-            *reinterpret_cast<uint4*>(dst + pl * TILE) = make_uint4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint4*>(dst + pl * QTILE) = make_uint4(o[0], o[1], o[2], o[3]);
           }
         }
       }
@@ -448,7 +452,7 @@ struct Cta {
   SPEC_DEV void clean_values(unsigned i, int key0) {
     wait(&sm->full[i % sh.stages], parity(i));
     const int r = (threadIdx.x - 128) & 127, key = key0 + r, j = key - w.s.len;
-    if (j < 0) return;
+    if (j < 0 || r >= BK) return;
     uint4* row = reinterpret_cast<uint4*>(stage(i) + (size_t)r * 128);
     bool clear = j >= w.s.rows;
     if (!clear) {
@@ -483,13 +487,13 @@ struct Cta {
     return ex2(fmaf(s, sh.scale2, -M));
   }
 
-  // The loops over a block's 128 scores of this thread's row take 32 a turn and
+  // The loops over a block's scores of this thread's row take 32 a turn and
   // stay rolled: an instruction that runs once costs 20 to 40 cycles, as the caches
   // are cold at a launch.
   // Scores that the row does not see: -inf.
   SPEC_DEV void hide(uint32_t sb, unsigned long long lo, unsigned long long hi) const {
 #pragma unroll 1
-    for (int c = 0; c < 4; ++c) {
+    for (int c = 0; c < BK / 32; ++c) {
       const uint32_t b = (uint32_t)((c < 2 ? lo : hi) >> (32 * (c & 1)));
       if (__all_sync(FULL, b == ~0u)) continue;
       float v[32];
@@ -503,39 +507,41 @@ struct Cta {
     }
     wait_st();
   }
-  // Their weights over them, and the weights' sum. A bf16 row's sum is that of the
-  // rounded weights: a rounding then moves a value's share, not the row's scale.
-  // The products of the first 64 keys start while the others' weights are made.
+  // Where the weights of 32 keys lie in a stream's columns: 16 columns of two each,
+  // over scores that have been read; with float rows three times 16 (leading parts,
+  // middle ones, last ones), the first 32 keys' behind the 64 scores.
+  static SPEC_DEV uint32_t weights_at(int c) { return F32 ? (c ? 0u : 64u) : 16u * c; }
+  // The weights of the scores, and their sum. A bf16 row's are rounded to bf16, and
+  // the sum is that of the rounded ones: a rounding then moves a value's share, not
+  // the row's scale. A float row's go out as three bf16 parts each, which hold all
+  // 24 bits. The products of the first half start while the others are made.
   SPEC_DEV float weights(uint32_t sb, float m, int s) const {
     const float2 sc = make_float2(sh.scale2, sh.scale2), mm = make_float2(-m, -m);
     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll 1
-    for (int c = 0; c < 4; ++c) {
+    for (int c = 0; c < BK / 32; ++c) {
       float v[32];
       ld32(sb + 32 * c, v);
       wait_ld();
-      uint32_t hi[16], lo[16];
+      uint32_t part[QPL][16];
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
         float2 x = fma2(make_float2(v[2 * e], v[2 * e + 1]), sc, mm);
         x.x = ex2(x.x);
         x.y = ex2(x.y);
-        hi[e] = pack2(x.x, x.y);
-        const float2 r = make_float2(bf16lo(hi[e]), bf16hi(hi[e]));
-        if (F32) {
-          sum[e & 1] = add2(sum[e & 1], x);
-          lo[e] = pack2(x.x - r.x, x.y - r.y);
-        } else {
-          sum[e & 1] = add2(sum[e & 1], r);
+        if (F32) sum[e & 1] = add2(sum[e & 1], x);
+#pragma unroll
+        for (int pl = 0; pl < QPL; ++pl) {
+          part[pl][e] = pack2(x.x, x.y);
+          const float2 r = make_float2(bf16lo(part[pl][e]), bf16hi(part[pl][e]));
+          if (!F32) sum[e & 1] = add2(sum[e & 1], r);
+          x.x -= r.x;
+          x.y -= r.y;
         }
       }
-      if (F32) {
-        st16(sb + 32 * c, hi);
-        st16(sb + 32 * c + 16, lo);
-      } else {
-        st16(sb + 16 * c, hi);
-      }
-      if (c & 1) hand_over(s, c >> 1);
+#pragma unroll
+      for (int pl = 0; pl < QPL; ++pl) st16(sb + weights_at(c) + 16 * pl, part[pl]);
+      if ((c + 1) % (BK / 64) == 0) hand_over(s, c / (BK / 64));
     }
     return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
   }
@@ -596,7 +602,7 @@ struct Cta {
           if (edge) hide(sb, visible(path, w.s.len, key0), visible(path, w.s.len, key0 + 64));
           float mx = -INFINITY;
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) mx = fmaxf(mx, ldmax32(sb + 32 * c));
+          for (int c = 0; c < BK / 32; ++c) mx = fmaxf(mx, ldmax32(sb + 32 * c));
           mx *= sh.scale2;
           const bool raise = mx > m + TAU || (m == -INFINITY && mx > -INFINITY);
           if (__any_sync(FULL, raise)) {
@@ -819,10 +825,10 @@ bool tc_ok(const TreeArgs& a) {
 
 Plan tc_plan(const TreeArgs& a) {
   Plan p;
-  p.blk = 7;
+  p.blk = a.q_dtype == DT_BF16 ? 7 : 6;
   p.tile = 7;
-  // what a unit's beginning and end cost, in tiles (8 x 64 rows, 30B-class: 114 us at 12, 120 at 5; fp32 rows, whose
-  // tiles take longer, 8 x 24: 34.6 at 12, 32 at 5)
+  // what a unit's beginning and end cost, in tiles (8 x 64 rows, 30B-class: 114 us at 12, 120 at 5; fp32 rows, 8 x 24:
+  // 41 at 3, 5 and 8, 42 at 11)
   p.head = a.q_dtype == DT_BF16 ? 12 : 5;
   p.units = 0;
   plan_heads(p, a);
@@ -841,9 +847,9 @@ void tc_setup() {
 
 int tc_launch(const TreeArgs& a, const Plan& p, cudaStream_t st) {
   const bool f32 = a.q_dtype == DT_F32;
-  const int tile = a.hd * BK * 2;
+  const int tile = a.hd * keys_of(f32) * 2;
   Shape sh;
-  const size_t q = std::max((size_t)p.tpu * (f32 ? 3 : 1) * tile, (size_t)NSM * 128);  // (and a row of results a softmax thread)
+  const size_t q = std::max((size_t)p.tpu * (f32 ? 3 : 1) * ROWS * a.hd * 2, (size_t)NSM * 128);  // (and a row of results a softmax thread)
   sh.q_bytes = (int)q;
   sh.stages = std::min(ST_MAX, (int)((SMEM_MAX - SMALL - q) / tile));
   sh.scale2 = LOG2E / sqrtf((float)a.hd);
