@@ -466,8 +466,8 @@ spec_status spec_accept_sampled(int32_t dtype, const void *logits, int64_t ld, i
  *  m: head_dim, n_kv_heads, kv_dtype and n_layers describe the cache.
  *  q ("device" float or bf16, q_dtype, row b*R + r at stride ldq elements, head h
  *     at column h*head_dim, already rotated) and out (the same type, stride ldo):
- *     16-byte aligned, strides multiples of 8, at least n_q_heads * head_dim. Rows
- *     from n_rows on are left as they were.
+ *     16-byte aligned, strides multiples of 8, at least n_q_heads * head_dim, no
+ *     element in both. Rows from n_rows on are left as they were.
  *  workspace ("device", 16-byte aligned, ws_bytes >=
  *     spec_attention_tree_workspace_bytes(...)) needs no initialisation; calls
  *     sharing one must not overlap. Its first int gets the call's outcome: 0; 2
@@ -476,9 +476,10 @@ spec_status spec_accept_sampled(int32_t dtype, const void *logits, int64_t ld, i
  *     an earlier row (it counts as -1) or a page id was out of range (rows of that
  *     sequence are then undefined); 4 (SPEC_ETIMEOUT's) where a wait inside a
  *     kernel ran out: out is then undefined.
- * B <= 1024, R <= 64, head_dim a multiple of 8, at most 256. What lies behind a
- * sequence's last key, and the values of rows that a row does not see, do not
- * reach it, infinities and NaN included. */
+ * B <= 1024, R <= 64, head_dim a multiple of 8, at most 256, R * n_q_heads /
+ * n_kv_heads <= 2^16. What lies behind a sequence's last key, and the values of
+ * rows that a row does not see, do not reach it, infinities and NaN included; an
+ * infinity that it does see may leave NaN. */
 size_t spec_attention_tree_workspace_bytes(const spec_model_desc *m, int32_t B, int32_t R, int32_t n_q_heads,
                                            int32_t max_pages_per_seq);
 spec_status spec_attention_tree(const spec_model_desc *m, const spec_kv_desc *kv, int32_t layer, int32_t B,
@@ -506,8 +507,8 @@ spec_status spec_rows_keep(const spec_model_desc *m, const spec_kv_desc *kv, int
  * pages of its own (a slot cut back into a shared page is forked before it is
  * written again).
  * Every call plans on the GPU, needs no answer from the host and can be captured.
- * A call with a slot out of range or named twice, a table entry out of range, or
- * more pages to hand out than are free or fit a table changes nothing; workspace
+ * A call with a slot out of range or named twice, a table entry that it follows out
+ * of range, or more pages to hand out than are free or fit a table changes nothing; workspace
  * ("device", 16-byte aligned, ws_bytes >= spec_pages_workspace_bytes(n_pages, n),
  * no initialisation) gets in its first int 0, or 2 for such a call. n <= 1024
  * slots, n_pages <= 2^20.
@@ -523,7 +524,7 @@ spec_status spec_rows_keep(const spec_model_desc *m, const spec_kv_desc *kv, int
  *    numbers below, both in ascending order, in every layer. table_out and
  *    refs_out get the tables afterwards (they may be kv->block_table and refs);
  *    moved ("device" int32 [n_pages]) each page's new number, -1 for one that was
- *    free; n_live ("device" int32 [1]) n. */
+ *    free; n_live ("device" int32 [1]) n. Entries that name no page in use become -1. */
 size_t spec_pages_workspace_bytes(int32_t n_pages, int32_t n);
 spec_status spec_pages_reserve(const spec_kv_desc *kv, int32_t *refs, int32_t n, const int32_t *ids,
                                const int32_t *lens, void *workspace, size_t ws_bytes, void *stream);
@@ -556,8 +557,8 @@ spec_status spec_pages_compact(const spec_model_desc *m, const spec_kv_desc *kv,
  *  mask        [n_masks] rows of ceil(V / 32) words at stride ld_mask: token t is
  *              allowed where bit t % 32 of word t / 32 is set. mask_ids [B*R] picks a
  *              row's mask, -1 none; NULL: row m has mask m;
- *  status      [1] set to 2 where a length, a parent or a mask id was out of range
- *              (taken to the nearest length, as -1); else left as it was.
+ *  status      [1] set to 2 where a length, a parent or a mask id that counts was out
+ *              of range (taken to the nearest length, as -1); else left as it was.
  * Settings out of range or not finite are off. Forbidden tokens get -inf; a logit
  * of -inf stays so. */
 typedef struct {

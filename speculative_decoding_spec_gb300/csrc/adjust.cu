@@ -34,6 +34,7 @@ struct Rules {
 };
 
 SPEC_DEV float adjusted(float x, uint32_t w, const Rules& k) {
+  if (x == -INFINITY) return x;  // (also where a reward is infinite)
   if (w & (COUNT | SEEN)) {
     x = x > 0.f ? __fdiv_rn(x, k.rep) : x * k.rep;
     const uint32_t c = w & COUNT;

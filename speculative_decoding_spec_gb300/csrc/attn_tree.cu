@@ -468,8 +468,9 @@ constexpr size_t HEAD_BYTES = 256 + 4 * 1024;  // (no kernel has more than 1024 
 static size_t part_rows(const Plan& p) { return p.units ? 0 : (size_t)2 * p.grid * p.tpu << p.tile; }
 
 // error word (256 bytes), the CTAs' words, maxima and sums, rows; 0 where a kernel's axis (whose
-// numbers have 32 bits, slots of rows among them) may not hold the call
+// numbers have 32 bits, slots of rows among them) may not hold the call, or a KV head has too many rows
 size_t attn_tree_bytes(int B, int R, int nq, int nkv, int hd, int max_pages) {
+  if ((long long)R * (nq / nkv) > TREE_HEAD_ROWS_MAX) return 0;
   size_t most = 0;
   for (int q : {DT_F32, DT_BF16})
     for (int kv : {DT_F32, DT_BF16}) {

@@ -433,7 +433,7 @@ struct TreeArgs {
   float* part_o;               // partial rows of split units (attn_tree.cuh)
   float2* part_ml;
 };
-constexpr int TREE_ROWS_MAX = 64, TREE_B_MAX = 1024;
+constexpr int TREE_ROWS_MAX = 64, TREE_B_MAX = 1024, TREE_HEAD_ROWS_MAX = 1 << 16;  // (the last: query rows a KV head)
 size_t attn_tree_bytes(int B, int R, int nq, int nkv, int hd, int max_pages);
 void setup_attn_tree_attributes();
 int attn_tree(TreeArgs a, void* ws, cudaStream_t st);

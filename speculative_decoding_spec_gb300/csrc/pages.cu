@@ -81,14 +81,16 @@ SPEC_DEV bool lowest_free(const int32_t* refs, int n_pages, int need, int* list,
 
 SPEC_DEV bool page_ok(const PagesArgs& a, int p) { return p >= 0 && p < a.n_pages; }
 
-// How many pages a slot's table names (to the first entry that names none).
-// By one warp.
+// How many pages a slot's table names (to the first entry that names none); -1
+// where one of them is out of range. By one warp.
 SPEC_DEV int held(const PagesArgs& a, int slot) {
   const int lane = threadIdx.x & 31;
   for (int i0 = 0; i0 < a.max_pages; i0 += 32) {
     const int i = i0 + lane;
-    const unsigned m = __ballot_sync(FULL, i >= a.max_pages || a.table[(size_t)slot * a.max_pages + i] < 0);
-    if (m) return i0 + __ffs(m) - 1;
+    const int p = i < a.max_pages ? a.table[(size_t)slot * a.max_pages + i] : -1;
+    const unsigned end = __ballot_sync(FULL, p < 0), out = __ballot_sync(FULL, p >= a.n_pages);
+    if (out & (end ? (end & -end) - 1 : ~0u)) return -1;  // (ahead of the end)
+    if (end) return i0 + __ffs(end) - 1;
   }
   return a.max_pages;
 }
@@ -137,7 +139,7 @@ __global__ void __launch_bounds__(PT) reserve_kernel(const __grid_constant__ Pag
       const int h = held(a, a.ids[i]), len = a.lens[i];
       if ((threadIdx.x & 31) == 0) {
         have[i] = h;
-        want[i] = len < 0 || pages_for(len) > a.max_pages ? -1 : max(pages_for(len) - h, 0);
+        want[i] = h < 0 || len < 0 || pages_for(len) > a.max_pages ? -1 : max(pages_for(len) - h, 0);
       }
     }
     __syncthreads();

@@ -1135,7 +1135,7 @@ spec_status spec_attention_tree(const spec_model_desc* m, const spec_kv_desc* kv
   if (!m || !model_ok(*m) || !kv_ok(kv) || layer < 0 || layer >= m->n_layers || B <= 0 || !seq_ids || !seq_len || R <= 0 ||
       n_q_heads <= 0 || n_q_heads % m->n_kv_heads || (q_dtype != SPEC_F32 && q_dtype != SPEC_BF16) || !q || !out ||
       !workspace || !aligned16({q, out, workspace, kv->pool}) || ldq % 8 || ldo % 8 ||
-      ldq < (int64_t)n_q_heads * m->head_dim || ldo < (int64_t)n_q_heads * m->head_dim)
+      ldq < (int64_t)n_q_heads * m->head_dim || ldo < (int64_t)n_q_heads * m->head_dim || q == out)
     return SPEC_EINVAL;
   if (B > TREE_B_MAX || R > TREE_ROWS_MAX || m->head_dim % 8) return SPEC_EUNSUPPORTED;
   const size_t need = attn_tree_bytes(B, R, n_q_heads, m->n_kv_heads, m->head_dim, kv->max_pages_per_seq);

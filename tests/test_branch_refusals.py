@@ -32,7 +32,7 @@ def _md(**kw):
 
 def test_attention_tree(lib):
     def call(m=None, kv=None, **kw):
-        a = dict(layer=0, B=2, seq_ids=P, seq_len=P, R=4, nq=12, parents=P, rows=P, dt=1, q=P, ldq=1536, out=P, ldo=1536,
+        a = dict(layer=0, B=2, seq_ids=P, seq_len=P, R=4, nq=12, parents=P, rows=P, dt=1, q=P, ldq=1536, out=2 * P, ldo=1536,
                  ws=P, n=1 << 40)
         a.update(kw)
         return lib.spec_attention_tree(C.byref(m or _md()), C.byref(kv or _kv()), *a.values(), None)
@@ -117,3 +117,16 @@ def test_adjust_logits(lib):
     assert call(R=65) == EUNSUPPORTED and call(dict(parents=None), R=1025) == EUNSUPPORTED and call(B=65536) == EUNSUPPORTED
     assert call(dict(n_bias=4096)) == EUNSUPPORTED
     assert call(dict(n_history=1 << 19, ld_history=1 << 19)) == EUNSUPPORTED
+
+
+def test_attention_tree_in_place_and_wide_heads(lib):
+    """One tensor for queries and results; more query rows on a KV head than a row's number has bits for."""
+    def call(q, out, nq, R):
+        return lib.spec_attention_tree(C.byref(_md()), C.byref(_kv()), 0, 1, P, P, R, nq, P, P, 1, q, nq * 128, out, nq * 128, P,
+                                       1 << 40, None)
+    assert call(P, P, 12, 4) == EINVAL
+    for R, G in ((64, 1025), (1, (1 << 16) + 1), (33, 2000)):
+        assert call(P, 2 * P, 4 * G, R) == EUNSUPPORTED, (R, G)
+        assert lib.spec_attention_tree_workspace_bytes(C.byref(_md()), 1, R, 4 * G, 4) == 0
+    for R, G in ((64, 1024), (1, 1 << 16)):
+        assert lib.spec_attention_tree_workspace_bytes(C.byref(_md()), 1, R, 4 * G, 4) > 0

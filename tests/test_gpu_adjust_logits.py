@@ -306,3 +306,16 @@ def test_large_with_as_many_tokens_as_a_table_holds(hist):
     a["bias_tokens"] = torch.tensor([[5, 7, 5, -1], [0, V, 9, 9]], dtype=torch.int32, device="cuda")
     a["bias_values"] = torch.tensor([[1.0, -inf, nan, 2.0], [3.0, 1.0, -inf, 2.0]], device="cuda")
     _check(x, a)
+
+
+@pytest.mark.parametrize("V", [600, 300007])
+def test_forbidden_stays_forbidden_with_infinite_rewards(V):
+    """Two occurrences at a frequency of -3e38 sum to an infinite reward."""
+    x, a = _case(2, 1, V, "f32", hist=0, bias=0, mask=False, seed=12)
+    x[:, 5:9] = -float("inf")
+    a["history"] = torch.tensor([[5, 5, 6, 7], [8, 8, 8, 5]], dtype=torch.int32, device="cuda")
+    a["hist_len"] = a["prompt_len"] = None
+    a["freq"] = torch.full((2,), -3e38, device="cuda")
+    a["tokens"] = torch.tensor([[7], [20]], dtype=torch.int32, device="cuda")
+    got = _call(x, a)
+    assert (got[:, 5:9] == -float("inf")).all() and not torch.isnan(got).any()

@@ -301,3 +301,19 @@ def test_refusals():
             f()
             pytest.fail("call %d was not refused" % k)
     s.same()
+
+
+@pytest.mark.parametrize("bad", [12, 1 << 30])
+def test_reserve_follows_no_entry_out_of_range(bad):
+    s = State(6, 12, 70)
+    s.fill([0, 1], [300, 130])
+    good = int(s.table[0, 1])
+    s.g["table"][0, 1] = s.table[0, 1] = bad
+    with pytest.raises(binding.SpecError):
+        binding.spec_pages_reserve(s.cache, cu([2, 0]), cu([64, 400]), sync=True)
+    assert np.array_equal(s.g["table"].cpu().numpy(), s.table) and np.array_equal(s.g["refs"].cpu().numpy(), s.refs)
+    s.g["table"][0, 1] = s.table[0, 1] = good
+    s.g["table"][0, 40] = s.table[0, 40] = bad              # (behind the row's end: nothing follows it)
+    s.fill([2, 0], [64, 310])
+    s.g["table"][0, 40] = s.table[0, 40] = -1
+    s.same()
