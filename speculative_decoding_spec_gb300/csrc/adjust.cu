@@ -598,6 +598,8 @@ int adjust_logits(AdjustArgs a, cudaStream_t st) {
   const long long tokens = (long long)a.n_history + a.R + a.n_bias;
   const long long bytes = (long long)a.B * a.R * a.V * es;
   void* args[] = {(void*)&a};
+  // From 1 MB on two kernels: 8 x 5 rows of 262144 19.5 us (one 31.5), 64 rows 27 (38), 4 x 5 rows of 32003
+  // 7.2 (11.7), one row of 262144 5.7 (6.2). Below, the launch saved is more: a call 16 us with the host, 18.5 with two.
   if (!words || (bytes >= (1 << 20) && tokens <= HASH_MAX * 3 / 4 && a.R <= TREE_ROWS_MAX && bytes < (1ll << 40))) {
     int launched = 0;
     if (!same || a.mask) {

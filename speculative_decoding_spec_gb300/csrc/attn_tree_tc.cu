@@ -7,17 +7,22 @@
 // with P = exp(S - m) written back over S in tensor memory, where the second
 // product takes it from. A thread owns a query row (a lane of tensor memory),
 // so maxima and sums need no exchange between threads. Q and P are bf16, or three
-// bf16 planes each of float rows and their weights (all 24 bits; with two planes of
-// P, whose blocks had 128 keys, an output was off by up to 3.6e-6 instead of 1.4e-6,
-// and 8 x 24 rows took 32 us instead of 41), K and V as they lie in the cache: pages arrive by TMA in the 128-byte swizzle layout, K
-// a K-major operand, V (stored [key][dim]) an MN-major one.
+// bf16 planes each of float rows and their weights (all 24 bits), K and V as they lie
+// in the cache: pages arrive by TMA in the 128-byte swizzle layout, K a K-major
+// operand, V (stored [key][dim]) an MN-major one.
+//
+// A product cuts its sum to 24 bits, so float rows take care: their smallest parts
+// first for S, and O out of tensor memory after every 16 blocks. 8 x 24 rows (contexts
+// of 1024 to 8192) are off by 1.8e-6 relative to all outputs, 3.3e-6 without either; two planes of
+// P, in blocks of 128 keys, 3.6e-6 (32 us instead of 43; a binary32 library product
+// 1.4e-6).
 //
 // Few rows leave most of the 128 lanes idle, and may: 128 keys are 64 KB at head
 // dim 128, about 2800 cycles at an SM's share of the HBM rate, while their products
 // take 1024 cycles and their softmax 1900 in either stream (500 for the maximum, 1400
 // for the weights; 8 x 64 rows are bound by that chain: 1750 cycles a block and tile).
 // Warps whose lanes hold no row skip the softmax. With three planes the products
-// take at least 3072 and bind.
+// take 3840 and bind (those of S 48 for 64 keys, 64 for 128: the queries are read again).
 //
 // Two streams hide the softmax behind the products: while one stream's softmax
 // runs, the tensor cores work on the other's. With one tile of query rows the
@@ -237,6 +242,9 @@ struct Cta {
   static constexpr int BK = keys_of(F32), PPB = BK / PAGE;
   static constexpr int NH = HD / 64, HALF = BK * 128, TILE = NH * HALF;      // of a block's keys or values
   static constexpr int QPL = F32 ? 3 : 1, QHALF = ROWS * 128, QTILE = NH * QHALF;  // of a tile of query rows
+  // Float rows: blocks after which O leaves tensor memory and is added up in binary32 (three
+  // products cut it for 16 keys; 8 x 24 rows take 43 us, 40 with 32 blocks, 45 with 8).
+  static constexpr int RUN = 16;
   static constexpr uint32_t O_COL = 256;
   const TreeArgs& a;
   const Plan& p;
@@ -324,7 +332,8 @@ struct Cta {
     return c;
   }
   SPEC_DEV void issue_s(int s, int t, Place k, bool last, uint32_t go) {
-    uint64_t q = desc_k(sa(qt) + (uint32_t)(t * QPL * QTILE));
+    // (the last parts of float rows first: what is cut is small until the first parts come)
+    uint64_t q = desc_k(sa(qt) + (uint32_t)((t * QPL + QPL - 1) * QTILE));
     const uint64_t kd = desc_k(sa(ring) + (uint32_t)(k.s * TILE));
     const uint32_t d = tmem + s * 128;
 #pragma unroll 1
@@ -334,7 +343,7 @@ struct Cta {
         const uint32_t h = i >> 2, off = 2 * (i & 3);
         mma_ss(d, q + h * (QHALF >> 4) + off, kd + h * (HALF >> 4) + off, idesc(ROWS, BK, false), i > 0 || pl > 0, go);
       }
-      q += QTILE >> 4;
+      q -= QTILE >> 4;
     }
     commit(&sm->sfull[s], go);
     commit(&sm->empty[k.s], go && last);
@@ -385,7 +394,7 @@ struct Cta {
         if (!ok) break;
         fence_after();
         if (v) {
-          issue_pv(s, 0, vt, n < 2, last, go);
+          issue_pv(s, 0, vt, (F32 ? n % RUN : n) < 2, last, go);
           ok = wait(&sm->pfull[s][1], (round >> s) & 1);
           round ^= 1u << s;
           if (!ok) break;
@@ -587,136 +596,165 @@ struct Cta {
       const int gr = row0 + mine, qi = mine < nrow ? p.row_of(gr) : 0, g = gr - qi * G;
       unsigned long long path = 0;
       for (int q = qi; q >= 0; q = sm->up[q]) path |= 1ull << q;
-      float m = -INFINITY, l = 0.f;
-      const int n0 = pair ? 0 : s, dn = pair ? 1 : 2;
-      for (int n = n0; n < N; n += dn) {
-        wait(&sm->sfull[s], round & 1);
-        fence_after();
-        const int key0 = (w.k0 + n) * BK;
-        const bool edge = key0 + BK > w.s.len;                        // rows of the tree, or the end, in this block
-        if (edge && (!pair || s == 0)) {
-          clean_values(t0 + place_v(n, N, pair), key0);
-          fence_async();
-        }
-        if (work) {
-          if (edge) hide(sb, visible(path, w.s.len, key0), visible(path, w.s.len, key0 + 64));
-          float mx = -INFINITY;
+      float m = -INFINITY, l = 0.f, Ma = -INFINITY, La = 0.f;  // (this stream's; both, of the runs before)
+      float acc[F32 ? 2 : 1][32];                                // the runs before: this thread's share of its row
+      for (int e0 = 0, e1; e0 < N; e0 = e1) {
+        e1 = F32 ? min(N, e0 + RUN) : N;
+        const int n0 = pair ? e0 : e0 + s, dn = pair ? 1 : 2;
+        l = 0.f;
+        for (int n = n0; n < e1; n += dn) {
+          wait(&sm->sfull[s], round & 1);
+          fence_after();
+          const int key0 = (w.k0 + n) * BK;
+          const bool edge = key0 + BK > w.s.len;                        // rows of the tree, or the end, in this block
+          if (edge && (!pair || s == 0)) {
+            clean_values(t0 + place_v(n, N, pair), key0);
+            fence_async();
+          }
+          if (work) {
+            if (edge) hide(sb, visible(path, w.s.len, key0), visible(path, w.s.len, key0 + 64));
+            float mx = -INFINITY;
 #pragma unroll 1
-          for (int c = 0; c < BK / 32; ++c) mx = fmaxf(mx, ldmax32(sb + 32 * c));
-          mx *= sh.scale2;
-          const bool raise = mx > m + TAU || (m == -INFINITY && mx > -INFINITY);
-          if (__any_sync(FULL, raise)) {
-            const float f = !raise ? 1.f : m == -INFINITY ? 0.f : ex2(m - mx);
-            if (raise) m = mx;
-            l *= f;
-            if (n != n0) {
-              wait(&sm->odone[s], (round & 1) ^ 1);
-              fence_after();
+            for (int c = 0; c < BK / 32; ++c) mx = fmaxf(mx, ldmax32(sb + 32 * c));
+            mx *= sh.scale2;
+            const bool raise = mx > m + TAU || (m == -INFINITY && mx > -INFINITY);
+            if (__any_sync(FULL, raise)) {
+              const float f = !raise ? 1.f : m == -INFINITY ? 0.f : ex2(m - mx);
+              if (raise) m = mx;
+              l *= f;
+              if (n != n0) {
+                wait(&sm->odone[s], (round & 1) ^ 1);
+                fence_after();
 #pragma unroll 1
-              for (int c = 0; c < HD / 32; ++c) {
-                float v[32];
-                ld32(ob + 32 * c, v);
-                wait_ld();
-                uint32_t u[32];
+                for (int c = 0; c < HD / 32; ++c) {
+                  float v[32];
+                  ld32(ob + 32 * c, v);
+                  wait_ld();
+                  uint32_t u[32];
 #pragma unroll
-                for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(v[e] * f);
-                st16(ob + 32 * c, u);
-                st16(ob + 32 * c + 16, u + 16);
+                  for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(v[e] * f);
+                  st16(ob + 32 * c, u);
+                  st16(ob + 32 * c + 16, u + 16);
+                }
+              }
+            }
+            const float mb = m == -INFINITY ? 0.f : m;
+            l += weights(sb, mb, s);
+          } else {
+            hand_over(s, 0);
+            hand_over(s, 1);
+          }
+          ++round;
+        }
+        // (the other stream's rounds are known too: both streams' O are read below)
+        other += pair ? N : (e1 - e0 + s) / 2;
+        sm->ml[s][r] = make_float2(m, l);
+        const bool both = pair || e1 - e0 > 1, end = e1 == N;
+        wait(&sm->odone[s], (round & 1) ^ 1);
+        if (!pair && both) wait(&sm->odone[s ^ 1], (other & 1) ^ 1);
+        sm_sync();
+        fence_after();
+        if (work) {
+          const bool whole = w.k0 == 0 && N == w.n.nb;
+          float f[2] = {1.f, 1.f}, M = m, L = l;
+          if (!pair) {
+            const float2 u = sm->ml[0][r], v = sm->ml[1][r];
+            M = fmaxf(u.x, v.x);
+            f[0] = u.x == -INFINITY ? 0.f : ex2(u.x - M);
+            f[1] = v.x == -INFINITY ? 0.f : ex2(v.x - M);
+            L = f[0] * u.y + f[1] * v.y;
+          }
+          float fa = 0.f;
+          if (F32) {
+            const float top = fmaxf(Ma, M), fn = M == -INFINITY ? 0.f : ex2(M - top);
+            fa = Ma == -INFINITY ? 0.f : ex2(Ma - top);
+            f[0] *= fn;
+            f[1] *= fn;
+            La = L = fa * La + fn * L;
+            Ma = M = top;
+          }
+          const unsigned long long bad = sm->bad & path;
+          const float inv = whole && end ? 1.f / L : 1.f;
+          const int c0 = pair ? 0 : s * (HD / 64), c1 = pair ? HD / 32 : c0 + HD / 64;
+          const size_t qat = ((size_t)w.n.b * a.R + qi) * a.ldq + (size_t)(w.n.kvh * G + g) * HD;
+          const size_t oat = ((size_t)w.n.b * a.R + qi) * a.ldo + (size_t)(w.n.kvh * G + g) * HD;
+          const size_t slot = (size_t)(2 * blockIdx.x + (w.k0 == 0)) * (p.tpu << p.tile) + mine;
+          float4* stg = reinterpret_cast<float4*>(qt) + (t >> 5) * 256;
+#pragma unroll 1
+          for (int c = c0; c < c1; ++c) {
+            float v[32];
+            if (pair) {
+              ld32(ob + 32 * c, v);
+              wait_ld();
+            } else {
+              const uint32_t o0 = tmem + lanes + O_COL + 32 * c;
+              ld32(o0, v);
+              wait_ld();
+              if (both) {
+                float u[32];
+                ld32(o0 + HD, u);
+                wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) v[e] = f[0] * v[e] + f[1] * u[e];
+              } else if (F32) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) v[e] *= f[0];
+              }
+            }
+            if (F32) {
+              float* sum = acc[c - c0];
+              if (e0 > 0)
+#pragma unroll
+                for (int e = 0; e < 32; ++e) v[e] += fa * sum[e];
+              if (!end) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) sum[e] = v[e];
+                continue;
+              }
+            }
+            if (bad && mine < nrow && key_here(bad)) {
+              for (unsigned long long b = bad; b; b &= b - 1) {
+                const int j = __ffsll((long long)b) - 1;
+                if (!in_piece(j)) continue;
+                const __nv_bfloat16* val;
+                const float pr = noted(qat, j, M == -INFINITY ? 0.f : M, &val);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) v[e] = fmaf(pr, __bfloat162float(val[32 * c + e]), v[e]);
+              }
+            }
+            // through shared memory (the query tiles are done with), so that stores are whole 128-byte (64: bf16) pieces of rows
+            __syncwarp();
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              stg[lane * 8 + (e ^ (lane & 7))] = make_float4(v[4 * e] * inv, v[4 * e + 1] * inv, v[4 * e + 2] * inv, v[4 * e + 3] * inv);
+            __syncwarp();
+            const int w0 = mine & ~31;                                  // the warp's first row
+            if (F32 || !whole) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const int rr = 4 * i + (lane >> 3), e = lane & 7;
+                const float4 x = stg[rr * 8 + (e ^ (rr & 7))];
+                const size_t to = __shfl_sync(FULL, (unsigned long long)oat, rr);
+                float* dst = whole ? (float*)a.out + to : a.part_o + (slot - lane + rr) * HD;
+                if (w0 + rr < nrow) *reinterpret_cast<float4*>(dst + 32 * c + 4 * e) = x;
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int rr = 8 * i + (lane >> 2), e = 2 * (lane & 3);
+                const float4 x = stg[rr * 8 + (e ^ (rr & 7))], y = stg[rr * 8 + ((e + 1) ^ (rr & 7))];
+                const size_t to = __shfl_sync(FULL, (unsigned long long)oat, rr);
+                if (w0 + rr < nrow)
+                  *reinterpret_cast<uint4*>((__nv_bfloat16*)a.out + to + 32 * c + 4 * e) =
+                      make_uint4(pack2(x.x, x.y), pack2(x.z, x.w), pack2(y.x, y.y), pack2(y.z, y.w));
               }
             }
           }
-          const float mb = m == -INFINITY ? 0.f : m;
-          l += weights(sb, mb, s);
-        } else {
-          hand_over(s, 0);
-          hand_over(s, 1);
+          if (!whole && end && mine < nrow && (pair || s == 0)) a.part_ml[slot] = make_float2(M, L);
         }
-        ++round;
+        fence_before();
+        if (!end) sm_sync();               // (O is read: its next products may come)
       }
-      // (the other stream's rounds are known too: both streams' O are read below)
-      other += pair ? N : s == 0 ? N / 2 : (N + 1) / 2;
-      sm->ml[s][r] = make_float2(m, l);
-      const bool both = pair || N > 1;
-      wait(&sm->odone[s], (round & 1) ^ 1);
-      if (!pair && both) wait(&sm->odone[s ^ 1], (other & 1) ^ 1);
-      sm_sync();
-      fence_after();
-      if (work) {
-        const bool whole = w.k0 == 0 && N == w.n.nb;
-        float f[2] = {1.f, 1.f}, M = m, L = l;
-        if (!pair) {
-          const float2 u = sm->ml[0][r], v = sm->ml[1][r];
-          M = fmaxf(u.x, v.x);
-          f[0] = u.x == -INFINITY ? 0.f : ex2(u.x - M);
-          f[1] = v.x == -INFINITY ? 0.f : ex2(v.x - M);
-          L = f[0] * u.y + f[1] * v.y;
-        }
-        const unsigned long long bad = sm->bad & path;
-        const float inv = whole ? 1.f / L : 1.f;
-        const int c0 = pair ? 0 : s * (HD / 64), c1 = pair ? HD / 32 : c0 + HD / 64;
-        const size_t qat = ((size_t)w.n.b * a.R + qi) * a.ldq + (size_t)(w.n.kvh * G + g) * HD;
-        const size_t oat = ((size_t)w.n.b * a.R + qi) * a.ldo + (size_t)(w.n.kvh * G + g) * HD;
-        const size_t slot = (size_t)(2 * blockIdx.x + (w.k0 == 0)) * (p.tpu << p.tile) + mine;
-        float4* stg = reinterpret_cast<float4*>(qt) + (t >> 5) * 256;
-#pragma unroll 1
-        for (int c = c0; c < c1; ++c) {
-          float v[32];
-          if (pair) {
-            ld32(ob + 32 * c, v);
-            wait_ld();
-          } else {
-            const uint32_t o0 = tmem + lanes + O_COL + 32 * c;
-            ld32(o0, v);
-            wait_ld();
-            if (both) {
-              float u[32];
-              ld32(o0 + HD, u);
-              wait_ld();
-#pragma unroll
-              for (int e = 0; e < 32; ++e) v[e] = f[0] * v[e] + f[1] * u[e];
-            }
-          }
-          if (bad && mine < nrow && key_here(bad)) {
-            for (unsigned long long b = bad; b; b &= b - 1) {
-              const int j = __ffsll((long long)b) - 1;
-              if (!in_piece(j)) continue;
-              const __nv_bfloat16* val;
-              const float pr = noted(qat, j, M == -INFINITY ? 0.f : M, &val);
-#pragma unroll
-              for (int e = 0; e < 32; ++e) v[e] = fmaf(pr, __bfloat162float(val[32 * c + e]), v[e]);
-            }
-          }
-          // through shared memory (the query tiles are done with), so that stores are whole 128-byte (64: bf16) pieces of rows
-          __syncwarp();
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            stg[lane * 8 + (e ^ (lane & 7))] = make_float4(v[4 * e] * inv, v[4 * e + 1] * inv, v[4 * e + 2] * inv, v[4 * e + 3] * inv);
-          __syncwarp();
-          const int w0 = mine & ~31;                                  // the warp's first row
-          if (F32 || !whole) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int rr = 4 * i + (lane >> 3), e = lane & 7;
-              const float4 x = stg[rr * 8 + (e ^ (rr & 7))];
-              const size_t to = __shfl_sync(FULL, (unsigned long long)oat, rr);
-              float* dst = whole ? (float*)a.out + to : a.part_o + (slot - lane + rr) * HD;
-              if (w0 + rr < nrow) *reinterpret_cast<float4*>(dst + 32 * c + 4 * e) = x;
-            }
-          } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int rr = 8 * i + (lane >> 2), e = 2 * (lane & 3);
-              const float4 x = stg[rr * 8 + (e ^ (rr & 7))], y = stg[rr * 8 + ((e + 1) ^ (rr & 7))];
-              const size_t to = __shfl_sync(FULL, (unsigned long long)oat, rr);
-              if (w0 + rr < nrow)
-                *reinterpret_cast<uint4*>((__nv_bfloat16*)a.out + to + 32 * c + 4 * e) =
-                    make_uint4(pack2(x.x, x.y), pack2(x.z, x.w), pack2(y.x, y.y), pack2(y.z, y.w));
-            }
-          }
-        }
-        if (!whole && mine < nrow && (pair || s == 0)) a.part_ml[slot] = make_float2(M, L);
-      }
-      fence_before();
       t0 += 2 * N;
       w.step(a, p);
     }
@@ -828,7 +866,7 @@ Plan tc_plan(const TreeArgs& a) {
   p.blk = a.q_dtype == DT_BF16 ? 7 : 6;
   p.tile = 7;
   // what a unit's beginning and end cost, in tiles (8 x 64 rows, 30B-class: 114 us at 12, 120 at 5; fp32 rows, 8 x 24:
-  // 41 at 3, 5 and 8, 42 at 11)
+  // the same at 3, 5 and 8, 2% more at 11)
   p.head = a.q_dtype == DT_BF16 ? 12 : 5;
   p.units = 0;
   plan_heads(p, a);
