@@ -20,7 +20,9 @@
 // Few rows leave most of the 128 lanes idle, and may: 128 keys are 64 KB at head
 // dim 128, about 2800 cycles at an SM's share of the HBM rate, while their products
 // take 1024 cycles and their softmax 1900 in either stream (500 for the maximum, 1400
-// for the weights; 8 x 64 rows are bound by that chain: 1750 cycles a block and tile).
+// for the weights). 8 x 64 rows take 1750 cycles a block and tile: a product of S takes
+// 80 cycles there, 64 alone, as its operands fill shared memory's bandwidth and copies
+// arrive beside them; neither a softmax in one pass nor fewer waits changes the total.
 // Warps whose lanes hold no row skip the softmax. With three planes the products
 // take 3840 and bind (those of S 48 for 64 keys, 64 for 128: the queries are read again).
 //
