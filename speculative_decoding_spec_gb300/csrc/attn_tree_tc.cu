@@ -12,10 +12,10 @@
 // operand, V (stored [key][dim]) an MN-major one.
 //
 // A product cuts its sum to 24 bits, so float rows take care: their smallest parts
-// first for S, and O out of tensor memory after every 16 blocks. 8 x 24 rows (contexts
-// of 1024 to 8192) are off by 1.8e-6 relative to all outputs, 3.3e-6 without either; two planes of
-// P, in blocks of 128 keys, 3.6e-6 (32 us instead of 43; a binary32 library product
-// 1.4e-6).
+// first for S, and O out of tensor memory after every 8 blocks. 8 x 24 rows (contexts
+// of 1024 to 8192) are off by 1.1e-6 relative to all outputs, 3.3e-6 without either;
+// two planes of P, in blocks of 128 keys, 3.6e-6 (32 us instead of 46; a binary32
+// library product 1.4e-6).
 //
 // Few rows leave most of the 128 lanes idle, and may: 128 keys are 64 KB at head
 // dim 128, about 2800 cycles at an SM's share of the HBM rate, while their products
@@ -245,8 +245,8 @@ struct Cta {
   static constexpr int NH = HD / 64, HALF = BK * 128, TILE = NH * HALF;      // of a block's keys or values
   static constexpr int QPL = F32 ? 3 : 1, QHALF = ROWS * 128, QTILE = NH * QHALF;  // of a tile of query rows
   // Float rows: blocks after which O leaves tensor memory and is added up in binary32 (three
-  // products cut it for 16 keys; 8 x 24 rows take 43 us, 40 with 32 blocks, 45 with 8).
-  static constexpr int RUN = 16;
+  // products cut it for 16 keys; 8 x 24 rows take 45 us, 43 with 16 blocks, 40 with 32).
+  static constexpr int RUN = 8;
   static constexpr uint32_t O_COL = 256;
   const TreeArgs& a;
   const Plan& p;
