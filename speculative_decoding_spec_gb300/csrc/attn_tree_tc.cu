@@ -67,7 +67,7 @@ struct Small {
   float2 ml[2][ROWS];                   // the streams' maxima and sums
   int up[64];                           // parents
 };
-constexpr size_t SMALL = 3072, SMEM_MAX = 227 * 1024;
+constexpr size_t SMALL = 3 * 1024, SMEM_MAX = 227 * 1024;
 static_assert(sizeof(Small) <= SMALL, "");
 
 struct Shape {

@@ -320,3 +320,15 @@ def test_float_rows_over_many_blocks(hd, grow):
     c.pool[0, pages[-1], 1, :, 130001 % 64 + 1] = float("inf")     # the second row's values: seen by it and its children
     out = c.call(sync=True)
     assert torch.isinf(out[1]).all() and torch.isfinite(out[0]).all()
+
+
+@pytest.mark.parametrize("q,kv", KINDS)
+def test_a_slot_named_twice(q, kv):
+    """Two trees over one slot's cache, as many rows each: the calls only read it."""
+    c = Case(12, 4, 128, [333], 9, q, kv, seed=21)
+    ids = c.seq_ids.repeat(2)
+    par = torch.from_numpy(np.concatenate([c.parents, np.arange(-1, 8, dtype=np.int32)[None]])).cuda()
+    out = binding.spec_attention_tree(c.cache, c.layer, ids, c.seq_len, c.q.repeat(2, 1), par, sync=True)
+    c.check(out[:9])
+    c.parents = par[1:].cpu().numpy()
+    c.check(out[9:])
