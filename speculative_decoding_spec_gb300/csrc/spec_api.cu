@@ -1157,7 +1157,8 @@ spec_status spec_attention_tree(const spec_model_desc* m, const spec_kv_desc* kv
 spec_status spec_rows_keep(const spec_model_desc* m, const spec_kv_desc* kv, int32_t B, const int32_t* seq_ids,
                            const int32_t* seq_len, int32_t n, const int32_t* rows, const int32_t* n_keep,
                            void* workspace, size_t ws_bytes, void* stream) {
-  if (!m || !model_ok(*m) || !kv_ok(kv) || B <= 0 || !seq_ids || !seq_len || n <= 0 || !rows || !n_keep || !workspace)
+  if (!m || !model_ok(*m) || !kv_ok(kv) || B <= 0 || !seq_ids || !seq_len || n <= 0 || !rows || !n_keep || !workspace ||
+      !aligned16({workspace}))
     return SPEC_EINVAL;
   if (B > TREE_B_MAX || n > TREE_ROWS_MAX || !rows_copy_ok(*m, *kv)) return SPEC_EUNSUPPORTED;
   if (ws_bytes < 256) return SPEC_ECAPACITY;

@@ -130,3 +130,8 @@ def test_attention_tree_in_place_and_wide_heads(lib):
         assert lib.spec_attention_tree_workspace_bytes(C.byref(_md()), 1, R, 4 * G, 4) == 0
     for R, G in ((64, 1024), (1, 1 << 16)):
         assert lib.spec_attention_tree_workspace_bytes(C.byref(_md()), 1, R, 4 * G, 4) > 0
+
+
+def test_rows_keep_workspace_alignment(lib):
+    for ws in (P + 1, P + 2, P + 4, P + 8):
+        assert lib.spec_rows_keep(C.byref(_md()), C.byref(_kv()), 2, P, P, 4, P, P, ws, 256, None) == EINVAL
