@@ -22,7 +22,7 @@ constexpr int N_MAX = 1024;   // slots of a call
 // Workspace: [0] error word, [1] copies (-1: the call changes nothing), [2] runs, from [64]
 // on the copies (fork: source page, page, rows; compact: from, to) and, behind a
 // fork's, the pages handed out (reserve: those alone) and where runs of copies of
-// one page begin.
+// the same rows begin.
 struct Ws {
   int *err, *jobs;
 };
@@ -252,11 +252,13 @@ __global__ void __launch_bounds__(PT) fork_kernel(const __grid_constant__ PagesA
       if (a.pending) a.pending[a.ids[i]] = a.pending[a.src[i]];
     }
   }
-  // copies of one page follow each other in the list (slots forked from one
-  // source): where each such run begins
+  // copies of the same rows follow each other in the list (slots forked from one
+  // source): where each such run begins. Sources that were cut back into a page that
+  // they share may hold different numbers of its rows.
   __syncthreads();
+  const int j = 3 * threadIdx.x;
   const bool first = !bad && threadIdx.x < need &&
-                     (threadIdx.x == 0 || w.jobs[3 * threadIdx.x] != w.jobs[3 * threadIdx.x - 3]);
+                     (j == 0 || w.jobs[j] != w.jobs[j - 3] || w.jobs[j + 2] != w.jobs[j - 1]);
   int runs;
   const int run = scan(first, red, &runs);
   if (first) list[N_MAX + run] = threadIdx.x;

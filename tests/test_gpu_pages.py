@@ -317,3 +317,22 @@ def test_reserve_follows_no_entry_out_of_range(bad):
     s.fill([2, 0], [64, 310])
     s.g["table"][0, 40] = s.table[0, 40] = -1
     s.same()
+
+
+@pytest.mark.parametrize("lens", [(100, 70), (70, 100), (100, 100), (65, 127), (127, 65)])
+@pytest.mark.parametrize("shape", SHAPES[:3])
+def test_fork_of_slots_cut_back_into_one_page(shape, lens):
+    """Slots that share a last page and hold different numbers of its rows, forked in one call: each child
+    gets its own source's rows."""
+    s = State(9, 60, 6, seed=sum(lens), **shape)
+    s.fill([0], [128])
+    s.ref_fork([0], [1])
+    s.fork([0], [1], sync=True)
+    s.seq_len[[0, 1]] = lens
+    s.g["seq_len"].copy_(cu(s.seq_len))
+    binding.spec_pages_release(s.cache, cu([0, 1]), cu(lens), sync=True)
+    s.same()                                                  # (both still name the page)
+    for src, dst in (([0, 1], [2, 3]), ([1, 0], [2, 3]), ([0, 0, 1, 1, 0, 1], [2, 3, 4, 5, 6, 7])):
+        s.ref_fork(src, dst)
+        s.fork(src, dst, sync=True)
+        s.same()
