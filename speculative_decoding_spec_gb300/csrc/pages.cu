@@ -139,7 +139,8 @@ __global__ void __launch_bounds__(PT) reserve_kernel(const __grid_constant__ Pag
       const int h = held(a, a.ids[i]), len = a.lens[i];
       if ((threadIdx.x & 31) == 0) {
         have[i] = h;
-        want[i] = h < 0 || len < 0 || pages_for(len) > a.max_pages ? -1 : max(pages_for(len) - h, 0);
+        // (one page more than there are is enough to be refused: N_MAX slots' sum stays below 2^31)
+        want[i] = h < 0 || len < 0 || pages_for(len) > a.max_pages ? -1 : min(max(pages_for(len) - h, 0), a.n_pages + 1);
       }
     }
     __syncthreads();

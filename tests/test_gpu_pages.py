@@ -336,3 +336,21 @@ def test_fork_of_slots_cut_back_into_one_page(shape, lens):
         s.ref_fork(src, dst)
         s.fork(src, dst, sync=True)
         s.same()
+
+
+@pytest.mark.parametrize("slots,width", [(1024, (1 << 21) + 64), (513, 1 << 22)])
+def test_reserve_of_more_pages_than_32_bits_count(slots, width):
+    """1024 slots that want some 2^21 pages each (2^31 together), and 513 that want 2^22: refused, and nothing is written."""
+    pool = torch.zeros((1, 9, 2, 1, 64, 8), dtype=torch.bfloat16, device="cuda")
+    table = torch.full((slots, width), -1, dtype=torch.int32, device="cuda")
+    refs = torch.zeros(9, dtype=torch.int32, device="cuda")
+    table[3, 0], refs[4] = 4, 1
+    cache = binding.Cache(pool, table, refs)
+    ids = torch.arange(slots, dtype=torch.int32, device="cuda")
+    with pytest.raises(binding.SpecError) as e:
+        binding.spec_pages_reserve(cache, ids, torch.full_like(ids, width * 64 - 1), sync=True)
+    assert e.value.code == binding.SPEC_ECAPACITY
+    assert refs.tolist() == [0, 0, 0, 0, 1, 0, 0, 0, 0] and int(table[3, 0]) == 4 and int(table.amax(1).sum()) == 4 - (slots - 1)
+    binding.spec_pages_reserve(cache, ids[:4], torch.full_like(ids[:4], 65), sync=True)
+    assert table[:5, :3].tolist() == [[0, 1, -1], [2, 3, -1], [5, 6, -1], [4, 7, -1], [-1, -1, -1]]
+    assert refs.tolist() == [1] * 8 + [0]
