@@ -477,7 +477,7 @@ spec_status spec_accept_sampled(int32_t dtype, const void *logits, int64_t ld, i
  *     sequence are then undefined); 4 (SPEC_ETIMEOUT's) where a wait inside a
  *     kernel ran out: out is then undefined.
  * B <= 1024, R <= 64, head_dim a multiple of 8, at most 256, R * n_q_heads /
- * n_kv_heads <= 2^16. What lies behind a sequence's last key, and the values of
+ * n_kv_heads <= 2^16; a length with its rows is at most 2^31 - 256. What lies behind a sequence's last key, and the values of
  * rows that a row does not see, do not reach it, infinities and NaN included; an
  * infinity that it does see may leave NaN. */
 size_t spec_attention_tree_workspace_bytes(const spec_model_desc *m, int32_t B, int32_t R, int32_t n_q_heads,

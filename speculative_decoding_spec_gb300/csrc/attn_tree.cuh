@@ -49,7 +49,8 @@ SPEC_DEV Seq seq_of(const TreeArgs& a, int b) {
   s.ok = s.slot >= 0 && s.slot < a.n_slots;
   s.len = s.ok ? a.seq_len[s.slot] : 0;
   s.rows = a.n_rows ? a.n_rows[b] : a.R;
-  s.ok = s.ok && s.len >= 0 && s.rows >= 0 && s.rows <= a.R && (long long)s.len + s.rows <= (long long)a.max_pages * PAGE;
+  s.ok = s.ok && s.len >= 0 && s.rows >= 0 && s.rows <= a.R &&
+         (long long)s.len + s.rows <= min((long long)a.max_pages * PAGE, TREE_POSITIONS_MAX);
   if (!s.ok) s.rows = 0;
   return s;
 }

@@ -433,6 +433,8 @@ struct TreeArgs {
   float* part_o;               // partial rows of split units (attn_tree.cuh)
   float2* part_ml;
 };
+// Positions of a sequence: however wide its table, the numbers of the last block's keys have 32 bits.
+constexpr long long TREE_POSITIONS_MAX = (1ll << 31) - 256;
 constexpr int TREE_ROWS_MAX = 64, TREE_B_MAX = 1024, TREE_HEAD_ROWS_MAX = 1 << 16;  // (the last: query rows a KV head)
 size_t attn_tree_bytes(int B, int R, int nq, int nkv, int hd, int max_pages);
 void setup_attn_tree_attributes();

@@ -332,3 +332,23 @@ def test_a_slot_named_twice(q, kv):
     c.check(out[:9])
     c.parents = par[1:].cpu().numpy()
     c.check(out[9:])
+
+
+@pytest.mark.parametrize("q,kv", KINDS)
+@pytest.mark.parametrize("back", [0, 3, 200, 251])
+def test_lengths_next_to_the_32nd_bit(q, kv, back):
+    """A table wide enough for 2^31 positions: a length whose last blocks pass 2^31 - 256 is out of range, and the
+    sequence beside it is as it is in a table of its own width."""
+    R, nq, hd = 4, 2, 64
+    c = Case(nq, 1, hd, [100], R, q, kv, layers=1, seed=back)
+    wide = torch.full((2, (1 << 25) + 4), -1, dtype=torch.int32, device="cuda")
+    wide[0, :c.table.shape[1]] = c.table[c.seq_ids[0]]
+    wide[1] = 0
+    lens = torch.tensor([100, (1 << 31) - 1 - back], dtype=torch.int64).to(torch.int32).cuda()
+    cache, ids = binding.Cache(c.pool, wide), torch.tensor([1, 0], dtype=torch.int32, device="cuda")
+    par = torch.from_numpy(np.concatenate([c.parents, c.parents])).cuda()
+    out = torch.full((2 * R, nq * hd), 5.0, dtype=c.q.dtype, device="cuda")
+    with pytest.raises(binding.SpecError) as e:
+        binding.spec_attention_tree(cache, 0, ids, lens, c.q.repeat(2, 1), par, out=out, sync=True)
+    assert e.value.code == binding.SPEC_ECAPACITY and (out[:R] == 5).all()
+    c.check(out[R:])
