@@ -493,7 +493,7 @@ spec_status spec_attention_tree(const spec_model_desc *m, const spec_kv_desc *kv
  * lengths stay as they are. workspace ("device", 16-byte aligned, ws_bytes >=
  * 256): its first int gets 0, or 2 where a slot, a count, a row or a page was out
  * of range, rows did not ascend or a slot was named twice; such a sequence is left
- * as it was.
+ * as it was. Positions are below 2^31 - 256.
  * head_dim times the type's size a multiple of 16. B <= 1024, n <= 64. */
 spec_status spec_rows_keep(const spec_model_desc *m, const spec_kv_desc *kv, int32_t B, const int32_t *seq_ids,
                            const int32_t *seq_len, int32_t n, const int32_t *rows, const int32_t *n_keep,

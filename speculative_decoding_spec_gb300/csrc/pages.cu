@@ -399,7 +399,7 @@ SPEC_DEV bool keep_ok(const KeepArgs& a, int b, int t, int nthr) {
     ok &= r[i] >= i && (i == 0 || r[i] > r[i - 1]);
     const long long p[2] = {(long long)len + r[i], (long long)len + i};
     for (int e = 0; e < 2 && ok; ++e) {
-      ok &= p[e] < (long long)a.max_pages * PAGE;
+      ok &= p[e] < min((long long)a.max_pages * PAGE, TREE_POSITIONS_MAX);
       if (ok) {
         const int g = a.table[(size_t)slot * a.max_pages + p[e] / PAGE];
         ok &= g >= 0 && g < a.n_pages;

@@ -354,3 +354,19 @@ def test_reserve_of_more_pages_than_32_bits_count(slots, width):
     binding.spec_pages_reserve(cache, ids[:4], torch.full_like(ids[:4], 65), sync=True)
     assert table[:5, :3].tolist() == [[0, 1, -1], [2, 3, -1], [5, 6, -1], [4, 7, -1], [-1, -1, -1]]
     assert refs.tolist() == [1] * 8 + [0]
+
+
+@pytest.mark.parametrize("back", [0, 3, 64, 200])
+def test_rows_keep_next_to_the_32nd_bit(back):
+    """Rows whose positions pass 2^31 - 256, in a table wide enough for them, are out of range; the sequence beside them moves."""
+    pool = torch.randn((2, 7, 2, 1, 64, 8), device="cuda")
+    table = torch.full((2, (1 << 25) + 4), -1, dtype=torch.int32, device="cuda")
+    table[0, :3] = cu([2, 5, 1])
+    table[1, -16:] = 3
+    lens = np.array([100, (1 << 31) - 1 - back])
+    rows, want, was = [[1, 3, 30], [1, 9, 63]], pool.cpu().numpy(), table[:, -16:].clone()
+    ref.keep(want, table[:, :3].cpu().numpy(), [0], lens, [rows[0]], [3])
+    with pytest.raises(binding.SpecError) as e:
+        binding.spec_rows_keep(binding.Cache(pool, table), cu([1, 0]), cu(lens), cu(rows[::-1]), cu([3, 3]), sync=True)
+    assert e.value.code == binding.SPEC_ECAPACITY
+    assert np.array_equal(pool.cpu().numpy(), want) and torch.equal(table[:, -16:], was)
