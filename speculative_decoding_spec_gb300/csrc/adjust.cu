@@ -238,6 +238,20 @@ struct Words {
     for (int e = 0; e < V::N; ++e) f[e] = (which >> e) & 1 ? -INFINITY : V::get(v, e);
     V::pack(v, f);
   }
+  // In place: the forbidden of a row's n logits set, so that the others are neither read
+  // nor written. A warp takes g <= 32 words of the mask at a time, those w, w + 1, ...,
+  // then `step` further on; a word's tokens are a lane each.
+  template <typename T>
+  static SPEC_DEV void forbid(T* row, const uint32_t* bits, int n, int w, int step, int g) {
+    const int lane = threadIdx.x & 31, words = (n + 31) / 32;
+    for (; w < words; w += step) {
+      const uint32_t mine = lane < g && w + lane < words ? ~bits[w + lane] : 0u;
+      for (uint32_t some = __ballot_sync(FULL, mine != 0); some; some &= some - 1) {
+        const int j = __ffs(some) - 1, i = 32 * (w + j) + lane;
+        if ((__shfl_sync(FULL, mine, j) >> lane) & 1 && i < n) put(row + i, -INFINITY);
+      }
+    }
+  }
   // f(i, word) for the words of [i0, i1) that are not zero (i0 a multiple of 16): 16
   // marks a thread. Few tokens of a vocabulary occur in a text, so a pass over the
   // marks costs less than a look at every word beside its logit, where one in 32
@@ -253,14 +267,13 @@ struct Words {
       }
   }
   // Logits [i0, nc) of row r, one a thread and turn.
-  template <typename T, bool SAME>
+  template <typename T>
   SPEC_DEV void singles(int r, int i0, const uint32_t* bits) const {
     const T* src = (const T*)a.logits + (m0 + r) * a.ld + c0;
     T* dst = (T*)a.out + (m0 + r) * a.ld_out + c0;
     for (int i = i0 + threadIdx.x; i < nc; i += NTHR) {
       const uint32_t w = use ? tab[i] : 0u;
       const bool ban = bits && !((bits[i >> 5] >> (i & 31)) & 1);
-      if (SAME && !w && !ban) continue;
       float x = value(src[i]);
       if (w) x = adjusted(x, w, k);
       put(dst + i, ban ? -INFINITY : x);
@@ -303,33 +316,39 @@ __global__ void __launch_bounds__(NTHR, 4) adjust_kernel(const __grid_constant__
     const uint32_t* bits = w.mask_of(r);
     const T* src = (const T*)a.logits + (w.m0 + r) * a.ld + w.c0;
     T* dst = (T*)a.out + (w.m0 + r) * a.ld_out + w.c0;
-    for (int turn = 0; turn < (SAME && !bits ? 0 : turns); ++turn) {
+    auto change = [&](int i, uint32_t word) {
+      if (!bits || (bits[i >> 5] >> (i & 31)) & 1) put(dst + i, adjusted(value(src[i]), word, w.k));
+    };
+    if constexpr (SAME) {
+      if (bits) {  // (chunks have 32 words and more: all warps have some)
+        const int g = min(32, a.chunk / NTHR);
+        Words::forbid(dst, bits, w.nc, (t >> 5) * g, NTHR / 32 * g, g);
+      }
+      w.each_word(0, w.nc, change);
+      continue;
+    }
+    for (int turn = 0; turn < turns; ++turn) {
       uint4 v[K];
       uint32_t which[K];
 #pragma unroll
       for (int u = 0; u < K; ++u) {
         const int i = (turn * K + u) * NTHR + t;
         which[u] = bits && i < nv ? w.template banned<V::N>(bits, i * V::N) : 0u;
-        if (!SAME) v[u] = next[u];
-        else if (which[u]) v[u] = *reinterpret_cast<const uint4*>((const char*)src + (size_t)i * 16);
+        v[u] = next[u];
       }
-      if (!SAME) {
-        if (turn + 1 < turns) fetch(r, turn + 1);
-        else if (r + 1 < w.r1) fetch(r + 1, 0);
-      }
+      if (turn + 1 < turns) fetch(r, turn + 1);
+      else if (r + 1 < w.r1) fetch(r + 1, 0);
 #pragma unroll
       for (int u = 0; u < K; ++u) {
         const int i = (turn * K + u) * NTHR + t;
         if (which[u]) w.template ban<T>(v[u], which[u]);
-        if (i < nv && (!SAME || which[u])) __stcs(reinterpret_cast<uint4*>(dst) + i, v[u]);
+        if (i < nv) __stcs(reinterpret_cast<uint4*>(dst) + i, v[u]);
       }
     }
-    w.template singles<T, SAME>(r, nv * V::N, bits);
+    w.template singles<T>(r, nv * V::N, bits);
     if (nv && w.use) {
-      if (!SAME || bits) __syncthreads();  // (their copies are stored, or their neighbours with a forbidden one)
-      w.each_word(0, nv * V::N, [&](int i, uint32_t word) {
-        if (!bits || (bits[i >> 5] >> (i & 31)) & 1) put(dst + i, adjusted(value(src[i]), word, w.k));
-      });
+      __syncthreads();  // (their copies are stored)
+      w.each_word(0, nv * V::N, change);
     }
   }
   w.done();
@@ -339,7 +358,7 @@ __global__ void __launch_bounds__(NTHR, 4) adjust_kernel(const __grid_constant__
 // forbidden: lines of 256 vectors, four of them on the way in each of five CTAs an
 // SM, every CTA the same number.
 constexpr int COPY_CTAS = 5;
-template <typename T, bool VEC, bool SAME>
+template <typename T, bool VEC>
 __global__ void __launch_bounds__(NTHR, 8) adjust_copy_kernel(const __grid_constant__ AdjustArgs a) {
   using V = Vec<T>;
   constexpr int N = VEC ? V::N : 1;
@@ -365,14 +384,13 @@ __global__ void __launch_bounds__(NTHR, 8) adjust_copy_kernel(const __grid_const
         if (id >= 0 && id < a.n_masks)
           ban[u] = ~a.mask[(size_t)id * a.ld_mask + ((at[u] * N) >> 5)] >> ((at[u] * N) & 31) & ((1u << N) - 1);
       }
-      if (SAME && !ban[u]) continue;
       const char* src = (const char*)((const T*)a.logits + (size_t)row[u] * a.ld);
       if constexpr (VEC) v[u] = load_shifted(src, (long long)at[u] * 16, (int)((uintptr_t)src & 15), (long long)a.V * sizeof(T));
       else v[u].x = sizeof(T) == 4 ? reinterpret_cast<const uint32_t*>(src)[at[u]] : reinterpret_cast<const uint16_t*>(src)[at[u]];
     }
 #pragma unroll
     for (int u = 0; u < K; ++u) {
-      if (at[u] >= nv || (SAME && !ban[u])) continue;
+      if (at[u] >= nv) continue;
       T* dst = (T*)a.out + (size_t)row[u] * a.ld_out;
       if constexpr (VEC) {
         if (ban[u]) Words::ban<T>(v[u], ban[u]);
@@ -396,9 +414,29 @@ __global__ void __launch_bounds__(NTHR, 8) adjust_copy_kernel(const __grid_const
         bad |= id < -1 || id >= a.n_masks;
         ban = id >= 0 && id < a.n_masks && !((a.mask[(size_t)id * a.ld_mask + (c >> 5)] >> (c & 31)) & 1);
       }
-      if (!SAME || ban)
-        put((T*)a.out + (size_t)r * a.ld_out + c, ban ? -INFINITY : value(((const T*)a.logits)[(size_t)r * a.ld + c]));
+      put((T*)a.out + (size_t)r * a.ld_out + c, ban ? -INFINITY : value(((const T*)a.logits)[(size_t)r * a.ld + c]));
     }
+  }
+  if (a.status && bad) atomicCAS(a.status, 0, (int)SPEC_ERR_CAPACITY);
+}
+
+// In place, the first kernel sets what is forbidden and does no more: FW words of a
+// row's mask a CTA and turn. Bound by the stores, 2 or 4 bytes a lane in whole lines:
+// 40 fp32 rows of 262144 with three quarters of the tokens forbidden take 10.5 us, with a
+// hundredth 3.9; 64 bf16 rows 15.7 and 5.1 (whole vectors read, changed and written
+// back took 13.7, 9.6, 11.8 and 8.7, but touched what stays as it is).
+constexpr int FW = 16 * NTHR / 32;
+template <typename T>
+__global__ void __launch_bounds__(NTHR, 8) adjust_forbid_kernel(const __grid_constant__ AdjustArgs a) {
+  grid_dep_launch();
+  const int words = (a.V + 31) / 32, per = (words + FW - 1) / FW;
+  bool bad = false;
+  for (int l = blockIdx.x; l < per * a.B * a.R; l += gridDim.x) {
+    const int r = l / per, w0 = (l - r * per) * FW, id = a.mask_ids ? a.mask_ids[r] : r;
+    bad |= id < -1 || id >= a.n_masks;
+    if (id >= 0 && id < a.n_masks)
+      Words::forbid((T*)a.out + (size_t)r * a.ld_out + 32 * w0, a.mask + (size_t)id * a.ld_mask + w0, min(32 * FW, a.V - 32 * w0),
+                    16 * (threadIdx.x >> 5), FW, 16);
   }
   if (a.status && bad) atomicCAS(a.status, 0, (int)SPEC_ERR_CAPACITY);
 }
@@ -562,14 +600,14 @@ __global__ void __maxnreg__(48) adjust_words_kernel(const __grid_constant__ Adju
 
 template <typename T>
 const void* pick(bool vec, bool same) {
-  return vec ? (same ? (const void*)adjust_kernel<T, true, true> : (const void*)adjust_kernel<T, true, false>)
-             : (same ? (const void*)adjust_kernel<T, false, true> : (const void*)adjust_kernel<T, false, false>);
+  return same ? (const void*)adjust_kernel<T, false, true>
+              : vec ? (const void*)adjust_kernel<T, true, false> : (const void*)adjust_kernel<T, false, false>;
 }
 
 template <typename T>
 const void* pick_copy(bool vec, bool same) {
-  return vec ? (same ? (const void*)adjust_copy_kernel<T, true, true> : (const void*)adjust_copy_kernel<T, true, false>)
-             : (same ? (const void*)adjust_copy_kernel<T, false, true> : (const void*)adjust_copy_kernel<T, false, false>);
+  return same ? (const void*)adjust_forbid_kernel<T>
+              : vec ? (const void*)adjust_copy_kernel<T, true> : (const void*)adjust_copy_kernel<T, false>;
 }
 template <typename T>
 void set_up() {
@@ -603,8 +641,8 @@ int adjust_logits(AdjustArgs a, cudaStream_t st) {
   if (!words || (bytes >= (1 << 20) && tokens <= HASH_MAX * 3 / 4 && a.R <= TREE_ROWS_MAX && bytes < (1ll << 40))) {
     int launched = 0;
     if (!same || a.mask) {
-      const long long lines = (((long long)a.V / (vec ? 16 / es : 1) + NTHR - 1) / NTHR) * a.B * a.R;
-      const unsigned grid = (unsigned)std::max(1ll, std::min<long long>(lines, COPY_CTAS * num_sms()));
+      const long long lines = (same ? (a.V + 32 * FW - 1ll) / (32 * FW) : ((long long)a.V / (vec ? 16 / es : 1) + NTHR - 1) / NTHR) * a.B * a.R;
+      const unsigned grid = (unsigned)std::max(1ll, std::min<long long>(lines, (same ? 8 : COPY_CTAS) * num_sms()));
       if (cudaLaunchKernel(f32 ? pick_copy<float>(vec, same) : pick_copy<__nv_bfloat16>(vec, same), dim3(grid), dim3(NTHR), args, 0,
                            st) != cudaSuccess)
         return -1;

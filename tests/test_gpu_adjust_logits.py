@@ -319,3 +319,33 @@ def test_forbidden_stays_forbidden_with_infinite_rewards(V):
     a["tokens"] = torch.tensor([[7], [20]], dtype=torch.int32, device="cuda")
     got = _call(x, a)
     assert (got[:, 5:9] == -float("inf")).all() and not torch.isnan(got).any()
+
+
+@pytest.mark.parametrize("V", [40, 4096, 5001, 300032, 300011])
+@pytest.mark.parametrize("pen", [False, True])
+def test_in_place_leaves_what_stays(V, pen):
+    """In place, a logit that stays as it is keeps its bits beside forbidden ones: a NaN's (a rewrite gives the type's own NaN)."""
+    x, a = _case(2, 2, V, "bf16", hist=20 if pen else 0, bias=0, seed=V, mask=True)
+    a["mask_ids"] = torch.tensor([0, 1, 0, 1], dtype=torch.int32, device="cuda")
+    if not pen:
+        a["rep"] = a["pres"] = a["freq"] = a["tokens"] = None
+    full = torch.zeros((4, (V + 7) // 8 * 8 + 8), dtype=torch.bfloat16, device="cuda")    # (rows on 16-byte boundaries, and 6 bytes behind them)
+    for at in (0, 3):
+        mine = full[:, at:at + V]
+        bits = mine.view(torch.int16)
+        g = torch.Generator(device="cuda").manual_seed(V)
+        bits.copy_(torch.randint(0x7f81, 0x7fff, (4, V), generator=g, device="cuda", dtype=torch.int16))
+        was = bits.clone()
+        _call(mine, a, out=mine)
+        words = a["mask"][a["mask_ids"].long()]
+        t = torch.arange(V, device="cuda")
+        banned = ((words[:, t // 32] >> (t % 32).int()) & 1) == 0
+        said = torch.zeros((4, V + 4), dtype=torch.bool, device="cuda")
+        if pen:
+            rows = torch.arange(4, device="cuda")[:, None]
+            said[rows, a["history"].repeat_interleave(2, 0).long()] = True      # (padding: -1 and V + 3 are columns behind)
+            said[rows, a["tokens"].repeat_interleave(2, 0).long()] = True
+        said = said[:, :V]
+        assert (mine[banned] == -float("inf")).all()
+        stays = ~banned & ~said
+        assert torch.equal(bits[stays], was[stays])
