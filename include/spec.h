@@ -559,7 +559,8 @@ spec_status spec_pages_compact(const spec_model_desc *m, const spec_kv_desc *kv,
  *              allowed where bit t % 32 of word t / 32 is set. mask_ids [B*R] picks a
  *              row's mask, -1 none; NULL: row m has mask m;
  *  status      [1] set to 2 where a length, a parent or a mask id that counts was out
- *              of range (taken to the nearest length, as -1); else left as it was.
+ *              of range (taken to the nearest length, as -1); else left as it was. Lengths
+ *              and parents of a sequence whose penalties are off do not count.
  * Settings out of range or not finite are off. Forbidden tokens get -inf; a logit
  * of -inf stays so. */
 typedef struct {

@@ -136,12 +136,12 @@ struct Words {
     use = count || a.n_bias > 0;
     n_hist = a.hist_len ? a.hist_len[b] : a.n_history;
     n_prompt = a.prompt_len ? a.prompt_len[b] : 0;
-    bad = a.history && (n_hist < 0 || n_hist > a.n_history || n_prompt < 0 || n_prompt > n_hist);
+    bad = a.history && count && (n_hist < 0 || n_hist > a.n_history || n_prompt < 0 || n_prompt > n_hist);
     n_hist = min(max(n_hist, 0), a.n_history);
   }
   SPEC_DEV void check() {
     if (!a.status || blockIdx.x || blockIdx.z) return;
-    if (a.parents)
+    if (a.parents && a.tokens && count)
       for (int r = threadIdx.x; r < a.R; r += NTHR) {
         const int p = a.parents[m0 + r];
         bad |= p < -1 || p >= r;
@@ -488,7 +488,7 @@ __global__ void __maxnreg__(48) adjust_words_kernel(const __grid_constant__ Adju
   const bool count = k.rep != 1.f || k.freq != 0.f || k.pres != 0.f;
   int n = a.hist_len ? a.hist_len[b] : a.n_history;
   const int np = a.prompt_len ? a.prompt_len[b] : 0;
-  bool bad = a.history && (n < 0 || n > a.n_history || np < 0 || np > n);
+  bool bad = a.history && count && (n < 0 || n > a.n_history || np < 0 || np > n);
   n = a.history && count ? min(max(n, 0), a.n_history) : 0;
   const int R = a.tokens && count ? a.R : 0;
   for (int i = t; i < slots / 4; i += WTHR) {
@@ -501,7 +501,7 @@ __global__ void __maxnreg__(48) adjust_words_kernel(const __grid_constant__ Adju
     for (int r = t; r >= 0;) {  // (a parent that is not an earlier row counts as none)
       m |= 1ull << r;
       const int p = a.parents ? a.parents[m0 + r] : r - 1;
-      bad |= p < -1 || p >= r;
+      bad |= R > 0 && (p < -1 || p >= r);
       r = p < r ? p : -1;
     }
     path[t] = m;

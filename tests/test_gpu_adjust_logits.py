@@ -349,3 +349,29 @@ def test_in_place_leaves_what_stays(V, pen):
         assert (mine[banned] == -float("inf")).all()
         stays = ~banned & ~said
         assert torch.equal(bits[stays], was[stays])
+
+
+@pytest.mark.parametrize("V", [600, 300007])
+def test_status_of_what_does_not_count(V):
+    """A length, prompt or parent that no penalty uses is not recorded, in small calls and in large ones."""
+    x, a = _case(3, 4, V, "f32", tree=True, seed=8)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    off = dict(a, rep=None, pres=None, freq=None)
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    for key, bad in (("hist_len", i32(-1, 1 << 30, 0)), ("prompt_len", i32(-7, 0, 1 << 30)),
+                     ("parents", torch.full_like(a["parents"], 99))):
+        b = dict(off, **{key: bad})
+        assert torch.equal(_call(x, b, status=status), _call(x, off)) and status[0] == 0, key
+        ones, zeros = torch.ones(3, device="cuda"), torch.zeros(3, device="cuda")
+        b.update(rep=ones, pres=zeros, freq=zeros)            # settings that change nothing
+        assert torch.equal(_call(x, b, status=status), _call(x, off)) and status[0] == 0, key
+        b["rep"] = torch.tensor([1.0, 1.0, 1.25], device="cuda")
+        _call(x, b, status=status)                            # the last sequence's count (a prompt longer than no history too)
+        assert status[0] == 2, key
+        status.zero_()
+    b = dict(off, rep=torch.tensor([1.0, 1.0, 1.25], device="cuda"), hist_len=i32(-1, 1 << 30, int(a["hist_len"][2])))
+    assert int(a["prompt_len"][2]) > 0
+    _call(x, b, status=status)                                # the others' do not
+    assert status[0] == 0
+    b = dict(a, tokens=None, parents=torch.full_like(a["parents"], 99))
+    assert torch.equal(_call(x, b, status=status), _call(x, dict(b, parents=None))) and status[0] == 0
