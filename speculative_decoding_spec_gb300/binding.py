@@ -336,6 +336,8 @@ class _on:
     def __init__(self, dev, stream):
         self.dev, self.ctx = dev, None
         if stream is not None:
+            if stream.device.index != dev:
+                raise SpecError("stream", SPEC_EINVAL, "the stream belongs to another GPU than the tensors")
             self.ctx = torch.cuda.stream(stream)
         elif dev != _current_device():
             self.ctx = torch.cuda.device(dev)

@@ -135,3 +135,23 @@ def test_attention_tree_in_place_and_wide_heads(lib):
 def test_rows_keep_workspace_alignment(lib):
     for ws in (P + 1, P + 2, P + 4, P + 8):
         assert lib.spec_rows_keep(C.byref(_md()), C.byref(_kv()), 2, P, P, 4, P, P, ws, 256, None) == EINVAL
+
+
+def test_stream_of_another_gpu(lib):
+    """A call whose stream is not on its tensors' GPU is refused, not sent to a stream of that GPU."""
+    import types
+    import torch
+    cache = types.SimpleNamespace(dev=0)
+    other = types.SimpleNamespace(device=torch.device("cuda", 1))
+    logits = types.SimpleNamespace(get_device=lambda: 0)
+    B = binding
+    for call in (lambda: B.spec_attention_tree(cache, 0, None, None, None, stream=other),
+                 lambda: B.spec_rows_keep(cache, None, None, None, None, stream=other),
+                 lambda: B.spec_pages_reserve(cache, None, None, stream=other),
+                 lambda: B.spec_pages_release(cache, None, stream=other),
+                 lambda: B.spec_pages_fork(cache, None, None, None, stream=other),
+                 lambda: B.spec_pages_compact(cache, stream=other),
+                 lambda: B.spec_adjust_logits(logits, stream=other)):
+        with pytest.raises(B.SpecError) as e:
+            call()
+        assert e.value.code == EINVAL and "another GPU" in str(e.value)
