@@ -651,6 +651,8 @@ def spec_pages_fork(cache: Cache, seq_len: torch.Tensor, src: torch.Tensor, dst:
             return spec_pages_fork(cache, seq_len, src, dst, pending, hid, workspace, None, sync)
     n, slots, model = dst.numel(), cache.n_slots, cache.model
     s, d = _ints(fn, "src", src, n, dev), _ints(fn, "dst", dst, n, dev)
+    if s == d and n:
+        raise SpecError(fn, SPEC_EINVAL, "src and dst are one tensor")
     state = spec_state(_ints(fn, "seq_len", seq_len, slots, dev),
                        None if pending is None else _ints(fn, "pending", pending, slots, dev))
     if hid is not None:
@@ -881,6 +883,8 @@ class Engine:
         check("spec_sync", lib().spec_sync(self.ctx, self.stream.cuda_stream))
 
     def seq_ids(self, ids):
+        """The slots as a tensor on the engine's GPU: one for lists of one length, which the
+        next such call writes again."""
         return self._in("seq_ids", torch.as_tensor(ids, dtype=torch.int32))
 
     # -- the C ABI --------------------------------------------------------------
@@ -1001,7 +1005,7 @@ class Engine:
         self._page_call(spec_pages_release, seq_ids, lens, sync=True)
 
     def spec_pages_fork(self, src, dst):
-        """Slots dst continue slots src: pages, length, pending token and hidden state."""
+        """Slots dst continue slots src (two tensors): pages, length, pending token and hidden state."""
         self._page_call(spec_pages_fork, self.seq_len, src, dst, pending=self.pending, hid=self.hid, sync=True)
 
     def spec_pages_compact(self):

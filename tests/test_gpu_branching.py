@@ -196,3 +196,17 @@ print("same")
 def test_first_call_is_captured(call):
     r = subprocess.run([sys.executable, "-c", FIRST % call], cwd=ROOT, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and "same" in r.stdout, r.stdout + r.stderr
+
+
+def test_engine_buffers_of_ids():
+    """Engine.seq_ids has one buffer for lists of one length: a fork of one tensor onto itself is named as such."""
+    t = _shape("f32")
+    eng = binding.Engine(synth.make_target(t, device="cuda"), None, n_slots=3, B_max=1, rows_max=4, max_ctx=128, n_pages=6)
+    eng.spec_pages_reserve(eng.seq_ids([0]), _int([100]))
+    eng.seq_len[0] = 100
+    with pytest.raises(binding.SpecError) as e:
+        eng.spec_pages_fork(eng.seq_ids([0]), eng.seq_ids([1]))
+    assert e.value.code == binding.SPEC_EINVAL and "one tensor" in str(e.value)
+    eng.spec_pages_fork(eng.seq_ids([0]), _int([1]))
+    assert eng.seq_len.tolist() == [100, 100, 0] and int(eng.block_table[0, 0]) == int(eng.block_table[1, 0])
+    eng.close()
