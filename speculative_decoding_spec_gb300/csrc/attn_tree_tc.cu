@@ -402,6 +402,13 @@ struct Cta {
           if (!ok) break;
           fence_after();
           issue_pv(s, 1, vt, false, last, go);
+          // the next scores overwrite the weights that these products read, in other columns than
+          // they write: only products of one accumulator and shape are ordered by themselves
+          if (k) {
+            ok = wait(&sm->odone[s], ((round >> s) & 1) ^ 1);
+            if (!ok) break;
+            fence_after();
+          }
         }
         if (k) issue_s(s, pair ? s : 0, kt, last, go);
       }
