@@ -361,10 +361,10 @@ def test_error_of_float_rows(hd, seed):
     slot, so that a CTA has some 70 blocks to itself): the limits are what a part, the order or the runs would cost."""
     from tests import float_rows_ref as fr
     c = Case(8, 2, hd, [60], 4, "f32", "bf16", layers=1, seed=seed)
-    assert fr.off(_np(c.call(sync=True)), c.want()[0]) <= fr.LIMITS[64]
+    assert fr.off(_np(c.call(sync=True)), c.want()[0]) <= fr.LIMITS[64, hd]
     c = Case(4, 1, hd, [4199], 1, "f32", "bf16", layers=1, seed=seed)
     q = torch.randn((160, 4 * hd), generator=torch.Generator(device="cuda").manual_seed(seed + 1000), device="cuda") * 1.5
     out = binding.spec_attention_tree(c.cache, 0, c.seq_ids.repeat(160), c.seq_len, q, sync=True)
     pages = c.table[int(c.seq_ids[0]), : -(-4200 // 64)].long()
     k, v = (_np(c.pool[0, pages, i, 0]).reshape(-1, hd)[:4200] for i in (0, 1))
-    assert fr.off(_np(out).reshape(-1, hd), fr.exact(_np(q).reshape(-1, hd), k, v)) <= fr.LIMITS[4200]
+    assert fr.off(_np(out).reshape(-1, hd), fr.exact(_np(q).reshape(-1, hd), k, v)) <= fr.LIMITS[4200, hd]
