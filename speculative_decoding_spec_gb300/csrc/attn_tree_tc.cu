@@ -41,6 +41,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <atomic>
 #include <mutex>
 
 #include "attn_tree.cuh"
@@ -73,6 +74,7 @@ static_assert(sizeof(Small) <= SMALL, "");
 struct Shape {
   int stages, q_bytes;                  // of the ring; of the query tiles
   float scale2;
+  int wait_extra;                       // arrivals that the first weights' barrier waits for and that never come (tests)
 };
 
 SPEC_DEV void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -222,8 +224,8 @@ SPEC_DEV bool wait_phase(uint64_t* b, unsigned parity, volatile int* abort, int*
   if (mbar_try(b, parity)) return true;
   const long long t0 = clock64();
   do {
-    if (mbar_try(b, parity)) return true;
     if (*abort) return false;
+    if (mbar_try(b, parity)) return true;
   } while (clock64() - t0 < WAIT_CYCLES);
   *abort = 1;
   set_error(err, SPEC_ERR_TIMEOUT);
@@ -801,7 +803,7 @@ __global__ void __launch_bounds__(NTHR, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm->sfull[i], 1);
-      mbar_init(&sm->pfull[i][0], 4);
+      mbar_init(&sm->pfull[i][0], 4 + (i == 0 ? sh.wait_extra : 0));
       mbar_init(&sm->pfull[i][1], 4);
       mbar_init(&sm->odone[i], 1);
     }
@@ -838,6 +840,7 @@ __global__ void __launch_bounds__(NTHR, 1)
   }
 }
 
+std::atomic<int> g_wait_extra{0};
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 std::once_flag g_once;
 void init_encode() {
@@ -900,6 +903,7 @@ int tc_launch(const TreeArgs& a, const Plan& p, cudaStream_t st) {
   sh.q_bytes = (int)q;
   sh.stages = std::min(ST_MAX, (int)((SMEM_MAX - SMALL - q) / tile));
   sh.scale2 = LOG2E / sqrtf((float)a.hd);
+  sh.wait_extra = g_wait_extra;
   CUtensorMap tm;
   if (!encode(&tm, a)) return -1;
   void* args[] = {(void*)&a, (void*)&p, (void*)&sh, (void*)&tm};
@@ -911,3 +915,7 @@ int tc_launch(const TreeArgs& a, const Plan& p, cudaStream_t st) {
 
 }  // namespace tree
 }  // namespace spec
+
+// For failure-detection tests only, and in no header: with 1, a wait of the next
+// launches runs out after about a second.
+extern "C" void spec_test_attention_tree_wait(int32_t extra) { spec::tree::g_wait_extra = extra > 0 ? 1 : 0; }

@@ -10,6 +10,8 @@ largest sum |q k| / sqrt(hd) of the row:
  - float rows on a bf16 cache: probabilities to 2^-16 (two bf16 planes): 2 * 2^-16 A;
  - bf16 rows: probabilities rounded to bf16 (2^-8) in both sums, 2 * 2^-8 A, and
    the result's rounding 2^-8 |o|."""
+import ctypes as C
+
 import numpy as np
 import pytest
 import torch
@@ -368,3 +370,24 @@ def test_error_of_float_rows(hd, seed):
     pages = c.table[int(c.seq_ids[0]), : -(-4200 // 64)].long()
     k, v = (_np(c.pool[0, pages, i, 0]).reshape(-1, hd)[:4200] for i in (0, 1))
     assert fr.off(_np(out).reshape(-1, hd), fr.exact(_np(q).reshape(-1, hd), k, v)) <= fr.LIMITS[4200, hd]
+
+
+@pytest.mark.parametrize("q", ["f32", "bf16"])
+@pytest.mark.parametrize("lens,R", [([100, 30], 5), ([60], 1), ([700, 1500, 40], 24)])
+def test_a_wait_that_runs_out(q, lens, R):
+    """Every CTA waits for weights that are never handed over: the call gives up after about a second, records the
+    timeout (in tables without cuts and with them) and returns, and the next call in the same workspace is right."""
+    c = Case(20, 4, 128, lens, R, q, "bf16")
+    ws = torch.full((1 << 26,), 0xAB, dtype=torch.uint8, device="cuda")
+    wait = binding.lib().spec_test_attention_tree_wait
+    wait.argtypes, wait.restype = [C.c_int32], None
+    want = c.call(workspace=ws, sync=True)
+    for _ in range(2):
+        wait(1)
+        try:
+            with pytest.raises(binding.SpecError) as e:
+                c.call(workspace=ws, sync=True)
+        finally:
+            wait(0)
+        assert e.value.code == binding.SPEC_ETIMEOUT and int(ws[:4].view(torch.int32)) == 4
+        assert torch.equal(c.call(workspace=ws, sync=True), want)
