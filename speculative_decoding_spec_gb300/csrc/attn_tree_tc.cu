@@ -224,8 +224,8 @@ SPEC_DEV bool wait_phase(uint64_t* b, unsigned parity, volatile int* abort, int*
   if (mbar_try(b, parity)) return true;
   const long long t0 = clock64();
   do {
-    if (*abort) return false;
     if (mbar_try(b, parity)) return true;
+    if (*abort) return false;
   } while (clock64() - t0 < WAIT_CYCLES);
   *abort = 1;
   set_error(err, SPEC_ERR_TIMEOUT);
