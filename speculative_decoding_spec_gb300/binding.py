@@ -1025,7 +1025,11 @@ class Engine:
 
     def load_prefilled(self, slot: int, contig: torch.Tensor):
         """Adopt cache contents [L][2][nkv][n][hd] for positions [0, n) of a slot
-        (synthetic long contexts) and set its committed length to n."""
+        (synthetic long contexts) and set its committed length to n. The slot must
+        have its pages."""
+        pages = self.block_table[slot, : -(-contig.shape[3] // PAGE)]
+        if contig.shape[3] > self.pages_per_seq * PAGE or int(pages.amin() if len(pages) else 0) < 0:
+            raise SpecError("load_prefilled", SPEC_ECAPACITY, "the slot has too few pages")
         synth.scatter_to_pages(self.pool, contig, self.block_table[slot])
         self.seq_len[slot] = contig.shape[3]
 

@@ -210,3 +210,22 @@ def test_engine_buffers_of_ids():
     eng.spec_pages_fork(eng.seq_ids([0]), _int([1]))
     assert eng.seq_len.tolist() == [100, 100, 0] and int(eng.block_table[0, 0]) == int(eng.block_table[1, 0])
     eng.close()
+
+
+def test_prefilled_contents_need_pages():
+    """Contents for a slot of a pooled engine that has no pages for them are refused: no other slot's page is written."""
+    t = _shape("f32")
+    eng = binding.Engine(synth.make_target(t, device="cuda"), None, n_slots=2, B_max=1, rows_max=4, max_ctx=192, n_pages=4)
+    kv = synth.make_prefilled_kv(t, 100, device="cuda")
+    eng.pool.fill_(7.0)
+    for pages in (0, 64):
+        if pages:
+            eng.spec_pages_reserve(_int([1]), _int([pages]))
+        with pytest.raises(binding.SpecError) as e:
+            eng.load_prefilled(1, kv)
+        assert e.value.code == binding.SPEC_ECAPACITY and (eng.pool == 7.0).all() and int(eng.seq_len[1]) == 0
+    eng.spec_pages_reserve(_int([1]), _int([100]))
+    eng.load_prefilled(1, kv)
+    assert int(eng.seq_len[1]) == 100 and torch.equal(eng.pool[:, 0], kv[:, :, :, :64].to(eng.pool.dtype))
+    assert (eng.pool[:, 2:] == 7.0).all()
+    eng.close()
