@@ -244,7 +244,7 @@ def sample_t(w):
 def branching(w):
     from perf import more_operators
     more_operators.own = True
-    for name in ("tree_8x64_30b_bf16", "tree_1x7_e2b_131072", "adjust_8x5x262144", "fork_1to8_30b", "compact_e4b"):
+    for name in ("tree_8x64_30b_bf16", "tree_8x24_e4b_ragged", "tree_1x7_e2b_131072", "adjust_8x5x262144", "fork_1to8_30b", "compact_e4b"):
         state = more_operators.prepare(next(c for c in more_operators.listed() if c["name"] == name), 1)
         for _ in range(2):
             more_operators.run(state)

@@ -422,8 +422,8 @@ __global__ void __launch_bounds__(NTHR, 8) adjust_copy_kernel(const __grid_const
 
 // In place, the first kernel sets what is forbidden and does no more: FW words of a
 // row's mask a CTA and turn. Bound by the stores, 2 or 4 bytes a lane in whole lines:
-// 40 fp32 rows of 262144 with three quarters of the tokens forbidden take 10.5 us, with a
-// hundredth 3.9; 64 bf16 rows 15.7 and 5.1 (whole vectors read, changed and written
+// 40 fp32 rows of 262144 with three quarters of the tokens forbidden take 10.5 us, with two
+// in a thousand 3.9; 64 bf16 rows 15.7 and 5.1 (whole vectors read, changed and written
 // back took 13.7, 9.6, 11.8 and 8.7, but touched what stays as it is).
 constexpr int FW = 16 * NTHR / 32;
 template <typename T>

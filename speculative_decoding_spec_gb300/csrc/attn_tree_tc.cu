@@ -14,17 +14,22 @@
 // A product cuts its sum to 24 bits, so float rows take care: their smallest parts
 // first for S, and O out of tensor memory after every 8 blocks. 8 x 24 rows (contexts
 // of 1024 to 8192) are off by 1.1e-6 relative to all outputs, 3.3e-6 without either;
-// two planes of P, in blocks of 128 keys, 3.6e-6 (32 us instead of 46; a binary32
+// two planes of P, in blocks of 128 keys, 3.6e-6 (32 us instead of 47; a binary32
 // library product 1.4e-6).
 //
 // Few rows leave most of the 128 lanes idle, and may: 128 keys are 64 KB at head
 // dim 128, about 2800 cycles at an SM's share of the HBM rate, while their products
 // take 1024 cycles and their softmax 1900 in either stream (500 for the maximum, 1400
-// for the weights). 8 x 64 rows take 1750 cycles a block and tile: a product of S takes
-// 80 cycles there, 64 alone, as its operands fill shared memory's bandwidth and copies
-// arrive beside them; neither a softmax in one pass nor fewer waits changes the total.
-// Warps whose lanes hold no row skip the softmax. With three planes the products
-// take 3840 and bind (those of S 48 for 64 keys, 64 for 128: the queries are read again).
+// for the weights). 8 x 64 rows take 1.02 us (1960 cycles) a block and tile, from the
+// slope over contexts of 4096 to 16384: a product of S takes 80 cycles there, 64 alone, as
+// its operands fill shared memory's bandwidth and copies arrive beside them, and a
+// stream's chain (weights, P V, S, maximum) has a wait at each step. Neither a softmax in
+// one pass nor fewer tries changes the total. The other 38 of their 121 us are the launch,
+// the beginnings and ends of two or three units a CTA, and the join. Float rows take 1.8 us
+// (3400 cycles) for 64 keys and a tile, of which three planes' products are 1920 (those of S 48
+// cycles for 64 keys, 64 for 128: the queries are read again), and 19 of the 47 us of 8 x 24
+// rows are the call's beginning, end and join; the tensor pipe is active for a third of the
+// time. Warps whose lanes hold no row skip the softmax.
 //
 // Two streams hide the softmax behind the products: while one stream's softmax
 // runs, the tensor cores work on the other's. With one tile of query rows the
@@ -33,8 +38,8 @@
 // head) each stream is a tile and a block is read once for both.
 //
 // Roles (384 threads, one CTA an SM): warp 0 loads (a ring of tiles, K and V in
-// the order in which they are used), warp 1 issues the products, warp 2 of CTA 0
-// checks the arguments, warps 4-7 and 8-11 are the streams' softmax. Waits are
+// the order in which they are used), warp 1 issues the products, warp 2 checks the CTA's
+// share of the arguments (without cuts CTA 0's all of them), warps 4-7 and 8-11 are the streams' softmax. Waits are
 // bounded; one that runs out sets SPEC_ERR_TIMEOUT and an abort flag that lets
 // every other wait pass, so that the CTA drains its copies and ends.
 #include <cuda.h>
@@ -247,7 +252,7 @@ struct Cta {
   static constexpr int NH = HD / 64, HALF = BK * 128, TILE = NH * HALF;      // of a block's keys or values
   static constexpr int QPL = F32 ? 3 : 1, QHALF = ROWS * 128, QTILE = NH * QHALF;  // of a tile of query rows
   // Float rows: blocks after which O leaves tensor memory and is added up in binary32 (three
-  // products cut it for 16 keys; 8 x 24 rows take 45 us, 43 with 16 blocks, 40 with 32).
+  // products cut it for 16 keys; 8 x 24 rows took 45 us, 43 with 16 blocks, 40 with 32).
   static constexpr int RUN = 8;
   static constexpr uint32_t O_COL = 256;
   const TreeArgs& a;
@@ -406,6 +411,8 @@ struct Cta {
           issue_pv(s, 1, vt, false, last, go);
           // the next scores overwrite the weights that these products read, in other columns than
           // they write: only products of one accumulator and shape are ordered by themselves
+          // (8 x 64 rows 121 us, 114 without; with the upper half of the scores, which the weights
+          // do not reach, made before the wait 119)
           if (k) {
             ok = wait(&sm->odone[s], ((round >> s) & 1) ^ 1);
             if (!ok) break;
@@ -608,7 +615,7 @@ struct Cta {
       unsigned long long path = 0;
       for (int q = qi; q >= 0; q = sm->up[q]) path |= 1ull << q;
       float m = -INFINITY, l = 0.f, Ma = -INFINITY, La = 0.f;  // (this stream's; both, of the runs before)
-      float acc[F32 ? 2 : 1][32];                                // the runs before: this thread's share of its row
+      float acc[F32 ? 2 : 1][32];  // the runs before: this thread's share of its row (in local memory: a rolled loop indexes it)
       for (int e0 = 0, e1; e0 < N; e0 = e1) {
         e1 = F32 ? min(N, e0 + RUN) : N;
         const int n0 = pair ? e0 : e0 + s, dn = pair ? 1 : 2;
@@ -877,8 +884,8 @@ Plan tc_plan(const TreeArgs& a) {
   Plan p;
   p.blk = a.q_dtype == DT_BF16 ? 7 : 6;
   p.tile = 7;
-  // what a unit's beginning and end cost, in tiles (8 x 64 rows, 30B-class: 114 us at 12, 120 at 5; fp32 rows, 8 x 24:
-  // the same at 3, 5 and 8, 2% more at 11)
+  // what a unit's beginning and end cost, in tiles (8 x 64 rows, 30B-class: 121 us at 12, 124 at 5 and at 16; fp32 rows,
+  // 8 x 24: within 3% at 3, 5 and 8, 2% more at 11)
   p.head = a.q_dtype == DT_BF16 ? 12 : 5;
   p.units = 0;
   plan_heads(p, a);
